@@ -60,10 +60,12 @@ typedef enum pkv_status {
     PKV_ERR_HEADS = 3,       /* num_q_heads / num_kv_heads is not one of 1, 2, 4, 8         */
     PKV_ERR_HEADDIM = 4,     /* head_dim is not 64 or 128                                   */
     PKV_ERR_BLOCKSIZE = 5,   /* block_size is not 16                                        */
-    PKV_ERR_ALIAS = 6,       /* copy_blocks: a dst repeats, or a dst is also a src          */
+    PKV_ERR_ALIAS = 6,       /* copy_blocks: a dst repeats, or a dst is also a src; rotary:
+                                buffers overlap; (device) a state slot is stored to by two
+                                sequences, or stored to by one and read by another         */
     PKV_ERR_WORKSPACE = 7,   /* workspace NULL, too small or not 256-byte aligned           */
     PKV_ERR_ALIGN = 8,       /* a device pointer is not 16-byte aligned                     */
-    PKV_ERR_RANGE = 9,       /* (device) block id, slot, length or V value out of range     */
+    PKV_ERR_RANGE = 9,       /* (device) block id, slot, length, V value or decay out of range */
     PKV_ERR_TIMEOUT = 10,    /* (device) a bounded wait inside a kernel expired             */
     PKV_ERR_CUDA = 11,       /* a CUDA runtime call failed (see pkv_last_cuda_error)        */
     PKV_ERR_UNSUPPORTED = 12, /* the current device is not compute capability 10.3          */
@@ -367,6 +369,161 @@ pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const void* q
                                          int32_t num_seqs, const int32_t* block_tables, int32_t max_blocks_per_seq,
                                          int32_t max_context_len, float scale, float* out, void* workspace,
                                          size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions.  The pages stop at attention's inputs; models turn q and
+ * k by their token's position first, and for images and video by several
+ * positions (time, height, width), each turning its own share of the pairs.
+ *
+ * For token t and pair i < rot_dim/2, with a = positions[axis(i)][t] *
+ * inv_freq[i] radians (the product exact, whatever the position),
+ *     (x, y) -> (x cos a - y sin a, x sin a + y cos a)
+ * where (x, y) are the elements (i, i + rot_dim/2) of the row, or
+ * (2i, 2i + 1) with PKV_ROTARY_ADJACENT_PAIRS.  Elements from rot_dim on are
+ * passed through.  axis(i): the first sections[0] pairs belong to axis 0, the
+ * next sections[1] to axis 1 and so on; with PKV_ROTARY_INTERLEAVED_AXES the
+ * pairs are dealt to the axes in turn (0, 1, 2, 0, 1, 2, ...), an axis that
+ * has its share being passed over.
+ */
+enum { PKV_ROTARY_ADJACENT_PAIRS = 1, PKV_ROTARY_INTERLEAVED_AXES = 2 };
+
+typedef struct pkv_rotary {
+    const float* inv_freq;    /* fp32 [rot_dim/2], device: radians per position              */
+    const int32_t* positions; /* int32 [num_axes][num_tokens], device; any value             */
+    int32_t rot_dim;          /* 16 .. head_dim, a multiple of 16                            */
+    int32_t num_axes;         /* 1 .. 4                                                      */
+    int32_t sections[4];      /* pairs of each axis, >= 0; they sum to rot_dim/2             */
+    int32_t flags;            /* PKV_ROTARY_* bits                                           */
+} pkv_rotary_t;
+
+/*
+ * pkv_rotary -- turn q and k.
+ *
+ *   q, k           bf16 [num_tokens][heads][head_dim]; the rows of a token are
+ *                  contiguous, and a token's rows lie q_stride (k_stride)
+ *                  elements after the last token's: a multiple of 8, at least
+ *                  heads * head_dim (views of a packed q/k/v projection)
+ *   q_out, k_out   bf16 [num_tokens][heads][head_dim], contiguous.  q_out may
+ *                  be q (k_out k) when that is contiguous; any other overlap
+ *                  of an output with an input or the other output gives
+ *                  PKV_ERR_ALIAS
+ *   Results are rounded to bf16 once, from fp32.  num_q_heads and
+ *   num_kv_heads are any counts >= 1.  num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_rotary(const pkv_rotary_t* rotary, const void* q, int64_t q_stride, int32_t num_q_heads,
+                      const void* k, int64_t k_stride, int32_t num_kv_heads, int32_t head_dim, int32_t num_tokens,
+                      void* q_out, void* k_out, void* stream);
+
+/*
+ * pkv_rotary_cache_write -- turn q and k, and store the turned k and v in
+ * their slots, in one launch: pkv_rotary and pkv_cache_write without k's way
+ * through memory.
+ *
+ *   v, v_stride    as k
+ *   slot_mapping   as for pkv_cache_write (a negative slot stores nothing; a
+ *                  slot past the pool raises PKV_ERR_RANGE on the device; the
+ *                  token's q is turned either way).  Slots must be distinct.
+ *   bf16 pools end as pkv_rotary followed by pkv_cache_write leaves them.
+ *   e4m3 pools hold the code nearest to x * (1/scale) of the fp32 x: k is
+ *   rounded once, not to bf16 in between.
+ */
+pkv_status pkv_rotary_cache_write(const pkv_cache_t* cache, const pkv_rotary_t* rotary, const void* q,
+                                  int64_t q_stride, int32_t num_q_heads, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const int32_t* slot_mapping, int32_t num_tokens,
+                                  void* q_out, void* stream);
+
+/*
+ * Linear attention with a decay for each head, for the layers of a model
+ * that keep one fixed-size state per sequence in place of a growing cache.
+ * Not on the pages; it takes their batches ([ENG] "Chunked Prefill": prompt
+ * chunks beside single tokens) as the attention calls above do.
+ *
+ * Per sequence and kv head g, over its tokens j in order, with q head h of
+ * the group (h / (Hq/Hkv) == g):
+ *     S_j = exp(log_decay[g]) S_(j-1) + k_j v_j^T,    out_j[h] = scale * q_j[h]^T S_j
+ * with S [head_dim][head_dim] (k index, v index) in fp32 and S before the
+ * first token zero.
+ *
+ * The states are a caller-owned pool, addressed by slot like the cache:
+ *   state_slots    int32 [num_seqs]: where a sequence's state is read.  It is
+ *                  read only when the sequence has tokens before this call
+ *                  (context_lens[s] above its rows in the call); a negative
+ *                  slot then skips the sequence: its out rows are zero and
+ *                  nothing is stored
+ *   new_slots      int32 [num_seqs] or NULL (= state_slots, in place): where
+ *                  the state after the call is stored; negative stores
+ *                  nothing.  Reading one slot and storing to another keeps
+ *                  the old state (a shared prefix, a draft that may be taken
+ *                  back), and many sequences may read one slot.  A slot must
+ *                  not be stored to by two sequences of a call, nor stored
+ *                  to by one and read by another: that raises PKV_ERR_ALIAS
+ *                  on the device (detail: the sequence), and the results of
+ *                  those sequences are then not valid
+ *   A slot >= num_slots that would be used raises PKV_ERR_RANGE on the
+ *   device; the sequence's out rows are then zero and nothing is stored.
+ *   log_decay      <= 0 (0 keeps everything, -inf nothing).  A value above 0
+ *                  or NaN counts as 0 and raises PKV_ERR_RANGE (detail: the
+ *                  head).
+ */
+typedef struct pkv_states {
+    float* states;           /* fp32 [num_slots][num_kv_heads][head_dim][head_dim], device   */
+    const float* log_decay;  /* fp32 [num_kv_heads], device                                  */
+    int32_t num_slots;       /* >= 0                                                         */
+    int32_t num_kv_heads;    /* >= 1                                                         */
+    int32_t head_dim;        /* 64 or 128                                                    */
+} pkv_states_t;
+
+/*
+ * pkv_linear_decode_attention -- one token per sequence.
+ *
+ *   q, k, v        bf16 [num_seqs][heads][head_dim] with token strides, as for
+ *                  pkv_rotary (strides multiples of 8, >= heads * head_dim)
+ *   context_lens   int32 [num_seqs], including this token: 0 marks padding (a
+ *                  zero out row, no state touched), 1 a sequence's first
+ *                  token, negative raises PKV_ERR_RANGE (a zero row)
+ *   out            fp32 [num_seqs][num_q_heads][head_dim], device memory or
+ *                  page-locked host memory mapped for the device
+ */
+pkv_status pkv_linear_decode_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
+                                       int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, const int32_t* state_slots, const int32_t* new_slots,
+                                       const int32_t* context_lens, int32_t num_seqs, float scale, float* out,
+                                       void* stream);
+
+/*
+ * pkv_linear_prefill_workspace_size -- bytes of workspace
+ * pkv_linear_prefill_attention needs for any batch of num_seqs sequences and
+ * num_tokens tokens.  Returns 0 for invalid arguments.
+ */
+size_t pkv_linear_prefill_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * pkv_linear_prefill_attention -- a mixed batch of prompt chunks and single
+ * tokens.  Sequence s owns rows query_start_loc[s] .. query_start_loc[s+1]-1;
+ * context_lens[s] includes them, so a sequence starts from zero when they are
+ * equal and goes on from its state when the context is longer (a shorter
+ * context raises PKV_ERR_RANGE and gives zero rows).  A sequence without rows
+ * is left alone.
+ *
+ *   query_start_loc, query_start_loc_host   as for
+ *                  pkv_chunked_prefill_attention, but rows behind the last
+ *                  sequence (query_start_loc[num_seqs] < num_tokens) are
+ *                  allowed, and left as they were in out.  Device values that
+ *                  differ from the host's raise PKV_ERR_RANGE where rows are
+ *                  out of range or missed
+ *   workspace      >= pkv_linear_prefill_workspace_size() bytes, 256-byte
+ *                  aligned; scratch, need not be cleared.  Calls that run
+ *                  concurrently need separate workspaces
+ *   The other arguments are those of pkv_linear_decode_attention.
+ */
+pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
+                                        int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                                        int64_t v_stride, int32_t num_tokens, const int32_t* query_start_loc,
+                                        const int32_t* query_start_loc_host, const int32_t* state_slots,
+                                        const int32_t* new_slots, const int32_t* context_lens, int32_t num_seqs,
+                                        float scale, float* out, void* workspace, size_t workspace_bytes,
+                                        void* stream);
 
 /*
  * pkv_decode_attention_static -- pkv_decode_attention for callers that

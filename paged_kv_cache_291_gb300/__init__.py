@@ -22,6 +22,8 @@ __all__ = [
     "PKVError", "lib_path", "load", "version", "status_string", "cache_write", "copy_blocks",
     "decode_workspace_size", "decode_attention", "decode_step", "prefill_workspace_size",
     "chunked_prefill_attention",
+    "rotary", "rotary_cache_write", "linear_decode_attention", "linear_prefill_attention",
+    "linear_prefill_workspace_size",
     "get_error", "Cache", "Blocks", "prefix_keys", "swap_out", "swap_in", "test_arm_decode_stall",
 ]
 
@@ -37,6 +39,7 @@ STATUS_NAMES = {
     14: "PKV_ERR_NO_BLOCKS", 15: "PKV_ERR_HOST_MEMORY", 16: "PKV_ERR_DTYPE",
 }
 PKV_KV_BF16, PKV_KV_E4M3 = 0, 1
+PKV_ROTARY_ADJACENT_PAIRS, PKV_ROTARY_INTERLEAVED_AXES = 1, 2
 
 
 class PKVError(RuntimeError):
@@ -64,6 +67,18 @@ class BlocksState(ctypes.Structure):
                 ("max_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("table_size", ctypes.c_int32)]
 
 
+class Rotary(ctypes.Structure):
+    """Mirror of ``pkv_rotary_t``."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("flags", ctypes.c_int32)]
+
+
+class States(ctypes.Structure):
+    """Mirror of ``pkv_states_t``."""
+    _fields_ = [("states", ctypes.c_void_p), ("log_decay", ctypes.c_void_p), ("num_slots", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
 def lib_path() -> str:
     return _LIB_PATH
 
@@ -78,6 +93,7 @@ def load():
                            "paged_kv_cache_291_gb300.build` or __graft_entry__.build() first")
     lib = ctypes.CDLL(_LIB_PATH)
     P, i32, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
+    i64 = ctypes.c_int64
     CP = ctypes.POINTER(Cache)
     sigs = {
         "pkv_cache_write": ([CP, P, P, P, i32, P], ctypes.c_int),
@@ -101,6 +117,14 @@ def load():
         "pkv_blocks_register": ([ctypes.POINTER(BlocksState), P, i32, P, i32, P], ctypes.c_int),
         "pkv_prefix_keys": ([P, P, P, P, i32, i32, P, P], ctypes.c_int),
         "pkv_swap_blocks": ([CP, i32, P, P, i32, P, ctypes.c_int64, P], ctypes.c_int),
+        "pkv_rotary": ([ctypes.POINTER(Rotary), P, i64, i32, P, i64, i32, i32, i32, P, P, P], ctypes.c_int),
+        "pkv_rotary_cache_write": ([CP, ctypes.POINTER(Rotary), P, i64, i32, P, i64, P, i64, P, i32, P, P],
+                                   ctypes.c_int),
+        "pkv_linear_decode_attention": ([ctypes.POINTER(States), P, i64, i32, P, i64, P, i64, P, P, P, i32, f32, P,
+                                         P], ctypes.c_int),
+        "pkv_linear_prefill_workspace_size": ([i32, i32, i32, i32, i32], sz),
+        "pkv_linear_prefill_attention": ([ctypes.POINTER(States), P, i64, i32, P, i64, P, i64, i32, P, P, P, P, P, i32,
+                                          f32, P, P, sz, P], ctypes.c_int),
         "pkv_get_error": ([P, ctypes.POINTER(i32)], ctypes.c_int),
         "pkv_test_arm_decode_stall": ([i32], ctypes.c_int),
         "pkv_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -416,6 +440,201 @@ def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, 
         float(scale), _out(out), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream_handle(stream))
     _check(st, "pkv_chunked_prefill_attention")
+    return out
+
+
+def _rows(t, name, heads, d, tokens):
+    """A bf16 CUDA tensor [tokens][heads][d] whose tokens may lie further
+    apart than their rows need (a view of a packed projection): its address
+    and token stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [{tokens}][{heads}][{d}], got {list(t.shape)}")
+    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a token's heads and dims must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if tokens > 1 else heads * d
+
+
+def _same_device(first, *others):
+    """Every tensor on the current device: the library launches there."""
+    torch = _torch()
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.is_cuda and t.device != first.device:
+            raise ValueError(f"tensors are on {first.device} and {t.device}")
+
+
+def _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, tokens) -> Rotary:
+    torch = _torch()
+    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
+    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+        raise ValueError("positions must be [num_tokens] or [num_axes][num_tokens]")
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [rot_dim / 2]")
+    pairs = int(inv_freq.shape[0])
+    if sections is None:
+        if axes != 1:
+            raise ValueError("several axes need sections")
+        sections = [pairs]
+    sections = [int(x) for x in sections]
+    if len(sections) != axes or axes > 4:
+        raise ValueError("sections must name the pairs of each of at most 4 axes")
+    flags = (PKV_ROTARY_ADJACENT_PAIRS if adjacent_pairs else 0) | (
+        PKV_ROTARY_INTERLEAVED_AXES if interleaved_axes else 0)
+    return Rotary(_dev(inv_freq, "inv_freq", dtype=torch.float32).value,
+                  _dev(positions, "positions", dtype=torch.int32).value, 2 * pairs, axes,
+                  (ctypes.c_int32 * 4)(*(sections + [0] * (4 - axes))), flags)
+
+
+def rotary(q, k, positions, inv_freq, sections=None, interleaved_axes: bool = False, adjacent_pairs: bool = False,
+           q_out=None, k_out=None, stream=None):
+    """Turn q [T][Hq][d] and k [T][Hkv][d] (bf16; a token's rows may be a view
+    of a packed projection) by positions int32 [T] or [axes][T]: pair i by
+    positions[axis(i)] * inv_freq[i] (fp32 [rot_dim/2]).  ``sections`` names
+    the pairs of each axis, in order or (``interleaved_axes``) dealt in turn;
+    pairs are (i, i + rot_dim/2), or (2i, 2i + 1) with ``adjacent_pairs``.
+    Returns (q_out, k_out), contiguous; q_out may be q and k_out k."""
+    torch = _torch()
+    lib = load()
+    T, hq, d = q.shape
+    hkv = k.shape[1]
+    r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T)
+    qp, qs = _rows(q, "q", hq, d, T)
+    kp, ks = _rows(k, "k", hkv, d, T)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=q.device)
+    if q_out.shape != (T, hq, d) or k_out.shape != (T, hkv, d):
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    _same_device(q, k, positions, inv_freq, q_out, k_out)
+    st = lib.pkv_rotary(ctypes.byref(r), qp, qs, hq, kp, ks, hkv, d, T, _dev(q_out, "q_out", dtype=torch.bfloat16),
+                        _dev(k_out, "k_out", dtype=torch.bfloat16), _stream_handle(stream))
+    _check(st, "pkv_rotary")
+    return q_out, k_out
+
+
+def rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_freq, sections=None,
+                       interleaved_axes: bool = False, adjacent_pairs: bool = False, q_out=None, stream=None,
+                       k_scale=None, v_scale=None):
+    """:func:`rotary` and :func:`cache_write` in one launch: turned q to
+    ``q_out`` (returned), turned k and v to their slots.  e4m3 pools need the
+    scales; their codes come from the unrounded turned k."""
+    torch = _torch()
+    lib = load()
+    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True)
+    T, hq, d = q.shape
+    r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T)
+    if d != c.head_dim:
+        raise ValueError("q head_dim does not match the pools")
+    if slot_mapping.dim() != 1 or slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    qp, qs = _rows(q, "q", hq, d, T)
+    kp, ks = _rows(k, "k", c.num_kv_heads, d, T)
+    vp, vs = _rows(v, "v", c.num_kv_heads, d, T)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    if q_out.shape != (T, hq, d):
+        raise ValueError("q_out must have the shape of q")
+    _same_device(q, k, v, k_pool, v_pool, slot_mapping, positions, inv_freq, q_out)
+    st = lib.pkv_rotary_cache_write(ctypes.byref(c), ctypes.byref(r), qp, qs, hq, kp, ks, vp, vs,
+                                    _dev(slot_mapping, "slot_mapping", dtype=torch.int32), T,
+                                    _dev(q_out, "q_out", dtype=torch.bfloat16), _stream_handle(stream))
+    _check(st, "pkv_rotary_cache_write")
+    return q_out
+
+
+def _states(states, log_decay) -> States:
+    torch = _torch()
+    if states.dim() != 4 or states.shape[2] != states.shape[3]:
+        raise ValueError("states must be [num_slots][num_kv_heads][head_dim][head_dim]")
+    n, hkv, d, _ = states.shape
+    if log_decay.dim() != 1 or log_decay.shape[0] != hkv:
+        raise ValueError("log_decay must be [num_kv_heads]")
+    return States(_dev(states, "states", dtype=torch.float32).value,
+                  _dev(log_decay, "log_decay", dtype=torch.float32).value, n, hkv, d)
+
+
+def _linear_batch(s, q, k, v, state_slots, context_lens, new_slots, out):
+    torch = _torch()
+    T, hq, d = q.shape
+    if d != s.head_dim:
+        raise ValueError("q head_dim does not match the states")
+    S = int(context_lens.shape[0])
+    if state_slots.shape != (S,) or (new_slots is not None and new_slots.shape != (S,)):
+        raise ValueError("state_slots, new_slots and context_lens must be [num_seqs]")
+    rows = [x for name, t, h in (("q", q, hq), ("k", k, s.num_kv_heads), ("v", v, s.num_kv_heads))
+            for x in _rows(t, name, h, d, T)]
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=torch.float32, device=q.device)
+    if out.shape != (T, hq, d):
+        raise ValueError("out must be [num_tokens][num_q_heads][head_dim]")
+    _same_device(q, k, v, state_slots, context_lens, new_slots, out)
+    slots = _dev(state_slots, "state_slots", dtype=torch.int32)
+    new = _dev(new_slots, "new_slots", dtype=torch.int32) if new_slots is not None else None
+    return rows, out, slots, new, _dev(context_lens, "context_lens", dtype=torch.int32), S
+
+
+def linear_decode_attention(states, log_decay, q, k, v, state_slots, context_lens, scale: float, new_slots=None,
+                            out=None, stream=None):
+    """Linear attention of one token per sequence: S <- exp(log_decay) S +
+    k v^T in slot ``state_slots[s]`` of states float32 [slots][Hkv][d][d]
+    (stored to ``new_slots[s]`` when given), out = scale q^T S, float32
+    [B][Hq][d].  context_lens counts the token: 1 starts from a zero state,
+    0 marks padding."""
+    lib = load()
+    s = _states(states, log_decay)
+    rows, out, slots, new, ctx, S = _linear_batch(s, q, k, v, state_slots, context_lens, new_slots, out)
+    if q.shape[0] != S:
+        raise ValueError("q must hold one token per sequence")
+    _same_device(q, states, log_decay)
+    st = lib.pkv_linear_decode_attention(ctypes.byref(s), rows[0], rows[1], q.shape[1], rows[2], rows[3], rows[4],
+                                         rows[5], slots, new, ctx, S, float(scale), _out(out), _stream_handle(stream))
+    _check(st, "pkv_linear_decode_attention")
+    return out
+
+
+def linear_prefill_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
+    n = load().pkv_linear_prefill_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim)
+    if n == 0:
+        raise PKVError(2, "pkv_linear_prefill_workspace_size")
+    return int(n)
+
+
+def linear_prefill_attention(states, log_decay, q, k, v, query_start_loc, state_slots, context_lens, scale: float,
+                             new_slots=None, out=None, workspace=None, query_start_loc_host=None, stream=None):
+    """Linear attention of a mixed batch of prompt chunks and single tokens
+    over their states (see :func:`linear_decode_attention`); returns ``out``
+    float32 [T][Hq][d].  context_lens counts the call's tokens: a sequence
+    starts from zero when it has no others."""
+    torch = _torch()
+    lib = load()
+    s = _states(states, log_decay)
+    rows, out, slots, new, ctx, S = _linear_batch(s, q, k, v, state_slots, context_lens, new_slots, out)
+    T, hq, d = q.shape
+    if query_start_loc.shape != (S + 1,):
+        raise ValueError("query_start_loc must have num_seqs + 1 entries")
+    if query_start_loc_host is None:
+        query_start_loc_host = query_start_loc
+    qh, qhp = _host_i32(query_start_loc_host)
+    if qh.shape != (S + 1,):
+        raise ValueError("query_start_loc_host must have num_seqs + 1 entries")
+    if workspace is None:
+        need = lib.pkv_linear_prefill_workspace_size(S, T, hq, s.num_kv_heads, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _same_device(q, states, log_decay, query_start_loc, workspace)
+    st = lib.pkv_linear_prefill_attention(
+        ctypes.byref(s), rows[0], rows[1], hq, rows[2], rows[3], rows[4], rows[5], T,
+        _dev(query_start_loc, "query_start_loc", dtype=torch.int32), qhp, slots, new, ctx, S, float(scale), _out(out),
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    _check(st, "pkv_linear_prefill_attention")
     return out
 
 

@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <unordered_set>
 
@@ -160,10 +161,10 @@ PKV_API const char* pkv_status_string(pkv_status s) {
         case PKV_ERR_HEADS: return "PKV_ERR_HEADS: num_q_heads / num_kv_heads must be 1, 2, 4 or 8";
         case PKV_ERR_HEADDIM: return "PKV_ERR_HEADDIM: head_dim must be 64 or 128";
         case PKV_ERR_BLOCKSIZE: return "PKV_ERR_BLOCKSIZE: block_size must be 16";
-        case PKV_ERR_ALIAS: return "PKV_ERR_ALIAS: copy_blocks destinations repeat or overlap sources";
+        case PKV_ERR_ALIAS: return "PKV_ERR_ALIAS: copy destinations repeat or overlap sources, buffers overlap, or sequences share a stored state slot";
         case PKV_ERR_WORKSPACE: return "PKV_ERR_WORKSPACE: workspace missing, too small or misaligned";
         case PKV_ERR_ALIGN: return "PKV_ERR_ALIGN: a device pointer is not 16-byte aligned";
-        case PKV_ERR_RANGE: return "PKV_ERR_RANGE: a block id, slot or context length was out of range";
+        case PKV_ERR_RANGE: return "PKV_ERR_RANGE: a block id, slot, context length or decay was out of range";
         case PKV_ERR_TIMEOUT: return "PKV_ERR_TIMEOUT: a bounded wait inside a kernel expired";
         case PKV_ERR_CUDA: return "PKV_ERR_CUDA: a CUDA runtime call failed";
         case PKV_ERR_UNSUPPORTED: return "PKV_ERR_UNSUPPORTED: the current device is not compute capability 10.3";
@@ -661,6 +662,263 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return PKV_OK;
+}
+
+namespace {
+
+// Strided bf16 rows: [tokens][heads][d], a token's rows `stride` elements
+// after the last's.
+pkv_status check_rows(const void* p, int64_t stride, int32_t heads, int32_t d) {
+    if (p == nullptr) return PKV_ERR_NULL;
+    if (stride < static_cast<int64_t>(heads) * d || stride % 8 != 0 || stride > (static_cast<int64_t>(1) << 31))
+        return PKV_ERR_SHAPE;
+    return aligned16(p) ? PKV_OK : PKV_ERR_ALIGN;
+}
+
+struct Span {
+    uintptr_t at;
+    size_t bytes;
+};
+
+Span rows_span(const void* p, int64_t stride, int32_t heads, int32_t d, int32_t tokens) {
+    return {reinterpret_cast<uintptr_t>(p),
+            (static_cast<size_t>(tokens - 1) * stride + static_cast<size_t>(heads) * d) * 2};
+}
+
+bool overlap(const Span& a, const Span& b) { return a.at < b.at + b.bytes && b.at < a.at + a.bytes; }
+
+// An output may be its own contiguous input; it overlaps no other buffer.
+bool clashes(const Span& out, const Span& own_input, bool own_contiguous, std::initializer_list<Span> others) {
+    if (overlap(out, own_input) && !(own_contiguous && out.at == own_input.at)) return true;
+    for (const Span& o : others)
+        if (overlap(out, o)) return true;
+    return false;
+}
+
+pkv_status fill_rotary(const pkv_rotary_t* r, int32_t hq, int32_t hkv, int32_t head_dim, int32_t num_tokens,
+                       pkv::RotaryArgs* a) {
+    if (r == nullptr) return PKV_ERR_NULL;
+    if (num_tokens < 0) return PKV_ERR_SHAPE;
+    if (hq < 1 || hkv < 1 || hq > 65536 || hkv > 65536) return PKV_ERR_HEADS;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_HEADDIM;
+    if (r->rot_dim < 16 || r->rot_dim > head_dim || r->rot_dim % 16 != 0 || r->num_axes < 1 || r->num_axes > 4 ||
+        (r->flags & ~(PKV_ROTARY_ADJACENT_PAIRS | PKV_ROTARY_INTERLEAVED_AXES)) != 0)
+        return PKV_ERR_SHAPE;
+    const int32_t pairs = r->rot_dim / 2;
+    int64_t sum = 0;
+    for (int32_t x = 0; x < r->num_axes; ++x) {
+        if (r->sections[x] < 0) return PKV_ERR_SHAPE;
+        sum += r->sections[x];
+    }
+    if (sum != pairs) return PKV_ERR_SHAPE;
+    if (num_tokens > 0 && (r->inv_freq == nullptr || r->positions == nullptr)) return PKV_ERR_NULL;
+    int32_t left[4] = {r->sections[0], r->sections[1], r->sections[2], r->sections[3]};
+    a->axis_of_pair[0] = a->axis_of_pair[1] = 0;
+    const bool in_turn = (r->flags & PKV_ROTARY_INTERLEAVED_AXES) != 0;
+    for (int32_t i = 0, axis = 0; i < pairs; ++i) {
+        while (left[axis] == 0) axis = (axis + 1) % r->num_axes;
+        --left[axis];
+        a->axis_of_pair[i >> 5] |= static_cast<uint64_t>(axis) << (2 * (i & 31));
+        if (in_turn) axis = (axis + 1) % r->num_axes;
+    }
+    a->inv_freq = r->inv_freq;
+    a->positions = r->positions;
+    a->rot_dim = r->rot_dim;
+    a->adjacent = (r->flags & PKV_ROTARY_ADJACENT_PAIRS) != 0;
+    a->num_tokens = num_tokens;
+    a->num_q_heads = hq;
+    a->num_kv_heads = hkv;
+    a->head_dim = head_dim;
+    return PKV_OK;
+}
+
+}  // namespace
+
+PKV_API pkv_status pkv_rotary(const pkv_rotary_t* rotary, const void* q, int64_t q_stride, int32_t num_q_heads,
+                              const void* k, int64_t k_stride, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t num_tokens, void* q_out, void* k_out, void* stream) {
+    pkv::RotaryArgs a = {};
+    pkv_status st = fill_rotary(rotary, num_q_heads, num_kv_heads, head_dim, num_tokens, &a);
+    if (st != PKV_OK) return st;
+    if (num_tokens == 0) return PKV_OK;
+    if ((st = check_rows(q, q_stride, num_q_heads, head_dim)) != PKV_OK) return st;
+    if ((st = check_rows(k, k_stride, num_kv_heads, head_dim)) != PKV_OK) return st;
+    const int64_t qs = static_cast<int64_t>(num_q_heads) * head_dim, ks = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if ((st = check_rows(q_out, qs, num_q_heads, head_dim)) != PKV_OK) return st;
+    if ((st = check_rows(k_out, ks, num_kv_heads, head_dim)) != PKV_OK) return st;
+    const Span in_q = rows_span(q, q_stride, num_q_heads, head_dim, num_tokens);
+    const Span in_k = rows_span(k, k_stride, num_kv_heads, head_dim, num_tokens);
+    const Span out_q = rows_span(q_out, qs, num_q_heads, head_dim, num_tokens);
+    const Span out_k = rows_span(k_out, ks, num_kv_heads, head_dim, num_tokens);
+    if (clashes(out_q, in_q, q_stride == qs || num_tokens == 1, {in_k, out_k}) ||
+        clashes(out_k, in_k, k_stride == ks || num_tokens == 1, {in_q}))
+        return PKV_ERR_ALIAS;
+    DeviceState* dev = nullptr;
+    if ((st = current_device(&dev)) != PKV_OK) return st;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.k_out = static_cast<uint16_t*>(k_out);
+    a.err = dev->err;
+    cudaError_t e = pkv::launch_rotary(a, dev->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+PKV_API pkv_status pkv_rotary_cache_write(const pkv_cache_t* cache, const pkv_rotary_t* rotary, const void* q,
+                                          int64_t q_stride, int32_t num_q_heads, const void* k, int64_t k_stride,
+                                          const void* v, int64_t v_stride, const int32_t* slot_mapping,
+                                          int32_t num_tokens, void* q_out, void* stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    const int32_t hkv = cache->num_kv_heads, d = cache->head_dim;
+    pkv::RotaryArgs a = {};
+    if ((st = fill_rotary(rotary, num_q_heads, hkv, d, num_tokens, &a)) != PKV_OK) return st;
+    if (num_tokens == 0) return PKV_OK;
+    if ((st = check_rows(q, q_stride, num_q_heads, d)) != PKV_OK) return st;
+    if ((st = check_rows(k, k_stride, hkv, d)) != PKV_OK) return st;
+    if ((st = check_rows(v, v_stride, hkv, d)) != PKV_OK) return st;
+    const int64_t qs = static_cast<int64_t>(num_q_heads) * d;
+    if ((st = check_rows(q_out, qs, num_q_heads, d)) != PKV_OK) return st;
+    if (slot_mapping == nullptr) return PKV_ERR_NULL;
+    const size_t pool = static_cast<size_t>(cache->num_blocks) * hkv * 16 * d * elem_bytes(cache);
+    const Span k_pool = {reinterpret_cast<uintptr_t>(cache->k_pool), pool};
+    const Span v_pool = {reinterpret_cast<uintptr_t>(cache->v_pool), pool};
+    const Span in_k = rows_span(k, k_stride, hkv, d, num_tokens), in_v = rows_span(v, v_stride, hkv, d, num_tokens);
+    const Span in_q = rows_span(q, q_stride, num_q_heads, d, num_tokens);
+    if (clashes(rows_span(q_out, qs, num_q_heads, d, num_tokens), in_q, q_stride == qs || num_tokens == 1,
+                {in_k, in_v, k_pool, v_pool}) ||
+        clashes(k_pool, in_q, false, {in_k, in_v, v_pool}) || clashes(v_pool, in_q, false, {in_k, in_v}))
+        return PKV_ERR_ALIAS;
+    DeviceState* dev = nullptr;
+    if ((st = current_device(&dev)) != PKV_OK) return st;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.slot_mapping = slot_mapping;
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.num_slots = static_cast<int64_t>(cache->num_blocks) * 16;
+    a.kv_e4m3 = cache->kv_dtype == PKV_KV_E4M3;
+    a.k_inv = 1.f / cache->k_scale;
+    a.v_inv = 1.f / cache->v_scale;
+    a.err = dev->err;
+    cudaError_t e = pkv::launch_rotary(a, dev->num_sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+namespace {
+
+// The checks and arguments both linear-attention calls share; a batch with
+// nothing to do is the callers' to return early on.
+pkv_status fill_linear(const pkv_states_t* states, const void* q, int64_t q_stride, int32_t num_q_heads,
+                       const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                       const int32_t* state_slots, const int32_t* new_slots, const int32_t* context_lens,
+                       int32_t num_seqs, int32_t num_tokens, float scale, float* out, pkv::LinearArgs* a,
+                       DeviceState** dev) {
+    const int32_t hkv = states->num_kv_heads, d = states->head_dim;
+    pkv_status st;
+    if (states->states == nullptr || states->log_decay == nullptr) return PKV_ERR_NULL;
+    if ((st = check_rows(q, q_stride, num_q_heads, d)) != PKV_OK) return st;
+    if ((st = check_rows(k, k_stride, hkv, d)) != PKV_OK) return st;
+    if ((st = check_rows(v, v_stride, hkv, d)) != PKV_OK) return st;
+    if (state_slots == nullptr || context_lens == nullptr || out == nullptr) return PKV_ERR_NULL;
+    if (!aligned16(states->states) || !aligned16(out)) return PKV_ERR_ALIGN;
+    if ((st = current_device(dev)) != PKV_OK) return st;
+    const void* out_dev = nullptr;
+    if ((st = device_address(out, &out_dev)) != PKV_OK) return st;
+    a->states = states->states;
+    a->log_decay = states->log_decay;
+    a->q = static_cast<const uint16_t*>(q);
+    a->k = static_cast<const uint16_t*>(k);
+    a->v = static_cast<const uint16_t*>(v);
+    a->q_stride = q_stride;
+    a->k_stride = k_stride;
+    a->v_stride = v_stride;
+    a->query_start_loc = nullptr;
+    a->context_lens = context_lens;
+    a->state_slots = state_slots;
+    a->new_slots = new_slots != nullptr ? new_slots : state_slots;
+    a->out = static_cast<float*>(const_cast<void*>(out_dev));
+    a->err = (*dev)->err;
+    a->num_slots = states->num_slots;
+    a->num_kv_heads = hkv;
+    a->num_q_heads = num_q_heads;
+    a->head_dim = d;
+    a->num_seqs = num_seqs;
+    a->num_tokens = num_tokens;
+    a->max_recurrent = 1;
+    a->scale = scale;
+    return PKV_OK;
+}
+
+pkv_status check_states(const pkv_states_t* s, int32_t num_q_heads) {
+    if (s == nullptr) return PKV_ERR_NULL;
+    if (s->num_slots < 0 || s->num_kv_heads < 1) return PKV_ERR_SHAPE;
+    if (s->head_dim != 64 && s->head_dim != 128) return PKV_ERR_HEADDIM;
+    return check_heads(num_q_heads, s->num_kv_heads);
+}
+
+}  // namespace
+
+PKV_API pkv_status pkv_linear_decode_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
+                                               int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                                               int64_t v_stride, const int32_t* state_slots,
+                                               const int32_t* new_slots, const int32_t* context_lens,
+                                               int32_t num_seqs, float scale, float* out, void* stream) {
+    pkv_status st = check_states(states, num_q_heads);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0) return PKV_ERR_SHAPE;
+    if (num_seqs == 0) return PKV_OK;
+    DeviceState* dev = nullptr;
+    pkv::LinearArgs a;
+    if ((st = fill_linear(states, q, q_stride, num_q_heads, k, k_stride, v, v_stride, state_slots, new_slots,
+                          context_lens, num_seqs, num_seqs, scale, out, &a, &dev)) != PKV_OK)
+        return st;
+    cudaError_t e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+PKV_API size_t pkv_linear_prefill_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                                 int32_t num_kv_heads, int32_t head_dim) {
+    if (num_seqs < 0 || num_tokens < 0 || check_heads(num_q_heads, num_kv_heads) != PKV_OK) return 0;
+    if (head_dim != 64 && head_dim != 128) return 0;
+    return 256;
+}
+
+PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
+                                                int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                                                int64_t v_stride, int32_t num_tokens,
+                                                const int32_t* query_start_loc, const int32_t* query_start_loc_host,
+                                                const int32_t* state_slots, const int32_t* new_slots,
+                                                const int32_t* context_lens, int32_t num_seqs, float scale,
+                                                float* out, void* workspace, size_t workspace_bytes, void* stream) {
+    pkv_status st = check_states(states, num_q_heads);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0 || num_tokens < 0) return PKV_ERR_SHAPE;
+    if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+    if (query_start_loc == nullptr || query_start_loc_host == nullptr) return PKV_ERR_NULL;
+    if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] > num_tokens) return PKV_ERR_SHAPE;
+    for (int32_t s = 0; s < num_seqs; ++s)
+        if (query_start_loc_host[s + 1] < query_start_loc_host[s]) return PKV_ERR_SHAPE;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_WORKSPACE;
+    if (workspace_bytes < pkv_linear_prefill_workspace_size(num_seqs, num_tokens, num_q_heads, states->num_kv_heads,
+                                                            states->head_dim))
+        return PKV_ERR_WORKSPACE;
+    DeviceState* dev = nullptr;
+    pkv::LinearArgs a;
+    if ((st = fill_linear(states, q, q_stride, num_q_heads, k, k_stride, v, v_stride, state_slots, new_slots,
+                          context_lens, num_seqs, num_tokens, scale, out, &a, &dev)) != PKV_OK)
+        return st;
+    a.query_start_loc = query_start_loc;
+    a.max_recurrent = INT32_MAX;
+    cudaError_t e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
 PKV_API pkv_status pkv_test_arm_decode_stall(int32_t launches) {

@@ -1,0 +1,92 @@
+// linear_device.cuh -- what the two forms of linear attention share: which
+// rows and states a sequence has, and the decay in extended precision.
+#pragma once
+
+#include <cstdint>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+// One sequence of a linear-attention call.
+struct LinearSeq {
+    int32_t row0;    // first row
+    int32_t rows;    // new tokens (0: nothing to do)
+    int32_t load;    // slot its state is read from, -1: it starts from zero
+    int32_t store;   // slot its state goes to, -1: nowhere
+    int32_t bad;     // rows get zeros and no state is stored
+};
+
+// `report`: whether this thread records what is out of range.
+__device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& A, int s, bool report) {
+    LinearSeq q;
+    const int n = __ldg(A.context_lens + s);
+    if (A.query_start_loc != nullptr) {
+        q.row0 = __ldg(A.query_start_loc + s);
+        const int end = __ldg(A.query_start_loc + s + 1);
+        q.rows = end - q.row0;
+        if (q.row0 < 0 || end < q.row0 || end > A.num_tokens) {
+            if (report) record_error(A.err, kErrRange, static_cast<uint32_t>(s));
+            q.row0 = q.rows = 0;
+        }
+    } else {
+        q.row0 = s;
+        q.rows = 1;
+    }
+    q.load = q.store = -1;
+    q.bad = 0;
+    if (q.rows == 0) return q;
+    if (n < q.rows) {
+        // A single-token row without a context is padding; anything else
+        // contradicts itself.
+        q.bad = 1;
+        if (report && !(n == 0 && A.query_start_loc == nullptr))
+            record_error(A.err, kErrRange, static_cast<uint32_t>(s));
+        return q;
+    }
+    const int from = __ldg(A.state_slots + s), to = __ldg(A.new_slots + s);
+    if ((n > q.rows && from >= A.num_slots) || to >= A.num_slots) {
+        if (report) record_error(A.err, kErrRange, static_cast<uint32_t>(s));
+        q.bad = 1;
+        return q;
+    }
+    if (n > q.rows && from < 0) {
+        q.bad = 1;  // no state to go on from: a skipped sequence
+        return q;
+    }
+    q.load = n > q.rows ? from : -1;
+    q.store = to;
+    return q;
+}
+
+// Whether a sequence reads or stores (for the check of shared slots).
+__device__ __forceinline__ bool linear_shares(const LinearArgs& A, int other, int store) {
+    const int n = __ldg(A.context_lens + other);
+    int rows = 1;
+    if (A.query_start_loc != nullptr)
+        rows = __ldg(A.query_start_loc + other + 1) - __ldg(A.query_start_loc + other);
+    if (rows <= 0 || n < rows) return false;
+    return __ldg(A.new_slots + other) == store || (n > rows && __ldg(A.state_slots + other) == store);
+}
+
+// exp(log_decay * tokens) as hi + lo (2^-48 relative): a state is multiplied
+// by it once per token or chunk, so a 2^-24 error of one factor would grow
+// with the length of the context.  A log decay above 0 or NaN counts as 0
+// and is reported; -inf keeps nothing.
+__device__ __forceinline__ float clean_log_decay(const LinearArgs& A, int h, bool report) {
+    float g = __ldg(A.log_decay + h);
+    if (!(g <= 0.f)) {
+        if (report) record_error(A.err, kErrRange, static_cast<uint32_t>(h));
+        g = 0.f;
+    }
+    return fmaxf(g, -1e30f);
+}
+
+__device__ __forceinline__ float2 decay_pair(float g, int tokens) {
+    const double x = exp(static_cast<double>(g) * tokens);
+    const float hi = static_cast<float>(x);
+    return make_float2(hi, static_cast<float>(x - static_cast<double>(hi)));
+}
+
+}  // namespace pkv

@@ -132,6 +132,55 @@ struct PrefillArgs {
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 
+// Rotary positions (rotary.cu): q and k rows turned, or q turned and k, v
+// stored in the pools (k_pool set).
+struct RotaryArgs {
+    const uint16_t* q;          // bf16 rows [num_tokens][heads][d], a token's rows q_stride elements after the last's
+    const uint16_t* k;
+    const uint16_t* v;          // cache write only
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* positions;   // [axes][num_tokens]
+    const float* inv_freq;      // [rot_dim / 2]
+    uint64_t axis_of_pair[2];   // 2 bits for each of 64 pairs
+    int32_t rot_dim, adjacent;
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;
+    uint16_t* q_out;            // bf16 [num_tokens][Hq][d]
+    uint16_t* k_out;            // bf16 [num_tokens][Hkv][d], or null
+    const int32_t* slot_mapping;
+    void* k_pool;               // null: no cache write
+    void* v_pool;
+    int64_t num_slots;
+    bool kv_e4m3;
+    float k_inv, v_inv;         // e4m3: reciprocal scales
+    unsigned long long* err;
+    int32_t runs, rows_per_run; // set by launch_rotary: runs of rows a token is cut into
+};
+
+cudaError_t launch_rotary(RotaryArgs a, int num_sms, cudaStream_t stream);
+
+// Linear attention over a pool of fp32 states (linear.cu): the recurrent
+// form for sequences of at most max_recurrent new tokens, and the chunked
+// form (linear_chunk.cu) for longer ones.
+struct LinearArgs {
+    float* states;                  // fp32 [num_slots][Hkv][d][d]
+    const float* log_decay;         // [Hkv]
+    const uint16_t* q;              // bf16 rows, token stride in elements
+    const uint16_t* k;
+    const uint16_t* v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* query_start_loc; // [S+1], or null: sequence s is row s
+    const int32_t* context_lens;    // [S]
+    const int32_t* state_slots;     // [S]
+    const int32_t* new_slots;       // [S] (state_slots when in place)
+    float* out;                     // fp32 [num_tokens][Hq][d]
+    unsigned long long* err;
+    int32_t num_slots, num_kv_heads, num_q_heads, head_dim, num_seqs, num_tokens;
+    int32_t max_recurrent;          // longest sequence the recurrent form takes
+    float scale;
+};
+
+cudaError_t launch_linear_recurrent(const LinearArgs& a, cudaStream_t stream);
+
 // Block bookkeeping state (pkv_blocks_t), all device memory.
 struct BlocksArgs {
     int32_t* tables;      // [max_seqs][max_blocks]
