@@ -67,10 +67,13 @@ class BlocksState(ctypes.Structure):
                 ("max_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32), ("table_size", ctypes.c_int32)]
 
 
+_Sections = ctypes.c_int32 * 4
+
+
 class Rotary(ctypes.Structure):
     """Mirror of ``pkv_rotary_t``."""
     _fields_ = [("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
-                ("num_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("flags", ctypes.c_int32)]
+                ("num_axes", ctypes.c_int32), ("sections", _Sections), ("flags", ctypes.c_int32)]
 
 
 class States(ctypes.Structure):
@@ -149,15 +152,22 @@ def status_string(status: int) -> str:
 
 # ---------------------------------------------------------------- helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream) -> ctypes.c_void_p:
     torch = _torch()
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the raw handle of torch.cuda.current_stream(), without building the object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -443,54 +453,84 @@ def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, 
     return out
 
 
-def _rows(t, name, heads, d, tokens):
-    """A bf16 CUDA tensor [tokens][heads][d] whose tokens may lie further
-    apart than their rows need (a view of a packed projection): its address
-    and token stride in elements."""
+# The rotary and linear-attention calls are made once per layer and step, on
+# batches whose kernels take a few microseconds: their checks read each tensor
+# attribute once, and hand addresses over as plain ints.
+
+def _device() -> int:
+    """The current device's index: the library launches there, so every
+    tensor of a call has to be on it."""
+    return _torch()._C._cuda_getDevice()
+
+
+def _refuse(t, name, dtype, dev):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [{tokens}][{heads}][{d}], got {list(t.shape)}")
-    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _addr(t, name, dtype, dev, shape) -> int:
+    """Address of a contiguous CUDA tensor of the current device."""
+    if not hasattr(t, "data_ptr") or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, dev, shape):
+    """Address and token stride (in elements) of rows [tokens][heads][d] whose
+    tokens may lie further apart than their rows need (a view of a packed
+    projection)."""
+    if not hasattr(t, "data_ptr") or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    tokens, heads, d = shape
+    st, sh, sd = t.stride()
+    if tokens and (sd != 1 or (sh != d and heads > 1)):
         raise ValueError(f"{name}: a token's heads and dims must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if tokens > 1 else heads * d
+    return t.data_ptr(), st if tokens > 1 else heads * d
 
 
-def _same_device(first, *others):
-    """Every tensor on the current device: the library launches there."""
+def _out_addr(t, dev, shape) -> int:
+    """An fp32 output on the device or in page-locked host memory."""
+    if t.shape != shape:
+        raise ValueError(f"out must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != dev:
+        if t.is_cuda:
+            _refuse(t, "out", _torch().float32, dev)
+        return _out(t)
+    return _addr(t, "out", _torch().float32, dev, shape)
+
+
+def _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, tokens, dev) -> Rotary:
     torch = _torch()
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {first.device}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.is_cuda and t.device != first.device:
-            raise ValueError(f"tensors are on {first.device} and {t.device}")
-
-
-def _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, tokens) -> Rotary:
-    torch = _torch()
-    axes = 1 if positions.dim() == 1 else int(positions.shape[0])
-    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+    shape = positions.shape
+    if len(shape) not in (1, 2):
         raise ValueError("positions must be [num_tokens] or [num_axes][num_tokens]")
+    axes = 1 if len(shape) == 1 else shape[0]
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [rot_dim / 2]")
-    pairs = int(inv_freq.shape[0])
+    pairs = inv_freq.shape[0]
     if sections is None:
         if axes != 1:
             raise ValueError("several axes need sections")
-        sections = [pairs]
-    sections = [int(x) for x in sections]
+        sections = (pairs,)
     if len(sections) != axes or axes > 4:
         raise ValueError("sections must name the pairs of each of at most 4 axes")
     flags = (PKV_ROTARY_ADJACENT_PAIRS if adjacent_pairs else 0) | (
         PKV_ROTARY_INTERLEAVED_AXES if interleaved_axes else 0)
-    return Rotary(_dev(inv_freq, "inv_freq", dtype=torch.float32).value,
-                  _dev(positions, "positions", dtype=torch.int32).value, 2 * pairs, axes,
-                  (ctypes.c_int32 * 4)(*(sections + [0] * (4 - axes))), flags)
+    return Rotary(_addr(inv_freq, "inv_freq", torch.float32, dev, (pairs,)),
+                  _addr(positions, "positions", torch.int32, dev, (tokens,) if len(shape) == 1 else (axes, tokens)),
+                  2 * pairs, axes, _Sections(*sections), flags)
 
 
 def rotary(q, k, positions, inv_freq, sections=None, interleaved_axes: bool = False, adjacent_pairs: bool = False,
@@ -503,21 +543,22 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved_axes: bool = Fa
     Returns (q_out, k_out), contiguous; q_out may be q and k_out k."""
     torch = _torch()
     lib = load()
-    T, hq, d = q.shape
-    hkv = k.shape[1]
-    r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T)
-    qp, qs = _rows(q, "q", hq, d, T)
-    kp, ks = _rows(k, "k", hkv, d, T)
+    dev = _device()
+    bf16 = torch.bfloat16
+    qshape = T, hq, d = q.shape
+    kshape = (T, k.shape[1], d)
+    qp, qs = _rows(q, "q", bf16, dev, qshape)
+    kp, ks = _rows(k, "k", bf16, dev, kshape)
+    r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T, dev)
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty(qshape, dtype=bf16, device=q.device)
     if k_out is None:
-        k_out = torch.empty((T, hkv, d), dtype=torch.bfloat16, device=q.device)
-    if q_out.shape != (T, hq, d) or k_out.shape != (T, hkv, d):
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    _same_device(q, k, positions, inv_freq, q_out, k_out)
-    st = lib.pkv_rotary(ctypes.byref(r), qp, qs, hq, kp, ks, hkv, d, T, _dev(q_out, "q_out", dtype=torch.bfloat16),
-                        _dev(k_out, "k_out", dtype=torch.bfloat16), _stream_handle(stream))
-    _check(st, "pkv_rotary")
+        k_out = torch.empty(kshape, dtype=bf16, device=q.device)
+    st = lib.pkv_rotary(ctypes.byref(r), qp, qs, hq, kp, ks, kshape[1], d, T,
+                        _addr(q_out, "q_out", bf16, dev, qshape), _addr(k_out, "k_out", bf16, dev, kshape),
+                        _stream_handle(stream))
+    if st:
+        _check(st, "pkv_rotary")
     return q_out, k_out
 
 
@@ -529,57 +570,36 @@ def rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_fre
     scales; their codes come from the unrounded turned k."""
     torch = _torch()
     lib = load()
+    dev = _device()
+    bf16 = torch.bfloat16
     c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True)
-    T, hq, d = q.shape
-    r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T)
+    if k_pool.get_device() != dev or v_pool.get_device() != dev:
+        raise ValueError(f"the pools are on {k_pool.device} and {v_pool.device}, the current device is cuda:{dev}")
+    qshape = T, hq, d = q.shape
     if d != c.head_dim:
         raise ValueError("q head_dim does not match the pools")
-    if slot_mapping.dim() != 1 or slot_mapping.shape[0] != T:
-        raise ValueError("slot_mapping must be [num_tokens]")
-    qp, qs = _rows(q, "q", hq, d, T)
-    kp, ks = _rows(k, "k", c.num_kv_heads, d, T)
-    vp, vs = _rows(v, "v", c.num_kv_heads, d, T)
+    kshape = (T, c.num_kv_heads, d)
+    qp, qs = _rows(q, "q", bf16, dev, qshape)
+    kp, ks = _rows(k, "k", bf16, dev, kshape)
+    vp, vs = _rows(v, "v", bf16, dev, kshape)
+    r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T, dev)
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
-    if q_out.shape != (T, hq, d):
-        raise ValueError("q_out must have the shape of q")
-    _same_device(q, k, v, k_pool, v_pool, slot_mapping, positions, inv_freq, q_out)
+        q_out = torch.empty(qshape, dtype=bf16, device=q.device)
     st = lib.pkv_rotary_cache_write(ctypes.byref(c), ctypes.byref(r), qp, qs, hq, kp, ks, vp, vs,
-                                    _dev(slot_mapping, "slot_mapping", dtype=torch.int32), T,
-                                    _dev(q_out, "q_out", dtype=torch.bfloat16), _stream_handle(stream))
-    _check(st, "pkv_rotary_cache_write")
+                                    _addr(slot_mapping, "slot_mapping", torch.int32, dev, (T,)), T,
+                                    _addr(q_out, "q_out", bf16, dev, qshape), _stream_handle(stream))
+    if st:
+        _check(st, "pkv_rotary_cache_write")
     return q_out
 
 
-def _states(states, log_decay) -> States:
-    torch = _torch()
-    if states.dim() != 4 or states.shape[2] != states.shape[3]:
-        raise ValueError("states must be [num_slots][num_kv_heads][head_dim][head_dim]")
-    n, hkv, d, _ = states.shape
-    if log_decay.dim() != 1 or log_decay.shape[0] != hkv:
-        raise ValueError("log_decay must be [num_kv_heads]")
-    return States(_dev(states, "states", dtype=torch.float32).value,
-                  _dev(log_decay, "log_decay", dtype=torch.float32).value, n, hkv, d)
-
-
-def _linear_batch(s, q, k, v, state_slots, context_lens, new_slots, out):
-    torch = _torch()
-    T, hq, d = q.shape
-    if d != s.head_dim:
-        raise ValueError("q head_dim does not match the states")
-    S = int(context_lens.shape[0])
-    if state_slots.shape != (S,) or (new_slots is not None and new_slots.shape != (S,)):
-        raise ValueError("state_slots, new_slots and context_lens must be [num_seqs]")
-    rows = [x for name, t, h in (("q", q, hq), ("k", k, s.num_kv_heads), ("v", v, s.num_kv_heads))
-            for x in _rows(t, name, h, d, T)]
-    if out is None:
-        out = torch.empty((T, hq, d), dtype=torch.float32, device=q.device)
-    if out.shape != (T, hq, d):
-        raise ValueError("out must be [num_tokens][num_q_heads][head_dim]")
-    _same_device(q, k, v, state_slots, context_lens, new_slots, out)
-    slots = _dev(state_slots, "state_slots", dtype=torch.int32)
-    new = _dev(new_slots, "new_slots", dtype=torch.int32) if new_slots is not None else None
-    return rows, out, slots, new, _dev(context_lens, "context_lens", dtype=torch.int32), S
+def _states(states, log_decay, d, dev) -> States:
+    f32 = _torch().float32
+    shape = states.shape
+    if len(shape) != 4 or shape[2] != d or shape[3] != d:
+        raise ValueError(f"states must be [num_slots][num_kv_heads][{d}][{d}] for q's head_dim, got {list(shape)}")
+    return States(_addr(states, "states", f32, dev, shape), _addr(log_decay, "log_decay", f32, dev, (shape[1],)),
+                  shape[0], shape[1], d)
 
 
 def linear_decode_attention(states, log_decay, q, k, v, state_slots, context_lens, scale: float, new_slots=None,
@@ -589,15 +609,25 @@ def linear_decode_attention(states, log_decay, q, k, v, state_slots, context_len
     (stored to ``new_slots[s]`` when given), out = scale q^T S, float32
     [B][Hq][d].  context_lens counts the token: 1 starts from a zero state,
     0 marks padding."""
+    torch = _torch()
     lib = load()
-    s = _states(states, log_decay)
-    rows, out, slots, new, ctx, S = _linear_batch(s, q, k, v, state_slots, context_lens, new_slots, out)
-    if q.shape[0] != S:
-        raise ValueError("q must hold one token per sequence")
-    _same_device(q, states, log_decay)
-    st = lib.pkv_linear_decode_attention(ctypes.byref(s), rows[0], rows[1], q.shape[1], rows[2], rows[3], rows[4],
-                                         rows[5], slots, new, ctx, S, float(scale), _out(out), _stream_handle(stream))
-    _check(st, "pkv_linear_decode_attention")
+    dev = _device()
+    bf16, i32 = torch.bfloat16, torch.int32
+    qshape = B, hq, d = q.shape
+    s = _states(states, log_decay, d, dev)
+    kshape, per_seq = (B, s.num_kv_heads, d), (B,)
+    qp, qs = _rows(q, "q", bf16, dev, qshape)
+    kp, ks = _rows(k, "k", bf16, dev, kshape)
+    vp, vs = _rows(v, "v", bf16, dev, kshape)
+    if out is None:
+        out = torch.empty(qshape, dtype=torch.float32, device=q.device)
+    st = lib.pkv_linear_decode_attention(
+        ctypes.byref(s), qp, qs, hq, kp, ks, vp, vs, _addr(state_slots, "state_slots", i32, dev, per_seq),
+        None if new_slots is None else _addr(new_slots, "new_slots", i32, dev, per_seq),
+        _addr(context_lens, "context_lens", i32, dev, per_seq), B, scale, _out_addr(out, dev, qshape),
+        _stream_handle(stream))
+    if st:
+        _check(st, "pkv_linear_decode_attention")
     return out
 
 
@@ -616,25 +646,36 @@ def linear_prefill_attention(states, log_decay, q, k, v, query_start_loc, state_
     starts from zero when it has no others."""
     torch = _torch()
     lib = load()
-    s = _states(states, log_decay)
-    rows, out, slots, new, ctx, S = _linear_batch(s, q, k, v, state_slots, context_lens, new_slots, out)
-    T, hq, d = q.shape
-    if query_start_loc.shape != (S + 1,):
-        raise ValueError("query_start_loc must have num_seqs + 1 entries")
-    if query_start_loc_host is None:
-        query_start_loc_host = query_start_loc
-    qh, qhp = _host_i32(query_start_loc_host)
+    dev = _device()
+    bf16, i32 = torch.bfloat16, torch.int32
+    qshape = T, hq, d = q.shape
+    s = _states(states, log_decay, d, dev)
+    S = context_lens.shape[0]
+    kshape, per_seq = (T, s.num_kv_heads, d), (S,)
+    qp, qs = _rows(q, "q", bf16, dev, qshape)
+    kp, ks = _rows(k, "k", bf16, dev, kshape)
+    vp, vs = _rows(v, "v", bf16, dev, kshape)
+    qh = query_start_loc if query_start_loc_host is None else query_start_loc_host
+    if isinstance(qh, torch.Tensor) and qh.dtype is i32 and not qh.is_cuda and qh.is_contiguous():
+        qhp = qh.data_ptr()
+    else:
+        qh, qhp = _host_i32(qh)
     if qh.shape != (S + 1,):
         raise ValueError("query_start_loc_host must have num_seqs + 1 entries")
+    if out is None:
+        out = torch.empty(qshape, dtype=torch.float32, device=q.device)
     if workspace is None:
-        need = lib.pkv_linear_prefill_workspace_size(S, T, hq, s.num_kv_heads, d)
+        need = lib.pkv_linear_prefill_workspace_size(S, T, hq, kshape[1], d)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _same_device(q, states, log_decay, query_start_loc, workspace)
     st = lib.pkv_linear_prefill_attention(
-        ctypes.byref(s), rows[0], rows[1], hq, rows[2], rows[3], rows[4], rows[5], T,
-        _dev(query_start_loc, "query_start_loc", dtype=torch.int32), qhp, slots, new, ctx, S, float(scale), _out(out),
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    _check(st, "pkv_linear_prefill_attention")
+        ctypes.byref(s), qp, qs, hq, kp, ks, vp, vs, T,
+        _addr(query_start_loc, "query_start_loc", i32, dev, (S + 1,)), qhp,
+        _addr(state_slots, "state_slots", i32, dev, per_seq),
+        None if new_slots is None else _addr(new_slots, "new_slots", i32, dev, per_seq),
+        _addr(context_lens, "context_lens", i32, dev, per_seq), S, scale, _out_addr(out, dev, qshape),
+        _addr(workspace, "workspace", workspace.dtype, dev, workspace.shape), workspace.nbytes, _stream_handle(stream))
+    if st:
+        _check(st, "pkv_linear_prefill_attention")
     return out
 
 

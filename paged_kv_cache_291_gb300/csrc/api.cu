@@ -859,7 +859,7 @@ pkv_status fill_linear(const pkv_states_t* states, const void* q, int64_t q_stri
 
 pkv_status check_states(const pkv_states_t* s, int32_t num_q_heads) {
     if (s == nullptr) return PKV_ERR_NULL;
-    if (s->num_slots < 0 || s->num_kv_heads < 1) return PKV_ERR_SHAPE;
+    if (s->num_slots < 0 || s->num_kv_heads < 1 || s->num_kv_heads > 65535) return PKV_ERR_SHAPE;
     if (s->head_dim != 64 && s->head_dim != 128) return PKV_ERR_HEADDIM;
     return check_heads(num_q_heads, s->num_kv_heads);
 }
@@ -888,7 +888,10 @@ PKV_API size_t pkv_linear_prefill_workspace_size(int32_t num_seqs, int32_t num_t
                                                  int32_t num_kv_heads, int32_t head_dim) {
     if (num_seqs < 0 || num_tokens < 0 || check_heads(num_q_heads, num_kv_heads) != PKV_OK) return 0;
     if (head_dim != 64 && head_dim != 128) return 0;
-    return 256;
+    DeviceState* dev = nullptr;
+    if (current_device(&dev) != PKV_OK) return 0;
+    const size_t bounds = static_cast<size_t>(pkv::linear_max_bounds(num_tokens, num_kv_heads, dev->num_sms));
+    return std::max<size_t>(256, bounds * num_kv_heads * head_dim * head_dim * sizeof(float));
 }
 
 PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
@@ -907,17 +910,22 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
     for (int32_t s = 0; s < num_seqs; ++s)
         if (query_start_loc_host[s + 1] < query_start_loc_host[s]) return PKV_ERR_SHAPE;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return PKV_ERR_WORKSPACE;
-    if (workspace_bytes < pkv_linear_prefill_workspace_size(num_seqs, num_tokens, num_q_heads, states->num_kv_heads,
-                                                            states->head_dim))
-        return PKV_ERR_WORKSPACE;
+    if (workspace_bytes < 256) return PKV_ERR_WORKSPACE;
     DeviceState* dev = nullptr;
     pkv::LinearArgs a;
     if ((st = fill_linear(states, q, q_stride, num_q_heads, k, k_stride, v, v_stride, state_slots, new_slots,
                           context_lens, num_seqs, num_tokens, scale, out, &a, &dev)) != PKV_OK)
         return st;
+    const size_t need = static_cast<size_t>(pkv::linear_max_bounds(num_tokens, a.num_kv_heads, dev->num_sms)) *
+                        a.num_kv_heads * a.head_dim * a.head_dim * sizeof(float);
+    if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
     a.query_start_loc = query_start_loc;
-    a.max_recurrent = INT32_MAX;
-    cudaError_t e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
+    a.max_recurrent = 16;
+    const pkv::LinearPlan plan = pkv::plan_linear(query_start_loc_host, num_seqs, num_tokens, a.num_kv_heads,
+                                                  num_q_heads / a.num_kv_heads, dev->num_sms, a.max_recurrent);
+    cudaError_t e = cudaSuccess;
+    if (plan.recurrent > 0) e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = pkv::launch_linear_chunks(a, plan, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
 #pragma unroll
         for (int i = 0; i < RPT; ++i) S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    if (tid == 0) lam_s = decay_pair(clean_log_decay(A, h, s == 0 && slice == 0), 1);
+    if (tid == 0) lam_s = decay_pair(clean_log_decay(A, h, true), 1);
     if (first && q.store >= 0) {
         // A slot that two sequences store to, or that one stores to and
         // another reads, has no defined content: reported.

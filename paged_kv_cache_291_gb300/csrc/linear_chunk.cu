@@ -1,0 +1,905 @@
+// linear_chunk.cu -- linear attention with a decay for each head, chunked
+// form on tcgen05 tensor cores.
+//
+// Mathematics.  The recurrence S <- lam S + k v^T, o = scale q^T S over a
+// chunk of C = 64 tokens (t, s count inside it, S is the state before it):
+//     P[s][t]  = scale lam^(t-s) (k_s . q_t)   for s <= t, else 0
+//     O^T      = scale lam^(t+1) (S^T Q^T)[.][t] + V^T P
+//     S^T     <- lam^C S^T + (V~)^T K,         V~_s = lam^(C-1-s) v_s
+// Four products of bf16 inputs with fp32 sums, held transposed so that every
+// one has the v index (or s) in the 128 tensor-memory lanes, S^T can stay in
+// tensor memory as an accumulator and be read from there as an operand, and
+// an output column is a coalesced row segment.
+//
+// Precision.  q, k and v are exact in bf16; S, P and V~ are fp32 values.  Each
+// is split into three bf16 terms by truncation (8 + 8 + 8 bits: exact), and
+// its product is taken three times, so the result is an fp32 one.  Two terms
+// (16 bits) would be off by 2^-17 of each value.  The state's decay factor is
+// an fp32 pair.
+//
+// Split.  A CTA takes one kv head of one piece of a sequence and walks its
+// chunks; all q heads of the group share the state's work.  Warps: 0-1 P (a
+// lane holds one s), 2 TMA loads, 3 MMA issue, 4-7 S (read, split, decay),
+// 8-11 V~, 12-15 the output.  K, V and Q tiles come through rings of three
+// 128-byte-swizzled stages.
+// Few (sequence, head) pairs leave SMs idle, so sequences are cut into pieces
+// of equal chunk counts: linear_state_kernel sums each piece's own state
+// (all but the last of a sequence), linear_scan_kernel carries the states
+// over the pieces, and the main kernel starts each piece from its own.
+//
+// Every wait is bounded; TMEM is freed on every exit path.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "linear_device.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int C = 64;                    // tokens per chunk
+constexpr int kPanel = C * 128;          // [64 tokens][64 dims] bf16, 128-byte swizzle
+constexpr int kTile = 2 * kPanel;        // room for head_dim 128
+constexpr int kStages = 3;
+
+constexpr int OFF_K = 0;
+constexpr int OFF_V = OFF_K + kStages * kTile;
+constexpr int OFF_Q = OFF_V + kStages * kTile;
+constexpr int OFF_VT = OFF_Q + kStages * kTile;       // V~: three terms
+constexpr int OFF_P = OFF_VT + 3 * kTile;             // P: three terms of [64 s][64 t]
+constexpr int OFF_TAB = OFF_P + 3 * kPanel;           // factors
+constexpr int TAB_P = 0;                              // float[128]: scale lam^(t-s) at 63 + t - s
+constexpr int TAB_O = 128;                            // float[64]: scale lam^(t+1)
+constexpr int TAB_V = 192;                            // float[64]: lam^j
+constexpr int TAB_LAM = 256;                          // float2[2]: lam^64, lam^(tail rows)
+constexpr int OFF_BAD = OFF_TAB + 264 * 4;            // int[4][128], see kBadBuffers
+constexpr int OFF_BAR = OFF_BAD + 4 * 128 * 4;
+constexpr int kBadBuffers = 4;
+
+enum {
+    B_KVFULL = 0,               // + stage
+    B_KVEMPTY = B_KVFULL + kStages,
+    B_QFULL = B_KVEMPTY + kStages,
+    B_QEMPTY = B_QFULL + kStages,
+    B_SCORES = B_QEMPTY + kStages,  // scores in TMEM
+    B_P,                        // P in shared memory (2 arrivals)
+    B_PFREE,                    // P read
+    B_S,                        // S split and decayed (4 arrivals)
+    B_SFREE,                    // the split S read by every q head of the chunk
+    B_VT,                       // V~ in shared memory (4 arrivals)
+    B_VTFREE,                   // V~ read, S holds the chunk
+    B_O,                        // outputs in TMEM
+    B_OFREE,                    // outputs read (4 arrivals)
+    NBAR
+};
+constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
+constexpr int OFF_TMEM = OFF_INFO + 16 * 4;
+constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;      // slack to align the base to 1024 B
+static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB)");
+static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
+
+constexpr int kThreads = 512;
+constexpr int kLoadWarp = 2, kMmaWarp = 3;
+
+// TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
+constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
+
+enum { I_SEQ = 0, I_ROW0, I_ROWS, I_FIRST, I_LAST, I_LOAD, I_STORE, I_BOUND, I_BAD };
+
+struct ChunkParams {
+    LinearArgs A;
+    float* bounds;          // fp32 [max_bounds][Hkv][d][d]: states between a sequence's pieces
+    int32_t max_bounds;
+    int32_t piece;          // chunks per piece
+    int32_t total;          // pieces the host counted
+};
+
+// Pieces of sequence s (0: the recurrent form takes it).
+__device__ __forceinline__ int pieces_of(const ChunkParams& P, int s) {
+    const int r0 = __ldg(P.A.query_start_loc + s), r1 = __ldg(P.A.query_start_loc + s + 1);
+    if (r0 < 0 || r1 > P.A.num_tokens || r1 - r0 <= P.A.max_recurrent) return 0;
+    return ((r1 - r0 + C - 1) / C + P.piece - 1) / P.piece;
+}
+
+struct PieceAt {
+    int seq, index, pieces;  // seq -1: none
+    int bound;               // boundaries of the sequences before
+    int total;               // entries of all sequences (only when `count`)
+};
+
+// Entry `at` of the pieces numbered over the sequences in order, the last
+// `skip` pieces of each left out.  One warp.
+__device__ __forceinline__ PieceAt find_piece(const ChunkParams& P, int at, int skip, bool count) {
+    const unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x % 32;
+    PieceAt r = {-1, 0, 0, 0, 0};
+    int base = 0, bounds = 0;
+    for (int s0 = 0; s0 < P.A.num_seqs && (r.seq < 0 || count); s0 += 32) {
+        const int np = s0 + lane < P.A.num_seqs ? pieces_of(P, s0 + lane) : 0;
+        const int ne = max(np - skip, 0), nb = max(np - 1, 0);
+        int incl = ne, binc = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(FULL, incl, o), u = __shfl_up_sync(FULL, binc, o);
+            if (lane >= o) incl += t, binc += u;
+        }
+        const unsigned hit = r.seq < 0 ? __ballot_sync(FULL, base + incl > at) : 0u;
+        if (hit) {
+            const int j = __ffs(hit) - 1;
+            r.seq = s0 + j;
+            r.index = at - (base + __shfl_sync(FULL, incl - ne, j));
+            r.pieces = __shfl_sync(FULL, np, j);
+            r.bound = bounds + __shfl_sync(FULL, binc - nb, j);
+        }
+        base += __shfl_sync(FULL, incl, 31);
+        bounds += __shfl_sync(FULL, binc, 31);
+    }
+    r.total = base;
+    return r;
+}
+
+// Two fp32 values as three packed bf16 pairs that sum to them exactly.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    hi = __byte_perm(ua, ub, 0x7632);
+    const float ra = a - __uint_as_float(ua & 0xffff0000u), rb = b - __uint_as_float(ub & 0xffff0000u);
+    const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
+    mid = __byte_perm(va, vb, 0x7632);
+    const float la = ra - __uint_as_float(va & 0xffff0000u), lb = rb - __uint_as_float(vb & 0xffff0000u);
+    lo = __byte_perm(__float_as_uint(la), __float_as_uint(lb), 0x7632);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity); }
+
+// V~ of one chunk, elementwise over the swizzled V tile: factor[rows - 1 - s]
+// * extra * v_s in three terms.  Rows past the piece become zero, there and in
+// K and V: they are other sequences' tokens, and a zero factor times a NaN
+// would poison the products.  Returns 0, or NaN if a value was not finite.
+template <int D, int THREADS>
+__device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t svt, const float* factor, float extra,
+                                           int rows, int tid) {
+    constexpr int kChunks = C * D * 2 / 16;  // 16-byte vectors of the tile
+    float acc = 0.f;
+#pragma unroll
+    for (int n = 0; n < kChunks / THREADS; ++n) {
+        const int i = n * THREADS + tid;
+        const int row = (i >> 3) & (C - 1);
+        const uint32_t at = static_cast<uint32_t>(i) * 16u;
+        if (row < rows) {
+            uint32_t x[4], hi[4], mid[4], lo[4];
+            tc::lds128(sv + at, x);
+            const float f = factor[rows - 1 - row] * extra;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = bf16lo(x[j]), b = bf16hi(x[j]);
+                acc = fmaf(a, 0.f, fmaf(b, 0.f, acc));
+                split3(a * f, b * f, hi[j], mid[j], lo[j]);
+            }
+            tc::sts128(svt + at, hi[0], hi[1], hi[2], hi[3]);
+            tc::sts128(svt + kTile + at, mid[0], mid[1], mid[2], mid[3]);
+            tc::sts128(svt + 2 * kTile + at, lo[0], lo[1], lo[2], lo[3]);
+        } else {
+            tc::sts128(svt + at, 0u, 0u, 0u, 0u);
+            tc::sts128(svt + kTile + at, 0u, 0u, 0u, 0u);
+            tc::sts128(svt + 2 * kTile + at, 0u, 0u, 0u, 0u);
+            tc::sts128(sv + at, 0u, 0u, 0u, 0u);
+            tc::sts128(sk + at, 0u, 0u, 0u, 0u);
+        }
+    }
+    return acc;
+}
+
+// S^T += (V~)^T K for one chunk, V~ in three terms: A is V~ stored [s][v]
+// (v contiguous), B is K stored [s][k] (k contiguous).
+template <int D>
+__device__ __forceinline__ void mma_state(uint32_t col_s, uint32_t svt, uint32_t sk, bool accumulate) {
+    constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 1, 1);
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int k = 0; k < C / 16; ++k)
+            tc::mma_bf16_ss(col_s, tc::smem_desc_sw128(svt + part * kTile + k * 2048, kPanel, 1024),
+                            tc::smem_desc_sw128(sk + k * 2048, kPanel, 1024), kIdesc,
+                            accumulate || part > 0 || k > 0 ? 1u : 0u);
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                        const __grid_constant__ CUtensorMap tm_v, const ChunkParams P) {
+    constexpr int kPanels = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    int* info = reinterpret_cast<int*>(smem + OFF_INFO);
+    float* tab = reinterpret_cast<float*>(smem + OFF_TAB);
+    int* bad_rows = reinterpret_cast<int*>(smem + OFF_BAD);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+    const LinearArgs& A = P.A;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int h = blockIdx.y;
+
+    // ---------------------------------------------------------- setup
+    griddep_launch_dependents();
+    if (threadIdx.x == 32 * kMmaWarp) {
+        for (int i = 0; i < NBAR; ++i)
+            mbar_init(&bar[i], i == B_P ? 2u : (i == B_S || i == B_VT || i == B_OFREE) ? 4u : 1u);
+        fence_mbar_init();
+    }
+    if (warp == kLoadWarp) {
+        tc::tmem_alloc(tmem_slot, kTmemCols);
+        tc::tmem_relinquish();
+        if (lane == 0) {
+            tc::prefetch_tensormap(&tm_q);
+            tc::prefetch_tensormap(&tm_k);
+            tc::prefetch_tensormap(&tm_v);
+        }
+    }
+    for (int i = threadIdx.x; i < kBadBuffers * 128; i += kThreads) bad_rows[i] = 0;
+    griddep_wait();
+    if (warp == 0) {
+        const bool last_entry = blockIdx.x == gridDim.x - 1;
+        const PieceAt at = find_piece(P, blockIdx.x, 0, last_entry && h == 0);
+        if (last_entry && h == 0 && at.total != P.total && lane == 0)
+            record_error(A.err, kErrRange, static_cast<uint32_t>(A.num_seqs));
+        int row0 = 0, rows = 0, load = -1, store = -1, bad = 0, bound = -1, last = 0;
+        if (at.seq >= 0) {
+            const LinearSeq q = linear_seq(A, at.seq, lane == 0 && h == 0 && at.index == 0);
+            const int skip = at.index * P.piece * C;
+            row0 = q.row0 + skip;
+            rows = min(q.rows - skip, P.piece * C);
+            last = at.index == at.pieces - 1;
+            bad = q.bad;
+            load = q.load;
+            store = last ? q.store : -1;
+            bound = at.index > 0 ? at.bound + at.index - 1 : -1;
+            if (bound >= P.max_bounds) {
+                if (lane == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(at.seq));
+                bad = 1;
+            }
+            if (h == 0 && at.index == 0 && !bad && q.store >= 0)
+                for (int o = lane; o < A.num_seqs; o += 32)
+                    if (o != at.seq && linear_shares(A, o, q.store))
+                        record_error(A.err, kErrAlias, static_cast<uint32_t>(at.seq));
+        }
+        if (lane == 0) {
+            info[I_SEQ] = at.seq;
+            info[I_ROW0] = row0;
+            info[I_ROWS] = rows;
+            info[I_LOAD] = load;
+            info[I_STORE] = store;
+            info[I_BOUND] = bound;
+            info[I_BAD] = bad;
+        }
+        const int tail = (rows - 1) % C + 1;
+        const float g = clean_log_decay(A, h, lane == 0);
+        if (lane < 2) {
+            const float2 x = decay_pair(g, lane == 0 ? C : tail);
+            tab[TAB_LAM + 2 * lane] = x.x;
+            tab[TAB_LAM + 2 * lane + 1] = x.y;
+        }
+        for (int j = lane; j < C; j += 32) {
+            const float x = expf(g * static_cast<float>(j));
+            tab[TAB_V + j] = x;
+            tab[TAB_P + 63 + j] = A.scale * x;
+            tab[TAB_P + j] = j < 63 ? 0.f : A.scale;
+            tab[TAB_O + j] = A.scale * expf(g * static_cast<float>(j + 1));
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const int row0 = info[I_ROW0], rows = info[I_ROWS], bad = info[I_BAD];
+    const int nch = bad ? 0 : (rows + C - 1) / C;
+    const int nitems = nch * G;
+    bool ok = true;
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------ TMA producer
+        for (int n = 0; n < nitems && ok; ++n) {
+            const int i = n / G, g = n % G;
+            if (g == 0) {
+                const int st = i % kStages;
+                if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kStages) & 1) ^ 1)) { ok = false; break; }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar[B_KVFULL + st], 2u * kPanels * kPanel);
+#pragma unroll
+                    for (int pn = 0; pn < kPanels; ++pn) {
+                        tc::tma_load_3d(smem + OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
+                                        &bar[B_KVFULL + st]);
+                        tc::tma_load_3d(smem + OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
+                                        &bar[B_KVFULL + st]);
+                    }
+                }
+                __syncwarp();
+            }
+            const int sq = n % kStages;
+            if (!warp_wait(&bar[B_QEMPTY + sq], ((n / kStages) & 1) ^ 1)) { ok = false; break; }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar[B_QFULL + sq], static_cast<uint32_t>(kPanels) * kPanel);
+#pragma unroll
+                for (int pn = 0; pn < kPanels; ++pn)
+                    tc::tma_load_3d(smem + OFF_Q + sq * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + g, row0 + i * C,
+                                    &bar[B_QFULL + sq]);
+            }
+            __syncwarp();
+        }
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------ MMA issuer
+        // Scores of item n + 1 go ahead of P V of item n, so that the P warps
+        // always have the next item's scores while the tensor cores work.
+        constexpr uint32_t kIdescScores = tc::idesc_bf16_f32(128, C, 0, 0);
+        constexpr uint32_t kIdescOS = tc::idesc_bf16_f32(128, C, 0, 0);
+        constexpr uint32_t kIdescOP = tc::idesc_bf16_f32(128, C, 1, 1);
+        const uint32_t sk0 = smem_addr(smem + OFF_K), sv0 = smem_addr(smem + OFF_V), sq0 = smem_addr(smem + OFF_Q);
+        const uint32_t svt = smem_addr(smem + OFF_VT), sp = smem_addr(smem + OFF_P);
+        // scores[s][t] = k_s . q_t (lanes past 63 take the rows that follow K in
+        // shared memory: never read)
+        auto scores = [&](int n) {
+            const uint32_t sk = sk0 + (n / G % kStages) * kTile, sq = sq0 + (n % kStages) * kTile;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
+                tc::mma_bf16_ss(tmem + COL_SCORES, tc::smem_desc_sw128(sk + off, 16, 1024),
+                                tc::smem_desc_sw128(sq + off, 16, 1024), kIdescScores, k > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(&bar[B_SCORES]);
+        };
+        // O_S^T[v][t] = sum_k S^T[v][k] q_t[k], S^T in three terms from TMEM
+        auto out_state = [&](int n) {
+            const uint32_t sq = sq0 + (n % kStages) * kTile;
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc::mma_bf16_ts(tmem + COL_OS, tmem + COL_SB + part * (D / 2) + 8 * k,
+                                    tc::smem_desc_sw128(sq + (k >> 2) * kPanel + (k & 3) * 32, 16, 1024), kIdescOS,
+                                    part > 0 || k > 0 ? 1u : 0u);
+            tc::mma_commit(&bar[B_QEMPTY + n % kStages]);
+        };
+        // O_P^T[v][t] = sum_s V[s][v] P[s][t], P in three terms
+        auto out_scores = [&](int n) {
+            const uint32_t sv = sv0 + (n / G % kStages) * kTile;
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+                for (int k = 0; k < C / 16; ++k)
+                    tc::mma_bf16_ss(tmem + COL_OP, tc::smem_desc_sw128(sv + k * 2048, kPanel, 1024),
+                                    tc::smem_desc_sw128(sp + part * kPanel + k * 2048, kPanel, 1024), kIdescOP,
+                                    part > 0 || k > 0 ? 1u : 0u);
+            if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kStages]);
+            tc::mma_commit(&bar[B_PFREE]);
+            tc::mma_commit(&bar[B_O]);  // last: once it is seen, nothing of this thread is in flight
+        };
+        if (nitems > 0) {
+            ok = warp_wait(&bar[B_KVFULL], 0) && warp_wait(&bar[B_QFULL], 0);
+            if (ok && lane == 0) scores(0);
+            __syncwarp();
+        }
+        for (int n = 0; n < nitems && ok; ++n) {
+            const int i = n / G, g = n % G;
+            if (g == 0) {
+                if (!warp_wait(&bar[B_S], i & 1) || !warp_wait(&bar[B_VT], i & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    mma_state<D>(tmem + COL_S, svt, sk0 + (i % kStages) * kTile, true);
+                    tc::mma_commit(&bar[B_VTFREE]);
+                }
+                __syncwarp();
+            }
+            if (n > 0 && !warp_wait(&bar[B_OFREE], (n - 1) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            if (lane == 0) {
+                out_state(n);
+                if (g == G - 1) tc::mma_commit(&bar[B_SFREE]);
+            }
+            __syncwarp();
+            if (!warp_wait(&bar[B_P], n & 1)) { ok = false; break; }
+            if (n + 1 < nitems) {
+                const int i1 = (n + 1) / G;
+                if (i1 != i && !warp_wait(&bar[B_KVFULL + i1 % kStages], (i1 / kStages) & 1)) { ok = false; break; }
+                if (!warp_wait(&bar[B_QFULL + (n + 1) % kStages], ((n + 1) / kStages) & 1)) { ok = false; break; }
+            }
+            tc::fence_after_sync();
+            if (lane == 0) {
+                if (n + 1 < nitems) scores(n + 1);
+                out_scores(n);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 2) {
+        // ------------------------------------------------------ P
+        const int s = 32 * warp + lane;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + COL_SCORES;
+        const uint32_t prow = smem_addr(smem + OFF_P) + s * 128;
+        const float* f = tab + TAB_P + 63 - s;
+        for (int n = 0; n < nitems && ok; ++n) {
+            if (!warp_wait(&bar[B_SCORES], n & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            uint32_t x[2][32];
+            tc::tmem_ld32x32b_x32(taddr, x[0]);
+            tc::tmem_ld32x32b_x32(taddr + 32, x[1]);
+            tc::tmem_wait_ld();
+            if (n > 0 && !warp_wait(&bar[B_PFREE], (n - 1) & 1)) { ok = false; break; }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = 8 * c + 2 * j;
+                    // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
+                    const float a = t >= s ? __uint_as_float(x[t >> 5][t & 31]) * f[t] : 0.f;
+                    const float b = t + 1 >= s ? __uint_as_float(x[t >> 5][(t & 31) + 1]) * f[t + 1] : 0.f;
+                    split3(a, b, hi[j], mid[j], lo[j]);
+                }
+                const uint32_t at = prow + ((c ^ (s & 7)) << 4);
+                tc::sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                tc::sts128(at + kPanel, mid[0], mid[1], mid[2], mid[3]);
+                tc::sts128(at + 2 * kPanel, lo[0], lo[1], lo[2], lo[3]);
+            }
+            tc::fence_proxy_async_smem();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_P]);
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ------------------------------------------------------ S
+        // Lane = v index.  Chunk 0 takes the state from memory, later ones
+        // from the accumulator; each leaves the three terms of S for the
+        // outputs and lam^rows S for the update.
+        const int w = warp - 4, dv = 32 * w + lane;
+        const bool live = 32 * w < D;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        const int64_t head = static_cast<int64_t>(D) * D;
+        const float* from = nullptr;
+        if (info[I_BOUND] >= 0)
+            from = P.bounds + (static_cast<int64_t>(info[I_BOUND]) * A.num_kv_heads + h) * head + dv;
+        else if (info[I_LOAD] >= 0)
+            from = A.states + (static_cast<int64_t>(info[I_LOAD]) * A.num_kv_heads + h) * head + dv;
+        for (int i = 0; i < nch && ok; ++i) {
+            if (i > 0 && !warp_wait(&bar[B_SFREE], (i - 1) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            const int which = i == nch - 1 ? 1 : 0;
+            const float2 lam = make_float2(tab[TAB_LAM + 2 * which], tab[TAB_LAM + 2 * which + 1]);
+            if (live) {
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t x[32];
+                    if (i > 0) {
+                        tc::tmem_ld32x32b_x32(tl + COL_S + 32 * b, x);
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[j] = from != nullptr ? __float_as_uint(from[(32 * b + j) * D]) : 0u;
+                    }
+                    uint32_t hi[16], mid[16], lo[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = __uint_as_float(x[2 * j]), c = __uint_as_float(x[2 * j + 1]);
+                        split3(a, c, hi[j], mid[j], lo[j]);
+                        x[2 * j] = __float_as_uint(fmaf(a, lam.x, a * lam.y));
+                        x[2 * j + 1] = __float_as_uint(fmaf(c, lam.x, c * lam.y));
+                    }
+                    tc::tmem_st32x32b_x16(tl + COL_SB + 16 * b, hi);
+                    tc::tmem_st32x32b_x16(tl + COL_SB + D / 2 + 16 * b, mid);
+                    tc::tmem_st32x32b_x16(tl + COL_SB + D + 16 * b, lo);
+                    tc::tmem_st32x32b_x32(tl + COL_S + 32 * b, x);
+                }
+                tc::tmem_wait_st();
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_S]);
+        }
+        if (ok && nch > 0 && info[I_STORE] >= 0 && live) {
+            if (!warp_wait(&bar[B_VTFREE], (nch - 1) & 1)) {
+                ok = false;
+            } else {
+                tc::fence_after_sync();
+                float* to = A.states + (static_cast<int64_t>(info[I_STORE]) * A.num_kv_heads + h) * head + dv;
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t x[32];
+                    tc::tmem_ld32x32b_x32(tl + COL_S + 32 * b, x);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) to[(32 * b + j) * D] = __uint_as_float(x[j]);
+                }
+            }
+        }
+    } else if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------------ V~
+        const int tid = threadIdx.x - 256;
+        for (int i = 0; i < nch && ok; ++i) {
+            const int st = i % kStages;
+            if (!warp_wait(&bar[B_KVFULL + st], (i / kStages) & 1)) { ok = false; break; }
+            if (i > 0 && !warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
+            const int nrows = min(C, rows - i * C);
+            const uint32_t sk = smem_addr(smem + OFF_K + st * kTile), sv = smem_addr(smem + OFF_V + st * kTile);
+            const float acc = convert_v<D, 128>(sk, sv, smem_addr(smem + OFF_VT), tab + TAB_V, 1.f, nrows, tid);
+            if (acc != 0.f) {
+                // A value that is not finite reaches the outputs of its column
+                // from its row on, and no earlier row: it leaves V for P V
+                // (V~ carries it into the state), and its row is noted.
+                for (int c = tid; c < C * D * 2 / 16; c += 128) {
+                    const int row = (c >> 3) & (C - 1);
+                    if (row >= nrows) continue;
+                    uint32_t x[4];
+                    tc::lds128(sv + c * 16, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t u = (x[e / 2] >> (16 * (e % 2))) & 0xffffu;
+                        if ((u & 0x7f80u) == 0x7f80u) {
+                            x[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
+                            const int col = (c >> 9) * 64 + (((c & 7) ^ (row & 7)) << 3) + e;
+                            atomicMax(&bad_rows[(i % kBadBuffers) * 128 + col], ((i + 1) << 6) | (C - 1 - row));
+                        }
+                    }
+                    tc::sts128(sv + c * 16, x[0], x[1], x[2], x[3]);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_VT]);
+        }
+    } else if (warp >= 12) {
+        // ------------------------------------------------------ outputs
+        // Lane = v index, column = token: a warp stores 32 consecutive floats of a row.
+        const int w = warp - 12, dv = 32 * w + lane;
+        const bool live = 32 * w < D;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        const int64_t row_step = static_cast<int64_t>(A.num_q_heads) * D;
+        for (int n = 0; n < nitems && ok; ++n) {
+            const int i = n / G, g = n % G;
+            if (!warp_wait(&bar[B_O], n & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            const int nrows = min(C, rows - i * C);
+            float* o = A.out + (static_cast<int64_t>(row0) + i * C) * row_step + (h * G + g) * D + dv;
+            const int mark = live ? bad_rows[(i % kBadBuffers) * 128 + dv] : 0;
+            const int nan_from = (mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C;
+#pragma unroll
+            for (int b = 0; b < C / 32; ++b) {
+                uint32_t xs[32], xp[32];
+                if (live) {
+                    tc::tmem_ld32x32b_x32(tl + COL_OS + 32 * b, xs);
+                    tc::tmem_ld32x32b_x32(tl + COL_OP + 32 * b, xp);
+                    tc::tmem_wait_ld();
+                }
+                if (b == C / 32 - 1) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[B_OFREE]);
+                }
+                if (live) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int t = 32 * b + j;
+                        float y = fmaf(tab[TAB_O + t], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                        if (t >= nan_from) y = __int_as_float(0x7fffffff);
+                        if (t < nrows) o[t * row_step] = y;
+                    }
+                }
+            }
+        }
+    }
+    if (bad && rows > 0) {
+        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(rows) * G * D; i += kThreads)
+            A.out[(row0 + i / (G * D)) * static_cast<int64_t>(A.num_q_heads) * D + h * G * D + i % (G * D)] = 0.f;
+    }
+    if (!ok) record_error(A.err, kErrTimeout, 0x200u + static_cast<uint32_t>(warp));
+    // ---------------------------------------------------------- teardown
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == kLoadWarp) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- pieces' own states
+// A piece's own state from zero: sum_s lam^(end-1-s) k_s v_s^T over all its
+// tokens, one accumulation with no rescaling (the factor of a chunk's end is
+// part of V~).  Warps 0-7 V~, 8 loads, 9 MMA; warps 0-3 store the sum.
+constexpr int kStateThreads = 320;
+constexpr int SOFF_K = 0;
+constexpr int SOFF_V = SOFF_K + kStages * kTile;
+constexpr int SOFF_VT = SOFF_V + kStages * kTile;     // two buffers of three terms
+constexpr int SOFF_TAB = SOFF_VT + 2 * 3 * kTile;
+constexpr int SOFF_BAR = SOFF_TAB + C * 4;
+enum { SB_FULL = 0, SB_EMPTY = kStages, SB_VT = 2 * kStages, SB_VTFREE = SB_VT + 2, SB_DONE = SB_VTFREE + 2, SNBAR };
+constexpr int SOFF_INFO = SOFF_BAR + SNBAR * 8;
+constexpr int SOFF_TMEM = SOFF_INFO + 8 * 4;
+constexpr int STATE_SMEM = SOFF_TMEM + 16 + 1024;
+static_assert(STATE_SMEM <= 232448, "shared memory budget (227 KB)");
+static_assert(2 * STATE_SMEM > 228 * 1024, "one CTA per SM");
+
+template <int D>
+__global__ void __launch_bounds__(kStateThreads, 1)
+    linear_state_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const ChunkParams P) {
+    constexpr int kPanels = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + SOFF_BAR);
+    int* info = reinterpret_cast<int*>(smem + SOFF_INFO);
+    float* tab = reinterpret_cast<float*>(smem + SOFF_TAB);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SOFF_TMEM);
+    const LinearArgs& A = P.A;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int h = blockIdx.y;
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < SNBAR; ++i) mbar_init(&bar[i], i == SB_VT || i == SB_VT + 1 ? 8u : 1u);
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tc::tmem_alloc(tmem_slot, 128);
+        tc::tmem_relinquish();
+        if (lane == 0) {
+            tc::prefetch_tensormap(&tm_k);
+            tc::prefetch_tensormap(&tm_v);
+        }
+    }
+    griddep_wait();
+    if (warp == 0) {
+        const PieceAt at = find_piece(P, blockIdx.x, 1, false);
+        int row0 = 0, rows = 0, bound = 0;
+        if (at.seq >= 0) {
+            const LinearSeq q = linear_seq(A, at.seq, false);
+            row0 = q.row0 + at.index * P.piece * C;
+            rows = q.bad ? 0 : P.piece * C;
+            bound = at.bound + at.index;
+            if (bound >= P.max_bounds) rows = 0;
+        }
+        if (lane == 0) {
+            info[0] = row0;
+            info[1] = rows;
+            info[2] = bound;
+        }
+    }
+    const float g = clean_log_decay(A, h, false);
+    if (threadIdx.x < C) tab[threadIdx.x] = expf(g * static_cast<float>(threadIdx.x));
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const int row0 = info[0], nch = info[1] / C;
+    bool ok = true;
+    if (warp == 8) {
+        for (int i = 0; i < nch && ok; ++i) {
+            const int st = i % kStages;
+            if (!warp_wait(&bar[SB_EMPTY + st], ((i / kStages) & 1) ^ 1)) { ok = false; break; }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar[SB_FULL + st], 2u * kPanels * kPanel);
+#pragma unroll
+                for (int pn = 0; pn < kPanels; ++pn) {
+                    tc::tma_load_3d(smem + SOFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
+                                    &bar[SB_FULL + st]);
+                    tc::tma_load_3d(smem + SOFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
+                                    &bar[SB_FULL + st]);
+                }
+            }
+            __syncwarp();
+        }
+    } else if (warp == 9) {
+        for (int i = 0; i < nch && ok; ++i) {
+            const int st = i % kStages, vb = i & 1;
+            if (!warp_wait(&bar[SB_VT + vb], (i >> 1) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            if (lane == 0) {
+                mma_state<D>(tmem, smem_addr(smem + SOFF_VT + vb * 3 * kTile), smem_addr(smem + SOFF_K + st * kTile),
+                             i > 0);
+                tc::mma_commit(&bar[SB_EMPTY + st]);
+                tc::mma_commit(&bar[SB_VTFREE + vb]);
+                if (i == nch - 1) tc::mma_commit(&bar[SB_DONE]);
+            }
+            __syncwarp();
+        }
+    } else {
+        for (int i = 0; i < nch && ok; ++i) {
+            const int st = i % kStages, vb = i & 1;
+            if (!warp_wait(&bar[SB_FULL + st], (i / kStages) & 1)) { ok = false; break; }
+            if (!warp_wait(&bar[SB_VTFREE + vb], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
+            convert_v<D, 256>(smem_addr(smem + SOFF_K + st * kTile), smem_addr(smem + SOFF_V + st * kTile),
+                              smem_addr(smem + SOFF_VT + vb * 3 * kTile), tab,
+                              expf(g * static_cast<float>((nch - 1 - i) * C)), C, threadIdx.x);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[SB_VT + vb]);
+        }
+        if (ok && nch > 0 && 32 * warp < D) {
+            if (!warp_wait(&bar[SB_DONE], 0)) {
+                ok = false;
+            } else {
+                tc::fence_after_sync();
+                float* to = P.bounds + (static_cast<int64_t>(info[2]) * A.num_kv_heads + h) * D * D + 32 * warp + lane;
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    uint32_t x[32];
+                    tc::tmem_ld32x32b_x32(tmem + (static_cast<uint32_t>(32 * warp) << 16) + 32 * b, x);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) to[(32 * b + j) * D] = __uint_as_float(x[j]);
+                }
+            }
+        }
+    }
+    if (!ok) record_error(A.err, kErrTimeout, 0x300u + static_cast<uint32_t>(warp));
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 8) tc::tmem_dealloc(tmem, 128);
+}
+
+// The states before each piece but the first, from the pieces' own:
+// bounds[j] <- lam^(piece tokens) (state before) + bounds[j], in order.
+// Grid (sequences * d^2 / 1024, Hkv); a thread carries four elements.
+__global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkParams P) {
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ int info[3];
+    __shared__ float2 lam_s;
+    const LinearArgs& A = P.A;
+    const int slices = A.head_dim * A.head_dim / 1024;
+    const int h = blockIdx.y, s = blockIdx.x / slices;
+    if (threadIdx.x < 32) {
+        int base = 0;
+        for (int o = threadIdx.x; o < s; o += 32) base += max(pieces_of(P, o) - 1, 0);
+        base = __reduce_add_sync(0xffffffffu, base);
+        if (threadIdx.x == 0) {
+            const LinearSeq q = linear_seq(A, s, false);
+            info[0] = base;
+            info[1] = q.bad ? 0 : pieces_of(P, s) - 1;
+            info[2] = q.load;
+        }
+    } else if (threadIdx.x == 32) {
+        lam_s = decay_pair(clean_log_decay(A, h, false), P.piece * C);
+    }
+    __syncthreads();
+    const int base = info[0], n = min(info[1], P.max_bounds - info[0]);
+    if (n <= 0) return;
+    const float2 lam = lam_s;
+    const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
+    const int64_t e = (blockIdx.x % slices * 256 + threadIdx.x) * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (info[2] >= 0)
+        x = *reinterpret_cast<const float4*>(A.states + (static_cast<int64_t>(info[2]) * A.num_kv_heads + h) * head + e);
+    float* p = P.bounds + (static_cast<int64_t>(base) * A.num_kv_heads + h) * head + e;
+    const int64_t step = static_cast<int64_t>(A.num_kv_heads) * head;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+        const float4 y = *reinterpret_cast<const float4*>(p + j * step);
+        x.x = fmaf(x.x, lam.x, fmaf(x.x, lam.y, y.x));
+        x.y = fmaf(x.y, lam.x, fmaf(x.y, lam.y, y.y));
+        x.z = fmaf(x.z, lam.x, fmaf(x.z, lam.y, y.z));
+        x.w = fmaf(x.w, lam.x, fmaf(x.w, lam.y, y.w));
+        *reinterpret_cast<float4*>(p + j * step) = x;
+    }
+}
+
+bool rows_map(CUtensorMap* map, const void* base, int64_t stride, int32_t heads, int32_t d, int32_t tokens) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, 1, C};
+    return make_bf16_map(map, base, 3, dims, strides, box);
+}
+
+template <typename K>
+cudaError_t configure(K kernel, int smem, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <int D, int G>
+cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
+                        cudaStream_t stream) {
+    static bool done[64] = {};
+    cudaError_t e = configure(linear_chunk_kernel<D, G>, SMEM_BYTES, done);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.total, P.A.num_kv_heads), dim3(kThreads), SMEM_BYTES,
+                             stream, tq, tk, tv, P);
+}
+
+template <int D>
+cudaError_t launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
+                       int32_t bounds, cudaStream_t stream) {
+    if (bounds > 0) {
+        static bool done[64] = {};
+        cudaError_t e = configure(linear_state_kernel<D>, STATE_SMEM, done);
+        if (e != cudaSuccess) return e;
+        e = launch_overlapped(linear_state_kernel<D>, dim3(bounds, P.A.num_kv_heads), dim3(kStateThreads), STATE_SMEM,
+                              stream, tk, tv, P);
+        if (e != cudaSuccess) return e;
+        e = launch_overlapped(linear_scan_kernel, dim3(P.A.num_seqs * (D * D / 1024), P.A.num_kv_heads), dim3(256), 0,
+                              stream, P);
+        if (e != cudaSuccess) return e;
+    }
+    switch (P.A.num_q_heads / P.A.num_kv_heads) {
+        case 1: return launch_main<D, 1>(tq, tk, tv, P, stream);
+        case 2: return launch_main<D, 2>(tq, tk, tv, P, stream);
+        case 4: return launch_main<D, 4>(tq, tk, tv, P, stream);
+        default: return launch_main<D, 8>(tq, tk, tv, P, stream);
+    }
+}
+
+}  // namespace
+
+int32_t linear_max_bounds(int32_t num_tokens, int32_t num_kv_heads, int num_sms) {
+    const int32_t fill = (2 * num_sms + num_kv_heads - 1) / num_kv_heads;
+    return num_tokens / C < fill ? num_tokens / C : fill;
+}
+
+LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t group,
+                       int num_sms, int32_t max_recurrent) {
+    LinearPlan best = {0, 1, 0, 0, linear_max_bounds(num_tokens, num_kv_heads, num_sms)};
+    int64_t chunks = 0, longest = 0;
+    for (int32_t s = 0; s < num_seqs; ++s) {
+        const int32_t rows = qsl[s + 1] - qsl[s];
+        if (rows > 0 && rows <= max_recurrent) ++best.recurrent;
+        if (rows <= max_recurrent) continue;
+        const int64_t n = (rows + C - 1) / C;
+        chunks += n;
+        longest = n > longest ? n : longest;
+    }
+    if (longest == 0) return best;
+    // Microseconds of a chunk and of a launch in the main and in the state
+    // kernel.  Cutting pays when one piece per (sequence, head) would leave
+    // most SMs idle; it costs the state kernel's pass over K and V.
+    const double chunk = 1.0 + 0.9 * group, state = 0.7, start = 5.0, join = 7.0;
+    auto span = [&](int64_t ctas, int64_t piece, int64_t work, double c) {
+        if (ctas <= num_sms) return piece * c;
+        const double even = static_cast<double>(work) * num_kv_heads * c / num_sms + 0.5 * piece * c;
+        return even > piece * c ? even : piece * c;
+    };
+    double best_us = 1e30;
+    int64_t last = 0;
+    for (int32_t cuts : {1, 2, 3, 4, 5, 6, 8, 9, 10, 12, 14, 16, 19, 24, 32, 38, 50, 64, 76, 100, 152}) {
+        const int64_t piece = (longest + cuts - 1) / cuts;
+        if (piece == last) continue;
+        last = piece;
+        int64_t pieces = 0, seqs = 0;
+        for (int32_t s = 0; s < num_seqs; ++s) {
+            const int32_t rows = qsl[s + 1] - qsl[s];
+            if (rows <= max_recurrent) continue;
+            pieces += ((rows + C - 1) / C + piece - 1) / piece;
+            ++seqs;
+        }
+        const int64_t bounds = pieces - seqs;
+        if (bounds > best.max_bounds) break;
+        double us = start + span(pieces * num_kv_heads, piece, chunks, chunk);
+        if (bounds > 0) us += join + span(bounds * num_kv_heads, piece, bounds * piece, state);
+        if (us < best_us) {
+            best_us = us;
+            best.piece_chunks = static_cast<int32_t>(piece);
+            best.pieces = static_cast<int32_t>(pieces);
+            best.bounds = static_cast<int32_t>(bounds);
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, cudaStream_t stream) {
+    if (plan.pieces == 0) return cudaSuccess;
+    CUtensorMap tq, tk, tv;
+    if (!rows_map(&tq, a.q, a.q_stride, a.num_q_heads, a.head_dim, a.num_tokens) ||
+        !rows_map(&tk, a.k, a.k_stride, a.num_kv_heads, a.head_dim, a.num_tokens) ||
+        !rows_map(&tv, a.v, a.v_stride, a.num_kv_heads, a.head_dim, a.num_tokens))
+        return cudaErrorInvalidValue;
+    ChunkParams P;
+    P.A = a;
+    P.bounds = static_cast<float*>(workspace);
+    P.max_bounds = plan.max_bounds;
+    P.piece = plan.piece_chunks;
+    P.total = plan.pieces;
+    return a.head_dim == 64 ? launch_all<64>(tq, tk, tv, P, plan.bounds, stream)
+                            : launch_all<128>(tq, tk, tv, P, plan.bounds, stream);
+}
+
+}  // namespace pkv
