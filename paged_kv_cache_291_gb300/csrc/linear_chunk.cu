@@ -140,15 +140,23 @@ __device__ __forceinline__ PieceAt find_piece(const ChunkParams& P, int at, int 
     return r;
 }
 
-// Two fp32 values as three packed bf16 pairs that sum to them exactly.
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    hi = __byte_perm(ua, ub, 0x7632);
-    const float ra = a - __uint_as_float(ua & 0xffff0000u), rb = b - __uint_as_float(ub & 0xffff0000u);
-    const uint32_t va = __float_as_uint(ra), vb = __float_as_uint(rb);
-    mid = __byte_perm(va, vb, 0x7632);
-    const float la = ra - __uint_as_float(va & 0xffff0000u), lb = rb - __uint_as_float(vb & 0xffff0000u);
-    lo = __byte_perm(__float_as_uint(la), __float_as_uint(lb), 0x7632);
+// Two fp32 values as three packed bf16 pairs that sum to them exactly: each
+// term is the upper half of what is left.
+__device__ __forceinline__ float2 less_upper(float2 x) {
+    const float2 u = make_float2(__uint_as_float((__float_as_uint(x.x) & 0xffff0000u) ^ 0x80000000u),
+                                 __uint_as_float((__float_as_uint(x.y) & 0xffff0000u) ^ 0x80000000u));
+    return __fadd2_rn(x, u);
+}
+
+__device__ __forceinline__ uint32_t uppers(float2 x) {
+    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+
+__device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = uppers(x);
+    x = less_upper(x);
+    mid = uppers(x);
+    lo = uppers(less_upper(x));
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity); }
@@ -161,8 +169,9 @@ template <int D, int THREADS>
 __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t svt, const float* factor, float extra,
                                            int rows, int tid) {
     constexpr int kChunks = C * D * 2 / 16;  // 16-byte vectors of the tile
-    float acc = 0.f;
-#pragma unroll
+    float2 acc = make_float2(0.f, 0.f);
+    const float2 zero = make_float2(0.f, 0.f);
+#pragma unroll 1
     for (int n = 0; n < kChunks / THREADS; ++n) {
         const int i = n * THREADS + tid;
         const int row = (i >> 3) & (C - 1);
@@ -171,11 +180,12 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
             uint32_t x[4], hi[4], mid[4], lo[4];
             tc::lds128(sv + at, x);
             const float f = factor[rows - 1 - row] * extra;
+            const float2 ff = make_float2(f, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float a = bf16lo(x[j]), b = bf16hi(x[j]);
-                acc = fmaf(a, 0.f, fmaf(b, 0.f, acc));
-                split3(a * f, b * f, hi[j], mid[j], lo[j]);
+                const float2 v = make_float2(bf16lo(x[j]), bf16hi(x[j]));
+                acc = __ffma2_rn(v, zero, acc);
+                split3(__fmul2_rn(v, ff), hi[j], mid[j], lo[j]);
             }
             tc::sts128(svt + at, hi[0], hi[1], hi[2], hi[3]);
             tc::sts128(svt + kTile + at, mid[0], mid[1], mid[2], mid[3]);
@@ -188,7 +198,7 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
             tc::sts128(sk + at, 0u, 0u, 0u, 0u);
         }
     }
-    return acc;
+    return acc.x + acc.y;
 }
 
 // S^T += (V~)^T K for one chunk, V~ in three terms: A is V~ stored [s][v]
@@ -196,13 +206,15 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
 template <int D>
 __device__ __forceinline__ void mma_state(uint32_t col_s, uint32_t svt, uint32_t sk, bool accumulate) {
     constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 1, 1);
-#pragma unroll
-    for (int part = 0; part < 3; ++part)
+    const uint64_t b = tc::smem_desc_sw128(sk, kPanel, 1024);
+#pragma unroll 1
+    for (int part = 2; part >= 0; --part) {  // smallest first: the sums truncate
+        const uint64_t a = tc::smem_desc_sw128(svt + part * kTile, kPanel, 1024);
 #pragma unroll
         for (int k = 0; k < C / 16; ++k)
-            tc::mma_bf16_ss(col_s, tc::smem_desc_sw128(svt + part * kTile + k * 2048, kPanel, 1024),
-                            tc::smem_desc_sw128(sk + k * 2048, kPanel, 1024), kIdesc,
-                            accumulate || part > 0 || k > 0 ? 1u : 0u);
+            tc::mma_bf16_ss(col_s, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc,
+                            accumulate || part < 2 || k > 0 ? 1u : 0u);
+    }
 }
 
 template <int D, int G>
@@ -238,6 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     for (int i = threadIdx.x; i < kBadBuffers * 128; i += kThreads) bad_rows[i] = 0;
+    for (int i = threadIdx.x; i < 3 * kPanel / 16; i += kThreads)
+        tc::sts128(smem_addr(smem + OFF_P) + i * 16, 0u, 0u, 0u, 0u);
+    tc::fence_proxy_async_smem();
     griddep_wait();
     if (warp == 0) {
         const bool last_entry = blockIdx.x == gridDim.x - 1;
@@ -338,38 +353,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t svt = smem_addr(smem + OFF_VT), sp = smem_addr(smem + OFF_P);
         // scores[s][t] = k_s . q_t (lanes past 63 take the rows that follow K in
         // shared memory: never read)
+        // Descriptors of consecutive K steps differ by their address field.
         auto scores = [&](int n) {
-            const uint32_t sk = sk0 + (n / G % kStages) * kTile, sq = sq0 + (n % kStages) * kTile;
+            const uint64_t a = tc::smem_desc_sw128(sk0 + (n / G % kStages) * kTile, 16, 1024);
+            const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kStages) * kTile, 16, 1024);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-                tc::mma_bf16_ss(tmem + COL_SCORES, tc::smem_desc_sw128(sk + off, 16, 1024),
-                                tc::smem_desc_sw128(sq + off, 16, 1024), kIdescScores, k > 0 ? 1u : 0u);
+                const uint32_t step = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+                tc::mma_bf16_ss(tmem + COL_SCORES, a + step, b + step, kIdescScores, k > 0 ? 1u : 0u);
             }
             tc::mma_commit(&bar[B_SCORES]);
         };
         // O_S^T[v][t] = sum_k S^T[v][k] q_t[k], S^T in three terms from TMEM
         auto out_state = [&](int n) {
-            const uint32_t sq = sq0 + (n % kStages) * kTile;
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
+            const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kStages) * kTile, 16, 1024);
+#pragma unroll 1
+            for (int part = 2; part >= 0; --part) {
+                const uint32_t a = tmem + COL_SB + part * (D / 2);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16_ts(tmem + COL_OS, tmem + COL_SB + part * (D / 2) + 8 * k,
-                                    tc::smem_desc_sw128(sq + (k >> 2) * kPanel + (k & 3) * 32, 16, 1024), kIdescOS,
-                                    part > 0 || k > 0 ? 1u : 0u);
+                    tc::mma_bf16_ts(tmem + COL_OS, a + 8 * k, b + (((k >> 2) * kPanel + (k & 3) * 32) >> 4), kIdescOS,
+                                    part < 2 || k > 0 ? 1u : 0u);
+            }
             tc::mma_commit(&bar[B_QEMPTY + n % kStages]);
         };
         // O_P^T[v][t] = sum_s V[s][v] P[s][t], P in three terms
         auto out_scores = [&](int n) {
-            const uint32_t sv = sv0 + (n / G % kStages) * kTile;
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
+            const uint64_t a = tc::smem_desc_sw128(sv0 + (n / G % kStages) * kTile, kPanel, 1024);
+#pragma unroll 1
+            for (int part = 2; part >= 0; --part) {
+                const uint64_t b = tc::smem_desc_sw128(sp + part * kPanel, kPanel, 1024);
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
-                    tc::mma_bf16_ss(tmem + COL_OP, tc::smem_desc_sw128(sv + k * 2048, kPanel, 1024),
-                                    tc::smem_desc_sw128(sp + part * kPanel + k * 2048, kPanel, 1024), kIdescOP,
-                                    part > 0 || k > 0 ? 1u : 0u);
+                    tc::mma_bf16_ss(tmem + COL_OP, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdescOP,
+                                    part < 2 || k > 0 ? 1u : 0u);
+            }
             if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kStages]);
             tc::mma_commit(&bar[B_PFREE]);
             tc::mma_commit(&bar[B_O]);  // last: once it is seen, nothing of this thread is in flight
@@ -419,26 +437,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < nitems && ok; ++n) {
             if (!warp_wait(&bar[B_SCORES], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t x[2][32];
-            tc::tmem_ld32x32b_x32(taddr, x[0]);
-            tc::tmem_ld32x32b_x32(taddr + 32, x[1]);
-            tc::tmem_wait_ld();
             if (n > 0 && !warp_wait(&bar[B_PFREE], (n - 1) & 1)) { ok = false; break; }
+            // Rows 32-63 keep the zeros of tokens 0-31 that the set-up wrote.
+#pragma unroll 1
+            for (int t0 = 32 * warp; t0 < C; t0 += 16) {
+                uint32_t x[16];
+                tc::tmem_ld32x32b_x16(taddr + t0, x);
+                tc::tmem_wait_ld();
+                const float* ft = f + t0;
+                const int first = s - t0;  // columns before it are masked
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                uint32_t hi[4], mid[4], lo[4];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = 8 * c + 2 * j;
-                    // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
-                    const float a = t >= s ? __uint_as_float(x[t >> 5][t & 31]) * f[t] : 0.f;
-                    const float b = t + 1 >= s ? __uint_as_float(x[t >> 5][(t & 31) + 1]) * f[t + 1] : 0.f;
-                    split3(a, b, hi[j], mid[j], lo[j]);
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = 8 * c + 2 * j;
+                        // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
+                        float2 y = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])),
+                                              make_float2(ft[t], ft[t + 1]));
+                        if (t < first) y.x = 0.f;
+                        if (t + 1 < first) y.y = 0.f;
+                        split3(y, hi[j], mid[j], lo[j]);
+                    }
+                    const uint32_t at = prow + (((t0 / 8 + c) ^ (s & 7)) << 4);
+                    tc::sts128(at, hi[0], hi[1], hi[2], hi[3]);
+                    tc::sts128(at + kPanel, mid[0], mid[1], mid[2], mid[3]);
+                    tc::sts128(at + 2 * kPanel, lo[0], lo[1], lo[2], lo[3]);
                 }
-                const uint32_t at = prow + ((c ^ (s & 7)) << 4);
-                tc::sts128(at, hi[0], hi[1], hi[2], hi[3]);
-                tc::sts128(at + kPanel, mid[0], mid[1], mid[2], mid[3]);
-                tc::sts128(at + 2 * kPanel, lo[0], lo[1], lo[2], lo[3]);
             }
             tc::fence_proxy_async_smem();
             tc::fence_before_sync();
@@ -465,7 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int which = i == nch - 1 ? 1 : 0;
             const float2 lam = make_float2(tab[TAB_LAM + 2 * which], tab[TAB_LAM + 2 * which + 1]);
             if (live) {
-#pragma unroll
+                const float2 lam_hi = make_float2(lam.x, lam.x), lam_lo = make_float2(lam.y, lam.y);
+#pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
                     uint32_t x[32];
                     if (i > 0) {
@@ -479,10 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t hi[16], mid[16], lo[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float a = __uint_as_float(x[2 * j]), c = __uint_as_float(x[2 * j + 1]);
-                        split3(a, c, hi[j], mid[j], lo[j]);
-                        x[2 * j] = __float_as_uint(fmaf(a, lam.x, a * lam.y));
-                        x[2 * j + 1] = __float_as_uint(fmaf(c, lam.x, c * lam.y));
+                        float2 y = make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                        split3(y, hi[j], mid[j], lo[j]);
+                        y = __ffma2_rn(y, lam_hi, __fmul2_rn(y, lam_lo));
+                        x[2 * j] = __float_as_uint(y.x);
+                        x[2 * j + 1] = __float_as_uint(y.y);
                     }
                     tc::tmem_st32x32b_x16(tl + COL_SB + 16 * b, hi);
                     tc::tmem_st32x32b_x16(tl + COL_SB + D / 2 + 16 * b, mid);
@@ -501,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 tc::fence_after_sync();
                 float* to = A.states + (static_cast<int64_t>(info[I_STORE]) * A.num_kv_heads + h) * head + dv;
-#pragma unroll
+#pragma unroll 1
                 for (int b = 0; b < D / 32; ++b) {
                     uint32_t x[32];
                     tc::tmem_ld32x32b_x32(tl + COL_S + 32 * b, x);
@@ -561,26 +588,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* o = A.out + (static_cast<int64_t>(row0) + i * C) * row_step + (h * G + g) * D + dv;
             const int mark = live ? bad_rows[(i % kBadBuffers) * 128 + dv] : 0;
             const int nan_from = (mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C;
-#pragma unroll
-            for (int b = 0; b < C / 32; ++b) {
-                uint32_t xs[32], xp[32];
+#pragma unroll 1
+            for (int t0 = 0; t0 < C; t0 += 16) {
+                uint32_t xs[16], xp[16];
                 if (live) {
-                    tc::tmem_ld32x32b_x32(tl + COL_OS + 32 * b, xs);
-                    tc::tmem_ld32x32b_x32(tl + COL_OP + 32 * b, xp);
+                    tc::tmem_ld32x32b_x16(tl + COL_OS + t0, xs);
+                    tc::tmem_ld32x32b_x16(tl + COL_OP + t0, xp);
                     tc::tmem_wait_ld();
                 }
-                if (b == C / 32 - 1) {
+                if (t0 == C - 16) {
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[B_OFREE]);
                 }
                 if (live) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int t = 32 * b + j;
-                        float y = fmaf(tab[TAB_O + t], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
-                        if (t >= nan_from) y = __int_as_float(0x7fffffff);
-                        if (t < nrows) o[t * row_step] = y;
+                    for (int j = 0; j < 16; ++j) {
+                        float y = fmaf(tab[TAB_O + t0 + j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                        if (t0 + j >= nan_from) y = __int_as_float(0x7fffffff);
+                        if (t0 + j < nrows) *o = y;
+                        o += row_step;
                     }
                 }
             }
