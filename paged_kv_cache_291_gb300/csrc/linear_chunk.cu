@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g == 0) {
                 const int st = i % kStages;
                 if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kStages) & 1) ^ 1)) { ok = false; break; }
-                if (lane == 0) {
+                if (tc::elect_one()) {
                     mbar_arrive_expect_tx(&bar[B_KVFULL + st], 2u * kPanels * kPanel);
 #pragma unroll
                     for (int pn = 0; pn < kPanels; ++pn) {
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int sq = n % kStages;
             if (!warp_wait(&bar[B_QEMPTY + sq], ((n / kStages) & 1) ^ 1)) { ok = false; break; }
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[B_QFULL + sq], static_cast<uint32_t>(kPanels) * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn)
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (nitems > 0) {
             ok = warp_wait(&bar[B_KVFULL], 0) && warp_wait(&bar[B_QFULL], 0);
-            if (ok && lane == 0) scores(0);
+            if (ok && tc::elect_one()) scores(0);
             __syncwarp();
         }
         for (int n = 0; n < nitems && ok; ++n) {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g == 0) {
                 if (!warp_wait(&bar[B_S], i & 1) || !warp_wait(&bar[B_VT], i & 1)) { ok = false; break; }
                 tc::fence_after_sync();
-                if (lane == 0) {
+                if (tc::elect_one()) {
                     mma_state<D>(tmem + COL_S, svt, sk0 + (i % kStages) * kTile, true);
                     tc::mma_commit(&bar[B_VTFREE]);
                 }
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (n > 0 && !warp_wait(&bar[B_OFREE], (n - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 out_state(n);
                 if (g == G - 1) tc::mma_commit(&bar[B_SFREE]);
             }
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!warp_wait(&bar[B_QFULL + (n + 1) % kStages], ((n + 1) / kStages) & 1)) { ok = false; break; }
             }
             tc::fence_after_sync();
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 if (n + 1 < nitems) scores(n + 1);
                 out_scores(n);
             }
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kStages;
             if (!warp_wait(&bar[SB_EMPTY + st], ((i / kStages) & 1) ^ 1)) { ok = false; break; }
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[SB_FULL + st], 2u * kPanels * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn) {
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             const int st = i % kStages, vb = i & 1;
             if (!warp_wait(&bar[SB_VT + vb], (i >> 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            if (lane == 0) {
+            if (tc::elect_one()) {
                 mma_state<D>(tmem, smem_addr(smem + SOFF_VT + vb * 3 * kTile), smem_addr(smem + SOFF_K + st * kTile),
                              i > 0);
                 tc::mma_commit(&bar[SB_EMPTY + st]);
