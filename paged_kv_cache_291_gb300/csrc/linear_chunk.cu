@@ -12,16 +12,16 @@
 // an output column is a coalesced row segment.
 //
 // Precision.  q, k and v are exact in bf16; S, P and V~ are fp32 values.  Each
-// is split into three bf16 terms by truncation (8 + 8 + 8 bits: exact), and
+// is split into three bf16 terms by truncation (8 + 8 + 8 bits, exact), and
 // its product is taken three times, so the result is an fp32 one.  Two terms
 // (16 bits) would be off by 2^-17 of each value.  The state's decay factor is
 // an fp32 pair.
 //
 // Split.  A CTA takes one kv head of one piece of a sequence and walks its
-// chunks; all q heads of the group share the state's work.  Warps: 0-1 P (a
-// lane holds one s), 2 TMA loads, 3 MMA issue, 4-7 S (read, split, decay),
-// 8-11 V~, 12-15 the output.  K, V and Q tiles come through rings of three
-// 128-byte-swizzled stages.
+// chunks; all q heads of the group share the state's work.  Its warps have
+// one part each: loads (TMA, 128-byte swizzle), MMA issue, P, V~, S (read,
+// split, decay) and the output; barriers order them, so the tensor cores work
+// on one chunk while the others prepare the next.
 // Few (sequence, head) pairs leave SMs idle, so sequences are cut into pieces
 // of equal chunk counts: linear_state_kernel sums each piece's own state
 // (all but the last of a sequence), linear_scan_kernel carries the states
@@ -42,13 +42,14 @@ namespace {
 constexpr int C = 64;                    // tokens per chunk
 constexpr int kPanel = C * 128;          // [64 tokens][64 dims] bf16, 128-byte swizzle
 constexpr int kTile = 2 * kPanel;        // room for head_dim 128
-constexpr int kStages = 3;
+constexpr int kStages = 2;               // K, V and Q tiles
+constexpr int kVtBufs = 2;               // V~
 
 constexpr int OFF_K = 0;
 constexpr int OFF_V = OFF_K + kStages * kTile;
 constexpr int OFF_Q = OFF_V + kStages * kTile;
 constexpr int OFF_VT = OFF_Q + kStages * kTile;       // V~: three terms
-constexpr int OFF_P = OFF_VT + 3 * kTile;             // P: three terms of [64 s][64 t]
+constexpr int OFF_P = OFF_VT + kVtBufs * 3 * kTile;           // P: three terms of [64 s][64 t]
 constexpr int OFF_TAB = OFF_P + 3 * kPanel;           // factors
 constexpr int TAB_P = 0;                              // float[128]: scale lam^(t-s) at 63 + t - s
 constexpr int TAB_O = 128;                            // float[64]: scale lam^(t+1)
@@ -64,13 +65,13 @@ enum {
     B_QFULL = B_KVEMPTY + kStages,
     B_QEMPTY = B_QFULL + kStages,
     B_SCORES = B_QEMPTY + kStages,  // scores in TMEM
-    B_P,                        // P in shared memory (2 arrivals)
+    B_P,                        // P in shared memory (3 arrivals)
     B_PFREE,                    // P read
-    B_S,                        // S split and decayed (4 arrivals)
+    B_S,                        // S split and decayed (8 arrivals)
     B_SFREE,                    // the split S read by every q head of the chunk
-    B_VT,                       // V~ in shared memory (4 arrivals)
-    B_VTFREE,                   // V~ read, S holds the chunk
-    B_O,                        // outputs in TMEM
+    B_VT,                       // + buffer: V~ in shared memory (3 arrivals)
+    B_VTFREE = B_VT + kVtBufs,  // + buffer: V~ read, S holds the chunk
+    B_O = B_VTFREE + kVtBufs,   // outputs in TMEM
     B_OFREE,                    // outputs read (4 arrivals)
     NBAR
 };
@@ -80,8 +81,12 @@ constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;      // slack to align the base
 static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB)");
 static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
 
-constexpr int kThreads = 512;
+// Warps, spread so that the four SM sub-partitions (warp % 4, which is also
+// the TMEM lane quarter a warp can reach) carry about the same work.
+constexpr int kThreads = 640;
 constexpr int kLoadWarp = 2, kMmaWarp = 3;
+// P: warps 0 (s 0-31, t 0-31), 4 (s 0-31, t 32-63) and 1 (s 32-63, t 32-63)
+constexpr int kVWarp = 5, kVWarps = 3, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 4;
 
 // TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
 constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
@@ -165,15 +170,14 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { retu
 // * extra * v_s in three terms.  Rows past the piece become zero, there and in
 // K and V: they are other sequences' tokens, and a zero factor times a NaN
 // would poison the products.  Returns 0, or NaN if a value was not finite.
-template <int D, int THREADS>
+template <int D, int THREADS, int UNROLL>
 __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t svt, const float* factor, float extra,
                                            int rows, int tid) {
     constexpr int kChunks = C * D * 2 / 16;  // 16-byte vectors of the tile
     float2 acc = make_float2(0.f, 0.f);
     const float2 zero = make_float2(0.f, 0.f);
-#pragma unroll 1
-    for (int n = 0; n < kChunks / THREADS; ++n) {
-        const int i = n * THREADS + tid;
+#pragma unroll UNROLL
+    for (int i = tid; i < kChunks; i += THREADS) {
         const int row = (i >> 3) & (C - 1);
         const uint32_t at = static_cast<uint32_t>(i) * 16u;
         if (row < rows) {
@@ -237,7 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     if (threadIdx.x == 32 * kMmaWarp) {
         for (int i = 0; i < NBAR; ++i)
-            mbar_init(&bar[i], i == B_P ? 2u : (i == B_S || i == B_VT || i == B_OFREE) ? 4u : 1u);
+            mbar_init(&bar[i], i == B_P                                  ? 3u
+                                : i == B_S                               ? static_cast<uint32_t>(kSWarps)
+                                : i >= B_VT && i < B_VT + kVtBufs        ? static_cast<uint32_t>(kVWarps)
+                                : i == B_OFREE                           ? static_cast<uint32_t>(kOWarps)
+                                                                         : 1u);
         fence_mbar_init();
     }
     if (warp == kLoadWarp) {
@@ -400,11 +408,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < nitems && ok; ++n) {
             const int i = n / G, g = n % G;
             if (g == 0) {
-                if (!warp_wait(&bar[B_S], i & 1) || !warp_wait(&bar[B_VT], i & 1)) { ok = false; break; }
+                if (!warp_wait(&bar[B_S], i & 1) || !warp_wait(&bar[B_VT + i % kVtBufs], (i / kVtBufs) & 1)) {
+                    ok = false;
+                    break;
+                }
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    mma_state<D>(tmem + COL_S, svt, sk0 + (i % kStages) * kTile, true);
-                    tc::mma_commit(&bar[B_VTFREE]);
+                    mma_state<D>(tmem + COL_S, svt + (i % kVtBufs) * 3 * kTile, sk0 + (i % kStages) * kTile, true);
+                    tc::mma_commit(&bar[B_VTFREE + i % kVtBufs]);
                 }
                 __syncwarp();
             }
@@ -428,10 +439,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
-    } else if (warp < 2) {
+    } else if (warp == 0 || warp == 1 || warp == 4) {
         // ------------------------------------------------------ P
-        const int s = 32 * warp + lane;
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * warp) << 16) + COL_SCORES;
+        const int s = 32 * (warp & 1) + lane, begin = warp == 0 ? 0 : 32;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + COL_SCORES;
         const uint32_t prow = smem_addr(smem + OFF_P) + s * 128;
         const float* f = tab + TAB_P + 63 - s;
         for (int n = 0; n < nitems && ok; ++n) {
@@ -440,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0 && !warp_wait(&bar[B_PFREE], (n - 1) & 1)) { ok = false; break; }
             // Rows 32-63 keep the zeros of tokens 0-31 that the set-up wrote.
 #pragma unroll 1
-            for (int t0 = 32 * warp; t0 < C; t0 += 16) {
+            for (int t0 = begin; t0 < begin + 32; t0 += 16) {
                 uint32_t x[16];
                 tc::tmem_ld32x32b_x16(taddr + t0, x);
                 tc::tmem_wait_ld();
@@ -470,51 +481,68 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_P]);
         }
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= kSWarp && warp < kSWarp + kSWarps) {
         // ------------------------------------------------------ S
-        // Lane = v index.  Chunk 0 takes the state from memory, later ones
-        // from the accumulator; each leaves the three terms of S for the
-        // outputs and lam^rows S for the update.
-        const int w = warp - 4, dv = 32 * w + lane;
+        // Lane = v index; the second four warps take the second half of the
+        // columns.  Per chunk: the three terms of S for the outputs and
+        // lam^rows S back into the accumulator for the update.
+        constexpr int kCols = D / 2, kBatches = kCols / 16;
+        const int w = warp & 3, dv = 32 * w + lane, c0 = warp - kSWarp < 4 ? 0 : kCols;
         const bool live = 32 * w < D;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        const uint32_t ts = tmem + (static_cast<uint32_t>(32 * w) << 16) + COL_S + c0;
+        const uint32_t tb = tmem + (static_cast<uint32_t>(32 * w) << 16) + COL_SB + c0 / 2;
         const int64_t head = static_cast<int64_t>(D) * D;
-        const float* from = nullptr;
-        if (info[I_BOUND] >= 0)
-            from = P.bounds + (static_cast<int64_t>(info[I_BOUND]) * A.num_kv_heads + h) * head + dv;
-        else if (info[I_LOAD] >= 0)
-            from = A.states + (static_cast<int64_t>(info[I_LOAD]) * A.num_kv_heads + h) * head + dv;
+        if (nch > 0 && live) {
+            const float* from = nullptr;
+            if (info[I_BOUND] >= 0)
+                from = P.bounds + (static_cast<int64_t>(info[I_BOUND]) * A.num_kv_heads + h) * head;
+            else if (info[I_LOAD] >= 0)
+                from = A.states + (static_cast<int64_t>(info[I_LOAD]) * A.num_kv_heads + h) * head;
+#pragma unroll 1
+            for (int b = 0; b < kCols / 32; ++b) {
+                uint32_t x[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    x[j] = from != nullptr ? __float_as_uint(from[(c0 + 32 * b + j) * D + dv]) : 0u;
+                tc::tmem_st32x32b_x32(ts + 32 * b, x);
+            }
+            tc::tmem_wait_st();
+        }
+        auto split = [&](uint32_t (&x)[16], int b, float2 lam) {
+            uint32_t hi[8], mid[8], lo[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 y = make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                split3(y, hi[j], mid[j], lo[j]);
+                y = __ffma2_rn(y, make_float2(lam.x, lam.x), __fmul2_rn(y, make_float2(lam.y, lam.y)));
+                x[2 * j] = __float_as_uint(y.x);
+                x[2 * j + 1] = __float_as_uint(y.y);
+            }
+            tc::tmem_st32x32b_x8(tb + 8 * b, hi);
+            tc::tmem_st32x32b_x8(tb + D / 2 + 8 * b, mid);
+            tc::tmem_st32x32b_x8(tb + D + 8 * b, lo);
+            tc::tmem_st32x32b_x16(ts + 16 * b, x);
+        };
         for (int i = 0; i < nch && ok; ++i) {
+            // S may be read when the last chunk's update is in it, its terms
+            // replaced when the last outputs have read them.
+            if (i > 0 && !warp_wait(&bar[B_VTFREE + (i - 1) % kVtBufs], ((i - 1) / kVtBufs) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            uint32_t xa[16], xb[16];
+            if (live) tc::tmem_ld32x32b_x16(ts, xa);
             if (i > 0 && !warp_wait(&bar[B_SFREE], (i - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             const int which = i == nch - 1 ? 1 : 0;
             const float2 lam = make_float2(tab[TAB_LAM + 2 * which], tab[TAB_LAM + 2 * which + 1]);
             if (live) {
-                const float2 lam_hi = make_float2(lam.x, lam.x), lam_lo = make_float2(lam.y, lam.y);
 #pragma unroll 1
-                for (int b = 0; b < D / 32; ++b) {
-                    uint32_t x[32];
-                    if (i > 0) {
-                        tc::tmem_ld32x32b_x32(tl + COL_S + 32 * b, x);
-                        tc::tmem_wait_ld();
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            x[j] = from != nullptr ? __float_as_uint(from[(32 * b + j) * D]) : 0u;
-                    }
-                    uint32_t hi[16], mid[16], lo[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float2 y = make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-                        split3(y, hi[j], mid[j], lo[j]);
-                        y = __ffma2_rn(y, lam_hi, __fmul2_rn(y, lam_lo));
-                        x[2 * j] = __float_as_uint(y.x);
-                        x[2 * j + 1] = __float_as_uint(y.y);
-                    }
-                    tc::tmem_st32x32b_x16(tl + COL_SB + 16 * b, hi);
-                    tc::tmem_st32x32b_x16(tl + COL_SB + D / 2 + 16 * b, mid);
-                    tc::tmem_st32x32b_x16(tl + COL_SB + D + 16 * b, lo);
-                    tc::tmem_st32x32b_x32(tl + COL_S + 32 * b, x);
+                for (int b = 0; b < kBatches; b += 2) {
+                    tc::tmem_wait_ld();
+                    tc::tmem_ld32x32b_x16(ts + 16 * b + 16, xb);
+                    split(xa, b, lam);
+                    tc::tmem_wait_ld();
+                    if (b + 2 < kBatches) tc::tmem_ld32x32b_x16(ts + 16 * b + 32, xa);
+                    split(xb, b + 1, lam);
                 }
                 tc::tmem_wait_st();
             }
@@ -523,36 +551,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar[B_S]);
         }
         if (ok && nch > 0 && info[I_STORE] >= 0 && live) {
-            if (!warp_wait(&bar[B_VTFREE], (nch - 1) & 1)) {
+            if (!warp_wait(&bar[B_VTFREE + (nch - 1) % kVtBufs], ((nch - 1) / kVtBufs) & 1)) {
                 ok = false;
             } else {
                 tc::fence_after_sync();
                 float* to = A.states + (static_cast<int64_t>(info[I_STORE]) * A.num_kv_heads + h) * head + dv;
 #pragma unroll 1
-                for (int b = 0; b < D / 32; ++b) {
+                for (int b = 0; b < kCols / 32; ++b) {
                     uint32_t x[32];
-                    tc::tmem_ld32x32b_x32(tl + COL_S + 32 * b, x);
+                    tc::tmem_ld32x32b_x32(ts + 32 * b, x);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) to[(32 * b + j) * D] = __uint_as_float(x[j]);
+                    for (int j = 0; j < 32; ++j) to[(c0 + 32 * b + j) * D] = __uint_as_float(x[j]);
                 }
             }
         }
-    } else if (warp >= 8 && warp < 12) {
+    } else if (warp >= kVWarp && warp < kVWarp + kVWarps) {
         // ------------------------------------------------------ V~
-        const int tid = threadIdx.x - 256;
+        const int tid = threadIdx.x - 32 * kVWarp;
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kStages;
             if (!warp_wait(&bar[B_KVFULL + st], (i / kStages) & 1)) { ok = false; break; }
-            if (i > 0 && !warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
+            const int vb = i % kVtBufs;
+            if (!warp_wait(&bar[B_VTFREE + vb], ((i / kVtBufs) & 1) ^ 1)) { ok = false; break; }
             const int nrows = min(C, rows - i * C);
             const uint32_t sk = smem_addr(smem + OFF_K + st * kTile), sv = smem_addr(smem + OFF_V + st * kTile);
-            const float acc = convert_v<D, 128>(sk, sv, smem_addr(smem + OFF_VT), tab + TAB_V, 1.f, nrows, tid);
+            const float acc = convert_v<D, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + OFF_VT) + vb * 3 * kTile,
+                                                              tab + TAB_V, 1.f, nrows, tid);
             if (acc != 0.f) {
                 // A value that is not finite reaches the outputs of its column
                 // from its row on, and no earlier row: it leaves V for P V
                 // (V~ carries it into the state), and its row is noted.
-                for (int c = tid; c < C * D * 2 / 16; c += 128) {
+                for (int c = tid; c < C * D * 2 / 16; c += 32 * kVWarps) {
                     const int row = (c >> 3) & (C - 1);
                     if (row >= nrows) continue;
                     uint32_t x[4];
@@ -571,12 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_VT]);
+            if (lane == 0) mbar_arrive(&bar[B_VT + vb]);
         }
-    } else if (warp >= 12) {
+    } else if (warp >= kOWarp) {
         // ------------------------------------------------------ outputs
         // Lane = v index, column = token: a warp stores 32 consecutive floats of a row.
-        const int w = warp - 12, dv = 32 * w + lane;
+        const int w = warp & 3, dv = 32 * w + lane;
         const bool live = 32 * w < D;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16);
         const int64_t row_step = static_cast<int64_t>(A.num_q_heads) * D;
@@ -630,12 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // tokens, one accumulation with no rescaling (the factor of a chunk's end is
 // part of V~).  Warps 0-7 V~, 8 loads, 9 MMA; warps 0-3 store the sum.
 constexpr int kStateThreads = 320;
+constexpr int kStateStages = 3;
 constexpr int SOFF_K = 0;
-constexpr int SOFF_V = SOFF_K + kStages * kTile;
-constexpr int SOFF_VT = SOFF_V + kStages * kTile;     // two buffers of three terms
+constexpr int SOFF_V = SOFF_K + kStateStages * kTile;
+constexpr int SOFF_VT = SOFF_V + kStateStages * kTile;     // two buffers of three terms
 constexpr int SOFF_TAB = SOFF_VT + 2 * 3 * kTile;
 constexpr int SOFF_BAR = SOFF_TAB + C * 4;
-enum { SB_FULL = 0, SB_EMPTY = kStages, SB_VT = 2 * kStages, SB_VTFREE = SB_VT + 2, SB_DONE = SB_VTFREE + 2, SNBAR };
+enum { SB_FULL = 0, SB_EMPTY = kStateStages, SB_VT = 2 * kStateStages, SB_VTFREE = SB_VT + 2, SB_DONE = SB_VTFREE + 2, SNBAR };
 constexpr int SOFF_INFO = SOFF_BAR + SNBAR * 8;
 constexpr int SOFF_TMEM = SOFF_INFO + 8 * 4;
 constexpr int STATE_SMEM = SOFF_TMEM + 16 + 1024;
@@ -696,8 +727,8 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     bool ok = true;
     if (warp == 8) {
         for (int i = 0; i < nch && ok; ++i) {
-            const int st = i % kStages;
-            if (!warp_wait(&bar[SB_EMPTY + st], ((i / kStages) & 1) ^ 1)) { ok = false; break; }
+            const int st = i % kStateStages;
+            if (!warp_wait(&bar[SB_EMPTY + st], ((i / kStateStages) & 1) ^ 1)) { ok = false; break; }
             if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[SB_FULL + st], 2u * kPanels * kPanel);
 #pragma unroll
@@ -712,7 +743,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
     } else if (warp == 9) {
         for (int i = 0; i < nch && ok; ++i) {
-            const int st = i % kStages, vb = i & 1;
+            const int st = i % kStateStages, vb = i & 1;
             if (!warp_wait(&bar[SB_VT + vb], (i >> 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) {
@@ -726,10 +757,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         }
     } else {
         for (int i = 0; i < nch && ok; ++i) {
-            const int st = i % kStages, vb = i & 1;
-            if (!warp_wait(&bar[SB_FULL + st], (i / kStages) & 1)) { ok = false; break; }
+            const int st = i % kStateStages, vb = i & 1;
+            if (!warp_wait(&bar[SB_FULL + st], (i / kStateStages) & 1)) { ok = false; break; }
             if (!warp_wait(&bar[SB_VTFREE + vb], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
-            convert_v<D, 256>(smem_addr(smem + SOFF_K + st * kTile), smem_addr(smem + SOFF_V + st * kTile),
+            convert_v<D, 256, 2>(smem_addr(smem + SOFF_K + st * kTile), smem_addr(smem + SOFF_V + st * kTile),
                               smem_addr(smem + SOFF_VT + vb * 3 * kTile), tab,
                               expf(g * static_cast<float>((nch - 1 - i) * C)), C, threadIdx.x);
             tc::fence_proxy_async_smem();
