@@ -12,7 +12,7 @@
 // an output column is a coalesced row segment.
 //
 // Precision.  q, k and v are exact in bf16; S, P and V~ are fp32 values.  Each
-// is split into three bf16 terms by truncation (8 + 8 + 8 bits, exact), and
+// is split into three bf16 terms (8 + 8 + 8 bits, exact), and
 // its product is taken three times, so the result is an fp32 one.  Two terms
 // (16 bits) would be off by 2^-17 of each value.  The state's decay factor is
 // an fp32 pair.
@@ -69,7 +69,7 @@ enum {
     B_PFREE,                    // P read
     B_S,                        // S split and decayed (8 arrivals)
     B_SFREE,                    // the split S read by every q head of the chunk
-    B_VT,                       // + buffer: V~ in shared memory (3 arrivals)
+    B_VT,                       // + buffer: V~ in shared memory (4 arrivals)
     B_VTFREE = B_VT + kVtBufs,  // + buffer: V~ read, S holds the chunk
     B_O = B_VTFREE + kVtBufs,   // outputs in TMEM
     B_OFREE,                    // outputs read (4 arrivals)
@@ -83,10 +83,11 @@ static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs
 
 // Warps, spread so that the four SM sub-partitions (warp % 4, which is also
 // the TMEM lane quarter a warp can reach) carry about the same work.
-constexpr int kThreads = 640;
+constexpr int kThreads = 672;
 constexpr int kLoadWarp = 2, kMmaWarp = 3;
 // P: warps 0 (s 0-31, t 0-31), 4 (s 0-31, t 32-63) and 1 (s 32-63, t 32-63)
-constexpr int kVWarp = 5, kVWarps = 3, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 4;
+// V~: warps 5, 6, 7 and 20
+constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 4;
 
 // TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
 constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
@@ -146,22 +147,27 @@ __device__ __forceinline__ PieceAt find_piece(const ChunkParams& P, int at, int 
 }
 
 // Two fp32 values as three packed bf16 pairs that sum to them exactly: each
-// term is the upper half of what is left.
-__device__ __forceinline__ float2 less_upper(float2 x) {
-    const float2 u = make_float2(__uint_as_float((__float_as_uint(x.x) & 0xffff0000u) ^ 0x80000000u),
-                                 __uint_as_float((__float_as_uint(x.y) & 0xffff0000u) ^ 0x80000000u));
-    return __fadd2_rn(x, u);
+// term is what is left, rounded to nearest.  The low half is widened by a
+// multiply: shifts, masks and packs share a pipe of half the rate, which these
+// conversions fill.
+__device__ __forceinline__ uint32_t pack_bf16(float2 x) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
+    return r;
 }
 
-__device__ __forceinline__ uint32_t uppers(float2 x) {
-    return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+__device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
+    uint32_t lo;
+    asm("mul.lo.u32 %0, %1, 65536;" : "=r"(lo) : "r"(u));
+    return make_float2(__uint_as_float(lo), __uint_as_float(u & 0xffff0000u));
 }
 
 __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = uppers(x);
-    x = less_upper(x);
-    mid = uppers(x);
-    lo = uppers(less_upper(x));
+    const float2 minus = make_float2(-1.f, -1.f);
+    hi = pack_bf16(x);
+    x = __ffma2_rn(unpack_bf16(hi), minus, x);
+    mid = pack_bf16(x);
+    lo = pack_bf16(__ffma2_rn(unpack_bf16(mid), minus, x));
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity); }
@@ -187,7 +193,7 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
             const float2 ff = make_float2(f, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 v = make_float2(bf16lo(x[j]), bf16hi(x[j]));
+                const float2 v = unpack_bf16(x[j]);
                 acc = __ffma2_rn(v, zero, acc);
                 split3(__fmul2_rn(v, ff), hi[j], mid[j], lo[j]);
             }
@@ -445,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + COL_SCORES;
         const uint32_t prow = smem_addr(smem + OFF_P) + s * 128;
         const float* f = tab + TAB_P + 63 - s;
+        const bool masked = warp != 4;
         for (int n = 0; n < nitems && ok; ++n) {
             if (!warp_wait(&bar[B_SCORES], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
@@ -466,8 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
                         float2 y = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])),
                                               make_float2(ft[t], ft[t + 1]));
-                        if (t < first) y.x = 0.f;
-                        if (t + 1 < first) y.y = 0.f;
+                        if (masked) {
+                            if (t < first) y.x = 0.f;
+                            if (t + 1 < first) y.y = 0.f;
+                        }
                         split3(y, hi[j], mid[j], lo[j]);
                     }
                     const uint32_t at = prow + (((t0 / 8 + c) ^ (s & 7)) << 4);
@@ -566,9 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp >= kVWarp && warp < kVWarp + kVWarps) {
+    } else if ((warp >= 5 && warp < 8) || warp == 20) {
         // ------------------------------------------------------ V~
-        const int tid = threadIdx.x - 32 * kVWarp;
+        const int tid = 32 * (warp & 3) + lane;
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kStages;
             if (!warp_wait(&bar[B_KVFULL + st], (i / kStages) & 1)) { ok = false; break; }
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_VT + vb]);
         }
-    } else if (warp >= kOWarp) {
+    } else {
         // ------------------------------------------------------ outputs
         // Lane = v index, column = token: a warp stores 32 consecutive floats of a row.
         const int w = warp & 3, dv = 32 * w + lane;
@@ -618,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float* o = A.out + (static_cast<int64_t>(row0) + i * C) * row_step + (h * G + g) * D + dv;
             const int mark = live ? bad_rows[(i % kBadBuffers) * 128 + dv] : 0;
             const int nan_from = (mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C;
+            const int plain = min(nrows, __reduce_min_sync(0xffffffffu, nan_from));  // columns that need no check
 #pragma unroll 1
             for (int t0 = 0; t0 < C; t0 += 16) {
                 uint32_t xs[16], xp[16];
@@ -632,12 +642,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&bar[B_OFREE]);
                 }
                 if (live) {
+                    float* ot = o + t0 * row_step;
+                    const float* ft = tab + TAB_O + t0;
+                    if (t0 + 16 <= plain) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float y = fmaf(tab[TAB_O + t0 + j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
-                        if (t0 + j >= nan_from) y = __int_as_float(0x7fffffff);
-                        if (t0 + j < nrows) *o = y;
-                        o += row_step;
+                        for (int j = 0; j < 16; ++j)
+                            ot[j * row_step] = fmaf(ft[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float y = fmaf(ft[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                            if (t0 + j >= nan_from) y = __int_as_float(0x7fffffff);
+                            if (t0 + j < nrows) ot[j * row_step] = y;
+                        }
                     }
                 }
             }
