@@ -42,8 +42,8 @@ namespace {
 constexpr int C = 64;                    // tokens per chunk
 constexpr int kPanel = C * 128;          // [64 tokens][64 dims] bf16, 128-byte swizzle
 constexpr int kTile = 2 * kPanel;        // room for head_dim 128
-constexpr int kStages = 2;               // K, V and Q tiles
-constexpr int kVtBufs = 2;               // V~
+constexpr int kStages = 3;               // K, V and Q tiles
+constexpr int kVtBufs = 1;               // V~
 
 constexpr int OFF_K = 0;
 constexpr int OFF_V = OFF_K + kStages * kTile;
@@ -54,7 +54,7 @@ constexpr int OFF_TAB = OFF_P + 3 * kPanel;           // factors
 constexpr int TAB_P = 0;                              // float[128]: scale lam^(t-s) at 63 + t - s
 constexpr int TAB_O = 128;                            // float[64]: scale lam^(t+1)
 constexpr int TAB_V = 192;                            // float[64]: lam^j
-constexpr int TAB_LAM = 256;                          // float2[2]: lam^64, lam^(tail rows)
+constexpr int TAB_LAM = 256;                          // float2: lam^64
 constexpr int OFF_BAD = OFF_TAB + 264 * 4;            // int[4][128], see kBadBuffers
 constexpr int OFF_BAR = OFF_BAD + 4 * 128 * 4;
 constexpr int kBadBuffers = 4;
@@ -71,8 +71,10 @@ enum {
     B_SFREE,                    // the split S read by every q head of the chunk
     B_VT,                       // + buffer: V~ in shared memory (4 arrivals)
     B_VTFREE = B_VT + kVtBufs,  // + buffer: V~ read, S holds the chunk
-    B_O = B_VTFREE + kVtBufs,   // outputs in TMEM
-    B_OFREE,                    // outputs read (4 arrivals)
+    B_OS = B_VTFREE + kVtBufs,  // the state's part of the outputs in TMEM
+    B_OSFREE,                   // and read (8 arrivals)
+    B_OP,                       // the scores' part
+    B_OPFREE,
     NBAR
 };
 constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
@@ -83,11 +85,11 @@ static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs
 
 // Warps, spread so that the four SM sub-partitions (warp % 4, which is also
 // the TMEM lane quarter a warp can reach) carry about the same work.
-constexpr int kThreads = 672;
+constexpr int kThreads = 768;
 constexpr int kLoadWarp = 2, kMmaWarp = 3;
 // P: warps 0 (s 0-31, t 0-31), 4 (s 0-31, t 32-63) and 1 (s 32-63, t 32-63)
-// V~: warps 5, 6, 7 and 20
-constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 4;
+// V~: warps 2 (which also loads), 5, 6 and 7
+constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 
 // TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
 constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
@@ -170,6 +172,13 @@ __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, ui
     lo = pack_bf16(__ffma2_rn(unpack_bf16(mid), minus, x));
 }
 
+// The next row's address, computed where it is used (32 hoisted ones would
+// not fit the registers).
+__device__ __forceinline__ float* walk(float* p, int64_t bytes) {
+    asm volatile("add.s64 %0, %0, %1;" : "+l"(p) : "l"(bytes));
+    return p;
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity); }
 
 // V~ of one chunk, elementwise over the swizzled V tile: factor[rows - 1 - s]
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bar[i], i == B_P                                  ? 3u
                                 : i == B_S                               ? static_cast<uint32_t>(kSWarps)
                                 : i >= B_VT && i < B_VT + kVtBufs        ? static_cast<uint32_t>(kVWarps)
-                                : i == B_OFREE                           ? static_cast<uint32_t>(kOWarps)
+                                : i == B_OSFREE || i == B_OPFREE         ? static_cast<uint32_t>(kOWarps)
                                                                          : 1u);
         fence_mbar_init();
     }
@@ -302,20 +311,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             info[I_BOUND] = bound;
             info[I_BAD] = bad;
         }
-        const int tail = (rows - 1) % C + 1;
-        const float g = clean_log_decay(A, h, lane == 0);
-        if (lane < 2) {
-            const float2 x = decay_pair(g, lane == 0 ? C : tail);
-            tab[TAB_LAM + 2 * lane] = x.x;
-            tab[TAB_LAM + 2 * lane + 1] = x.y;
+    } else if (warp == kSWarp) {
+        if (lane == 0) {
+            const float2 x = decay_pair(clean_log_decay(A, h, true), C);
+            tab[TAB_LAM] = x.x;
+            tab[TAB_LAM + 1] = x.y;
         }
-        for (int j = lane; j < C; j += 32) {
-            const float x = expf(g * static_cast<float>(j));
-            tab[TAB_V + j] = x;
-            tab[TAB_P + 63 + j] = A.scale * x;
-            tab[TAB_P + j] = j < 63 ? 0.f : A.scale;
-            tab[TAB_O + j] = A.scale * expf(g * static_cast<float>(j + 1));
-        }
+    } else if (warp == kSWarp + 1 || warp == kSWarp + 2) {
+        const float g = clean_log_decay(A, h, false);
+        const int j = 32 * (warp - kSWarp - 1) + lane;
+        const float x = expf(g * static_cast<float>(j));
+        tab[TAB_V + j] = x;
+        tab[TAB_P + 63 + j] = A.scale * x;
+        if (j < 63) tab[TAB_P + j] = 0.f;
+        tab[TAB_O + j] = A.scale * expf(g * static_cast<float>(j + 1));
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -326,40 +335,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int nitems = nch * G;
     bool ok = true;
 
-    if (warp == kLoadWarp) {
-        // ------------------------------------------------------ TMA producer
-        for (int n = 0; n < nitems && ok; ++n) {
-            const int i = n / G, g = n % G;
-            if (g == 0) {
-                const int st = i % kStages;
-                if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kStages) & 1) ^ 1)) { ok = false; break; }
-                if (tc::elect_one()) {
-                    mbar_arrive_expect_tx(&bar[B_KVFULL + st], 2u * kPanels * kPanel);
-#pragma unroll
-                    for (int pn = 0; pn < kPanels; ++pn) {
-                        tc::tma_load_3d(smem + OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
-                                        &bar[B_KVFULL + st]);
-                        tc::tma_load_3d(smem + OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
-                                        &bar[B_KVFULL + st]);
-                    }
-                }
-                __syncwarp();
-            }
-            const int sq = n % kStages;
-            if (!warp_wait(&bar[B_QEMPTY + sq], ((n / kStages) & 1) ^ 1)) { ok = false; break; }
-            if (tc::elect_one()) {
-                mbar_arrive_expect_tx(&bar[B_QFULL + sq], static_cast<uint32_t>(kPanels) * kPanel);
-#pragma unroll
-                for (int pn = 0; pn < kPanels; ++pn)
-                    tc::tma_load_3d(smem + OFF_Q + sq * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + g, row0 + i * C,
-                                    &bar[B_QFULL + sq]);
-            }
-            __syncwarp();
-        }
-    } else if (warp == kMmaWarp) {
+    if (warp == kMmaWarp) {
         // ------------------------------------------------------ MMA issuer
-        // Scores of item n + 1 go ahead of P V of item n, so that the P warps
-        // always have the next item's scores while the tensor cores work.
+        // Order of the products: the state's outputs first, which frees the
+        // terms of S, then the state's update, so that the S warps work while
+        // the scores of the next item and P V run.
         constexpr uint32_t kIdescScores = tc::idesc_bf16_f32(128, C, 0, 0);
         constexpr uint32_t kIdescOS = tc::idesc_bf16_f32(128, C, 0, 0);
         constexpr uint32_t kIdescOP = tc::idesc_bf16_f32(128, C, 1, 1);
@@ -390,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     part < 2 || k > 0 ? 1u : 0u);
             }
             tc::mma_commit(&bar[B_QEMPTY + n % kStages]);
+            tc::mma_commit(&bar[B_OS]);
         };
         // O_P^T[v][t] = sum_s V[s][v] P[s][t], P in three terms
         auto out_scores = [&](int n) {
@@ -404,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kStages]);
             tc::mma_commit(&bar[B_PFREE]);
-            tc::mma_commit(&bar[B_O]);  // last: once it is seen, nothing of this thread is in flight
+            tc::mma_commit(&bar[B_OP]);  // last: once it is seen, nothing of this thread is in flight
         };
         if (nitems > 0) {
             ok = warp_wait(&bar[B_KVFULL], 0) && warp_wait(&bar[B_QFULL], 0);
@@ -413,36 +394,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int n = 0; n < nitems && ok; ++n) {
             const int i = n / G, g = n % G;
-            if (g == 0) {
-                if (!warp_wait(&bar[B_S], i & 1) || !warp_wait(&bar[B_VT + i % kVtBufs], (i / kVtBufs) & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc::fence_after_sync();
-                if (tc::elect_one()) {
-                    mma_state<D>(tmem + COL_S, svt + (i % kVtBufs) * 3 * kTile, sk0 + (i % kStages) * kTile, true);
-                    tc::mma_commit(&bar[B_VTFREE + i % kVtBufs]);
-                }
-                __syncwarp();
-            }
-            if (n > 0 && !warp_wait(&bar[B_OFREE], (n - 1) & 1)) { ok = false; break; }
+            if (g == 0 && !warp_wait(&bar[B_S], i & 1)) { ok = false; break; }
+            if (n > 0 && !warp_wait(&bar[B_OSFREE], (n - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) {
                 out_state(n);
                 if (g == G - 1) tc::mma_commit(&bar[B_SFREE]);
             }
             __syncwarp();
+            if (g == 0) {
+                if (!warp_wait(&bar[B_VT + i % kVtBufs], (i / kVtBufs) & 1)) { ok = false; break; }
+                if (tc::elect_one()) {
+                    mma_state<D>(tmem + COL_S, svt + (i % kVtBufs) * 3 * kTile, sk0 + (i % kStages) * kTile, true);
+                    tc::mma_commit(&bar[B_VTFREE + i % kVtBufs]);
+                }
+                __syncwarp();
+            }
             if (!warp_wait(&bar[B_P], n & 1)) { ok = false; break; }
             if (n + 1 < nitems) {
                 const int i1 = (n + 1) / G;
                 if (i1 != i && !warp_wait(&bar[B_KVFULL + i1 % kStages], (i1 / kStages) & 1)) { ok = false; break; }
                 if (!warp_wait(&bar[B_QFULL + (n + 1) % kStages], ((n + 1) / kStages) & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                if (tc::elect_one()) scores(n + 1);
+                __syncwarp();
             }
+            if (n > 0 && !warp_wait(&bar[B_OPFREE], (n - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            if (tc::elect_one()) {
-                if (n + 1 < nitems) scores(n + 1);
-                out_scores(n);
-            }
+            if (tc::elect_one()) out_scores(n);
             __syncwarp();
         }
     } else if (warp == 0 || warp == 1 || warp == 4) {
@@ -541,8 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live) tc::tmem_ld32x32b_x16(ts, xa);
             if (i > 0 && !warp_wait(&bar[B_SFREE], (i - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            const int which = i == nch - 1 ? 1 : 0;
-            const float2 lam = make_float2(tab[TAB_LAM + 2 * which], tab[TAB_LAM + 2 * which + 1]);
+            // a tail's factor is applied once: fp32 is enough
+            const int nrows = min(C, rows - i * C);
+            const float2 lam = nrows == C ? make_float2(tab[TAB_LAM], tab[TAB_LAM + 1]) : make_float2(tab[TAB_V + nrows], 0.f);
             if (live) {
 #pragma unroll 1
                 for (int b = 0; b < kBatches; b += 2) {
@@ -575,9 +555,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if ((warp >= 5 && warp < 8) || warp == 20) {
-        // ------------------------------------------------------ V~
-        const int tid = 32 * (warp & 3) + lane;
+    } else if (warp == kLoadWarp || (warp >= 5 && warp < 8)) {
+        // ------------------------------------------------------ loads and V~
+        // The load warp converts its share too.  The loads that follow chunk
+        // i's conversion wait for items that end before the next conversion
+        // could start, so neither holds the other up.
+        auto load_kv = [&](int i) -> bool {
+            if (i >= nch) return true;
+            const int st = i % kStages;
+            if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kStages) & 1) ^ 1)) return false;
+            if (tc::elect_one()) {
+                mbar_arrive_expect_tx(&bar[B_KVFULL + st], 2u * kPanels * kPanel);
+#pragma unroll
+                for (int pn = 0; pn < kPanels; ++pn) {
+                    tc::tma_load_3d(smem + OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
+                                    &bar[B_KVFULL + st]);
+                    tc::tma_load_3d(smem + OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
+                                    &bar[B_KVFULL + st]);
+                }
+            }
+            __syncwarp();
+            return true;
+        };
+        auto load_q = [&](int n) -> bool {
+            if (n >= nitems) return true;
+            const int st = n % kStages;
+            if (!warp_wait(&bar[B_QEMPTY + st], ((n / kStages) & 1) ^ 1)) return false;
+            if (tc::elect_one()) {
+                mbar_arrive_expect_tx(&bar[B_QFULL + st], static_cast<uint32_t>(kPanels) * kPanel);
+#pragma unroll
+                for (int pn = 0; pn < kPanels; ++pn)
+                    tc::tma_load_3d(smem + OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + n % G,
+                                    row0 + n / G * C, &bar[B_QFULL + st]);
+            }
+            __syncwarp();
+            return true;
+        };
+        if (warp == kLoadWarp)
+            ok = load_kv(0) && load_q(0) && load_kv(1) && load_q(1) && load_q(2);
+        const int tid = 32 * (warp == kLoadWarp ? 0 : warp - 4) + lane;
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kStages;
             if (!warp_wait(&bar[B_KVFULL + st], (i / kStages) & 1)) { ok = false; break; }
@@ -611,50 +627,66 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_VT + vb]);
+            if (warp == kLoadWarp) {
+                for (int n = (i - 1) * G + kStages; n < i * G + kStages && ok; ++n)
+                    if (n >= kStages) ok = load_q(n);
+                ok = ok && load_kv(i + 2);
+            }
         }
+        if (warp == kLoadWarp)
+            for (int n = (nch - 1) * G + kStages; n < nitems && ok; ++n) ok = load_q(n);
     } else {
         // ------------------------------------------------------ outputs
-        // Lane = v index, column = token: a warp stores 32 consecutive floats of a row.
-        const int w = warp & 3, dv = 32 * w + lane;
+        // Lane = v index, column = token: a warp stores 32 consecutive floats
+        // of a row; the second four warps take tokens 32-63.  The state's part
+        // is taken into registers as soon as it is there, so that the next
+        // item's can be computed.
+        const int w = warp & 3, dv = 32 * w + lane, t0 = warp - kOWarp < 4 ? 0 : 32;
         const bool live = 32 * w < D;
-        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16);
+        const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16) + t0;
         const int64_t row_step = static_cast<int64_t>(A.num_q_heads) * D;
+        const float* f = tab + TAB_O + t0;
+        const int64_t row_bytes = row_step * 4;
         for (int n = 0; n < nitems && ok; ++n) {
             const int i = n / G, g = n % G;
-            if (!warp_wait(&bar[B_O], n & 1)) { ok = false; break; }
+            if (!warp_wait(&bar[B_OS], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            const int nrows = min(C, rows - i * C);
-            float* o = A.out + (static_cast<int64_t>(row0) + i * C) * row_step + (h * G + g) * D + dv;
-            const int mark = live ? bad_rows[(i % kBadBuffers) * 128 + dv] : 0;
-            const int nan_from = (mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C;
-            const int plain = min(nrows, __reduce_min_sync(0xffffffffu, nan_from));  // columns that need no check
-#pragma unroll 1
-            for (int t0 = 0; t0 < C; t0 += 16) {
-                uint32_t xs[16], xp[16];
-                if (live) {
-                    tc::tmem_ld32x32b_x16(tl + COL_OS + t0, xs);
-                    tc::tmem_ld32x32b_x16(tl + COL_OP + t0, xp);
-                    tc::tmem_wait_ld();
-                }
-                if (t0 == C - 16) {
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[B_OFREE]);
-                }
-                if (live) {
-                    float* ot = o + t0 * row_step;
-                    const float* ft = tab + TAB_O + t0;
-                    if (t0 + 16 <= plain) {
+            uint32_t xs[32];
+            if (live) {
+                tc::tmem_ld32x32b_x32(tl + COL_OS, xs);
+                tc::tmem_wait_ld();
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_OSFREE]);
+            if (!warp_wait(&bar[B_OP], n & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            uint32_t xp[32];
+            if (live) {
+                tc::tmem_ld32x32b_x32(tl + COL_OP, xp);
+                tc::tmem_wait_ld();
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_OPFREE]);
+            if (live) {
+                const int nrows = min(C, rows - i * C) - t0;
+                const int mark = bad_rows[(i % kBadBuffers) * 128 + dv];
+                const int nan_from = ((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0;
+                float* o = A.out + (static_cast<int64_t>(row0) + i * C + t0) * row_step + (h * G + g) * D + dv;
+                if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            ot[j * row_step] = fmaf(ft[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
-                    } else {
+                    for (int j = 0; j < 32; ++j) {
+                        *o = fmaf(f[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                        o = walk(o, row_bytes);
+                    }
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float y = fmaf(ft[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
-                            if (t0 + j >= nan_from) y = __int_as_float(0x7fffffff);
-                            if (t0 + j < nrows) ot[j * row_step] = y;
-                        }
+                    for (int j = 0; j < 32; ++j) {
+                        float y = fmaf(f[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                        if (j >= nan_from) y = __int_as_float(0x7fffffff);
+                        if (j < nrows) *o = y;
+                        o = walk(o, row_bytes);
                     }
                 }
             }
