@@ -30,6 +30,7 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
 _lib = None
+_calls = None
 
 PKV_OK = 0
 STATUS_NAMES = {
@@ -88,7 +89,7 @@ def lib_path() -> str:
 
 def load():
     """Load libpagedkv.so (raises if it is missing: there is no fallback)."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
@@ -138,8 +139,23 @@ def load():
         fn = getattr(lib, name)
         fn.argtypes = argt
         fn.restype = rest
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("the package's _binding module is not built; run `python -m "
+                           f"paged_kv_cache_291_gb300.build` or __graft_entry__.build() first ({e})") from e
+    _calls = _binding
     _lib = lib
     return lib
+
+
+def _fast():
+    """The compiled calls (csrc/binding.cpp).  Each returns the status of a
+    plain valid call it has made, or None without having launched anything:
+    then the wrapper's own checks say what is wrong, or it makes the call."""
+    if _calls is None:
+        load()
+    return _calls
 
 
 def version() -> str:
@@ -453,9 +469,8 @@ def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, 
     return out
 
 
-# The rotary and linear-attention calls are made once per layer and step, on
-# batches whose kernels take a few microseconds: their checks read each tensor
-# attribute once, and hand addresses over as plain ints.
+# The rotary and linear-attention calls go through the compiled binding; what
+# it hands back is checked and called here.
 
 def _device() -> int:
     """The current device's index: the library launches there, so every
@@ -542,6 +557,15 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved_axes: bool = Fa
     pairs are (i, i + rot_dim/2), or (2i, 2i + 1) with ``adjacent_pairs``.
     Returns (q_out, k_out), contiguous; q_out may be q and k_out k."""
     torch = _torch()
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+    st = _fast().rotary(q, k, positions, inv_freq, sections, interleaved_axes, adjacent_pairs, q_out, k_out, stream)
+    if st == PKV_OK:
+        return q_out, k_out
+    if st is not None:
+        raise PKVError(st, "pkv_rotary")
     lib = load()
     dev = _device()
     bf16 = torch.bfloat16
@@ -550,10 +574,6 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved_axes: bool = Fa
     qp, qs = _rows(q, "q", bf16, dev, qshape)
     kp, ks = _rows(k, "k", bf16, dev, kshape)
     r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T, dev)
-    if q_out is None:
-        q_out = torch.empty(qshape, dtype=bf16, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(kshape, dtype=bf16, device=q.device)
     st = lib.pkv_rotary(ctypes.byref(r), qp, qs, hq, kp, ks, kshape[1], d, T,
                         _addr(q_out, "q_out", bf16, dev, qshape), _addr(k_out, "k_out", bf16, dev, kshape),
                         _stream_handle(stream))
@@ -569,6 +589,14 @@ def rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_fre
     ``q_out`` (returned), turned k and v to their slots.  e4m3 pools need the
     scales; their codes come from the unrounded turned k."""
     torch = _torch()
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    st = _fast().rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_freq, sections,
+                                    interleaved_axes, adjacent_pairs, q_out, k_scale, v_scale, stream)
+    if st == PKV_OK:
+        return q_out
+    if st is not None:
+        raise PKVError(st, "pkv_rotary_cache_write")
     lib = load()
     dev = _device()
     bf16 = torch.bfloat16
@@ -583,8 +611,6 @@ def rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_fre
     kp, ks = _rows(k, "k", bf16, dev, kshape)
     vp, vs = _rows(v, "v", bf16, dev, kshape)
     r = _rotary(positions, inv_freq, sections, interleaved_axes, adjacent_pairs, T, dev)
-    if q_out is None:
-        q_out = torch.empty(qshape, dtype=bf16, device=q.device)
     st = lib.pkv_rotary_cache_write(ctypes.byref(c), ctypes.byref(r), qp, qs, hq, kp, ks, vp, vs,
                                     _addr(slot_mapping, "slot_mapping", torch.int32, dev, (T,)), T,
                                     _addr(q_out, "q_out", bf16, dev, qshape), _stream_handle(stream))
@@ -610,6 +636,13 @@ def linear_decode_attention(states, log_decay, q, k, v, state_slots, context_len
     [B][Hq][d].  context_lens counts the token: 1 starts from a zero state,
     0 marks padding."""
     torch = _torch()
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    st = _fast().linear_decode(states, log_decay, q, k, v, state_slots, context_lens, scale, new_slots, out, stream)
+    if st == PKV_OK:
+        return out
+    if st is not None:
+        raise PKVError(st, "pkv_linear_decode_attention")
     lib = load()
     dev = _device()
     bf16, i32 = torch.bfloat16, torch.int32
@@ -619,8 +652,6 @@ def linear_decode_attention(states, log_decay, q, k, v, state_slots, context_len
     qp, qs = _rows(q, "q", bf16, dev, qshape)
     kp, ks = _rows(k, "k", bf16, dev, kshape)
     vp, vs = _rows(v, "v", bf16, dev, kshape)
-    if out is None:
-        out = torch.empty(qshape, dtype=torch.float32, device=q.device)
     st = lib.pkv_linear_decode_attention(
         ctypes.byref(s), qp, qs, hq, kp, ks, vp, vs, _addr(state_slots, "state_slots", i32, dev, per_seq),
         None if new_slots is None else _addr(new_slots, "new_slots", i32, dev, per_seq),
@@ -645,6 +676,21 @@ def linear_prefill_attention(states, log_decay, q, k, v, query_start_loc, state_
     float32 [T][Hq][d].  context_lens counts the call's tokens: a sequence
     starts from zero when it has no others."""
     torch = _torch()
+    qh = query_start_loc if query_start_loc_host is None else query_start_loc_host
+    if not isinstance(qh, torch.Tensor) or qh.is_cuda or qh.dtype is not torch.int32:
+        qh = torch.from_numpy(_host_i32(qh)[0])
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        need = load().pkv_linear_prefill_workspace_size(context_lens.shape[0], q.shape[0], q.shape[1], k.shape[1],
+                                                        q.shape[2])
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    st = _fast().linear_prefill(states, log_decay, q, k, v, state_slots, context_lens, scale, new_slots, out, stream,
+                                query_start_loc, qh, workspace)
+    if st == PKV_OK:
+        return out
+    if st is not None:
+        raise PKVError(st, "pkv_linear_prefill_attention")
     lib = load()
     dev = _device()
     bf16, i32 = torch.bfloat16, torch.int32
@@ -655,21 +701,11 @@ def linear_prefill_attention(states, log_decay, q, k, v, query_start_loc, state_
     qp, qs = _rows(q, "q", bf16, dev, qshape)
     kp, ks = _rows(k, "k", bf16, dev, kshape)
     vp, vs = _rows(v, "v", bf16, dev, kshape)
-    qh = query_start_loc if query_start_loc_host is None else query_start_loc_host
-    if isinstance(qh, torch.Tensor) and qh.dtype is i32 and not qh.is_cuda and qh.is_contiguous():
-        qhp = qh.data_ptr()
-    else:
-        qh, qhp = _host_i32(qh)
-    if qh.shape != (S + 1,):
+    if qh.shape != (S + 1,) or not qh.is_contiguous():
         raise ValueError("query_start_loc_host must have num_seqs + 1 entries")
-    if out is None:
-        out = torch.empty(qshape, dtype=torch.float32, device=q.device)
-    if workspace is None:
-        need = lib.pkv_linear_prefill_workspace_size(S, T, hq, kshape[1], d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     st = lib.pkv_linear_prefill_attention(
         ctypes.byref(s), qp, qs, hq, kp, ks, vp, vs, T,
-        _addr(query_start_loc, "query_start_loc", i32, dev, (S + 1,)), qhp,
+        _addr(query_start_loc, "query_start_loc", i32, dev, (S + 1,)), qh.data_ptr(),
         _addr(state_slots, "state_slots", i32, dev, per_seq),
         None if new_slots is None else _addr(new_slots, "new_slots", i32, dev, per_seq),
         _addr(context_lens, "context_lens", i32, dev, per_seq), S, scale, _out_addr(out, dev, qshape),

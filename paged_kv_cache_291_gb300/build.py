@@ -2,7 +2,9 @@
 
 Each .cu under csrc/ is compiled to an object in parallel, then the objects
 are linked into ``libpagedkv.so`` beside this file (CUDA runtime linked
-statically, only the ``pkv_*`` symbols exported).  Used by
+statically, only the ``pkv_*`` symbols exported).  csrc/binding.cpp, the
+CPython module that hands torch tensors to some of the calls, is compiled
+against the installed torch at the same time.  Used by
 ``__graft_entry__.build()`` and by the package on import when the library is
 stale; it needs nvcc but no GPU.
 """
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(HERE, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,14 +42,14 @@ def sources():
 def _deps():
     files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "pkv.h"))
-    files.append(os.path.abspath(__file__))
+    files += [BINDING_SRC, os.path.abspath(__file__)]
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -69,14 +74,40 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
+    binding_obj = os.path.join(BUILD, "binding.o")
+
+    def compile_binding():
+        import torch
+        from torch.utils import cpp_extension
+        cmd = [os.environ.get("CXX", "g++"), "-c", BINDING_SRC, "-o", binding_obj, "-O2", "-std=c++17", "-fPIC",
+               "-fvisibility=hidden", "-w", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+               "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+               "-I", os.path.join(os.path.dirname(os.path.dirname(cc)), "include")]
+        for d in cpp_extension.include_paths():
+            cmd += ["-isystem", d]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+
     with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, "-shared"] + ARCH + ["-o", tmp] + objs + ["-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding_obj, "-L", HERE, "-lpagedkv", "-L", libs,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,$ORIGIN,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
     return LIB
 
 
