@@ -41,47 +41,62 @@ namespace {
 
 constexpr int C = 64;                    // tokens per chunk
 constexpr int kPanel = C * 128;          // [64 tokens][64 dims] bf16, 128-byte swizzle
-constexpr int kTile = 2 * kPanel;        // room for head_dim 128
-constexpr int kStages = 3;               // K, V and Q tiles
-constexpr int kVtBufs = 1;               // V~
+constexpr int kPTile = C * 128;          // one term of P, [64 s][64 t] bf16
 
-constexpr int OFF_K = 0;
-constexpr int OFF_V = OFF_K + kStages * kTile;
-constexpr int OFF_Q = OFF_V + kStages * kTile;
-constexpr int OFF_VT = OFF_Q + kStages * kTile;       // V~: three terms
-constexpr int OFF_P = OFF_VT + kVtBufs * 3 * kTile;           // P: three terms of [64 s][64 t]
-constexpr int OFF_TAB = OFF_P + 3 * kPanel;           // factors
+// Ring depths and the shared-memory map of the main kernel.
+template <int D>
+struct Layout {
+    static constexpr int kTile = D / 64 * kPanel;     // a K, V or Q tile, or one term of V~
+    static constexpr int kKv = D == 64 ? 4 : 3;       // K and V stages
+    static constexpr int kQ = D == 64 ? 4 : 2;        // Q stages
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = OFF_K + kKv * kTile;
+    static constexpr int OFF_Q = OFF_V + kKv * kTile;
+    static constexpr int OFF_VT = OFF_Q + kQ * kTile;
+    static constexpr int OFF_P = OFF_VT + 3 * kTile;  // two buffers of three terms
+    static constexpr int OFF_REST = OFF_P + 2 * 3 * kPTile;
+};
 constexpr int TAB_P = 0;                              // float[128]: scale lam^(t-s) at 63 + t - s
 constexpr int TAB_O = 128;                            // float[64]: scale lam^(t+1)
 constexpr int TAB_V = 192;                            // float[64]: lam^j
 constexpr int TAB_LAM = 256;                          // float2: lam^64
-constexpr int OFF_BAD = OFF_TAB + 264 * 4;            // int[4][128], see kBadBuffers
-constexpr int OFF_BAR = OFF_BAD + 4 * 128 * 4;
-constexpr int kBadBuffers = 4;
+constexpr int kBadBuffers = 3;
 
 enum {
-    B_KVFULL = 0,               // + stage
-    B_KVEMPTY = B_KVFULL + kStages,
-    B_QFULL = B_KVEMPTY + kStages,
-    B_QEMPTY = B_QFULL + kStages,
-    B_SCORES = B_QEMPTY + kStages,  // scores in TMEM
-    B_P,                        // P in shared memory (3 arrivals)
-    B_PFREE,                    // P read
-    B_S,                        // S split and decayed (8 arrivals)
+    B_KVFULL = 0,               // + stage (room for 4)
+    B_KVEMPTY = B_KVFULL + 4,
+    B_QFULL = B_KVEMPTY + 4,
+    B_QEMPTY = B_QFULL + 4,
+    B_SCORES = B_QEMPTY + 4,    // scores in TMEM
+    B_SCFREE,                   // and read (3 arrivals)
+    B_P,                        // + buffer: P in shared memory (3 arrivals)
+    B_PFREE = B_P + 2,          // + buffer: P read
+    B_S = B_PFREE + 2,          // S split and decayed (8 arrivals)
     B_SFREE,                    // the split S read by every q head of the chunk
-    B_VT,                       // + buffer: V~ in shared memory (4 arrivals)
-    B_VTFREE = B_VT + kVtBufs,  // + buffer: V~ read, S holds the chunk
-    B_OS = B_VTFREE + kVtBufs,  // the state's part of the outputs in TMEM
+    B_VT,                       // V~ in shared memory (4 arrivals)
+    B_VTFREE,                   // V~ read, S holds the chunk
+    B_OS,                       // the state's part of the outputs in TMEM
     B_OSFREE,                   // and read (8 arrivals)
     B_OP,                       // the scores' part
     B_OPFREE,
     NBAR
 };
-constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
-constexpr int OFF_TMEM = OFF_INFO + 16 * 4;
-constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;      // slack to align the base to 1024 B
-static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB)");
-static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
+enum { I_SEQ = 0, I_ROW0, I_ROWS, I_LOAD, I_STORE, I_BOUND, I_BAD, I_COUNT };
+
+// What follows the tiles.
+struct Rest {
+    float tab[258];
+    int bad_rows[kBadBuffers][128];  // see where V~ is made
+    uint64_t bar[NBAR];
+    int info[I_COUNT];
+    uint32_t tmem;
+};
+template <int D>
+constexpr int smem_bytes() {
+    return Layout<D>::OFF_REST + static_cast<int>(sizeof(Rest));
+}
+static_assert(smem_bytes<128>() <= 232448, "shared memory budget (227 KB)");
+static_assert(2 * smem_bytes<64>() > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
 
 // Warps, spread so that the four SM sub-partitions (warp % 4, which is also
 // the TMEM lane quarter a warp can reach) carry about the same work.
@@ -93,8 +108,6 @@ constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 
 // TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
 constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
-
-enum { I_SEQ = 0, I_ROW0, I_ROWS, I_FIRST, I_LAST, I_LOAD, I_STORE, I_BOUND, I_BAD };
 
 struct ChunkParams {
     LinearArgs A;
@@ -185,7 +198,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { retu
 // * extra * v_s in three terms.  Rows past the piece become zero, there and in
 // K and V: they are other sequences' tokens, and a zero factor times a NaN
 // would poison the products.  Returns 0, or NaN if a value was not finite.
-template <int D, int THREADS, int UNROLL>
+template <int D, int TERM, int THREADS, int UNROLL>
 __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t svt, const float* factor, float extra,
                                            int rows, int tid) {
     constexpr int kChunks = C * D * 2 / 16;  // 16-byte vectors of the tile
@@ -207,12 +220,12 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
                 split3(__fmul2_rn(v, ff), hi[j], mid[j], lo[j]);
             }
             tc::sts128(svt + at, hi[0], hi[1], hi[2], hi[3]);
-            tc::sts128(svt + kTile + at, mid[0], mid[1], mid[2], mid[3]);
-            tc::sts128(svt + 2 * kTile + at, lo[0], lo[1], lo[2], lo[3]);
+            tc::sts128(svt + TERM + at, mid[0], mid[1], mid[2], mid[3]);
+            tc::sts128(svt + 2 * TERM + at, lo[0], lo[1], lo[2], lo[3]);
         } else {
             tc::sts128(svt + at, 0u, 0u, 0u, 0u);
-            tc::sts128(svt + kTile + at, 0u, 0u, 0u, 0u);
-            tc::sts128(svt + 2 * kTile + at, 0u, 0u, 0u, 0u);
+            tc::sts128(svt + TERM + at, 0u, 0u, 0u, 0u);
+            tc::sts128(svt + 2 * TERM + at, 0u, 0u, 0u, 0u);
             tc::sts128(sv + at, 0u, 0u, 0u, 0u);
             tc::sts128(sk + at, 0u, 0u, 0u, 0u);
         }
@@ -222,13 +235,13 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
 
 // S^T += (V~)^T K for one chunk, V~ in three terms: A is V~ stored [s][v]
 // (v contiguous), B is K stored [s][k] (k contiguous).
-template <int D>
+template <int D, int TERM>
 __device__ __forceinline__ void mma_state(uint32_t col_s, uint32_t svt, uint32_t sk, bool accumulate) {
     constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 1, 1);
     const uint64_t b = tc::smem_desc_sw128(sk, kPanel, 1024);
 #pragma unroll 1
     for (int part = 2; part >= 0; --part) {  // smallest first: the sums truncate
-        const uint64_t a = tc::smem_desc_sw128(svt + part * kTile, kPanel, 1024);
+        const uint64_t a = tc::smem_desc_sw128(svt + part * TERM, kPanel, 1024);
 #pragma unroll
         for (int k = 0; k < C / 16; ++k)
             tc::mma_bf16_ss(col_s, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc,
@@ -240,27 +253,33 @@ template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const ChunkParams P) {
+    using L = Layout<D>;
     constexpr int kPanels = D / 64;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-    int* info = reinterpret_cast<int*>(smem + OFF_INFO);
-    float* tab = reinterpret_cast<float*>(smem + OFF_TAB);
-    int* bad_rows = reinterpret_cast<int*>(smem + OFF_BAD);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+    constexpr int kTile = L::kTile, kKv = L::kKv, kQ = L::kQ;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Rest& rest = *reinterpret_cast<Rest*>(smem + L::OFF_REST);
+    uint64_t* bar = rest.bar;
+    int* info = rest.info;
+    float* tab = rest.tab;
+    uint32_t* tmem_slot = &rest.tmem;
     const LinearArgs& A = P.A;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int h = blockIdx.y;
 
     // ---------------------------------------------------------- setup
     griddep_launch_dependents();
+    if ((smem_addr(smem) & 1023) != 0) {  // the swizzled tiles need it; dynamic shared memory starts there
+        griddep_wait();
+        if (threadIdx.x == 0) record_error(A.err, kErrRange, 0xffffffffu);
+        return;
+    }
     if (threadIdx.x == 32 * kMmaWarp) {
         for (int i = 0; i < NBAR; ++i)
-            mbar_init(&bar[i], i == B_P                                  ? 3u
-                                : i == B_S                               ? static_cast<uint32_t>(kSWarps)
-                                : i >= B_VT && i < B_VT + kVtBufs        ? static_cast<uint32_t>(kVWarps)
-                                : i == B_OSFREE || i == B_OPFREE         ? static_cast<uint32_t>(kOWarps)
-                                                                         : 1u);
+            mbar_init(&bar[i], i == B_SCFREE || i == B_P || i == B_P + 1 ? 3u
+                                : i == B_S                                ? static_cast<uint32_t>(kSWarps)
+                                : i == B_VT                               ? static_cast<uint32_t>(kVWarps)
+                                : i == B_OSFREE || i == B_OPFREE          ? static_cast<uint32_t>(kOWarps)
+                                                                          : 1u);
         fence_mbar_init();
     }
     if (warp == kLoadWarp) {
@@ -272,9 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::prefetch_tensormap(&tm_v);
         }
     }
-    for (int i = threadIdx.x; i < kBadBuffers * 128; i += kThreads) bad_rows[i] = 0;
-    for (int i = threadIdx.x; i < 3 * kPanel / 16; i += kThreads)
-        tc::sts128(smem_addr(smem + OFF_P) + i * 16, 0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < kBadBuffers * 128; i += kThreads) rest.bad_rows[0][i] = 0;
+    for (int i = threadIdx.x; i < 2 * 3 * kPTile / 16; i += kThreads)
+        tc::sts128(smem_addr(smem + L::OFF_P) + i * 16, 0u, 0u, 0u, 0u);
     tc::fence_proxy_async_smem();
     griddep_wait();
     if (warp == 0) {
@@ -343,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdescScores = tc::idesc_bf16_f32(128, C, 0, 0);
         constexpr uint32_t kIdescOS = tc::idesc_bf16_f32(128, C, 0, 0);
         constexpr uint32_t kIdescOP = tc::idesc_bf16_f32(128, C, 1, 1);
-        const uint32_t sk0 = smem_addr(smem + OFF_K), sv0 = smem_addr(smem + OFF_V), sq0 = smem_addr(smem + OFF_Q);
-        const uint32_t svt = smem_addr(smem + OFF_VT), sp = smem_addr(smem + OFF_P);
+        const uint32_t sk0 = smem_addr(smem + L::OFF_K), sv0 = smem_addr(smem + L::OFF_V), sq0 = smem_addr(smem + L::OFF_Q);
+        const uint32_t svt = smem_addr(smem + L::OFF_VT), sp = smem_addr(smem + L::OFF_P);
         // scores[s][t] = k_s . q_t (lanes past 63 take the rows that follow K in
         // shared memory: never read)
         // Descriptors of consecutive K steps differ by their address field.
         auto scores = [&](int n) {
-            const uint64_t a = tc::smem_desc_sw128(sk0 + (n / G % kStages) * kTile, 16, 1024);
-            const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kStages) * kTile, 16, 1024);
+            const uint64_t a = tc::smem_desc_sw128(sk0 + (n / G % kKv) * kTile, 16, 1024);
+            const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kQ) * kTile, 16, 1024);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t step = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
@@ -360,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // O_S^T[v][t] = sum_k S^T[v][k] q_t[k], S^T in three terms from TMEM
         auto out_state = [&](int n) {
-            const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kStages) * kTile, 16, 1024);
+            const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kQ) * kTile, 16, 1024);
 #pragma unroll 1
             for (int part = 2; part >= 0; --part) {
                 const uint32_t a = tmem + COL_SB + part * (D / 2);
@@ -369,22 +388,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::mma_bf16_ts(tmem + COL_OS, a + 8 * k, b + (((k >> 2) * kPanel + (k & 3) * 32) >> 4), kIdescOS,
                                     part < 2 || k > 0 ? 1u : 0u);
             }
-            tc::mma_commit(&bar[B_QEMPTY + n % kStages]);
+            tc::mma_commit(&bar[B_QEMPTY + n % kQ]);
             tc::mma_commit(&bar[B_OS]);
         };
         // O_P^T[v][t] = sum_s V[s][v] P[s][t], P in three terms
         auto out_scores = [&](int n) {
-            const uint64_t a = tc::smem_desc_sw128(sv0 + (n / G % kStages) * kTile, kPanel, 1024);
+            const uint64_t a = tc::smem_desc_sw128(sv0 + (n / G % kKv) * kTile, kPanel, 1024);
 #pragma unroll 1
             for (int part = 2; part >= 0; --part) {
-                const uint64_t b = tc::smem_desc_sw128(sp + part * kPanel, kPanel, 1024);
+                const uint64_t b = tc::smem_desc_sw128(sp + ((n & 1) * 3 + part) * kPTile, kPTile, 1024);
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
                     tc::mma_bf16_ss(tmem + COL_OP, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdescOP,
                                     part < 2 || k > 0 ? 1u : 0u);
             }
-            if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kStages]);
-            tc::mma_commit(&bar[B_PFREE]);
+            if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kKv]);
+            tc::mma_commit(&bar[B_PFREE + (n & 1)]);
             tc::mma_commit(&bar[B_OP]);  // last: once it is seen, nothing of this thread is in flight
         };
         if (nitems > 0) {
@@ -403,22 +422,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (g == 0) {
-                if (!warp_wait(&bar[B_VT + i % kVtBufs], (i / kVtBufs) & 1)) { ok = false; break; }
+                if (!warp_wait(&bar[B_VT], i & 1)) { ok = false; break; }
                 if (tc::elect_one()) {
-                    mma_state<D>(tmem + COL_S, svt + (i % kVtBufs) * 3 * kTile, sk0 + (i % kStages) * kTile, true);
-                    tc::mma_commit(&bar[B_VTFREE + i % kVtBufs]);
+                    mma_state<D, kTile>(tmem + COL_S, svt, sk0 + (i % kKv) * kTile, true);
+                    tc::mma_commit(&bar[B_VTFREE]);
                 }
                 __syncwarp();
             }
-            if (!warp_wait(&bar[B_P], n & 1)) { ok = false; break; }
             if (n + 1 < nitems) {
                 const int i1 = (n + 1) / G;
-                if (i1 != i && !warp_wait(&bar[B_KVFULL + i1 % kStages], (i1 / kStages) & 1)) { ok = false; break; }
-                if (!warp_wait(&bar[B_QFULL + (n + 1) % kStages], ((n + 1) / kStages) & 1)) { ok = false; break; }
+                if (!warp_wait(&bar[B_SCFREE], n & 1) ||
+                    (i1 != i && !warp_wait(&bar[B_KVFULL + i1 % kKv], (i1 / kKv) & 1)) ||
+                    !warp_wait(&bar[B_QFULL + (n + 1) % kQ], ((n + 1) / kQ) & 1)) {
+                    ok = false;
+                    break;
+                }
                 tc::fence_after_sync();
                 if (tc::elect_one()) scores(n + 1);
                 __syncwarp();
             }
+            if (!warp_wait(&bar[B_P + (n & 1)], (n >> 1) & 1)) { ok = false; break; }
             if (n > 0 && !warp_wait(&bar[B_OPFREE], (n - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) out_scores(n);
@@ -427,47 +450,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 0 || warp == 1 || warp == 4) {
         // ------------------------------------------------------ P
         const int s = 32 * (warp & 1) + lane, begin = warp == 0 ? 0 : 32;
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + COL_SCORES;
-        const uint32_t prow = smem_addr(smem + OFF_P) + s * 128;
-        const float* f = tab + TAB_P + 63 - s;
-        const bool masked = warp != 4;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + COL_SCORES + begin;
+        const uint32_t prow = smem_addr(smem + L::OFF_P) + s * 128;
+        const float* f = tab + TAB_P + 63 - s + begin;
+        // Rows 32-63 keep the zeros of tokens 0-31 that the set-up wrote.
+        auto convert = [&](const uint32_t (&x)[32], uint32_t at, int first) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = 8 * c + 2 * j;
+                    float2 y = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])),
+                                          make_float2(f[t], f[t + 1]));
+                    // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
+                    if (t < first) y.x = 0.f;
+                    if (t + 1 < first) y.y = 0.f;
+                    split3(y, hi[j], mid[j], lo[j]);
+                }
+                const uint32_t a = at + (((begin / 8 + c) ^ (s & 7)) << 4);
+                tc::sts128(a, hi[0], hi[1], hi[2], hi[3]);
+                tc::sts128(a + kPTile, mid[0], mid[1], mid[2], mid[3]);
+                tc::sts128(a + 2 * kPTile, lo[0], lo[1], lo[2], lo[3]);
+            }
+        };
         for (int n = 0; n < nitems && ok; ++n) {
             if (!warp_wait(&bar[B_SCORES], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            if (n > 0 && !warp_wait(&bar[B_PFREE], (n - 1) & 1)) { ok = false; break; }
-            // Rows 32-63 keep the zeros of tokens 0-31 that the set-up wrote.
-#pragma unroll 1
-            for (int t0 = begin; t0 < begin + 32; t0 += 16) {
-                uint32_t x[16];
-                tc::tmem_ld32x32b_x16(taddr + t0, x);
-                tc::tmem_wait_ld();
-                const float* ft = f + t0;
-                const int first = s - t0;  // columns before it are masked
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int t = 8 * c + 2 * j;
-                        // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
-                        float2 y = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])),
-                                              make_float2(ft[t], ft[t + 1]));
-                        if (masked) {
-                            if (t < first) y.x = 0.f;
-                            if (t + 1 < first) y.y = 0.f;
-                        }
-                        split3(y, hi[j], mid[j], lo[j]);
-                    }
-                    const uint32_t at = prow + (((t0 / 8 + c) ^ (s & 7)) << 4);
-                    tc::sts128(at, hi[0], hi[1], hi[2], hi[3]);
-                    tc::sts128(at + kPanel, mid[0], mid[1], mid[2], mid[3]);
-                    tc::sts128(at + 2 * kPanel, lo[0], lo[1], lo[2], lo[3]);
-                }
-            }
-            tc::fence_proxy_async_smem();
+            uint32_t x[32];
+            tc::tmem_ld32x32b_x32(taddr, x);
+            tc::tmem_wait_ld();
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_P]);
+            if (lane == 0) mbar_arrive(&bar[B_SCFREE]);
+            if (!warp_wait(&bar[B_PFREE + (n & 1)], ((n >> 1) & 1) ^ 1)) { ok = false; break; }
+            const uint32_t at = prow + (n & 1) * 3 * kPTile;
+            if (warp == 4) convert(x, at, 0);
+            else convert(x, at, lane);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_P + (n & 1)]);
         }
     } else if (warp >= kSWarp && warp < kSWarp + kSWarps) {
         // ------------------------------------------------------ S
@@ -514,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < nch && ok; ++i) {
             // S may be read when the last chunk's update is in it, its terms
             // replaced when the last outputs have read them.
-            if (i > 0 && !warp_wait(&bar[B_VTFREE + (i - 1) % kVtBufs], ((i - 1) / kVtBufs) & 1)) { ok = false; break; }
+            if (i > 0 && !warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             uint32_t xa[16], xb[16];
             if (live) tc::tmem_ld32x32b_x16(ts, xa);
@@ -540,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar[B_S]);
         }
         if (ok && nch > 0 && info[I_STORE] >= 0 && live) {
-            if (!warp_wait(&bar[B_VTFREE + (nch - 1) % kVtBufs], ((nch - 1) / kVtBufs) & 1)) {
+            if (!warp_wait(&bar[B_VTFREE], (nch - 1) & 1)) {
                 ok = false;
             } else {
                 tc::fence_after_sync();
@@ -562,15 +584,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // could start, so neither holds the other up.
         auto load_kv = [&](int i) -> bool {
             if (i >= nch) return true;
-            const int st = i % kStages;
-            if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kStages) & 1) ^ 1)) return false;
+            const int st = i % kKv;
+            if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kKv) & 1) ^ 1)) return false;
             if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[B_KVFULL + st], 2u * kPanels * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn) {
-                    tc::tma_load_3d(smem + OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
+                    tc::tma_load_3d(smem + L::OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
                                     &bar[B_KVFULL + st]);
-                    tc::tma_load_3d(smem + OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
+                    tc::tma_load_3d(smem + L::OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
                                     &bar[B_KVFULL + st]);
                 }
             }
@@ -579,30 +601,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto load_q = [&](int n) -> bool {
             if (n >= nitems) return true;
-            const int st = n % kStages;
-            if (!warp_wait(&bar[B_QEMPTY + st], ((n / kStages) & 1) ^ 1)) return false;
+            const int st = n % kQ;
+            if (!warp_wait(&bar[B_QEMPTY + st], ((n / kQ) & 1) ^ 1)) return false;
             if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[B_QFULL + st], static_cast<uint32_t>(kPanels) * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn)
-                    tc::tma_load_3d(smem + OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + n % G,
+                    tc::tma_load_3d(smem + L::OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + n % G,
                                     row0 + n / G * C, &bar[B_QFULL + st]);
             }
             __syncwarp();
             return true;
         };
-        if (warp == kLoadWarp)
-            ok = load_kv(0) && load_q(0) && load_kv(1) && load_q(1) && load_q(2);
+        if (warp == kLoadWarp) {
+            ok = load_kv(0);
+            for (int n = 0; n < kQ && ok; ++n) ok = load_q(n);
+            for (int i = 1; i < kKv - 1 && ok; ++i) ok = load_kv(i);
+        }
         const int tid = 32 * (warp == kLoadWarp ? 0 : warp - 4) + lane;
         for (int i = 0; i < nch && ok; ++i) {
-            const int st = i % kStages;
-            if (!warp_wait(&bar[B_KVFULL + st], (i / kStages) & 1)) { ok = false; break; }
-            const int vb = i % kVtBufs;
-            if (!warp_wait(&bar[B_VTFREE + vb], ((i / kVtBufs) & 1) ^ 1)) { ok = false; break; }
+            const int st = i % kKv;
+            if (!warp_wait(&bar[B_KVFULL + st], (i / kKv) & 1)) { ok = false; break; }
+            if (!warp_wait(&bar[B_VTFREE], (i & 1) ^ 1)) { ok = false; break; }
             const int nrows = min(C, rows - i * C);
-            const uint32_t sk = smem_addr(smem + OFF_K + st * kTile), sv = smem_addr(smem + OFF_V + st * kTile);
-            const float acc = convert_v<D, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + OFF_VT) + vb * 3 * kTile,
-                                                              tab + TAB_V, 1.f, nrows, tid);
+            const uint32_t sk = smem_addr(smem + L::OFF_K + st * kTile), sv = smem_addr(smem + L::OFF_V + st * kTile);
+            const float acc = convert_v<D, kTile, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + L::OFF_VT), tab + TAB_V,
+                                                                     1.f, nrows, tid);
             if (acc != 0.f) {
                 // A value that is not finite reaches the outputs of its column
                 // from its row on, and no earlier row: it leaves V for P V
@@ -618,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if ((u & 0x7f80u) == 0x7f80u) {
                             x[e / 2] &= e % 2 ? 0x0000ffffu : 0xffff0000u;
                             const int col = (c >> 9) * 64 + (((c & 7) ^ (row & 7)) << 3) + e;
-                            atomicMax(&bad_rows[(i % kBadBuffers) * 128 + col], ((i + 1) << 6) | (C - 1 - row));
+                            atomicMax(&rest.bad_rows[i % kBadBuffers][col], ((i + 1) << 6) | (C - 1 - row));
                         }
                     }
                     tc::sts128(sv + c * 16, x[0], x[1], x[2], x[3]);
@@ -626,15 +650,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_VT + vb]);
+            if (lane == 0) mbar_arrive(&bar[B_VT]);
             if (warp == kLoadWarp) {
-                for (int n = (i - 1) * G + kStages; n < i * G + kStages && ok; ++n)
-                    if (n >= kStages) ok = load_q(n);
-                ok = ok && load_kv(i + 2);
+                for (int n = (i - 1) * G + kQ; n < i * G + kQ && ok; ++n)
+                    if (n >= kQ) ok = load_q(n);
+                ok = ok && load_kv(i + kKv - 1);
             }
         }
         if (warp == kLoadWarp)
-            for (int n = (nch - 1) * G + kStages; n < nitems && ok; ++n) ok = load_q(n);
+            for (int n = (nch - 1) * G + kQ; n < nitems && ok; ++n) ok = load_q(n);
     } else {
         // ------------------------------------------------------ outputs
         // Lane = v index, column = token: a warp stores 32 consecutive floats
@@ -671,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar[B_OPFREE]);
             if (live) {
                 const int nrows = min(C, rows - i * C) - t0;
-                const int mark = bad_rows[(i % kBadBuffers) * 128 + dv];
+                const int mark = rest.bad_rows[i % kBadBuffers][dv];
                 const int nan_from = ((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0;
                 float* o = A.out + (static_cast<int64_t>(row0) + i * C + t0) * row_step + (h * G + g) * D + dv;
                 if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
@@ -710,6 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // part of V~).  Warps 0-7 V~, 8 loads, 9 MMA; warps 0-3 store the sum.
 constexpr int kStateThreads = 320;
 constexpr int kStateStages = 3;
+constexpr int kTile = 2 * kPanel;        // room for head_dim 128
 constexpr int SOFF_K = 0;
 constexpr int SOFF_V = SOFF_K + kStateStages * kTile;
 constexpr int SOFF_VT = SOFF_V + kStateStages * kTile;     // two buffers of three terms
@@ -796,7 +821,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (!warp_wait(&bar[SB_VT + vb], (i >> 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) {
-                mma_state<D>(tmem, smem_addr(smem + SOFF_VT + vb * 3 * kTile), smem_addr(smem + SOFF_K + st * kTile),
+                mma_state<D, kTile>(tmem, smem_addr(smem + SOFF_VT + vb * 3 * kTile), smem_addr(smem + SOFF_K + st * kTile),
                              i > 0);
                 tc::mma_commit(&bar[SB_EMPTY + st]);
                 tc::mma_commit(&bar[SB_VTFREE + vb]);
@@ -809,7 +834,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             const int st = i % kStateStages, vb = i & 1;
             if (!warp_wait(&bar[SB_FULL + st], (i / kStateStages) & 1)) { ok = false; break; }
             if (!warp_wait(&bar[SB_VTFREE + vb], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
-            convert_v<D, 256, 2>(smem_addr(smem + SOFF_K + st * kTile), smem_addr(smem + SOFF_V + st * kTile),
+            convert_v<D, kTile, 256, 2>(smem_addr(smem + SOFF_K + st * kTile), smem_addr(smem + SOFF_V + st * kTile),
                               smem_addr(smem + SOFF_VT + vb * 3 * kTile), tab,
                               expf(g * static_cast<float>((nch - 1 - i) * C)), C, threadIdx.x);
             tc::fence_proxy_async_smem();
@@ -908,10 +933,10 @@ template <int D, int G>
 cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
                         cudaStream_t stream) {
     static bool done[64] = {};
-    cudaError_t e = configure(linear_chunk_kernel<D, G>, SMEM_BYTES, done);
+    cudaError_t e = configure(linear_chunk_kernel<D, G>, smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.total, P.A.num_kv_heads), dim3(kThreads), SMEM_BYTES,
-                             stream, tq, tk, tv, P);
+    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.total, P.A.num_kv_heads), dim3(kThreads),
+                             smem_bytes<D>(), stream, tq, tk, tv, P);
 }
 
 template <int D>
