@@ -890,8 +890,7 @@ PKV_API size_t pkv_linear_prefill_workspace_size(int32_t num_seqs, int32_t num_t
     if (head_dim != 64 && head_dim != 128) return 0;
     DeviceState* dev = nullptr;
     if (current_device(&dev) != PKV_OK) return 0;
-    const size_t bounds = static_cast<size_t>(pkv::linear_max_bounds(num_tokens, num_kv_heads, dev->num_sms));
-    return std::max<size_t>(256, bounds * num_kv_heads * head_dim * head_dim * sizeof(float));
+    return pkv::linear_workspace_bytes(num_seqs, num_tokens, num_kv_heads, head_dim, dev->num_sms);
 }
 
 PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
@@ -916,16 +915,17 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
     if ((st = fill_linear(states, q, q_stride, num_q_heads, k, k_stride, v, v_stride, state_slots, new_slots,
                           context_lens, num_seqs, num_tokens, scale, out, &a, &dev)) != PKV_OK)
         return st;
-    const size_t need = static_cast<size_t>(pkv::linear_max_bounds(num_tokens, a.num_kv_heads, dev->num_sms)) *
-                        a.num_kv_heads * a.head_dim * a.head_dim * sizeof(float);
-    if (workspace_bytes < need) return PKV_ERR_WORKSPACE;
+    if (workspace_bytes <
+        pkv::linear_workspace_bytes(num_seqs, num_tokens, a.num_kv_heads, a.head_dim, dev->num_sms))
+        return PKV_ERR_WORKSPACE;
     a.query_start_loc = query_start_loc;
     a.max_recurrent = 16;
     const pkv::LinearPlan plan = pkv::plan_linear(query_start_loc_host, num_seqs, num_tokens, a.num_kv_heads,
-                                                  num_q_heads / a.num_kv_heads, dev->num_sms, a.max_recurrent);
+                                                  num_q_heads / a.num_kv_heads, a.head_dim, dev->num_sms,
+                                                  a.max_recurrent);
     cudaError_t e = cudaSuccess;
     if (plan.recurrent > 0) e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = pkv::launch_linear_chunks(a, plan, workspace, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = pkv::launch_linear_chunks(a, plan, workspace, dev->num_sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 

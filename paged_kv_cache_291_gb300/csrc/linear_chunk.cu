@@ -17,15 +17,15 @@
 // (16 bits) would be off by 2^-17 of each value.  The state's decay factor is
 // an fp32 pair.
 //
-// Split.  A CTA takes one kv head of one piece of a sequence and walks its
-// chunks; all q heads of the group share the state's work.  Its warps have
+// Split.  A CTA takes one kv head of a range of chunks and walks them; all q
+// heads of the group share the state's work.  Its warps have
 // one part each: loads (TMA, 128-byte swizzle), MMA issue, P, V~, S (read,
 // split, decay) and the output; barriers order them, so the tensor cores work
 // on one chunk while the others prepare the next.
-// Few (sequence, head) pairs leave SMs idle, so sequences are cut into pieces
-// of equal chunk counts: linear_state_kernel sums each piece's own state
-// (all but the last of a sequence), linear_scan_kernel carries the states
-// over the pieces, and the main kernel starts each piece from its own.
+// The chunks of all sequences are cut into equal ranges, one CTA each per kv
+// head, whatever the lengths of the sequences.  Where a border lies inside a
+// sequence, linear_state_kernel sums the part's own state first and
+// linear_scan_kernel carries the states over the borders.
 //
 // Every wait is bounded; TMEM is freed on every exit path.
 #include <cuda.h>
@@ -81,7 +81,7 @@ enum {
     B_OPFREE,
     NBAR
 };
-enum { I_SEQ = 0, I_ROW0, I_ROWS, I_LOAD, I_STORE, I_BOUND, I_BAD, I_COUNT };
+enum { I_SEGS = 0, I_CHUNKS, I_BAD, I_COUNT };
 
 // What follows the tiles.
 struct Rest {
@@ -109,57 +109,81 @@ constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 // TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
 constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
 
+constexpr int kMaxSegments = 128;  // of one range: ranges are at most this long when there are more sequences
+constexpr int kFromBounds = -2;
+
+struct Segment {
+    int row0, rows;   // rows <= 0: -rows rows get zeros and nothing else happens
+    int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before
+    int seq, first;   // first: holds the sequence's first row
+    int pad[2];
+};
+
+// Work: the chunks of the sequences in order (those of more than
+// max_recurrent rows), cut into ranges of equal counts; a CTA takes one range
+// of one kv head.  A range is a list of segments, each a run of one
+// sequence's chunks; only the first can continue a sequence that began in an
+// earlier range, and only the last can be continued.
 struct ChunkParams {
     LinearArgs A;
-    float* bounds;          // fp32 [max_bounds][Hkv][d][d]: states between a sequence's pieces
-    int32_t max_bounds;
-    int32_t piece;          // chunks per piece
-    int32_t total;          // pieces the host counted
+    float* bounds;          // fp32 [ranges - 1][Hkv][d][d]: the state at the end of each range
+    int4* tails;            // [ranges - 1]: what the scan needs of a range's last segment
+    Segment* segments;      // [ranges][Hkv][kMaxSegments]
+    int32_t ranges, range;  // ranges, and chunks of each
+    int32_t units;          // chunks the host counted
 };
 
-// Pieces of sequence s (0: the recurrent form takes it).
-__device__ __forceinline__ int pieces_of(const ChunkParams& P, int s) {
+// Chunks of sequence s (0: the recurrent form takes it).
+__device__ __forceinline__ int chunks_of(const ChunkParams& P, int s) {
     const int r0 = __ldg(P.A.query_start_loc + s), r1 = __ldg(P.A.query_start_loc + s + 1);
     if (r0 < 0 || r1 > P.A.num_tokens || r1 - r0 <= P.A.max_recurrent) return 0;
-    return ((r1 - r0 + C - 1) / C + P.piece - 1) / P.piece;
+    return (r1 - r0 + C - 1) / C;
 }
 
-struct PieceAt {
-    int seq, index, pieces;  // seq -1: none
-    int bound;               // boundaries of the sequences before
-    int total;               // entries of all sequences (only when `count`)
-};
-
-// Entry `at` of the pieces numbered over the sequences in order, the last
-// `skip` pieces of each left out.  One warp.
-__device__ __forceinline__ PieceAt find_piece(const ChunkParams& P, int at, int skip, bool count) {
+// One warp: calls f(sequence, its first unit, the unit behind its last) in
+// every lane whose sequence has units in [u0, u1), with the lanes' ballot;
+// returns the units seen (all of them when `count`).
+template <typename F>
+__device__ __forceinline__ int scan_units(const ChunkParams& P, int u0, int u1, bool count, F f) {
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x % 32;
-    PieceAt r = {-1, 0, 0, 0, 0};
-    int base = 0, bounds = 0;
-    for (int s0 = 0; s0 < P.A.num_seqs && (r.seq < 0 || count); s0 += 32) {
-        const int np = s0 + lane < P.A.num_seqs ? pieces_of(P, s0 + lane) : 0;
-        const int ne = max(np - skip, 0), nb = max(np - 1, 0);
-        int incl = ne, binc = nb;
+    int base = 0;
+    for (int s0 = 0; s0 < P.A.num_seqs && (base < u1 || count); s0 += 32) {
+        const int nc = s0 + lane < P.A.num_seqs ? chunks_of(P, s0 + lane) : 0;
+        int incl = nc;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(FULL, incl, o), u = __shfl_up_sync(FULL, binc, o);
-            if (lane >= o) incl += t, binc += u;
+            const int t = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl += t;
         }
-        const unsigned hit = r.seq < 0 ? __ballot_sync(FULL, base + incl > at) : 0u;
-        if (hit) {
-            const int j = __ffs(hit) - 1;
-            r.seq = s0 + j;
-            r.index = at - (base + __shfl_sync(FULL, incl - ne, j));
-            r.pieces = __shfl_sync(FULL, np, j);
-            r.bound = bounds + __shfl_sync(FULL, binc - nb, j);
-        }
+        const int first = base + incl - nc, end = base + incl;
+        const bool in = nc > 0 && first < u1 && end > u0;
+        f(s0 + lane, first, end, in, __ballot_sync(FULL, in));
         base += __shfl_sync(FULL, incl, 31);
-        bounds += __shfl_sync(FULL, binc, 31);
     }
-    r.total = base;
-    return r;
+    return base;
 }
+
+// Walks the chunks of a range in order.
+struct Cursor {
+    const Segment* seg;
+    int k, n;
+    int row, left;  // the chunk's first row, and rows left in its segment
+
+    __device__ __forceinline__ Cursor(const Segment* s, int count) : seg(s), k(-1), n(count), row(0), left(0) { open(); }
+    __device__ __forceinline__ void open() {
+        left = 0;
+        while (left <= 0 && ++k < n) {
+            row = seg[k].row0;
+            left = seg[k].rows;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        row += C;
+        left -= C;
+        if (left <= 0) open();
+    }
+};
 
 // Two fp32 values as three packed bf16 pairs that sum to them exactly: each
 // term is what is left, rounded to nearest.  The low half is widened by a
@@ -296,39 +320,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::sts128(smem_addr(smem + L::OFF_P) + i * 16, 0u, 0u, 0u, 0u);
     tc::fence_proxy_async_smem();
     griddep_wait();
+    Segment* segs = P.segments + (static_cast<int64_t>(blockIdx.x) * gridDim.y + h) * kMaxSegments;
     if (warp == 0) {
-        const bool last_entry = blockIdx.x == gridDim.x - 1;
-        const PieceAt at = find_piece(P, blockIdx.x, 0, last_entry && h == 0);
-        if (last_entry && h == 0 && at.total != P.total && lane == 0)
-            record_error(A.err, kErrRange, static_cast<uint32_t>(A.num_seqs));
-        int row0 = 0, rows = 0, load = -1, store = -1, bad = 0, bound = -1, last = 0;
-        if (at.seq >= 0) {
-            const LinearSeq q = linear_seq(A, at.seq, lane == 0 && h == 0 && at.index == 0);
-            const int skip = at.index * P.piece * C;
-            row0 = q.row0 + skip;
-            rows = min(q.rows - skip, P.piece * C);
-            last = at.index == at.pieces - 1;
-            bad = q.bad;
-            load = q.load;
-            store = last ? q.store : -1;
-            bound = at.index > 0 ? at.bound + at.index - 1 : -1;
-            if (bound >= P.max_bounds) {
-                if (lane == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(at.seq));
-                bad = 1;
+        const bool last = blockIdx.x == gridDim.x - 1 && h == 0;
+        const int u0 = blockIdx.x * P.range, u1 = u0 + P.range;
+        int nseg = 0, chunks = 0, any_bad = 0;
+        const int seen = scan_units(P, u0, u1, last, [&](int s, int first, int end, bool in, unsigned lanes) {
+            const int k = nseg + __popc(lanes & ((1u << lane) - 1));
+            int n = 0, bad = 0;
+            if (in && k < kMaxSegments) {
+                const LinearSeq q = linear_seq(A, s, h == 0 && first >= u0);
+                const int c0 = max(u0, first) - first, c1 = min(u1, end) - first;
+                Segment g;
+                g.row0 = q.row0 + c0 * C;
+                g.rows = min(q.rows, c1 * C) - c0 * C;
+                g.load = c0 > 0 ? kFromBounds : q.load;
+                g.store = end <= u1 ? q.store : -1;
+                g.seq = s;
+                g.first = c0 == 0;
+                bad = q.bad;
+                n = bad ? 0 : c1 - c0;
+                if (bad) g.rows = -g.rows;
+                segs[k] = g;
             }
-            if (h == 0 && at.index == 0 && !bad && q.store >= 0)
-                for (int o = lane; o < A.num_seqs; o += 32)
-                    if (o != at.seq && linear_shares(A, o, q.store))
-                        record_error(A.err, kErrAlias, static_cast<uint32_t>(at.seq));
+            nseg += __popc(lanes);
+            chunks += __reduce_add_sync(0xffffffffu, n);
+            any_bad |= __any_sync(0xffffffffu, bad);
+        });
+        if (last && seen != P.units && lane == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(A.num_seqs));
+        if (nseg > kMaxSegments) {
+            // device lengths that are not the host's: the rest is dropped
+            if (lane == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(A.num_seqs));
+            nseg = kMaxSegments;
         }
         if (lane == 0) {
-            info[I_SEQ] = at.seq;
-            info[I_ROW0] = row0;
-            info[I_ROWS] = rows;
-            info[I_LOAD] = load;
-            info[I_STORE] = store;
-            info[I_BOUND] = bound;
-            info[I_BAD] = bad;
+            info[I_SEGS] = nseg;
+            info[I_CHUNKS] = chunks;
+            info[I_BAD] = any_bad;
         }
     } else if (warp == kSWarp) {
         if (lane == 0) {
@@ -349,8 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const int row0 = info[I_ROW0], rows = info[I_ROWS], bad = info[I_BAD];
-    const int nch = bad ? 0 : (rows + C - 1) / C;
+    const int nseg = info[I_SEGS], nch = info[I_CHUNKS];
     const int nitems = nch * G;
     bool ok = true;
 
@@ -502,22 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + (static_cast<uint32_t>(32 * w) << 16) + COL_S + c0;
         const uint32_t tb = tmem + (static_cast<uint32_t>(32 * w) << 16) + COL_SB + c0 / 2;
         const int64_t head = static_cast<int64_t>(D) * D;
-        if (nch > 0 && live) {
-            const float* from = nullptr;
-            if (info[I_BOUND] >= 0)
-                from = P.bounds + (static_cast<int64_t>(info[I_BOUND]) * A.num_kv_heads + h) * head;
-            else if (info[I_LOAD] >= 0)
-                from = A.states + (static_cast<int64_t>(info[I_LOAD]) * A.num_kv_heads + h) * head;
-#pragma unroll 1
-            for (int b = 0; b < kCols / 32; ++b) {
-                uint32_t x[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    x[j] = from != nullptr ? __float_as_uint(from[(c0 + 32 * b + j) * D + dv]) : 0u;
-                tc::tmem_st32x32b_x32(ts + 32 * b, x);
-            }
-            tc::tmem_wait_st();
-        }
+        auto state_at = [&](int load) -> const float* {
+            if (load == kFromBounds)
+                return P.bounds + (static_cast<int64_t>(blockIdx.x - 1) * A.num_kv_heads + h) * head;
+            return load >= 0 ? A.states + (static_cast<int64_t>(load) * A.num_kv_heads + h) * head : nullptr;
+        };
         auto split = [&](uint32_t (&x)[16], int b, float2 lam) {
             uint32_t hi[8], mid[8], lo[8];
 #pragma unroll
@@ -533,40 +549,61 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_st32x32b_x8(tb + D + 8 * b, lo);
             tc::tmem_st32x32b_x16(ts + 16 * b, x);
         };
-        for (int i = 0; i < nch && ok; ++i) {
-            // S may be read when the last chunk's update is in it, its terms
-            // replaced when the last outputs have read them.
+        int i = 0;  // chunk of the range
+        for (int k = 0; k < nseg && ok; ++k) {
+            const int rows = segs[k].rows, store = segs[k].store;
+            if (rows <= 0) continue;
+            // The last segment's update has to be in before S is replaced.
             if (i > 0 && !warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t xa[16], xb[16];
-            if (live) tc::tmem_ld32x32b_x16(ts, xa);
-            if (i > 0 && !warp_wait(&bar[B_SFREE], (i - 1) & 1)) { ok = false; break; }
-            tc::fence_after_sync();
-            // a tail's factor is applied once: fp32 is enough
-            const int nrows = min(C, rows - i * C);
-            const float2 lam = nrows == C ? make_float2(tab[TAB_LAM], tab[TAB_LAM + 1]) : make_float2(tab[TAB_V + nrows], 0.f);
+            const float* from = state_at(segs[k].load);
             if (live) {
 #pragma unroll 1
-                for (int b = 0; b < kBatches; b += 2) {
-                    tc::tmem_wait_ld();
-                    tc::tmem_ld32x32b_x16(ts + 16 * b + 16, xb);
-                    split(xa, b, lam);
-                    tc::tmem_wait_ld();
-                    if (b + 2 < kBatches) tc::tmem_ld32x32b_x16(ts + 16 * b + 32, xa);
-                    split(xb, b + 1, lam);
+                for (int b = 0; b < kCols / 32; ++b) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        x[j] = from != nullptr ? __float_as_uint(from[(c0 + 32 * b + j) * D + dv]) : 0u;
+                    tc::tmem_st32x32b_x32(ts + 32 * b, x);
                 }
                 tc::tmem_wait_st();
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_S]);
-        }
-        if (ok && nch > 0 && info[I_STORE] >= 0 && live) {
-            if (!warp_wait(&bar[B_VTFREE], (nch - 1) & 1)) {
-                ok = false;
-            } else {
+            if (k + 1 < nseg && segs[k + 1].rows > 0 && segs[k + 1].load >= 0) {
+                const float* next = state_at(segs[k + 1].load);
+                for (int j = threadIdx.x - 32 * kSWarp; j < D * D / 32; j += 32 * kSWarps) prefetch_l2(next + 32 * j);
+            }
+            for (int left = rows; left > 0; left -= C, ++i) {
+                // S may be read when the last chunk's update is in it, its
+                // terms replaced when the last outputs have read them.
+                if (i > 0 && !warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
                 tc::fence_after_sync();
-                float* to = A.states + (static_cast<int64_t>(info[I_STORE]) * A.num_kv_heads + h) * head + dv;
+                uint32_t xa[16], xb[16];
+                if (live) tc::tmem_ld32x32b_x16(ts, xa);
+                if (i > 0 && !warp_wait(&bar[B_SFREE], (i - 1) & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                // a tail's factor is applied once: fp32 is enough
+                const float2 lam = left >= C ? make_float2(tab[TAB_LAM], tab[TAB_LAM + 1]) : make_float2(tab[TAB_V + left], 0.f);
+                if (live) {
+#pragma unroll 1
+                    for (int b = 0; b < kBatches; b += 2) {
+                        tc::tmem_wait_ld();
+                        tc::tmem_ld32x32b_x16(ts + 16 * b + 16, xb);
+                        split(xa, b, lam);
+                        tc::tmem_wait_ld();
+                        if (b + 2 < kBatches) tc::tmem_ld32x32b_x16(ts + 16 * b + 32, xa);
+                        split(xb, b + 1, lam);
+                    }
+                    tc::tmem_wait_st();
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[B_S]);
+            }
+            if (!ok || store < 0) continue;
+            if (!warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            if (live) {
+                float* to = A.states + (static_cast<int64_t>(store) * A.num_kv_heads + h) * head + dv;
 #pragma unroll 1
                 for (int b = 0; b < kCols / 32; ++b) {
                     uint32_t x[32];
@@ -582,48 +619,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The load warp converts its share too.  The loads that follow chunk
         // i's conversion wait for items that end before the next conversion
         // could start, so neither holds the other up.
-        auto load_kv = [&](int i) -> bool {
-            if (i >= nch) return true;
-            const int st = i % kKv;
-            if (!warp_wait(&bar[B_KVEMPTY + st], ((i / kKv) & 1) ^ 1)) return false;
+        Cursor kv_at(segs, nseg), q_at(segs, nseg), at(segs, nseg);
+        int kv_next = 0, q_next = 0;
+        auto load_kv = [&]() -> bool {
+            if (kv_next >= nch) return true;
+            const int st = kv_next % kKv;
+            if (!warp_wait(&bar[B_KVEMPTY + st], ((kv_next / kKv) & 1) ^ 1)) return false;
             if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[B_KVFULL + st], 2u * kPanels * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn) {
-                    tc::tma_load_3d(smem + L::OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
+                    tc::tma_load_3d(smem + L::OFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, kv_at.row,
                                     &bar[B_KVFULL + st]);
-                    tc::tma_load_3d(smem + L::OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
+                    tc::tma_load_3d(smem + L::OFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, kv_at.row,
                                     &bar[B_KVFULL + st]);
                 }
             }
             __syncwarp();
+            ++kv_next;
+            kv_at.next();
             return true;
         };
-        auto load_q = [&](int n) -> bool {
-            if (n >= nitems) return true;
-            const int st = n % kQ;
-            if (!warp_wait(&bar[B_QEMPTY + st], ((n / kQ) & 1) ^ 1)) return false;
+        auto load_q = [&]() -> bool {
+            if (q_next >= nitems) return true;
+            const int st = q_next % kQ;
+            if (!warp_wait(&bar[B_QEMPTY + st], ((q_next / kQ) & 1) ^ 1)) return false;
             if (tc::elect_one()) {
                 mbar_arrive_expect_tx(&bar[B_QFULL + st], static_cast<uint32_t>(kPanels) * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn)
-                    tc::tma_load_3d(smem + L::OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + n % G,
-                                    row0 + n / G * C, &bar[B_QFULL + st]);
+                    tc::tma_load_3d(smem + L::OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + q_next % G,
+                                    q_at.row, &bar[B_QFULL + st]);
             }
             __syncwarp();
+            ++q_next;
+            if (q_next % G == 0) q_at.next();
             return true;
         };
         if (warp == kLoadWarp) {
-            ok = load_kv(0);
-            for (int n = 0; n < kQ && ok; ++n) ok = load_q(n);
-            for (int i = 1; i < kKv - 1 && ok; ++i) ok = load_kv(i);
+            ok = load_kv();
+            for (int n = 0; n < kQ && ok; ++n) ok = load_q();
+            for (int i = 1; i < kKv - 1 && ok; ++i) ok = load_kv();
         }
         const int tid = 32 * (warp == kLoadWarp ? 0 : warp - 4) + lane;
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kKv;
             if (!warp_wait(&bar[B_KVFULL + st], (i / kKv) & 1)) { ok = false; break; }
             if (!warp_wait(&bar[B_VTFREE], (i & 1) ^ 1)) { ok = false; break; }
-            const int nrows = min(C, rows - i * C);
+            const int nrows = min(C, at.left);
+            at.next();
             const uint32_t sk = smem_addr(smem + L::OFF_K + st * kTile), sv = smem_addr(smem + L::OFF_V + st * kTile);
             const float acc = convert_v<D, kTile, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + L::OFF_VT), tab + TAB_V,
                                                                      1.f, nrows, tid);
@@ -652,13 +696,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_VT]);
             if (warp == kLoadWarp) {
-                for (int n = (i - 1) * G + kQ; n < i * G + kQ && ok; ++n)
-                    if (n >= kQ) ok = load_q(n);
-                ok = ok && load_kv(i + kKv - 1);
+                while (q_next < i * G + kQ && q_next < nitems && ok) ok = load_q();
+                ok = ok && load_kv();
             }
         }
         if (warp == kLoadWarp)
-            for (int n = (nch - 1) * G + kQ; n < nitems && ok; ++n) ok = load_q(n);
+            while (q_next < nitems && ok) ok = load_q();
     } else {
         // ------------------------------------------------------ outputs
         // Lane = v index, column = token: a warp stores 32 consecutive floats
@@ -671,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t row_step = static_cast<int64_t>(A.num_q_heads) * D;
         const float* f = tab + TAB_O + t0;
         const int64_t row_bytes = row_step * 4;
+        Cursor at(segs, nseg);
         for (int n = 0; n < nitems && ok; ++n) {
             const int i = n / G, g = n % G;
             if (!warp_wait(&bar[B_OS], n & 1)) { ok = false; break; }
@@ -694,10 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_OPFREE]);
             if (live) {
-                const int nrows = min(C, rows - i * C) - t0;
+                const int nrows = min(C, at.left) - t0;
                 const int mark = rest.bad_rows[i % kBadBuffers][dv];
                 const int nan_from = ((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0;
-                float* o = A.out + (static_cast<int64_t>(row0) + i * C + t0) * row_step + (h * G + g) * D + dv;
+                float* o = A.out + (static_cast<int64_t>(at.row) + t0) * row_step + (h * G + g) * D + dv;
                 if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
@@ -714,11 +758,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            if (g == G - 1) at.next();
         }
     }
-    if (bad && rows > 0) {
-        for (int64_t i = threadIdx.x; i < static_cast<int64_t>(rows) * G * D; i += kThreads)
-            A.out[(row0 + i / (G * D)) * static_cast<int64_t>(A.num_q_heads) * D + h * G * D + i % (G * D)] = 0.f;
+    if (info[I_BAD]) {
+        for (int k = 0; k < nseg; ++k) {
+            const int64_t n = -static_cast<int64_t>(segs[k].rows) * G * D;  // negative for the others
+            for (int64_t i = threadIdx.x; i < n; i += kThreads)
+                A.out[(segs[k].row0 + i / (G * D)) * static_cast<int64_t>(A.num_q_heads) * D + h * G * D +
+                      i % (G * D)] = 0.f;
+        }
+    }
+    if (h == 0) {
+        // A slot that two sequences store to, or that one stores to and
+        // another reads, has no defined content: reported.
+        for (int k = 0; k < nseg; ++k) {
+            if (segs[k].rows <= 0 || !segs[k].first) continue;
+            const int to = __ldg(A.new_slots + segs[k].seq);
+            if (to < 0) continue;
+            for (int o = threadIdx.x; o < A.num_seqs; o += kThreads)
+                if (o != segs[k].seq && linear_shares(A, o, to))
+                    record_error(A.err, kErrAlias, static_cast<uint32_t>(segs[k].seq));
+        }
     }
     if (!ok) record_error(A.err, kErrTimeout, 0x200u + static_cast<uint32_t>(warp));
     // ---------------------------------------------------------- teardown
@@ -728,8 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// ---------------------------------------------------------------- pieces' own states
-// A piece's own state from zero: sum_s lam^(end-1-s) k_s v_s^T over all its
+// ---------------------------------------------------------------- ranges' own states
+// The own state, from zero, of a range's last segment, where its sequence
+// goes on in the next range: sum_s lam^(end-1-s) k_s v_s^T over the segment's
 // tokens, one accumulation with no rescaling (the factor of a chunk's end is
 // part of V~).  Warps 0-7 V~, 8 loads, 9 MMA; warps 0-3 store the sum.
 constexpr int kStateThreads = 320;
@@ -776,20 +838,22 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     }
     griddep_wait();
     if (warp == 0) {
-        const PieceAt at = find_piece(P, blockIdx.x, 1, false);
-        int row0 = 0, rows = 0, bound = 0;
-        if (at.seq >= 0) {
-            const LinearSeq q = linear_seq(A, at.seq, false);
-            row0 = q.row0 + at.index * P.piece * C;
-            rows = q.bad ? 0 : P.piece * C;
-            bound = at.bound + at.index;
-            if (bound >= P.max_bounds) rows = 0;
-        }
+        const int u0 = blockIdx.x * P.range, u1 = u0 + P.range;
         if (lane == 0) {
-            info[0] = row0;
-            info[1] = rows;
-            info[2] = bound;
+            info[0] = info[1] = 0;
+            if (h == 0) P.tails[blockIdx.x] = make_int4(0, 0, 0, -1);
         }
+        __syncwarp();
+        scan_units(P, u1 - 1, u1, false, [&](int s, int first, int end, bool in, unsigned) {
+            if (!in || end <= u1) return;
+            const LinearSeq q = linear_seq(A, s, false);
+            const int c0 = max(u0, first) - first, c1 = u1 - first;
+            if (q.bad) return;
+            info[0] = q.row0 + c0 * C;
+            info[1] = c1 - c0;
+            // chunks, whether it holds the sequence's first row, and the state that goes before it
+            if (h == 0) P.tails[blockIdx.x] = make_int4(c1 - c0, c0 == 0, 0, q.load);
+        });
     }
     const float g = clean_log_decay(A, h, false);
     if (threadIdx.x < C) tab[threadIdx.x] = expf(g * static_cast<float>(threadIdx.x));
@@ -797,7 +861,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const int row0 = info[0], nch = info[1] / C;
+    const int row0 = info[0], nch = info[1];
     bool ok = true;
     if (warp == 8) {
         for (int i = 0; i < nch && ok; ++i) {
@@ -846,7 +910,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 ok = false;
             } else {
                 tc::fence_after_sync();
-                float* to = P.bounds + (static_cast<int64_t>(info[2]) * A.num_kv_heads + h) * D * D + 32 * warp + lane;
+                float* to = P.bounds + (static_cast<int64_t>(blockIdx.x) * A.num_kv_heads + h) * D * D + 32 * warp + lane;
 #pragma unroll
                 for (int b = 0; b < D / 32; ++b) {
                     uint32_t x[32];
@@ -865,49 +929,42 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     if (warp == 8) tc::tmem_dealloc(tmem, 128);
 }
 
-// The states before each piece but the first, from the pieces' own:
-// bounds[j] <- lam^(piece tokens) (state before) + bounds[j], in order.
-// Grid (sequences * d^2 / 1024, Hkv); a thread carries four elements.
+// The states at the ends of the ranges, from the ranges' own: bounds[x] <-
+// lam^(tokens of the segment) (state before it) + bounds[x], in order, the
+// state before being the sequence's where the segment begins it and
+// bounds[x - 1] otherwise.  Grid (d^2 / 512, Hkv); a thread carries two
+// elements.
 __global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkParams P) {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ int info[3];
     __shared__ float2 lam_s;
     const LinearArgs& A = P.A;
-    const int slices = A.head_dim * A.head_dim / 1024;
-    const int h = blockIdx.y, s = blockIdx.x / slices;
-    if (threadIdx.x < 32) {
-        int base = 0;
-        for (int o = threadIdx.x; o < s; o += 32) base += max(pieces_of(P, o) - 1, 0);
-        base = __reduce_add_sync(0xffffffffu, base);
-        if (threadIdx.x == 0) {
-            const LinearSeq q = linear_seq(A, s, false);
-            info[0] = base;
-            info[1] = q.bad ? 0 : pieces_of(P, s) - 1;
-            info[2] = q.load;
-        }
-    } else if (threadIdx.x == 32) {
-        lam_s = decay_pair(clean_log_decay(A, h, false), P.piece * C);
-    }
-    __syncthreads();
-    const int base = info[0], n = min(info[1], P.max_bounds - info[0]);
-    if (n <= 0) return;
-    const float2 lam = lam_s;
+    const int h = blockIdx.y;
+    const float g = clean_log_decay(A, h, false);
+    if (threadIdx.x == 0) lam_s = decay_pair(g, P.range * C);
     const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
-    const int64_t e = (blockIdx.x % slices * 256 + threadIdx.x) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (info[2] >= 0)
-        x = *reinterpret_cast<const float4*>(A.states + (static_cast<int64_t>(info[2]) * A.num_kv_heads + h) * head + e);
-    float* p = P.bounds + (static_cast<int64_t>(base) * A.num_kv_heads + h) * head + e;
+    const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 2;
+    float* p = P.bounds + h * head + e;
     const int64_t step = static_cast<int64_t>(A.num_kv_heads) * head;
+    __syncthreads();
+    const float2 lam = lam_s;
+    float2 x = make_float2(0.f, 0.f);
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-        const float4 y = *reinterpret_cast<const float4*>(p + j * step);
-        x.x = fmaf(x.x, lam.x, fmaf(x.x, lam.y, y.x));
-        x.y = fmaf(x.y, lam.x, fmaf(x.y, lam.y, y.y));
-        x.z = fmaf(x.z, lam.x, fmaf(x.z, lam.y, y.z));
-        x.w = fmaf(x.w, lam.x, fmaf(x.w, lam.y, y.w));
-        *reinterpret_cast<float4*>(p + j * step) = x;
+    for (int r = 0; r < P.ranges - 1; ++r) {
+        const int4 tail = P.tails[r];
+        const float2 y = *reinterpret_cast<const float2*>(p + r * step);
+        if (tail.x <= 0) continue;
+        float2 f = lam;
+        if (tail.y) {
+            // a sequence's first segment: its length is its own, its factor applied once
+            f = make_float2(expf(g * static_cast<float>(tail.x * C)), 0.f);
+            x = make_float2(0.f, 0.f);
+            if (tail.w >= 0)
+                x = *reinterpret_cast<const float2*>(A.states + (static_cast<int64_t>(tail.w) * A.num_kv_heads + h) * head + e);
+        }
+        x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y.x));
+        x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y.y));
+        *reinterpret_cast<float2*>(p + r * step) = x;
     }
 }
 
@@ -935,22 +992,21 @@ cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     static bool done[64] = {};
     cudaError_t e = configure(linear_chunk_kernel<D, G>, smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.total, P.A.num_kv_heads), dim3(kThreads),
+    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.ranges, P.A.num_kv_heads), dim3(kThreads),
                              smem_bytes<D>(), stream, tq, tk, tv, P);
 }
 
 template <int D>
 cudaError_t launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
-                       int32_t bounds, cudaStream_t stream) {
-    if (bounds > 0) {
+                       bool cut, cudaStream_t stream) {
+    if (cut) {
         static bool done[64] = {};
         cudaError_t e = configure(linear_state_kernel<D>, STATE_SMEM, done);
         if (e != cudaSuccess) return e;
-        e = launch_overlapped(linear_state_kernel<D>, dim3(bounds, P.A.num_kv_heads), dim3(kStateThreads), STATE_SMEM,
-                              stream, tk, tv, P);
+        e = launch_overlapped(linear_state_kernel<D>, dim3(P.ranges - 1, P.A.num_kv_heads), dim3(kStateThreads),
+                              STATE_SMEM, stream, tk, tv, P);
         if (e != cudaSuccess) return e;
-        e = launch_overlapped(linear_scan_kernel, dim3(P.A.num_seqs * (D * D / 1024), P.A.num_kv_heads), dim3(256), 0,
-                              stream, P);
+        e = launch_overlapped(linear_scan_kernel, dim3(D * D / 512, P.A.num_kv_heads), dim3(256), 0, stream, P);
         if (e != cudaSuccess) return e;
     }
     switch (P.A.num_q_heads / P.A.num_kv_heads) {
@@ -963,75 +1019,93 @@ cudaError_t launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
 
 }  // namespace
 
-int32_t linear_max_bounds(int32_t num_tokens, int32_t num_kv_heads, int num_sms) {
-    const int32_t fill = (2 * num_sms + num_kv_heads - 1) / num_kv_heads;
-    return num_tokens / C < fill ? num_tokens / C : fill;
+// Ranges a plan may have: two waves of CTAs, or what keeps every range within
+// the segments a CTA lists.
+static int64_t max_ranges(int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int num_sms) {
+    const int64_t waves = (2 * static_cast<int64_t>(num_sms) + num_kv_heads - 1) / num_kv_heads;
+    const int64_t units = num_tokens / C + num_seqs;
+    const int64_t lists = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 0;
+    return waves > lists ? waves : lists;
+}
+
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                              int num_sms) {
+    const size_t n = static_cast<size_t>(max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms));
+    return n * num_kv_heads * (static_cast<size_t>(head_dim) * head_dim * sizeof(float) + kMaxSegments * sizeof(Segment)) +
+           round256(n * sizeof(int4));
 }
 
 LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t group,
-                       int num_sms, int32_t max_recurrent) {
-    LinearPlan best = {0, 1, 0, 0, linear_max_bounds(num_tokens, num_kv_heads, num_sms)};
-    int64_t chunks = 0, longest = 0;
+                       int32_t head_dim, int num_sms, int32_t max_recurrent) {
+    LinearPlan best = {0, 0, 0, 0, false};
+    int64_t units = 0;
     for (int32_t s = 0; s < num_seqs; ++s) {
         const int32_t rows = qsl[s + 1] - qsl[s];
         if (rows > 0 && rows <= max_recurrent) ++best.recurrent;
-        if (rows <= max_recurrent) continue;
-        const int64_t n = (rows + C - 1) / C;
-        chunks += n;
-        longest = n > longest ? n : longest;
+        if (rows > max_recurrent) units += (rows + C - 1) / C;
     }
-    if (longest == 0) return best;
-    // Microseconds of a chunk and of a launch in the main and in the state
-    // kernel.  Cutting pays when one piece per (sequence, head) would leave
-    // most SMs idle; it costs the state kernel's pass over K and V.
-    const double chunk = 1.0 + 0.9 * group, state = 0.7, start = 5.0, join = 7.0;
-    auto span = [&](int64_t ctas, int64_t piece, int64_t work, double c) {
-        if (ctas <= num_sms) return piece * c;
-        const double even = static_cast<double>(work) * num_kv_heads * c / num_sms + 0.5 * piece * c;
-        return even > piece * c ? even : piece * c;
-    };
+    if (units == 0) return best;
+    best.units = static_cast<int32_t>(units);
+    const int64_t most = max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms);
+    // Microseconds of a chunk in the main and in the state kernel, and of a
+    // kernel's start and end.  More ranges fill more SMs; where they cut
+    // sequences, the state kernel reads K and V of all but the last range once
+    // more, and the states are carried over.
+    const double chunk = (head_dim == 64 ? 0.5 : 1.2) + (head_dim == 64 ? 1.2 : 1.6) * group;
+    const double state = head_dim == 64 ? 0.6 : 1.0, start = 6.0, join = 12.0;
     double best_us = 1e30;
-    int64_t last = 0;
-    for (int32_t cuts : {1, 2, 3, 4, 5, 6, 8, 9, 10, 12, 14, 16, 19, 24, 32, 38, 50, 64, 76, 100, 152}) {
-        const int64_t piece = (longest + cuts - 1) / cuts;
-        if (piece == last) continue;
-        last = piece;
-        int64_t pieces = 0, seqs = 0;
-        for (int32_t s = 0; s < num_seqs; ++s) {
+    for (int64_t n = 1; n <= most && n <= units; ++n) {
+        const int64_t range = (units + n - 1) / n;
+        if ((units + range - 1) / range != n) continue;  // the same ranges as a smaller n
+        if (num_seqs > kMaxSegments && range > kMaxSegments) continue;
+        const int64_t waves = (n * num_kv_heads + num_sms - 1) / num_sms;
+        double us = waves * (start + range * chunk);
+        if (us >= best_us) continue;
+        bool cut = false;
+        int64_t end = 0;  // whether a border lies inside a sequence
+        for (int32_t s = 0; s < num_seqs && !cut && n > 1; ++s) {
             const int32_t rows = qsl[s + 1] - qsl[s];
             if (rows <= max_recurrent) continue;
-            pieces += ((rows + C - 1) / C + piece - 1) / piece;
-            ++seqs;
+            const int64_t first = end;
+            end += (rows + C - 1) / C;
+            const int64_t border = (first / range + 1) * range;
+            cut = border < end;
         }
-        const int64_t bounds = pieces - seqs;
-        if (bounds > best.max_bounds) break;
-        double us = start + span(pieces * num_kv_heads, piece, chunks, chunk);
-        if (bounds > 0) us += join + span(bounds * num_kv_heads, piece, bounds * piece, state);
+        if (cut) us += join + ((n - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
         if (us < best_us) {
             best_us = us;
-            best.piece_chunks = static_cast<int32_t>(piece);
-            best.pieces = static_cast<int32_t>(pieces);
-            best.bounds = static_cast<int32_t>(bounds);
+            best.ranges = static_cast<int32_t>(n);
+            best.range = static_cast<int32_t>(range);
+            best.cut = cut;
         }
     }
     return best;
 }
 
-cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, cudaStream_t stream) {
-    if (plan.pieces == 0) return cudaSuccess;
+cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, int num_sms,
+                                 cudaStream_t stream) {
+    if (plan.units == 0) return cudaSuccess;
     CUtensorMap tq, tk, tv;
     if (!rows_map(&tq, a.q, a.q_stride, a.num_q_heads, a.head_dim, a.num_tokens) ||
         !rows_map(&tk, a.k, a.k_stride, a.num_kv_heads, a.head_dim, a.num_tokens) ||
         !rows_map(&tv, a.v, a.v_stride, a.num_kv_heads, a.head_dim, a.num_tokens))
         return cudaErrorInvalidValue;
+    const size_t n = static_cast<size_t>(max_ranges(a.num_seqs, a.num_tokens, a.num_kv_heads, num_sms));
     ChunkParams P;
     P.A = a;
-    P.bounds = static_cast<float*>(workspace);
-    P.max_bounds = plan.max_bounds;
-    P.piece = plan.piece_chunks;
-    P.total = plan.pieces;
-    return a.head_dim == 64 ? launch_all<64>(tq, tk, tv, P, plan.bounds, stream)
-                            : launch_all<128>(tq, tk, tv, P, plan.bounds, stream);
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    P.tails = reinterpret_cast<int4*>(at);
+    at += round256(n * sizeof(int4));
+    P.bounds = reinterpret_cast<float*>(at);
+    at += n * a.num_kv_heads * static_cast<size_t>(a.head_dim) * a.head_dim * sizeof(float);
+    P.segments = reinterpret_cast<Segment*>(at);
+    P.ranges = plan.ranges;
+    P.range = plan.range;
+    P.units = plan.units;
+    return a.head_dim == 64 ? launch_all<64>(tq, tk, tv, P, plan.cut, stream)
+                            : launch_all<128>(tq, tk, tv, P, plan.cut, stream);
 }
 
 }  // namespace pkv

@@ -181,22 +181,22 @@ struct LinearArgs {
 
 cudaError_t launch_linear_recurrent(const LinearArgs& a, cudaStream_t stream);
 
-// How the chunked form cuts a batch: sequences of more than max_recurrent
-// rows go in pieces of piece_chunks chunks of 64 tokens.
+// How the chunked form cuts a batch: the chunks (64 tokens) of the sequences
+// of more than max_recurrent rows, in order, in `ranges` ranges of `range`.
 struct LinearPlan {
-    int32_t recurrent;     // sequences the recurrent form takes
-    int32_t piece_chunks;
-    int32_t pieces;        // of all sequences
-    int32_t bounds;        // states between pieces (pieces less the sequences they belong to)
-    int32_t max_bounds;    // states the workspace holds
+    int32_t recurrent;   // sequences the recurrent form takes
+    int32_t units;       // chunks of the others
+    int32_t ranges, range;
+    bool cut;            // a border lies inside a sequence
 };
 
-// States the workspace of a batch holds, whatever its lengths.
-int32_t linear_max_bounds(int32_t num_tokens, int32_t num_kv_heads, int num_sms);
+size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                              int num_sms);
 LinearPlan plan_linear(const int32_t* query_start_loc_host, int32_t num_seqs, int32_t num_tokens,
-                       int32_t num_kv_heads, int32_t group, int num_sms, int32_t max_recurrent);
+                       int32_t num_kv_heads, int32_t group, int32_t head_dim, int num_sms, int32_t max_recurrent);
 
-cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, cudaStream_t stream);
+cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, int num_sms,
+                                 cudaStream_t stream);
 
 // Block bookkeeping state (pkv_blocks_t), all device memory.
 struct BlocksArgs {
