@@ -85,7 +85,7 @@ enum { I_SEGS = 0, I_CHUNKS, I_BAD, I_COUNT };
 
 // What follows the tiles.
 struct Rest {
-    float tab[258];
+    alignas(16) float tab[260];
     int bad_rows[kBadBuffers][128];  // see where V~ is made
     uint64_t bar[NBAR];
     int info[I_COUNT];
@@ -481,19 +481,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t prow = smem_addr(smem + L::OFF_P) + s * 128;
         const float* f = tab + TAB_P + 63 - s + begin;
         // Rows 32-63 keep the zeros of tokens 0-31 that the set-up wrote.
-        auto convert = [&](const uint32_t (&x)[32], uint32_t at, int first) {
+        auto convert = [&](uint32_t (&x)[32], uint32_t at, int first) {
+            // factors first: they cannot be loaded past the stores
+#pragma unroll
+            for (int t = 0; t < 32; t += 2) {
+                float2 y = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])),
+                                      make_float2(f[t], f[t + 1]));
+                // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
+                if (t < first) y.x = 0.f;
+                if (t + 1 < first) y.y = 0.f;
+                x[t] = __float_as_uint(y.x);
+                x[t + 1] = __float_as_uint(y.y);
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int t = 8 * c + 2 * j;
-                    float2 y = __fmul2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])),
-                                          make_float2(f[t], f[t + 1]));
-                    // a masked score may be NaN (another sequence's key): selected away, not multiplied by 0
-                    if (t < first) y.x = 0.f;
-                    if (t + 1 < first) y.y = 0.f;
-                    split3(y, hi[j], mid[j], lo[j]);
+                    split3(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])), hi[j], mid[j], lo[j]);
                 }
                 const uint32_t a = at + (((begin / 8 + c) ^ (s & 7)) << 4);
                 tc::sts128(a, hi[0], hi[1], hi[2], hi[3]);
@@ -668,6 +674,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(&bar[B_VTFREE], (i & 1) ^ 1)) { ok = false; break; }
             const int nrows = min(C, at.left);
             at.next();
+            // Chunk i - 1's update has read its first item's q by now.
+            if (warp == kLoadWarp && i > 0)
+                while (q_next <= (i - 1) * G + kQ && q_next < nitems && ok) ok = load_q();
             const uint32_t sk = smem_addr(smem + L::OFF_K + st * kTile), sv = smem_addr(smem + L::OFF_V + st * kTile);
             const float acc = convert_v<D, kTile, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + L::OFF_VT), tab + TAB_V,
                                                                      1.f, nrows, tid);
@@ -727,6 +736,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_OSFREE]);
+            // the factors here, not among the stores, which they could not be loaded past
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 ff = *reinterpret_cast<const float4*>(f + j);
+                xs[j] = __float_as_uint(ff.x * __uint_as_float(xs[j]));
+                xs[j + 1] = __float_as_uint(ff.y * __uint_as_float(xs[j + 1]));
+                xs[j + 2] = __float_as_uint(ff.z * __uint_as_float(xs[j + 2]));
+                xs[j + 3] = __float_as_uint(ff.w * __uint_as_float(xs[j + 3]));
+            }
             if (!warp_wait(&bar[B_OP], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
             uint32_t xp[32];
@@ -745,13 +763,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        *o = fmaf(f[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                        *o = __uint_as_float(xs[j]) + __uint_as_float(xp[j]);
                         o = walk(o, row_bytes);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float y = fmaf(f[j], __uint_as_float(xs[j]), __uint_as_float(xp[j]));
+                        float y = __uint_as_float(xs[j]) + __uint_as_float(xp[j]);
                         if (j >= nan_from) y = __int_as_float(0x7fffffff);
                         if (j < nrows) *o = y;
                         o = walk(o, row_bytes);
@@ -949,22 +967,40 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkParams P) {
     __syncthreads();
     const float2 lam = lam_s;
     float2 x = make_float2(0.f, 0.f);
-#pragma unroll 4
-    for (int r = 0; r < P.ranges - 1; ++r) {
-        const int4 tail = P.tails[r];
-        const float2 y = *reinterpret_cast<const float2*>(p + r * step);
-        if (tail.x <= 0) continue;
-        float2 f = lam;
-        if (tail.y) {
-            // a sequence's first segment: its length is its own, its factor applied once
-            f = make_float2(expf(g * static_cast<float>(tail.x * C)), 0.f);
-            x = make_float2(0.f, 0.f);
-            if (tail.w >= 0)
-                x = *reinterpret_cast<const float2*>(A.states + (static_cast<int64_t>(tail.w) * A.num_kv_heads + h) * head + e);
+    // Loads of several ranges together: they hang on nothing but the list.
+    constexpr int kBatch = 8;
+    for (int r0 = 0; r0 < P.ranges - 1; r0 += kBatch) {
+        int4 tail[kBatch];
+        float2 y[kBatch], before[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            tail[j] = make_int4(0, 0, 0, -1);
+            y[j] = make_float2(0.f, 0.f);
+            if (r0 + j < P.ranges - 1) {
+                tail[j] = P.tails[r0 + j];
+                y[j] = *reinterpret_cast<const float2*>(p + (r0 + j) * step);
+            }
         }
-        x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y.x));
-        x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y.y));
-        *reinterpret_cast<float2*>(p + r * step) = x;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            before[j] = make_float2(0.f, 0.f);
+            if (tail[j].x > 0 && tail[j].y && tail[j].w >= 0)
+                before[j] = *reinterpret_cast<const float2*>(
+                    A.states + (static_cast<int64_t>(tail[j].w) * A.num_kv_heads + h) * head + e);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (tail[j].x <= 0) continue;
+            float2 f = lam;
+            if (tail[j].y) {
+                // a sequence's first segment: its length is its own, its factor applied once
+                f = make_float2(expf(g * static_cast<float>(tail[j].x * C)), 0.f);
+                x = before[j];
+            }
+            x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y[j].x));
+            x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y[j].y));
+            *reinterpret_cast<float2*>(p + (r0 + j) * step) = x;
+        }
     }
 }
 
