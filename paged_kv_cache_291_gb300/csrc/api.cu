@@ -880,7 +880,7 @@ PKV_API pkv_status pkv_linear_decode_attention(const pkv_states_t* states, const
     if ((st = fill_linear(states, q, q_stride, num_q_heads, k, k_stride, v, v_stride, state_slots, new_slots,
                           context_lens, num_seqs, num_seqs, scale, out, &a, &dev)) != PKV_OK)
         return st;
-    cudaError_t e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
+    cudaError_t e = pkv::launch_linear_recurrent(a, 1, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
@@ -890,7 +890,7 @@ PKV_API size_t pkv_linear_prefill_workspace_size(int32_t num_seqs, int32_t num_t
     if (head_dim != 64 && head_dim != 128) return 0;
     DeviceState* dev = nullptr;
     if (current_device(&dev) != PKV_OK) return 0;
-    return pkv::linear_workspace_bytes(num_seqs, num_tokens, num_kv_heads, head_dim, dev->num_sms);
+    return pkv::linear_workspace_bytes(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim, dev->num_sms);
 }
 
 PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
@@ -916,7 +916,7 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
                           context_lens, num_seqs, num_tokens, scale, out, &a, &dev)) != PKV_OK)
         return st;
     if (workspace_bytes <
-        pkv::linear_workspace_bytes(num_seqs, num_tokens, a.num_kv_heads, a.head_dim, dev->num_sms))
+        pkv::linear_workspace_bytes(num_seqs, num_tokens, num_q_heads, a.num_kv_heads, a.head_dim, dev->num_sms))
         return PKV_ERR_WORKSPACE;
     a.query_start_loc = query_start_loc;
     a.max_recurrent = 16;
@@ -924,7 +924,7 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
                                                   num_q_heads / a.num_kv_heads, a.head_dim, dev->num_sms,
                                                   a.max_recurrent);
     cudaError_t e = cudaSuccess;
-    if (plan.recurrent > 0) e = pkv::launch_linear_recurrent(a, static_cast<cudaStream_t>(stream));
+    if (plan.recurrent > 0) e = pkv::launch_linear_recurrent(a, plan.recurrent, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = pkv::launch_linear_chunks(a, plan, workspace, dev->num_sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }

@@ -30,7 +30,7 @@ constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t u) { return __uint_as_float(static_cast<uint32_t>(u) << 16); }
 
-// TT: tokens staged at a time (1 for the decode call).
+// TT: tokens staged at a time.
 template <int D, int G, int TT>
 __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const LinearArgs A) {
     constexpr int RPT = D / kRowLanes;          // rows of S per thread
@@ -144,27 +144,27 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
 }
 
 template <int D, int G>
-cudaError_t launch(const LinearArgs& a, cudaStream_t stream) {
+cudaError_t launch(const LinearArgs& a, int32_t longest, cudaStream_t stream) {
     const int64_t grid = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * (D / kCols);
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    auto kernel = a.query_start_loc == nullptr ? linear_recurrent_kernel<D, G, 1> : linear_recurrent_kernel<D, G, 4>;
+    auto kernel = longest <= 1 ? linear_recurrent_kernel<D, G, 1> : linear_recurrent_kernel<D, G, 4>;
     return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a);
 }
 
 template <int D>
-cudaError_t launch_groups(const LinearArgs& a, cudaStream_t stream) {
+cudaError_t launch_groups(const LinearArgs& a, int32_t longest, cudaStream_t stream) {
     switch (a.num_q_heads / a.num_kv_heads) {
-        case 1: return launch<D, 1>(a, stream);
-        case 2: return launch<D, 2>(a, stream);
-        case 4: return launch<D, 4>(a, stream);
-        default: return launch<D, 8>(a, stream);
+        case 1: return launch<D, 1>(a, longest, stream);
+        case 2: return launch<D, 2>(a, longest, stream);
+        case 4: return launch<D, 4>(a, longest, stream);
+        default: return launch<D, 8>(a, longest, stream);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_linear_recurrent(const LinearArgs& a, cudaStream_t stream) {
-    return a.head_dim == 64 ? launch_groups<64>(a, stream) : launch_groups<128>(a, stream);
+cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, cudaStream_t stream) {
+    return a.head_dim == 64 ? launch_groups<64>(a, longest, stream) : launch_groups<128>(a, longest, stream);
 }
 
 }  // namespace pkv

@@ -128,9 +128,10 @@ struct ChunkParams {
     LinearArgs A;
     float* bounds;          // fp32 [ranges - 1][Hkv][d][d]: the state at the end of each range
     int4* tails;            // [ranges - 1]: what the scan needs of a range's last segment
-    Segment* segments;      // [ranges][Hkv][kMaxSegments]
+    Segment* segments;      // [ranges][CTAs of a range][kMaxSegments]
     int32_t ranges, range;  // ranges, and chunks of each
     int32_t units;          // chunks the host counted
+    int32_t subs;           // CTAs a kv head's group of q heads is dealt to
 };
 
 // Chunks of sequence s (0: the recurrent form takes it).
@@ -273,6 +274,7 @@ __device__ __forceinline__ void mma_state(uint32_t col_s, uint32_t svt, uint32_t
     }
 }
 
+// G: q heads per CTA.
 template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -288,7 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = &rest.tmem;
     const LinearArgs& A = P.A;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int h = blockIdx.y;
+    const int h = blockIdx.y / P.subs, sub = blockIdx.y % P.subs;
+    const int hq0 = (h * P.subs + sub) * G;  // first of this CTA's q heads
+    const bool reports = blockIdx.y == 0;
 
     // ---------------------------------------------------------- setup
     griddep_launch_dependents();
@@ -320,22 +324,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::sts128(smem_addr(smem + L::OFF_P) + i * 16, 0u, 0u, 0u, 0u);
     tc::fence_proxy_async_smem();
     griddep_wait();
-    Segment* segs = P.segments + (static_cast<int64_t>(blockIdx.x) * gridDim.y + h) * kMaxSegments;
+    Segment* segs = P.segments + (static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y) * kMaxSegments;
     if (warp == 0) {
-        const bool last = blockIdx.x == gridDim.x - 1 && h == 0;
+        const bool last = blockIdx.x == gridDim.x - 1 && reports;
         const int u0 = blockIdx.x * P.range, u1 = u0 + P.range;
         int nseg = 0, chunks = 0, any_bad = 0;
         const int seen = scan_units(P, u0, u1, last, [&](int s, int first, int end, bool in, unsigned lanes) {
             const int k = nseg + __popc(lanes & ((1u << lane) - 1));
             int n = 0, bad = 0;
             if (in && k < kMaxSegments) {
-                const LinearSeq q = linear_seq(A, s, h == 0 && first >= u0);
+                const LinearSeq q = linear_seq(A, s, reports && first >= u0);
                 const int c0 = max(u0, first) - first, c1 = min(u1, end) - first;
                 Segment g;
                 g.row0 = q.row0 + c0 * C;
                 g.rows = min(q.rows, c1 * C) - c0 * C;
                 g.load = c0 > 0 ? kFromBounds : q.load;
-                g.store = end <= u1 ? q.store : -1;
+                g.store = end <= u1 && sub == 0 ? q.store : -1;
                 g.seq = s;
                 g.first = c0 == 0;
                 bad = q.bad;
@@ -654,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&bar[B_QFULL + st], static_cast<uint32_t>(kPanels) * kPanel);
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn)
-                    tc::tma_load_3d(smem + L::OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, h * G + q_next % G,
+                    tc::tma_load_3d(smem + L::OFF_Q + st * kTile + pn * kPanel, &tm_q, 64 * pn, hq0 + q_next % G,
                                     q_at.row, &bar[B_QFULL + st]);
             }
             __syncwarp();
@@ -759,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nrows = min(C, at.left) - t0;
                 const int mark = rest.bad_rows[i % kBadBuffers][dv];
                 const int nan_from = ((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0;
-                float* o = A.out + (static_cast<int64_t>(at.row) + t0) * row_step + (h * G + g) * D + dv;
+                float* o = A.out + (static_cast<int64_t>(at.row) + t0) * row_step + (hq0 + g) * D + dv;
                 if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
@@ -783,11 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < nseg; ++k) {
             const int64_t n = -static_cast<int64_t>(segs[k].rows) * G * D;  // negative for the others
             for (int64_t i = threadIdx.x; i < n; i += kThreads)
-                A.out[(segs[k].row0 + i / (G * D)) * static_cast<int64_t>(A.num_q_heads) * D + h * G * D +
+                A.out[(segs[k].row0 + i / (G * D)) * static_cast<int64_t>(A.num_q_heads) * D + hq0 * D +
                       i % (G * D)] = 0.f;
         }
     }
-    if (h == 0) {
+    if (reports) {
         // A slot that two sequences store to, or that one stores to and
         // another reads, has no defined content: reported.
         for (int k = 0; k < nseg; ++k) {
@@ -1028,7 +1032,7 @@ cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
     static bool done[64] = {};
     cudaError_t e = configure(linear_chunk_kernel<D, G>, smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.ranges, P.A.num_kv_heads), dim3(kThreads),
+    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.ranges, P.A.num_kv_heads * P.subs), dim3(kThreads),
                              smem_bytes<D>(), stream, tq, tk, tv, P);
 }
 
@@ -1045,7 +1049,7 @@ cudaError_t launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUten
         e = launch_overlapped(linear_scan_kernel, dim3(D * D / 512, P.A.num_kv_heads), dim3(256), 0, stream, P);
         if (e != cudaSuccess) return e;
     }
-    switch (P.A.num_q_heads / P.A.num_kv_heads) {
+    switch (P.A.num_q_heads / P.A.num_kv_heads / P.subs) {
         case 1: return launch_main<D, 1>(tq, tk, tv, P, stream);
         case 2: return launch_main<D, 2>(tq, tk, tv, P, stream);
         case 4: return launch_main<D, 4>(tq, tk, tv, P, stream);
@@ -1066,55 +1070,61 @@ static int64_t max_ranges(int32_t num_seqs, int32_t num_tokens, int32_t num_kv_h
 
 static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
-                              int num_sms) {
+size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int num_sms) {
     const size_t n = static_cast<size_t>(max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms));
-    return n * num_kv_heads * (static_cast<size_t>(head_dim) * head_dim * sizeof(float) + kMaxSegments * sizeof(Segment)) +
-           round256(n * sizeof(int4));
+    return round256(n * sizeof(int4)) + n * num_kv_heads * head_dim * head_dim * sizeof(float) +
+           n * num_q_heads * kMaxSegments * sizeof(Segment);
 }
 
 LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t group,
                        int32_t head_dim, int num_sms, int32_t max_recurrent) {
-    LinearPlan best = {0, 0, 0, 0, false};
+    LinearPlan best = {0, 0, 0, 0, 1, false};
     int64_t units = 0;
     for (int32_t s = 0; s < num_seqs; ++s) {
         const int32_t rows = qsl[s + 1] - qsl[s];
-        if (rows > 0 && rows <= max_recurrent) ++best.recurrent;
-        if (rows > max_recurrent) units += (rows + C - 1) / C;
+        if (rows <= max_recurrent) best.recurrent = rows > best.recurrent ? rows : best.recurrent;
+        else units += (rows + C - 1) / C;
     }
     if (units == 0) return best;
     best.units = static_cast<int32_t>(units);
     const int64_t most = max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms);
-    // Microseconds of a chunk in the main and in the state kernel, and of a
-    // kernel's start and end.  More ranges fill more SMs; where they cut
-    // sequences, the state kernel reads K and V of all but the last range once
-    // more, and the states are carried over.
-    const double chunk = (head_dim == 64 ? 0.5 : 1.2) + (head_dim == 64 ? 1.2 : 1.6) * group;
-    const double state = head_dim == 64 ? 0.6 : 1.0, start = 6.0, join = 12.0;
+    // Microseconds of a chunk in the main and in the state kernel, of a
+    // kernel's start and end, and of the two more kernels that join ranges.
+    // More ranges fill more SMs; where they cut sequences, the state kernel
+    // reads K and V of all but the last range once more, and the states are
+    // carried over.  Dealing a group's q heads to several CTAs fills SMs too,
+    // and repeats the state's work in each.
+    const bool narrow = head_dim == 64;
+    const double fixed = narrow ? 0.3 : 1.2, item = narrow ? 1.4 : 1.5, state = narrow ? 0.5 : 0.9, start = 8.0,
+                 join = 11.0;
     double best_us = 1e30;
-    for (int64_t n = 1; n <= most && n <= units; ++n) {
-        const int64_t range = (units + n - 1) / n;
-        if ((units + range - 1) / range != n) continue;  // the same ranges as a smaller n
-        if (num_seqs > kMaxSegments && range > kMaxSegments) continue;
-        const int64_t waves = (n * num_kv_heads + num_sms - 1) / num_sms;
-        double us = waves * (start + range * chunk);
-        if (us >= best_us) continue;
-        bool cut = false;
-        int64_t end = 0;  // whether a border lies inside a sequence
-        for (int32_t s = 0; s < num_seqs && !cut && n > 1; ++s) {
-            const int32_t rows = qsl[s + 1] - qsl[s];
-            if (rows <= max_recurrent) continue;
-            const int64_t first = end;
-            end += (rows + C - 1) / C;
-            const int64_t border = (first / range + 1) * range;
-            cut = border < end;
-        }
-        if (cut) us += join + ((n - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
-        if (us < best_us) {
-            best_us = us;
-            best.ranges = static_cast<int32_t>(n);
-            best.range = static_cast<int32_t>(range);
-            best.cut = cut;
+    for (int32_t subs = 1; subs <= group; subs *= 2) {
+        const int64_t heads = static_cast<int64_t>(num_kv_heads) * subs;
+        const double chunk = fixed + item * (group / subs);
+        for (int64_t n = 1; n <= most && n <= units; ++n) {
+            const int64_t range = (units + n - 1) / n;
+            if ((units + range - 1) / range != n) continue;  // the same ranges as a smaller n
+            if (num_seqs > kMaxSegments && range > kMaxSegments) continue;
+            double us = (n * heads + num_sms - 1) / num_sms * (start + range * chunk);
+            if (us >= best_us) continue;
+            bool cut = false;  // whether a border lies inside a sequence
+            int64_t end = 0;
+            for (int32_t s = 0; s < num_seqs && !cut && n > 1; ++s) {
+                const int32_t rows = qsl[s + 1] - qsl[s];
+                if (rows <= max_recurrent) continue;
+                const int64_t first = end;
+                end += (rows + C - 1) / C;
+                cut = (first / range + 1) * range < end;
+            }
+            if (cut) us += join + ((n - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
+            if (us < best_us) {
+                best_us = us;
+                best.ranges = static_cast<int32_t>(n);
+                best.range = static_cast<int32_t>(range);
+                best.subs = subs;
+                best.cut = cut;
+            }
         }
     }
     return best;
@@ -1140,6 +1150,7 @@ cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, vo
     P.ranges = plan.ranges;
     P.range = plan.range;
     P.units = plan.units;
+    P.subs = plan.subs;
     return a.head_dim == 64 ? launch_all<64>(tq, tk, tv, P, plan.cut, stream)
                             : launch_all<128>(tq, tk, tv, P, plan.cut, stream);
 }

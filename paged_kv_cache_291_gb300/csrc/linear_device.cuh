@@ -21,7 +21,8 @@ struct LinearSeq {
 // `report`: whether this thread records what is out of range.
 __device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& A, int s, bool report) {
     LinearSeq q;
-    const int n = __ldg(A.context_lens + s);
+    // loads that hang on nothing, together
+    const int n = __ldg(A.context_lens + s), from = __ldg(A.state_slots + s), to = __ldg(A.new_slots + s);
     if (A.query_start_loc != nullptr) {
         q.row0 = __ldg(A.query_start_loc + s);
         const int end = __ldg(A.query_start_loc + s + 1);
@@ -45,7 +46,6 @@ __device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& A, int s, bool
             record_error(A.err, kErrRange, static_cast<uint32_t>(s));
         return q;
     }
-    const int from = __ldg(A.state_slots + s), to = __ldg(A.new_slots + s);
     if ((n > q.rows && from >= A.num_slots) || to >= A.num_slots) {
         if (report) record_error(A.err, kErrRange, static_cast<uint32_t>(s));
         q.bad = 1;
@@ -70,10 +70,7 @@ __device__ __forceinline__ bool linear_shares(const LinearArgs& A, int other, in
     return __ldg(A.new_slots + other) == store || (n > rows && __ldg(A.state_slots + other) == store);
 }
 
-// exp(log_decay * tokens) as hi + lo (2^-48 relative): a state is multiplied
-// by it once per token or chunk, so a 2^-24 error of one factor would grow
-// with the length of the context.  A log decay above 0 or NaN counts as 0
-// and is reported; -inf keeps nothing.
+// A log decay above 0 or NaN counts as 0 and is reported; -inf keeps nothing.
 __device__ __forceinline__ float clean_log_decay(const LinearArgs& A, int h, bool report) {
     float g = __ldg(A.log_decay + h);
     if (!(g <= 0.f)) {
@@ -83,10 +80,39 @@ __device__ __forceinline__ float clean_log_decay(const LinearArgs& A, int h, boo
     return fmaxf(g, -1e30f);
 }
 
+// exp(g * tokens) as hi + lo, g <= 0.  A state is multiplied by it once per
+// token or chunk, so the 2^-25 of one fp32 factor would grow with the length
+// of the context.  x = g * tokens as an fp32 pair; n = the nearest whole
+// multiple of ln 2, r = x - n ln 2 (ln 2 in two parts, the first short enough
+// that n times it is exact), |r| <= 0.35; exp(r) = 1 + r + r^2 (1/2 + r/6 +
+// ...), the Taylor terms from r^2 on in fp32: off by 2^-24 of r^2 / 2, which
+// for the slow decays, where it counts, is far below 2^-40.
 __device__ __forceinline__ float2 decay_pair(float g, int tokens) {
-    const double x = exp(static_cast<double>(g) * tokens);
-    const float hi = static_cast<float>(x);
-    return make_float2(hi, static_cast<float>(x - static_cast<double>(hi)));
+    const float t = static_cast<float>(tokens);
+    const float x = g * t;
+    if (x < -100.f) return make_float2(0.f, 0.f);
+    const float xl = fmaf(g, t, -x);
+    const float n = rintf(x * 1.44269504f);
+    constexpr float kLn2Hi = 0.693145752f;       // 15 bits
+    constexpr float kLn2Lo = 1.42860677e-6f;     // ln 2 - kLn2Hi
+    const float rh = fmaf(n, -kLn2Hi, x);
+    const float rl = fmaf(n, -kLn2Lo, xl);
+    const float r = rh + rl;
+    float p = 1.f / 362880.f;
+    p = fmaf(p, r, 1.f / 40320.f);
+    p = fmaf(p, r, 1.f / 5040.f);
+    p = fmaf(p, r, 1.f / 720.f);
+    p = fmaf(p, r, 1.f / 120.f);
+    p = fmaf(p, r, 1.f / 24.f);
+    p = fmaf(p, r, 1.f / 6.f);
+    p = fmaf(p, r, 0.5f);
+    const float tail = fmaf(p * r, r, rl);       // what 1 + rh lacks
+    const float one = 1.f + rh;
+    const float rest = (rh - (one - 1.f)) + tail;
+    const float hi = one + rest;
+    const float lo = rest - (hi - one);
+    const float scale = exp2f(n);
+    return make_float2(hi * scale, lo * scale);
 }
 
 }  // namespace pkv

@@ -179,19 +179,21 @@ struct LinearArgs {
     float scale;
 };
 
-cudaError_t launch_linear_recurrent(const LinearArgs& a, cudaStream_t stream);
+// longest: rows of the longest sequence it will meet.
+cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, cudaStream_t stream);
 
 // How the chunked form cuts a batch: the chunks (64 tokens) of the sequences
 // of more than max_recurrent rows, in order, in `ranges` ranges of `range`.
 struct LinearPlan {
-    int32_t recurrent;   // sequences the recurrent form takes
+    int32_t recurrent;   // rows of the longest sequence the recurrent form takes, 0: none
     int32_t units;       // chunks of the others
     int32_t ranges, range;
+    int32_t subs;        // CTAs that share a kv head's q heads
     bool cut;            // a border lies inside a sequence
 };
 
-size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
-                              int num_sms);
+size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                              int32_t head_dim, int num_sms);
 LinearPlan plan_linear(const int32_t* query_start_loc_host, int32_t num_seqs, int32_t num_tokens,
                        int32_t num_kv_heads, int32_t group, int32_t head_dim, int num_sms, int32_t max_recurrent);
 
