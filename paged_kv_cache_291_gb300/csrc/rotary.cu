@@ -225,11 +225,14 @@ cudaError_t launch_rotary(RotaryArgs a, int num_sms, cudaStream_t stream) {
     const int mode = a.k_pool == nullptr ? 0 : a.kv_e4m3 ? 2 : 1;
     const int rows = a.num_q_heads + (mode == 0 ? 1 : 2) * a.num_kv_heads;
     const int side = 512 / a.head_dim;  // rows a warp holds side by side
-    // A warp that takes more rows computes its sines and cosines for more of
-    // them, but few tokens need their rows spread over the SMs.
     const int groups = (rows + side - 1) / side;
-    const int64_t want = static_cast<int64_t>(num_sms) * 32;  // warps
+    // A warp's sines and cosines serve all its rows, so a token goes to one
+    // warp where there are tokens enough for 16 warps an SM, and to more where
+    // not; a warp that takes more than 7 row groups ends too long after the
+    // others.
+    const int64_t want = static_cast<int64_t>(num_sms) * 16;
     int64_t runs = (want + a.num_tokens - 1) / a.num_tokens;
+    runs = runs > (groups + 6) / 7 ? runs : (groups + 6) / 7;
     if (runs > groups) runs = groups;
     a.rows_per_run = static_cast<int32_t>((groups + runs - 1) / runs) * side;
     a.runs = (rows + a.rows_per_run - 1) / a.rows_per_run;
