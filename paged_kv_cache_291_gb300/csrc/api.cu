@@ -919,7 +919,7 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
         pkv::linear_workspace_bytes(num_seqs, num_tokens, num_q_heads, a.num_kv_heads, a.head_dim, dev->num_sms))
         return PKV_ERR_WORKSPACE;
     a.query_start_loc = query_start_loc;
-    a.max_recurrent = 16;
+    a.max_recurrent = pkv::linear_max_recurrent(num_q_heads / a.num_kv_heads);
     const pkv::LinearPlan plan = pkv::plan_linear(query_start_loc_host, num_seqs, num_tokens, a.num_kv_heads,
                                                   num_q_heads / a.num_kv_heads, a.head_dim, dev->num_sms,
                                                   a.max_recurrent);

@@ -182,6 +182,13 @@ struct LinearArgs {
 // longest: rows of the longest sequence it will meet.
 cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, cudaStream_t stream);
 
+// Rows up to which the recurrent form is the faster one.  It reads and writes
+// the state at the full rate and then pays for each token and q head; the
+// chunked form costs a state and a chunk whatever the rows.  16/8 heads of 128,
+// 64 sequences going on: 8 rows 29 us against 32, 16 rows 55 against 33; one
+// q head to a state crosses at 11 to 12 rows, eight at 5.
+inline int32_t linear_max_recurrent(int32_t group) { return group == 1 ? 11 : group == 2 ? 8 : group == 4 ? 6 : 5; }
+
 // How the chunked form cuts a batch: the chunks (64 tokens) of the sequences
 // of more than max_recurrent rows, in order, in `ranges` ranges of `range`.
 struct LinearPlan {
