@@ -383,6 +383,158 @@ def test_states_past_two_gigabytes(pkv):
     assert torch.equal(states[n - 2], b.states[int(b.new[1])])
 
 
+def test_prefill_more_sequences_than_a_range_lists(pkv):
+    """300 one- and two-chunk sequences on one head: ranges are held to the
+    128 segments a CTA lists."""
+    rng = np.random.default_rng(70)
+    lens = [int(x) for x in rng.integers(12, 90, 300)]
+    b = Batch(71, lens, [int(x) for x in rng.integers(0, 2, 300) * 5], 1, 1, 64)
+    b.check(b.prefill(pkv), "300 sequences")
+    assert pkv.get_error() == (0, 0)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_prefill_random_batches(pkv, seed):
+    """Batches whose ranges begin and end anywhere in the sequences."""
+    rng = np.random.default_rng(80 + seed)
+    group, d = [(1, 128), (2, 64), (4, 128), (8, 64), (2, 128), (4, 64)][seed]
+    hkv = int(rng.integers(1, 4))
+    lens = [int(np.exp(rng.uniform(0, np.log(700)))) for _ in range(int(rng.integers(1, 9)))]
+    past = [int(x) for x in rng.integers(0, 2, len(lens)) * 9]
+    b = Batch(90 + seed, lens, past, group * hkv, hkv, d, packed=bool(seed % 2), separate=bool(seed % 3))
+    b.check(b.prefill(pkv), f"lens {lens}")
+    assert pkv.get_error() == (0, 0)
+
+
+@pytest.mark.parametrize("n,hq,d", [(5, 2, 64), (150, 2, 64), (150, 1, 128)])
+def test_values_that_are_not_finite_keep_their_place(pkv, n, hq, d):
+    """A NaN or infinite v element reaches its own column from its own token
+    on; a NaN q row its own outputs; a NaN k row all outputs from its token
+    on.  Nothing earlier changes."""
+    b = Batch(100, [n], [3], hq, 1, d, packed=False)
+    want, _ = b.oracle()
+    bound, _ = b.oracle(absolute=True)
+    c = (40 + 4 * n) * 2.0 ** -24
+    t = n * 2 // 3
+    clean = {x: getattr(b, x).clone() for x in "qkv"}
+
+    def run(name, index, value):
+        for x in "qkv":
+            getattr(b, x).copy_(clean[x])
+        getattr(b, name)[index] = value
+        out = f64(b.prefill(pkv))
+        assert pkv.get_error() == (0, 0)
+        return out
+
+    def same(got, sel):
+        assert np.all(np.abs(got[sel] - want[sel]) <= c * bound[sel])
+
+    for value in (float("nan"), float("inf")):
+        out = run("v", (t, 0, 7), value)
+        same(out, np.s_[:t])
+        assert not np.isfinite(out[t:, :, 7]).any()
+        others = [e for e in range(d) if e != 7]
+        same(out, np.s_[:, :, others])
+        assert not torch.isfinite(b.states[int(b.new[0]), 0, :, 7]).any()
+        assert torch.isfinite(b.states[int(b.new[0]), 0, :, 8]).all()
+    out = run("q", (t, 0), float("nan"))
+    assert np.isnan(out[t, 0]).all()
+    out[t, 0] = want[t, 0]
+    same(out, np.s_[:])
+    out = run("k", (t, 0), float("nan"))
+    same(out, np.s_[:t])
+    assert np.isnan(out[t:]).all()
+
+
+def test_device_lengths_that_are_not_the_hosts_are_reported(pkv):
+    b = Batch(101, [100, 100], [0, 0], 2, 1, 64)
+    for device in ([0, 170, 200], [0, 100, 130], [0, 100, 900], [0, -5, 200]):
+        pkv.linear_prefill_attention(*b.args(), dev_tensor(np.array(device, np.int32)), dev_tensor(b.slots),
+                                     dev_tensor(b.ctx), b.scale, new_slots=dev_tensor(b.new),
+                                     query_start_loc_host=b.qsl)
+        st, _ = pkv.get_error()
+        assert st == 9, device
+
+
+def test_prefill_group_dealt_to_several_ctas_stores_the_state_once(pkv):
+    """Few heads and a short prompt: the q heads of a state go to CTAs of their own."""
+    b = Batch(102, [80], [4], 8, 1, 64, separate=False)
+    b.check(b.prefill(pkv), "dealt")
+    assert pkv.get_error() == (0, 0)
+
+
+def test_two_graphs_on_one_workspace(pkv):
+    """Graphs that share a workspace replay one after the other."""
+    a, b = (Batch(103 + i, [700, 3, 60], [0, 4, 4], 2, 1, 128, packed=False) for i in range(2))
+    ws = torch.empty(pkv.linear_prefill_workspace_size(3, 763, 2, 1, 128), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros((763, 2, 128), device="cuda") for _ in range(2)]
+    graphs = []
+    torch.cuda.synchronize()
+    for x, out in ((a, outs[0]), (b, outs[1])):
+        dev = [dev_tensor(y) for y in (x.g, x.qsl, x.slots, x.ctx, x.new)]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pkv.linear_prefill_attention(x.states, dev[0], x.q, x.k, x.v, dev[1], dev[2], dev[3], x.scale,
+                                         new_slots=dev[4], out=out, workspace=ws, query_start_loc_host=x.qsl)
+        graphs.append((g, dev))
+    for g, _ in graphs + graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert pkv.get_error() == (0, 0)
+    a.check(outs[0], "first graph")
+    b.check(outs[1], "second graph")
+
+
+def test_decode_many_sequences_and_heads(pkv):
+    b = Batch(105, [1] * 150, [0 if s % 5 == 0 else s for s in range(150)], 5, 5, 64)
+    b.check(b.decode(pkv), "150 sequences")
+    assert pkv.get_error() == (0, 0)
+
+
+def test_slow_decay_keeps_its_accuracy_over_many_steps(pkv):
+    """3,000 single-token steps of a head that forgets 1/10,000 a step: a
+    factor rounded to fp32 once would be off by 2^-25 a step, 9e-5 at the
+    end; the pair keeps the recurrence at its own roundings, which are
+    independent: 2^-24 times the root of the steps, 3.3e-6, of the norm."""
+    steps, d = 3000, 64
+    rng = np.random.default_rng(106)
+    S0 = rng.standard_normal((1, 1, d, d)).astype(np.float32)
+    states = dev_tensor(S0)
+    g = np.array([-1.00007e-4], np.float32)
+    zero = torch.zeros((1, 1, d), dtype=torch.bfloat16, device="cuda")
+    slots = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ctx = torch.full((1,), 5, dtype=torch.int32, device="cuda")
+    gd = dev_tensor(g)
+    for _ in range(steps):
+        pkv.linear_decode_attention(states, gd, zero, zero, zero, slots, ctx, 1.0)
+    want = S0.astype(np.float64) * np.exp(float(g[0]) * steps)
+    err = np.linalg.norm(states.double().cpu().numpy() - want) / np.linalg.norm(want)
+    assert err <= 2.0 ** -24 * np.sqrt(steps), err
+
+
+def test_binding_refuses_what_it_cannot_pass_on(pkv):
+    b = Batch(107, [1] * 3, [2] * 3, 2, 1, 64)
+    args = list(b.args()) + [dev_tensor(b.slots), dev_tensor(b.ctx)]
+    for i, bad, kind in ((0, b.states.double(), TypeError), (0, b.states[:, :, :32], ValueError),
+                         (1, dev_tensor(np.zeros(2, np.float32)), ValueError), (2, b.q.float(), TypeError),
+                         (3, b.k[:2], ValueError), (4, b.v.cpu(), ValueError), (5, args[5].long(), TypeError),
+                         (6, args[6][:2], ValueError)):
+        broken = list(args)
+        broken[i] = bad
+        with pytest.raises(kind):
+            pkv.linear_decode_attention(*broken, b.scale)
+    with pytest.raises(ValueError):
+        pkv.linear_decode_attention(*args, b.scale, out=torch.zeros((3, 2, 32), device="cuda"))
+    with pytest.raises(ValueError):
+        pkv.linear_decode_attention(*args, b.scale, out=torch.zeros((3, 2, 64)))
+    with pytest.raises(ValueError):
+        pkv.linear_prefill_attention(*args[:5], dev_tensor(np.array([0, 1, 3], np.int32)), args[5], args[6], b.scale)
+    with pytest.raises(pkv.PKVError) as e:
+        pkv.linear_prefill_attention(*args[:5], dev_tensor(b.qsl), args[5], args[6], b.scale,
+                                     workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 7
+
 def test_hybrid_layers_prefill_then_decode(pkv):
     """A two-layer step as a hybrid stack runs it: rotary, then softmax
     attention over the paged cache in one layer and linear attention over the
