@@ -34,7 +34,7 @@
 #include <cstdint>
 
 #include "linear_device.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_rows.cuh"
 
 namespace pkv {
 namespace {
