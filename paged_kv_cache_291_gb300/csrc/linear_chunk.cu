@@ -55,6 +55,15 @@ struct Layout {
     static constexpr int OFF_VT = OFF_Q + kQ * kTile;
     static constexpr int OFF_P = OFF_VT + 3 * kTile;  // two buffers of three terms
     static constexpr int OFF_REST = OFF_P + 2 * 3 * kPTile;
+    // TMEM columns: scores, S, its three terms, the two parts of the outputs.
+    // V P takes P's terms one after the other into one sum at head_dim 128; at
+    // 64 there are columns for three sums, so they go side by side in one MMA
+    // of N = 192, which reads V once (a ragged batch of 12 prompts, 32/8
+    // heads: 49.5 to 39 us).
+    static constexpr int kSums = D == 64 ? 3 : 1;
+    static constexpr uint32_t COL_SCORES = 0, COL_S = C, COL_SB = COL_S + D, COL_OS = COL_SB + 3 * D / 2,
+                              COL_OP = COL_OS + C;
+    static_assert(COL_OP + kSums * C <= 512, "TMEM columns");
 };
 constexpr int TAB_P = 0;                              // float[128]: scale lam^(t-s) at 63 + t - s
 constexpr int TAB_O = 128;                            // float[64]: scale lam^(t+1)
@@ -106,8 +115,7 @@ constexpr int kLoadWarp = 2, kMmaWarp = 3;
 // V~: warps 2 (which also loads), 5, 6 and 7
 constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 
-// TMEM columns (head_dim 128; 64 uses the first half of S and of each term).
-constexpr uint32_t COL_SCORES = 0, COL_S = 64, COL_SB = 192, COL_OS = 384, COL_OP = 448, kTmemCols = 512;
+constexpr uint32_t kTmemCols = 512;
 
 constexpr int kMaxSegments = 128;  // of one range: ranges are at most this long when there are more sequences
 constexpr int kFromBounds = -2;
@@ -220,12 +228,12 @@ __device__ __forceinline__ float* walk(float* p, int64_t bytes) {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity); }
 
 // V~ of one chunk, elementwise over the swizzled V tile: factor[rows - 1 - s]
-// * extra * v_s in three terms.  Rows past the piece become zero, there and in
+// * v_s in three terms.  Rows past the piece become zero, there and in
 // K and V: they are other sequences' tokens, and a zero factor times a NaN
 // would poison the products.  Returns 0, or NaN if a value was not finite.
 template <int D, int TERM, int THREADS, int UNROLL>
-__device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t svt, const float* factor, float extra,
-                                           int rows, int tid) {
+__device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t svt, const float* factor, int rows,
+                                           int tid) {
     constexpr int kChunks = C * D * 2 / 16;  // 16-byte vectors of the tile
     float2 acc = make_float2(0.f, 0.f);
     const float2 zero = make_float2(0.f, 0.f);
@@ -236,7 +244,7 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
         if (row < rows) {
             uint32_t x[4], hi[4], mid[4], lo[4];
             tc::lds128(sv + at, x);
-            const float f = factor[rows - 1 - row] * extra;
+            const float f = factor[rows - 1 - row];
             const float2 ff = make_float2(f, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the scores of the next item and P V run.
         constexpr uint32_t kIdescScores = tc::idesc_bf16_f32(128, C, 0, 0);
         constexpr uint32_t kIdescOS = tc::idesc_bf16_f32(128, C, 0, 0);
-        constexpr uint32_t kIdescOP = tc::idesc_bf16_f32(128, C, 1, 1);
+        constexpr uint32_t kIdescOP = tc::idesc_bf16_f32(128, L::kSums * C, 1, 1);
         const uint32_t sk0 = smem_addr(smem + L::OFF_K), sv0 = smem_addr(smem + L::OFF_V), sq0 = smem_addr(smem + L::OFF_Q);
         const uint32_t svt = smem_addr(smem + L::OFF_VT), sp = smem_addr(smem + L::OFF_P);
         // scores[s][t] = k_s . q_t (lanes past 63 take the rows that follow K in
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 const uint32_t step = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
-                tc::mma_bf16_ss(tmem + COL_SCORES, a + step, b + step, kIdescScores, k > 0 ? 1u : 0u);
+                tc::mma_bf16_ss(tmem + L::COL_SCORES, a + step, b + step, kIdescScores, k > 0 ? 1u : 0u);
             }
             tc::mma_commit(&bar[B_SCORES]);
         };
@@ -413,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b = tc::smem_desc_sw128(sq0 + (n % kQ) * kTile, 16, 1024);
 #pragma unroll 1
             for (int part = 2; part >= 0; --part) {
-                const uint32_t a = tmem + COL_SB + part * (D / 2);
+                const uint32_t a = tmem + L::COL_SB + part * (D / 2);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16_ts(tmem + COL_OS, a + 8 * k, b + (((k >> 2) * kPanel + (k & 3) * 32) >> 4), kIdescOS,
+                    tc::mma_bf16_ts(tmem + L::COL_OS, a + 8 * k, b + (((k >> 2) * kPanel + (k & 3) * 32) >> 4), kIdescOS,
                                     part < 2 || k > 0 ? 1u : 0u);
             }
             tc::mma_commit(&bar[B_QEMPTY + n % kQ]);
@@ -426,12 +434,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto out_scores = [&](int n) {
             const uint64_t a = tc::smem_desc_sw128(sv0 + (n / G % kKv) * kTile, kPanel, 1024);
 #pragma unroll 1
-            for (int part = 2; part >= 0; --part) {
+            for (int part = 3 - L::kSums; part >= 0; --part) {
                 const uint64_t b = tc::smem_desc_sw128(sp + ((n & 1) * 3 + part) * kPTile, kPTile, 1024);
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
-                    tc::mma_bf16_ss(tmem + COL_OP, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdescOP,
-                                    part < 2 || k > 0 ? 1u : 0u);
+                    tc::mma_bf16_ss(tmem + L::COL_OP, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdescOP,
+                                    part < 3 - L::kSums || k > 0 ? 1u : 0u);
             }
             if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kKv]);
             tc::mma_commit(&bar[B_PFREE + (n & 1)]);
@@ -455,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g == 0) {
                 if (!warp_wait(&bar[B_VT], i & 1)) { ok = false; break; }
                 if (tc::elect_one()) {
-                    mma_state<D, kTile>(tmem + COL_S, svt, sk0 + (i % kKv) * kTile, true);
+                    mma_state<D, kTile>(tmem + L::COL_S, svt, sk0 + (i % kKv) * kTile, true);
                     tc::mma_commit(&bar[B_VTFREE]);
                 }
                 __syncwarp();
@@ -481,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 0 || warp == 1 || warp == 4) {
         // ------------------------------------------------------ P
         const int s = 32 * (warp & 1) + lane, begin = warp == 0 ? 0 : 32;
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + COL_SCORES + begin;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(32 * (warp & 1)) << 16) + L::COL_SCORES + begin;
         const uint32_t prow = smem_addr(smem + L::OFF_P) + s * 128;
         const float* f = tab + TAB_P + 63 - s + begin;
         // Rows 32-63 keep the zeros of tokens 0-31 that the set-up wrote.
@@ -536,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kCols = D / 2, kBatches = kCols / 16;
         const int w = warp & 3, dv = 32 * w + lane, c0 = warp - kSWarp < 4 ? 0 : kCols;
         const bool live = 32 * w < D;
-        const uint32_t ts = tmem + (static_cast<uint32_t>(32 * w) << 16) + COL_S + c0;
-        const uint32_t tb = tmem + (static_cast<uint32_t>(32 * w) << 16) + COL_SB + c0 / 2;
+        const uint32_t ts = tmem + (static_cast<uint32_t>(32 * w) << 16) + L::COL_S + c0;
+        const uint32_t tb = tmem + (static_cast<uint32_t>(32 * w) << 16) + L::COL_SB + c0 / 2;
         const int64_t head = static_cast<int64_t>(D) * D;
         auto state_at = [&](int load) -> const float* {
             if (load == kFromBounds)
@@ -683,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 while (q_next <= (i - 1) * G + kQ && q_next < nitems && ok) ok = load_q();
             const uint32_t sk = smem_addr(smem + L::OFF_K + st * kTile), sv = smem_addr(smem + L::OFF_V + st * kTile);
             const float acc = convert_v<D, kTile, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + L::OFF_VT), tab + TAB_V,
-                                                                     1.f, nrows, tid);
+                                                                     nrows, tid);
             if (acc != 0.f) {
                 // A value that is not finite reaches the outputs of its column
                 // from its row on, and no earlier row: it leaves V for P V
@@ -734,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_after_sync();
             uint32_t xs[32];
             if (live) {
-                tc::tmem_ld32x32b_x32(tl + COL_OS, xs);
+                tc::tmem_ld32x32b_x32(tl + L::COL_OS, xs);
                 tc::tmem_wait_ld();
             }
             tc::fence_before_sync();
@@ -751,10 +759,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!warp_wait(&bar[B_OP], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
-            uint32_t xp[32];
             if (live) {
-                tc::tmem_ld32x32b_x32(tl + COL_OP, xp);
-                tc::tmem_wait_ld();
+#pragma unroll
+                for (int part = L::kSums - 1; part >= 0; --part) {
+                    uint32_t xp[32];
+                    tc::tmem_ld32x32b_x32(tl + L::COL_OP + part * C, xp);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        xs[j] = __float_as_uint(__uint_as_float(xs[j]) + __uint_as_float(xp[j]));
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -767,13 +781,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        *o = __uint_as_float(xs[j]) + __uint_as_float(xp[j]);
+                        *o = __uint_as_float(xs[j]);
                         o = walk(o, row_bytes);
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        float y = __uint_as_float(xs[j]) + __uint_as_float(xp[j]);
+                        float y = __uint_as_float(xs[j]);
                         if (j >= nan_from) y = __int_as_float(0x7fffffff);
                         if (j < nrows) *o = y;
                         o = walk(o, row_bytes);
@@ -815,21 +829,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The own state, from zero, of a range's last segment, where its sequence
 // goes on in the next range: sum_s lam^(end-1-s) k_s v_s^T over the segment's
 // tokens, one accumulation with no rescaling (the factor of a chunk's end is
-// part of V~).  Warps 0-7 V~, 8 loads, 9 MMA; warps 0-3 store the sum.
+// part of V~).  Warps 0-7 make V~, 8 loads, 9 issues the MMAs; warps 0-3
+// store the sum.  There is room in tensor memory here, so V~ goes there: it
+// is read from the V tile by transposing 8x8 loads, whose fragments are what
+// a 16-lane store takes, and the product needs shared memory for K alone.
+// (With V~ in shared memory the kernel was bound by it: 31 us for 8 ranges of
+// 29 chunks and 16 heads of 128.)
 constexpr int kStateThreads = 320;
-constexpr int kStateStages = 3;
+constexpr int kStateStages = 5;
 constexpr int kTile = 2 * kPanel;        // room for head_dim 128
 constexpr int SOFF_K = 0;
 constexpr int SOFF_V = SOFF_K + kStateStages * kTile;
-constexpr int SOFF_VT = SOFF_V + kStateStages * kTile;     // two buffers of three terms
-constexpr int SOFF_TAB = SOFF_VT + 2 * 3 * kTile;
-constexpr int SOFF_BAR = SOFF_TAB + C * 4;
+constexpr int SOFF_BAR = SOFF_V + kStateStages * kTile;
 enum { SB_FULL = 0, SB_EMPTY = kStateStages, SB_VT = 2 * kStateStages, SB_VTFREE = SB_VT + 2, SB_DONE = SB_VTFREE + 2, SNBAR };
 constexpr int SOFF_INFO = SOFF_BAR + SNBAR * 8;
 constexpr int SOFF_TMEM = SOFF_INFO + 8 * 4;
 constexpr int STATE_SMEM = SOFF_TMEM + 16 + 1024;
 static_assert(STATE_SMEM <= 232448, "shared memory budget (227 KB)");
-static_assert(2 * STATE_SMEM > 228 * 1024, "one CTA per SM");
+static_assert(2 * STATE_SMEM > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
+constexpr uint32_t SCOL_VT = 128;        // V~: two buffers of three terms of 32 columns
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(saddr)
+                 : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kStateThreads, 1)
@@ -840,7 +865,6 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + SOFF_BAR);
     int* info = reinterpret_cast<int*>(smem + SOFF_INFO);
-    float* tab = reinterpret_cast<float*>(smem + SOFF_TAB);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SOFF_TMEM);
     const LinearArgs& A = P.A;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -851,7 +875,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         fence_mbar_init();
     }
     if (warp == 8) {
-        tc::tmem_alloc(tmem_slot, 128);
+        tc::tmem_alloc(tmem_slot, kTmemCols);
         tc::tmem_relinquish();
         if (lane == 0) {
             tc::prefetch_tensormap(&tm_k);
@@ -878,7 +902,6 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         });
     }
     const float g = clean_log_decay(A, h, false);
-    if (threadIdx.x < C) tab[threadIdx.x] = expf(g * static_cast<float>(threadIdx.x));
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -907,8 +930,16 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (!warp_wait(&bar[SB_VT + vb], (i >> 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) {
-                mma_state<D, kTile>(tmem, smem_addr(smem + SOFF_VT + vb * 3 * kTile), smem_addr(smem + SOFF_K + st * kTile),
-                             i > 0);
+                constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 0, 1);
+                const uint64_t b = tc::smem_desc_sw128(smem_addr(smem + SOFF_K + st * kTile), kPanel, 1024);
+#pragma unroll 1
+                for (int part = 2; part >= 0; --part) {  // smallest first: the sums truncate
+                    const uint32_t a = tmem + SCOL_VT + (vb * 3 + part) * (C / 2);
+#pragma unroll
+                    for (int k = 0; k < C / 16; ++k)
+                        tc::mma_bf16_ts(tmem, a + 8 * k, b + k * (2048 >> 4), kIdesc,
+                                        i > 0 || part < 2 || k > 0 ? 1u : 0u);
+                }
                 tc::mma_commit(&bar[SB_EMPTY + st]);
                 tc::mma_commit(&bar[SB_VTFREE + vb]);
                 if (i == nch - 1) tc::mma_commit(&bar[SB_DONE]);
@@ -916,14 +947,42 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             __syncwarp();
         }
     } else {
+        // Warp w: 16 lanes (v indices) from 32 (w % 4) + 16 (w / 4).  Thread t
+        // holds lanes t/4 and t/4 + 8 of them, tokens 8 g + 2 (t % 4) and + 1.
+        const int dv0 = 32 * (warp & 3) + 16 * (warp >> 2);
+        const bool live = dv0 < D;
+        const int m = lane >> 3;  // the matrix whose row address this lane gives
+        const uint32_t row = 8 * (m >> 1) + (lane & 7);
+        const uint32_t from = (dv0 / 64) * kPanel + row * 128 + ((((dv0 % 64) / 8 + (m & 1)) ^ (lane & 7)) << 4);
+        const uint32_t to = tmem + (static_cast<uint32_t>(dv0) << 16) + SCOL_VT;
+        float2 f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int s = 8 * j + 2 * (lane & 3);
+            f[j] = make_float2(expf(g * static_cast<float>(C - 1 - s)), expf(g * static_cast<float>(C - 2 - s)));
+        }
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kStateStages, vb = i & 1;
+            const float x = expf(g * static_cast<float>((nch - 1 - i) * C));
+            const float2 end = make_float2(x, x);
             if (!warp_wait(&bar[SB_FULL + st], (i / kStateStages) & 1)) { ok = false; break; }
             if (!warp_wait(&bar[SB_VTFREE + vb], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
-            convert_v<D, kTile, 256, 2>(smem_addr(smem + SOFF_K + st * kTile), smem_addr(smem + SOFF_V + st * kTile),
-                              smem_addr(smem + SOFF_VT + vb * 3 * kTile), tab,
-                              expf(g * static_cast<float>((nch - 1 - i) * C)), C, threadIdx.x);
-            tc::fence_proxy_async_smem();
+            tc::fence_after_sync();
+            if (live) {
+                const uint32_t tile = smem_addr(smem + SOFF_V + st * kTile) + from;
+                uint32_t v[16], hi[16], mid[16], lo[16];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)  // 16 tokens each
+                    ldmatrix_x4_trans(tile + j * 2048, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    split3(__fmul2_rn(unpack_bf16(v[j]), __fmul2_rn(f[j / 2], end)), hi[j], mid[j], lo[j]);
+                tc::tmem_st16x128b_x8(to + (vb * 3) * (C / 2), hi);
+                tc::tmem_st16x128b_x8(to + (vb * 3 + 1) * (C / 2), mid);
+                tc::tmem_st16x128b_x8(to + (vb * 3 + 2) * (C / 2), lo);
+                tc::tmem_wait_st();
+            }
+            tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[SB_VT + vb]);
         }
@@ -948,7 +1007,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 8) tc::tmem_dealloc(tmem, 128);
+    if (warp == 8) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
 // The states at the ends of the ranges, from the ranges' own: bounds[x] <-
