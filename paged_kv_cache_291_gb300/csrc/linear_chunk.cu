@@ -43,36 +43,32 @@ constexpr int C = 64;                    // tokens per chunk
 constexpr int kPanel = C * 128;          // [64 tokens][64 dims] bf16, 128-byte swizzle
 constexpr int kPTile = C * 128;          // one term of P, [64 s][64 t] bf16
 
-// Rings, shared memory and tensor memory of the main kernel.  Both widths
-// are short of one kind.
-//  * head_dim 128 is bound by shared-memory traffic, and V~ is a third of it:
-//    its first two terms go to tensor memory.  The columns for them come from
-//    the outputs: the state's part is scaled in place, and V P added to it.
-//  * head_dim 64 has no columns for V~ beside three sums of V P: P's terms go
-//    side by side in one MMA of N = 192, which reads V once (a ragged batch of
-//    12 prompts, 32/8 heads: 49.5 to 39 us).
+// Ring depths and the shared-memory map of the main kernel.
 template <int D>
 struct Layout {
-    static constexpr bool kWide = D == 128;
     static constexpr int kTile = D / 64 * kPanel;     // a K, V or Q tile, or one term of V~
-    static constexpr int kKv = kWide ? 3 : 4;         // K and V stages
-    static constexpr int kQ = kWide ? 3 : 4;          // Q stages
+    static constexpr int kKv = D == 64 ? 4 : 3;       // K and V stages
+    static constexpr int kQ = D == 64 ? 4 : 2;        // Q stages
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = OFF_K + kKv * kTile;
     static constexpr int OFF_Q = OFF_V + kKv * kTile;
-    static constexpr int OFF_VT = OFF_Q + kQ * kTile; // V~: the last term, or all three
-    static constexpr int OFF_P = OFF_VT + (kWide ? 1 : 3) * kTile;  // two buffers of three terms
+    static constexpr int OFF_VT = OFF_Q + kQ * kTile;
+    static constexpr int OFF_P = OFF_VT + 3 * kTile;  // two buffers of three terms
     static constexpr int OFF_REST = OFF_P + 2 * 3 * kPTile;
-    static constexpr int kSums = kWide ? 1 : 3;       // of V P
+    // TMEM columns: scores, S, its three terms, the two parts of the outputs.
+    // V P takes P's terms one after the other into one sum at head_dim 128; at
+    // 64 there are columns for three sums, so they go side by side in one MMA
+    // of N = 192, which reads V once (a ragged batch of 12 prompts, 32/8
+    // heads: 49.5 to 39 us).
+    static constexpr int kSums = D == 64 ? 3 : 1;
     static constexpr uint32_t COL_SCORES = 0, COL_S = C, COL_SB = COL_S + D, COL_OS = COL_SB + 3 * D / 2,
-                              COL_OP = kWide ? COL_OS : COL_OS + C, COL_VT = COL_OS + C;
-    static_assert(kWide ? COL_VT + C <= 512 : COL_OP + kSums * C <= 512, "TMEM columns");
+                              COL_OP = COL_OS + C;
+    static_assert(COL_OP + kSums * C <= 512, "TMEM columns");
 };
 constexpr int TAB_P = 0;                              // float[128]: scale lam^(t-s) at 63 + t - s
 constexpr int TAB_O = 128;                            // float[64]: scale lam^(t+1)
 constexpr int TAB_V = 192;                            // float[64]: lam^j
 constexpr int TAB_LAM = 256;                          // float2: lam^64
-constexpr int TAB_R = 260;                            // float[128]: lam^(63-s), then zeros
 constexpr int kBadBuffers = 3;
 
 enum {
@@ -86,19 +82,19 @@ enum {
     B_PFREE = B_P + 2,          // + buffer: P read
     B_S = B_PFREE + 2,          // S split and decayed (8 arrivals)
     B_SFREE,                    // the split S read by every q head of the chunk
-    B_VT,                       // V~ made (4 arrivals; 8 at head_dim 128)
+    B_VT,                       // V~ in shared memory (4 arrivals)
     B_VTFREE,                   // V~ read, S holds the chunk
     B_OS,                       // the state's part of the outputs in TMEM
-    B_OSFREE,                   // and read, or scaled (8 arrivals)
+    B_OSFREE,                   // and read (8 arrivals)
     B_OP,                       // the scores' part
-    B_OPFREE,                   // and read (8 arrivals)
+    B_OPFREE,
     NBAR
 };
 enum { I_SEGS = 0, I_CHUNKS, I_BAD, I_COUNT };
 
 // What follows the tiles.
 struct Rest {
-    alignas(16) float tab[388];
+    alignas(16) float tab[260];
     int bad_rows[kBadBuffers][128];  // see where V~ is made
     uint64_t bar[NBAR];
     int info[I_COUNT];
@@ -116,7 +112,7 @@ static_assert(2 * smem_bytes<64>() > 228 * 1024, "the 512-column TMEM allocation
 constexpr int kThreads = 768;
 constexpr int kLoadWarp = 2, kMmaWarp = 3;
 // P: warps 0 (s 0-31, t 0-31), 4 (s 0-31, t 32-63) and 1 (s 32-63, t 32-63)
-// V~: warps 2 (which also loads), 5, 6 and 7; at head_dim 128 the S warps
+// V~: warps 2 (which also loads), 5, 6 and 7
 constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 
 constexpr uint32_t kTmemCols = 512;
@@ -270,19 +266,20 @@ __device__ __forceinline__ float convert_v(uint32_t sk, uint32_t sv, uint32_t sv
     return acc.x + acc.y;
 }
 
-// Four 8x8 tiles of 16-bit elements, transposed: thread t holds row t/4,
-// columns 2 (t%4) and + 1 of each.  Lanes 8m .. 8m + 7 give tile m's rows.
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
-                 : "r"(saddr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b),
-                 "r"(c), "r"(d)
-                 : "memory");
+// S^T += (V~)^T K for one chunk, V~ in three terms: A is V~ stored [s][v]
+// (v contiguous), B is K stored [s][k] (k contiguous).
+template <int D, int TERM>
+__device__ __forceinline__ void mma_state(uint32_t col_s, uint32_t svt, uint32_t sk, bool accumulate) {
+    constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 1, 1);
+    const uint64_t b = tc::smem_desc_sw128(sk, kPanel, 1024);
+#pragma unroll 1
+    for (int part = 2; part >= 0; --part) {  // smallest first: the sums truncate
+        const uint64_t a = tc::smem_desc_sw128(svt + part * TERM, kPanel, 1024);
+#pragma unroll
+        for (int k = 0; k < C / 16; ++k)
+            tc::mma_bf16_ss(col_s, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc,
+                            accumulate || part < 2 || k > 0 ? 1u : 0u);
+    }
 }
 
 // G: q heads per CTA.
@@ -316,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NBAR; ++i)
             mbar_init(&bar[i], i == B_SCFREE || i == B_P || i == B_P + 1 ? 3u
                                 : i == B_S                                ? static_cast<uint32_t>(kSWarps)
-                                : i == B_VT                               ? static_cast<uint32_t>(L::kWide ? kSWarps : kVWarps)
+                                : i == B_VT                               ? static_cast<uint32_t>(kVWarps)
                                 : i == B_OSFREE || i == B_OPFREE          ? static_cast<uint32_t>(kOWarps)
                                                                           : 1u);
         fence_mbar_init();
@@ -384,8 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = 32 * (warp - kSWarp - 1) + lane;
         const float x = expf(g * static_cast<float>(j));
         tab[TAB_V + j] = x;
-        tab[TAB_R + 63 - j] = x;
-        tab[TAB_R + 64 + j] = 0.f;
         tab[TAB_P + 63 + j] = A.scale * x;
         if (j < 63) tab[TAB_P + j] = 0.f;
         tab[TAB_O + j] = A.scale * expf(g * static_cast<float>(j + 1));
@@ -444,31 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < C / 16; ++k)
                     tc::mma_bf16_ss(tmem + L::COL_OP, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdescOP,
-                                    L::kWide || part < 3 - L::kSums || k > 0 ? 1u : 0u);
+                                    part < 3 - L::kSums || k > 0 ? 1u : 0u);
             }
             if (n % G == G - 1) tc::mma_commit(&bar[B_KVEMPTY + n / G % kKv]);
             tc::mma_commit(&bar[B_PFREE + (n & 1)]);
             tc::mma_commit(&bar[B_OP]);  // last: once it is seen, nothing of this thread is in flight
-        };
-        // S^T += (V~)^T K, V~ in three terms
-        auto update = [&](int i) {
-            const uint64_t b = tc::smem_desc_sw128(sk0 + (i % kKv) * kTile, kPanel, 1024);
-#pragma unroll 1
-            for (int part = 2; part >= 0; --part) {  // smallest first: the sums truncate
-                if (L::kWide && part < 2) {
-                    constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 0, 1);
-                    const uint32_t a = tmem + L::COL_VT + part * (C / 2);
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        tc::mma_bf16_ts(tmem + L::COL_S, a + 8 * k, b + k * (2048 >> 4), kIdesc, 1u);
-                } else {
-                    constexpr uint32_t kIdesc = tc::idesc_bf16_f32(128, D, 1, 1);
-                    const uint64_t a = tc::smem_desc_sw128(svt + (L::kWide ? 0 : part * kTile), kPanel, 1024);
-#pragma unroll
-                    for (int k = 0; k < C / 16; ++k)
-                        tc::mma_bf16_ss(tmem + L::COL_S, a + k * (2048 >> 4), b + k * (2048 >> 4), kIdesc, 1u);
-                }
-            }
         };
         if (nitems > 0) {
             ok = warp_wait(&bar[B_KVFULL], 0) && warp_wait(&bar[B_QFULL], 0);
@@ -478,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int n = 0; n < nitems && ok; ++n) {
             const int i = n / G, g = n % G;
             if (g == 0 && !warp_wait(&bar[B_S], i & 1)) { ok = false; break; }
-            if (n > 0 && !warp_wait(&bar[L::kWide ? B_OPFREE : B_OSFREE], (n - 1) & 1)) { ok = false; break; }
+            if (n > 0 && !warp_wait(&bar[B_OSFREE], (n - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) {
                 out_state(n);
@@ -488,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (g == 0) {
                 if (!warp_wait(&bar[B_VT], i & 1)) { ok = false; break; }
                 if (tc::elect_one()) {
-                    update(i);
+                    mma_state<D, kTile>(tmem + L::COL_S, svt, sk0 + (i % kKv) * kTile, true);
                     tc::mma_commit(&bar[B_VTFREE]);
                 }
                 __syncwarp();
@@ -506,10 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             if (!warp_wait(&bar[B_P + (n & 1)], (n >> 1) & 1)) { ok = false; break; }
-            if (L::kWide ? !warp_wait(&bar[B_OSFREE], n & 1) : n > 0 && !warp_wait(&bar[B_OPFREE], (n - 1) & 1)) {
-                ok = false;
-                break;
-            }
+            if (n > 0 && !warp_wait(&bar[B_OPFREE], (n - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (tc::elect_one()) out_scores(n);
             __syncwarp();
@@ -558,7 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar[B_SCFREE]);
             if (!warp_wait(&bar[B_PFREE + (n & 1)], ((n >> 1) & 1) ^ 1)) { ok = false; break; }
             const uint32_t at = prow + (n & 1) * 3 * kPTile;
-            convert(x, at, warp == 4 ? 0 : lane);
+            if (warp == 4) convert(x, at, 0);
+            else convert(x, at, lane);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_P + (n & 1)]);
@@ -593,69 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::tmem_st32x32b_x8(tb + D / 2 + 8 * b, mid);
             tc::tmem_st32x32b_x8(tb + D + 8 * b, lo);
             tc::tmem_st32x32b_x16(ts + 16 * b, x);
-        };
-        // V~ of chunk i at head_dim 128: warp w takes 16 v indices; thread t
-        // holds indices t/4 and + 8 of them, tokens 8 g + 2 (t % 4) and + 1.
-        auto transposed_v = [&](int i, int nrows) {
-            const int dv0 = 32 * w + 16 * ((warp - kSWarp) >> 2);
-            const uint32_t row = 8 * (lane >> 4) + (lane & 7);
-            const uint32_t at = (dv0 / 64) * kPanel + row * 128 +
-                                ((((dv0 % 64) / 8 + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
-            const uint32_t sv = smem_addr(smem + L::OFF_V + (i % kKv) * kTile), svt = smem_addr(smem + L::OFF_VT);
-            const uint32_t to = tmem + (static_cast<uint32_t>(dv0) << 16) + L::COL_VT;
-            const float* f = tab + TAB_R + C - nrows + 2 * (lane & 3);  // zeros for rows past the segment
-            const int mine = nrows - 2 * (lane & 3);
-            const float2 zero = make_float2(0.f, 0.f);
-            float2 acc = zero;
-            // rolled: these roles share the instruction cache, and straight-line code starves on it
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {  // 16 tokens each
-                uint32_t v[4], hi[4], mid[4], lo[4];
-                ldmatrix_x4_trans(sv + at + j * 2048, v[0], v[1], v[2], v[3]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int s = 16 * j + 8 * (e >> 1);
-                    float2 x = unpack_bf16(v[e]);
-                    if (nrows < C) {  // other sequences' tokens: whatever they hold
-                        if (s >= mine) x.x = 0.f;
-                        if (s + 1 >= mine) x.y = 0.f;
-                    }
-                    acc = __ffma2_rn(x, zero, acc);
-                    split3(__fmul2_rn(x, make_float2(f[s], f[s + 1])), hi[e], mid[e], lo[e]);
-                }
-                tc::tmem_st16x128b_x2(to + 8 * j, hi);
-                tc::tmem_st16x128b_x2(to + C / 2 + 8 * j, mid);
-                stmatrix_x4_trans(svt + at + j * 2048, lo[0], lo[1], lo[2], lo[3]);
-            }
-            if (nrows < C) {
-                // those rows leave K and V too: a zero factor times a NaN would poison the products
-                const uint32_t sk = smem_addr(smem + L::OFF_K + (i % kKv) * kTile);
-                for (int c = threadIdx.x - 32 * kSWarp; c < kTile / 16; c += 32 * kSWarps) {
-                    if (((c >> 3) & (C - 1)) < nrows) continue;
-                    tc::sts128(sk + c * 16, 0u, 0u, 0u, 0u);
-                    tc::sts128(sv + c * 16, 0u, 0u, 0u, 0u);
-                }
-            }
-            if (acc.x + acc.y != 0.f) {
-                // A value that is not finite reaches the outputs of its column
-                // from its row on, and no earlier row: it leaves V for V P (V~
-                // carries it into the state), and its row is noted.
-                for (int e = 0; e < 32; ++e) {
-                    const int col = dv0 + (lane >> 2) + 8 * (e & 1), s = 8 * (e >> 2) + 2 * (lane & 3) + ((e >> 1) & 1);
-                    if (s >= nrows) continue;
-                    const uint32_t a = sv + (col / 64) * kPanel + s * 128 + ((((col % 64) / 8) ^ (s & 7)) << 4) + (col % 8) * 2;
-                    uint16_t u;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(a) : "memory");
-                    if ((u & 0x7f80u) != 0x7f80u) continue;
-                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(0)) : "memory");
-                    atomicMax(&rest.bad_rows[i % kBadBuffers][col], ((i + 1) << 6) | (C - 1 - s));
-                }
-            }
-            tc::tmem_wait_st();
-            tc::fence_proxy_async_smem();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_VT]);
         };
         int i = 0;  // chunk of the range
         for (int k = 0; k < nseg && ok; ++k) {
@@ -706,10 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_S]);
-                if constexpr (L::kWide) {
-                    if (!warp_wait(&bar[B_KVFULL + i % kKv], (i / kKv) & 1)) { ok = false; break; }
-                    transposed_v(i, min(C, left));
-                }
             }
             if (!ok || store < 0) continue;
             if (!warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
@@ -726,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == kLoadWarp || (!L::kWide && warp >= 5 && warp < 8)) {
+    } else if (warp == kLoadWarp || (warp >= 5 && warp < 8)) {
         // ------------------------------------------------------ loads and V~
         // The load warp converts its share too.  The loads that follow chunk
         // i's conversion wait for items that end before the next conversion
@@ -768,12 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (q_next % G == 0) q_at.next();
             return true;
         };
-        if constexpr (L::kWide) {
-            while (q_next < nitems && ok) {
-                if (q_next % G == 0) ok = load_kv();
-                ok = ok && load_q();
-            }
-        } else {
         if (warp == kLoadWarp) {
             ok = load_kv();
             for (int n = 0; n < kQ && ok; ++n) ok = load_q();
@@ -823,14 +723,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (warp == kLoadWarp)
             while (q_next < nitems && ok) ok = load_q();
-        }
-    } else if (warp >= kOWarp) {
+    } else {
         // ------------------------------------------------------ outputs
         // Lane = v index, column = token: a warp stores 32 consecutive floats
-        // of a row; the second four warps take tokens 32-63.  At head_dim 64 the
-        // state's part is taken into registers as soon as it is there, so that
-        // the next item's can be computed; at 128 it is scaled in place and V P
-        // is added to it.
+        // of a row; the second four warps take tokens 32-63.  The state's part
+        // is taken into registers as soon as it is there, so that the next
+        // item's can be computed.
         const int w = warp & 3, dv = 32 * w + lane, t0 = warp - kOWarp < 4 ? 0 : 32;
         const bool live = 32 * w < D;
         const uint32_t tl = tmem + (static_cast<uint32_t>(32 * w) << 16) + t0;
@@ -847,11 +745,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tmem_ld32x32b_x32(tl + L::COL_OS, xs);
                 tc::tmem_wait_ld();
             }
-            if constexpr (!L::kWide) {
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[B_OSFREE]);
-            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_OSFREE]);
             // the factors here, not among the stores, which they could not be loaded past
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
@@ -860,13 +756,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 xs[j + 1] = __float_as_uint(ff.y * __uint_as_float(xs[j + 1]));
                 xs[j + 2] = __float_as_uint(ff.z * __uint_as_float(xs[j + 2]));
                 xs[j + 3] = __float_as_uint(ff.w * __uint_as_float(xs[j + 3]));
-            }
-            if constexpr (L::kWide) {
-                tc::tmem_st32x32b_x32(tl + L::COL_OS, xs);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[B_OSFREE]);
             }
             if (!warp_wait(&bar[B_OP], n & 1)) { ok = false; break; }
             tc::fence_after_sync();
@@ -878,8 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        xs[j] = L::kWide ? xp[j]
-                                         : __float_as_uint(__uint_as_float(xs[j]) + __uint_as_float(xp[j]));
+                        xs[j] = __float_as_uint(__uint_as_float(xs[j]) + __uint_as_float(xp[j]));
                 }
             }
             tc::fence_before_sync();
@@ -888,16 +776,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live) {
                 const int nrows = min(C, at.left) - t0;
                 const int mark = rest.bad_rows[i % kBadBuffers][dv];
-                const int nan_from = max(((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0, 0);
+                const int nan_from = ((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0;
                 float* o = A.out + (static_cast<int64_t>(at.row) + t0) * row_step + (hq0 + g) * D + dv;
-                const int plain = min(nrows, nan_from);
+                if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (j < plain) *o = __uint_as_float(xs[j]);
-                    o = walk(o, row_bytes);
+                    for (int j = 0; j < 32; ++j) {
+                        *o = __uint_as_float(xs[j]);
+                        o = walk(o, row_bytes);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float y = __uint_as_float(xs[j]);
+                        if (j >= nan_from) y = __int_as_float(0x7fffffff);
+                        if (j < nrows) *o = y;
+                        o = walk(o, row_bytes);
+                    }
                 }
-                for (int j = plain; j < min(nrows, 32); ++j)  // behind a value that is not finite
-                    o[(j - 32) * row_step] = __int_as_float(0x7fffffff);
             }
             if (g == G - 1) at.next();
         }
@@ -953,6 +848,13 @@ constexpr int STATE_SMEM = SOFF_TMEM + 16 + 1024;
 static_assert(STATE_SMEM <= 232448, "shared memory budget (227 KB)");
 static_assert(2 * STATE_SMEM > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
 constexpr uint32_t SCOL_VT = 128;        // V~: two buffers of three terms of 32 columns
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+                 : "r"(saddr)
+                 : "memory");
+}
 
 template <int D>
 __global__ void __launch_bounds__(kStateThreads, 1)

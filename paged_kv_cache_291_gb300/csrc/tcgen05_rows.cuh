@@ -59,15 +59,6 @@ __device__ __forceinline__ void tmem_st32x32b_x8(uint32_t taddr, const uint32_t 
         : "memory");
 }
 
-// 16 lanes x 4 columns per repetition, 2 repetitions (8 columns): thread t
-// writes, for repetition g, r[2g] to lane (taddr.lane + t/4) and r[2g+1] to
-// lane (taddr.lane + t/4 + 8), both at column 4g + t%4.
-__device__ __forceinline__ void tmem_st16x128b_x2(uint32_t taddr, const uint32_t (&r)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
-                 : "memory");
-}
-
 // One lane of a converged warp (the same one every time), in a form the
 // compiler knows to leave one lane: what it issues then takes its operands
 // from uniform registers directly.
