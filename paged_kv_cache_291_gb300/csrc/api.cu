@@ -880,7 +880,7 @@ PKV_API pkv_status pkv_linear_decode_attention(const pkv_states_t* states, const
     if ((st = fill_linear(states, q, q_stride, num_q_heads, k, k_stride, v, v_stride, state_slots, new_slots,
                           context_lens, num_seqs, num_seqs, scale, out, &a, &dev)) != PKV_OK)
         return st;
-    cudaError_t e = pkv::launch_linear_recurrent(a, 1, static_cast<cudaStream_t>(stream));
+    cudaError_t e = pkv::launch_linear_recurrent(a, 1, pkv::LinearScan{}, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
@@ -923,9 +923,7 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
     const pkv::LinearPlan plan = pkv::plan_linear(query_start_loc_host, num_seqs, num_tokens, a.num_kv_heads,
                                                   num_q_heads / a.num_kv_heads, a.head_dim, dev->num_sms,
                                                   a.max_recurrent);
-    cudaError_t e = cudaSuccess;
-    if (plan.recurrent > 0) e = pkv::launch_linear_recurrent(a, plan.recurrent, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = pkv::launch_linear_chunks(a, plan, workspace, dev->num_sms, static_cast<cudaStream_t>(stream));
+    cudaError_t e = pkv::launch_linear_prefill(a, plan, workspace, dev->num_sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 

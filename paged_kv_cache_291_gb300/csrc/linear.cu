@@ -23,7 +23,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = kScanThreads;
 constexpr int kCols = 32;                       // columns of S per CTA
 constexpr int kRowLanes = kThreads / (kCols / 4);  // 16 threads share a column quad
 constexpr int kWarps = kThreads / 32;
@@ -32,17 +32,24 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t u) { return __uint_as_floa
 
 // TT: tokens staged at a time.
 template <int D, int G, int TT>
-__global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const LinearArgs A) {
+__global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const LinearArgs A, const LinearScan scan) {
     constexpr int RPT = D / kRowLanes;          // rows of S per thread
     constexpr int SLICES = D / kCols;
-    __shared__ float sk[TT][D], sv[TT][kCols], sq[TT][G][D];
-    __shared__ float red[TT][kWarps][G][kCols];
+    // sv and red are read and written as float4
+    __shared__ __align__(16) float sk[TT][D], sv[TT][kCols], sq[TT][G][D];
+    __shared__ __align__(16) float red[TT][kWarps][G][kCols];
     __shared__ float2 lam_s;
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int slice = blockIdx.x % SLICES;
-    const int h = blockIdx.x / SLICES % A.num_kv_heads;
-    const int s = blockIdx.x / SLICES / A.num_kv_heads;
+    if (blockIdx.x < static_cast<unsigned>(scan.blocks)) {
+        griddep_wait();
+        scan_ranges(A, scan, blockIdx.x);
+        return;
+    }
+    const int unit = blockIdx.x - scan.blocks;
+    const int slice = unit % SLICES;
+    const int h = unit / SLICES % A.num_kv_heads;
+    const int s = unit / SLICES / A.num_kv_heads;
     const int col = (tid % 8) * 4;              // within the slice
     const int r0 = tid / 8;
     griddep_wait();
@@ -144,27 +151,27 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
 }
 
 template <int D, int G>
-cudaError_t launch(const LinearArgs& a, int32_t longest, cudaStream_t stream) {
-    const int64_t grid = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * (D / kCols);
+cudaError_t launch(const LinearArgs& a, int32_t longest, const LinearScan& scan, cudaStream_t stream) {
+    const int64_t grid = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * (D / kCols) + scan.blocks;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
     auto kernel = longest <= 1 ? linear_recurrent_kernel<D, G, 1> : linear_recurrent_kernel<D, G, 4>;
-    return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a);
+    return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a, scan);
 }
 
 template <int D>
-cudaError_t launch_groups(const LinearArgs& a, int32_t longest, cudaStream_t stream) {
+cudaError_t launch_groups(const LinearArgs& a, int32_t longest, const LinearScan& scan, cudaStream_t stream) {
     switch (a.num_q_heads / a.num_kv_heads) {
-        case 1: return launch<D, 1>(a, longest, stream);
-        case 2: return launch<D, 2>(a, longest, stream);
-        case 4: return launch<D, 4>(a, longest, stream);
-        default: return launch<D, 8>(a, longest, stream);
+        case 1: return launch<D, 1>(a, longest, scan, stream);
+        case 2: return launch<D, 2>(a, longest, scan, stream);
+        case 4: return launch<D, 4>(a, longest, scan, stream);
+        default: return launch<D, 8>(a, longest, scan, stream);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, cudaStream_t stream) {
-    return a.head_dim == 64 ? launch_groups<64>(a, longest, stream) : launch_groups<128>(a, longest, stream);
+cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, const LinearScan& scan, cudaStream_t stream) {
+    return a.head_dim == 64 ? launch_groups<64>(a, longest, scan, stream) : launch_groups<128>(a, longest, scan, stream);
 }
 
 }  // namespace pkv

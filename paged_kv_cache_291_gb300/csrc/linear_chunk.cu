@@ -39,7 +39,7 @@
 namespace pkv {
 namespace {
 
-constexpr int C = 64;                    // tokens per chunk
+constexpr int C = kLinearChunk;          // tokens per chunk
 constexpr int kPanel = C * 128;          // [64 tokens][64 dims] bf16, 128-byte swizzle
 constexpr int kPTile = C * 128;          // one term of P, [64 s][64 t] bf16
 
@@ -194,10 +194,6 @@ struct Cursor {
     }
 };
 
-// Two fp32 values as three packed bf16 pairs that sum to them exactly: each
-// term is what is left, rounded to nearest.  The low half is widened by a
-// multiply: shifts, masks and packs share a pipe of half the rate, which these
-// conversions fill.
 __device__ __forceinline__ uint32_t pack_bf16(float2 x) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
@@ -210,12 +206,28 @@ __device__ __forceinline__ float2 unpack_bf16(uint32_t u) {
     return make_float2(__uint_as_float(lo), __uint_as_float(u & 0xffff0000u));
 }
 
+// x - h for the two bf16 of h, exactly: one mixed-precision fma each, which
+// takes a half of the pair as it is.  Shifts, masks and packs share a pipe of
+// half the rate, and these conversions fill it.
+__device__ __forceinline__ float2 less_bf16(float2 x, uint32_t h) {
+    float2 r;
+    asm("{\n\t.reg .b16 lo, hi, m;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "mov.b16 m, 0xBF80;\n\t"  // -1
+        "fma.rn.f32.bf16 %0, lo, m, %3;\n\t"
+        "fma.rn.f32.bf16 %1, hi, m, %4;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(h), "f"(x.x), "f"(x.y));
+    return r;
+}
+
+// Two fp32 values as three packed bf16 pairs that sum to them exactly: each
+// term is what is left, rounded to nearest.
 __device__ __forceinline__ void split3(float2 x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    const float2 minus = make_float2(-1.f, -1.f);
     hi = pack_bf16(x);
-    x = __ffma2_rn(unpack_bf16(hi), minus, x);
+    x = less_bf16(x, hi);
     mid = pack_bf16(x);
-    lo = pack_bf16(__ffma2_rn(unpack_bf16(mid), minus, x));
+    lo = pack_bf16(less_bf16(x, mid));
 }
 
 // The next row's address, computed where it is used (32 hoisted ones would
@@ -530,8 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bar[B_SCFREE]);
             if (!warp_wait(&bar[B_PFREE + (n & 1)], ((n >> 1) & 1) ^ 1)) { ok = false; break; }
             const uint32_t at = prow + (n & 1) * 3 * kPTile;
-            if (warp == 4) convert(x, at, 0);
-            else convert(x, at, lane);
+            convert(x, at, warp == 4 ? 0 : lane);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar[B_P + (n & 1)]);
@@ -690,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (warp == kLoadWarp && i > 0)
                 while (q_next <= (i - 1) * G + kQ && q_next < nitems && ok) ok = load_q();
             const uint32_t sk = smem_addr(smem + L::OFF_K + st * kTile), sv = smem_addr(smem + L::OFF_V + st * kTile);
-            const float acc = convert_v<D, kTile, 32 * kVWarps, 2>(sk, sv, smem_addr(smem + L::OFF_VT), tab + TAB_V,
+            const float acc = convert_v<D, kTile, 32 * kVWarps, 4>(sk, sv, smem_addr(smem + L::OFF_VT), tab + TAB_V,
                                                                      nrows, tid);
             if (acc != 0.f) {
                 // A value that is not finite reaches the outputs of its column
@@ -776,23 +787,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live) {
                 const int nrows = min(C, at.left) - t0;
                 const int mark = rest.bad_rows[i % kBadBuffers][dv];
-                const int nan_from = ((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0;
+                const int nan_from = max(((mark >> 6) == i + 1 ? C - 1 - (mark & (C - 1)) : C) - t0, 0);
                 float* o = A.out + (static_cast<int64_t>(at.row) + t0) * row_step + (hq0 + g) * D + dv;
-                if (nrows >= 32 && __all_sync(0xffffffffu, nan_from >= 32)) {
+                const int plain = min(nrows, nan_from);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        *o = __uint_as_float(xs[j]);
-                        o = walk(o, row_bytes);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float y = __uint_as_float(xs[j]);
-                        if (j >= nan_from) y = __int_as_float(0x7fffffff);
-                        if (j < nrows) *o = y;
-                        o = walk(o, row_bytes);
-                    }
+                for (int j = 0; j < 32; ++j) {
+                    if (j < plain) *o = __uint_as_float(xs[j]);
+                    o = walk(o, row_bytes);
                 }
+                for (int j = plain; j < min(nrows, 32); ++j)  // behind a value that is not finite
+                    o[(j - 32) * row_step] = __int_as_float(0x7fffffff);
             }
             if (g == G - 1) at.next();
         }
@@ -1010,61 +1014,10 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     if (warp == 8) tc::tmem_dealloc(tmem, kTmemCols);
 }
 
-// The states at the ends of the ranges, from the ranges' own: bounds[x] <-
-// lam^(tokens of the segment) (state before it) + bounds[x], in order, the
-// state before being the sequence's where the segment begins it and
-// bounds[x - 1] otherwise.  Grid (d^2 / 512, Hkv); a thread carries two
-// elements.
-__global__ void __launch_bounds__(256) linear_scan_kernel(const ChunkParams P) {
+__global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearArgs A, const LinearScan S) {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ float2 lam_s;
-    const LinearArgs& A = P.A;
-    const int h = blockIdx.y;
-    const float g = clean_log_decay(A, h, false);
-    if (threadIdx.x == 0) lam_s = decay_pair(g, P.range * C);
-    const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
-    const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 2;
-    float* p = P.bounds + h * head + e;
-    const int64_t step = static_cast<int64_t>(A.num_kv_heads) * head;
-    __syncthreads();
-    const float2 lam = lam_s;
-    float2 x = make_float2(0.f, 0.f);
-    // Loads of several ranges together: they hang on nothing but the list.
-    constexpr int kBatch = 8;
-    for (int r0 = 0; r0 < P.ranges - 1; r0 += kBatch) {
-        int4 tail[kBatch];
-        float2 y[kBatch], before[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            tail[j] = make_int4(0, 0, 0, -1);
-            y[j] = make_float2(0.f, 0.f);
-            if (r0 + j < P.ranges - 1) {
-                tail[j] = P.tails[r0 + j];
-                y[j] = *reinterpret_cast<const float2*>(p + (r0 + j) * step);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            before[j] = make_float2(0.f, 0.f);
-            if (tail[j].x > 0 && tail[j].y && tail[j].w >= 0)
-                before[j] = *reinterpret_cast<const float2*>(
-                    A.states + (static_cast<int64_t>(tail[j].w) * A.num_kv_heads + h) * head + e);
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (tail[j].x <= 0) continue;
-            float2 f = lam;
-            if (tail[j].y) {
-                // a sequence's first segment: its length is its own, its factor applied once
-                f = make_float2(expf(g * static_cast<float>(tail[j].x * C)), 0.f);
-                x = before[j];
-            }
-            x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y[j].x));
-            x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y[j].y));
-            *reinterpret_cast<float2*>(p + (r0 + j) * step) = x;
-        }
-    }
+    scan_ranges(A, S, blockIdx.x);
 }
 
 bool rows_map(CUtensorMap* map, const void* base, int64_t stride, int32_t heads, int32_t d, int32_t tokens) {
@@ -1096,18 +1049,17 @@ cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUte
 }
 
 template <int D>
-cudaError_t launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
-                       bool cut, cudaStream_t stream) {
-    if (cut) {
-        static bool done[64] = {};
-        cudaError_t e = configure(linear_state_kernel<D>, STATE_SMEM, done);
-        if (e != cudaSuccess) return e;
-        e = launch_overlapped(linear_state_kernel<D>, dim3(P.ranges - 1, P.A.num_kv_heads), dim3(kStateThreads),
-                              STATE_SMEM, stream, tk, tv, P);
-        if (e != cudaSuccess) return e;
-        e = launch_overlapped(linear_scan_kernel, dim3(D * D / 512, P.A.num_kv_heads), dim3(256), 0, stream, P);
-        if (e != cudaSuccess) return e;
-    }
+cudaError_t launch_state(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P, cudaStream_t stream) {
+    static bool done[64] = {};
+    cudaError_t e = configure(linear_state_kernel<D>, STATE_SMEM, done);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(linear_state_kernel<D>, dim3(P.ranges - 1, P.A.num_kv_heads), dim3(kStateThreads),
+                             STATE_SMEM, stream, tk, tv, P);
+}
+
+template <int D>
+cudaError_t launch_groups(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
+                          cudaStream_t stream) {
     switch (P.A.num_q_heads / P.A.num_kv_heads / P.subs) {
         case 1: return launch_main<D, 1>(tq, tk, tv, P, stream);
         case 2: return launch_main<D, 2>(tq, tk, tv, P, stream);
@@ -1189,9 +1141,10 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     return best;
 }
 
-cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, int num_sms,
-                                 cudaStream_t stream) {
-    if (plan.units == 0) return cudaSuccess;
+cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, void* workspace, int num_sms,
+                                  cudaStream_t stream) {
+    if (plan.units == 0)
+        return plan.recurrent > 0 ? launch_linear_recurrent(a, plan.recurrent, LinearScan{}, stream) : cudaSuccess;
     CUtensorMap tq, tk, tv;
     if (!rows_map(&tq, a.q, a.q_stride, a.num_q_heads, a.head_dim, a.num_tokens) ||
         !rows_map(&tk, a.k, a.k_stride, a.num_kv_heads, a.head_dim, a.num_tokens) ||
@@ -1210,8 +1163,21 @@ cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, vo
     P.range = plan.range;
     P.units = plan.units;
     P.subs = plan.subs;
-    return a.head_dim == 64 ? launch_all<64>(tq, tk, tv, P, plan.cut, stream)
-                            : launch_all<128>(tq, tk, tv, P, plan.cut, stream);
+    LinearScan scan = {};
+    cudaError_t e = cudaSuccess;
+    if (plan.cut) {
+        e = a.head_dim == 64 ? launch_state<64>(tk, tv, P, stream) : launch_state<128>(tk, tv, P, stream);
+        if (e != cudaSuccess) return e;
+        scan = {P.bounds, P.tails, P.ranges, P.range * C,
+                a.num_kv_heads * (a.head_dim * a.head_dim / (2 * kScanThreads))};
+    }
+    // The scan rides in the recurrent form's grid where there is one.
+    if (plan.recurrent > 0)
+        e = launch_linear_recurrent(a, plan.recurrent, scan, stream);
+    else if (plan.cut)
+        e = launch_overlapped(linear_scan_kernel, dim3(scan.blocks), dim3(kScanThreads), 0, stream, a, scan);
+    if (e != cudaSuccess) return e;
+    return a.head_dim == 64 ? launch_groups<64>(tq, tk, tv, P, stream) : launch_groups<128>(tq, tk, tv, P, stream);
 }
 
 }  // namespace pkv

@@ -115,4 +115,62 @@ __device__ __forceinline__ float2 decay_pair(float g, int tokens) {
     return make_float2(hi * scale, lo * scale);
 }
 
+constexpr int kScanThreads = 128;
+constexpr int kLinearChunk = 64;  // tokens of a chunk
+
+// The states at the ends of the ranges, from the ranges' own: bounds[x] <-
+// lam^(tokens of the segment) (state before it) + bounds[x], in order, the
+// state before being the sequence's where the segment begins it and
+// bounds[x - 1] otherwise.  Block `block` of S.blocks; a thread carries two
+// elements.
+__device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearScan& S, int block) {
+    __shared__ float2 lam_s;
+    const int slices = A.head_dim * A.head_dim / (2 * kScanThreads);
+    const int h = block / slices;
+    const float g = clean_log_decay(A, h, false);
+    if (threadIdx.x == 0) lam_s = decay_pair(g, S.tokens);
+    const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
+    const int64_t e = (static_cast<int64_t>(block % slices) * kScanThreads + threadIdx.x) * 2;
+    float* p = S.bounds + h * head + e;
+    const int64_t step = static_cast<int64_t>(A.num_kv_heads) * head;
+    __syncthreads();
+    const float2 lam = lam_s;
+    float2 x = make_float2(0.f, 0.f);
+    // Loads of several ranges together: they hang on nothing but the list.
+    constexpr int kBatch = 8;
+    for (int r0 = 0; r0 < S.ranges - 1; r0 += kBatch) {
+        int4 tail[kBatch];
+        float2 y[kBatch], before[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            tail[j] = make_int4(0, 0, 0, -1);
+            y[j] = make_float2(0.f, 0.f);
+            if (r0 + j < S.ranges - 1) {
+                tail[j] = S.tails[r0 + j];
+                y[j] = *reinterpret_cast<const float2*>(p + (r0 + j) * step);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            before[j] = make_float2(0.f, 0.f);
+            if (tail[j].x > 0 && tail[j].y && tail[j].w >= 0)
+                before[j] = *reinterpret_cast<const float2*>(
+                    A.states + (static_cast<int64_t>(tail[j].w) * A.num_kv_heads + h) * head + e);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (tail[j].x <= 0) continue;
+            float2 f = lam;
+            if (tail[j].y) {
+                // a sequence's first segment: its length is its own, its factor applied once
+                f = make_float2(expf(g * static_cast<float>(tail[j].x * kLinearChunk)), 0.f);
+                x = before[j];
+            }
+            x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y[j].x));
+            x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y[j].y));
+            *reinterpret_cast<float2*>(p + (r0 + j) * step) = x;
+        }
+    }
+}
+
 }  // namespace pkv

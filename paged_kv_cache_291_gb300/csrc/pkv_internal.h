@@ -179,8 +179,18 @@ struct LinearArgs {
     float scale;
 };
 
-// longest: rows of the longest sequence it will meet.
-cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, cudaStream_t stream);
+// The join of the chunked form's ranges (linear_device.cuh).
+struct LinearScan {
+    float* bounds;
+    const int4* tails;
+    int32_t ranges;
+    int32_t tokens;      // of a whole range
+    int32_t blocks;      // 0: nothing to join
+};
+
+// longest: rows of the longest sequence it will meet; scan.blocks more CTAs
+// join the ranges.
+cudaError_t launch_linear_recurrent(const LinearArgs& a, int32_t longest, const LinearScan& scan, cudaStream_t stream);
 
 // Rows up to which the recurrent form is the faster one.  It reads and writes
 // the state at the full rate and then pays for each token and q head; the
@@ -204,8 +214,8 @@ size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_
 LinearPlan plan_linear(const int32_t* query_start_loc_host, int32_t num_seqs, int32_t num_tokens,
                        int32_t num_kv_heads, int32_t group, int32_t head_dim, int num_sms, int32_t max_recurrent);
 
-cudaError_t launch_linear_chunks(const LinearArgs& a, const LinearPlan& plan, void* workspace, int num_sms,
-                                 cudaStream_t stream);
+cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, void* workspace, int num_sms,
+                                  cudaStream_t stream);
 
 // Block bookkeeping state (pkv_blocks_t), all device memory.
 struct BlocksArgs {
