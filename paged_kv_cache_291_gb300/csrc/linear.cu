@@ -30,8 +30,10 @@ constexpr int kWarps = kThreads / 32;
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t u) { return __uint_as_float(static_cast<uint32_t>(u) << 16); }
 
-// TT: tokens staged at a time.
-template <int D, int G, int TT>
+// TT: tokens staged at a time.  SCAN: the first scan.blocks CTAs join the
+// chunked form's ranges; the decode call's kernel does without, whose
+// registers it would take.
+template <int D, int G, int TT, bool SCAN>
 __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const LinearArgs A, const LinearScan scan) {
     constexpr int RPT = D / kRowLanes;          // rows of S per thread
     constexpr int SLICES = D / kCols;
@@ -41,12 +43,15 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
     __shared__ float2 lam_s;
     griddep_launch_dependents();
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    if (blockIdx.x < static_cast<unsigned>(scan.blocks)) {
-        griddep_wait();
-        scan_ranges(A, scan, blockIdx.x);
-        return;
+    int unit = blockIdx.x;
+    if constexpr (SCAN) {
+        if (unit < scan.blocks) {
+            griddep_wait();
+            scan_ranges(A, scan, unit);
+            return;
+        }
+        unit -= scan.blocks;
     }
-    const int unit = blockIdx.x - scan.blocks;
     const int slice = unit % SLICES;
     const int h = unit / SLICES % A.num_kv_heads;
     const int s = unit / SLICES / A.num_kv_heads;
@@ -154,7 +159,10 @@ template <int D, int G>
 cudaError_t launch(const LinearArgs& a, int32_t longest, const LinearScan& scan, cudaStream_t stream) {
     const int64_t grid = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads * (D / kCols) + scan.blocks;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    auto kernel = longest <= 1 ? linear_recurrent_kernel<D, G, 1> : linear_recurrent_kernel<D, G, 4>;
+    auto kernel = scan.blocks == 0 ? (longest <= 1 ? linear_recurrent_kernel<D, G, 1, false>
+                                                   : linear_recurrent_kernel<D, G, 4, false>)
+                                   : (longest <= 1 ? linear_recurrent_kernel<D, G, 1, true>
+                                                   : linear_recurrent_kernel<D, G, 4, true>);
     return launch_overlapped(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, a, scan);
 }
 
