@@ -13,7 +13,8 @@
 // one pass through shared memory.
 //
 // Bound: HBM, 8 d^2 bytes of state per (sequence, kv head) against 2 d^2
-// (1 + group) flops.
+// (1 + group) flops.  128 sequences of 40 heads of 128: 678 MB in 99.3 us,
+// 6.8 TB/s, the rate of a copy; one sequence of 16 heads 2.8 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
