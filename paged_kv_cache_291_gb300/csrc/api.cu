@@ -853,6 +853,8 @@ pkv_status fill_linear(const pkv_states_t* states, const void* q, int64_t q_stri
     a->num_seqs = num_seqs;
     a->num_tokens = num_tokens;
     a->max_recurrent = 1;
+    a->recurrent_rows = true;
+    a->chunk_rows = false;
     a->scale = scale;
     return PKV_OK;
 }
@@ -923,6 +925,8 @@ PKV_API pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, cons
     const pkv::LinearPlan plan = pkv::plan_linear(query_start_loc_host, num_seqs, num_tokens, a.num_kv_heads,
                                                   num_q_heads / a.num_kv_heads, a.head_dim, dev->num_sms,
                                                   a.max_recurrent);
+    a.recurrent_rows = plan.recurrent > 0;
+    a.chunk_rows = plan.units > 0;
     cudaError_t e = pkv::launch_linear_prefill(a, plan, workspace, dev->num_sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }

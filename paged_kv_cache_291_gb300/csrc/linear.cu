@@ -61,7 +61,11 @@ __global__ void __launch_bounds__(kThreads) linear_recurrent_kernel(const Linear
     griddep_wait();
     const bool first = h == 0 && slice == 0;
     const LinearSeq q = linear_seq(A, s, first && tid == 0);
-    if (q.rows == 0 || q.rows > A.max_recurrent) return;
+    if (q.rows == 0 || q.rows > A.max_recurrent) {
+        // rows that the host left to no kernel
+        if (q.rows > 0 && !A.chunk_rows && first && tid == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(s));
+        return;
+    }
     if (q.bad) {
         for (int i = tid; i < q.rows * G * kCols; i += kThreads) {
             const int t = i / (G * kCols), g = i / kCols % G;

@@ -39,6 +39,8 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "linear_device.cuh"
 #include "tcgen05_rows.cuh"
@@ -379,6 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             any_bad |= __any_sync(0xffffffffu, bad);
         });
         if (last && seen != P.units && lane == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(A.num_seqs));
+        if (last && !A.recurrent_rows) {
+            // rows that the host left to no kernel
+            for (int s = lane; s < A.num_seqs; s += 32) {
+                const LinearSeq q = linear_seq(A, s, true);
+                if (q.rows > 0 && q.rows <= A.max_recurrent) record_error(A.err, kErrRange, static_cast<uint32_t>(s));
+            }
+        }
         if (nseg > kMaxSegments) {
             // device lengths that are not the host's: the rest is dropped
             if (lane == 0) record_error(A.err, kErrRange, static_cast<uint32_t>(A.num_seqs));
@@ -1113,37 +1122,43 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     // reads K and V of all but the last range once more, and the states are
     // carried over.  Dealing a group's q heads to several CTAs fills SMs too,
     // and repeats the state's work in each.
+    // Whether a range may end at a unit without cutting a sequence (without
+    // the room to say so, none may: the join is then launched needlessly).
+    std::unique_ptr<uint8_t[]> begins(new (std::nothrow) uint8_t[static_cast<size_t>(units)]());
+    for (int32_t s = 0, at = 0; s < num_seqs && begins; ++s) {
+        const int32_t rows = qsl[s + 1] - qsl[s];
+        if (rows <= max_recurrent) continue;
+        begins[at] = 1;
+        at += (rows + C - 1) / C;
+    }
     const bool narrow = head_dim == 64;
     const double fixed = narrow ? 0.3 : 1.2, item = narrow ? 1.4 : 1.5, state = narrow ? 0.5 : 0.9, start = 8.0,
                  join = 11.0;
+    const int64_t least = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 1;
+    const int64_t last = most < units ? most : units;
     double best_us = 1e30;
     for (int32_t subs = 1; subs <= group; subs *= 2) {
         const int64_t heads = static_cast<int64_t>(num_kv_heads) * subs;
         const double chunk = fixed + item * (group / subs);
-        for (int64_t n = 1; n <= most && n <= units; ++n) {
-            const int64_t range = (units + n - 1) / n;
-            if ((units + range - 1) / range != n) continue;  // the same ranges as a smaller n
-            if (num_seqs > kMaxSegments && range > kMaxSegments) continue;
-            double us = (n * heads + num_sms - 1) / num_sms * (start + range * chunk);
-            if (us >= best_us) continue;
+        auto consider = [&](int64_t count) {
+            if (count < least || count > last) return;
+            const int64_t range = (units + count - 1) / count, ranges = (units + range - 1) / range;  // count or fewer
+            double us = (ranges * heads + num_sms - 1) / num_sms * (start + range * chunk);
+            if (us >= best_us) return;
             bool cut = false;  // whether a border lies inside a sequence
-            int64_t end = 0;
-            for (int32_t s = 0; s < num_seqs && !cut && n > 1; ++s) {
-                const int32_t rows = qsl[s + 1] - qsl[s];
-                if (rows <= max_recurrent) continue;
-                const int64_t first = end;
-                end += (rows + C - 1) / C;
-                cut = (first / range + 1) * range < end;
-            }
-            if (cut) us += join + ((n - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
-            if (us < best_us) {
-                best_us = us;
-                best.ranges = static_cast<int32_t>(n);
-                best.range = static_cast<int32_t>(range);
-                best.subs = subs;
-                best.cut = cut;
-            }
-        }
+            for (int64_t u = range; u < units && !cut; u += range) cut = !begins || begins[u] == 0;
+            if (cut) us += join + ((ranges - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
+            if (us >= best_us) return;
+            best_us = us;
+            best.ranges = static_cast<int32_t>(ranges);
+            best.range = static_cast<int32_t>(range);
+            best.subs = subs;
+            best.cut = cut;
+        };
+        // What fits one and two waves of CTAs, then a spread of counts.
+        consider(num_sms / heads);
+        consider(2 * num_sms / heads);
+        for (int64_t n = least; n <= last; n += 1 + n / 16) consider(n);
     }
     return best;
 }

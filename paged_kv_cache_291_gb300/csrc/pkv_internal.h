@@ -176,6 +176,7 @@ struct LinearArgs {
     unsigned long long* err;
     int32_t num_slots, num_kv_heads, num_q_heads, head_dim, num_seqs, num_tokens;
     int32_t max_recurrent;          // longest sequence the recurrent form takes
+    bool recurrent_rows, chunk_rows;// whether the host planned rows for each form
     float scale;
 };
 

@@ -446,14 +446,34 @@ def test_values_that_are_not_finite_keep_their_place(pkv, n, hq, d):
     assert np.isnan(out[t:]).all()
 
 
-def test_device_lengths_that_are_not_the_hosts_are_reported(pkv):
-    b = Batch(101, [100, 100], [0, 0], 2, 1, 64)
-    for device in ([0, 170, 200], [0, 100, 130], [0, 100, 900], [0, -5, 200]):
+@pytest.mark.parametrize("lens,devices", [
+    ([100, 100], ([0, 170, 200], [0, 100, 130], [0, 100, 900], [0, -5, 200])),
+    ([64, 64], ([0, 64, 67],)),      # the host saw no short sequence
+    ([3, 4], ([0, 3, 60],)),         # the host saw short ones only
+])
+def test_device_lengths_that_are_not_the_hosts_are_reported(pkv, lens, devices):
+    b = Batch(101, lens, [0, 0], 2, 1, 64, pad_rows=60)
+    for device in devices:
         pkv.linear_prefill_attention(*b.args(), dev_tensor(np.array(device, np.int32)), dev_tensor(b.slots),
                                      dev_tensor(b.ctx), b.scale, new_slots=dev_tensor(b.new),
                                      query_start_loc_host=b.qsl)
         st, _ = pkv.get_error()
         assert st == 9, device
+
+
+def test_calls_on_a_stream_of_the_callers(pkv):
+    """The stream argument, and torch's current stream."""
+    st = torch.cuda.Stream()
+    for explicit in (True, False):
+        a, b = Batch(108, [1] * 3, [2] * 3, 2, 1, 64), Batch(109, [90, 2], [0, 3], 2, 1, 64)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st if not explicit else torch.cuda.default_stream()):
+            kw = dict(stream=st) if explicit else {}
+            out_a, out_b = a.decode(pkv, **kw), b.prefill(pkv, **kw)
+        torch.cuda.synchronize()
+        assert pkv.get_error() == (0, 0)
+        a.check(out_a, "decode")
+        b.check(out_b, "prefill")
 
 
 def test_prefill_group_dealt_to_several_ctas_stores_the_state_once(pkv):

@@ -222,6 +222,24 @@ def test_rotary_replayed_from_a_graph_on_another_stream(pkv):
     b.check_bf16(k_out, b.k, "k")
 
 
+def test_rotary_on_a_stream_of_the_callers(pkv):
+    """The stream argument takes the same way as the call without it."""
+    b = Batch(16, 40, 4, 2, 128, 128, [64], False, False)
+    st = torch.cuda.Stream()
+    pos, f = dev_tensor(b.pos), dev_tensor(b.f)
+    pools = [torch.zeros((4, 2, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(4)]
+    slots = dev_tensor(np.arange(40, dtype=np.int32))
+    torch.cuda.synchronize()
+    q, k = pkv.rotary(b.q, b.k, pos, f, stream=st)
+    q1 = pkv.rotary_cache_write(pools[0], pools[1], b.q, b.k, b.v, slots, pos, f, stream=st)
+    torch.cuda.synchronize()
+    b.check_bf16(q, b.q, "q")
+    b.check_bf16(k, b.k, "k")
+    q2 = pkv.rotary_cache_write(pools[2], pools[3], b.q, b.k, b.v, slots, pos, f)
+    assert torch.equal(q1, q) and torch.equal(q2, q)
+    assert torch.equal(pools[0], pools[2]) and torch.equal(pools[1], pools[3])
+
+
 def test_binding_refuses_what_it_cannot_pass_on(pkv):
     b = Batch(15, 4, 4, 2, 64, 64, [32], False, False, packed=False)
     pos, f = dev_tensor(b.pos), dev_tensor(b.f)
