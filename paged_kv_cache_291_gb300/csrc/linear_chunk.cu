@@ -1132,8 +1132,7 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
         at += (rows + C - 1) / C;
     }
     const bool narrow = head_dim == 64;
-    const double fixed = narrow ? 0.3 : 1.2, item = narrow ? 1.4 : 1.5, state = narrow ? 0.5 : 0.9, start = 8.0,
-                 join = 11.0;
+    const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5;
     const int64_t least = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 1;
     const int64_t last = most < units ? most : units;
     double best_us = 1e30;
@@ -1147,7 +1146,7 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
             if (us >= best_us) return;
             bool cut = false;  // whether a border lies inside a sequence
             for (int64_t u = range; u < units && !cut; u += range) cut = !begins || begins[u] == 0;
-            if (cut) us += join + ((ranges - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
+            if (cut) us += 7.0 + 0.15 * ranges + ((ranges - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
             if (us >= best_us) return;
             best_us = us;
             best.ranges = static_cast<int32_t>(ranges);
