@@ -101,10 +101,29 @@ enum {
 };
 enum { I_SEGS = 0, I_CHUNKS, I_BAD, I_COUNT };
 
+constexpr int kMaxSegments = 128;  // of one range: ranges are at most this long when there are more sequences
+constexpr int kFromBounds = -2;
+
+struct Segment {
+    int row0, rows;   // rows <= 0: -rows rows get zeros and nothing else happens
+    int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before
+    int seq, first;   // first: holds the sequence's first row
+    int pad[2];
+};
+
+// The list's first segments are in shared memory: most lists have no more,
+// and every warp starts with a look at them.
+constexpr int kNearSegments = 4;
+struct Segments {
+    Segment *near, *far;
+    __device__ __forceinline__ Segment& operator[](int k) const { return k < kNearSegments ? near[k] : far[k]; }
+};
+
 // What follows the tiles.
 struct Rest {
     alignas(16) float tab[260];
     int bad_rows[kBadBuffers][128];  // see where V~ is made
+    Segment near[kNearSegments];
     uint64_t bar[NBAR];
     int info[I_COUNT];
     uint32_t tmem;
@@ -126,16 +145,6 @@ constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 
 constexpr uint32_t kTmemCols = 512;
 
-constexpr int kMaxSegments = 128;  // of one range: ranges are at most this long when there are more sequences
-constexpr int kFromBounds = -2;
-
-struct Segment {
-    int row0, rows;   // rows <= 0: -rows rows get zeros and nothing else happens
-    int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before
-    int seq, first;   // first: holds the sequence's first row
-    int pad[2];
-};
-
 // Work: the chunks of the sequences in order (those of more than
 // max_recurrent rows), cut into ranges of equal counts; a CTA takes one range
 // of one kv head.  A range is a list of segments, each a run of one
@@ -151,23 +160,19 @@ struct ChunkParams {
     int32_t subs;           // CTAs a kv head's group of q heads is dealt to
 };
 
-// Chunks of sequence s (0: the recurrent form takes it).
-__device__ __forceinline__ int chunks_of(const ChunkParams& P, int s) {
-    const int r0 = __ldg(P.A.query_start_loc + s), r1 = __ldg(P.A.query_start_loc + s + 1);
-    if (r0 < 0 || r1 > P.A.num_tokens || r1 - r0 <= P.A.max_recurrent) return 0;
-    return (r1 - r0 + C - 1) / C;
-}
-
-// One warp: calls f(sequence, its first unit, the unit behind its last) in
-// every lane whose sequence has units in [u0, u1), with the lanes' ballot;
-// returns the units seen (all of them when `count`).
+// One warp: calls f(sequence s, what it is, its first unit, the unit behind
+// its last, whether it has units in [u0, u1), the lanes' ballot of that) in
+// every lane; returns the units seen (all of them when `count`).  A sequence
+// is read as a whole before its units are known: one round trip, not two.
 template <typename F>
 __device__ __forceinline__ int scan_units(const ChunkParams& P, int u0, int u1, bool count, F f) {
     const unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x % 32;
     int base = 0;
     for (int s0 = 0; s0 < P.A.num_seqs && (base < u1 || count); s0 += 32) {
-        const int nc = s0 + lane < P.A.num_seqs ? chunks_of(P, s0 + lane) : 0;
+        LinearSeq q = {};
+        if (s0 + lane < P.A.num_seqs) q = linear_seq(P.A, s0 + lane, false);
+        const int nc = q.rows > P.A.max_recurrent ? (q.rows + C - 1) / C : 0;
         int incl = nc;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -176,7 +181,7 @@ __device__ __forceinline__ int scan_units(const ChunkParams& P, int u0, int u1, 
         }
         const int first = base + incl - nc, end = base + incl;
         const bool in = nc > 0 && first < u1 && end > u0;
-        f(s0 + lane, first, end, in, __ballot_sync(FULL, in));
+        f(s0 + lane, q, first, end, in, __ballot_sync(FULL, in));
         base += __shfl_sync(FULL, incl, 31);
     }
     return base;
@@ -184,11 +189,11 @@ __device__ __forceinline__ int scan_units(const ChunkParams& P, int u0, int u1, 
 
 // Walks the chunks of a range in order.
 struct Cursor {
-    const Segment* seg;
+    Segments seg;
     int k, n;
     int row, left;  // the chunk's first row, and rows left in its segment
 
-    __device__ __forceinline__ Cursor(const Segment* s, int count) : seg(s), k(-1), n(count), row(0), left(0) { open(); }
+    __device__ __forceinline__ Cursor(Segments s, int count) : seg(s), k(-1), n(count), row(0), left(0) { open(); }
     __device__ __forceinline__ void open() {
         left = 0;
         while (left <= 0 && ++k < n) {
@@ -353,16 +358,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::sts128(smem_addr(smem + L::OFF_P) + i * 16, 0u, 0u, 0u, 0u);
     tc::fence_proxy_async_smem();
     griddep_wait();
-    Segment* segs = P.segments + (static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y) * kMaxSegments;
+    const Segments segs = {
+        rest.near, P.segments + (static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y) * kMaxSegments};
     if (warp == 0) {
         const bool last = blockIdx.x == gridDim.x - 1 && reports;
         const int u0 = blockIdx.x * P.range, u1 = u0 + P.range;
         int nseg = 0, chunks = 0, any_bad = 0;
-        const int seen = scan_units(P, u0, u1, last, [&](int s, int first, int end, bool in, unsigned lanes) {
+        const int seen = scan_units(P, u0, u1, last, [&](int s, const LinearSeq& q, int first, int end, bool in,
+                                                          unsigned lanes) {
             const int k = nseg + __popc(lanes & ((1u << lane) - 1));
             int n = 0, bad = 0;
             if (in && k < kMaxSegments) {
-                const LinearSeq q = linear_seq(A, s, reports && first >= u0);
+                if (q.bad && reports && first >= u0) linear_seq(A, s, true);
                 const int c0 = max(u0, first) - first, c1 = min(u1, end) - first;
                 Segment g;
                 g.row0 = q.row0 + c0 * C;
@@ -910,11 +917,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             if (h == 0) P.tails[blockIdx.x] = make_int4(0, 0, 0, -1);
         }
         __syncwarp();
-        scan_units(P, u1 - 1, u1, false, [&](int s, int first, int end, bool in, unsigned) {
-            if (!in || end <= u1) return;
-            const LinearSeq q = linear_seq(A, s, false);
+        scan_units(P, u1 - 1, u1, false, [&](int, const LinearSeq& q, int first, int end, bool in, unsigned) {
+            if (!in || end <= u1 || q.bad) return;
             const int c0 = max(u0, first) - first, c1 = u1 - first;
-            if (q.bad) return;
             info[0] = q.row0 + c0 * C;
             info[1] = c1 - c0;
             // chunks, whether it holds the sequence's first row, and the state that goes before it
@@ -1116,12 +1121,6 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     if (units == 0) return best;
     best.units = static_cast<int32_t>(units);
     const int64_t most = max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms);
-    // Microseconds of a chunk in the main and in the state kernel, of a
-    // kernel's start and end, and of the two more kernels that join ranges.
-    // More ranges fill more SMs; where they cut sequences, the state kernel
-    // reads K and V of all but the last range once more, and the states are
-    // carried over.  Dealing a group's q heads to several CTAs fills SMs too,
-    // and repeats the state's work in each.
     // Whether a range may end at a unit without cutting a sequence (without
     // the room to say so, none may: the join is then launched needlessly).
     std::unique_ptr<uint8_t[]> begins(new (std::nothrow) uint8_t[static_cast<size_t>(units)]());
@@ -1131,6 +1130,15 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
         begins[at] = 1;
         at += (rows + C - 1) / C;
     }
+    // Microseconds of a chunk in the main kernel (what a chunk costs, and each
+    // of its q heads) and in the state kernel, of a kernel's start and end,
+    // and of the two more kernels that join ranges.  More ranges fill more
+    // SMs; where they cut sequences, the state kernel reads K and V of all but
+    // the last range once more, and the states are carried over.  Dealing a
+    // group's q heads to several CTAs fills SMs too, and repeats the state's
+    // work in each.  The constants are fitted to the times of forced plans
+    // over nine batches (128 to 16,384 tokens, both widths, one sequence and
+    // many); the plans taken are within 4 % of the best forced one.
     const bool narrow = head_dim == 64;
     const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5;
     const int64_t least = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 1;

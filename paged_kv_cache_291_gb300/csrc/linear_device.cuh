@@ -125,42 +125,43 @@ constexpr int kLinearChunk = 64;  // tokens of a chunk
 // elements.
 __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearScan& S, int block) {
     __shared__ float2 lam_s;
+    __shared__ __align__(16) int4 tails[kScanThreads];
     const int slices = A.head_dim * A.head_dim / (2 * kScanThreads);
-    const int h = block / slices;
+    const int h = block / slices, tid = threadIdx.x;
     const float g = clean_log_decay(A, h, false);
-    if (threadIdx.x == 0) lam_s = decay_pair(g, S.tokens);
     const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
-    const int64_t e = (static_cast<int64_t>(block % slices) * kScanThreads + threadIdx.x) * 2;
+    const int64_t e = (static_cast<int64_t>(block % slices) * kScanThreads + tid) * 2;
     float* p = S.bounds + h * head + e;
     const int64_t step = static_cast<int64_t>(A.num_kv_heads) * head;
-    __syncthreads();
-    const float2 lam = lam_s;
     float2 x = make_float2(0.f, 0.f);
-    // Loads of several ranges together: they hang on nothing but the list.
+    // Loads of several ranges together: they hang on nothing but the list,
+    // and the first ones not even on that.
     constexpr int kBatch = 8;
     for (int r0 = 0; r0 < S.ranges - 1; r0 += kBatch) {
-        int4 tail[kBatch];
+        const int n = min(kBatch, S.ranges - 1 - r0);
+        const bool list = r0 % kScanThreads == 0;
+        if (list) {
+            if (r0 > 0) __syncthreads();
+            if (r0 + tid < S.ranges - 1) tails[tid] = S.tails[r0 + tid];
+            if (r0 == 0 && tid == kScanThreads - 1) lam_s = decay_pair(g, S.tokens);
+        }
         float2 y[kBatch], before[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            tail[j] = make_int4(0, 0, 0, -1);
-            y[j] = make_float2(0.f, 0.f);
-            if (r0 + j < S.ranges - 1) {
-                tail[j] = S.tails[r0 + j];
-                y[j] = *reinterpret_cast<const float2*>(p + (r0 + j) * step);
-            }
-        }
+        for (int j = 0; j < kBatch; ++j)
+            if (j < n) y[j] = *reinterpret_cast<const float2*>(p + (r0 + j) * step);
+        if (list) __syncthreads();
+        const int4* tail = tails + r0 % kScanThreads;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             before[j] = make_float2(0.f, 0.f);
-            if (tail[j].x > 0 && tail[j].y && tail[j].w >= 0)
+            if (j < n && tail[j].x > 0 && tail[j].y && tail[j].w >= 0)
                 before[j] = *reinterpret_cast<const float2*>(
                     A.states + (static_cast<int64_t>(tail[j].w) * A.num_kv_heads + h) * head + e);
         }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            if (tail[j].x <= 0) continue;
-            float2 f = lam;
+            if (j >= n || tail[j].x <= 0) continue;
+            float2 f = lam_s;
             if (tail[j].y) {
                 // a sequence's first segment: its length is its own, its factor applied once
                 f = make_float2(expf(g * static_cast<float>(tail[j].x * kLinearChunk)), 0.f);
