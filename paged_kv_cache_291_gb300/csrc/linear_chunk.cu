@@ -31,7 +31,7 @@
 // the outputs' product (900), updated (900).  At head_dim 128 and one q head a
 // chunk takes 5,000 cycles against 3,500 of its bytes at HBM's rate; the
 // tensor pipe is 39% active and nothing is full.  16,384 tokens of 16 heads of
-// 128: 123 us (states of the ranges 24, scan 5, main 89); 12 prompts, 6,171
+// 128: 119 us (states of the ranges 24, scan 5, main 85); 12 prompts, 6,171
 // tokens, 32/8 heads of 64: 52 us.
 //
 // Every wait is bounded; TMEM is freed on every exit path.
@@ -104,6 +104,14 @@ enum { I_SEGS = 0, I_CHUNKS, I_BAD, I_COUNT };
 constexpr int kMaxSegments = 128;  // of one range: ranges are at most this long when there are more sequences
 constexpr int kFromBounds = -2;
 
+// K and V are read twice in the same order, by the state kernel and by the
+// main one.  When they are more than the L2 keeps beside the rest, the oldest
+// lines, which are wanted first, would go first: the state kernel then loads
+// with evict_first, so that its later tiles replace each other.  16 heads of
+// 128, 50 MB of K and V: 60.4 to 58.4 us; 134 MB: 123.9 to 119.8; 34 MB: 48.1
+// both ways; a mixed batch with 13 MB: 32.6 to 33.1, which is why not always.
+constexpr int64_t kOverflowBytes = 40 << 20;
+
 struct Segment {
     int row0, rows;   // rows <= 0: -rows rows get zeros and nothing else happens
     int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before
@@ -158,6 +166,7 @@ struct ChunkParams {
     int32_t ranges, range;  // ranges, and chunks of each
     int32_t units;          // chunks the host counted
     int32_t subs;           // CTAs a kv head's group of q heads is dealt to
+    int32_t overflow;       // K and V, which are read twice, are more than the L2 keeps
 };
 
 // One warp: calls f(sequence s, what it is, its first unit, the unit behind
@@ -934,6 +943,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
     const int row0 = info[0], nch = info[1];
     bool ok = true;
     if (warp == 8) {
+        const uint64_t policy = P.overflow ? l2_policy_evict_first() : tc::l2_policy_evict_normal();
         for (int i = 0; i < nch && ok; ++i) {
             const int st = i % kStateStages;
             if (!warp_wait(&bar[SB_EMPTY + st], ((i / kStateStages) & 1) ^ 1)) { ok = false; break; }
@@ -942,9 +952,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
 #pragma unroll
                 for (int pn = 0; pn < kPanels; ++pn) {
                     tc::tma_load_3d(smem + SOFF_V + st * kTile + pn * kPanel, &tm_v, 64 * pn, h, row0 + i * C,
-                                    &bar[SB_FULL + st]);
+                                    &bar[SB_FULL + st], policy);
                     tc::tma_load_3d(smem + SOFF_K + st * kTile + pn * kPanel, &tm_k, 64 * pn, h, row0 + i * C,
-                                    &bar[SB_FULL + st]);
+                                    &bar[SB_FULL + st], policy);
                 }
             }
             __syncwarp();
@@ -1192,6 +1202,7 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.range = plan.range;
     P.units = plan.units;
     P.subs = plan.subs;
+    P.overflow = static_cast<int64_t>(plan.units) * C * a.num_kv_heads * a.head_dim * 4 > kOverflowBytes;
     LinearScan scan = {};
     cudaError_t e = cudaSuccess;
     if (plan.cut) {

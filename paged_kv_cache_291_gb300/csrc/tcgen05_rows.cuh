@@ -1,5 +1,6 @@
 // tcgen05_rows.cuh -- tensor-memory accesses in which a thread holds a lane
-// (32 lanes x N columns a warp), and the election of one lane.
+// (32 lanes x N columns a warp), the election of one lane, and TMA loads that
+// tell the L2 how long to keep what they read.
 #pragma once
 
 #include "tcgen05.cuh"
@@ -56,6 +57,22 @@ __device__ __forceinline__ void tmem_st32x32b_x8(uint32_t taddr, const uint32_t 
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+        : "memory");
+}
+
+// The usual policy, where one is chosen when the kernel runs.
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
+        "{%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
 }
 
