@@ -393,6 +393,33 @@ def test_prefill_more_sequences_than_a_range_lists(pkv):
     assert pkv.get_error() == (0, 0)
 
 
+def test_prefill_joins_more_ranges_than_are_listed_at_once(pkv):
+    """100,000 tokens of one head: 1,563 chunks in more than the 128 ranges
+    that the join lists at once, with a decay slow enough to carry a state
+    over many of them.  Tolerance: a term meets no more than 28 half steps per
+    chunk (twelve truncating sums of the tensor cores, a whole step each, and
+    four roundings of the decay), four per join (at most 152), and forty in its
+    own chunk."""
+    b = Batch(72, [100000], [4], 1, 1, 64)
+    b.g[:] = -2e-4
+    out = b.prefill(pkv)
+    assert pkv.get_error() == (0, 0)
+    want, after = b.oracle()
+    bound, bound_after = b.oracle(absolute=True)
+    c = (40 + 28 * 1563 + 4 * 152) * 2.0 ** -24
+    assert np.all(np.abs(f64(out) - want) <= c * bound)
+    i = int(b.new[0])
+    assert np.all(np.abs(b.states[i].double().cpu().numpy() - after[i]) <= c * bound_after[i])
+
+
+def test_prefill_more_keys_and_values_than_the_cache_keeps(pkv):
+    """44 MB of K and V, cut into ranges: the first of their two readings asks
+    for another cache policy."""
+    b = Batch(73, [2700], [0], 64, 64, 64)
+    b.check(b.prefill(pkv), "2,700 tokens of 64 heads")
+    assert pkv.get_error() == (0, 0)
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_prefill_random_batches(pkv, seed):
     """Batches whose ranges begin and end anywhere in the sequences."""
