@@ -25,7 +25,9 @@
 // The chunks of all sequences are cut into equal ranges, one CTA each per kv
 // head, whatever the lengths of the sequences.  Where a border lies inside a
 // sequence, linear_state_kernel sums the part's own state first and
-// linear_scan_kernel carries the states over the borders.
+// linear_scan_kernel carries the states over the borders.  The CTAs of one
+// launch come in no order, so a slot that a sequence reads in its first range
+// and replaces in its last is read by the scan, which copies it for the first.
 //
 // Bound.  A chunk's chain: the state is split (1,500 to 2,000 cycles), read by
 // the outputs' product (900), updated (900).  At head_dim 128 and one q head a
@@ -102,7 +104,7 @@ enum {
 enum { I_SEGS = 0, I_CHUNKS, I_BAD, I_COUNT };
 
 constexpr int kMaxSegments = 128;  // of one range: ranges are at most this long when there are more sequences
-constexpr int kFromBounds = -2;
+constexpr int kFromBounds = -2, kFromStarts = -3;
 
 // K and V are read twice in the same order, by the state kernel and by the
 // main one.  When they are more than the L2 keeps beside the rest, the oldest
@@ -114,7 +116,8 @@ constexpr int64_t kOverflowBytes = 40 << 20;
 
 struct Segment {
     int row0, rows;   // rows <= 0: -rows rows get zeros and nothing else happens
-    int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before
+    int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before;
+                      // kFromStarts: this range's copy of a slot that a later range's CTA stores to
     int seq, first;   // first: holds the sequence's first row
     int pad[2];
 };
@@ -161,6 +164,7 @@ constexpr uint32_t kTmemCols = 512;
 struct ChunkParams {
     LinearArgs A;
     float* bounds;          // fp32 [ranges - 1][Hkv][d][d]: the state at the end of each range
+    float* starts;          // the same: where a range's last segment begins a sequence that goes on in place, its state
     int4* tails;            // [ranges - 1]: what the scan needs of a range's last segment
     Segment* segments;      // [ranges][CTAs of a range][kMaxSegments]
     int32_t ranges, range;  // ranges, and chunks of each
@@ -383,7 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Segment g;
                 g.row0 = q.row0 + c0 * C;
                 g.rows = min(q.rows, c1 * C) - c0 * C;
-                g.load = c0 > 0 ? kFromBounds : q.load;
+                // In place, the CTA of the sequence's last range may store
+                // before this one reads: the join has copied the state.
+                g.load = c0 > 0 ? kFromBounds : end > u1 && q.load >= 0 && q.load == q.store ? kFromStarts : q.load;
                 g.store = end <= u1 && sub == 0 ? q.store : -1;
                 g.seq = s;
                 g.first = c0 == 0;
@@ -593,6 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto state_at = [&](int load) -> const float* {
             if (load == kFromBounds)
                 return P.bounds + (static_cast<int64_t>(blockIdx.x - 1) * A.num_kv_heads + h) * head;
+            if (load == kFromStarts) return P.starts + (static_cast<int64_t>(blockIdx.x) * A.num_kv_heads + h) * head;
             return load >= 0 ? A.states + (static_cast<int64_t>(load) * A.num_kv_heads + h) * head : nullptr;
         };
         auto split = [&](uint32_t (&x)[16], int b, float2 lam) {
@@ -931,8 +938,9 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             const int c0 = max(u0, first) - first, c1 = u1 - first;
             info[0] = q.row0 + c0 * C;
             info[1] = c1 - c0;
-            // chunks, whether it holds the sequence's first row, and the state that goes before it
-            if (h == 0) P.tails[blockIdx.x] = make_int4(c1 - c0, c0 == 0, 0, q.load);
+            // chunks, whether it holds the sequence's first row, whether the sequence's state is replaced in
+            // place, and the state that goes before it
+            if (h == 0) P.tails[blockIdx.x] = make_int4(c1 - c0, c0 == 0, q.load == q.store, q.load);
         });
     }
     const float g = clean_log_decay(A, h, false);
@@ -1115,7 +1123,7 @@ static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                               int32_t head_dim, int num_sms) {
     const size_t n = static_cast<size_t>(max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms));
-    return round256(n * sizeof(int4)) + n * num_kv_heads * head_dim * head_dim * sizeof(float) +
+    return round256(n * sizeof(int4)) + 2 * n * num_kv_heads * head_dim * head_dim * sizeof(float) +
            n * num_q_heads * kMaxSegments * sizeof(Segment);
 }
 
@@ -1196,7 +1204,10 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.tails = reinterpret_cast<int4*>(at);
     at += round256(n * sizeof(int4));
     P.bounds = reinterpret_cast<float*>(at);
-    at += n * a.num_kv_heads * static_cast<size_t>(a.head_dim) * a.head_dim * sizeof(float);
+    const size_t states = n * a.num_kv_heads * static_cast<size_t>(a.head_dim) * a.head_dim;
+    at += states * sizeof(float);
+    P.starts = P.bounds + states;
+    at += states * sizeof(float);
     P.segments = reinterpret_cast<Segment*>(at);
     P.ranges = plan.ranges;
     P.range = plan.range;
@@ -1208,7 +1219,7 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     if (plan.cut) {
         e = a.head_dim == 64 ? launch_state<64>(tk, tv, P, stream) : launch_state<128>(tk, tv, P, stream);
         if (e != cudaSuccess) return e;
-        scan = {P.bounds, P.tails, P.ranges, P.range * C,
+        scan = {P.bounds, P.starts, P.tails, P.ranges, P.range * C,
                 a.num_kv_heads * (a.head_dim * a.head_dim / (2 * kScanThreads))};
     }
     // The scan rides in the recurrent form's grid where there is one.

@@ -121,8 +121,10 @@ constexpr int kLinearChunk = 64;  // tokens of a chunk
 // The states at the ends of the ranges, from the ranges' own: bounds[x] <-
 // lam^(tokens of the segment) (state before it) + bounds[x], in order, the
 // state before being the sequence's where the segment begins it and
-// bounds[x - 1] otherwise.  Block `block` of S.blocks; a thread carries two
-// elements.
+// bounds[x - 1] otherwise.  starts[x] <- the sequence's, where its slot is also
+// the one its new state goes to, which the chunked form's CTAs would otherwise
+// read and replace in no order.  Block `block` of S.blocks; a thread carries
+// two elements.
 __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearScan& S, int block) {
     __shared__ float2 lam_s;
     __shared__ __align__(16) int4 tails[kScanThreads];
@@ -166,6 +168,8 @@ __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearSca
                 // a sequence's first segment: its length is its own, its factor applied once
                 f = make_float2(expf(g * static_cast<float>(tail[j].x * kLinearChunk)), 0.f);
                 x = before[j];
+                if (tail[j].z && tail[j].w >= 0)
+                    *reinterpret_cast<float2*>(S.starts + h * head + e + (r0 + j) * step) = x;
             }
             x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y[j].x));
             x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y[j].y));

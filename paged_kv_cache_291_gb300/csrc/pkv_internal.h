@@ -183,6 +183,7 @@ struct LinearArgs {
 // The join of the chunked form's ranges (linear_device.cuh).
 struct LinearScan {
     float* bounds;
+    float* starts;
     const int4* tails;
     int32_t ranges;
     int32_t tokens;      // of a whole range
