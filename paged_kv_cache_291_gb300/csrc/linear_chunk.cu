@@ -28,6 +28,8 @@
 // linear_scan_kernel carries the states over the borders.  The CTAs of one
 // launch come in no order, so a slot that a sequence reads in its first range
 // and replaces in its last is read by the scan, which copies it for the first.
+// Where a group's q heads are dealt to several CTAs, all of them read the slot
+// and reach the same new state; the last to reach it stores it.
 //
 // Bound.  A chunk's chain: the state is split (1,500 to 2,000 cycles), read by
 // the outputs' product (900), updated (900).  At head_dim 128 and one q head a
@@ -119,7 +121,7 @@ struct Segment {
     int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before;
                       // kFromStarts: this range's copy of a slot that a later range's CTA stores to
     int seq, first;   // first: holds the sequence's first row
-    int pad[2];
+    int shared, pad;  // shared: other CTAs read the slot that is stored to, the last of them stores
 };
 
 // The list's first segments are in shared memory: most lists have no more,
@@ -166,6 +168,8 @@ struct ChunkParams {
     float* bounds;          // fp32 [ranges - 1][Hkv][d][d]: the state at the end of each range
     float* starts;          // the same: where a range's last segment begins a sequence that goes on in place, its state
     int4* tails;            // [ranges - 1]: what the scan needs of a range's last segment
+    uint32_t* claims;       // [num_seqs][Hkv], cleared by the scan: CTAs of a shared segment that are done with
+                            // its slot, 4 bits for each of the warps that hold a part of the state
     Segment* segments;      // [ranges][CTAs of a range][kMaxSegments]
     int32_t ranges, range;  // ranges, and chunks of each
     int32_t units;          // chunks the host counted
@@ -390,7 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // In place, the CTA of the sequence's last range may store
                 // before this one reads: the join has copied the state.
                 g.load = c0 > 0 ? kFromBounds : end > u1 && q.load >= 0 && q.load == q.store ? kFromStarts : q.load;
-                g.store = end <= u1 && sub == 0 ? q.store : -1;
+                g.shared = P.subs > 1 && c0 == 0 && end <= u1 && q.load >= 0 && q.load == q.store;
+                g.store = end <= u1 && (sub == 0 || g.shared) ? q.store : -1;
                 g.seq = s;
                 g.first = c0 == 0;
                 bad = q.bad;
@@ -670,6 +675,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok || store < 0) continue;
             if (!warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
+            if (live && segs[k].shared) {
+                // The same warp of every CTA that shares the segment holds the
+                // same part of the state.  Whoever comes last here knows that
+                // the others have read it.
+                uint32_t before = 0;
+                if (lane == 0) {
+                    const int at = 4 * (warp - kSWarp);
+                    __threadfence();
+                    before = atomicAdd(P.claims + static_cast<int64_t>(segs[k].seq) * A.num_kv_heads + h, 1u << at);
+                    __threadfence();
+                    before = (before >> at) & 15u;
+                }
+                if (__shfl_sync(0xffffffffu, before, 0) != static_cast<uint32_t>(P.subs - 1)) continue;
+            }
             if (live) {
                 float* to = A.states + (static_cast<int64_t>(store) * A.num_kv_heads + h) * head + dv;
 #pragma unroll 1
@@ -1124,7 +1143,8 @@ size_t linear_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_
                               int32_t head_dim, int num_sms) {
     const size_t n = static_cast<size_t>(max_ranges(num_seqs, num_tokens, num_kv_heads, num_sms));
     return round256(n * sizeof(int4)) + 2 * n * num_kv_heads * head_dim * head_dim * sizeof(float) +
-           n * num_q_heads * kMaxSegments * sizeof(Segment);
+           n * num_q_heads * kMaxSegments * sizeof(Segment) +
+           static_cast<size_t>(num_seqs) * num_kv_heads * sizeof(uint32_t);
 }
 
 LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens, int32_t num_kv_heads, int32_t group,
@@ -1153,12 +1173,14 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     // and of the two more kernels that join ranges.  More ranges fill more
     // SMs; where they cut sequences, the state kernel reads K and V of all but
     // the last range once more, and the states are carried over.  Dealing a
-    // group's q heads to several CTAs fills SMs too, and repeats the state's
-    // work in each.  The constants are fitted to the times of forced plans
+    // group's q heads to several CTAs fills SMs too, repeats the state's work
+    // in each, and takes a launch that clears their counters where there is
+    // none before the main kernel anyway.  The constants are fitted to the times of forced plans
     // over nine batches (128 to 16,384 tokens, both widths, one sequence and
     // many); the plans taken are within 4 % of the best forced one.
     const bool narrow = head_dim == 64;
-    const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5;
+    const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5,
+                 clear = 1.5;
     const int64_t least = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 1;
     const int64_t last = most < units ? most : units;
     double best_us = 1e30;
@@ -1173,6 +1195,7 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
             bool cut = false;  // whether a border lies inside a sequence
             for (int64_t u = range; u < units && !cut; u += range) cut = !begins || begins[u] == 0;
             if (cut) us += 7.0 + 0.15 * ranges + ((ranges - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
+            if (subs > 1 && !cut && best.recurrent == 0) us += clear;
             if (us >= best_us) return;
             best_us = us;
             best.ranges = static_cast<int32_t>(ranges);
@@ -1209,6 +1232,8 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.starts = P.bounds + states;
     at += states * sizeof(float);
     P.segments = reinterpret_cast<Segment*>(at);
+    at += n * a.num_q_heads * kMaxSegments * sizeof(Segment);
+    P.claims = reinterpret_cast<uint32_t*>(at);
     P.ranges = plan.ranges;
     P.range = plan.range;
     P.units = plan.units;
@@ -1216,16 +1241,26 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.overflow = static_cast<int64_t>(plan.units) * C * a.num_kv_heads * a.head_dim * 4 > kOverflowBytes;
     LinearScan scan = {};
     cudaError_t e = cudaSuccess;
+    if (plan.subs > 1) {
+        scan.claims = P.claims;
+        scan.num_claims = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+        const int64_t blocks = (scan.num_claims + 8 * kScanThreads - 1) / (8 * kScanThreads);
+        scan.blocks = static_cast<int32_t>(blocks < num_sms ? blocks : num_sms);
+    }
     if (plan.cut) {
         e = a.head_dim == 64 ? launch_state<64>(tk, tv, P, stream) : launch_state<128>(tk, tv, P, stream);
         if (e != cudaSuccess) return e;
-        scan = {P.bounds, P.starts, P.tails, P.ranges, P.range * C,
-                a.num_kv_heads * (a.head_dim * a.head_dim / (2 * kScanThreads))};
+        scan.bounds = P.bounds;
+        scan.starts = P.starts;
+        scan.tails = P.tails;
+        scan.ranges = P.ranges;
+        scan.tokens = P.range * C;
+        scan.blocks = a.num_kv_heads * (a.head_dim * a.head_dim / (2 * kScanThreads));
     }
     // The scan rides in the recurrent form's grid where there is one.
     if (plan.recurrent > 0)
         e = launch_linear_recurrent(a, plan.recurrent, scan, stream);
-    else if (plan.cut)
+    else if (scan.blocks > 0)
         e = launch_overlapped(linear_scan_kernel, dim3(scan.blocks), dim3(kScanThreads), 0, stream, a, scan);
     if (e != cudaSuccess) return e;
     return a.head_dim == 64 ? launch_groups<64>(tq, tk, tv, P, stream) : launch_groups<128>(tq, tk, tv, P, stream);

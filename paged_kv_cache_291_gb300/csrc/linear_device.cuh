@@ -124,12 +124,18 @@ constexpr int kLinearChunk = 64;  // tokens of a chunk
 // bounds[x - 1] otherwise.  starts[x] <- the sequence's, where its slot is also
 // the one its new state goes to, which the chunked form's CTAs would otherwise
 // read and replace in no order.  Block `block` of S.blocks; a thread carries
-// two elements.
+// two elements.  Clears the counters of the call too, which may be all there
+// is to do (no ranges).
 __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearScan& S, int block) {
     __shared__ float2 lam_s;
     __shared__ __align__(16) int4 tails[kScanThreads];
+    const int tid = threadIdx.x;
+    for (int64_t i = static_cast<int64_t>(block) * kScanThreads + tid; i < S.num_claims;
+         i += static_cast<int64_t>(S.blocks) * kScanThreads)
+        S.claims[i] = 0;
+    if (S.ranges == 0) return;
     const int slices = A.head_dim * A.head_dim / (2 * kScanThreads);
-    const int h = block / slices, tid = threadIdx.x;
+    const int h = block / slices;
     const float g = clean_log_decay(A, h, false);
     const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
     const int64_t e = (static_cast<int64_t>(block % slices) * kScanThreads + tid) * 2;

@@ -180,14 +180,17 @@ struct LinearArgs {
     float scale;
 };
 
-// The join of the chunked form's ranges (linear_device.cuh).
+// What goes before the chunked form's main kernel: the join of its ranges,
+// and counters to clear (linear_device.cuh).
 struct LinearScan {
     float* bounds;
     float* starts;
     const int4* tails;
-    int32_t ranges;
+    uint32_t* claims;
+    int64_t num_claims;
+    int32_t ranges;      // 0: nothing to join
     int32_t tokens;      // of a whole range
-    int32_t blocks;      // 0: nothing to join
+    int32_t blocks;      // 0: nothing to do
 };
 
 // longest: rows of the longest sequence it will meet; scan.blocks more CTAs

@@ -38,12 +38,14 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     // and of the two more kernels that join ranges.  More ranges fill more
     // SMs; where they cut sequences, the state kernel reads K and V of all but
     // the last range once more, and the states are carried over.  Dealing a
-    // group's q heads to several CTAs fills SMs too, and repeats the state's
-    // work in each.  The constants are fitted to the times of forced plans
+    // group's q heads to several CTAs fills SMs too, repeats the state's work
+    // in each, and takes a launch that clears their counters where there is
+    // none before the main kernel anyway.  The constants are fitted to the times of forced plans
     // over nine batches (128 to 16,384 tokens, both widths, one sequence and
     // many); the plans taken are within 4 % of the best forced one.
     const bool narrow = head_dim == 64;
-    const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5;
+    const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5,
+                 clear = 1.5;
     const int64_t least = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 1;
     const int64_t last = most < units ? most : units;
     double best_us = 1e30;
@@ -58,6 +60,7 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
             bool cut = false;  // whether a border lies inside a sequence
             for (int64_t u = range; u < units && !cut; u += range) cut = !begins || begins[u] == 0;
             if (cut) us += 7.0 + 0.15 * ranges + ((ranges - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
+            if (subs > 1 && !cut && best.recurrent == 0) us += clear;
             if (us >= best_us) return;
             best_us = us;
             best.ranges = static_cast<int32_t>(ranges);

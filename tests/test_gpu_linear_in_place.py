@@ -99,3 +99,51 @@ def test_cut_sequences_in_place_in_a_replayed_graph(pkv):
         assert pkv.get_error() == (0, 0)
         assert torch.equal(out, want)
         assert torch.equal(b.states[dev[2].long()], states[dev[2].long()])
+
+
+# Batches whose plan deals the q heads of a state to several blocks, with
+# sequences that lie whole in a range.
+DEALT = [
+    ([80], 8, 1, 64),
+    ([40], 8, 1, 128),
+    ([64] * 6, 8, 2, 128),
+    ([100] * 40, 32, 8, 64),
+    ([90, 64, 3, 200, 1, 70, 65], 16, 2, 64),
+    ([30, 1, 64, 2, 100], 32, 4, 128),
+]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", DEALT)
+def test_dealt_heads_in_place(pkv, lens, hq, hkv, d):
+    b = Batch(250 + len(lens), lens, [4 + s % 3 for s in range(len(lens))], hq, hkv, d)
+    assert_in_place_equals_separate(pkv, b, "dealt")
+
+
+def test_dealt_heads_in_place_against_the_oracle(pkv):
+    b = Batch(260, [64, 40, 100, 1, 128], [3, 0, 4, 5, 6], 8, 2, 64, separate=False)
+    b.check(b.prefill(pkv), "in place")
+    assert pkv.get_error() == (0, 0)
+
+
+def test_in_place_while_another_stream_holds_multiprocessors(pkv):
+    """The blocks of a call then start at different times."""
+    other = Batch(261, [6000], [0], 16, 16, 128, packed=False)
+    batches = [Batch(262, [100] * 40, [4] * 40, 32, 8, 64), Batch(263, [64] * 12, [4] * 12, 16, 4, 128),
+               Batch(264, [1283, 1092, 453, 1107], [4] * 4, 16, 16, 128)]
+    wants = [run(pkv, b, dev_tensor(b.new), dev_tensor(b.S0)) for b in batches]
+    want_other = other.prefill(pkv)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        outs = []
+        with torch.cuda.stream(side):
+            others = [other.prefill(pkv) for _ in range(8)]
+        for b in batches:
+            outs.append(run(pkv, b, None, dev_tensor(b.S0)))
+        torch.cuda.synchronize()
+        assert pkv.get_error() == (0, 0)
+        for b, (want, after), (out, states) in zip(batches, wants, outs):
+            assert torch.equal(out, want)
+            assert torch.equal(states[dev_tensor(b.slots).long()], after[dev_tensor(b.new).long()])
+        for x in others:
+            assert torch.equal(x, want_other)
