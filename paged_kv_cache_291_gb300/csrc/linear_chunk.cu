@@ -27,7 +27,7 @@
 // sequence, linear_state_kernel sums the part's own state first and
 // linear_scan_kernel carries the states over the borders.  The CTAs of one
 // launch come in no order, so a slot that a sequence reads in its first range
-// and replaces in its last is read by the scan, which copies it for the first.
+// and replaces in its last is copied by linear_state_kernel for the first.
 // Where a group's q heads are dealt to several CTAs, all of them read the slot
 // and reach the same new state; the last to reach it stores it.
 //
@@ -119,9 +119,10 @@ constexpr int64_t kOverflowBytes = 40 << 20;
 struct Segment {
     int row0, rows;   // rows <= 0: -rows rows get zeros and nothing else happens
     int load, store;  // slots, -1: none; load kFromBounds: the state at the end of the range before;
-                      // kFromStarts: this range's copy of a slot that a later range's CTA stores to
+                      // kFromStarts: this range's copy of a slot that a later range's CTA stores to;
+                      // store -2 - slot: other CTAs read this slot too, the last of them stores
     int seq, first;   // first: holds the sequence's first row
-    int shared, pad;  // shared: other CTAs read the slot that is stored to, the last of them stores
+    int pad[2];
 };
 
 // The list's first segments are in shared memory: most lists have no more,
@@ -132,6 +133,14 @@ struct Segments {
     __device__ __forceinline__ Segment& operator[](int k) const { return k < kNearSegments ? near[k] : far[k]; }
 };
 
+// Warps, spread so that the four SM sub-partitions (warp % 4, which is also
+// the TMEM lane quarter a warp can reach) carry about the same work.
+constexpr int kThreads = 768;
+constexpr int kLoadWarp = 2, kMmaWarp = 3;
+// P: warps 0 (s 0-31, t 0-31), 4 (s 0-31, t 32-63) and 1 (s 32-63, t 32-63)
+// V~: warps 2 (which also loads), 5, 6 and 7
+constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
+
 // What follows the tiles.
 struct Rest {
     alignas(16) float tab[260];
@@ -139,6 +148,7 @@ struct Rest {
     Segment near[kNearSegments];
     uint64_t bar[NBAR];
     int info[I_COUNT];
+    int stores[kSWarps];             // whether the warp's CTA is the one that stores a shared segment
     uint32_t tmem;
 };
 template <int D>
@@ -147,14 +157,6 @@ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<128>() <= 232448, "shared memory budget (227 KB)");
 static_assert(2 * smem_bytes<64>() > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
-
-// Warps, spread so that the four SM sub-partitions (warp % 4, which is also
-// the TMEM lane quarter a warp can reach) carry about the same work.
-constexpr int kThreads = 768;
-constexpr int kLoadWarp = 2, kMmaWarp = 3;
-// P: warps 0 (s 0-31, t 0-31), 4 (s 0-31, t 32-63) and 1 (s 32-63, t 32-63)
-// V~: warps 2 (which also loads), 5, 6 and 7
-constexpr int kVWarps = 4, kSWarp = 8, kSWarps = 8, kOWarp = 16, kOWarps = 8;
 
 constexpr uint32_t kTmemCols = 512;
 
@@ -168,8 +170,8 @@ struct ChunkParams {
     float* bounds;          // fp32 [ranges - 1][Hkv][d][d]: the state at the end of each range
     float* starts;          // the same: where a range's last segment begins a sequence that goes on in place, its state
     int4* tails;            // [ranges - 1]: what the scan needs of a range's last segment
-    uint32_t* claims;       // [num_seqs][Hkv], cleared by the scan: CTAs of a shared segment that are done with
-                            // its slot, 4 bits for each of the warps that hold a part of the state
+    uint32_t* claims;       // [num_seqs][Hkv], cleared by an earlier launch: CTAs of a shared segment that have
+                            // read its slot, 4 bits for each of the warps that hold a part of the state
     Segment* segments;      // [ranges][CTAs of a range][kMaxSegments]
     int32_t ranges, range;  // ranges, and chunks of each
     int32_t units;          // chunks the host counted
@@ -392,10 +394,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.row0 = q.row0 + c0 * C;
                 g.rows = min(q.rows, c1 * C) - c0 * C;
                 // In place, the CTA of the sequence's last range may store
-                // before this one reads: the join has copied the state.
-                g.load = c0 > 0 ? kFromBounds : end > u1 && q.load >= 0 && q.load == q.store ? kFromStarts : q.load;
-                g.shared = P.subs > 1 && c0 == 0 && end <= u1 && q.load >= 0 && q.load == q.store;
-                g.store = end <= u1 && (sub == 0 || g.shared) ? q.store : -1;
+                // before this one reads: the state has been copied.  Of the
+                // CTAs that share a kv head's q heads, one stores.
+                const bool place = c0 == 0 && q.load >= 0 && q.load == q.store;
+                g.load = c0 > 0 ? kFromBounds : place && end > u1 ? kFromStarts : q.load;
+                if (end > u1) g.store = -1;
+                else if (place && P.subs > 1) g.store = -2 - q.store;
+                else g.store = sub == 0 ? q.store : -1;
                 g.seq = s;
                 g.first = c0 == 0;
                 bad = q.bad;
@@ -671,26 +676,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_S]);
-            }
-            if (!ok || store < 0) continue;
-            if (!warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
-            tc::fence_after_sync();
-            if (live && segs[k].shared) {
-                // The same warp of every CTA that shares the segment holds the
-                // same part of the state.  Whoever comes last here knows that
-                // the others have read it.
-                uint32_t before = 0;
-                if (lane == 0) {
+                if (store < -1 && left == rows && lane == 0) {
+                    // The same warp of every CTA that reads the slot holds the
+                    // same part of the state.  Whoever comes last here
+                    // knows that the others have read it, and stores it at
+                    // the end.  Here, because this warp waits for the update
+                    // next (at the end it would be 1 us a segment).
                     const int at = 4 * (warp - kSWarp);
                     __threadfence();
-                    before = atomicAdd(P.claims + static_cast<int64_t>(segs[k].seq) * A.num_kv_heads + h, 1u << at);
+                    const uint32_t before =
+                        atomicAdd(P.claims + static_cast<int64_t>(segs[k].seq) * A.num_kv_heads + h, 1u << at);
                     __threadfence();
-                    before = (before >> at) & 15u;
+                    rest.stores[warp - kSWarp] = ((before >> at) & 15u) == static_cast<uint32_t>(P.subs - 1);
                 }
-                if (__shfl_sync(0xffffffffu, before, 0) != static_cast<uint32_t>(P.subs - 1)) continue;
             }
+            if (!ok || store == -1) continue;
+            __syncwarp();
+            if (store < -1 && !rest.stores[warp - kSWarp]) continue;
+            const int slot = store < -1 ? -2 - store : store;
+            if (!warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
             if (live) {
-                float* to = A.states + (static_cast<int64_t>(store) * A.num_kv_heads + h) * head + dv;
+                float* to = A.states + (static_cast<int64_t>(slot) * A.num_kv_heads + h) * head + dv;
 #pragma unroll 1
                 for (int b = 0; b < kCols / 32; ++b) {
                     uint32_t x[32];
@@ -892,12 +899,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // goes on in the next range: sum_s lam^(end-1-s) k_s v_s^T over the segment's
 // tokens, one accumulation with no rescaling (the factor of a chunk's end is
 // part of V~).  Warps 0-7 make V~, 8 loads, 9 issues the MMAs; warps 0-3
-// store the sum.  There is room in tensor memory here, so V~ goes there: it
+// store the sum.  Warps 10-13 copy the state that the call replaces in place,
+// if it does: beside the others, where it costs nothing (after them it was
+// 1.3 us of a prompt of 300 tokens).  There is room in tensor memory here, so V~ goes there: it
 // is read from the V tile by transposing 8x8 loads, whose fragments are what
 // a 16-lane store takes, and the product needs shared memory for K alone.
 // (With V~ in shared memory the kernel was bound by it: 31 us for 8 ranges of
 // 29 chunks and 16 heads of 128.)
-constexpr int kStateThreads = 320;
+constexpr int kStateThreads = 448;
 constexpr int kStateStages = 5;
 constexpr int kTile = 2 * kPanel;        // room for head_dim 128
 constexpr int SOFF_K = 0;
@@ -949,6 +958,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
         const int u0 = blockIdx.x * P.range, u1 = u0 + P.range;
         if (lane == 0) {
             info[0] = info[1] = 0;
+            info[2] = -1;
             if (h == 0) P.tails[blockIdx.x] = make_int4(0, 0, 0, -1);
         }
         __syncwarp();
@@ -957,10 +967,15 @@ __global__ void __launch_bounds__(kStateThreads, 1)
             const int c0 = max(u0, first) - first, c1 = u1 - first;
             info[0] = q.row0 + c0 * C;
             info[1] = c1 - c0;
-            // chunks, whether it holds the sequence's first row, whether the sequence's state is replaced in
-            // place, and the state that goes before it
-            if (h == 0) P.tails[blockIdx.x] = make_int4(c1 - c0, c0 == 0, q.load == q.store, q.load);
+            if (c0 == 0 && q.load == q.store) info[2] = q.load;
+            // chunks, whether it holds the sequence's first row, and the state that goes before it
+            if (h == 0) P.tails[blockIdx.x] = make_int4(c1 - c0, c0 == 0, 0, q.load);
         });
+    } else if (warp == 10 && P.subs > 1) {
+        const int64_t n = static_cast<int64_t>(A.num_seqs) * A.num_kv_heads;
+        for (int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * 32 + lane; i < n;
+             i += static_cast<int64_t>(gridDim.x) * gridDim.y * 32)
+            P.claims[i] = 0;
     }
     const float g = clean_log_decay(A, h, false);
     tc::fence_before_sync();
@@ -1007,6 +1022,22 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 if (i == nch - 1) tc::mma_commit(&bar[SB_DONE]);
             }
             __syncwarp();
+        }
+    } else if (warp >= 10) {
+        if (info[2] >= 0) {
+            const float4* src = reinterpret_cast<const float4*>(
+                A.states + (static_cast<int64_t>(info[2]) * A.num_kv_heads + h) * D * D);
+            float4* dst = reinterpret_cast<float4*>(
+                P.starts + (static_cast<int64_t>(blockIdx.x) * A.num_kv_heads + h) * D * D);
+            constexpr int kCopiers = kStateThreads - 320, kAhead = 8;
+#pragma unroll 1
+            for (int at = threadIdx.x - 320; at < D * D / 4; at += kCopiers * kAhead) {
+                float4 x[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) x[j] = src[at + kCopiers * j];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) dst[at + kCopiers * j] = x[j];
+            }
         }
     } else {
         // Warp w: 16 lanes (v indices) from 32 (w % 4) + 16 (w / 4).  Thread t
@@ -1180,7 +1211,7 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     // many); the plans taken are within 4 % of the best forced one.
     const bool narrow = head_dim == 64;
     const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5,
-                 clear = 1.5;
+                 clear = 0.9;
     const int64_t least = num_seqs > kMaxSegments ? (units + kMaxSegments - 1) / kMaxSegments : 1;
     const int64_t last = most < units ? most : units;
     double best_us = 1e30;
@@ -1241,7 +1272,7 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.overflow = static_cast<int64_t>(plan.units) * C * a.num_kv_heads * a.head_dim * 4 > kOverflowBytes;
     LinearScan scan = {};
     cudaError_t e = cudaSuccess;
-    if (plan.subs > 1) {
+    if (plan.subs > 1 && !plan.cut) {
         scan.claims = P.claims;
         scan.num_claims = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
         const int64_t blocks = (scan.num_claims + 8 * kScanThreads - 1) / (8 * kScanThreads);
@@ -1251,7 +1282,6 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
         e = a.head_dim == 64 ? launch_state<64>(tk, tv, P, stream) : launch_state<128>(tk, tv, P, stream);
         if (e != cudaSuccess) return e;
         scan.bounds = P.bounds;
-        scan.starts = P.starts;
         scan.tails = P.tails;
         scan.ranges = P.ranges;
         scan.tokens = P.range * C;

@@ -121,21 +121,19 @@ constexpr int kLinearChunk = 64;  // tokens of a chunk
 // The states at the ends of the ranges, from the ranges' own: bounds[x] <-
 // lam^(tokens of the segment) (state before it) + bounds[x], in order, the
 // state before being the sequence's where the segment begins it and
-// bounds[x - 1] otherwise.  starts[x] <- the sequence's, where its slot is also
-// the one its new state goes to, which the chunked form's CTAs would otherwise
-// read and replace in no order.  Block `block` of S.blocks; a thread carries
-// two elements.  Clears the counters of the call too, which may be all there
-// is to do (no ranges).
+// bounds[x - 1] otherwise.  Block `block` of S.blocks; a thread carries two
+// elements.  Without ranges there are only counters to clear.
 __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearScan& S, int block) {
     __shared__ float2 lam_s;
     __shared__ __align__(16) int4 tails[kScanThreads];
-    const int tid = threadIdx.x;
-    for (int64_t i = static_cast<int64_t>(block) * kScanThreads + tid; i < S.num_claims;
-         i += static_cast<int64_t>(S.blocks) * kScanThreads)
-        S.claims[i] = 0;
-    if (S.ranges == 0) return;
+    if (S.ranges == 0) {
+        for (int64_t i = static_cast<int64_t>(block) * kScanThreads + threadIdx.x; i < S.num_claims;
+             i += static_cast<int64_t>(S.blocks) * kScanThreads)
+            S.claims[i] = 0;
+        return;
+    }
     const int slices = A.head_dim * A.head_dim / (2 * kScanThreads);
-    const int h = block / slices;
+    const int h = block / slices, tid = threadIdx.x;
     const float g = clean_log_decay(A, h, false);
     const int64_t head = static_cast<int64_t>(A.head_dim) * A.head_dim;
     const int64_t e = (static_cast<int64_t>(block % slices) * kScanThreads + tid) * 2;
@@ -174,8 +172,6 @@ __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearSca
                 // a sequence's first segment: its length is its own, its factor applied once
                 f = make_float2(expf(g * static_cast<float>(tail[j].x * kLinearChunk)), 0.f);
                 x = before[j];
-                if (tail[j].z && tail[j].w >= 0)
-                    *reinterpret_cast<float2*>(S.starts + h * head + e + (r0 + j) * step) = x;
             }
             x.x = fmaf(x.x, f.x, fmaf(x.x, f.y, y[j].x));
             x.y = fmaf(x.y, f.x, fmaf(x.y, f.y, y[j].y));

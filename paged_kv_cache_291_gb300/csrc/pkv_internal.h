@@ -184,9 +184,8 @@ struct LinearArgs {
 // and counters to clear (linear_device.cuh).
 struct LinearScan {
     float* bounds;
-    float* starts;
     const int4* tails;
-    uint32_t* claims;
+    uint32_t* claims;    // counters to clear where there is nothing to join
     int64_t num_claims;
     int32_t ranges;      // 0: nothing to join
     int32_t tokens;      // of a whole range
