@@ -14,6 +14,7 @@ arrays int32; outputs float32.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -187,6 +188,23 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """Makes the stream a call launches on torch's current one, for what the
+    call allocates and reads back: torch then hands the memory of a workspace
+    that the call lets go of to later work on that stream only, and what it
+    hands out is free of earlier work there."""
+    if stream is None:
+        return _CURRENT
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):  # an object with a handle, or the handle
+        handle = _stream_handle(stream).value
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _dev(t, name, elem_size=None, dtype=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
@@ -281,8 +299,9 @@ def copy_blocks(k_pool, v_pool, src, dst, check_host: bool = True, src_host=None
         if sh.shape[0] != n or dh.shape[0] != n:
             raise ValueError("host id lists must match the device ones")
     elif check_host:
-        sh, sp = _host_i32(src)
-        dh, dp = _host_i32(dst)
+        with _on(stream):
+            sh, sp = _host_i32(src)
+            dh, dp = _host_i32(dst)
     st = lib.pkv_copy_blocks(ctypes.byref(c), _dev(src, "src", dtype=torch.int32),
                              _dev(dst, "dst", dtype=torch.int32), n, sp, dp, _stream_handle(stream))
     _check(st, "pkv_copy_blocks")
@@ -317,11 +336,13 @@ def decode_attention(k_pool, v_pool, q, block_tables, context_lens, max_context_
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("block_tables must be [B][max_blocks] and context_lens [B]")
     if out is None:
-        out = torch.empty((B, hq, d), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty((B, hq, d), dtype=torch.float32, device=q.device)
     if workspace is None:
         need = load().pkv_decode_workspace_size(B, hq, c.num_kv_heads, d, int(max_context_len),
                                                 int(partition_blocks))
-        workspace = new_workspace(need, q.device)  # a size of 0 means bad arguments: the call reports them
+        with _on(stream):
+            workspace = new_workspace(need, q.device)  # a size of 0 means bad arguments: the call reports them
     st = lib.pkv_decode_attention(ctypes.byref(c), _dev(q, "q", 2), hq,
                                   _dev(block_tables, "block_tables", dtype=torch.int32), int(block_tables.shape[1]),
                                   _dev(context_lens, "context_lens", dtype=torch.int32), B, int(max_context_len),
@@ -349,10 +370,12 @@ def decode_step(k_pool, v_pool, k_new, v_new, slot_mapping, q, block_tables, con
     if k_new.shape != (B, c.num_kv_heads, d) or v_new.shape != k_new.shape or slot_mapping.shape[0] != B:
         raise ValueError("k_new/v_new must be [B][num_kv_heads][head_dim] and slot_mapping [B]")
     if out is None:
-        out = torch.empty((B, hq, d), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty((B, hq, d), dtype=torch.float32, device=q.device)
     if workspace is None:
         need = lib.pkv_decode_workspace_size(B, hq, c.num_kv_heads, d, int(max_context_len), int(partition_blocks))
-        workspace = new_workspace(need, q.device)
+        with _on(stream):
+            workspace = new_workspace(need, q.device)
     st = lib.pkv_decode_step(ctypes.byref(c), _dev(k_new, "k_new", 2), _dev(v_new, "v_new", 2),
                              _dev(slot_mapping, "slot_mapping", dtype=torch.int32), _dev(q, "q", 2), hq,
                              _dev(block_tables, "block_tables", dtype=torch.int32), int(block_tables.shape[1]),
@@ -417,11 +440,13 @@ def decode_attention_shared_prefix(k_pool, v_pool, q, block_tables, context_lens
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape[0] != B:
         raise ValueError("block_tables must be [B][max_blocks] and context_lens [B]")
     if out is None:
-        out = torch.empty((B, hq, d), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty((B, hq, d), dtype=torch.float32, device=q.device)
     if workspace is None:
         need = lib.pkv_decode_shared_prefix_workspace_size(B, hq, c.num_kv_heads, d, int(max_context_len),
                                                            int(shared_blocks))
-        workspace = new_workspace(need, q.device)
+        with _on(stream):
+            workspace = new_workspace(need, q.device)
     st = lib.pkv_decode_attention_shared_prefix(
         ctypes.byref(c), _dev(q, "q", 2), hq, _dev(block_tables, "block_tables", dtype=torch.int32),
         int(block_tables.shape[1]), _dev(context_lens, "context_lens", dtype=torch.int32), B, int(max_context_len),
@@ -453,12 +478,15 @@ def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, 
         raise ValueError("query_start_loc must have num_seqs + 1 entries")
     if query_start_loc_host is None:
         query_start_loc_host = query_start_loc
-    qh, qhp = _host_i32(query_start_loc_host)
+    with _on(stream):
+        qh, qhp = _host_i32(query_start_loc_host)
     if out is None:
-        out = torch.empty((T, hq, d), dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty((T, hq, d), dtype=torch.float32, device=q.device)
     if workspace is None:
         need = load().pkv_prefill_workspace_size(S, T, hq, c.num_kv_heads, d, int(max_context_len))
-        workspace = new_workspace(need, q.device)
+        with _on(stream):
+            workspace = new_workspace(need, q.device)
     st = lib.pkv_chunked_prefill_attention(
         ctypes.byref(c), _dev(q, "q", 2), hq, T, _dev(query_start_loc, "query_start_loc", dtype=torch.int32), qhp,
         _dev(context_lens, "context_lens", dtype=torch.int32), S,
@@ -558,9 +586,11 @@ def rotary(q, k, positions, inv_freq, sections=None, interleaved_axes: bool = Fa
     Returns (q_out, k_out), contiguous; q_out may be q and k_out k."""
     torch = _torch()
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
+        with _on(stream):
+            k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device)
     st = _fast().rotary(q, k, positions, inv_freq, sections, interleaved_axes, adjacent_pairs, q_out, k_out, stream)
     if st == PKV_OK:
         return q_out, k_out
@@ -590,7 +620,8 @@ def rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_fre
     scales; their codes come from the unrounded turned k."""
     torch = _torch()
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     st = _fast().rotary_cache_write(k_pool, v_pool, q, k, v, slot_mapping, positions, inv_freq, sections,
                                     interleaved_axes, adjacent_pairs, q_out, k_scale, v_scale, stream)
     if st == PKV_OK:
@@ -637,7 +668,8 @@ def linear_decode_attention(states, log_decay, q, k, v, state_slots, context_len
     0 marks padding."""
     torch = _torch()
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     st = _fast().linear_decode(states, log_decay, q, k, v, state_slots, context_lens, scale, new_slots, out, stream)
     if st == PKV_OK:
         return out
@@ -678,13 +710,16 @@ def linear_prefill_attention(states, log_decay, q, k, v, query_start_loc, state_
     torch = _torch()
     qh = query_start_loc if query_start_loc_host is None else query_start_loc_host
     if not isinstance(qh, torch.Tensor) or qh.is_cuda or qh.dtype is not torch.int32:
-        qh = torch.from_numpy(_host_i32(qh)[0])
+        with _on(stream):
+            qh = torch.from_numpy(_host_i32(qh)[0])
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
     if workspace is None:
         need = load().pkv_linear_prefill_workspace_size(context_lens.shape[0], q.shape[0], q.shape[1], k.shape[1],
                                                         q.shape[2])
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     st = _fast().linear_prefill(states, log_decay, q, k, v, state_slots, context_lens, scale, new_slots, out, stream,
                                 query_start_loc, qh, workspace)
     if st == PKV_OK:
@@ -752,7 +787,8 @@ def prefix_keys(token_ids, token_start_loc, max_blocks: int, extra=None, parent_
     torch = _torch()
     S = int(token_start_loc.shape[0]) - 1
     if keys is None:
-        keys = torch.zeros((max(S, 1), max(max_blocks, 1), 32), dtype=torch.uint8, device=token_ids.device)
+        with _on(stream):
+            keys = torch.zeros((max(S, 1), max(max_blocks, 1), 32), dtype=torch.uint8, device=token_ids.device)
     ep = _dev(extra, "extra", dtype=torch.int64) if extra is not None else None
     pp = _dev(parent_keys, "parent_keys", dtype=torch.uint8) if parent_keys is not None else None
     st = load().pkv_prefix_keys(_dev(token_ids, "token_ids", dtype=torch.int32),
@@ -816,8 +852,9 @@ class Blocks:
         """Prefix-cache hits for empty rows: returns matched [S] (int32 CUDA)."""
         torch = _torch()
         S = int(num_keys.shape[0])
-        matched = matched if matched is not None else torch.empty((max(S, 1),), dtype=torch.int32,
-                                                                  device=self.block_tables.device)
+        if matched is None:
+            with _on(stream):
+                matched = torch.empty((max(S, 1),), dtype=torch.int32, device=self.block_tables.device)
         st = load().pkv_blocks_match(ctypes.byref(self._state()), _dev(keys, "keys", dtype=torch.uint8),
                                      int(keys.shape[1]), _dev(num_keys, "num_keys", dtype=torch.int32), S,
                                      _dev(matched, "matched", dtype=torch.int32), _stream_handle(stream))
@@ -846,10 +883,11 @@ class Blocks:
         S = int(query_start_loc.shape[0]) - 1
         dev = self.block_tables.device
         i32 = dict(dtype=torch.int32, device=dev)
-        slot_mapping = slot_mapping if slot_mapping is not None else torch.empty((num_tokens,), **i32)
-        cow_src = cow_src if cow_src is not None else torch.empty((max(S, 1),), **i32)
-        cow_dst = cow_dst if cow_dst is not None else torch.empty((max(S, 1),), **i32)
-        cow_count = cow_count if cow_count is not None else torch.empty((1,), **i32)
+        with _on(stream):
+            slot_mapping = slot_mapping if slot_mapping is not None else torch.empty((num_tokens,), **i32)
+            cow_src = cow_src if cow_src is not None else torch.empty((max(S, 1),), **i32)
+            cow_dst = cow_dst if cow_dst is not None else torch.empty((max(S, 1),), **i32)
+            cow_count = cow_count if cow_count is not None else torch.empty((1,), **i32)
         if slot_mapping.shape[0] < num_tokens or cow_src.shape[0] < S or cow_dst.shape[0] < S:
             raise ValueError("output tensors are too small")
         sp = _dev(slot_mapping, "slot_mapping", dtype=torch.int32) if num_tokens > 0 else None
