@@ -177,6 +177,7 @@ struct ChunkParams {
     int32_t units;          // chunks the host counted
     int32_t subs;           // CTAs a kv head's group of q heads is dealt to
     int32_t overflow;       // K and V, which are read twice, are more than the L2 keeps
+    int32_t cut;            // the ranges' own states are there and joined
 };
 
 // One warp: calls f(sequence s, what it is, its first unit, the unit behind
@@ -404,6 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.seq = s;
                 g.first = c0 == 0;
                 bad = q.bad;
+                // Device lengths that are not the host's: the plan cuts no
+                // sequence, or ends before this one does, so its states are
+                // not carried over the border.
+                if (!P.cut ? c0 > 0 || end > u1 : end > u1 && blockIdx.x == gridDim.x - 1) {
+                    if (reports) record_error(A.err, kErrRange, static_cast<uint32_t>(s));
+                    bad = 1;
+                }
                 n = bad ? 0 : c1 - c0;
                 if (bad) g.rows = -g.rows;
                 segs[k] = g;
@@ -1269,6 +1277,7 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.range = plan.range;
     P.units = plan.units;
     P.subs = plan.subs;
+    P.cut = plan.cut;
     P.overflow = static_cast<int64_t>(plan.units) * C * a.num_kv_heads * a.head_dim * 4 > kOverflowBytes;
     LinearScan scan = {};
     cudaError_t e = cudaSuccess;
