@@ -60,14 +60,21 @@ __device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& A, int s, bool
     return q;
 }
 
-// Whether a sequence reads or stores (for the check of shared slots).
+// Whether a sequence reads or stores that slot (for the check of shared
+// slots): as linear_seq has it, where one that is skipped or refused does
+// neither.
 __device__ __forceinline__ bool linear_shares(const LinearArgs& A, int other, int store) {
+    const int from = __ldg(A.state_slots + other), to = __ldg(A.new_slots + other);
+    if ((from != store && to != store) || to >= A.num_slots) return false;
     const int n = __ldg(A.context_lens + other);
     int rows = 1;
-    if (A.query_start_loc != nullptr)
-        rows = __ldg(A.query_start_loc + other + 1) - __ldg(A.query_start_loc + other);
+    if (A.query_start_loc != nullptr) {
+        const int row0 = __ldg(A.query_start_loc + other), end = __ldg(A.query_start_loc + other + 1);
+        if (row0 < 0 || end > A.num_tokens) return false;
+        rows = end - row0;
+    }
     if (rows <= 0 || n < rows) return false;
-    return __ldg(A.new_slots + other) == store || (n > rows && __ldg(A.state_slots + other) == store);
+    return n == rows ? to == store : from >= 0 && from < A.num_slots;
 }
 
 // A log decay above 0 or NaN counts as 0 and is reported; -inf keeps nothing.
