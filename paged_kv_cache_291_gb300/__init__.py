@@ -17,6 +17,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import warnings
 from typing import Optional, Tuple
 
 __all__ = [
@@ -90,7 +91,7 @@ def lib_path() -> str:
 
 def load():
     """Load libpagedkv.so (raises if it is missing: there is no fallback)."""
-    global _lib, _calls
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
@@ -140,22 +141,36 @@ def load():
         fn = getattr(lib, name)
         fn.argtypes = argt
         fn.restype = rest
-    try:
-        from . import _binding
-    except ImportError as e:
-        raise RuntimeError("the package's _binding module is not built; run `python -m "
-                           f"paged_kv_cache_291_gb300.build` or __graft_entry__.build() first ({e})") from e
-    _calls = _binding
     _lib = lib
     return lib
+
+
+class _NoCalls:
+    """In place of the compiled calls, where they cannot be loaded."""
+
+    @staticmethod
+    def rotary(*args):
+        return None
+
+    rotary_cache_write = linear_decode = linear_prefill = rotary
 
 
 def _fast():
     """The compiled calls (csrc/binding.cpp).  Each returns the status of a
     plain valid call it has made, or None without having launched anything:
-    then the wrapper's own checks say what is wrong, or it makes the call."""
+    then the wrapper's own checks say what is wrong, or it makes the call.
+    The module belongs to the torch it was built against; without it, which
+    is said once, the wrappers make every call of the library themselves."""
+    global _calls
     if _calls is None:
         load()
+        try:
+            from . import _binding
+            _calls = _binding
+        except ImportError as e:
+            warnings.warn("the package's _binding module is not built for this torch, so calls take longer on the "
+                          f"host; run `python -m paged_kv_cache_291_gb300.build` ({e})", RuntimeWarning, stacklevel=3)
+            _calls = _NoCalls
     return _calls
 
 

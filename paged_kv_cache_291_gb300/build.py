@@ -4,12 +4,14 @@ Each .cu under csrc/ is compiled to an object in parallel, then the objects
 are linked into ``libpagedkv.so`` beside this file (CUDA runtime linked
 statically, only the ``pkv_*`` symbols exported).  csrc/binding.cpp, the
 CPython module that hands torch tensors to some of the calls, is compiled
-against the installed torch at the same time.  Used by
+against the installed torch at the same time; without a torch, or where that
+module does not build, the library is complete all the same.  Used by
 ``__graft_entry__.build()`` and by the package on import when the library is
 stale; it needs nvcc but no GPU.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -46,10 +48,14 @@ def _deps():
     return files
 
 
+def _targets():
+    return [LIB, BINDING] if importlib.util.find_spec("torch") is not None else [LIB]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    if not all(os.path.exists(f) for f in _targets()):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in _targets())
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -90,15 +96,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
             raise RuntimeError(f"{cmd[0]} failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
 
     with ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(compile_binding)
+        binding = ex.submit(compile_binding) if BINDING in _targets() else None
         objs = list(ex.map(compile_one, sources()))
-        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, "-shared"] + ARCH + ["-o", tmp] + objs + ["-Xcompiler", "-fPIC"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if binding is None:
+        return LIB
+    binding.result()
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = BINDING + f".tmp{os.getpid()}"
