@@ -328,8 +328,10 @@ __device__ __forceinline__ void mma_state(uint32_t col_s, uint32_t svt, uint32_t
     }
 }
 
-// G: q heads per CTA.
-template <int D, int G>
+// G: q heads per CTA.  DEALT: the group's q heads are dealt to P.subs CTAs,
+// otherwise one (a kernel starts with cold instructions: without the counting
+// 30 ranges of two chunks, 3 heads of 64, take 21.1 us and with it 22.1).
+template <int D, int G, bool DEALT>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const ChunkParams P) {
@@ -344,8 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = &rest.tmem;
     const LinearArgs& A = P.A;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int h = blockIdx.y / P.subs, sub = blockIdx.y % P.subs;
-    const int hq0 = (h * P.subs + sub) * G;  // first of this CTA's q heads
+    const int subs = DEALT ? P.subs : 1;
+    const int h = blockIdx.y / subs, sub = blockIdx.y % subs;
+    const int hq0 = (h * subs + sub) * G;  // first of this CTA's q heads
     const bool reports = blockIdx.y == 0;
 
     // ---------------------------------------------------------- setup
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool place = c0 == 0 && q.load >= 0 && q.load == q.store;
                 g.load = c0 > 0 ? kFromBounds : place && end > u1 ? kFromStarts : q.load;
                 if (end > u1) g.store = -1;
-                else if (place && P.subs > 1) g.store = -2 - q.store;
+                else if (DEALT && place) g.store = -2 - q.store;
                 else g.store = sub == 0 ? q.store : -1;
                 g.seq = s;
                 g.first = c0 == 0;
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_S]);
-                if (store < -1 && left == rows && lane == 0) {
+                if (DEALT && store < -1 && left == rows && lane == 0) {
                     // The same warp of every CTA that reads the slot holds the
                     // same part of the state.  Whoever comes last here
                     // knows that the others have read it, and stores it at
@@ -699,9 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!ok || store == -1) continue;
-            __syncwarp();
-            if (store < -1 && !rest.stores[warp - kSWarp]) continue;
-            const int slot = store < -1 ? -2 - store : store;
+            int slot = store;
+            if constexpr (DEALT) {
+                __syncwarp();
+                if (store < -1) {
+                    if (!rest.stores[warp - kSWarp]) continue;
+                    slot = -2 - store;
+                }
+            }
             if (!warp_wait(&bar[B_VTFREE], (i - 1) & 1)) { ok = false; break; }
             tc::fence_after_sync();
             if (live) {
@@ -907,14 +915,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // goes on in the next range: sum_s lam^(end-1-s) k_s v_s^T over the segment's
 // tokens, one accumulation with no rescaling (the factor of a chunk's end is
 // part of V~).  Warps 0-7 make V~, 8 loads, 9 issues the MMAs; warps 0-3
-// store the sum.  Warps 10-13 copy the state that the call replaces in place,
-// if it does: beside the others, where it costs nothing (after them it was
-// 1.3 us of a prompt of 300 tokens).  There is room in tensor memory here, so V~ goes there: it
+// store the sum.  Warps 10 and 11 copy the state that the call replaces in place,
+// if it does: beside the others (after them it was 1.3 us of a prompt of 300
+// tokens).  There is room in tensor memory here, so V~ goes there: it
 // is read from the V tile by transposing 8x8 loads, whose fragments are what
 // a 16-lane store takes, and the product needs shared memory for K alone.
 // (With V~ in shared memory the kernel was bound by it: 31 us for 8 ranges of
 // 29 chunks and 16 heads of 128.)
-constexpr int kStateThreads = 448;
+constexpr int kStateThreads = 384;
 constexpr int kStateStages = 5;
 constexpr int kTile = 2 * kPanel;        // room for head_dim 128
 constexpr int SOFF_K = 0;
@@ -1037,7 +1045,7 @@ __global__ void __launch_bounds__(kStateThreads, 1)
                 A.states + (static_cast<int64_t>(info[2]) * A.num_kv_heads + h) * D * D);
             float4* dst = reinterpret_cast<float4*>(
                 P.starts + (static_cast<int64_t>(blockIdx.x) * A.num_kv_heads + h) * D * D);
-            constexpr int kCopiers = kStateThreads - 320, kAhead = 8;
+            constexpr int kCopiers = kStateThreads - 320, kAhead = 16;
 #pragma unroll 1
             for (int at = threadIdx.x - 320; at < D * D / 4; at += kCopiers * kAhead) {
                 float4 x[kAhead];
@@ -1117,6 +1125,15 @@ __global__ void __launch_bounds__(kScanThreads) linear_scan_kernel(const LinearA
     scan_ranges(A, S, blockIdx.x);
 }
 
+// The counters of dealt q heads, where linear_state_kernel does not clear them.
+__global__ void __launch_bounds__(kScanThreads) linear_clear_kernel(uint32_t* claims, int64_t n) {
+    griddep_launch_dependents();
+    griddep_wait();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kScanThreads + threadIdx.x; i < n;
+         i += static_cast<int64_t>(gridDim.x) * kScanThreads)
+        claims[i] = 0;
+}
+
 bool rows_map(CUtensorMap* map, const void* base, int64_t stride, int32_t heads, int32_t d, int32_t tokens) {
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
                                 static_cast<cuuint64_t>(tokens)};
@@ -1135,13 +1152,13 @@ cudaError_t configure(K kernel, int smem, bool (&done)[64]) {
     return e;
 }
 
-template <int D, int G>
+template <int D, int G, bool DEALT>
 cudaError_t launch_main(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
                         cudaStream_t stream) {
     static bool done[64] = {};
-    cudaError_t e = configure(linear_chunk_kernel<D, G>, smem_bytes<D>(), done);
+    cudaError_t e = configure(linear_chunk_kernel<D, G, DEALT>, smem_bytes<D>(), done);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(linear_chunk_kernel<D, G>, dim3(P.ranges, P.A.num_kv_heads * P.subs), dim3(kThreads),
+    return launch_overlapped(linear_chunk_kernel<D, G, DEALT>, dim3(P.ranges, P.A.num_kv_heads * P.subs), dim3(kThreads),
                              smem_bytes<D>(), stream, tq, tk, tv, P);
 }
 
@@ -1154,14 +1171,14 @@ cudaError_t launch_state(const CUtensorMap& tk, const CUtensorMap& tv, const Chu
                              STATE_SMEM, stream, tk, tv, P);
 }
 
-template <int D>
+template <int D, bool DEALT>
 cudaError_t launch_groups(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& P,
                           cudaStream_t stream) {
     switch (P.A.num_q_heads / P.A.num_kv_heads / P.subs) {
-        case 1: return launch_main<D, 1>(tq, tk, tv, P, stream);
-        case 2: return launch_main<D, 2>(tq, tk, tv, P, stream);
-        case 4: return launch_main<D, 4>(tq, tk, tv, P, stream);
-        default: return launch_main<D, 8>(tq, tk, tv, P, stream);
+        case 1: return launch_main<D, 1, DEALT>(tq, tk, tv, P, stream);
+        case 2: return launch_main<D, 2, DEALT>(tq, tk, tv, P, stream);
+        case 4: return launch_main<D, 4, DEALT>(tq, tk, tv, P, stream);
+        default: return launch_main<D, DEALT ? 4 : 8, DEALT>(tq, tk, tv, P, stream);  // 8 are never dealt
     }
 }
 
@@ -1213,8 +1230,8 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     // SMs; where they cut sequences, the state kernel reads K and V of all but
     // the last range once more, and the states are carried over.  Dealing a
     // group's q heads to several CTAs fills SMs too, repeats the state's work
-    // in each, and takes a launch that clears their counters where there is
-    // none before the main kernel anyway.  The constants are fitted to the times of forced plans
+    // in each, and takes a launch that clears their counters where the state
+    // kernel is not there to do it.  The constants are fitted to the times of forced plans
     // over nine batches (128 to 16,384 tokens, both widths, one sequence and
     // many); the plans taken are within 4 % of the best forced one.
     const bool narrow = head_dim == 64;
@@ -1234,7 +1251,7 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
             bool cut = false;  // whether a border lies inside a sequence
             for (int64_t u = range; u < units && !cut; u += range) cut = !begins || begins[u] == 0;
             if (cut) us += 7.0 + 0.15 * ranges + ((ranges - 1) * num_kv_heads + num_sms - 1) / num_sms * range * state;
-            if (subs > 1 && !cut && best.recurrent == 0) us += clear;
+            if (subs > 1 && !cut) us += clear;
             if (us >= best_us) return;
             best_us = us;
             best.ranges = static_cast<int32_t>(ranges);
@@ -1281,12 +1298,6 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     P.overflow = static_cast<int64_t>(plan.units) * C * a.num_kv_heads * a.head_dim * 4 > kOverflowBytes;
     LinearScan scan = {};
     cudaError_t e = cudaSuccess;
-    if (plan.subs > 1 && !plan.cut) {
-        scan.claims = P.claims;
-        scan.num_claims = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-        const int64_t blocks = (scan.num_claims + 8 * kScanThreads - 1) / (8 * kScanThreads);
-        scan.blocks = static_cast<int32_t>(blocks < num_sms ? blocks : num_sms);
-    }
     if (plan.cut) {
         e = a.head_dim == 64 ? launch_state<64>(tk, tv, P, stream) : launch_state<128>(tk, tv, P, stream);
         if (e != cudaSuccess) return e;
@@ -1299,10 +1310,21 @@ cudaError_t launch_linear_prefill(const LinearArgs& a, const LinearPlan& plan, v
     // The scan rides in the recurrent form's grid where there is one.
     if (plan.recurrent > 0)
         e = launch_linear_recurrent(a, plan.recurrent, scan, stream);
-    else if (scan.blocks > 0)
+    else if (plan.cut)
         e = launch_overlapped(linear_scan_kernel, dim3(scan.blocks), dim3(kScanThreads), 0, stream, a, scan);
     if (e != cudaSuccess) return e;
-    return a.head_dim == 64 ? launch_groups<64>(tq, tk, tv, P, stream) : launch_groups<128>(tq, tk, tv, P, stream);
+    if (plan.subs > 1 && !plan.cut) {
+        const int64_t n = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+        const int64_t blocks = (n + 8 * kScanThreads - 1) / (8 * kScanThreads);
+        e = launch_overlapped(linear_clear_kernel, dim3(static_cast<unsigned>(blocks < num_sms ? blocks : num_sms)),
+                              dim3(kScanThreads), 0, stream, P.claims, n);
+        if (e != cudaSuccess) return e;
+    }
+    if (P.subs > 1)
+        return a.head_dim == 64 ? launch_groups<64, true>(tq, tk, tv, P, stream)
+                                : launch_groups<128, true>(tq, tk, tv, P, stream);
+    return a.head_dim == 64 ? launch_groups<64, false>(tq, tk, tv, P, stream)
+                            : launch_groups<128, false>(tq, tk, tv, P, stream);
 }
 
 }  // namespace pkv

@@ -130,16 +130,10 @@ constexpr int kLinearChunk = 64;  // tokens of a chunk
 // lam^(tokens of the segment) (state before it) + bounds[x], in order, the
 // state before being the sequence's where the segment begins it and
 // bounds[x - 1] otherwise.  Block `block` of S.blocks; a thread carries two
-// elements.  Without ranges there are only counters to clear.
+// elements.
 __device__ __forceinline__ void scan_ranges(const LinearArgs& A, const LinearScan& S, int block) {
     __shared__ float2 lam_s;
     __shared__ __align__(16) int4 tails[kScanThreads];
-    if (S.ranges == 0) {
-        for (int64_t i = static_cast<int64_t>(block) * kScanThreads + threadIdx.x; i < S.num_claims;
-             i += static_cast<int64_t>(S.blocks) * kScanThreads)
-            S.claims[i] = 0;
-        return;
-    }
     const int slices = A.head_dim * A.head_dim / (2 * kScanThreads);
     const int h = block / slices, tid = threadIdx.x;
     const float g = clean_log_decay(A, h, false);

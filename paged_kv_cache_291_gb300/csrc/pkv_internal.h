@@ -180,16 +180,13 @@ struct LinearArgs {
     float scale;
 };
 
-// What goes before the chunked form's main kernel: the join of its ranges,
-// and counters to clear (linear_device.cuh).
+// The join of the chunked form's ranges (linear_device.cuh).
 struct LinearScan {
     float* bounds;
     const int4* tails;
-    uint32_t* claims;    // counters to clear where there is nothing to join
-    int64_t num_claims;
-    int32_t ranges;      // 0: nothing to join
+    int32_t ranges;
     int32_t tokens;      // of a whole range
-    int32_t blocks;      // 0: nothing to do
+    int32_t blocks;      // 0: nothing to join
 };
 
 // longest: rows of the longest sequence it will meet; scan.blocks more CTAs
