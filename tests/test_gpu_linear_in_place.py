@@ -147,3 +147,21 @@ def test_in_place_while_another_stream_holds_multiprocessors(pkv):
             assert torch.equal(states[dev_tensor(b.slots).long()], after[dev_tensor(b.new).long()])
         for x in others:
             assert torch.equal(x, want_other)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d", [([100] * 40, 32, 8, 64), ([90, 64, 3, 200, 1, 70, 65], 16, 2, 64),
+                                           ([500, 300, 640], 16, 8, 128)])
+def test_counters_and_copies_stay_in_a_workspace_that_needs_no_clearing(pkv, lens, hq, hkv, d):
+    """Dealt heads alone, both, and a cut alone, in a workspace of the size
+    asked for, full of ones before each call."""
+    b = Batch(270 + len(lens), lens, [4] * len(lens), hq, hkv, d)
+    want, after = run(pkv, b, dev_tensor(b.new), dev_tensor(b.S0))
+    need = pkv.linear_prefill_workspace_size(len(lens), b.T, hq, hkv, d)
+    ws = torch.empty(need + 4096, dtype=torch.uint8, device="cuda")
+    for fill in (0xFF, 0x11, 0):
+        ws.fill_(fill)
+        out, states = run(pkv, b, None, dev_tensor(b.S0), workspace=ws[:need])
+        assert pkv.get_error() == (0, 0)
+        assert torch.all(ws[need:] == fill)
+        assert torch.equal(out, want)
+        assert torch.equal(states[dev_tensor(b.slots).long()], after[dev_tensor(b.new).long()])
