@@ -376,7 +376,8 @@ pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const void* q
  * positions (time, height, width), each turning its own share of the pairs.
  *
  * For token t and pair i < rot_dim/2, with a = positions[axis(i)][t] *
- * inv_freq[i] radians (the product exact, whatever the position),
+ * inv_freq[i] radians (off by 2^-47 of its size at most, whatever the
+ * position),
  *     (x, y) -> (x cos a - y sin a, x sin a + y cos a)
  * where (x, y) are the elements (i, i + rot_dim/2) of the row, or
  * (2i, 2i + 1) with PKV_ROTARY_ADJACENT_PAIRS.  Elements from rot_dim on are
@@ -458,7 +459,8 @@ pkv_status pkv_rotary_cache_write(const pkv_cache_t* cache, const pkv_rotary_t* 
  *                  not be stored to by two sequences of a call, nor stored
  *                  to by one and read by another: that raises PKV_ERR_ALIAS
  *                  on the device (detail: the sequence), and the results of
- *                  those sequences are then not valid
+ *                  those sequences are then not valid.  A sequence that is
+ *                  skipped or refused neither reads nor stores
  *   A slot >= num_slots that would be used raises PKV_ERR_RANGE on the
  *   device; the sequence's out rows are then zero and nothing is stored.
  *   log_decay      <= 0 (0 keeps everything, -inf nothing).  A value above 0
@@ -511,11 +513,18 @@ size_t pkv_linear_prefill_workspace_size(int32_t num_seqs, int32_t num_tokens, i
  *                  sequence (query_start_loc[num_seqs] < num_tokens) are
  *                  allowed, and left as they were in out.  Device values that
  *                  differ from the host's raise PKV_ERR_RANGE where rows are
- *                  out of range or missed
+ *                  out of range or missed, or where a sequence would need
+ *                  states that the host's values plan nothing for (its rows
+ *                  are then zero and nothing is stored); host values without
+ *                  rows launch nothing
  *   workspace      >= pkv_linear_prefill_workspace_size() bytes, 256-byte
  *                  aligned; scratch, need not be cleared.  Calls that run
  *                  concurrently need separate workspaces
  *   The other arguments are those of pkv_linear_decode_attention.
+ *   Results in place are those with separate slots, bit for bit.  The states
+ *   and weighted scores go whole (24 bits) into tensor-core products, whose
+ *   fp32 sums truncate where an fp32 add rounds: outputs and states are off by
+ *   2e-7 to 7e-7 of their norm (300 to 16,384 tokens), fp32 adds by 2e-7.
  */
 pkv_status pkv_linear_prefill_attention(const pkv_states_t* states, const void* q, int64_t q_stride,
                                         int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,

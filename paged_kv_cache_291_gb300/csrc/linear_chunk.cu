@@ -13,9 +13,11 @@
 //
 // Precision.  q, k and v are exact in bf16; S, P and V~ are fp32 values.  Each
 // is split into three bf16 terms (8 + 8 + 8 bits, exact), and
-// its product is taken three times, so the result is an fp32 one.  Two terms
-// (16 bits) would be off by 2^-17 of each value.  The state's decay factor is
-// an fp32 pair.
+// its product is taken three times, so that operands of 24 bits go in whole;
+// two terms would be off by up to 2^-19 of a value's binade.  The products'
+// fp32 sums truncate, where an fp32 add rounds: 300 tokens are off by 2.3e-7
+// of the norm, 16,384 by 5.9e-7 to 6.6e-7, plain fp32 sums by 2.1e-7 and
+// 2.3e-7.  The state's decay factor is an fp32 pair.
 //
 // Split.  A CTA takes one kv head of a range of chunks and walks them; all q
 // heads of the group share the state's work.  Its warps have
@@ -34,9 +36,9 @@
 // Bound.  A chunk's chain: the state is split (1,500 to 2,000 cycles), read by
 // the outputs' product (900), updated (900).  At head_dim 128 and one q head a
 // chunk takes 5,000 cycles against 3,500 of its bytes at HBM's rate; the
-// tensor pipe is 39% active and nothing is full.  16,384 tokens of 16 heads of
+// tensor pipe is 38% active and nothing is full.  16,384 tokens of 16 heads of
 // 128: 119 us (states of the ranges 24, scan 5, main 85); 12 prompts, 6,171
-// tokens, 32/8 heads of 64: 52 us.
+// tokens, 32/8 heads of 64: 53 us.
 //
 // Every wait is bounded; TMEM is freed on every exit path.
 #include <cuda.h>
@@ -112,8 +114,8 @@ constexpr int kFromBounds = -2, kFromStarts = -3;
 // main one.  When they are more than the L2 keeps beside the rest, the oldest
 // lines, which are wanted first, would go first: the state kernel then loads
 // with evict_first, so that its later tiles replace each other.  16 heads of
-// 128, 50 MB of K and V: 60.4 to 58.4 us; 134 MB: 123.9 to 119.8; 34 MB: 48.1
-// both ways; a mixed batch with 13 MB: 32.6 to 33.1, which is why not always.
+// 128, calls on the same inputs in a graph: 134 MB of K and V 121.7 to 117.3
+// us, 67 MB 70.2 to 68.5, 50 MB 54.9 and 55.0, 34 MB 41.8 both ways.
 constexpr int64_t kOverflowBytes = 40 << 20;
 
 struct Segment {

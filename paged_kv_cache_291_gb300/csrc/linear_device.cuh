@@ -91,8 +91,8 @@ __device__ __forceinline__ float clean_log_decay(const LinearArgs& A, int h, boo
 // exp(g * tokens) as hi + lo, g <= 0.  A state is multiplied by it once per
 // token or chunk, so the 2^-25 of one fp32 factor would grow with the length
 // of the context.  x = g * tokens as an fp32 pair; n = the nearest whole
-// multiple of ln 2, r = x - n ln 2 (ln 2 in two parts, the first short enough
-// that n times it is exact), |r| <= 0.35; exp(r) = 1 + r + r^2 (1/2 + r/6 +
+// multiple of ln 2, r = x - n ln 2 (Cody and Waite's reduction: ln 2 in two
+// parts, the first short enough that n times it is exact), |r| <= 0.35; exp(r) = 1 + r + r^2 (1/2 + r/6 +
 // ...), the Taylor terms from r^2 on in fp32: off by 2^-24 of r^2 / 2, which
 // for the slow decays, where it counts, is far below 2^-40.
 __device__ __forceinline__ float2 decay_pair(float g, int tokens) {
