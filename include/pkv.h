@@ -377,7 +377,7 @@ pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const void* q
  *
  * For token t and pair i < rot_dim/2, with a = positions[axis(i)][t] *
  * inv_freq[i] radians (off by 2^-47 of its size at most, whatever the
- * position),
+ * position, before what is left of it within a turn becomes an fp32 value),
  *     (x, y) -> (x cos a - y sin a, x sin a + y cos a)
  * where (x, y) are the elements (i, i + rot_dim/2) of the row, or
  * (2i, 2i + 1) with PKV_ROTARY_ADJACENT_PAIRS.  Elements from rot_dim on are

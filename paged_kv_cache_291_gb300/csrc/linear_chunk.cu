@@ -1233,9 +1233,9 @@ LinearPlan plan_linear(const int32_t* qsl, int32_t num_seqs, int32_t num_tokens,
     // the last range once more, and the states are carried over.  Dealing a
     // group's q heads to several CTAs fills SMs too, repeats the state's work
     // in each, and takes a launch that clears their counters where the state
-    // kernel is not there to do it.  The constants are fitted to the times of forced plans
-    // over nine batches (128 to 16,384 tokens, both widths, one sequence and
-    // many); the plans taken are within 4 % of the best forced one.
+    // kernel is not there to do it.  The constants are fitted to the times of
+    // forced plans over nine batches (128 to 16,384 tokens, both widths, one
+    // sequence and many), of which the plans taken were within 4 % of the best.
     const bool narrow = head_dim == 64;
     const double fixed = narrow ? 0.45 : 1.3, item = narrow ? 1.25 : 1.3, state = narrow ? 0.5 : 1.0, start = 5.5,
                  clear = 0.9;

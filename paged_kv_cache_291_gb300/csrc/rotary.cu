@@ -46,7 +46,7 @@ __device__ __forceinline__ void turn_of(float f, int32_t pos, float& c, float& s
     float hi = f * kHi;
     float lo = fmaf(f, kLo, fmaf(f, kHi, -hi));
     hi -= rintf(hi);  // exact; whole turns do not matter
-    lo -= rintf(lo);  // nor here: above 2^24 radians a step this part has some too
+    lo -= rintf(lo);  // above 2^23 turns a step this part has some too
     const long long step = __float2ll_rn(hi * 0x1p64f) + __float2ll_rn(lo * 0x1p64f);
     const unsigned long long turns =
         static_cast<unsigned long long>(step) * static_cast<unsigned long long>(static_cast<long long>(pos));
