@@ -73,7 +73,7 @@ typedef enum pkv_status {
     PKV_ERR_NO_BLOCKS = 14,  /* (device) the free queue cannot supply the blocks an append needs */
     PKV_ERR_HOST_MEMORY = 15, /* a host buffer is not page-locked memory mapped for the device   */
     PKV_ERR_DTYPE = 16       /* kv_dtype unknown, e4m3 scales not finite and > 0, or the call
-                                does not take an e4m3 pool                                     */
+                                does not take a pool of that kind                              */
 } pkv_status;
 
 /*
@@ -84,8 +84,21 @@ typedef enum pkv_status {
  * pool.  The pages have no fp8 pool: it is the bandwidth-halving variant of
  * the write and the gather, chosen because decode reads the whole cache every
  * step ([ENG] "Prefill/Decode").
+ *
+ * PKV_KV_E4M3_BLOCKS and PKV_KV_INT8_BLOCKS hold 8-bit codes with a scale for
+ * each (block, kv head), K and V apart: an element stands for value(code) *
+ * block_scales[block][kv head][0 for K, 1 for V], value being that of the
+ * e4m3 code or of the signed 8-bit integer.  A scale follows the rows that
+ * are in the block, so one pool serves layers and heads of any magnitude.
+ * pkv_cache_append writes them, pkv_cache_read reads rows back, the attention
+ * calls and the block copies and swaps take them; pkv_cache_write,
+ * pkv_rotary_cache_write and pkv_decode_step, which store rows one by one,
+ * refuse them (PKV_ERR_DTYPE).
+ * A scale that a call uses is finite and at least 2^-100; another one raises
+ * PKV_ERR_RANGE on the device and counts as 2^-100.  No code of an int8 pool
+ * is -128 after pkv_cache_append (if found, it counts as -128).
  */
-enum { PKV_KV_BF16 = 0, PKV_KV_E4M3 = 1 };
+enum { PKV_KV_BF16 = 0, PKV_KV_E4M3 = 1, PKV_KV_E4M3_BLOCKS = 2, PKV_KV_INT8_BLOCKS = 3 };
 
 typedef struct pkv_cache {
     void* k_pool;         /* elem [num_blocks][num_kv_heads][16][head_dim], device        */
@@ -94,10 +107,12 @@ typedef struct pkv_cache {
     int32_t num_kv_heads; /* >= 1                                                         */
     int32_t head_dim;     /* 64 or 128                                                    */
     int32_t block_size;   /* tokens per block; must be 16 ([KV2] section 2 default)       */
-    int32_t kv_dtype;     /* PKV_KV_BF16 (0, also what zero-initialisation gives) or
-                             PKV_KV_E4M3                                                   */
-    float k_scale;        /* e4m3 pools: K element = value(code) * k_scale; finite, > 0    */
-    float v_scale;        /* e4m3 pools: V element = value(code) * v_scale; ignored for bf16 */
+    int32_t kv_dtype;     /* PKV_KV_BF16 (0, also what zero-initialisation gives), or
+                             another PKV_KV_*                                              */
+    float k_scale;        /* PKV_KV_E4M3: K element = value(code) * k_scale; finite, > 0   */
+    float v_scale;        /* PKV_KV_E4M3: V element = value(code) * v_scale; ignored for the others */
+    float* block_scales;  /* PKV_KV_*_BLOCKS: fp32 [num_blocks][num_kv_heads][2], device,
+                             16-byte aligned; not looked at for the others                 */
 } pkv_cache_t;
 
 /*
@@ -121,6 +136,70 @@ pkv_status pkv_cache_write(const pkv_cache_t* cache, const void* k_new, const vo
                            const int32_t* slot_mapping, int32_t num_tokens, void* stream);
 
 /*
+ * pkv_cache_append -- store the step's new K/V rows in 8 bits, with a scale
+ * for each (block, kv head): the write of the PKV_KV_*_BLOCKS pools.  The
+ * rows are those at the ends of the sequences' contexts, so a block's rows
+ * are known together, which a scale for the block needs.
+ *
+ *   k_new, v_new     bf16 [num_tokens][num_kv_heads][head_dim]; the rows of a
+ *                    token are contiguous, and a token's rows lie k_stride
+ *                    (v_stride) elements after the last token's: a multiple
+ *                    of 8, at least num_kv_heads * head_dim
+ *   query_start_loc  int32 [num_seqs+1], device: sequence s owns the rows
+ *                    query_start_loc[s] .. query_start_loc[s+1]-1, non-decreasing
+ *                    from 0.  Rows behind the last sequence are not stored
+ *   context_lens     int32 [num_seqs], including the new rows: row i of a
+ *                    sequence's n rows goes to position context_lens[s] - n + i,
+ *                    row (position % 16) of block block_tables[s][position / 16]
+ *   block_tables     int32 [num_seqs][max_blocks_per_seq]
+ *
+ *   Per touched (block, kv head), K and V apart, in fp32 with one rounding
+ *   an operation, and amax the largest |x| of the block's new rows:
+ *       scale = max(old, amax * (1 / L), 2^-100),    L = 448 (e4m3) or 127 (int8)
+ *       code(x) = the code nearest to x * (1 / scale), ties to even, at most L
+ *   old is the block's scale when it held rows of the context before the
+ *   call, and 0 when its first row is among the new ones (the block starts
+ *   anew, whatever it held).  Where the scale has grown, the earlier rows are
+ *   encoded again, from value(code) * (old * (1 / scale)): each growth costs
+ *   them half a step of the new scale at most.  Rows of the block behind the
+ *   context are left as they are.
+ *   Values that are not finite do not count in amax.  An infinity is stored as
+ *   the largest code of its sign, a NaN as the NaN code (e4m3) or 0 (int8),
+ *   and either raises PKV_ERR_RANGE (detail: the sequence) once stored.
+ *   A block must not be appended to by two sequences of a call (copy-on-write
+ *   sees to that), nor be shared beyond its earlier rows' owner.
+ *   PKV_ERR_RANGE on the device (detail: the sequence) for rows out of range,
+ *   a context shorter than its rows or longer than the table, or a block id
+ *   out of range: those rows are not stored.  num_tokens == 0 or num_seqs ==
+ *   0 is a no-op.
+ */
+pkv_status pkv_cache_append(const pkv_cache_t* cache, const void* k_new, int64_t k_stride, const void* v_new,
+                            int64_t v_stride, int32_t num_tokens, const int32_t* query_start_loc,
+                            const int32_t* context_lens, int32_t num_seqs, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, void* stream);
+
+/*
+ * pkv_cache_read -- rows of the cache back as bf16, in the order of their
+ * sequences: the inverse of the write, for pools of every kind.  Sequence s
+ * takes rows query_start_loc[s] .. query_start_loc[s+1]-1 of the outputs for
+ * the last rows of its context (as many as it has; its whole context where
+ * they are equal).
+ *
+ *   k_out, v_out     bf16 [num_tokens][num_kv_heads][head_dim], contiguous,
+ *                    device; value(code) * scale, the product in fp32, rounded
+ *                    to bf16 (to nearest even); bf16 pools bit for bit.  They
+ *                    must not overlap each other, the pools or the scales
+ *                    (PKV_ERR_ALIAS)
+ *   The other arguments and the device errors are those of pkv_cache_append.
+ *   A sequence that is out of range gets zero rows where its rows are inside
+ *   the outputs, a block id out of range zero rows for that block; rows
+ *   behind the last sequence are left as they were.
+ */
+pkv_status pkv_cache_read(const pkv_cache_t* cache, void* k_out, void* v_out, int32_t num_tokens,
+                          const int32_t* query_start_loc, const int32_t* context_lens, int32_t num_seqs,
+                          const int32_t* block_tables, int32_t max_blocks_per_seq, void* stream);
+
+/*
  * pkv_copy_blocks -- copy-on-write of shared blocks.
  * [KV2] section 2, "Sharing blocks": requests may point at the same physical
  * block under a reference count; a block is copied only when someone must
@@ -136,7 +215,7 @@ pkv_status pkv_cache_write(const pkv_cache_t* cache, const void* k_new, const vo
  *                         ids are in range (PKV_ERR_RANGE) before launching.
  *                         The same src may appear many times.
  *   Other ids out of range found on the device are skipped and raise
- *   PKV_ERR_RANGE.
+ *   PKV_ERR_RANGE.  Pools with a scale per block: the scales are copied too.
  */
 pkv_status pkv_copy_blocks(const pkv_cache_t* cache, const int32_t* src, const int32_t* dst, int32_t num_pairs,
                            const int32_t* src_host, const int32_t* dst_host, void* stream);
@@ -157,7 +236,9 @@ pkv_status pkv_copy_blocks(const pkv_cache_t* cache, const int32_t* src, const i
  *                  16-byte aligned, holding num_host_slots slabs of
  *                  [2][num_kv_heads][16][head_dim] pool elements (the K block, then the
  *                  V block); the kernel reads and writes it directly, over the
- *                  host link, bit-exact
+ *                  host link, bit-exact.  Pools with a scale per block: a slab goes on
+ *                  with the block's scales, fp32 [num_kv_heads][2], and ends at the next
+ *                  multiple of 16 bytes
  *   Returns PKV_ERR_HOST_MEMORY, launching nothing, when `host` is not such
  *   memory.  Block ids or slots out of range found on the device are skipped
  *   and raise PKV_ERR_RANGE.  n <= 65535 pairs per call.

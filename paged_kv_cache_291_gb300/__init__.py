@@ -10,7 +10,10 @@ or ``__graft_entry__.build()``).
 
 Tensors: K/V pools are 2-byte (bf16) CUDA tensors
 ``[num_blocks][num_kv_heads][16][head_dim]``; q/k_new/v_new bf16; index
-arrays int32; outputs float32.
+arrays int32; outputs float32.  8-bit pools are uint8 or float8_e4m3fn
+(e4m3 codes) with ``k_scale`` and ``v_scale``, or, with ``block_scales``
+float32 ``[num_blocks][num_kv_heads][2]``, those or int8, a scale for each
+block and kv head.
 """
 from __future__ import annotations
 
@@ -21,7 +24,8 @@ import warnings
 from typing import Optional, Tuple
 
 __all__ = [
-    "PKVError", "lib_path", "load", "version", "status_string", "cache_write", "copy_blocks",
+    "PKVError", "lib_path", "load", "version", "status_string", "cache_write", "cache_append", "cache_read",
+    "copy_blocks",
     "decode_workspace_size", "decode_attention", "decode_step", "prefill_workspace_size",
     "chunked_prefill_attention",
     "rotary", "rotary_cache_write", "linear_decode_attention", "linear_prefill_attention",
@@ -41,7 +45,7 @@ STATUS_NAMES = {
     10: "PKV_ERR_TIMEOUT", 11: "PKV_ERR_CUDA", 12: "PKV_ERR_UNSUPPORTED", 13: "PKV_ERR_SCRATCH_LIMIT",
     14: "PKV_ERR_NO_BLOCKS", 15: "PKV_ERR_HOST_MEMORY", 16: "PKV_ERR_DTYPE",
 }
-PKV_KV_BF16, PKV_KV_E4M3 = 0, 1
+PKV_KV_BF16, PKV_KV_E4M3, PKV_KV_E4M3_BLOCKS, PKV_KV_INT8_BLOCKS = 0, 1, 2, 3
 PKV_ROTARY_ADJACENT_PAIRS, PKV_ROTARY_INTERLEAVED_AXES = 1, 2
 
 
@@ -58,7 +62,8 @@ class Cache(ctypes.Structure):
     """Mirror of ``pkv_cache_t``."""
     _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
-                ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+                ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
+                ("block_scales", ctypes.c_void_p)]
 
 
 class BlocksState(ctypes.Structure):
@@ -103,6 +108,8 @@ def load():
     CP = ctypes.POINTER(Cache)
     sigs = {
         "pkv_cache_write": ([CP, P, P, P, i32, P], ctypes.c_int),
+        "pkv_cache_append": ([CP, P, i64, P, i64, i32, P, P, i32, P, i32, P], ctypes.c_int),
+        "pkv_cache_read": ([CP, P, P, i32, P, P, i32, P, i32, P], ctypes.c_int),
         "pkv_copy_blocks": ([CP, P, P, i32, P, P, P], ctypes.c_int),
         "pkv_decode_workspace_size": ([i32, i32, i32, i32, i32, i32], sz),
         "pkv_decode_attention": ([CP, P, i32, P, i32, P, i32, i32, f32, P, P, sz, i32, P], ctypes.c_int),
@@ -248,15 +255,29 @@ def _out(t, name="out"):
     return _dev(t, name, dtype=torch.float32)
 
 
-def _cache(k_pool, v_pool, k_scale=None, v_scale=None, need_scales=False) -> Cache:
+def _cache(k_pool, v_pool, k_scale=None, v_scale=None, need_scales=False, block_scales=None) -> Cache:
     """Descriptor of a pool pair: 2-byte elements are bf16, 1-byte elements
-    (uint8 or float8_e4m3fn) e4m3 codes with one scale per pool."""
+    (uint8 or float8_e4m3fn) e4m3 codes with one scale per pool, or, with
+    block_scales, e4m3 or int8 codes with a scale per (block, kv head)."""
     if k_pool.shape != v_pool.shape or k_pool.dim() != 4:
         raise ValueError("k_pool and v_pool must both be [num_blocks][num_kv_heads][16][head_dim]")
     nb, hkv, bs, d = k_pool.shape
     es = k_pool.element_size()
     if es not in (1, 2):
         raise TypeError("pools must have 2-byte (bf16) or 1-byte (e4m3) elements")
+    if block_scales is not None:
+        torch = _torch()
+        if k_pool.dtype not in (torch.int8, torch.uint8, torch.float8_e4m3fn) or v_pool.dtype != k_pool.dtype:
+            raise TypeError("pools with block_scales must both be int8, or e4m3 codes (uint8 or float8_e4m3fn)")
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a pool has block_scales or k_scale and v_scale, not both")
+        if tuple(block_scales.shape) != (nb, hkv, 2):
+            raise ValueError("block_scales must be [num_blocks][num_kv_heads][2]")
+        if not k_pool.get_device() == v_pool.get_device() == block_scales.get_device():
+            raise ValueError("the pools and block_scales must be on one device")
+        return Cache(_dev(k_pool, "k_pool").value, _dev(v_pool, "v_pool").value, nb, hkv, d, bs,
+                     PKV_KV_INT8_BLOCKS if k_pool.dtype == torch.int8 else PKV_KV_E4M3_BLOCKS, 1.0, 1.0,
+                     _dev(block_scales, "block_scales", dtype=torch.float32).value)
     if es == 1 and need_scales and (k_scale is None or v_scale is None):
         raise ValueError("an e4m3 pool needs k_scale and v_scale")
     return Cache(_dev(k_pool, "k_pool", es).value, _dev(v_pool, "v_pool", es).value, nb, hkv, d, bs,
@@ -291,9 +312,68 @@ def cache_write(k_pool, v_pool, k_new, v_new, slot_mapping, stream=None, k_scale
     _check(st, "pkv_cache_write")
 
 
+def _cache_rows(k_pool, v_pool, query_start_loc, context_lens, block_tables, k_scale, v_scale, block_scales, dev):
+    """Descriptor and index arguments of cache_append and cache_read."""
+    i32 = _torch().int32
+    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True, block_scales=block_scales)
+    if k_pool.get_device() != dev or v_pool.get_device() != dev:
+        raise ValueError(f"the pools are on {k_pool.device} and {v_pool.device}, the current device is cuda:{dev}")
+    if context_lens.dim() != 1 or block_tables.dim() != 2:
+        raise ValueError("context_lens must be [num_seqs] and block_tables [num_seqs][max_blocks]")
+    S, wide = context_lens.shape[0], block_tables.shape[1]
+    return c, (_addr(query_start_loc, "query_start_loc", i32, dev, (S + 1,)),
+               _addr(context_lens, "context_lens", i32, dev, (S,)), S,
+               _addr(block_tables, "block_tables", i32, dev, (S, wide)), wide)
+
+
+def cache_append(k_pool, v_pool, block_scales, k_new, v_new, query_start_loc, context_lens, block_tables,
+                 stream=None) -> None:
+    """Store rows k_new/v_new [T][Hkv][d] (bf16; a token's rows may be a view
+    of a packed projection) in 8 bits at the ends of their sequences'
+    contexts, with a scale for each (block, kv head): sequence s owns rows
+    query_start_loc[s] .. query_start_loc[s+1]-1, and context_lens[s] counts
+    them.  The pools are int8, or e4m3 codes (uint8 or float8_e4m3fn), and
+    block_scales float32 [num_blocks][Hkv][2] (K, V).  A block whose scale has
+    to grow has its earlier rows encoded again."""
+    torch = _torch()
+    lib = load()
+    dev = _device()
+    c, index = _cache_rows(k_pool, v_pool, query_start_loc, context_lens, block_tables, None, None, block_scales, dev)
+    shape = (k_new.shape[0], c.num_kv_heads, c.head_dim)
+    kp, ks = _rows(k_new, "k_new", torch.bfloat16, dev, shape)
+    vp, vs = _rows(v_new, "v_new", torch.bfloat16, dev, shape)
+    st = lib.pkv_cache_append(ctypes.byref(c), kp, ks, vp, vs, shape[0], *index, _stream_handle(stream))
+    if st:
+        _check(st, "pkv_cache_append")
+
+
+def cache_read(k_pool, v_pool, query_start_loc, context_lens, block_tables, num_tokens: int, k_out=None, v_out=None,
+               k_scale=None, v_scale=None, block_scales=None, stream=None):
+    """Rows of the cache back as bf16, from pools of any kind: sequence s
+    takes rows query_start_loc[s] .. query_start_loc[s+1]-1 of the outputs
+    [num_tokens][Hkv][d] for the last rows of its context.  Returns (k_out,
+    v_out)."""
+    torch = _torch()
+    lib = load()
+    dev = _device()
+    c, index = _cache_rows(k_pool, v_pool, query_start_loc, context_lens, block_tables, k_scale, v_scale,
+                           block_scales, dev)
+    shape = (int(num_tokens), c.num_kv_heads, c.head_dim)
+    with _on(stream):
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if v_out is None else v_out
+    st = lib.pkv_cache_read(ctypes.byref(c), _addr(k_out, "k_out", torch.bfloat16, dev, shape),
+                            _addr(v_out, "v_out", torch.bfloat16, dev, shape), shape[0], *index,
+                            _stream_handle(stream))
+    if st:
+        _check(st, "pkv_cache_read")
+    return k_out, v_out
+
+
 def copy_blocks(k_pool, v_pool, src, dst, check_host: bool = True, src_host=None, dst_host=None,
-                stream=None) -> None:
-    """Copy-on-write: pool[dst[i]] <- pool[src[i]] (K and V, whole blocks).
+                stream=None, block_scales=None) -> None:
+    """Copy-on-write: pool[dst[i]] <- pool[src[i]] (K and V, whole blocks,
+    with their block_scales where the pool has them).
 
     The library rejects aliasing destinations before launching when it gets
     host copies of the id lists: pass them as ``src_host``/``dst_host``, or
@@ -302,7 +382,7 @@ def copy_blocks(k_pool, v_pool, src, dst, check_host: bool = True, src_host=None
     """
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool)
+    c = _cache(k_pool, v_pool, block_scales=block_scales)
     n = int(src.shape[0])
     if dst.shape[0] != n:
         raise ValueError("src and dst must have the same length")
@@ -339,12 +419,12 @@ def new_workspace(nbytes: int, device=None):
 
 def decode_attention(k_pool, v_pool, q, block_tables, context_lens, max_context_len: int, scale: float,
                      out=None, workspace=None, partition_blocks: int = 0, stream=None, k_scale=None,
-                     v_scale=None):
-    """Paged decode attention; returns ``out`` float32 [B][Hq][d].  e4m3 pools
+                     v_scale=None, block_scales=None):
+    """Paged decode attention; returns ``out`` float32 [B][Hq][d].  8-bit pools
     (1-byte elements) need the scales they were written with."""
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True)
+    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True, block_scales=block_scales)
     B, hq, d = q.shape
     if d != c.head_dim:
         raise ValueError("q head_dim does not match the pools")
@@ -440,15 +520,15 @@ def decode_shared_prefix_workspace_size(num_seqs, num_q_heads, num_kv_heads, hea
 
 def decode_attention_shared_prefix(k_pool, v_pool, q, block_tables, context_lens, max_context_len: int,
                                    shared_blocks: int, scale: float, out=None, workspace=None, stream=None,
-                                   k_scale=None, v_scale=None):
+                                   k_scale=None, v_scale=None, block_scales=None):
     """Decode attention for a batch whose block tables all start with the
     same ``shared_blocks`` full blocks: those are read once per kv head for
     every sequence (tensor cores), the rest per sequence; returns ``out``
-    float32 [B][Hq][d].  e4m3 pools (with their scales) attend the shared
+    float32 [B][Hq][d].  8-bit pools (with their scales) attend the shared
     blocks per sequence."""
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True)
+    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True, block_scales=block_scales)
     B, hq, d = q.shape
     if d != c.head_dim:
         raise ValueError("q head_dim does not match the pools")
@@ -481,12 +561,12 @@ def prefill_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head
 
 def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, block_tables,
                               max_context_len: int, scale: float, out=None, workspace=None,
-                              query_start_loc_host=None, stream=None):
+                              query_start_loc_host=None, stream=None, block_scales=None):
     """Mixed batch of causal prefill chunks and decode rows; returns ``out``
-    float32 [Tq][Hq][d]."""
+    float32 [Tq][Hq][d].  Pools are bf16, or 8-bit with ``block_scales``."""
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool)
+    c = _cache(k_pool, v_pool, block_scales=block_scales)
     T, hq, d = q.shape
     S = int(context_lens.shape[0])
     if query_start_loc.shape[0] != S + 1:
@@ -765,18 +845,21 @@ def linear_prefill_attention(states, log_decay, q, k, v, query_start_loc, state_
     return out
 
 
-def _swap(direction, k_pool, v_pool, blocks, slots, host, stream):
+def _swap(direction, k_pool, v_pool, blocks, slots, host, stream, block_scales):
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool)
+    c = _cache(k_pool, v_pool, block_scales=block_scales)
     n = int(blocks.shape[0])
     if slots.shape[0] != n:
         raise ValueError("blocks and slots must have the same length")
     if not isinstance(host, torch.Tensor) or host.is_cuda or not host.is_contiguous():
         raise ValueError("host must be a contiguous CPU tensor in page-locked memory")
     slab = 2 * c.num_kv_heads * 16 * c.head_dim * k_pool.element_size()
+    if block_scales is not None:
+        slab += (8 * c.num_kv_heads + 15) // 16 * 16
     if host.numel() * host.element_size() % slab:
-        raise ValueError("host must hold whole slabs of [2][num_kv_heads][16][head_dim] pool elements")
+        raise ValueError("host must hold whole slabs of [2][num_kv_heads][16][head_dim] pool elements, each followed "
+                         "by the block's scales [num_kv_heads][2] up to 16 bytes where the pool has them")
     num_slots = host.numel() * host.element_size() // slab
     st = lib.pkv_swap_blocks(ctypes.byref(c), int(direction), _dev(blocks, "blocks", dtype=torch.int32),
                              _dev(slots, "slots", dtype=torch.int32), n, ctypes.c_void_p(host.data_ptr()),
@@ -784,15 +867,17 @@ def _swap(direction, k_pool, v_pool, blocks, slots, host, stream):
     _check(st, "pkv_swap_blocks")
 
 
-def swap_out(k_pool, v_pool, blocks, slots, host, stream=None) -> None:
+def swap_out(k_pool, v_pool, blocks, slots, host, stream=None, block_scales=None) -> None:
     """host slab slots[i] <- pool block blocks[i] (K then V); ``host`` is a
-    pinned CPU tensor of whole [2][Hkv][16][d] slabs of the pools' elements."""
-    _swap(0, k_pool, v_pool, blocks, slots, host, stream)
+    pinned CPU tensor of whole [2][Hkv][16][d] slabs of the pools' elements,
+    each followed by the block's scales, fp32 [Hkv][2], up to a multiple of 16
+    bytes, where the pool has block_scales."""
+    _swap(0, k_pool, v_pool, blocks, slots, host, stream, block_scales)
 
 
-def swap_in(k_pool, v_pool, blocks, slots, host, stream=None) -> None:
+def swap_in(k_pool, v_pool, blocks, slots, host, stream=None, block_scales=None) -> None:
     """pool block blocks[i] <- host slab slots[i]."""
-    _swap(1, k_pool, v_pool, blocks, slots, host, stream)
+    _swap(1, k_pool, v_pool, blocks, slots, host, stream, block_scales)
 
 
 def prefix_keys(token_ids, token_start_loc, max_blocks: int, extra=None, parent_keys=None, keys=None,

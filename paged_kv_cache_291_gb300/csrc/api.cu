@@ -82,22 +82,29 @@ pkv_status current_device(DeviceState** out) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether the pool has a scale for each (block, kv head).
+bool scaled(const pkv_cache_t* c) { return c->kv_dtype == PKV_KV_E4M3_BLOCKS || c->kv_dtype == PKV_KV_INT8_BLOCKS; }
+
 pkv_status check_cache(const pkv_cache_t* c) {
     if (c == nullptr || c->k_pool == nullptr || c->v_pool == nullptr) return PKV_ERR_NULL;
     if (c->block_size != 16) return PKV_ERR_BLOCKSIZE;
     if (c->num_blocks < 0 || c->num_kv_heads < 1) return PKV_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128) return PKV_ERR_HEADDIM;
     if (!aligned16(c->k_pool) || !aligned16(c->v_pool)) return PKV_ERR_ALIGN;
-    if (c->kv_dtype != PKV_KV_BF16 && c->kv_dtype != PKV_KV_E4M3) return PKV_ERR_DTYPE;
+    if (c->kv_dtype < PKV_KV_BF16 || c->kv_dtype > PKV_KV_INT8_BLOCKS) return PKV_ERR_DTYPE;
     if (c->kv_dtype == PKV_KV_E4M3) {
         // 1/scale must be a finite fp32 too.
         for (float x : {c->k_scale, c->v_scale})
             if (!(std::isfinite(x) && x > 0.f && std::isfinite(1.f / x))) return PKV_ERR_DTYPE;
     }
+    if (scaled(c)) {
+        if (c->block_scales == nullptr) return PKV_ERR_NULL;
+        if (!aligned16(c->block_scales)) return PKV_ERR_ALIGN;
+    }
     return PKV_OK;
 }
 
-int32_t elem_bytes(const pkv_cache_t* c) { return c->kv_dtype == PKV_KV_E4M3 ? 1 : 2; }
+int32_t elem_bytes(const pkv_cache_t* c) { return c->kv_dtype == PKV_KV_BF16 ? 2 : 1; }
 
 // The address a kernel uses for p: device memory as it is, page-locked host
 // memory mapped for the device through the pointer the runtime reports for
@@ -173,7 +180,7 @@ PKV_API const char* pkv_status_string(pkv_status s) {
         case PKV_ERR_NO_BLOCKS: return "PKV_ERR_NO_BLOCKS: the free queue holds fewer blocks than the append needs";
         case PKV_ERR_HOST_MEMORY: return "PKV_ERR_HOST_MEMORY: the host buffer is not page-locked memory mapped for the device";
         case PKV_ERR_DTYPE:
-            return "PKV_ERR_DTYPE: unknown kv_dtype, e4m3 scales not finite and positive, or a call without e4m3 support";
+            return "PKV_ERR_DTYPE: unknown kv_dtype, e4m3 scales not finite and positive, or a call without support for the pool's kind";
     }
     return "unknown pkv_status";
 }
@@ -182,6 +189,7 @@ PKV_API pkv_status pkv_cache_write(const pkv_cache_t* cache, const void* k_new, 
                                    const int32_t* slot_mapping, int32_t num_tokens, void* stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
+    if (scaled(cache)) return PKV_ERR_DTYPE;  // rows one by one: pkv_cache_append takes a block's rows together
     if (num_tokens < 0) return PKV_ERR_SHAPE;
     if (num_tokens == 0) return PKV_OK;
     if (k_new == nullptr || v_new == nullptr || slot_mapping == nullptr) return PKV_ERR_NULL;
@@ -229,7 +237,8 @@ PKV_API pkv_status pkv_copy_blocks(const pkv_cache_t* cache, const int32_t* src,
         const int32_t n = std::min<int32_t>(65535, num_pairs - base);
         cudaError_t e = pkv::launch_copy_blocks(src + base, dst + base, n, cache->k_pool, cache->v_pool,
                                                 cache->num_blocks, cache->num_kv_heads, cache->head_dim,
-                                                elem_bytes(cache), dev->err, static_cast<cudaStream_t>(stream));
+                                                elem_bytes(cache), scaled(cache) ? cache->block_scales : nullptr,
+                                                dev->err, static_cast<cudaStream_t>(stream));
         if (e != cudaSuccess) return cuda_fail(e);
     }
     return PKV_OK;
@@ -388,7 +397,8 @@ PKV_API pkv_status pkv_swap_blocks(const pkv_cache_t* cache, int32_t direction, 
     if (attr.type != cudaMemoryTypeHost || attr.devicePointer == nullptr) return PKV_ERR_HOST_MEMORY;
     cudaError_t e = pkv::launch_swap_blocks(direction, blocks, slots, n, attr.devicePointer, num_host_slots,
                                             cache->k_pool, cache->v_pool, cache->num_blocks, cache->num_kv_heads,
-                                            cache->head_dim, elem_bytes(cache), dev->err,
+                                            cache->head_dim, elem_bytes(cache),
+                                            scaled(cache) ? cache->block_scales : nullptr, dev->err,
                                             static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
@@ -425,6 +435,20 @@ PKV_API size_t pkv_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
 
 namespace {
 
+// What attention over a pool with a scale per block takes from the pool.
+pkv::ScaledArgs scaled_args(const pkv_cache_t* cache, const DeviceState* dev) {
+    pkv::ScaledArgs a = {};
+    a.k_pool = cache->k_pool;
+    a.v_pool = cache->v_pool;
+    a.block_scales = cache->block_scales;
+    a.num_blocks = cache->num_blocks;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.head_dim = cache->head_dim;
+    a.kv_dtype = cache->kv_dtype;
+    a.err = dev->err;
+    return a;
+}
+
 pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_heads,
                          const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
                          const int32_t* query_start_loc, int32_t num_seqs, int32_t max_context_len, float scale,
@@ -459,6 +483,22 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
         return st;
     if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return PKV_ERR_WORKSPACE;
+    if (scaled(cache)) {
+        pkv::ScaledArgs b = scaled_args(cache, dev);
+        b.q = q;
+        b.block_tables = block_tables;
+        b.context_lens = context_lens;
+        b.query_start_loc = query_start_loc;
+        b.out = out;
+        b.num_q_heads = num_q_heads;
+        b.num_seqs = num_seqs;
+        b.num_tokens = num_seqs;
+        b.max_blocks_per_seq = max_blocks_per_seq;
+        b.max_context_len = max_context_len;
+        b.scale = scale;
+        cudaError_t e = pkv::launch_scaled_attention(b, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+    }
     pkv::DecodeArgs a;
     a.k_pool = cache->k_pool;
     a.v_pool = cache->v_pool;
@@ -569,6 +609,7 @@ PKV_API pkv_status pkv_decode_step(const pkv_cache_t* cache, const void* k_new, 
                                    int32_t partition_blocks, void* stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
+    if (scaled(cache)) return PKV_ERR_DTYPE;
     if (num_seqs > 0) {
         if (k_new == nullptr || v_new == nullptr || slot_mapping == nullptr) return PKV_ERR_NULL;
         if (!aligned16(k_new) || !aligned16(v_new)) return PKV_ERR_ALIGN;
@@ -593,7 +634,7 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
                                                  void* stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
-    if (cache->kv_dtype != PKV_KV_BF16) return PKV_ERR_DTYPE;  // the tcgen05 tiles read bf16 K/V
+    if (cache->kv_dtype == PKV_KV_E4M3) return PKV_ERR_DTYPE;
     if ((st = check_heads(num_q_heads, cache->num_kv_heads)) != PKV_OK) return st;
     if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 0 || max_context_len < 0) return PKV_ERR_SHAPE;
     if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
@@ -614,6 +655,22 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
     const void* out_dev = nullptr;
     if ((st = device_address(out, &out_dev)) != PKV_OK) return st;
     out = static_cast<float*>(const_cast<void*>(out_dev));
+    if (scaled(cache)) {
+        pkv::ScaledArgs b = scaled_args(cache, dev);
+        b.q = q;
+        b.block_tables = block_tables;
+        b.context_lens = context_lens;
+        b.query_start_loc = query_start_loc;
+        b.out = out;
+        b.num_q_heads = num_q_heads;
+        b.num_seqs = num_seqs;
+        b.num_tokens = num_tokens;
+        b.max_blocks_per_seq = max_blocks_per_seq;
+        b.max_context_len = max_context_len;
+        b.scale = scale;
+        cudaError_t e = pkv::launch_scaled_attention(b, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+    }
     if (decode_rows > 0) {
         st = decode_common(cache, q, num_q_heads, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
                            num_seqs, max_context_len, scale, out, workspace, workspace_bytes, 0, stream);
@@ -695,6 +752,42 @@ bool clashes(const Span& out, const Span& own_input, bool own_contiguous, std::i
     return false;
 }
 
+// The checks and arguments the append and the read share.
+pkv_status fill_cache_rows(const pkv_cache_t* cache, int32_t num_tokens, const int32_t* query_start_loc,
+                           const int32_t* context_lens, int32_t num_seqs, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, pkv::CacheRowsArgs* a) {
+    if (query_start_loc == nullptr || context_lens == nullptr || block_tables == nullptr) return PKV_ERR_NULL;
+    // One CTA per block unit and 8 jobs of 2 a kv head: what a grid can hold.
+    if (num_tokens / 16 + 2ll * num_seqs > INT32_MAX || cache->num_kv_heads > 262140) return PKV_ERR_SHAPE;
+    *a = {};
+    a->k_pool = cache->k_pool;
+    a->v_pool = cache->v_pool;
+    a->block_scales = cache->block_scales;
+    a->query_start_loc = query_start_loc;
+    a->context_lens = context_lens;
+    a->block_tables = block_tables;
+    a->num_tokens = num_tokens;
+    a->num_seqs = num_seqs;
+    a->max_blocks_per_seq = max_blocks_per_seq;
+    a->num_blocks = cache->num_blocks;
+    a->num_kv_heads = cache->num_kv_heads;
+    a->head_dim = cache->head_dim;
+    a->kv_dtype = cache->kv_dtype;
+    a->k_scale = cache->k_scale;
+    a->v_scale = cache->v_scale;
+    return PKV_OK;
+}
+
+Span pool_span(const pkv_cache_t* c, const void* pool) {
+    return {reinterpret_cast<uintptr_t>(pool),
+            static_cast<size_t>(c->num_blocks) * c->num_kv_heads * 16 * c->head_dim * elem_bytes(c)};
+}
+
+Span scales_span(const pkv_cache_t* c) {
+    if (!scaled(c)) return {0, 0};
+    return {reinterpret_cast<uintptr_t>(c->block_scales), static_cast<size_t>(c->num_blocks) * c->num_kv_heads * 8};
+}
+
 pkv_status fill_rotary(const pkv_rotary_t* r, int32_t hq, int32_t hkv, int32_t head_dim, int32_t num_tokens,
                        pkv::RotaryArgs* a) {
     if (r == nullptr) return PKV_ERR_NULL;
@@ -734,6 +827,69 @@ pkv_status fill_rotary(const pkv_rotary_t* r, int32_t hq, int32_t hkv, int32_t h
 
 }  // namespace
 
+PKV_API pkv_status pkv_cache_append(const pkv_cache_t* cache, const void* k_new, int64_t k_stride, const void* v_new,
+                                    int64_t v_stride, int32_t num_tokens, const int32_t* query_start_loc,
+                                    const int32_t* context_lens, int32_t num_seqs, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, void* stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (!scaled(cache)) return PKV_ERR_DTYPE;  // pools without a scale per block: pkv_cache_write
+    if (num_tokens < 0 || num_seqs < 0 || max_blocks_per_seq < 0) return PKV_ERR_SHAPE;
+    if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+    const int32_t hkv = cache->num_kv_heads, d = cache->head_dim;
+    if ((st = check_rows(k_new, k_stride, hkv, d)) != PKV_OK) return st;
+    if ((st = check_rows(v_new, v_stride, hkv, d)) != PKV_OK) return st;
+    pkv::CacheRowsArgs a;
+    if ((st = fill_cache_rows(cache, num_tokens, query_start_loc, context_lens, num_seqs, block_tables,
+                              max_blocks_per_seq, &a)) != PKV_OK)
+        return st;
+    const Span in_k = rows_span(k_new, k_stride, hkv, d, num_tokens);
+    const Span in_v = rows_span(v_new, v_stride, hkv, d, num_tokens);
+    const Span k_pool = pool_span(cache, cache->k_pool), v_pool = pool_span(cache, cache->v_pool);
+    const Span scales = scales_span(cache);
+    if (clashes(k_pool, in_k, false, {in_v, v_pool, scales}) || clashes(v_pool, in_k, false, {in_v, scales}) ||
+        clashes(scales, in_k, false, {in_v}))
+        return PKV_ERR_ALIAS;
+    DeviceState* dev = nullptr;
+    if ((st = current_device(&dev)) != PKV_OK) return st;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.err = dev->err;
+    cudaError_t e = pkv::launch_cache_append(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+PKV_API pkv_status pkv_cache_read(const pkv_cache_t* cache, void* k_out, void* v_out, int32_t num_tokens,
+                                  const int32_t* query_start_loc, const int32_t* context_lens, int32_t num_seqs,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq, void* stream) {
+    pkv_status st = check_cache(cache);
+    if (st != PKV_OK) return st;
+    if (num_tokens < 0 || num_seqs < 0 || max_blocks_per_seq < 0) return PKV_ERR_SHAPE;
+    if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+    const int32_t hkv = cache->num_kv_heads, d = cache->head_dim;
+    const int64_t stride = static_cast<int64_t>(hkv) * d;
+    if ((st = check_rows(k_out, stride, hkv, d)) != PKV_OK) return st;
+    if ((st = check_rows(v_out, stride, hkv, d)) != PKV_OK) return st;
+    pkv::CacheRowsArgs a;
+    if ((st = fill_cache_rows(cache, num_tokens, query_start_loc, context_lens, num_seqs, block_tables,
+                              max_blocks_per_seq, &a)) != PKV_OK)
+        return st;
+    const Span out_k = rows_span(k_out, stride, hkv, d, num_tokens), out_v = rows_span(v_out, stride, hkv, d, num_tokens);
+    const Span k_pool = pool_span(cache, cache->k_pool), v_pool = pool_span(cache, cache->v_pool);
+    const Span scales = scales_span(cache);
+    if (clashes(out_k, k_pool, false, {out_v, v_pool, scales}) || clashes(out_v, k_pool, false, {v_pool, scales}))
+        return PKV_ERR_ALIAS;
+    DeviceState* dev = nullptr;
+    if ((st = current_device(&dev)) != PKV_OK) return st;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.err = dev->err;
+    cudaError_t e = pkv::launch_cache_read(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
 PKV_API pkv_status pkv_rotary(const pkv_rotary_t* rotary, const void* q, int64_t q_stride, int32_t num_q_heads,
                               const void* k, int64_t k_stride, int32_t num_kv_heads, int32_t head_dim,
                               int32_t num_tokens, void* q_out, void* k_out, void* stream) {
@@ -772,6 +928,7 @@ PKV_API pkv_status pkv_rotary_cache_write(const pkv_cache_t* cache, const pkv_ro
                                           int32_t num_tokens, void* q_out, void* stream) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
+    if (scaled(cache)) return PKV_ERR_DTYPE;
     const int32_t hkv = cache->num_kv_heads, d = cache->head_dim;
     pkv::RotaryArgs a = {};
     if ((st = fill_rotary(rotary, num_q_heads, hkv, d, num_tokens, &a)) != PKV_OK) return st;

@@ -166,6 +166,7 @@ PyObject* rotary_cache_write(PyObject*, Args a, Py_ssize_t n) {
     cache.block_size = 16;
     cache.kv_dtype = e4m3 ? PKV_KV_E4M3 : PKV_KV_BF16;
     cache.k_scale = cache.v_scale = 1.f;
+    cache.block_scales = nullptr;
     if (e4m3) {
         cache.k_scale = c.real(a[12]);
         cache.v_scale = c.real(a[13]);

@@ -86,11 +86,13 @@ __global__ void __launch_bounds__(256) cache_write_e4m3_kernel(
 }
 
 // Grid: x = chunk groups, y = pair.  Each pair copies the K slab then the V
-// slab of one block ([Hkv][16][d] elements each).
+// slab of one block ([Hkv][16][d] elements each), and its block_scales words
+// of scales (8-byte pairs, 0 for pools without).
 __global__ void __launch_bounds__(256) copy_blocks_kernel(const int32_t* __restrict__ src,
                                                           const int32_t* __restrict__ dst, int64_t block_chunks,
                                                           int32_t num_blocks, uint4* __restrict__ k_pool,
-                                                          uint4* __restrict__ v_pool, unsigned long long* err) {
+                                                          uint4* __restrict__ v_pool, uint2* __restrict__ scales,
+                                                          int32_t block_scales, unsigned long long* err) {
     griddep_launch_dependents();
     griddep_wait();
     const int32_t pair = blockIdx.y;
@@ -114,15 +116,20 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(const int32_t* __restr
             vd[i - block_chunks] = vs[i - block_chunks];
         }
     }
+    if (blockIdx.x == 0)
+        for (int32_t i = threadIdx.x; i < block_scales; i += blockDim.x)
+            scales[static_cast<int64_t>(d) * block_scales + i] = scales[static_cast<int64_t>(s) * block_scales + i];
 }
 
 // Grid: x = chunk groups, y = pair.  Pair i moves block blocks[i] of the
 // pool and slab slots[i] of the host buffer ([slots][2][Hkv][16][d] pool
-// elements: the K block, then the V block) in the given direction.
+// elements: the K block, then the V block, then block_scales 8-byte pairs of
+// scales up to a multiple of 16 bytes) in the given direction.
 __global__ void __launch_bounds__(256) swap_blocks_kernel(int32_t direction, const int32_t* __restrict__ blocks,
                                                           const int32_t* __restrict__ slots, int64_t block_chunks,
                                                           int32_t num_blocks, int64_t num_slots,
                                                           uint4* __restrict__ k_pool, uint4* __restrict__ v_pool,
+                                                          uint2* __restrict__ scales, int32_t block_scales,
                                                           uint4* __restrict__ host, unsigned long long* err) {
     griddep_launch_dependents();
     griddep_wait();
@@ -136,13 +143,21 @@ __global__ void __launch_bounds__(256) swap_blocks_kernel(int32_t direction, con
     }
     uint4* kb = k_pool + static_cast<int64_t>(b) * block_chunks;
     uint4* vb = v_pool + static_cast<int64_t>(b) * block_chunks;
-    uint4* slab = host + static_cast<int64_t>(h) * 2 * block_chunks;
+    uint4* slab = host + static_cast<int64_t>(h) * (2 * block_chunks + (block_scales + 1) / 2);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < 2 * block_chunks;
          i += stride) {
         uint4* dev = i < block_chunks ? kb + i : vb + (i - block_chunks);
         if (direction == 0) slab[i] = *dev;
         else *dev = slab[i];
+    }
+    if (blockIdx.x == 0) {
+        uint2* kept = reinterpret_cast<uint2*>(slab + 2 * block_chunks);
+        uint2* own = scales + static_cast<int64_t>(b) * block_scales;
+        for (int32_t i = threadIdx.x; i < block_scales; i += blockDim.x) {
+            if (direction == 0) kept[i] = own[i];
+            else own[i] = kept[i];
+        }
     }
 }
 
@@ -171,8 +186,8 @@ cudaError_t launch_copy16(void* dst, const void* src, int64_t chunks, int num_sm
 
 cudaError_t launch_swap_blocks(int32_t direction, const int32_t* blocks, const int32_t* slots, int32_t n,
                                void* host, int64_t num_slots, void* k_pool, void* v_pool, int32_t num_blocks,
-                               int32_t num_kv_heads, int32_t head_dim, int32_t elem_bytes, unsigned long long* err,
-                               cudaStream_t stream) {
+                               int32_t num_kv_heads, int32_t head_dim, int32_t elem_bytes, float* block_scales,
+                               unsigned long long* err, cudaStream_t stream) {
     const int64_t block_chunks = static_cast<int64_t>(num_kv_heads) * kBlockSize * head_dim * elem_bytes / 16;
     const int threads = 256;
     int64_t gx = (2 * block_chunks + threads - 1) / threads;
@@ -180,7 +195,8 @@ cudaError_t launch_swap_blocks(int32_t direction, const int32_t* blocks, const i
     dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(n));
     return launch_overlapped(swap_blocks_kernel, grid, dim3(threads), 0, stream, direction, blocks, slots,
                              block_chunks, num_blocks, num_slots, static_cast<uint4*>(k_pool),
-                             static_cast<uint4*>(v_pool), static_cast<uint4*>(host), err);
+                             static_cast<uint4*>(v_pool), reinterpret_cast<uint2*>(block_scales),
+                             block_scales != nullptr ? num_kv_heads : 0, static_cast<uint4*>(host), err);
 }
 
 cudaError_t launch_cache_write(const void* k_new, const void* v_new, const int32_t* slot_mapping,
@@ -215,7 +231,8 @@ cudaError_t launch_cache_write_e4m3(const void* k_new, const void* v_new, const 
 
 cudaError_t launch_copy_blocks(const int32_t* src, const int32_t* dst, int32_t num_pairs, void* k_pool,
                                void* v_pool, int32_t num_blocks, int32_t num_kv_heads, int32_t head_dim,
-                               int32_t elem_bytes, unsigned long long* err, cudaStream_t stream) {
+                               int32_t elem_bytes, float* block_scales, unsigned long long* err,
+                               cudaStream_t stream) {
     if (num_pairs == 0) return cudaSuccess;
     const int64_t block_chunks = static_cast<int64_t>(num_kv_heads) * kBlockSize * head_dim * elem_bytes / 16;
     const int threads = 256;
@@ -223,7 +240,8 @@ cudaError_t launch_copy_blocks(const int32_t* src, const int32_t* dst, int32_t n
     if (gx > 64) gx = 64;
     dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(num_pairs));
     return launch_overlapped(copy_blocks_kernel, grid, dim3(threads), 0, stream, src, dst, block_chunks, num_blocks,
-                             static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), err);
+                             static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool),
+                             reinterpret_cast<uint2*>(block_scales), block_scales != nullptr ? num_kv_heads : 0, err);
 }
 
 }  // namespace pkv

@@ -98,10 +98,53 @@ cudaError_t launch_cache_write_e4m3(const void* k_new, const void* v_new, const 
                                     int32_t num_kv_heads, int32_t head_dim, float k_inv_scale, float v_inv_scale,
                                     unsigned long long* err, cudaStream_t stream);
 
-// elem_bytes: 2 for bf16 pools, 1 for e4m3 pools.
+// elem_bytes: 2 for bf16 pools, 1 for 8-bit pools.  block_scales: those of a
+// pool with a scale per (block, kv head), moved with its blocks, or null.
 cudaError_t launch_copy_blocks(const int32_t* src, const int32_t* dst, int32_t num_pairs, void* k_pool,
                                void* v_pool, int32_t num_blocks, int32_t num_kv_heads, int32_t head_dim,
-                               int32_t elem_bytes, unsigned long long* err, cudaStream_t stream);
+                               int32_t elem_bytes, float* block_scales, unsigned long long* err,
+                               cudaStream_t stream);
+
+// The rows at the ends of the sequences' contexts, into an 8-bit pool with a
+// scale per (block, kv head) or out of a pool of any kind (scaled_cache.cu).
+struct CacheRowsArgs {
+    void* k_pool;
+    void* v_pool;
+    float* block_scales;
+    const void* k_new;                // append: bf16 rows, token stride in elements
+    const void* v_new;
+    int64_t k_stride, v_stride;
+    void* k_out;                      // read: bf16 [num_tokens][Hkv][d]
+    void* v_out;
+    const int32_t* query_start_loc;   // device [S+1]
+    const int32_t* context_lens;
+    const int32_t* block_tables;
+    unsigned long long* err;
+    int32_t num_tokens, num_seqs, max_blocks_per_seq, num_blocks, num_kv_heads, head_dim;
+    int32_t kv_dtype;
+    float k_scale, v_scale;           // pools with one scale
+};
+
+cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream);
+
+// Attention over an 8-bit pool with a scale per (block, kv head).
+struct ScaledArgs {
+    const void* k_pool;
+    const void* v_pool;
+    const float* block_scales;
+    const void* q;                    // bf16 [num_tokens][Hq][d]
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* query_start_loc;   // device [S+1], or null: row s is sequence s
+    float* out;
+    unsigned long long* err;
+    int32_t num_blocks, num_kv_heads, num_q_heads, head_dim, kv_dtype;
+    int32_t num_seqs, num_tokens, max_blocks_per_seq, max_context_len;
+    float scale;
+};
+
+cudaError_t launch_scaled_attention(const ScaledArgs& a, cudaStream_t stream);
 
 // Copy `chunks` 16-byte chunks from src to dst (device addresses) with a
 // kernel.
@@ -109,8 +152,8 @@ cudaError_t launch_copy16(void* dst, const void* src, int64_t chunks, int num_sm
 
 cudaError_t launch_swap_blocks(int32_t direction, const int32_t* blocks, const int32_t* slots, int32_t n,
                                void* host, int64_t num_slots, void* k_pool, void* v_pool, int32_t num_blocks,
-                               int32_t num_kv_heads, int32_t head_dim, int32_t elem_bytes, unsigned long long* err,
-                               cudaStream_t stream);
+                               int32_t num_kv_heads, int32_t head_dim, int32_t elem_bytes, float* block_scales,
+                               unsigned long long* err, cudaStream_t stream);
 
 // Chunked prefill (tcgen05) launch description.
 struct PrefillArgs {
