@@ -94,7 +94,7 @@ typedef enum pkv_status {
  * calls and the block copies and swaps take them; pkv_cache_write,
  * pkv_rotary_cache_write and pkv_decode_step, which store rows one by one,
  * refuse them (PKV_ERR_DTYPE).
- * A scale that a call uses is finite and at least 2^-100; another one raises
+ * A scale that a call uses is in [2^-100, 2^122]; another one raises
  * PKV_ERR_RANGE on the device and counts as 2^-100.  No code of an int8 pool
  * is -128 after pkv_cache_append (if found, it counts as -128).
  */

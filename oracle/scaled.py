@@ -22,7 +22,7 @@ import numpy as np
 
 from . import fp8
 
-LEAST = np.float32(2.0 ** -100)
+LEAST, MOST = np.float32(2.0 ** -100), np.float32(2.0 ** 122)
 
 
 def largest(pool) -> float:
@@ -43,7 +43,7 @@ def encode(x, like) -> np.ndarray:
 
 
 def used_scale(s) -> np.float32:
-    return np.float32(s) if np.isfinite(s) and s >= LEAST else LEAST
+    return np.float32(s) if LEAST <= s <= MOST else LEAST
 
 
 def bf16_values(bits) -> np.ndarray:
@@ -118,7 +118,7 @@ def attention(k_pool, v_pool, scales, q, start, context_lens, tables, scale):
             continue
         pos = np.arange(n)
         blocks = np.asarray(tables[s])[pos // 16]
-        sc = np.where(np.isfinite(scales) & (scales >= LEAST), scales, LEAST).astype(np.float64)[blocks]
+        sc = np.where((scales >= LEAST) & (scales <= MOST), scales, LEAST).astype(np.float64)[blocks]
         K = values(k_pool[blocks, :, pos % 16]) * sc[..., 0, None]
         V = values(v_pool[blocks, :, pos % 16]) * sc[..., 1, None]
         for h in range(hq):

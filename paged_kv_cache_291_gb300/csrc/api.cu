@@ -463,6 +463,8 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
     if (num_seqs == 0) return PKV_OK;
     if (q == nullptr || block_tables == nullptr || context_lens == nullptr || out == nullptr) return PKV_ERR_NULL;
     if (!aligned16(q) || !aligned16(out)) return PKV_ERR_ALIGN;
+    if (scaled(cache) && static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > INT32_MAX)
+        return PKV_ERR_SHAPE;  // slabs are counted in 32 bits
     DeviceState* dev = nullptr;
     if ((st = current_device(&dev)) != PKV_OK) return st;
     // out may be page-locked host memory: the kernel then writes the rows
@@ -483,22 +485,6 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
         return st;
     if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return PKV_ERR_WORKSPACE;
-    if (scaled(cache)) {
-        pkv::ScaledArgs b = scaled_args(cache, dev);
-        b.q = q;
-        b.block_tables = block_tables;
-        b.context_lens = context_lens;
-        b.query_start_loc = query_start_loc;
-        b.out = out;
-        b.num_q_heads = num_q_heads;
-        b.num_seqs = num_seqs;
-        b.num_tokens = num_seqs;
-        b.max_blocks_per_seq = max_blocks_per_seq;
-        b.max_context_len = max_context_len;
-        b.scale = scale;
-        cudaError_t e = pkv::launch_scaled_attention(b, static_cast<cudaStream_t>(stream));
-        return e == cudaSuccess ? PKV_OK : cuda_fail(e);
-    }
     pkv::DecodeArgs a;
     a.k_pool = cache->k_pool;
     a.v_pool = cache->v_pool;
@@ -521,6 +507,8 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
     a.kv_e4m3 = cache->kv_dtype == PKV_KV_E4M3;
     a.k_scale = cache->k_scale;
     a.v_scale = cache->v_scale;
+    a.block_scales = scaled(cache) ? cache->block_scales : nullptr;
+    a.int8_codes = cache->kv_dtype == PKV_KV_INT8_BLOCKS;
     a.k_new = k_new;
     a.v_new = v_new;
     a.slot_mapping = slot_mapping;

@@ -71,6 +71,8 @@ DecodePlan plan_decode_ranges(int32_t num_seqs, int32_t num_kv_heads, int32_t ma
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     if (a.num_seqs == 0) return cudaSuccess;
     const bool stall = take_stall();
+    if (a.block_scales != nullptr)
+        return a.int8_codes ? launch_decode_scaled_int8(a, stall, stream) : launch_decode_scaled_e4m3(a, stall, stream);
     if (a.k_new != nullptr) return launch_decode_fused(a, stall, stream);
     return launch_decode_t<false>(a, stall, stream);
 }

@@ -158,12 +158,16 @@ struct DecodeParams {
     int32_t skip_blocks;
     const float2* pre_ml;
     const float* pre_o;
+    const float2* block_scales;  // pools with a scale per block: [num_blocks][Hkv] (K, V)
 };
 
 constexpr int align_up(int x, int a) { return (x + a - 1) / a * a; }
 
 template <int D, int G, int EB>
 struct Cfg {
+    static constexpr int HEAD_DIM = D, GROUP = G, ELEM = EB;
+    static constexpr bool SCALED = false;  // a scale per (block, kv head), two blocks a stage (decode_scaled.cuh)
+    static constexpr int BPS = 1;          // blocks a stage
     static constexpr bool MMA = use_mma<D, G, EB>();
     static constexpr int ALIGN_PAD = MMA ? 1024 : 0;  // swizzled tiles need a 1024-byte aligned ring
     static constexpr int W = consumer_warps<D, G, EB>();  // consumer warps
@@ -335,6 +339,27 @@ __device__ __forceinline__ void tma_tile_g2s(void* smem_dst, const CUtensorMap* 
         : "memory");
 }
 
+// The 16 rows of slab `slab` of a 3-D map (dims, rows, slabs).
+__device__ __forceinline__ void tma_slab_g2s(void* smem_dst, const CUtensorMap* map, int32_t slab, uint64_t* bar,
+                                             uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], "
+        "[%1, {%2, %2, %3}], [%4], %5;" ::"r"(smem_addr(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slab), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
+}
+
+// Eight bytes from global to shared memory, asynchronously; cp_async_arrive
+// arrives on `bar` (counting as one of its arrivals) once the copies that
+// this thread issued before it have landed.
+__device__ __forceinline__ void cp_async8(void* smem_dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem_dst)), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Byte offset of 16-byte chunk c of row r in a slab stored as 128-byte
 // swizzled panels of 16 rows (a tiled TMA copy with the 128-byte swizzle:
 // within a row's 128 bytes the chunk index is XORed with r mod 8).
@@ -479,10 +504,10 @@ __device__ __forceinline__ void compute_block(const uint8_t* kst, const uint8_t*
     __syncwarp();
 }
 
-template <int D, int G, int EB, bool FUSED>
+template <class C, bool FUSED>
 __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, const CUtensorMap* tmv, uint8_t* smem,
                              const Bars& B, volatile int* abort_flag, int lane) {
-    using C = Cfg<D, G, EB>;
+    constexpr int D = C::HEAD_DIM, G = C::GROUP, EB = C::ELEM;
     ItemDesc* descs = reinterpret_cast<ItemDesc*>(smem + C::OFF_DESC);
     int* stage_new = reinterpret_cast<int*>(smem + C::OFF_NEW);
     const unsigned FULL = 0xffffffffu;
@@ -593,9 +618,11 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
         const int rot = static_cast<int>(pos % C::W);
         const int row = P.qsl ? __ldg(P.qsl + s) : s;
         const int32_t* trow = P.block_tables + static_cast<size_t>(s) * P.max_blocks;
-        // First batch of table entries, requested before the descriptor work.
-        int e = 0;
-        if (lane < b1 - b0) e = __ldg(trow + b0 + lane);
+        // First batch of table entries, requested before the descriptor work
+        // (a lane's stage may hold two blocks: e and its odd one).
+        int e = 0, odd = 0;
+        if (C::BPS * lane < b1 - b0) e = __ldg(trow + b0 + C::BPS * lane);
+        if (C::BPS == 2 && C::BPS * lane + 1 < b1 - b0) odd = __ldg(trow + b0 + C::BPS * lane + 1);
         // Fused step (bf16 pools): the item holds the pair's last block, whose
         // row srow is the new token; its slot is read now, used when that
         // block is issued.
@@ -635,6 +662,60 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
         // batch and no lane waits on its own batch.  The next batch's
         // table entries are requested before this batch's copies.
         constexpr int kBatch = C::STAGES < 32 ? C::STAGES : 32;
+        if constexpr (C::SCALED) {
+            // The same with two blocks a stage: stage i of the item holds
+            // blocks b0 + 2 i and the next one, if the item has it.  Their
+            // scales come with them: an 8-byte asynchronous copy each, whose
+            // completion is the full barrier's second arrival.
+            const int nst = (b1 - b0 + 1) / 2;
+            for (int base = 0; base < nst; base += kBatch) {
+                const int cnt = min(kBatch, nst - base);
+                const int next = b0 + 2 * (base + kBatch + lane);
+                int e_next = 0, odd_next = 0;
+                if (lane < kBatch && next < b1) e_next = __ldg(trow + next);
+                if (lane < kBatch && next + 1 < b1) odd_next = __ldg(trow + next + 1);
+                const int i = base + lane;
+                const int w = (i + rot) % C::W;
+                const int first_w = (w - rot + C::W) % C::W;
+                const uint32_t jw = static_cast<uint32_t>(__shfl_sync(FULL, static_cast<int>(given), w)) +
+                                    static_cast<uint32_t>((i - first_w) / C::W);
+                const uint32_t st = static_cast<uint32_t>(w * C::SW) + jw % C::SW;
+                const bool two = b0 + 2 * i + 1 < b1;
+                int bad = 0;
+                if (lane < cnt) {
+                    int phys[2] = {e, two ? odd : e};
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (phys[x] < 0 || phys[x] >= P.num_blocks) {
+                            record_error(P.err, kErrRange, static_cast<uint32_t>(s));
+                            phys[x] = 0;  // never dereference an invalid id
+                        }
+                    }
+                    if (!mbar_wait(&B.empty[st], ((jw / C::SW) & 1) ^ 1)) {
+                        bad = 1;
+                    } else {
+                        uint8_t* dst = smem + st * C::STAGE_BYTES;
+                        uint8_t* sc = smem + C::OFF_SCALES + st * 16;
+                        const int slab0 = phys[0] * P.hkv + g, slab1 = phys[1] * P.hkv + g;
+                        cp_async8(sc, P.block_scales + slab0);
+                        if (two) cp_async8(sc + 8, P.block_scales + slab1);
+                        cp_async_arrive(&B.full[st]);
+                        mbar_arrive_expect_tx(&B.full[st], (two ? 4 : 2) * C::SLAB);
+                        tma_slab_g2s(dst, tmk, slab0, &B.full[st], policy);
+                        if (two) tma_slab_g2s(dst + C::SLAB, tmk, slab1, &B.full[st], policy);
+                        tma_slab_g2s(dst + 2 * C::SLAB, tmv, slab0, &B.full[st], policy);
+                        if (two) tma_slab_g2s(dst + 3 * C::SLAB, tmv, slab1, &B.full[st], policy);
+                    }
+                }
+                if (__any_sync(FULL, bad)) {
+                    if (lane < cnt && !bad) mbar_wait(&B.full[st], (jw / C::SW) & 1);
+                    aborted = true;
+                    break;
+                }
+                e = e_next;
+                odd = odd_next;
+            }
+        } else {
         for (int base = b0; base < b1; base += kBatch) {
             const int cnt = min(kBatch, b1 - base);
             int e_next = 0;
@@ -705,10 +786,11 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
             }
             e = e_next;
         }
+        }
         // Blocks each warp received from this item.
         if (lane < C::W && !aborted) {
             const int first_w = (lane - rot + C::W) % C::W;
-            const int nb = b1 - b0;
+            const int nb = (b1 - b0 + C::BPS - 1) / C::BPS;
             if (first_w < nb)
                 given += static_cast<uint32_t>((nb - first_w + C::W - 1) / C::W);
         }
@@ -1184,9 +1266,17 @@ __device__ void run_consumer(const DecodeParams& P, uint8_t* smem, const Bars& B
     }
 }
 
-template <int D, int G, int EB>
+// The row of an item whose sum is L: o / L, or 0 for an empty context (L = 0).
+// Pools with a scale per block keep a NaN as it is; the others give 0 for it.
+template <class C>
+__device__ __forceinline__ float4 finish_row(float4 a, float L, float v_scale) {
+    const bool any = C::SCALED ? L != 0.f : L > 0.f;
+    return any ? normalise<C::SCALED ? 2 : C::ELEM>(a, L, v_scale) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+template <class C>
 __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, volatile int* abort_flag, int lane) {
-    using C = Cfg<D, G, EB>;
+    constexpr int D = C::HEAD_DIM, G = C::GROUP;
     const ItemDesc* descs = reinterpret_cast<const ItemDesc*>(smem + C::OFF_DESC);
     const float* mo = reinterpret_cast<const float*>(smem + C::OFF_MO);
     const float2* ml = reinterpret_cast<const float2*>(smem + C::OFF_ML);
@@ -1297,8 +1387,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
                     a.w = fmaf(v[w].w, wt, a.w);
                 }
                 if (d.nparts == 1) {
-                    const float L = msm[g].y;
-                    a = (L > 0.f) ? normalise<EB>(a, L, P.v_scale) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    a = finish_row<C>(a, msm[g].y, P.v_scale);
                 }
                 dst[k] = a;
             }
@@ -1385,8 +1474,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
                 for (int j = 0; j < NJ; ++j) {
                     const int c = lane + 32 * j;
                     if (c < CH) {
-                        const float Lg = pick(L, c / (D / 4));
-                        out4[c] = (Lg > 0.f) ? normalise<EB>(acc[j], Lg, P.v_scale) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        out4[c] = finish_row<C>(acc[j], pick(L, c / (D / 4)), P.v_scale);
                     }
                 }
                 if (lane == 0) atomicExch(ctr, 0u);
@@ -1572,11 +1660,11 @@ __global__ void __launch_bounds__(Cfg<D, G, EB>::THREADS, 1)
         griddep_wait();
         // Test hook: no descriptor is ever published, so the other warps
         // leave through their bounded waits; nothing is in flight.
-        if (!P.stall) run_producer<D, G, EB, FUSED>(P, &tm_k, &tm_v, smem, B, abort_flag, lane);
+        if (!P.stall) run_producer<C, FUSED>(P, &tm_k, &tm_v, smem, B, abort_flag, lane);
     } else if (warp == C::MERGER_WARP) {
         prefetch_first_blocks<D, G, EB>(P, lane, C::STAGES);
         griddep_wait();
-        run_merger<D, G, EB>(P, smem, B, abort_flag, lane);
+        run_merger<C>(P, smem, B, abort_flag, lane);
     } else {
         prefetch_inputs<D, FUSED>(P, threadIdx.x, C::W * 32);
         if constexpr (C::MMA) {
@@ -1630,10 +1718,9 @@ cudaError_t dispatch_g(const DecodeParams& P, int G, int grid, cudaStream_t stre
     }
 }
 
-// One decode launch (FUSED: with each sequence's new row) from the checked
-// arguments; a.stall set arms the test hook for this launch.
-template <bool FUSED>
-cudaError_t launch_decode_t(const DecodeArgs& a, bool stall, cudaStream_t stream) {
+// The kernel's parameters from the checked arguments; stall arms the test
+// hook for this launch.
+inline DecodeParams decode_params(const DecodeArgs& a, bool stall) {
     const DecodeWsLayout L =
         decode_ws_layout(a.num_seqs, a.num_q_heads, a.num_kv_heads, a.head_dim, a.plan.max_ranges,
                          a.prefix_chunks > 0);
@@ -1661,6 +1748,7 @@ cudaError_t launch_decode_t(const DecodeArgs& a, bool stall, cudaStream_t stream
     P.max_ranges = a.plan.max_ranges;
     P.scale_log2 = a.scale * kLog2e;
     P.v_scale = 1.f;
+    P.block_scales = reinterpret_cast<const float2*>(a.block_scales);
     P.stall = stall ? 1 : 0;
     P.k_new = static_cast<const uint8_t*>(a.k_new);
     P.v_new = static_cast<const uint8_t*>(a.v_new);
@@ -1670,11 +1758,20 @@ cudaError_t launch_decode_t(const DecodeArgs& a, bool stall, cudaStream_t stream
     P.skip_blocks = a.skip_blocks;
     P.pre_ml = a.prefix_chunks > 0 ? reinterpret_cast<const float2*>(ws + L.pre_ml) : nullptr;
     P.pre_o = a.prefix_chunks > 0 ? reinterpret_cast<const float*>(ws + L.pre_o) : nullptr;
-    const int G = a.num_q_heads / a.num_kv_heads;
     if (a.kv_e4m3) {
         // q' = q * scale*log2(e) * k_scale against the K codes.
         P.scale_log2 = a.scale * kLog2e * a.k_scale;
         P.v_scale = a.v_scale;
+    }
+    return P;
+}
+
+// One decode launch (FUSED: with each sequence's new row).
+template <bool FUSED>
+cudaError_t launch_decode_t(const DecodeArgs& a, bool stall, cudaStream_t stream) {
+    const DecodeParams P = decode_params(a, stall);
+    const int G = a.num_q_heads / a.num_kv_heads;
+    if (a.kv_e4m3) {
         if (a.head_dim == 128) return dispatch_g<128, 1, FUSED>(P, G, a.plan.grid, stream);
         if (a.head_dim == 64) return dispatch_g<64, 1, FUSED>(P, G, a.plan.grid, stream);
         return cudaErrorInvalidValue;

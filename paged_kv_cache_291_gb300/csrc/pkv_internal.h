@@ -36,8 +36,10 @@ struct DecodeArgs {
     int32_t num_seqs, max_blocks_per_seq, max_context_len;
     DecodePlan plan;
     float scale;
-    bool kv_e4m3;                  // pools hold e4m3 codes (else bf16)
-    float k_scale, v_scale;        // e4m3 pools: element = code value * scale
+    bool kv_e4m3;                  // pools hold e4m3 codes with one scale a pool
+    float k_scale, v_scale;        // those: element = code value * scale
+    const float* block_scales = nullptr;  // 8-bit pools with a scale per (block, kv head), else null
+    bool int8_codes = false;              // those: int8 codes (else e4m3)
     // Fused step: each sequence's new row (bf16 [S][Hkv][d]) and its slot,
     // stored and used in the same launch; all null for plain decode.
     const void* k_new = nullptr;
@@ -73,15 +75,19 @@ int32_t shared_prefix_chunks(int32_t num_seqs, int32_t num_q_heads, int32_t num_
 // launch it right before launch_decode(a) on the same stream.
 cudaError_t launch_shared_prefix(const DecodeArgs& a, cudaStream_t stream);
 
-// A tiled tensor map with the 128-byte swizzle (element type dtype, or bf16).
+// A tiled tensor map (element type dtype, or bf16 and the 128-byte swizzle).
 bool make_tile_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, cuuint32_t rank,
-                   const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box);
+                   const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 bool make_bf16_map(CUtensorMap* map, const void* base, cuuint32_t rank, const cuuint64_t* dims,
                    const cuuint64_t* strides_bytes, const cuuint32_t* box);
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // The fused step's variant (a.k_new set), called by launch_decode.
 cudaError_t launch_decode_fused(const DecodeArgs& a, bool stall, cudaStream_t stream);
+// Pools with a scale per block (a.block_scales set), called by launch_decode.
+cudaError_t launch_decode_scaled_e4m3(const DecodeArgs& a, bool stall, cudaStream_t stream);
+cudaError_t launch_decode_scaled_int8(const DecodeArgs& a, bool stall, cudaStream_t stream);
 
 // Test hook: the next `launches` decode launches run with a producer warp
 // that issues nothing, so their other warps time out (PKV_ERR_TIMEOUT).

@@ -736,13 +736,14 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 bool make_tile_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, cuuint32_t rank,
-                   const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+                   const cuuint64_t* dims, const cuuint64_t* strides_bytes, const cuuint32_t* box,
+                   CUtensorMapSwizzle swizzle) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint32_t elem_strides[3] = {1, 1, 1};
     std::memset(map, 0, sizeof(*map));
     const CUresult r = fn(map, dtype, rank, const_cast<void*>(base), dims, strides_bytes, box, elem_strides,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }

@@ -13,7 +13,7 @@ namespace pkv {
 // Element kinds, as the kernels are instantiated (pkv_cache_t.kv_dtype).
 constexpr int kKindBf16 = 0, kKindE4m3 = 1, kKindE4m3Blocks = 2, kKindInt8Blocks = 3;
 
-constexpr float kLeastScale = 0x1p-100f;
+constexpr float kLeastScale = 0x1p-100f, kMostScale = 0x1p122f;
 
 // The largest code of a kind, and its reciprocal rounded to fp32.
 template <int KIND>
@@ -21,10 +21,11 @@ constexpr float code_max() { return KIND == kKindInt8Blocks ? 127.f : 448.f; }
 template <int KIND>
 constexpr float inv_code_max() { return 1.f / code_max<KIND>(); }
 
-// A stored scale as the calls use it: finite and at least 2^-100, anything
-// else (`bad` is then set) counts as 2^-100.
+// A stored scale as the calls use it: 2^-100 to 2^122 (the append's are in
+// there for every bf16 value); anything else (`bad` is then set) counts as
+// 2^-100.
 __device__ __forceinline__ float checked_scale(float s, bool& bad) {
-    const bool ok = s >= kLeastScale && s < INFINITY;
+    const bool ok = s >= kLeastScale && s <= kMostScale;
     bad |= !ok;
     return ok ? s : kLeastScale;
 }
