@@ -64,6 +64,7 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "scaled_device.cuh"
 
 namespace pkv {
 
@@ -159,6 +160,9 @@ struct DecodeParams {
     const float2* pre_ml;
     const float* pre_o;
     const float2* block_scales;  // pools with a scale per block: [num_blocks][Hkv] (K, V)
+    // Units a pair counts beyond its blocks in the cut of the work, for what
+    // an item costs however short it is; they hold no keys.
+    int32_t extra_units;
 };
 
 constexpr int align_up(int x, int a) { return (x + a - 1) / a * a; }
@@ -232,7 +236,30 @@ struct Bars {
     uint64_t* iempty;  // [ITEMS]    consumers and merger read the descriptor
     uint64_t* mfull;   // [MERGE]    8 consumer states published
     uint64_t* mempty;  // [MERGE]    merger done with the buffer
+    uint64_t* ofull;   // [W][ORDERS] an order for a consumer warp (pools with a scale per block)
+    uint64_t* oempty;  // [W][ORDERS] its stage is done with
 };
+
+// A stage a consumer warp is to load: the slabs of its blocks (the second if
+// `two`) and their scales, K's and V's, the latter as f 2^e with f in [1, 2).
+struct __align__(16) BlockScales {
+    float k, f, e, inv_2e;
+};
+struct __align__(16) Order {
+    int32_t slab[2], two, unused;
+    BlockScales scales[2];
+};
+
+__device__ __forceinline__ BlockScales block_scales_of(float2 s, bool& bad) {
+    BlockScales r;
+    r.k = checked_scale(s.x, bad);
+    const uint32_t bits = __float_as_uint(checked_scale(s.y, bad));
+    const int e = static_cast<int>(bits >> 23) - 127;
+    r.f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+    r.e = static_cast<float>(e);
+    r.inv_2e = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    return r;
+}
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -315,7 +342,7 @@ __device__ __forceinline__ int seq_units(const DecodeParams& P, int s, int& n_ou
         n = n < 0 ? 0 : P.ctx_cap;
     }
     n_out = n;
-    return max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks);
+    return max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks) + P.extra_units;
 }
 
 __device__ __forceinline__ uint4 lds128(const void* p) {
@@ -347,17 +374,6 @@ __device__ __forceinline__ void tma_slab_g2s(void* smem_dst, const CUtensorMap* 
         "[%1, {%2, %2, %3}], [%4], %5;" ::"r"(smem_addr(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(slab), "r"(smem_addr(bar)), "l"(policy)
         : "memory");
-}
-
-// Eight bytes from global to shared memory, asynchronously; cp_async_arrive
-// arrives on `bar` (counting as one of its arrivals) once the copies that
-// this thread issued before it have landed.
-__device__ __forceinline__ void cp_async8(void* smem_dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem_dst)), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Byte offset of 16-byte chunk c of row r in a slab stored as 128-byte
@@ -663,10 +679,15 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
         // table entries are requested before this batch's copies.
         constexpr int kBatch = C::STAGES < 32 ? C::STAGES : 32;
         if constexpr (C::SCALED) {
-            // The same with two blocks a stage: stage i of the item holds
-            // blocks b0 + 2 i and the next one, if the item has it.  Their
-            // scales come with them: an 8-byte asynchronous copy each, whose
-            // completion is the full barrier's second arrival.
+            // Two blocks a stage: stage i of the item holds blocks b0 + 2 i and
+            // the next one, if the item has it, and goes to warp w = (i + rot)
+            // % W, which issues the copies itself: lane k of a batch leaves
+            // the slabs and scales of one stage in w's ring of orders.  Issuing
+            // a stage's four tiled copies takes one thread about 740 cycles,
+            // two stages' share of HBM time, so one producer warp cannot
+            // (68 contexts of 40/40 x 128: 633 us; two of them 430).
+            constexpr int kBatch = 32 < C::ORDERS / 2 * C::W ? 32 : C::ORDERS / 2 * C::W;
+            Order* orders = reinterpret_cast<Order*>(smem + C::OFF_ORDERS);
             const int nst = (b1 - b0 + 1) / 2;
             for (int base = 0; base < nst; base += kBatch) {
                 const int cnt = min(kBatch, nst - base);
@@ -679,36 +700,31 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
                 const int first_w = (w - rot + C::W) % C::W;
                 const uint32_t jw = static_cast<uint32_t>(__shfl_sync(FULL, static_cast<int>(given), w)) +
                                     static_cast<uint32_t>((i - first_w) / C::W);
-                const uint32_t st = static_cast<uint32_t>(w * C::SW) + jw % C::SW;
-                const bool two = b0 + 2 * i + 1 < b1;
                 int bad = 0;
                 if (lane < cnt) {
-                    int phys[2] = {e, two ? odd : e};
+                    Order o;
+                    o.two = b0 + 2 * i + 1 < b1;
+                    bool bad_scale = false;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        if (phys[x] < 0 || phys[x] >= P.num_blocks) {
+                        int id = x && o.two ? odd : e;
+                        if (id < 0 || id >= P.num_blocks) {
                             record_error(P.err, kErrRange, static_cast<uint32_t>(s));
-                            phys[x] = 0;  // never dereference an invalid id
+                            id = 0;  // never dereference an invalid id
                         }
+                        o.slab[x] = id * P.hkv + g;
+                        o.scales[x] = block_scales_of(__ldg(P.block_scales + o.slab[x]), bad_scale);
                     }
-                    if (!mbar_wait(&B.empty[st], ((jw / C::SW) & 1) ^ 1)) {
+                    if (bad_scale) record_error(P.err, kErrRange, static_cast<uint32_t>(s));
+                    const uint32_t at = static_cast<uint32_t>(w * C::ORDERS) + jw % C::ORDERS;
+                    if (!mbar_wait(&B.oempty[at], ((jw / C::ORDERS) & 1) ^ 1)) {
                         bad = 1;
                     } else {
-                        uint8_t* dst = smem + st * C::STAGE_BYTES;
-                        uint8_t* sc = smem + C::OFF_SCALES + st * 16;
-                        const int slab0 = phys[0] * P.hkv + g, slab1 = phys[1] * P.hkv + g;
-                        cp_async8(sc, P.block_scales + slab0);
-                        if (two) cp_async8(sc + 8, P.block_scales + slab1);
-                        cp_async_arrive(&B.full[st]);
-                        mbar_arrive_expect_tx(&B.full[st], (two ? 4 : 2) * C::SLAB);
-                        tma_slab_g2s(dst, tmk, slab0, &B.full[st], policy);
-                        if (two) tma_slab_g2s(dst + C::SLAB, tmk, slab1, &B.full[st], policy);
-                        tma_slab_g2s(dst + 2 * C::SLAB, tmv, slab0, &B.full[st], policy);
-                        if (two) tma_slab_g2s(dst + 3 * C::SLAB, tmv, slab1, &B.full[st], policy);
+                        orders[at] = o;
+                        mbar_arrive(&B.ofull[at]);
                     }
                 }
                 if (__any_sync(FULL, bad)) {
-                    if (lane < cnt && !bad) mbar_wait(&B.full[st], (jw / C::SW) & 1);
                     aborted = true;
                     break;
                 }
@@ -861,7 +877,7 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
         *abort_flag = 1;
         record_error(P.err, kErrTimeout, 1u);
         // Never leave with bulk copies still in flight.
-        if (lane < C::W) {
+        if (!C::SCALED && lane < C::W) {
             for (uint32_t k = 0; k < C::SW; ++k) {
                 if (k < given) {
                     const uint32_t jl = given - 1 - ((given - 1 - k) % C::SW);  // last use of stage k
@@ -1558,7 +1574,7 @@ __device__ void prefetch_first_blocks(const DecodeParams& P, int lane, int max_u
         if (s < P.num_seqs) {
             const bool dec = P.qsl == nullptr || ld_l2_only(P.qsl + s + 1) - ld_l2_only(P.qsl + s) == 1;
             const int n = min(max(ld_l2_only(P.context_lens + s), 0), P.ctx_cap);
-            u[w] = dec ? max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks) : 0;
+            u[w] = dec ? max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks) + P.extra_units : 0;
         }
     }
     long long per_head = 0;
@@ -1749,6 +1765,7 @@ inline DecodeParams decode_params(const DecodeArgs& a, bool stall) {
     P.scale_log2 = a.scale * kLog2e;
     P.v_scale = 1.f;
     P.block_scales = reinterpret_cast<const float2*>(a.block_scales);
+    P.extra_units = 0;
     P.stall = stall ? 1 : 0;
     P.k_new = static_cast<const uint8_t*>(a.k_new);
     P.v_new = static_cast<const uint8_t*>(a.v_new);

@@ -34,6 +34,7 @@
 
 #include "decode_kernel.cuh"
 #include "scaled_device.cuh"
+#include "tcgen05_rows.cuh"
 
 namespace pkv {
 namespace {
@@ -43,14 +44,21 @@ struct ScaledCfg {
     static constexpr int HEAD_DIM = D, GROUP = G, ELEM = 1;
     static constexpr bool SCALED = true, MMA = true;
     static constexpr int BPS = 2;
-#ifdef PKV_SCALED_WARPS
-    static constexpr int W = PKV_SCALED_WARPS;
-#else
-    static constexpr int W = 8;  // consumer warps
-#endif
+    // Consumer warps: each is bound by the latency of its own chain, so as many
+    // as the ring has two stages for (68 contexts of 40/40 x 128: 8 warps
+    // 394 us, 11 375, 12 359; 10 that no longer have two stages each, at head
+    // groups of 8, 55 against 44 with 8).
+    static constexpr int W = G <= 2 ? 12 : 8;
     static constexpr int MERGE_LANES = W <= 8 ? 8 : 16;
+    // What a pair costs beyond its blocks, in blocks: its warps' states are
+    // handed over and merged, and its last stages leave warps idle.  Without
+    // it the CTA that gets the short contexts ends last (31 contexts of 300
+    // to 4,096 tokens, 64/8 x 128: 44.2 us with 0, 41.6 with 4, 37 with 8 and
+    // 16; 68 contexts of 40/40 x 128: 359 with 0, 340 with 8 and 16).
+    static constexpr int EXTRA_UNITS = 12;
     static constexpr int MERGE_BUFS = 1;
     static constexpr int PRODUCER_WARP = W, MERGER_WARP = W + 1, THREADS = 32 * (W + 2);
+    static constexpr int ORDERS = 8;  // stages a consumer warp is told of ahead
     static constexpr int SLAB = kBlockSize * D;
     static constexpr int STAGE_BYTES = 4 * SLAB;  // K of two blocks, V of two blocks
     static constexpr int QBYTES = G * D * 2;
@@ -61,13 +69,14 @@ struct ScaledCfg {
     static constexpr int R_WT = R_ML + MERGE_BUFS * W * G * 8;
     static constexpr int R_MSM = align_up(R_WT + G * (W + 1) * 4, 8);
     static constexpr int R_BAR = align_up(R_MSM + G * 8, 8);
-    // 226 KB less the regions above, 64 barriers beside the stages' own, the
-    // flag and the 1,024-byte alignment of the ring.
-    static constexpr int STAGES_FIT = (226 * 1024 - R_BAR - 64 * 8 - 32 - 1024) / (STAGE_BYTES + 16 + 16);
+    // 226 KB less the regions above, the orders and their barriers, 32 more
+    // barriers and the 1,024-byte alignment of the ring; a stage has one barrier.
+    static constexpr int STAGES_FIT =
+        (226 * 1024 - R_BAR - W * ORDERS * ((int)sizeof(Order) + 16) - 32 * 8 - 32 - 1024) / (STAGE_BYTES + 8);
     static constexpr int SW_FIT = STAGES_FIT / W;
     static constexpr int SW = SW_FIT < 6 ? SW_FIT : 6;
     static constexpr int STAGES = SW * W;
-    static constexpr int NBAR = 2 * STAGES + 2 * kItemRing + 2 * MERGE_BUFS;
+    static constexpr int NBAR = STAGES + 2 * kItemRing + 2 * MERGE_BUFS + 2 * W * ORDERS;
     static constexpr int OFF_REST = STAGES * STAGE_BYTES;
     static constexpr int OFF_ITEMQ = OFF_REST + R_ITEMQ;
     static constexpr int OFF_DESC = OFF_REST + R_DESC;
@@ -77,12 +86,12 @@ struct ScaledCfg {
     static constexpr int OFF_MSM = OFF_REST + R_MSM;
     static constexpr int OFF_BAR = OFF_REST + R_BAR;
     static constexpr int OFF_FLAG = OFF_BAR + NBAR * 8;
-    static constexpr int OFF_SCALES = align_up(OFF_FLAG + 4, 16);  // [STAGES] two (K, V) pairs
-    static constexpr int OFF_NEW = OFF_SCALES;                     // of fused steps only, which there are none of
-    static constexpr int SMEM = OFF_SCALES + STAGES * 16 + 1024;
+    static constexpr int OFF_ORDERS = align_up(OFF_FLAG + 4, 16);
+    static constexpr int OFF_NEW = OFF_ORDERS;  // of fused steps only, which there are none of
+    static constexpr int SMEM = OFF_ORDERS + W * ORDERS * (int)sizeof(Order) + 1024;
     static_assert(SW >= 1, "ring too shallow");
     static_assert(OFF_ITEMQ % 16 == 0 && OFF_DESC % 16 == 0 && OFF_MO % 16 == 0 && OFF_ML % 8 == 0 &&
-                      OFF_MSM % 8 == 0 && OFF_BAR % 8 == 0 && STAGE_BYTES % 1024 == 0 && SLAB % 512 == 0,
+                      OFF_BAR % 8 == 0 && STAGE_BYTES % 1024 == 0 && SLAB % 512 == 0,
                   "shared-memory regions aligned for their widest access");
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -94,10 +103,16 @@ constexpr float kScaledThreshold = 3.0f, kScaledShift = 11.0f;
 // bytes with chunks XORed by r mod 8, rows of 64 bytes with chunks XORed by
 // (r / 2) mod 4.
 template <int D>
-__device__ __forceinline__ uint32_t slab_at(int r, int c) {
-    return D == 128 ? static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4))
-                    : static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+__device__ __forceinline__ int slab_at(int r, int c) {
+    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
+
+// Where lane (g, t) reads: K chunk 2t (+ 1) of row key_row(g) (64-byte rows:
+// chunk t), its D / 8 dims of V rows key_row(2t) and key_row(2t + 1).  The other half of
+// a block is 8 rows on, with the same swizzle.
+struct LaneOffsets {
+    int k, k1, v0, v1;
+};
 
 // Row of a block (within its half) that column n of an S tile stands for.
 // Rows of 128 bytes: n itself; reading chunk 2t + c of rows g (K) and chunk g
@@ -108,6 +123,17 @@ __device__ __forceinline__ uint32_t slab_at(int r, int c) {
 template <int D>
 __device__ __forceinline__ int key_row(int n) {
     return D == 128 ? n : ((n & 2) << 1) | ((n & 1) << 1) | ((n >> 2) ^ (n & 1));
+}
+
+template <int D>
+__device__ __forceinline__ LaneOffsets lane_offsets(int g, int t) {
+    LaneOffsets r;
+    r.k = slab_at<D>(key_row<D>(g), D == 128 ? 2 * t : t);
+    r.k1 = r.k ^ 16;
+    const int c = D == 128 ? g : g >> 1, in = D == 128 ? 0 : 8 * (g & 1);
+    r.v0 = slab_at<D>(key_row<D>(2 * t), c) + in;
+    r.v1 = slab_at<D>(key_row<D>(2 * t + 1), c) + in;
+    return r;
 }
 
 // Two codes in bytes 0 and 1 (HI: 2 and 3) of w to an fp16 pair, exactly.
@@ -130,42 +156,68 @@ __device__ __forceinline__ uint32_t turned(uint32_t w) {
     return KIND == kKindInt8Blocks ? w ^ 0x80808080u : w;
 }
 
-// S tile: eight keys (rows key_row(0..7) + 8 half of the slab).
+// Unlike mma_f16 and lds128 free to be moved: the order of the products and of
+// the loads of a stage is the compiler's, so that chains run side by side (in
+// program order a stage takes three times as long).
+__device__ __forceinline__ void mma_free(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Scores of a block, S = K Q^T: lane (g, t) gets those of rows key_row(g) (s[0],
+// s[1]) and key_row(g) + 8 (s[2], s[3]) for heads 2t and 2t + 1.
 template <int D, int KIND>
-__device__ __forceinline__ void scores(const uint8_t* k, int half, const uint32_t (&qa)[D / 8], float (&s)[4], int g,
-                                       int t) {
+__device__ __forceinline__ void scores(const uint8_t* k, const uint32_t (&qb)[D / 8], float (&s)[4],
+                                       const LaneOffsets& at) {
     s[0] = s[1] = s[2] = s[3] = 0.f;
-    const int row = 8 * half + key_row<D>(g);
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-        const uint4 u = lds128(k + slab_at<D>(row, D == 128 ? 2 * t + c : t));
-        const uint32_t w[4] = {turned<KIND>(u.x), turned<KIND>(u.y), turned<KIND>(u.z), turned<KIND>(u.w)};
+        uint32_t w[2][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint4 u = *reinterpret_cast<const uint4*>(k + (c ? at.k1 : at.k) + x * 8 * D);
+            w[x][0] = turned<KIND>(u.x), w[x][1] = turned<KIND>(u.y);
+            w[x][2] = turned<KIND>(u.z), w[x][3] = turned<KIND>(u.w);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            mma_f16(s, qa[2 * (4 * c + i)], 0u, qa[2 * (4 * c + i) + 1], 0u, widen2<KIND, false>(w[i]),
-                    widen2<KIND, true>(w[i]));
+            mma_free(s, widen2<KIND, false>(w[0][i]), widen2<KIND, false>(w[1][i]), widen2<KIND, true>(w[0][i]),
+                     widen2<KIND, true>(w[1][i]), qb[2 * (4 * c + i)], qb[2 * (4 * c + i) + 1]);
     }
 }
 
-// O += P V over one block: p[0..1] the hi and lo pair of the keys of half 0,
-// p[2..3] of half 1.  Rows past the context are zero where their codes could
-// be NaN.
+// An 8 x 8 matrix of 16-bit values, lane (g, t) holding row g, columns 2t and
+// 2t + 1, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// O^T += V^T P^T over one block: p[0] and p[2] are P (rounded to fp16) of
+// the keys of halves 0 and 1, p[1] and p[3] what the rounding lost.  Tile mm's
+// rows g and g + 8 are dims (D / 8) g + 2 mm and + 1, its columns the heads.
+// Rows past the context are zero where their codes could be NaN.
 template <int D, int KIND>
-__device__ __forceinline__ void weigh(const uint8_t* v, int valid, const uint32_t (&p)[4], float (&o)[D / 8][4], int g,
-                                      int t) {
+__device__ __forceinline__ void weigh(const uint8_t* v, int valid, const uint32_t (&p)[4], float (&o)[D / 16][4],
+                                      const LaneOffsets& at, int t) {
     constexpr int NW = D / 32;  // words of a lane's D / 8 dims
     uint32_t w[4][NW];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int row = 8 * (j >> 1) + key_row<D>(2 * t + (j & 1));
+        const uint8_t* src = v + (j & 1 ? at.v1 : at.v0) + (j >> 1) * 8 * D;
         if constexpr (D == 128) {
-            const uint4 u = lds128(v + slab_at<D>(row, g));
+            const uint4 u = *reinterpret_cast<const uint4*>(src);
             w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
         } else {
-            const uint2 u = lds64(v + slab_at<D>(row, g >> 1) + 8 * (g & 1));
+            const uint2 u = *reinterpret_cast<const uint2*>(src);
             w[j][0] = u.x, w[j][1] = u.y;
         }
         if (KIND != kKindInt8Blocks && valid < kBlockSize) {
+            const int row = 8 * (j >> 1) + key_row<D>(2 * t + (j & 1));
 #pragma unroll
             for (int i = 0; i < NW; ++i) w[j][i] = row < valid ? w[j][i] : 0u;
         }
@@ -178,14 +230,30 @@ __device__ __forceinline__ void weigh(const uint8_t* v, int valid, const uint32_
         for (int x = 0; x < 2; ++x) {
             const uint32_t a = __byte_perm(w[0][i], w[1][i], x ? 0x7362 : 0x5140);
             const uint32_t b = __byte_perm(w[2][i], w[3][i], x ? 0x7362 : 0x5140);
-            mma_f16(o[4 * i + 2 * x], p[0], p[1], p[2], p[3], widen2<KIND, false>(a), widen2<KIND, false>(b));
-            mma_f16(o[4 * i + 2 * x + 1], p[0], p[1], p[2], p[3], widen2<KIND, true>(a), widen2<KIND, true>(b));
+            const uint32_t a0 = widen2<KIND, false>(a), a1 = widen2<KIND, true>(a);
+            const uint32_t a2 = widen2<KIND, false>(b), a3 = widen2<KIND, true>(b);
+            mma_free(o[2 * i + x], a0, a1, a2, a3, p[0], p[2]);
+            mma_free(o[2 * i + x], a0, a1, a2, a3, p[1], p[3]);
         }
     }
 }
 
+// Whether the phase with the given parity has completed, for the whole warp.
+__device__ __forceinline__ bool mbar_test_warp(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, ok);
+}
+
 template <class C, int KIND>
-__device__ void run_consumer_scaled(const DecodeParams& P, uint8_t* smem, const Bars& B, volatile int* abort_flag,
+__device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tmk, const CUtensorMap* tmv,
+                                    uint8_t* smem, const Bars& B, volatile int* abort_flag,
                                     int warp, int lane) {
     constexpr int D = C::HEAD_DIM, G = C::GROUP;
     constexpr int QW = D / 8;   // q words of a lane: its D / 4 dims
@@ -194,32 +262,63 @@ __device__ void run_consumer_scaled(const DecodeParams& P, uint8_t* smem, const 
     float* mo = reinterpret_cast<float*>(smem + C::OFF_MO);
     float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
     const int g = lane >> 2, t = lane & 3;
-    uint32_t taken = 0, item_seq = 0;
+    const LaneOffsets at = lane_offsets<D>(g, t);
+    const Order* orders = reinterpret_cast<const Order*>(smem + C::OFF_ORDERS) + warp * C::ORDERS;
+    uint64_t* ofull = B.ofull + warp * C::ORDERS;
+    uint64_t* full = B.full + warp * C::SW;
+    uint8_t* ring = smem + warp * C::SW * C::STAGE_BYTES;
+    const uint64_t policy = l2_policy_evict_first();
+    uint32_t taken = 0, issued = 0, item_seq = 0;  // stages consumed, asked for
     bool ok = true;
+    // Asks for the stages that are free and ordered.
+    auto issue = [&]() {
+        while (issued - taken < C::SW && mbar_test_warp(&ofull[issued % C::ORDERS], (issued / C::ORDERS) & 1)) {
+            const Order* o = orders + issued % C::ORDERS;
+            const int slab0 = o->slab[0], slab1 = o->slab[1];
+            const bool two = o->two != 0;
+            if (tc::elect_one()) {
+                uint8_t* dst = ring + issued % C::SW * C::STAGE_BYTES;
+                uint64_t* bar = &full[issued % C::SW];
+                mbar_arrive_expect_tx(bar, (two ? 4 : 2) * C::SLAB);
+                tma_slab_g2s(dst, tmk, slab0, bar, policy);
+                if (two) tma_slab_g2s(dst + C::SLAB, tmk, slab1, bar, policy);
+                tma_slab_g2s(dst + 2 * C::SLAB, tmv, slab0, bar, policy);
+                if (two) tma_slab_g2s(dst + 3 * C::SLAB, tmv, slab1, bar, policy);
+            }
+            __syncwarp();
+            ++issued;
+        }
+    };
     while (ok) {
         const uint32_t slot = item_seq % kItemRing;
-        if (*abort_flag || !mbar_wait_warp(&B.ifull[slot], (item_seq / kItemRing) & 1)) {
-            ok = false;
-            break;
+        // The item's stages may be ordered before its q has landed.
+        issue();
+        if (!mbar_test_warp(&B.ifull[slot], (item_seq / kItemRing) & 1)) {
+            const uint64_t t0 = global_timer_ns();
+            while (ok && !mbar_test_warp(&B.ifull[slot], (item_seq / kItemRing) & 1)) {
+                issue();
+                ok = !__any_sync(FULL, *abort_flag != 0 || global_timer_ns() - t0 > kWaitLimitNs);
+            }
+            if (!ok) break;
         }
         const ItemDesc d = descs[slot];
         if (d.s < 0) break;
         // q of head g, dims (D / 4) t and on, as the A operand (zero for g >=
         // G), scaled by a power of two so that the largest is in [2^14, 2^15)
         // of fp16; the scores get the factor back.
-        uint32_t qa[QW];
-        float f;
+        uint32_t qb[QW];
+        float f0, f1;
         {
             const uint8_t* qs = smem + C::OFF_ITEMQ + slot * C::QBYTES + (g * D + t * (D / 4)) * 2;
 #pragma unroll
             for (int c = 0; c < QW / 4; ++c) {
                 uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (g < G) u = lds128(qs + 16 * c);
-                qa[4 * c] = u.x, qa[4 * c + 1] = u.y, qa[4 * c + 2] = u.z, qa[4 * c + 3] = u.w;
+                if (g < G) u = *reinterpret_cast<const uint4*>(qs + 16 * c);
+                qb[4 * c] = u.x, qb[4 * c + 1] = u.y, qb[4 * c + 2] = u.z, qb[4 * c + 3] = u.w;
             }
             float mx = 0.f;
 #pragma unroll
-            for (int i = 0; i < QW; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qa[i])), fabsf(bf16hi(qa[i]))));
+            for (int i = 0; i < QW; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(qb[i])), fabsf(bf16hi(qb[i]))));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
             int e = 0;
@@ -227,110 +326,117 @@ __device__ void run_consumer_scaled(const DecodeParams& P, uint8_t* smem, const 
             const float down = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
             const float up = __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 #pragma unroll
-            for (int i = 0; i < QW; ++i) qa[i] = f16x2_rn(bf16lo(qa[i]) * down, bf16hi(qa[i]) * down);
-            f = P.scale_log2 * up;
+            for (int i = 0; i < QW; ++i) qb[i] = f16x2_rn(bf16lo(qb[i]) * down, bf16hi(qb[i]) * down);
+            f0 = P.scale_log2 * __shfl_sync(FULL, up, 8 * t);
+            f1 = P.scale_log2 * __shfl_sync(FULL, up, 8 * t + 4);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.iempty[slot]);
-        float m = -INFINITY, l = 0.f;
-        float o[D / 8][4];
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float o[D / 16][4];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         const int nst = (d.b1 - d.b0 + 1) / 2;
         const int first = (warp - d.rot + C::W) % C::W;
         for (int b = first; b < nst; b += C::W) {
-            const uint32_t st = static_cast<uint32_t>(warp * C::SW) + taken % C::SW;
-            if (*abort_flag || !mbar_wait_warp(&B.full[st], (taken / C::SW) & 1)) {
+            const uint32_t st = taken % C::SW;
+            issue();
+            if (issued == taken) {  // not even this one is ordered yet
+                if (!mbar_wait_warp(&ofull[taken % C::ORDERS], (taken / C::ORDERS) & 1)) {
+                    ok = false;
+                    break;
+                }
+                issue();
+            }
+            if (*abort_flag || !mbar_wait_warp(&full[st], (taken / C::SW) & 1)) {
                 ok = false;
                 break;
             }
+            const Order* order = orders + taken % C::ORDERS;
             const int blk = d.b0 + 2 * b;
             const int keys = min(2 * kBlockSize, (min(d.b1 * kBlockSize, d.n) - blk * kBlockSize));
-            const int valid[2] = {min(keys, kBlockSize), max(keys - kBlockSize, 0)};
-            const uint8_t* kst = smem + st * C::STAGE_BYTES;
-            float4 sc = *reinterpret_cast<const float4*>(smem + C::OFF_SCALES + st * 16);
-            if (valid[1] == 0) sc.z = sc.w = 1.f;
-            bool bad = false;
-            const float ks[2] = {checked_scale(sc.x, bad), checked_scale(sc.z, bad)};
-            const float vs[2] = {checked_scale(sc.y, bad), checked_scale(sc.w, bad)};
-            if (bad && lane == 0) record_error(P.err, kErrRange, static_cast<uint32_t>(d.s));
-            // Scores of keys 8 half + key_row(2t), key_row(2t + 1) of each block.
-            float x[2][4];
+            {
+                constexpr int NB = C::BPS, i0 = 0;
+                const uint8_t* kst = ring + st * C::STAGE_BYTES + i0 * C::SLAB;
+                float u[NB][4];
+                BlockScales sc[NB];
+                int valid[NB];
+                float mb0 = -INFINITY, mb1 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < NB; ++i) scores<D, KIND>(kst + i * C::SLAB, qb, u[i], at);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float s[4];
-                    scores<D, KIND>(kst + i * C::SLAB, half, qa, s, g, t);
-                    x[i][2 * half] = s[0], x[i][2 * half + 1] = s[1];
+                for (int i = 0; i < NB; ++i) {
+                    valid[i] = min(max(keys - (i0 + i) * kBlockSize, 0), kBlockSize);
+                    sc[i] = order->scales[i0 + i];
+                    const float k0 = f0 * sc[i].k, k1 = f1 * sc[i].k;
+                    u[i][0] *= k0, u[i][1] *= k1, u[i][2] *= k0, u[i][3] *= k1;
+                    if (valid[i] < kBlockSize) {
+                        if (key_row<D>(g) >= valid[i]) u[i][0] = u[i][1] = -INFINITY;
+                        if (key_row<D>(g) + 8 >= valid[i]) u[i][2] = u[i][3] = -INFINITY;
+                    }
+                    mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]) + sc[i].e);
+                    mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]) + sc[i].e);
                 }
-            }
-            float mb = -INFINITY, ve[2], vf[2], back[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t bits = __float_as_uint(vs[i]);
-                const int e = static_cast<int>(bits >> 23) - 127;
-                ve[i] = static_cast<float>(e);
-                vf[i] = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-                back[i] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                const float kf = f * ks[i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[i][j] *= kf;
-                    if (valid[i] < kBlockSize && 8 * (j >> 1) + key_row<D>(2 * t + (j & 1)) >= valid[i])
-                        x[i][j] = -INFINITY;
+                for (int off = 4; off < 32; off <<= 1) {
+                    mb0 = fmaxf(mb0, __shfl_xor_sync(FULL, mb0, off));
+                    mb1 = fmaxf(mb1, __shfl_xor_sync(FULL, mb1, off));
                 }
-                mb = fmaxf(mb, fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) + ve[i]);
-            }
-            mb = fmaxf(mb, __shfl_xor_sync(FULL, mb, 1));
-            mb = fmaxf(mb, __shfl_xor_sync(FULL, mb, 2));
-            const bool moves = mb > m + kScaledThreshold;
-            if (__any_sync(FULL, moves)) {
-                const float a = moves ? fast_exp2(m - mb) : 1.f;
-                m = moves ? mb : m;
-                l *= a;
+                // A new reference only where the maximum grew by more than 2^3.
+                const bool moves0 = mb0 > m0 + kScaledThreshold, moves1 = mb1 > m1 + kScaledThreshold;
+                if (__any_sync(FULL, moves0 || moves1)) {
+                    const float a0 = moves0 ? fast_exp2(m0 - mb0) : 1.f, a1 = moves1 ? fast_exp2(m1 - mb1) : 1.f;
+                    m0 = moves0 ? mb0 : m0;
+                    m1 = moves1 ? mb1 : m1;
+                    l0 *= a0;
+                    l1 *= a1;
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j) o[j][0] *= a, o[j][1] *= a, o[j][2] *= a, o[j][3] *= a;
-            }
+                    for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
+                }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (i == 1 && valid[1] == 0) break;
-                const float add = ve[i] + kScaledShift - m;
-                float u[4];
+                for (int i = 0; i < NB; ++i) {
+                    if (NB > 1 && i > 0 && valid[i] == 0) break;
+                    const float add0 = sc[i].e + kScaledShift - m0, add1 = sc[i].e + kScaledShift - m1;
+                    u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
+                    u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
+                    l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);
+                    l1 = fmaf(u[i][1] + u[i][3], sc[i].inv_2e, l1);
+                    uint32_t p[4];
+                    split_pair_f16(u[i][0] * sc[i].f, u[i][1] * sc[i].f, p[0], p[1]);
+                    split_pair_f16(u[i][2] * sc[i].f, u[i][3] * sc[i].f, p[2], p[3]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] = fast_exp2(x[i][j] + add);
-                l = fmaf((u[0] + u[1]) + (u[2] + u[3]), back[i], l);
-                uint32_t p[4];
-                split_pair_f16(u[0] * vf[i], u[1] * vf[i], p[0], p[1]);
-                split_pair_f16(u[2] * vf[i], u[3] * vf[i], p[2], p[3]);
-                weigh<D, KIND>(kst + (2 + i) * C::SLAB, valid[i], p, o, g, t);
+                    for (int j = 0; j < 4; ++j) p[j] = transposed(p[j]);
+                    weigh<D, KIND>(kst + (2 + i) * C::SLAB, valid[i], p, o, at, t);
+                }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&B.empty[st]);
+            if (lane == 0) mbar_arrive(&B.oempty[warp * C::ORDERS + taken % C::ORDERS]);
             ++taken;
         }
         if (!ok) break;
-        // This warp's state for the merger: lane (g, t) has dims (D / 4) t
-        // and on of head g, D / 8 of them in the first accumulator of each
-        // pair and D / 8 in the second.
+        // This warp's state for the merger: (m, l) and O of heads 2t and
+        // 2t + 1, each lane its D / 8 dims.
         const int buf = item_seq % C::MERGE_BUFS;
         if (!mbar_wait_warp(&B.mempty[buf], ((item_seq / C::MERGE_BUFS) & 1) ^ 1)) {
             ok = false;
             break;
         }
-        l += __shfl_xor_sync(FULL, l, 1);
-        l += __shfl_xor_sync(FULL, l, 2);
-        if (g < G) {
-            const size_t base = static_cast<size_t>((buf * C::W + warp) * G + g);
-            if (t == 0) ml[base] = make_float2(m, l);
-            float* dst = mo + base * D + t * (D / 4);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+        for (int off = 4; off < 32; off <<= 1) {
+            l0 += __shfl_xor_sync(FULL, l0, off);
+            l1 += __shfl_xor_sync(FULL, l1, off);
+        }
 #pragma unroll
-                for (int j = 0; j < D / 8; j += 4)
-                    *reinterpret_cast<float4*>(dst + e * (D / 8) + j) =
-                        make_float4(o[j][e] + o[j][2 + e], o[j + 1][e] + o[j + 1][2 + e],
-                                    o[j + 2][e] + o[j + 2][2 + e], o[j + 3][e] + o[j + 3][2 + e]);
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * t + e;
+            if (h < G) {
+                const size_t base = static_cast<size_t>((buf * C::W + warp) * G + h);
+                if (g == 0) ml[base] = make_float2(e ? m1 : m0, e ? l1 : l0);
+                float* dst = mo + base * D + g * (D / 8);
+#pragma unroll
+                for (int j = 0; j < D / 16; j += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * j) =
+                        make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
             }
         }
         __syncwarp();
@@ -340,6 +446,8 @@ __device__ void run_consumer_scaled(const DecodeParams& P, uint8_t* smem, const 
     if (!ok) {
         *abort_flag = 1;
         record_error(P.err, kErrTimeout, 2u);
+        // Never leave with copies still in flight.
+        for (; taken != issued; ++taken) mbar_wait(&full[taken % C::SW], (taken / C::SW) & 1);
     }
 }
 
@@ -353,30 +461,25 @@ __global__ void __launch_bounds__(ScaledCfg<D, G, KIND>::THREADS, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     Bars B;
     B.full = bars;
-    B.empty = bars + C::STAGES;
-    B.ifull = bars + 2 * C::STAGES;
+    B.empty = nullptr;  // a consumer warp fills its own stages
+    B.ifull = bars + C::STAGES;
     B.iempty = B.ifull + kItemRing;
     B.mfull = B.iempty + kItemRing;
     B.mempty = B.mfull + C::MERGE_BUFS;
+    B.ofull = B.mempty + C::MERGE_BUFS;
+    B.oempty = B.ofull + C::W * C::ORDERS;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&B.full[i], 2);  // the tiles' bytes, the scales
-            mbar_init(&B.empty[i], 1);
-        }
-        for (int i = 0; i < kItemRing; ++i) {
-            mbar_init(&B.ifull[i], 1);
-            mbar_init(&B.iempty[i], C::W + 1);
-        }
-        for (int i = 0; i < C::MERGE_BUFS; ++i) {
-            mbar_init(&B.mfull[i], C::W);
-            mbar_init(&B.mempty[i], 1);
-        }
-        *abort_flag = 0;
-        fence_mbar_init();
+    // One arrival completes every barrier but two kinds: consumers and merger
+    // hand a descriptor back, the consumers hand a merge buffer over.
+    for (int i = threadIdx.x; i < C::NBAR; i += C::THREADS) {
+        const bool iempty = &bars[i] >= B.iempty && &bars[i] < B.iempty + kItemRing;
+        const bool mfull = &bars[i] >= B.mfull && &bars[i] < B.mfull + C::MERGE_BUFS;
+        mbar_init(&bars[i], iempty ? C::W + 1 : mfull ? C::W : 1);
     }
+    if (threadIdx.x == 0) *abort_flag = 0;
+    fence_mbar_init();
     griddep_launch_dependents();
     __syncthreads();
     // Until griddep_wait() returns, only L2 prefetches touch global memory.
@@ -389,13 +492,15 @@ __global__ void __launch_bounds__(ScaledCfg<D, G, KIND>::THREADS, 1)
         run_merger<C>(P, smem, B, abort_flag, lane);
     } else {
         prefetch_inputs<D, false>(P, threadIdx.x, C::W * 32);
-        run_consumer_scaled<C, KIND>(P, smem, B, abort_flag, warp, lane);
+        griddep_wait();  // consumers read the pools themselves
+        run_consumer_scaled<C, KIND>(P, &tm_k, &tm_v, smem, B, abort_flag, warp, lane);
     }
 }
 
 template <int D, int G, int KIND>
-cudaError_t launch_scaled_one(const DecodeParams& P, int grid, cudaStream_t stream) {
+cudaError_t launch_scaled_one(DecodeParams P, int grid, cudaStream_t stream) {
     using C = ScaledCfg<D, G, KIND>;
+    if (P.range_units <= 0) P.extra_units = C::EXTRA_UNITS;
     // Rows of D bytes, 16 a slab, one slab per (block, kv head).
     CUtensorMap tk, tv;
     const cuuint64_t slabs = static_cast<cuuint64_t>(P.num_blocks) * P.hkv;
