@@ -435,20 +435,6 @@ PKV_API size_t pkv_decode_workspace_size(int32_t num_seqs, int32_t num_q_heads, 
 
 namespace {
 
-// What attention over a pool with a scale per block takes from the pool.
-pkv::ScaledArgs scaled_args(const pkv_cache_t* cache, const DeviceState* dev) {
-    pkv::ScaledArgs a = {};
-    a.k_pool = cache->k_pool;
-    a.v_pool = cache->v_pool;
-    a.block_scales = cache->block_scales;
-    a.num_blocks = cache->num_blocks;
-    a.num_kv_heads = cache->num_kv_heads;
-    a.head_dim = cache->head_dim;
-    a.kv_dtype = cache->kv_dtype;
-    a.err = dev->err;
-    return a;
-}
-
 pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_heads,
                          const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
                          const int32_t* query_start_loc, int32_t num_seqs, int32_t max_context_len, float scale,
@@ -630,6 +616,8 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
         block_tables == nullptr || out == nullptr)
         return PKV_ERR_NULL;
     if (!aligned16(q) || !aligned16(out)) return PKV_ERR_ALIGN;
+    if (scaled(cache) && static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > INT32_MAX)
+        return PKV_ERR_SHAPE;  // slabs are counted in 32 bits
     if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] != num_tokens) return PKV_ERR_SHAPE;
     int32_t tiles = 0, decode_rows = 0;
     for (int32_t s = 0; s < num_seqs; ++s) {
@@ -643,22 +631,6 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
     const void* out_dev = nullptr;
     if ((st = device_address(out, &out_dev)) != PKV_OK) return st;
     out = static_cast<float*>(const_cast<void*>(out_dev));
-    if (scaled(cache)) {
-        pkv::ScaledArgs b = scaled_args(cache, dev);
-        b.q = q;
-        b.block_tables = block_tables;
-        b.context_lens = context_lens;
-        b.query_start_loc = query_start_loc;
-        b.out = out;
-        b.num_q_heads = num_q_heads;
-        b.num_seqs = num_seqs;
-        b.num_tokens = num_tokens;
-        b.max_blocks_per_seq = max_blocks_per_seq;
-        b.max_context_len = max_context_len;
-        b.scale = scale;
-        cudaError_t e = pkv::launch_scaled_attention(b, static_cast<cudaStream_t>(stream));
-        return e == cudaSuccess ? PKV_OK : cuda_fail(e);
-    }
     if (decode_rows > 0) {
         st = decode_common(cache, q, num_q_heads, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
                            num_seqs, max_context_len, scale, out, workspace, workspace_bytes, 0, stream);
@@ -702,7 +674,10 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
             a.split_tiles = static_cast<int32_t>(extra);
         }
         a.scale = scale;
-        cudaError_t e = pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
+        a.block_scales = scaled(cache) ? cache->block_scales : nullptr;
+        a.int8_codes = cache->kv_dtype == PKV_KV_INT8_BLOCKS;
+        cudaError_t e = scaled(cache) ? pkv::launch_prefill_scaled(a, static_cast<cudaStream_t>(stream))
+                                      : pkv::launch_prefill(a, static_cast<cudaStream_t>(stream));
         if (e == cudaErrorNotSupported) return PKV_ERR_UNSUPPORTED;
         if (e != cudaSuccess) return cuda_fail(e);
     }

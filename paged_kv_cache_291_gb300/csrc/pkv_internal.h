@@ -134,24 +134,6 @@ struct CacheRowsArgs {
 cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream);
 
-// Attention over an 8-bit pool with a scale per (block, kv head).
-struct ScaledArgs {
-    const void* k_pool;
-    const void* v_pool;
-    const float* block_scales;
-    const void* q;                    // bf16 [num_tokens][Hq][d]
-    const int32_t* block_tables;
-    const int32_t* context_lens;
-    const int32_t* query_start_loc;   // device [S+1], or null: row s is sequence s
-    float* out;
-    unsigned long long* err;
-    int32_t num_blocks, num_kv_heads, num_q_heads, head_dim, kv_dtype;
-    int32_t num_seqs, num_tokens, max_blocks_per_seq, max_context_len;
-    float scale;
-};
-
-cudaError_t launch_scaled_attention(const ScaledArgs& a, cudaStream_t stream);
-
 // Copy `chunks` 16-byte chunks from src to dst (device addresses) with a
 // kernel.
 cudaError_t launch_copy16(void* dst, const void* src, int64_t chunks, int num_sms, cudaStream_t stream);
@@ -177,9 +159,12 @@ struct PrefillArgs {
     int32_t split_last;               // last row tiles of each sequence split by head (two-head CTAs only)
     int32_t split_tiles;              // tiles so split over all sequences (extra CTAs per head pair)
     float scale;
+    const float* block_scales = nullptr;  // 8-bit pools with a scale per (block, kv head), else null
+    bool int8_codes = false;              // those: int8 codes (else e4m3)
 };
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream);
 
 // Rotary positions (rotary.cu): q and k rows turned, or q turned and k, v
 // stored in the pools (k_pool set).

@@ -51,13 +51,14 @@
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "prefill_tile.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kTileM = 128;                          // query rows per unit
+constexpr int kTileM = kPrefillRows;                 // query rows per unit
 constexpr int kTileN = 128;                          // keys per key tile
 constexpr int kMaxHeadDim = 128;                     // head_dim 64 uses the first panel of each tile
 constexpr int kUnits = 2;                            // q heads per CTA (max)
@@ -127,7 +128,7 @@ enum {
 };
 
 // Tile info slots (written by warp 0 before the CTA-wide sync).
-enum { I_S = 0, I_ROW0, I_ROWS, I_PMIN, I_PMAX, I_NT, I_KLAST, I_BAD, I_CTX, I_VMAX, I_UNITS, I_H0 };
+enum { I_S = 0, I_ROW0, I_ROWS, I_PMIN, I_PMAX, I_NT, I_KLAST, I_BAD, I_VMAX, I_UNITS, I_H0 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -247,78 +248,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     if (warp == 0) {
         griddep_wait();
-        // Find the sequence and row tile of this CTA: entries are numbered
-        // over the prefill sequences (query_len > 1) in order, one per row
-        // tile of 128 rows (ceil(qlen/128) tiles), and two for each of the
-        // last split_last tiles (one per q head).
-        const int tile = blockIdx.x;
-        const int split = P.units == 2 ? P.split_last : 0;
-        int base = 0, found = -1, e = 0, nt_s = 0;
-        for (int s0 = 0; s0 < P.num_seqs && found < 0; s0 += 32) {
-            const int s = s0 + lane;
-            int nt = 0;
-            if (s < P.num_seqs) {
-                const int ql = __ldg(P.qsl + s + 1) - __ldg(P.qsl + s);
-                nt = ql > 1 ? (ql + kTileM - 1) / kTileM : 0;
-            }
-            const int ne = nt + min(split, nt);
-            int incl = ne;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(FULL, incl, o);
-                if (lane >= o) incl += t;
-            }
-            const unsigned hit = __ballot_sync(FULL, base + incl > tile);
-            if (hit) {
-                const int j = __ffs(hit) - 1;
-                found = s0 + j;
-                e = tile - (base + __shfl_sync(FULL, incl - ne, j));
-                nt_s = __shfl_sync(FULL, nt, j);
-            } else {
-                base += __shfl_sync(FULL, incl, 31);
-            }
-        }
-        // Entry e of the sequence: row tile e while e < nt - sl (both
-        // heads), then tile nt - sl + (e - (nt - sl)) / 2, one head each.
-        const int sl = min(split, nt_s);
-        int tloc = e, cta_units = P.units, cta_h0 = blockIdx.y * P.units;
-        if (sl > 0 && e >= nt_s - sl) {
-            const int k = e - (nt_s - sl);
-            tloc = nt_s - sl + k / 2;
-            cta_units = 1;
-            cta_h0 += k % 2;
-        }
+        const PrefillTile tile = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.ctx_cap, P.units, P.split_last,
+                                                   blockIdx.x, blockIdx.y, P.err, lane);
         if (lane == 0) {
-            info[I_UNITS] = cta_units;
-            info[I_H0] = cta_h0;
-            int bad = 0, s = found, row0 = 0, rows = 0, pmin = 0, pmax = 0, nt = 0, klast = 0, ctx = 0;
-            if (s < 0) {
-                bad = 1;
-            } else {
-                const int q0 = __ldg(P.qsl + s);
-                const int ql = __ldg(P.qsl + s + 1) - q0;
-                ctx = __ldg(P.context_lens + s);
-                if (ctx > P.ctx_cap || ql > ctx) {
-                    record_error(P.err, kErrRange, static_cast<uint32_t>(s));
-                    bad = 1;
-                }
-                row0 = q0 + tloc * kTileM;
-                rows = min(kTileM, ql - tloc * kTileM);
-                pmin = ctx - ql + tloc * kTileM;
-                pmax = pmin + rows - 1;
-                nt = pmax / kTileN + 1;
-                klast = pmax + 1 - (nt - 1) * kTileN;
-                if (bad) nt = 0;
-            }
-            info[I_S] = s;
-            info[I_ROW0] = row0;
-            info[I_ROWS] = (s < 0) ? 0 : rows;
-            info[I_PMIN] = pmin;
-            info[I_PMAX] = pmax;
-            info[I_NT] = nt;
-            info[I_KLAST] = klast;
-            info[I_BAD] = bad;
-            info[I_CTX] = ctx;
+            info[I_UNITS] = tile.units;
+            info[I_H0] = tile.h0;
+            info[I_S] = tile.s;
+            info[I_ROW0] = tile.row0;
+            info[I_ROWS] = tile.rows;
+            info[I_PMIN] = tile.pmin;
+            info[I_PMAX] = tile.pmax;
+            info[I_NT] = tile.nt;
+            info[I_KLAST] = tile.klast;
+            info[I_BAD] = tile.bad;
             info[I_VMAX] = 0;  // largest |v| the converters see (fp32 bits; non-negative floats order as ints)
         }
     }

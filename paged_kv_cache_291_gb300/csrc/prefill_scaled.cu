@@ -1,0 +1,761 @@
+// prefill_scaled.cu -- causal chunked-prefill attention over 8-bit pools with
+// a scale for each (block, kv head), on tcgen05 tensor cores.
+//
+// With K_j = ks_b c_j and V_j = vs_b d_j (codes c, d; b the block of key j),
+//     s_j = (scale log2 e ks_b) (q . c_j),  out = sum_j 2^(s_j) vs_b d_j / sum_j 2^(s_j).
+// Codes are exact in fp16, so both products take fp16 operands: K and V tiles
+// are widened once per CTA, for two q heads of 128 rows each, and the scales
+// only touch scores and weights.
+//
+//  * A CTA owns 128 query rows of the two q heads of a GQA group ("units"; one
+//    unit when Hq/Hkv is odd, or for the split tiles of find_prefill_tile).
+//    Warp 16 loads Q and the key tiles' codes (128 keys = 8 paged blocks, each
+//    one TMA box), warp 17 issues tcgen05.mma, warps 0-7 and 8-15 run the
+//    softmax of units 0 and 1, two per quarter of tensor memory's lanes, 16
+//    rows each.
+//  * Warps 0-15 widen a sixteenth of each K and V tile, from unswizzled codes to
+//    the 128-byte swizzled panels the MMAs read, in the time they would wait
+//    for scores; the codes' buffers are refilled a tile ahead.  Rows past the
+//    last visible key become zero (0 times a NaN code would be NaN).
+//  * q goes to fp16 once, each row scaled by a power of two so that its largest
+//    value is in [2^14, 2^15); the scores take the factor back.
+//  * The running maximum is that of y_j = s_j + log2 vs_b; P = 2^(y_j - m + 12) is
+//    the weight with its V scale, in two fp16 terms (the rounded value and what
+//    the rounding lost: 2^-22, where one term would be 2^-11), which take exactly
+//    the columns of the scores they replace; the row sum adds P / vs_b block by
+//    block.  m moves, and O is rescaled, when the maximum grows by more than 2^3:
+//    P stays below 2^15, and weights end 2^-36 below the largest.
+//  * A tile with a NaN code among its visible V (the append stores one for a
+//    NaN) is left out of the tensor cores' sums of earlier rows only by
+//    recomputing: such a CTA's rows are redone on CUDA cores.
+//  * Every wait is bounded; tensor memory is freed on every exit path.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "prefill_tile.cuh"
+#include "scaled_device.cuh"
+#include "tcgen05_rows.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kTileM = kPrefillRows;
+constexpr int kTileN = 128;                          // keys per key tile
+constexpr int kUnits = 2;                            // q heads per CTA (max)
+constexpr int kBlocksPerTile = kTileN / kBlockSize;  // 8
+constexpr int kPanelBytes = 128 * 128;               // 128 rows x 64 fp16, swizzled
+constexpr int kTileBytes = 2 * kPanelBytes;
+constexpr int kCodeBytes = kTileN * 128;             // a tile's codes at head_dim 128
+
+constexpr int OFF_Q = 0;                             // kUnits Q tiles
+constexpr int OFF_K = OFF_Q + kUnits * kTileBytes;   // 2 widened K tiles
+constexpr int OFF_V = OFF_K + 2 * kTileBytes;        // 2 widened V tiles
+constexpr int OFF_KC = OFF_V + 2 * kTileBytes;       // codes of one K tile
+constexpr int OFF_VC = OFF_KC + kCodeBytes;          // codes of one V tile
+constexpr int OFF_SCALES = OFF_VC + kCodeBytes;      // [4 tiles][8 blocks] (K scale, log2 of V's, 1 / V's, 0)
+constexpr int OFF_ROWF = OFF_SCALES + 4 * kBlocksPerTile * 16;  // [kUnits][128] factor of a row's scores
+constexpr int OFF_BAR = OFF_ROWF + kUnits * kTileM * 4;
+constexpr int NBAR = 20;
+constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
+constexpr int OFF_TMEM = OFF_INFO + 12 * 4;
+constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;     // slack to align the base to 1024 B
+static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB)");
+static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
+
+constexpr int kSoftmaxWarps = 8;                     // per unit
+constexpr int kLoadWarp = 16, kMmaWarp = 17;
+constexpr int kThreads = 32 * 18;
+constexpr int kWidenWarps = kSoftmaxWarps * kUnits;  // all of them, whatever the units
+
+constexpr uint32_t kTmemCols = 512;
+// Unit u: S and then P (hi, lo) at columns [256u, 256u + 128), O at + 128.
+__host__ __device__ constexpr uint32_t col_s(int u) { return static_cast<uint32_t>(u) * 256u; }
+__host__ __device__ constexpr uint32_t col_o(int u) { return static_cast<uint32_t>(u) * 256u + 128u; }
+
+// Key tiles that O stays in tensor memory for.  The tensor cores' sums lose half
+// a unit in the last place on average at each of a tile's 16 steps, always to
+// the same side: 2.5e-6 of the output's norm after 12 tiles, 3.5e-5 after 128.
+// Every kKeep tiles O is added, with rounding, to what was moved out before.
+constexpr int kKeep = 4;
+constexpr float kThreshold = 3.0f, kShift = 12.0f;   // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+    const uint8_t* q;       // bf16 [num_tokens][hq][D] (for the redo)
+    const uint8_t* k_pool;
+    const uint8_t* v_pool;
+    const float2* scales;   // [num_blocks][hkv]
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* qsl;
+    float* out;
+    unsigned long long* err;
+    int32_t num_blocks, hkv, hq, num_seqs, max_blocks, ctx_cap, units, split_last;
+    float scale_log2;
+};
+
+enum {
+    B_QFULL = 0,
+    B_QCONV = 1,   // Q in fp16 (8 warps per unit)
+    B_KCFULL = 2,  // codes of a K tile and the tile's scales
+    B_KCEMPTY = 3, // widened (16 warps)
+    B_VCFULL = 4,
+    B_VCEMPTY = 5,
+    B_KCONV = 6,   // + stage: K tile widened (16 warps)
+    B_KEMPTY = 8,  // + stage: read by the MMAs
+    B_VCONV = 10,  // + stage
+    B_VEMPTY = 12, // + stage
+    B_SFULL = 14,  // + unit
+    B_PFULL = 16,  // + unit (8 warps)
+    B_ODONE = 18,  // + unit
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// A pair of weights (below 2^15) as two fp16 pairs: the first 11 bits, and the
+// rest rounded, 2^-22 of the weight (2^-25 below 2^-14).
+__device__ __forceinline__ void split2(float2 p, uint32_t& hi, uint32_t& lo) {
+    const float2 h = make_float2(__uint_as_float(__float_as_uint(p.x) & 0xffffe000u),
+                                 __uint_as_float(__float_as_uint(p.y) & 0xffffe000u));
+    hi = tc::pack_f16x2(h.x, h.y);
+    const float2 r = __ffma2_rn(h, make_float2(-1.f, -1.f), p);
+    lo = tc::pack_f16x2(r.x, r.y);
+}
+
+// Four codes to two fp16 pairs, exactly.  int8: code + 128 as the low byte of
+// 0x6400 is 1024 + 128 + code, less 1152.
+template <int KIND>
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
+    if constexpr (KIND == kKindInt8Blocks) {
+        w ^= 0x80808080u;
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(a) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+        asm("sub.f16x2 %0, %1, %2;" : "=r"(b) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+    } else {
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(a), "=r"(b)
+            : "r"(w));
+    }
+}
+
+// A warp's eighth rows of a tile, codes [128][D] to fp16 panels; rows >= nrows
+// become zero.  Lane l takes 16 codes of row 8 warp + 2 (l / 8) + (l / 4) % 2:
+// at head_dim 128 neighbouring rows take different halves of their chunks, so
+// that neither the eight lanes that load nor those that store together meet in
+// a bank.  Returns non-zero top bits where a visible code is NaN.
+template <int D, int KIND>
+__device__ __forceinline__ uint32_t widen_rows(uint32_t codes, uint32_t tile, int warp, int lane, int nrows) {
+    constexpr int PASSES = D / 64;
+    const int rr = (lane >> 2) & 1, row = 8 * warp + 2 * (lane >> 3) + rr;
+    uint32_t x[PASSES][4];
+#pragma unroll
+    for (int s = 0; s < PASSES; ++s) {
+        const int c = PASSES == 2 ? (lane & 3) + 4 * (rr ^ s) : lane & 3;
+        tc::lds128(codes + row * D + c * 16, x[s]);
+    }
+    uint32_t nan = 0;
+#pragma unroll
+    for (int s = 0; s < PASSES; ++s) {
+        const int c = PASSES == 2 ? (lane & 3) + 4 * (rr ^ s) : lane & 3;
+        if (row >= nrows) x[s][0] = x[s][1] = x[s][2] = x[s][3] = 0u;
+        if constexpr (KIND != kKindInt8Blocks) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) nan |= (x[s][i] & 0x7f7f7f7fu) + 0x01010101u;
+        }
+        const uint32_t at = tile + (c >> 2) * kPanelBytes + row * 128;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t h[4];
+            widen4<KIND>(x[s][2 * i], h[0], h[1]);
+            widen4<KIND>(x[s][2 * i + 1], h[2], h[3]);
+            tc::sts128(at + (((2 * (c & 3) + i) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+        }
+    }
+    return nan & 0x80808080u;
+}
+
+// A CTA's rows on CUDA cores, for V with NaN codes: warp w takes the (row,
+// unit) items w, w + 18, ...; lane l owns D / 32 consecutive dims; keys in order
+// with a running maximum and sum.
+template <int D, int KIND>
+__device__ __noinline__ void redo_rows(const Params& P, const PrefillTile& T, int g, int warp, int lane) {
+    constexpr int DPL = D / 32;
+    const int32_t* trow = P.block_tables + static_cast<size_t>(T.s) * P.max_blocks;
+    for (int item = warp; item < T.rows * T.units; item += kThreads / 32) {
+        const int m = item / T.units, h = T.h0 + item % T.units;
+        const size_t at = (static_cast<size_t>(T.row0 + m) * P.hq + h) * D + lane * DPL;
+        float q[DPL], o[DPL];
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) {
+            q[i] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(P.q)[at + i]) << 16) *
+                   P.scale_log2;
+            o[i] = 0.f;
+        }
+        float mx = -INFINITY, l = 0.f;
+        for (int j = 0; j <= T.pmin + m; ++j) {
+            int phys = __ldg(trow + j / kBlockSize);
+            if (phys < 0 || phys >= P.num_blocks) phys = 0;  // reported by the tensor-core pass already
+            const size_t slab = static_cast<size_t>(phys) * P.hkv + g;
+            const float2 s = __ldg(P.scales + slab);
+            bool bad = false;
+            const float ks = checked_scale(s.x, bad), vs = checked_scale(s.y, bad);
+            const size_t src = (slab * kBlockSize + j % kBlockSize) * D + lane * DPL;
+            uint32_t wk = 0, wv = 0;
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) {
+                wk |= static_cast<uint32_t>(P.k_pool[src + i]) << (8 * i);
+                wv |= static_cast<uint32_t>(P.v_pool[src + i]) << (8 * i);
+            }
+            float k[4], v[4];
+            decode4<KIND>(wk, k);
+            decode4<KIND>(wv, v);
+            float part = 0.f;
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) part = fmaf(q[i], k[i], part);
+            const float x = warp_sum(part) * ks;
+            const float mn = fmaxf(mx, x);
+            const float alpha = mx == mn ? 1.f : fast_exp2(mx - mn), p = fast_exp2(x - mn);
+            mx = mn;
+            l = fmaf(l, alpha, p);
+#pragma unroll
+            for (int i = 0; i < DPL; ++i) o[i] = fmaf(p, v[i] * vs, o[i] * alpha);
+        }
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) P.out[at + i] = o[i] / l;
+    }
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_scaled_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const Params P) {
+    constexpr int kPanels = D / 64;  // 64-dim swizzled panels of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    PrefillTile* info = reinterpret_cast<PrefillTile*>(smem + OFF_INFO);
+    int* redo = reinterpret_cast<int*>(smem + OFF_INFO + sizeof(PrefillTile));
+    static_assert(sizeof(PrefillTile) + 4 <= 12 * 4, "info");
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+    float* rowf = reinterpret_cast<float*>(smem + OFF_ROWF);
+    float4* scales = reinterpret_cast<float4*>(smem + OFF_SCALES);
+    const int warp = threadIdx.x / 32;
+    const int lane = threadIdx.x % 32;
+    const unsigned FULL = 0xffffffffu;
+
+    griddep_launch_dependents();
+    if (warp == 0) {
+        griddep_wait();
+        const PrefillTile t = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.ctx_cap, P.units, P.split_last,
+                                                blockIdx.x, blockIdx.y, P.err, lane);
+        if (lane == 0) {
+            *info = t;
+            *redo = 0;
+        }
+    }
+    if (threadIdx.x == 32 * kMmaWarp) {
+        for (int i = 0; i < NBAR; ++i) {
+            const bool widened = i == B_KCEMPTY || i == B_VCEMPTY || (i >= B_KCONV && i < B_KEMPTY) ||
+                                 (i >= B_VCONV && i < B_VEMPTY) || i == B_QCONV;
+            const bool rows = i >= B_PFULL && i < B_ODONE;
+            mbar_init(&bar[i], widened ? kWidenWarps : rows ? kSoftmaxWarps : 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kLoadWarp) {
+        tc::tmem_alloc(tmem_slot, kTmemCols);
+        tc::tmem_relinquish();
+        if (lane == 0) {
+            tc::prefetch_tensormap(&tm_q);
+            tc::prefetch_tensormap(&tm_k);
+            tc::prefetch_tensormap(&tm_v);
+        }
+    }
+    griddep_wait();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const PrefillTile T = *info;
+    const int nt = T.nt, units = T.units;
+    const int g = T.h0 / (P.hq / P.hkv);                           // the kv head both units read
+    const int nblk = (T.pmax + 1 + kBlockSize - 1) / kBlockSize;   // blocks holding keys 0..pmax
+    bool ok = true;
+
+    if (warp == kLoadWarp && nt > 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&bar[B_QFULL], static_cast<uint32_t>(units) * kPanels * kPanelBytes);
+            for (int u = 0; u < units; ++u) {
+#pragma unroll
+                for (int pn = 0; pn < kPanels; ++pn)
+                    tc::tma_load_3d(smem + OFF_Q + u * kTileBytes + pn * kPanelBytes, &tm_q, 64 * pn, T.h0 + u, T.row0,
+                                    &bar[B_QFULL]);
+            }
+        }
+        const int32_t* trow = P.block_tables + static_cast<size_t>(T.s) * P.max_blocks;
+        // A tile's table entries and scales are looked up while the tile
+        // before it is on its way.
+        int slab = 0;
+        float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+        auto look_up = [&](int j) {
+            sc = make_float4(1.f, 0.f, 1.f, 0.f);
+            if (lane < min(kBlocksPerTile, nblk - j * kBlocksPerTile)) {
+                int e = __ldg(trow + j * kBlocksPerTile + lane);
+                bool bad = e < 0 || e >= P.num_blocks;
+                if (bad) e = 0;  // never dereference an invalid id
+                slab = e * P.hkv + g;
+                const float2 s = __ldg(P.scales + slab);
+                sc.x = checked_scale(s.x, bad);
+                const float vs = checked_scale(s.y, bad);
+                sc.y = log2f(vs);
+                sc.z = 1.f / vs;
+                if (bad) record_error(P.err, kErrRange, static_cast<uint32_t>(T.s));
+            }
+        };
+        look_up(0);
+        for (int j = 0; j < nt && ok; ++j) {
+            const int nvb = min(kBlocksPerTile, nblk - j * kBlocksPerTile);
+            const uint32_t bytes = static_cast<uint32_t>(nvb) * kBlockSize * D;
+            const int now = slab;
+            if (!mbar_wait_warp(&bar[B_KCEMPTY], (j & 1) ^ 1)) { ok = false; break; }
+            // The tile four before this one has been through its softmax:
+            // every warp widened the last K tile after that.
+            if (lane < kBlocksPerTile) scales[(j & 3) * kBlocksPerTile + lane] = sc;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&bar[B_KCFULL], bytes);
+            __syncwarp();
+            if (lane < nvb)
+                tc::tma_load_3d(smem + OFF_KC + lane * kBlockSize * D, &tm_k, 0, 0, now, &bar[B_KCFULL]);
+            if (j + 1 < nt) look_up(j + 1);
+            if (!mbar_wait_warp(&bar[B_VCEMPTY], (j & 1) ^ 1)) { ok = false; break; }
+            if (lane == 0) mbar_arrive_expect_tx(&bar[B_VCFULL], bytes);
+            __syncwarp();
+            if (lane < nvb)
+                tc::tma_load_3d(smem + OFF_VC + lane * kBlockSize * D, &tm_v, 0, 0, now, &bar[B_VCFULL]);
+            __syncwarp();
+        }
+    } else if (warp == kMmaWarp && nt > 0) {
+        // ------------------------------------------------------ MMA issuer
+        constexpr uint32_t kIdescQK = tc::idesc_f16_f32(kTileM, kTileN, 0, 0);
+        constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kTileM, D, 0, 1);
+        auto qk = [&](int u, int j) {
+            const uint32_t sq = smem_addr(smem + OFF_Q + u * kTileBytes);
+            const uint32_t sk = smem_addr(smem + OFF_K + (j & 1) * kTileBytes);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (k >> 2) * kPanelBytes + (k & 3) * 32;
+                tc::mma_bf16_ss(tmem + col_s(u), tc::smem_desc_sw128(sq + off, 16, 1024),
+                                tc::smem_desc_sw128(sk + off, 16, 1024), kIdescQK, k > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(&bar[B_SFULL + u]);
+        };
+        // O_u += P_u V: key step k covers keys 16k .. 16k + 15, P's rounded
+        // values in columns [8k, 8k + 8) of the unit's S, the rest 64 on.
+        auto pv = [&](int u, int j) {
+            const uint32_t svb = smem_addr(smem + OFF_V + (j & 1) * kTileBytes);
+#pragma unroll
+            for (int k = 0; k < kTileN / 16; ++k) {
+                const uint64_t vdesc = tc::smem_desc_sw128(svb + k * 2048, kPanelBytes, 1024);
+                tc::mma_bf16_ts(tmem + col_o(u), tmem + col_s(u) + 64 + 8 * k, vdesc, kIdescPV,
+                                (j % kKeep > 0 || k > 0) ? 1u : 0u);
+                tc::mma_bf16_ts(tmem + col_o(u), tmem + col_s(u) + 8 * k, vdesc, kIdescPV, 1u);
+            }
+            tc::mma_commit(&bar[B_ODONE + u]);
+        };
+        ok = mbar_wait_warp(&bar[B_QCONV], 0) && mbar_wait_warp(&bar[B_KCONV], 0);
+        if (ok) {
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+                for (int u = 0; u < units; ++u) qk(u, 0);
+                tc::mma_commit(&bar[B_KEMPTY]);
+            }
+            __syncwarp();
+        }
+        // Per tile, unit by unit: P_u V, then (once P_u has been read) the
+        // next tile's S_u, so that one unit's softmax runs beside the other's
+        // MMAs.
+        for (int j = 0; j < nt && ok; ++j) {
+            if (!mbar_wait_warp(&bar[B_VCONV + (j & 1)], (j >> 1) & 1)) { ok = false; break; }
+            const bool next = j + 1 < nt;
+            if (next && !mbar_wait_warp(&bar[B_KCONV + ((j + 1) & 1)], ((j + 1) >> 1) & 1)) { ok = false; break; }
+            for (int u = 0; u < units && ok; ++u) {
+                if (!mbar_wait_warp(&bar[B_PFULL + u], j & 1)) { ok = false; break; }
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    pv(u, j);
+                    if (u == units - 1) tc::mma_commit(&bar[B_VEMPTY + (j & 1)]);
+                }
+                __syncwarp();
+                if (next) {
+                    if (!mbar_wait_warp(&bar[B_ODONE + u], j & 1)) { ok = false; break; }
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) qk(u, j + 1);
+                    __syncwarp();
+                }
+            }
+            if (!ok) break;
+            if (next && tc::elect_one()) tc::mma_commit(&bar[B_KEMPTY + ((j + 1) & 1)]);
+            __syncwarp();
+        }
+    } else if (warp < kWidenWarps && nt > 0) {
+        uint32_t nan = 0;
+        // K and V tile j of the sequence to fp16, this warp's rows.
+        auto widen_k = [&](int j) -> bool {
+            if (!mbar_wait_warp(&bar[B_KCFULL], j & 1) ||
+                !mbar_wait_warp(&bar[B_KEMPTY + (j & 1)], ((j >> 1) & 1) ^ 1))
+                return false;
+            widen_rows<D, KIND>(smem_addr(smem + OFF_KC), smem_addr(smem + OFF_K + (j & 1) * kTileBytes), warp, lane,
+                                kTileN);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar[B_KCONV + (j & 1)]);
+                mbar_arrive(&bar[B_KCEMPTY]);
+            }
+            return true;
+        };
+        auto widen_v = [&](int j) -> bool {
+            if (!mbar_wait_warp(&bar[B_VCFULL], j & 1) ||
+                !mbar_wait_warp(&bar[B_VEMPTY + (j & 1)], ((j >> 1) & 1) ^ 1))
+                return false;
+            nan |= widen_rows<D, KIND>(smem_addr(smem + OFF_VC), smem_addr(smem + OFF_V + (j & 1) * kTileBytes), warp,
+                                       lane, j == nt - 1 ? T.klast : kTileN);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bar[B_VCONV + (j & 1)]);
+                mbar_arrive(&bar[B_VCEMPTY]);
+            }
+            return true;
+        };
+        // ------------------------------------------------------ Q to fp16
+        // Two lanes a row, 64 dims (one panel's 128 bytes) each; the chunks
+        // are taken from a place that differs by row, for the banks.
+        const int u = warp / kSoftmaxWarps;
+        if (u < units) {
+            ok = mbar_wait_warp(&bar[B_QFULL], 0);
+            if (ok) {
+                const int row = 16 * (warp % kSoftmaxWarps) + lane / 2, pn = lane & 1;
+                const uint32_t at = smem_addr(smem + OFF_Q + u * kTileBytes) + pn * kPanelBytes + row * 128;
+                const bool mine = pn < kPanels;
+                float mx = 0.f;
+                if (mine) {
+#pragma unroll 2
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t x[4];
+                        tc::lds128(at + (((c + row) & 7) << 4), x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(x[i])), fabsf(bf16hi(x[i]))));
+                    }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+                int e = 0;
+                if (mx < INFINITY) e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
+                const float down = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+                if (mine) {
+#pragma unroll 2
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t x[4];
+                        const uint32_t a = at + (((c + row) & 7) << 4);
+                        tc::lds128(a, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = tc::pack_f16x2(bf16lo(x[i]) * down, bf16hi(x[i]) * down);
+                        tc::sts128(a, x[0], x[1], x[2], x[3]);
+                    }
+                }
+                if (pn == 0)
+                    rowf[u * kTileM + row] =
+                        P.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+                tc::fence_proxy_async_smem();
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && ok) mbar_arrive(&bar[B_QCONV]);
+        ok = ok && widen_k(0);
+        if (u >= units) {
+            for (int j = 0; j < nt && ok; ++j) ok = widen_v(j) && (j + 1 >= nt || widen_k(j + 1));
+        } else {
+            // -------------------------------------------------- softmax rows
+            // Warps w and w + 4 of a unit share quarter w % 4 of the lanes, 16
+            // rows each.  Thread t holds rows t/4 and t/4 + 8 of those and columns
+            // 8g + 2(t%4) and + 1 of every group g of 8, so a row's maximum and
+            // sum take two shuffles, and its P pairs land in the layout of the
+            // 16x128b store.  A block's 16 keys are two groups.
+            const int hh = (warp >> 2) & 1;
+            const int ma = 32 * (warp & 3) + 16 * hh + lane / 4;  // tile rows ma and ma + 8
+            const int mb = ma + 8;
+            const int tq = lane & 3;
+            const uint32_t tlane = static_cast<uint32_t>(32 * (warp & 3) + 16 * hh) << 16;
+            const int pos_a = (ma < T.rows) ? T.pmin + ma : T.pmax;
+            const int pos_b = (mb < T.rows) ? T.pmin + mb : T.pmax;
+            // Rows of this warp were scaled by its own lanes' neighbours: wait
+            // for all of the unit's.
+            ok = ok && mbar_wait_warp(&bar[B_QCONV], 0);
+            const float fa = rowf[u * kTileM + ma], fb = rowf[u * kTileM + mb];
+            // References of P, and of what was moved out of tensor memory.
+            float mua = 0.f, mub = 0.f, mfa = 0.f, mfb = 0.f, la = 0.f, lb = 0.f;
+            float* oa = P.out + (static_cast<size_t>(T.row0 + ma) * P.hq + T.h0 + u) * D + 2 * tq;
+            float* ob = P.out + (static_cast<size_t>(T.row0 + mb) * P.hq + T.h0 + u) * D + 2 * tq;
+            // O = what was moved out, times fac, plus what tensor memory has,
+            // times alpha; stored times inv.
+            auto move_out = [&](bool first, float fac_a, float fac_b, float alpha_a, float alpha_b, float inv_a,
+                                float inv_b) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t r[32];
+                    tc::tmem_ld16x256b_x8(tmem + tlane + col_o(u) + 64 * c, r);
+                    float2 xa[8], xb[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        xa[i] = xb[i] = make_float2(0.f, 0.f);
+                        if (!first && ma < T.rows) xa[i] = *reinterpret_cast<const float2*>(oa + 64 * c + 8 * i);
+                        if (!first && mb < T.rows) xb[i] = *reinterpret_cast<const float2*>(ob + 64 * c + 8 * i);
+                    }
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        xa[i].x = fmaf(__uint_as_float(r[4 * i]), alpha_a, xa[i].x * fac_a) * inv_a;
+                        xa[i].y = fmaf(__uint_as_float(r[4 * i + 1]), alpha_a, xa[i].y * fac_a) * inv_a;
+                        xb[i].x = fmaf(__uint_as_float(r[4 * i + 2]), alpha_b, xb[i].x * fac_b) * inv_b;
+                        xb[i].y = fmaf(__uint_as_float(r[4 * i + 3]), alpha_b, xb[i].y * fac_b) * inv_b;
+                        if (ma < T.rows) *reinterpret_cast<float2*>(oa + 64 * c + 8 * i) = xa[i];
+                        if (mb < T.rows) *reinterpret_cast<float2*>(ob + 64 * c + 8 * i) = xb[i];
+                    }
+                }
+            };
+            for (int j = 0; j < nt && ok; ++j) {
+                if (!widen_v(j) || (j + 1 < nt && !widen_k(j + 1)) || !mbar_wait_warp(&bar[B_SFULL + u], j & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                const int kbase = j * kTileN;
+                const bool full = kbase + kTileN - 1 <= __shfl_sync(FULL, pos_a, 0);
+                const float4* sct = scales + (j & 3) * kBlocksPerTile;
+                uint32_t sr[64];  // groups 0-7, then 8-15
+                tc::tmem_ld16x256b_x8(tmem + tlane + col_s(u), *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                tc::tmem_ld16x256b_x8(tmem + tlane + col_s(u) + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                tc::tmem_wait_ld();
+                // Pass 1: the exponents of P against the reference so far, in
+                // place of the scores, and each row's largest.
+                const float ra = kShift - mua, rb = kShift - mub;
+                float xa = -INFINITY, xb = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < kBlocksPerTile; ++b) {
+                    const float4 sc = sct[b];
+                    const float2 pa = make_float2(fa * sc.x, fa * sc.x), pb = make_float2(fb * sc.x, fb * sc.x);
+                    const float2 ca = make_float2(sc.y + ra, sc.y + ra), cb = make_float2(sc.y + rb, sc.y + rb);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t* s = &sr[4 * (2 * b + h)];
+                        float2 ya = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), pa, ca);
+                        float2 yb = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), pb, cb);
+                        if (!full) {  // keys past the row's position (NaN in unused slots included)
+                            const int key = kbase + 16 * b + 8 * h + 2 * tq;
+                            if (key > pos_a) ya.x = -INFINITY;
+                            if (key + 1 > pos_a) ya.y = -INFINITY;
+                            if (key > pos_b) yb.x = -INFINITY;
+                            if (key + 1 > pos_b) yb.y = -INFINITY;
+                        }
+                        xa = fmax3(xa, ya.x, ya.y);
+                        xb = fmax3(xb, yb.x, yb.y);
+                        s[0] = __float_as_uint(ya.x), s[1] = __float_as_uint(ya.y);
+                        s[2] = __float_as_uint(yb.x), s[3] = __float_as_uint(yb.y);
+                    }
+                }
+                xa = fmaxf(xa, __shfl_xor_sync(FULL, xa, 1));
+                xb = fmaxf(xb, __shfl_xor_sync(FULL, xb, 1));
+                xa = fmaxf(xa, __shfl_xor_sync(FULL, xa, 2));
+                xb = fmaxf(xb, __shfl_xor_sync(FULL, xb, 2));
+                // The reference moves in the first tile, and where the largest
+                // passed it by more than 2^3.
+                float alpha_a = 1.f, alpha_b = 1.f;
+                const bool need_a = j == 0 || xa > kShift + kThreshold, need_b = j == 0 || xb > kShift + kThreshold;
+                const bool moves = __any_sync(FULL, need_a || need_b);
+                if (moves) {
+                    const float da = need_a ? xa - kShift : 0.f, db = need_b ? xb - kShift : 0.f;
+                    mua += da;
+                    mub += db;
+                    alpha_a = fast_exp2(-da);
+                    alpha_b = fast_exp2(-db);
+                    if (j > 0) {
+                        la *= alpha_a;
+                        lb *= alpha_b;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            sr[4 * i + c] = __float_as_uint(__uint_as_float(sr[4 * i + c]) - da);
+                            sr[4 * i + 2 + c] = __float_as_uint(__uint_as_float(sr[4 * i + 2 + c]) - db);
+                        }
+                    }
+                }
+                // Pass 2: P in two fp16 terms over the scores, its first 11 bits
+                // and the rest; the row sums without the V scales.
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int b = 4 * hf; b < 4 * hf + 4; ++b) {
+                        float2 ta = make_float2(0.f, 0.f), tb = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t* s = &sr[4 * (2 * b + h)];
+                            const int at = 2 * (2 * (b - 4 * hf) + h);
+                            const float2 pa = make_float2(fast_exp2(__uint_as_float(s[0])), fast_exp2(__uint_as_float(s[1])));
+                            const float2 pb = make_float2(fast_exp2(__uint_as_float(s[2])), fast_exp2(__uint_as_float(s[3])));
+                            ta = __fadd2_rn(ta, pa);
+                            tb = __fadd2_rn(tb, pb);
+                            split2(pa, hi[at], lo[at]);
+                            split2(pb, hi[at + 1], lo[at + 1]);
+                        }
+                        const float inv = sct[b].z;
+                        la = fmaf(ta.x + ta.y, inv, la);
+                        lb = fmaf(tb.x + tb.y, inv, lb);
+                    }
+                    tc::tmem_st16x128b_x8(tmem + tlane + col_s(u) + 32 * hf, hi);
+                    tc::tmem_st16x128b_x8(tmem + tlane + col_s(u) + 64 + 32 * hf, lo);
+                }
+                if (j > 0 && j % kKeep == 0) {
+                    // The MMA warp starts O anew with this tile's P V.
+                    move_out(j == kKeep, fast_exp2(mfa - mua), fast_exp2(mfb - mub), alpha_a, alpha_b, 1.f, 1.f);
+                    mfa = mua;
+                    mfb = mub;
+                } else if (moves && j > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t r[32];
+                        const uint32_t at = tmem + tlane + col_o(u) + 64 * c;
+                        tc::tmem_ld16x256b_x8(at, r);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            r[4 * i] = __float_as_uint(__uint_as_float(r[4 * i]) * alpha_a);
+                            r[4 * i + 1] = __float_as_uint(__uint_as_float(r[4 * i + 1]) * alpha_a);
+                            r[4 * i + 2] = __float_as_uint(__uint_as_float(r[4 * i + 2]) * alpha_b);
+                            r[4 * i + 3] = __float_as_uint(__uint_as_float(r[4 * i + 3]) * alpha_b);
+                        }
+                        tc::tmem_st16x256b_x8(at, r);
+                    }
+                }
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[B_PFULL + u]);
+            }
+            if (ok && !mbar_wait_warp(&bar[B_ODONE + u], (nt - 1) & 1)) ok = false;
+            if (ok) {
+                tc::fence_after_sync();
+                la += __shfl_xor_sync(FULL, la, 1);
+                lb += __shfl_xor_sync(FULL, lb, 1);
+                la += __shfl_xor_sync(FULL, la, 2);
+                lb += __shfl_xor_sync(FULL, lb, 2);
+                move_out(nt <= kKeep, fast_exp2(mfa - mua), fast_exp2(mfb - mub), 1.f, 1.f, 1.f / la, 1.f / lb);
+            }
+        }
+        if (__any_sync(FULL, nan != 0) && lane == 0) atomicOr(redo, 1);
+    } else if (warp < kWidenWarps && T.bad && T.s >= 0) {
+        // Zero rows for a sequence whose arguments are out of range.
+        for (int i = threadIdx.x; i < T.rows * units * (D / 4); i += kWidenWarps * 32) {
+            const int c = i % (D / 4), h = i / (D / 4) % units, m = i / (D / 4) / units;
+            reinterpret_cast<float4*>(P.out + (static_cast<size_t>(T.row0 + m) * P.hq + T.h0 + h) * D)[c] =
+                make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    if (!ok) record_error(P.err, kErrTimeout, 0x100u + static_cast<uint32_t>(warp));
+    // ---------------------------------------------------------- teardown
+    tc::fence_before_sync();
+    const bool all_ok = __syncthreads_and(ok);
+    tc::fence_after_sync();
+    if (warp == kLoadWarp) tc::tmem_dealloc(tmem, kTmemCols);
+    if (KIND != kKindInt8Blocks && *redo && all_ok) redo_rows<D, KIND>(P, T, g, warp, lane);
+}
+
+template <int D, int KIND>
+cudaError_t launch(const Params& P, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
+                   cudaStream_t stream) {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !configured[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(prefill_scaled_kernel<D, KIND>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    return launch_overlapped(prefill_scaled_kernel<D, KIND>, grid, dim3(kThreads), SMEM_BYTES, stream, tq, tk, tv, P);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
+    if (a.num_tiles == 0) return cudaSuccess;
+    const cuuint64_t d = static_cast<cuuint64_t>(a.head_dim);
+    CUtensorMap tq, tk, tv;
+    {
+        const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(a.num_q_heads), static_cast<cuuint64_t>(a.num_tokens)};
+        const cuuint64_t strides[2] = {d * 2, static_cast<cuuint64_t>(a.num_q_heads) * d * 2};
+        const cuuint32_t box[3] = {64, 1, kTileM};
+        if (!make_bf16_map(&tq, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    {
+        // Rows of head_dim codes, 16 a slab, one slab per (block, kv head).
+        const cuuint64_t slabs = static_cast<cuuint64_t>(a.num_blocks) * a.num_kv_heads;
+        const cuuint64_t dims[3] = {d, kBlockSize, slabs > 0 ? slabs : 1};
+        const cuuint64_t strides[2] = {d, d * kBlockSize};
+        const cuuint32_t box[3] = {static_cast<cuuint32_t>(a.head_dim), kBlockSize, 1};
+        if (!make_tile_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k_pool, 3, dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_NONE) ||
+            !make_tile_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.v_pool, 3, dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_NONE))
+            return cudaErrorInvalidValue;
+    }
+    Params P;
+    P.q = static_cast<const uint8_t*>(a.q);
+    P.k_pool = static_cast<const uint8_t*>(a.k_pool);
+    P.v_pool = static_cast<const uint8_t*>(a.v_pool);
+    P.scales = reinterpret_cast<const float2*>(a.block_scales);
+    P.block_tables = a.block_tables;
+    P.context_lens = a.context_lens;
+    P.qsl = a.query_start_loc;
+    P.out = a.out;
+    P.err = a.err;
+    P.num_blocks = a.num_blocks;
+    P.hkv = a.num_kv_heads;
+    P.hq = a.num_q_heads;
+    P.num_seqs = a.num_seqs;
+    P.max_blocks = a.max_blocks_per_seq;
+    P.ctx_cap = static_cast<int32_t>(
+        std::min<int64_t>(a.max_context_len, static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize));
+    // Two q heads per CTA when a GQA group holds an even number of them.
+    P.units = ((a.num_q_heads / a.num_kv_heads) % 2 == 0) ? 2 : 1;
+    P.split_last = P.units == 2 ? a.split_last : 0;
+    P.scale_log2 = a.scale * kLog2e;
+    const dim3 grid(static_cast<unsigned>(a.num_tiles + (P.units == 2 ? a.split_tiles : 0)),
+                    static_cast<unsigned>(a.num_q_heads / P.units));
+    if (a.head_dim == 128)
+        return a.int8_codes ? launch<128, kKindInt8Blocks>(P, tq, tk, tv, grid, stream)
+                            : launch<128, kKindE4m3Blocks>(P, tq, tk, tv, grid, stream);
+    return a.int8_codes ? launch<64, kKindInt8Blocks>(P, tq, tk, tv, grid, stream)
+                        : launch<64, kKindE4m3Blocks>(P, tq, tk, tv, grid, stream);
+}
+
+}  // namespace pkv

@@ -1,0 +1,89 @@
+// prefill_tile.cuh -- which query rows a CTA of the prefill kernels takes.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+constexpr int kPrefillRows = 128;  // query rows of a CTA and q head
+
+// A CTA's share of a mixed batch: rows row0 .. row0 + rows - 1 of sequence s,
+// at positions pmin .. pmax, for `units` q heads from h0 on; nt key tiles of
+// 128, the last with klast visible keys.  bad: the sequence's arguments are
+// out of range (its rows are zero), or there is no such tile (s < 0).
+struct PrefillTile {
+    int s, row0, rows, pmin, pmax, nt, klast, bad, units, h0;
+};
+
+// For a whole warp, the result on every lane.  Entries are numbered over the
+// prefill sequences (query_len > 1) in order, one per row tile of 128 rows
+// (ceil(qlen/128) tiles), and two for each of the last split_last tiles (one
+// per q head).
+__device__ __forceinline__ PrefillTile find_prefill_tile(const int32_t* qsl, const int32_t* context_lens,
+                                                         int num_seqs, int ctx_cap, int cta_units, int split_last,
+                                                         int tile, int pair, unsigned long long* err, int lane) {
+    const unsigned FULL = 0xffffffffu;
+    const int split = cta_units == 2 ? split_last : 0;
+    int base = 0, found = -1, e = 0, nt_s = 0;
+    for (int s0 = 0; s0 < num_seqs && found < 0; s0 += 32) {
+        const int s = s0 + lane;
+        int nt = 0;
+        if (s < num_seqs) {
+            const int ql = __ldg(qsl + s + 1) - __ldg(qsl + s);
+            nt = ql > 1 ? (ql + kPrefillRows - 1) / kPrefillRows : 0;
+        }
+        const int ne = nt + min(split, nt);
+        int incl = ne;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl += t;
+        }
+        const unsigned hit = __ballot_sync(FULL, base + incl > tile);
+        if (hit) {
+            const int j = __ffs(hit) - 1;
+            found = s0 + j;
+            e = tile - (base + __shfl_sync(FULL, incl - ne, j));
+            nt_s = __shfl_sync(FULL, nt, j);
+        } else {
+            base += __shfl_sync(FULL, incl, 31);
+        }
+    }
+    // Entry e of the sequence: row tile e while e < nt - sl (both heads), then
+    // tile nt - sl + (e - (nt - sl)) / 2, one head each.
+    const int sl = min(split, nt_s);
+    PrefillTile r = {};
+    r.s = found;
+    r.units = cta_units;
+    r.h0 = pair * cta_units;
+    int tloc = e;
+    if (sl > 0 && e >= nt_s - sl) {
+        const int k = e - (nt_s - sl);
+        tloc = nt_s - sl + k / 2;
+        r.units = 1;
+        r.h0 += k % 2;
+    }
+    if (found < 0) {
+        r.bad = 1;
+        return r;
+    }
+    const int q0 = __ldg(qsl + found);
+    const int ql = __ldg(qsl + found + 1) - q0;
+    const int ctx = __ldg(context_lens + found);
+    if (ctx > ctx_cap || ql > ctx) {
+        if (lane == 0) record_error(err, kErrRange, static_cast<uint32_t>(found));
+        r.bad = 1;
+    }
+    r.row0 = q0 + tloc * kPrefillRows;
+    r.rows = min(kPrefillRows, ql - tloc * kPrefillRows);
+    r.pmin = ctx - ql + tloc * kPrefillRows;
+    r.pmax = r.pmin + r.rows - 1;
+    r.nt = r.bad ? 0 : r.pmax / 128 + 1;
+    r.klast = r.pmax + 1 - (r.pmax / 128) * 128;
+    return r;
+}
+
+}  // namespace pkv
