@@ -511,33 +511,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float fa = rowf[u * kTileM + ma], fb = rowf[u * kTileM + mb];
             // References of P, and of what was moved out of tensor memory.
             float mua = 0.f, mub = 0.f, mfa = 0.f, mfb = 0.f, la = 0.f, lb = 0.f;
-            float* oa = P.out + (static_cast<size_t>(T.row0 + ma) * P.hq + T.h0 + u) * D + 2 * tq;
-            float* ob = P.out + (static_cast<size_t>(T.row0 + mb) * P.hq + T.h0 + u) * D + 2 * tq;
-            // O = what was moved out, times fac, plus what tensor memory has,
-            // times alpha; stored times inv.
-            auto move_out = [&](bool first, float fac_a, float fac_b, float alpha_a, float alpha_b, float inv_a,
-                                float inv_b) {
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t r[32];
-                    tc::tmem_ld16x256b_x8(tmem + tlane + col_o(u) + 64 * c, r);
-                    float2 xa[8], xb[8];
+            // Where rows start in out, worked out when wanted: held over the
+            // tiles they would cost the scores their registers.
+            const volatile PrefillTile* where = info;
+            auto row_at = [&](int m) {
+                return P.out + (static_cast<size_t>(where->row0 + m) * P.hq + where->h0 + u) * D;
+            };
+            // What is moved out waits in the warp's own 16 rows of out, in the
+            // order of its registers: D / 8 pieces of 16 bytes a thread, 32 of
+            // them together.  (In the rows' own order a request meets eight lines
+            // with 32 bytes each: 99 us more over 128 tiles.)  Rows that the warp
+            // does not have 16 of are kept in the rows' order.
+            const bool whole = 32 * (warp & 3) + 16 * hh + 16 <= T.rows;
+            auto pieces = [&]() {
+                return reinterpret_cast<float4*>(row_at(32 * (warp & 3) + 16 * hh + (D == 128 ? 0 : lane / 16)) +
+                                                 4 * (D == 128 ? lane : lane & 15));
+            };
+            const int pitch = P.hq * D / 4 * (D == 128 ? 1 : 2);  // of a thread's pieces
+            // 32 values of a thread: columns 64 c and on.
+            auto load_kept = [&](int c, float (&x)[32]) {
+                if (whole) {
+                    const float4* src = pieces() + static_cast<size_t>(8 * c) * pitch;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        xa[i] = xb[i] = make_float2(0.f, 0.f);
-                        if (!first && ma < T.rows) xa[i] = *reinterpret_cast<const float2*>(oa + 64 * c + 8 * i);
-                        if (!first && mb < T.rows) xb[i] = *reinterpret_cast<const float2*>(ob + 64 * c + 8 * i);
+                        const float4 v = src[static_cast<size_t>(i) * pitch];
+                        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
                     }
-                    tc::tmem_wait_ld();
+                } else {
+                    const float *oa = row_at(ma) + 2 * tq, *ob = row_at(mb) + 2 * tq;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        xa[i].x = fmaf(__uint_as_float(r[4 * i]), alpha_a, xa[i].x * fac_a) * inv_a;
-                        xa[i].y = fmaf(__uint_as_float(r[4 * i + 1]), alpha_a, xa[i].y * fac_a) * inv_a;
-                        xb[i].x = fmaf(__uint_as_float(r[4 * i + 2]), alpha_b, xb[i].x * fac_b) * inv_b;
-                        xb[i].y = fmaf(__uint_as_float(r[4 * i + 3]), alpha_b, xb[i].y * fac_b) * inv_b;
-                        if (ma < T.rows) *reinterpret_cast<float2*>(oa + 64 * c + 8 * i) = xa[i];
-                        if (mb < T.rows) *reinterpret_cast<float2*>(ob + 64 * c + 8 * i) = xb[i];
+                        float2 va = make_float2(0.f, 0.f), vb = va;
+                        if (ma < T.rows) va = *reinterpret_cast<const float2*>(oa + 64 * c + 8 * i);
+                        if (mb < T.rows) vb = *reinterpret_cast<const float2*>(ob + 64 * c + 8 * i);
+                        x[4 * i] = va.x, x[4 * i + 1] = va.y, x[4 * i + 2] = vb.x, x[4 * i + 3] = vb.y;
                     }
+                }
+            };
+            auto store_rows = [&](int c, const float (&x)[32]) {
+                float *oa = row_at(ma) + 2 * tq, *ob = row_at(mb) + 2 * tq;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (ma < T.rows)
+                        *reinterpret_cast<float2*>(oa + 64 * c + 8 * i) = make_float2(x[4 * i], x[4 * i + 1]);
+                    if (mb < T.rows)
+                        *reinterpret_cast<float2*>(ob + 64 * c + 8 * i) = make_float2(x[4 * i + 2], x[4 * i + 3]);
+                }
+            };
+            // x = x fac + (tensor memory's columns 64 c and on) alpha.
+            auto join = [&](int c, float (&x)[32], float fac_a, float fac_b, float alpha_a, float alpha_b) {
+                uint32_t r[32];
+                tc::tmem_ld16x256b_x8(tmem + tlane + col_o(u) + 64 * c, r);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const bool row_b = i & 2;
+                    x[i] = fmaf(__uint_as_float(r[i]), row_b ? alpha_b : alpha_a, x[i] * (row_b ? fac_b : fac_a));
                 }
             };
             for (int j = 0; j < nt && ok; ++j) {
@@ -611,15 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Pass 2: P in two fp16 terms over the scores, its first 11 bits
                 // and the rest; the row sums without the V scales.
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t hi[16], lo[16];
+                for (int qt = 0; qt < 4; ++qt) {
+                    uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int b = 4 * hf; b < 4 * hf + 4; ++b) {
+                    for (int b = 2 * qt; b < 2 * qt + 2; ++b) {
                         float2 ta = make_float2(0.f, 0.f), tb = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t* s = &sr[4 * (2 * b + h)];
-                            const int at = 2 * (2 * (b - 4 * hf) + h);
+                            const int at = 2 * (2 * (b - 2 * qt) + h);
                             const float2 pa = make_float2(fast_exp2(__uint_as_float(s[0])), fast_exp2(__uint_as_float(s[1])));
                             const float2 pb = make_float2(fast_exp2(__uint_as_float(s[2])), fast_exp2(__uint_as_float(s[3])));
                             ta = __fadd2_rn(ta, pa);
@@ -631,12 +660,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         la = fmaf(ta.x + ta.y, inv, la);
                         lb = fmaf(tb.x + tb.y, inv, lb);
                     }
-                    tc::tmem_st16x128b_x8(tmem + tlane + col_s(u) + 32 * hf, hi);
-                    tc::tmem_st16x128b_x8(tmem + tlane + col_s(u) + 64 + 32 * hf, lo);
+                    tc::tmem_st16x128b_x4(tmem + tlane + col_s(u) + 16 * qt, hi);
+                    tc::tmem_st16x128b_x4(tmem + tlane + col_s(u) + 64 + 16 * qt, lo);
                 }
                 if (j > 0 && j % kKeep == 0) {
                     // The MMA warp starts O anew with this tile's P V.
-                    move_out(j == kKeep, fast_exp2(mfa - mua), fast_exp2(mfb - mub), alpha_a, alpha_b, 1.f, 1.f);
+                    const float fac_a = fast_exp2(mfa - mua), fac_b = fast_exp2(mfb - mub);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        float x[32];
+                        if (j > kKeep) {
+                            load_kept(c, x);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                        }
+                        join(c, x, fac_a, fac_b, alpha_a, alpha_b);
+                        if (whole) {
+                            float4* dst = pieces() + static_cast<size_t>(8 * c) * pitch;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[static_cast<size_t>(i) * pitch] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        } else {
+                            store_rows(c, x);
+                        }
+                    }
                     mfa = mua;
                     mfb = mub;
                 } else if (moves && j > 0) {
@@ -668,7 +716,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lb += __shfl_xor_sync(FULL, lb, 1);
                 la += __shfl_xor_sync(FULL, la, 2);
                 lb += __shfl_xor_sync(FULL, lb, 2);
-                move_out(nt <= kKeep, fast_exp2(mfa - mua), fast_exp2(mfb - mub), 1.f, 1.f, 1.f / la, 1.f / lb);
+                const float inva = 1.f / la, invb = 1.f / lb;
+                const float fac_a = fast_exp2(mfa - mua), fac_b = fast_exp2(mfb - mub);
+                auto kept_or_zero = [&](int c, float (&x)[32]) {
+                    if (nt > kKeep) {
+                        load_kept(c, x);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    }
+                };
+                float x[32], y[D == 128 ? 32 : 1];
+                kept_or_zero(0, x);
+                join(0, x, fac_a * inva, fac_b * invb, inva, invb);
+                if constexpr (D == 128) kept_or_zero(1, y);
+                __syncwarp();  // the rows are read before they are written in their own order
+                store_rows(0, x);
+                if constexpr (D == 128) {
+                    join(1, y, fac_a * inva, fac_b * invb, inva, invb);
+                    store_rows(1, y);
+                }
             }
         }
         if (__any_sync(FULL, nan != 0) && lane == 0) atomicOr(redo, 1);
