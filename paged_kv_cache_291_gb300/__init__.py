@@ -160,6 +160,7 @@ class _NoCalls:
         return None
 
     rotary_cache_write = linear_decode = linear_prefill = rotary
+    cache_append = cache_read = decode_scaled = prefill_scaled = rotary
 
 
 def _fast():
@@ -273,8 +274,8 @@ def _cache(k_pool, v_pool, k_scale=None, v_scale=None, need_scales=False, block_
             raise ValueError("a pool has block_scales or k_scale and v_scale, not both")
         if tuple(block_scales.shape) != (nb, hkv, 2):
             raise ValueError("block_scales must be [num_blocks][num_kv_heads][2]")
-        if not k_pool.get_device() == v_pool.get_device() == block_scales.get_device():
-            raise ValueError("the pools and block_scales must be on one device")
+        if not k_pool.get_device() == v_pool.get_device() == block_scales.get_device() == _device():
+            raise ValueError("the pools and block_scales must be on the current device")
         return Cache(_dev(k_pool, "k_pool").value, _dev(v_pool, "v_pool").value, nb, hkv, d, bs,
                      PKV_KV_INT8_BLOCKS if k_pool.dtype == torch.int8 else PKV_KV_E4M3_BLOCKS, 1.0, 1.0,
                      _dev(block_scales, "block_scales", dtype=torch.float32).value)
@@ -335,6 +336,14 @@ def cache_append(k_pool, v_pool, block_scales, k_new, v_new, query_start_loc, co
     them.  The pools are int8, or e4m3 codes (uint8 or float8_e4m3fn), and
     block_scales float32 [num_blocks][Hkv][2] (K, V).  A block whose scale has
     to grow has its earlier rows encoded again."""
+    if block_scales is None:
+        raise ValueError("cache_append needs block_scales; pools without them take cache_write")
+    st = _fast().cache_append(k_pool, v_pool, block_scales, k_new, v_new, query_start_loc, context_lens, block_tables,
+                              stream)
+    if st == PKV_OK:
+        return
+    if st is not None:
+        raise PKVError(st, "pkv_cache_append")
     torch = _torch()
     lib = load()
     dev = _device()
@@ -354,14 +363,22 @@ def cache_read(k_pool, v_pool, query_start_loc, context_lens, block_tables, num_
     [num_tokens][Hkv][d] for the last rows of its context.  Returns (k_out,
     v_out)."""
     torch = _torch()
+    shape = (int(num_tokens), k_pool.shape[1], k_pool.shape[3])
+    if k_out is None or v_out is None:
+        with _on(stream):
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if k_out is None else k_out
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if v_out is None else v_out
+    if block_scales is not None and k_scale is None and v_scale is None:
+        st = _fast().cache_read(k_pool, v_pool, block_scales, query_start_loc, context_lens, block_tables, shape[0],
+                                k_out, v_out, stream)
+        if st == PKV_OK:
+            return k_out, v_out
+        if st is not None:
+            raise PKVError(st, "pkv_cache_read")
     lib = load()
     dev = _device()
     c, index = _cache_rows(k_pool, v_pool, query_start_loc, context_lens, block_tables, k_scale, v_scale,
                            block_scales, dev)
-    shape = (int(num_tokens), c.num_kv_heads, c.head_dim)
-    with _on(stream):
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device) if v_out is None else v_out
     st = lib.pkv_cache_read(ctypes.byref(c), _addr(k_out, "k_out", torch.bfloat16, dev, shape),
                             _addr(v_out, "v_out", torch.bfloat16, dev, shape), shape[0], *index,
                             _stream_handle(stream))
@@ -422,9 +439,12 @@ def decode_attention(k_pool, v_pool, q, block_tables, context_lens, max_context_
                      v_scale=None, block_scales=None):
     """Paged decode attention; returns ``out`` float32 [B][Hq][d].  8-bit pools
     (1-byte elements) need the scales they were written with."""
+    if block_scales is not None:
+        return _decode_scaled(k_pool, v_pool, q, block_tables, context_lens, max_context_len, scale, out, workspace,
+                              partition_blocks, stream, k_scale, v_scale, block_scales)
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True, block_scales=block_scales)
+    c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True)
     B, hq, d = q.shape
     if d != c.head_dim:
         raise ValueError("q head_dim does not match the pools")
@@ -444,6 +464,45 @@ def decode_attention(k_pool, v_pool, q, block_tables, context_lens, max_context_
                                   float(scale), _out(out),
                                   _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
                                   int(partition_blocks), _stream_handle(stream))
+    _check(st, "pkv_decode_attention")
+    return out
+
+
+def _decode_scaled(k_pool, v_pool, q, block_tables, context_lens, max_context_len, scale, out, workspace,
+                   partition_blocks, stream, k_scale, v_scale, block_scales):
+    """:func:`decode_attention` over pools with a scale per block."""
+    torch = _torch()
+    if k_scale is not None or v_scale is not None:
+        raise ValueError("a pool has block_scales or k_scale and v_scale, not both")
+    if out is None:
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        need = load().pkv_decode_workspace_size(q.shape[0], q.shape[1], k_pool.shape[1], q.shape[2],
+                                                int(max_context_len), int(partition_blocks))
+        with _on(stream):
+            workspace = new_workspace(need, q.device)
+    st = _fast().decode_scaled(k_pool, v_pool, block_scales, q, block_tables, context_lens, max_context_len, scale, out,
+                               workspace, partition_blocks, stream)
+    if st == PKV_OK:
+        return out
+    if st is not None:
+        raise PKVError(st, "pkv_decode_attention")
+    lib = load()
+    dev = _device()
+    c = _cache(k_pool, v_pool, block_scales=block_scales)
+    B, hq, d = q.shape
+    if d != c.head_dim:
+        raise ValueError("q head_dim does not match the pools")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [B][max_blocks]")
+    i32, wide = torch.int32, block_tables.shape[1]
+    st = lib.pkv_decode_attention(ctypes.byref(c), _addr(q, "q", torch.bfloat16, dev, (B, hq, d)), hq,
+                                  _addr(block_tables, "block_tables", i32, dev, (B, wide)), wide,
+                                  _addr(context_lens, "context_lens", i32, dev, (B,)), B, int(max_context_len),
+                                  float(scale), _out_addr(out, dev, q.shape),
+                                  _addr(workspace, "workspace", workspace.dtype, dev, workspace.shape),
+                                  workspace.nbytes, int(partition_blocks), _stream_handle(stream))
     _check(st, "pkv_decode_attention")
     return out
 
@@ -564,9 +623,12 @@ def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, 
                               query_start_loc_host=None, stream=None, block_scales=None):
     """Mixed batch of causal prefill chunks and decode rows; returns ``out``
     float32 [Tq][Hq][d].  Pools are bf16, or 8-bit with ``block_scales``."""
+    if block_scales is not None:
+        return _prefill_scaled(k_pool, v_pool, q, query_start_loc, context_lens, block_tables, max_context_len, scale,
+                               out, workspace, query_start_loc_host, stream, block_scales)
     torch = _torch()
     lib = load()
-    c = _cache(k_pool, v_pool, block_scales=block_scales)
+    c = _cache(k_pool, v_pool)
     T, hq, d = q.shape
     S = int(context_lens.shape[0])
     if query_start_loc.shape[0] != S + 1:
@@ -592,8 +654,54 @@ def chunked_prefill_attention(k_pool, v_pool, q, query_start_loc, context_lens, 
     return out
 
 
-# The rotary and linear-attention calls go through the compiled binding; what
-# it hands back is checked and called here.
+def _prefill_scaled(k_pool, v_pool, q, query_start_loc, context_lens, block_tables, max_context_len, scale, out,
+                    workspace, query_start_loc_host, stream, block_scales):
+    """:func:`chunked_prefill_attention` over pools with a scale per block."""
+    torch = _torch()
+    qh = query_start_loc if query_start_loc_host is None else query_start_loc_host
+    if not isinstance(qh, torch.Tensor) or qh.is_cuda or qh.dtype is not torch.int32:
+        with _on(stream):
+            qh = torch.from_numpy(_host_i32(qh)[0])
+    if out is None:
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        need = load().pkv_prefill_workspace_size(context_lens.shape[0], q.shape[0], q.shape[1], k_pool.shape[1],
+                                                 q.shape[2], int(max_context_len))
+        with _on(stream):
+            workspace = new_workspace(need, q.device)
+    st = _fast().prefill_scaled(k_pool, v_pool, block_scales, q, query_start_loc, qh, context_lens, block_tables,
+                                max_context_len, scale, out, workspace, stream)
+    if st == PKV_OK:
+        return out
+    if st is not None:
+        raise PKVError(st, "pkv_chunked_prefill_attention")
+    lib = load()
+    dev = _device()
+    c = _cache(k_pool, v_pool, block_scales=block_scales)
+    T, hq, d = q.shape
+    S = context_lens.shape[0]
+    if d != c.head_dim:
+        raise ValueError("q head_dim does not match the pools")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs][max_blocks]")
+    if tuple(qh.shape) != (S + 1,) or not qh.is_contiguous():
+        raise ValueError("query_start_loc_host must have num_seqs + 1 entries")
+    i32, wide = torch.int32, block_tables.shape[1]
+    st = lib.pkv_chunked_prefill_attention(
+        ctypes.byref(c), _addr(q, "q", torch.bfloat16, dev, (T, hq, d)), hq, T,
+        _addr(query_start_loc, "query_start_loc", i32, dev, (S + 1,)), qh.data_ptr(),
+        _addr(context_lens, "context_lens", i32, dev, (S,)), S,
+        _addr(block_tables, "block_tables", i32, dev, (S, wide)), wide, int(max_context_len), float(scale),
+        _out_addr(out, dev, q.shape), _addr(workspace, "workspace", workspace.dtype, dev, workspace.shape),
+        workspace.nbytes, _stream_handle(stream))
+    _check(st, "pkv_chunked_prefill_attention")
+    return out
+
+
+# The rotary and linear-attention calls, and those on pools with a scale per
+# block, go through the compiled binding; what it hands back is checked and
+# called here.
 
 def _device() -> int:
     """The current device's index: the library launches there, so every

@@ -1,5 +1,6 @@
-// binding.cpp -- the rotary and linear-attention calls from torch tensors to
-// the C-ABI of include/pkv.h, as a CPython module.
+// binding.cpp -- the rotary and linear-attention calls, and those on pools with
+// a scale per block, from torch tensors to the C-ABI of include/pkv.h, as a
+// CPython module.
 //
 // These calls are made once per layer and step, and their kernels often take
 // less time than it takes Python to read a dozen tensors' attributes.  Each
@@ -68,6 +69,17 @@ struct Call {
             ok = false;
         }
         return static_cast<float>(x);
+    }
+    // An int that fits 32 bits.
+    int32_t whole(PyObject* o) {
+        if (!PyLong_CheckExact(o)) {
+            ok = false;
+            return 0;
+        }
+        int overflow = 0;
+        const long x = PyLong_AsLongAndOverflow(o, &overflow);
+        if (overflow != 0 || x < INT32_MIN || x > INT32_MAX) ok = false;
+        return static_cast<int32_t>(x);
     }
     // The stream argument: None is torch's current stream; anything else is the wrapper's.
     void* stream(PyObject* o) {
@@ -254,6 +266,141 @@ PyObject* linear_prefill(PyObject*, Args a, Py_ssize_t n) {
         ws.data_ptr(), ws.nbytes(), l.stream));
 }
 
+// k_pool, v_pool, block_scales: pools with a scale for each (block, kv head).
+void fill_scaled(Call& c, Args a, pkv_cache_t* cache) {
+    if (!c.dims(a[0], 4)) return;
+    const c10::ScalarType type = THPVariable_Unpack(a[0]).scalar_type();
+    const bool int8 = type == c10::kChar;
+    const int64_t nb = c.size(a[0], 0), hkv = c.size(a[0], 1), d = c.size(a[0], 3);
+    if ((!int8 && type != c10::kByte && type != c10::ScalarType::Float8_e4m3fn) || nb > kMaxInt || hkv > kMaxInt ||
+        d > kMaxInt) {
+        c.ok = false;
+        return;
+    }
+    cache->k_pool = c.plain(a[0], type, {nb, hkv, 16, d});
+    cache->v_pool = c.plain(a[1], type, {nb, hkv, 16, d});
+    cache->block_scales = static_cast<float*>(c.plain(a[2], c10::kFloat, {nb, hkv, 2}));
+    cache->num_blocks = static_cast<int32_t>(nb);
+    cache->num_kv_heads = static_cast<int32_t>(hkv);
+    cache->head_dim = static_cast<int32_t>(d);
+    cache->block_size = 16;
+    cache->kv_dtype = int8 ? PKV_KV_INT8_BLOCKS : PKV_KV_E4M3_BLOCKS;
+    cache->k_scale = cache->v_scale = 1.f;
+}
+
+// query_start_loc, context_lens, block_tables
+struct Index {
+    const int32_t *start, *lens, *tables;
+    int32_t seqs, wide;
+};
+
+void fill_index(Call& c, PyObject* start, PyObject* lens, PyObject* tables, Index* x) {
+    if (!c.dims(lens, 1) || !c.dims(tables, 2)) return;
+    const int64_t seqs = c.size(lens, 0), wide = c.size(tables, 1);
+    if (seqs >= kMaxInt || wide > kMaxInt) {
+        c.ok = false;
+        return;
+    }
+    x->seqs = static_cast<int32_t>(seqs);
+    x->wide = static_cast<int32_t>(wide);
+    x->start = start == nullptr ? nullptr : static_cast<const int32_t*>(c.plain(start, c10::kInt, {seqs + 1}));
+    x->lens = static_cast<const int32_t*>(c.plain(lens, c10::kInt, {seqs}));
+    x->tables = static_cast<const int32_t*>(c.plain(tables, c10::kInt, {seqs, wide}));
+}
+
+// k_pool, v_pool, block_scales, k_new, v_new, query_start_loc, context_lens, block_tables, stream
+PyObject* cache_append(PyObject*, Args a, Py_ssize_t n) {
+    if (n != 9) return none();
+    Call c;
+    pkv_cache_t cache;
+    Index x;
+    fill_scaled(c, a, &cache);
+    fill_index(c, a[5], a[6], a[7], &x);
+    if (!c.dims(a[3], 3)) return none();
+    const int64_t T = c.size(a[3], 0);
+    int64_t ks = 0, vs = 0;
+    const void* k = c.rows(a[3], T, cache.num_kv_heads, cache.head_dim, &ks);
+    const void* v = c.rows(a[4], T, cache.num_kv_heads, cache.head_dim, &vs);
+    void* stream = c.stream(a[8]);
+    if (!c.ok || T > kMaxInt) return none();
+    return status(pkv_cache_append(&cache, k, ks, v, vs, static_cast<int32_t>(T), x.start, x.lens, x.seqs, x.tables,
+                                   x.wide, stream));
+}
+
+// k_pool, v_pool, block_scales, query_start_loc, context_lens, block_tables, num_tokens, k_out, v_out, stream
+PyObject* cache_read(PyObject*, Args a, Py_ssize_t n) {
+    if (n != 10) return none();
+    Call c;
+    pkv_cache_t cache;
+    Index x;
+    fill_scaled(c, a, &cache);
+    fill_index(c, a[3], a[4], a[5], &x);
+    const int32_t T = c.whole(a[6]);
+    if (!c.ok) return none();
+    void* k = c.plain(a[7], c10::kBFloat16, {T, cache.num_kv_heads, cache.head_dim});
+    void* v = c.plain(a[8], c10::kBFloat16, {T, cache.num_kv_heads, cache.head_dim});
+    void* stream = c.stream(a[9]);
+    if (!c.ok) return none();
+    return status(pkv_cache_read(&cache, k, v, T, x.start, x.lens, x.seqs, x.tables, x.wide, stream));
+}
+
+// A workspace: any contiguous tensor of the device.
+const at::Tensor* workspace(Call& c, PyObject* o) {
+    if (!c.ok || !THPVariable_Check(o)) return c.fail();
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.get_device() != c.dev || !t.is_contiguous()) return c.fail();
+    return &t;
+}
+
+// k_pool, v_pool, block_scales, q, block_tables, context_lens, max_context_len, scale, out, workspace,
+// partition_blocks, stream
+PyObject* decode_scaled(PyObject*, Args a, Py_ssize_t n) {
+    if (n != 12) return none();
+    Call c;
+    pkv_cache_t cache;
+    Index x;
+    fill_scaled(c, a, &cache);
+    fill_index(c, nullptr, a[5], a[4], &x);
+    if (!c.dims(a[3], 3)) return none();
+    const int64_t hq = c.size(a[3], 1);
+    const void* q = c.plain(a[3], c10::kBFloat16, {x.seqs, hq, cache.head_dim});
+    const int32_t longest = c.whole(a[6]), part = c.whole(a[10]);
+    const float scale = c.real(a[7]);
+    void* out = c.plain(a[8], c10::kFloat, {x.seqs, hq, cache.head_dim});
+    const at::Tensor* ws = workspace(c, a[9]);
+    void* stream = c.stream(a[11]);
+    if (!c.ok || hq > kMaxInt) return none();
+    return status(pkv_decode_attention(&cache, q, static_cast<int32_t>(hq), x.tables, x.wide, x.lens, x.seqs, longest,
+                                       scale, static_cast<float*>(out), ws->data_ptr(), ws->nbytes(), part, stream));
+}
+
+// k_pool, v_pool, block_scales, q, query_start_loc, query_start_loc_host (int32 CPU tensor), context_lens,
+// block_tables, max_context_len, scale, out, workspace, stream
+PyObject* prefill_scaled(PyObject*, Args a, Py_ssize_t n) {
+    if (n != 13) return none();
+    Call c;
+    pkv_cache_t cache;
+    Index x;
+    fill_scaled(c, a, &cache);
+    fill_index(c, a[4], a[6], a[7], &x);
+    if (!c.dims(a[3], 3) || !THPVariable_Check(a[5])) return none();
+    const int64_t T = c.size(a[3], 0), hq = c.size(a[3], 1);
+    const void* q = c.plain(a[3], c10::kBFloat16, {T, hq, cache.head_dim});
+    const int32_t longest = c.whole(a[8]);
+    const float scale = c.real(a[9]);
+    void* out = c.plain(a[10], c10::kFloat, {T, hq, cache.head_dim});
+    const at::Tensor* ws = workspace(c, a[11]);
+    void* stream = c.stream(a[12]);
+    const at::Tensor& host = THPVariable_Unpack(a[5]);
+    if (!c.ok || T > kMaxInt || hq > kMaxInt || !host.is_cpu() || host.scalar_type() != c10::kInt || host.dim() != 1 ||
+        host.size(0) != x.seqs + 1 || !host.is_contiguous())
+        return none();
+    return status(pkv_chunked_prefill_attention(
+        &cache, q, static_cast<int32_t>(hq), static_cast<int32_t>(T), x.start,
+        static_cast<const int32_t*>(host.data_ptr()), x.lens, x.seqs, x.tables, x.wide, longest, scale,
+        static_cast<float*>(out), ws->data_ptr(), ws->nbytes(), stream));
+}
+
 // C++ exceptions end here: torch's accessors may throw on unusual tensors.
 template <PyObject* (*F)(PyObject*, Args, Py_ssize_t)>
 PyObject* guarded(PyObject* self, Args a, Py_ssize_t n) {
@@ -272,6 +419,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<rotary>("rotary"), method<rotary_cache_write>("rotary_cache_write"),
                            method<linear_decode>("linear_decode"), method<linear_prefill>("linear_prefill"),
+                           method<cache_append>("cache_append"), method<cache_read>("cache_read"),
+                           method<decode_scaled>("decode_scaled"), method<prefill_scaled>("prefill_scaled"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
