@@ -172,6 +172,7 @@ struct Cfg {
     static constexpr int HEAD_DIM = D, GROUP = G, ELEM = EB;
     static constexpr bool SCALED = false;  // a scale per (block, kv head), two blocks a stage (decode_scaled.cuh)
     static constexpr int BPS = 1;          // blocks a stage
+    static constexpr int MERGERS = 1;      // merger warps, each with its share of the group's heads
     static constexpr bool MMA = use_mma<D, G, EB>();
     static constexpr int ALIGN_PAD = MMA ? 1024 : 0;  // swizzled tiles need a 1024-byte aligned ring
     static constexpr int W = consumer_warps<D, G, EB>();  // consumer warps
@@ -326,6 +327,12 @@ __device__ __forceinline__ long long auto_range_units(long long T, unsigned grid
     return RU;
 }
 
+// What a pair counts beyond its blocks in the cut of T blocks of work: nothing
+// where the CTAs have few, whose pairs it would only split.
+__device__ __forceinline__ int extra_units(const DecodeParams& P, long long T) {
+    return P.extra_units > 0 && T >= 4ll * P.extra_units * gridDim.x ? P.extra_units : 0;
+}
+
 // Units of work of one kv head of sequence s: one per 16-token block of its
 // context past the shared prefix (at least one, so that an empty context
 // still yields its output row), 0 for rows that are not decode rows.  The
@@ -342,7 +349,7 @@ __device__ __forceinline__ int seq_units(const DecodeParams& P, int s, int& n_ou
         n = n < 0 ? 0 : P.ctx_cap;
     }
     n_out = n;
-    return max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks) + P.extra_units;
+    return max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks);
 }
 
 __device__ __forceinline__ uint4 lds128(const void* p) {
@@ -538,11 +545,13 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
     struct Win {
         int s0, base, u, n, incl;
     };
+    int extra = 0;
     auto load_window = [&](Win& W, bool report) {
         const int s = W.s0 + lane;
         W.u = 0;
         W.n = 0;
         if (s < P.num_seqs) W.u = seq_units(P, s, W.n, report);
+        if (W.u > 0) W.u += extra;
         W.incl = W.u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -567,11 +576,13 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
     // Smallest and largest units of a decode row's pair (rows with none
     // excluded): equal for a batch whose contexts span the same blocks.
     int umin = win.u > 0 ? win.u : INT32_MAX, umax = win.u;
+    long long rows = win.u > 0 ? 1 : 0;  // sequences with units, summed over the lanes where they are wanted
     for (int s0 = 32; s0 < P.num_seqs; s0 += 32) {
         int n, u = 0;
         if (s0 + lane < P.num_seqs) u = seq_units(P, s0 + lane, n, blockIdx.x == 0);
         umin = min(umin, u > 0 ? u : INT32_MAX);
         umax = max(umax, u);
+        rows += u > 0 ? 1 : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
         per_head += u;
@@ -580,6 +591,17 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
     for (int o = 16; o > 0; o >>= 1) {
         umin = min(umin, __shfl_xor_sync(FULL, umin, o));
         umax = max(umax, __shfl_xor_sync(FULL, umax, o));
+    }
+    if constexpr (C::SCALED) {
+        extra = extra_units(P, per_head * P.hkv);
+        if (extra > 0) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(FULL, rows, o);
+            per_head += rows * extra;
+            umin += umin < INT32_MAX ? extra : 0;
+            umax += umax > 0 ? extra : 0;
+            load_window(win, false);
+        }
     }
     const long long T = per_head * P.hkv;
     long long RU = P.range_units;
@@ -1291,8 +1313,12 @@ __device__ __forceinline__ float4 finish_row(float4 a, float L, float v_scale) {
 }
 
 template <class C>
-__device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, volatile int* abort_flag, int lane) {
+__device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, volatile int* abort_flag, int lane,
+                           int share = 0) {
     constexpr int D = C::HEAD_DIM, G = C::GROUP;
+    constexpr int MG = G / C::MERGERS;  // heads of this warp, from share * MG on
+    static_assert(MG * C::MERGERS == G, "a merger's heads");
+    const int g0 = share * MG;
     const ItemDesc* descs = reinterpret_cast<const ItemDesc*>(smem + C::OFF_DESC);
     const float* mo = reinterpret_cast<const float*>(smem + C::OFF_MO);
     const float2* ml = reinterpret_cast<const float2*>(smem + C::OFF_ML);
@@ -1313,6 +1339,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
         const unsigned FULL = 0xffffffffu;
         constexpr int W = C::W;
         constexpr int CH = G * D / 4;
+        constexpr int MCH = MG * D / 4;  // this warp's
         constexpr int WL = C::MERGE_LANES;
         constexpr int NJ = (CH + 31) / 32;
         const int h0 = d.g * G;
@@ -1347,10 +1374,10 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
         // l_p, o_p) the reference becomes max(M, m_p): the warps' weights
         // take the factor 2^(M - max) and o_p the weight 2^(m_p - max).
 #pragma unroll
-        for (int i0 = 0; i0 < G * WL; i0 += 32) {
+        for (int i0 = 0; i0 < MG * WL; i0 += 32) {
             const int i = i0 + lane;
-            const int w = i % WL, gi = i / WL;
-            const bool live = gi < G && w < W;
+            const int w = i % WL, gi = g0 + i / WL;
+            const bool live = i / WL < MG && w < W;
             const float2 e = live ? ml[(buf * W + w) * G + gi] : make_float2(-INFINITY, 0.f);
             float M = e.x;
 #pragma unroll
@@ -1382,9 +1409,9 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
                           ? reinterpret_cast<float4*>(P.out + (static_cast<size_t>(d.row) * P.hq + h0) * D)
                           : reinterpret_cast<float4*>(P.part_o + pi0 * D);
 #pragma unroll
-        for (int j = 0; j < (CH + 31) / 32; ++j) {
-            const int k = lane + 32 * j;
-            if (k < CH) {
+        for (int j = 0; j < (MCH + 31) / 32; ++j) {
+            const int k = g0 * (D / 4) + lane + 32 * j;
+            if (lane + 32 * j < MCH) {
                 const int g = k / (D / 4);
                 float4 v[W];
 #pragma unroll
@@ -1408,7 +1435,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
                 dst[k] = a;
             }
         }
-        if (d.nparts > 1 && lane < G) P.part_ml[pi0 + lane] = msm[lane];
+        if (d.nparts > 1 && lane < MG) P.part_ml[pi0 + g0 + lane] = msm[g0 + lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.mempty[buf]);
         if (d.nparts > 1) {
@@ -1418,7 +1445,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
             uint32_t* ctr = P.counters + static_cast<size_t>(d.s) * P.hkv + d.g;
             if (lane == 0) ticket = atomicAdd(ctr, 1u);
             ticket = __shfl_sync(FULL, ticket, 0);
-            if (ticket == static_cast<uint32_t>(d.nparts - 1)) {
+            if (ticket == static_cast<uint32_t>(d.nparts * C::MERGERS - 1)) {
                 // Last part in: merge all parts of (s, kv head), in part
                 // order.  Part k of the pair lives in range r0 + k, in slot
                 // slot0 for k = 0 and slot 0 after that; its G heads' (m, l)
@@ -1574,8 +1601,18 @@ __device__ void prefetch_first_blocks(const DecodeParams& P, int lane, int max_u
         if (s < P.num_seqs) {
             const bool dec = P.qsl == nullptr || ld_l2_only(P.qsl + s + 1) - ld_l2_only(P.qsl + s) == 1;
             const int n = min(max(ld_l2_only(P.context_lens + s), 0), P.ctx_cap);
-            u[w] = dec ? max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks) + P.extra_units : 0;
+            u[w] = dec ? max(1, (n + kBlockSize - 1) / kBlockSize - P.skip_blocks) : 0;
         }
+    }
+    if (P.extra_units > 0) {
+        long long blocks = 0;
+#pragma unroll
+        for (int w = 0; w < kSpecWindows; ++w) blocks += u[w];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) blocks += __shfl_xor_sync(FULL, blocks, o);
+        const int extra = extra_units(P, blocks * P.hkv);
+#pragma unroll
+        for (int w = 0; w < kSpecWindows; ++w) u[w] += u[w] > 0 ? extra : 0;
     }
     long long per_head = 0;
 #pragma unroll
@@ -1621,6 +1658,8 @@ __device__ void prefetch_first_blocks(const DecodeParams& P, int lane, int max_u
             for (int b = lane; b < cnt && P.skip_blocks + b0 + b < P.max_blocks; b += 32) {
                 const int phys = ld_l2_only(trow + b0 + b);
                 if (phys >= 0 && phys < P.num_blocks) {
+                    if (P.block_scales != nullptr)
+                        prefetch_l2(P.block_scales + static_cast<size_t>(phys) * P.hkv + g);
                     const size_t slab = (static_cast<size_t>(phys) * P.hkv + g) * C::SLAB;
                     bulk_prefetch_l2(P.k_pool + slab, C::SLAB);
                     bulk_prefetch_l2(P.v_pool + slab, C::SLAB);

@@ -57,7 +57,8 @@ struct ScaledCfg {
     // 16; 68 contexts of 40/40 x 128: 359 with 0, 340 with 8 and 16).
     static constexpr int EXTRA_UNITS = 12;
     static constexpr int MERGE_BUFS = 1;
-    static constexpr int PRODUCER_WARP = W, MERGER_WARP = W + 1, THREADS = 32 * (W + 2);
+    static constexpr int MERGERS = G == 8 ? 2 : 1;
+    static constexpr int PRODUCER_WARP = W, MERGER_WARP = W + 1, THREADS = 32 * (W + 1 + MERGERS);
     static constexpr int ORDERS = 8;  // stages a consumer warp is told of ahead
     static constexpr int SLAB = kBlockSize * D;
     static constexpr int STAGE_BYTES = 4 * SLAB;  // K of two blocks, V of two blocks
@@ -471,12 +472,14 @@ __global__ void __launch_bounds__(ScaledCfg<D, G, KIND>::THREADS, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
-    // One arrival completes every barrier but two kinds: consumers and merger
-    // hand a descriptor back, the consumers hand a merge buffer over.
+    // One arrival completes every barrier but three kinds: consumers and mergers
+    // hand a descriptor back, the consumers fill a merge buffer and the mergers
+    // empty it.
     for (int i = threadIdx.x; i < C::NBAR; i += C::THREADS) {
         const bool iempty = &bars[i] >= B.iempty && &bars[i] < B.iempty + kItemRing;
         const bool mfull = &bars[i] >= B.mfull && &bars[i] < B.mfull + C::MERGE_BUFS;
-        mbar_init(&bars[i], iempty ? C::W + 1 : mfull ? C::W : 1);
+        const bool mempty = &bars[i] >= B.mempty && &bars[i] < B.mempty + C::MERGE_BUFS;
+        mbar_init(&bars[i], iempty ? C::W + C::MERGERS : mfull ? C::W : mempty ? C::MERGERS : 1);
     }
     if (threadIdx.x == 0) *abort_flag = 0;
     fence_mbar_init();
@@ -486,10 +489,10 @@ __global__ void __launch_bounds__(ScaledCfg<D, G, KIND>::THREADS, 1)
     if (warp == C::PRODUCER_WARP) {
         griddep_wait();
         if (!P.stall) run_producer<C, false>(P, &tm_k, &tm_v, smem, B, abort_flag, lane);
-    } else if (warp == C::MERGER_WARP) {
-        prefetch_first_blocks<D, G, 1>(P, lane, 2 * C::STAGES);
+    } else if (warp >= C::MERGER_WARP) {
+        if (warp == C::MERGER_WARP) prefetch_first_blocks<D, G, 1>(P, lane, 2 * C::STAGES);
         griddep_wait();
-        run_merger<C>(P, smem, B, abort_flag, lane);
+        run_merger<C>(P, smem, B, abort_flag, lane, warp - C::MERGER_WARP);
     } else {
         prefetch_inputs<D, false>(P, threadIdx.x, C::W * 32);
         griddep_wait();  // consumers read the pools themselves
