@@ -82,7 +82,7 @@ __host__ __device__ constexpr uint32_t col_o(int u) { return static_cast<uint32_
 // a unit in the last place on average at each of a tile's 16 steps, always to
 // the same side: 2.5e-6 of the output's norm after 12 tiles, 3.5e-5 after 128.
 // Every kKeep tiles O is added, with rounding, to what was moved out before.
-constexpr int kKeep = 4;
+constexpr int kKeep = 3;
 constexpr float kThreshold = 3.0f, kShift = 12.0f;   // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -366,16 +366,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::mma_commit(&bar[B_SFULL + u]);
         };
-        // O_u += P_u V: key step k covers keys 16k .. 16k + 15, P's rounded
-        // values in columns [8k, 8k + 8) of the unit's S, the rest 64 on.
+        // O_u += P_u V: key step k covers keys 16k .. 16k + 15.  The first terms
+        // of 32 keys' P take the first 16 of the columns of their scores, the
+        // second terms the other 16.
         auto pv = [&](int u, int j) {
             const uint32_t svb = smem_addr(smem + OFF_V + (j & 1) * kTileBytes);
 #pragma unroll
             for (int k = 0; k < kTileN / 16; ++k) {
                 const uint64_t vdesc = tc::smem_desc_sw128(svb + k * 2048, kPanelBytes, 1024);
-                tc::mma_bf16_ts(tmem + col_o(u), tmem + col_s(u) + 64 + 8 * k, vdesc, kIdescPV,
-                                (j % kKeep > 0 || k > 0) ? 1u : 0u);
-                tc::mma_bf16_ts(tmem + col_o(u), tmem + col_s(u) + 8 * k, vdesc, kIdescPV, 1u);
+                const uint32_t p = tmem + col_s(u) + 32 * (k / 2) + 8 * (k % 2);
+                tc::mma_bf16_ts(tmem + col_o(u), p + 16, vdesc, kIdescPV, (j % kKeep > 0 || k > 0) ? 1u : 0u);
+                tc::mma_bf16_ts(tmem + col_o(u), p, vdesc, kIdescPV, 1u);
             }
             tc::mma_commit(&bar[B_ODONE + u]);
         };
@@ -578,35 +579,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kbase = j * kTileN;
                 const bool full = kbase + kTileN - 1 <= __shfl_sync(FULL, pos_a, 0);
                 const float4* sct = scales + (j & 3) * kBlocksPerTile;
-                uint32_t sr[64];  // groups 0-7, then 8-15
-                tc::tmem_ld16x256b_x8(tmem + tlane + col_s(u), *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                tc::tmem_ld16x256b_x8(tmem + tlane + col_s(u) + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-                tc::tmem_wait_ld();
-                // Pass 1: the exponents of P against the reference so far, in
-                // place of the scores, and each row's largest.
-                const float ra = kShift - mua, rb = kShift - mub;
-                float xa = -INFINITY, xb = -INFINITY;
+                // The scores are taken from tensor memory twice, 32 keys at a
+                // time and the next 32 on their way: held over both passes, 64
+                // a thread, they would push other values out of registers.
+                // Exponents of P against a reference, of 32 keys.
+                auto exponents = [&](int c, uint32_t (&sr)[16], float ra, float rb) {
 #pragma unroll
-                for (int b = 0; b < kBlocksPerTile; ++b) {
-                    const float4 sc = sct[b];
-                    const float2 pa = make_float2(fa * sc.x, fa * sc.x), pb = make_float2(fb * sc.x, fb * sc.x);
-                    const float2 ca = make_float2(sc.y + ra, sc.y + ra), cb = make_float2(sc.y + rb, sc.y + rb);
+                    for (int b = 0; b < 2; ++b) {
+                        const float4 sc = sct[2 * c + b];
+                        const float2 pa = make_float2(fa * sc.x, fa * sc.x), pb = make_float2(fb * sc.x, fb * sc.x);
+                        const float2 ca = make_float2(sc.y + ra, sc.y + ra), cb = make_float2(sc.y + rb, sc.y + rb);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t* s = &sr[4 * (2 * b + h)];
-                        float2 ya = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), pa, ca);
-                        float2 yb = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), pb, cb);
-                        if (!full) {  // keys past the row's position (NaN in unused slots included)
-                            const int key = kbase + 16 * b + 8 * h + 2 * tq;
-                            if (key > pos_a) ya.x = -INFINITY;
-                            if (key + 1 > pos_a) ya.y = -INFINITY;
-                            if (key > pos_b) yb.x = -INFINITY;
-                            if (key + 1 > pos_b) yb.y = -INFINITY;
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t* s = &sr[4 * (2 * b + h)];
+                            float2 ya = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), pa, ca);
+                            float2 yb = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), pb, cb);
+                            if (!full) {  // keys past the row's position (NaN in unused slots included)
+                                const int key = kbase + 32 * c + 16 * b + 8 * h + 2 * tq;
+                                if (key > pos_a) ya.x = -INFINITY;
+                                if (key + 1 > pos_a) ya.y = -INFINITY;
+                                if (key > pos_b) yb.x = -INFINITY;
+                                if (key + 1 > pos_b) yb.y = -INFINITY;
+                            }
+                            s[0] = __float_as_uint(ya.x), s[1] = __float_as_uint(ya.y);
+                            s[2] = __float_as_uint(yb.x), s[3] = __float_as_uint(yb.y);
                         }
-                        xa = fmax3(xa, ya.x, ya.y);
-                        xb = fmax3(xb, yb.x, yb.y);
-                        s[0] = __float_as_uint(ya.x), s[1] = __float_as_uint(ya.y);
-                        s[2] = __float_as_uint(yb.x), s[3] = __float_as_uint(yb.y);
+                    }
+                };
+                const uint32_t ts = tmem + tlane + col_s(u);
+                uint32_t sr[2][16];
+                // Pass 1: each row's largest exponent against the reference so
+                // far.
+                float xa = -INFINITY, xb = -INFINITY;
+                tc::tmem_ld16x256b_x4(ts, sr[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tc::tmem_wait_ld(sr[c & 1]);
+                    tc::tmem_ld16x256b_x4(ts + 32 * ((c + 1) & 3), sr[(c + 1) & 1]);  // at last, the first again
+                    exponents(c, sr[c & 1], kShift - mua, kShift - mub);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        xa = fmax3(xa, __uint_as_float(sr[c & 1][i]), __uint_as_float(sr[c & 1][i + 1]));
+                        xb = fmax3(xb, __uint_as_float(sr[c & 1][i + 2]), __uint_as_float(sr[c & 1][i + 3]));
                     }
                 }
                 xa = fmaxf(xa, __shfl_xor_sync(FULL, xa, 1));
@@ -628,27 +642,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         la *= alpha_a;
                         lb *= alpha_b;
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            sr[4 * i + c] = __float_as_uint(__uint_as_float(sr[4 * i + c]) - da);
-                            sr[4 * i + 2 + c] = __float_as_uint(__uint_as_float(sr[4 * i + 2 + c]) - db);
-                        }
-                    }
                 }
-                // Pass 2: P in two fp16 terms over the scores, its first 11 bits
-                // and the rest; the row sums without the V scales.
+                // Pass 2: P in two fp16 terms, its first 11 bits and the rest,
+                // over the 32 keys' scores; the row sums without the V scales.
 #pragma unroll
-                for (int qt = 0; qt < 4; ++qt) {
+                for (int c = 0; c < 4; ++c) {
+                    tc::tmem_wait_ld(sr[c & 1]);
+                    if (c < 3) tc::tmem_ld16x256b_x4(ts + 32 * (c + 1), sr[(c + 1) & 1]);
+                    exponents(c, sr[c & 1], kShift - mua, kShift - mub);
                     uint32_t hi[8], lo[8];
 #pragma unroll
-                    for (int b = 2 * qt; b < 2 * qt + 2; ++b) {
+                    for (int b = 0; b < 2; ++b) {
                         float2 ta = make_float2(0.f, 0.f), tb = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const uint32_t* s = &sr[4 * (2 * b + h)];
-                            const int at = 2 * (2 * (b - 2 * qt) + h);
+                            const uint32_t* s = &sr[c & 1][4 * (2 * b + h)];
+                            const int at = 2 * (2 * b + h);
                             const float2 pa = make_float2(fast_exp2(__uint_as_float(s[0])), fast_exp2(__uint_as_float(s[1])));
                             const float2 pb = make_float2(fast_exp2(__uint_as_float(s[2])), fast_exp2(__uint_as_float(s[3])));
                             ta = __fadd2_rn(ta, pa);
@@ -656,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             split2(pa, hi[at], lo[at]);
                             split2(pb, hi[at + 1], lo[at + 1]);
                         }
-                        const float inv = sct[b].z;
+                        const float inv = sct[2 * c + b].z;
                         la = fmaf(ta.x + ta.y, inv, la);
                         lb = fmaf(tb.x + tb.y, inv, lb);
                     }
-                    tc::tmem_st16x128b_x4(tmem + tlane + col_s(u) + 16 * qt, hi);
-                    tc::tmem_st16x128b_x4(tmem + tlane + col_s(u) + 64 + 16 * qt, lo);
+                    tc::tmem_st16x128b_x4(ts + 32 * c, hi);
+                    tc::tmem_st16x128b_x4(ts + 32 * c + 16, lo);
                 }
                 if (j > 0 && j % kKeep == 0) {
                     // The MMA warp starts O anew with this tile's P V.
