@@ -96,7 +96,8 @@ typedef enum pkv_status {
  * refuse them (PKV_ERR_DTYPE).
  * A scale that a call uses is in [2^-100, 2^122]; another one raises
  * PKV_ERR_RANGE on the device and counts as 2^-100.  No code of an int8 pool
- * is -128 after pkv_cache_append (if found, it counts as -128).
+ * is -128 after pkv_cache_append (if found, it counts as -128).  Attention over
+ * them needs num_blocks >= 1 and num_blocks * num_kv_heads < 2^31.
  */
 enum { PKV_KV_BF16 = 0, PKV_KV_E4M3 = 1, PKV_KV_E4M3_BLOCKS = 2, PKV_KV_INT8_BLOCKS = 3 };
 
@@ -166,8 +167,8 @@ pkv_status pkv_cache_write(const pkv_cache_t* cache, const void* k_new, const vo
  *   Values that are not finite do not count in amax.  An infinity is stored as
  *   the largest code of its sign, a NaN as the NaN code (e4m3) or 0 (int8),
  *   and either raises PKV_ERR_RANGE (detail: the sequence) once stored.
- *   A block must not be appended to by two sequences of a call (copy-on-write
- *   sees to that), nor be shared beyond its earlier rows' owner.
+ *   A block that the call appends to must belong to one sequence alone
+ *   (copy-on-write sees to that).
  *   PKV_ERR_RANGE on the device (detail: the sequence) for rows out of range,
  *   a context shorter than its rows or longer than the table, or a block id
  *   out of range: those rows are not stored.  num_tokens == 0 or num_seqs ==
@@ -441,8 +442,12 @@ size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t 
  *   |v| > 65504, or every |v| < 2^-12) is recomputed in the same launch in
  *   fp32 on CUDA cores, so every finite bf16 V is accepted (|v| up to about
  *   1e36, where fp32 sums of weighted rows overflow), at a lower speed for
- *   such tiles.  head_dim 64 or 128.  Takes bf16 pools only (an e4m3 pool:
- *   PKV_ERR_DTYPE).
+ *   such tiles.  head_dim 64 or 128.  An e4m3 pool with one scale gives
+ *   PKV_ERR_DTYPE.
+ *   PKV_KV_*_BLOCKS pools: as for pkv_decode_attention; query rows are off
+ *   by up to 1e-6 of their norm.  Where V holds a NaN code among a tile's keys,
+ *   the tile's rows are computed again on CUDA cores.  The call uses out as
+ *   scratch before it stores the rows there.
  */
 pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const void* q, int32_t num_q_heads,
                                          int32_t num_tokens, const int32_t* query_start_loc,

@@ -85,6 +85,12 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // Whether the pool has a scale for each (block, kv head).
 bool scaled(const pkv_cache_t* c) { return c->kv_dtype == PKV_KV_E4M3_BLOCKS || c->kv_dtype == PKV_KV_INT8_BLOCKS; }
 
+// Attention over such a pool counts slabs in 32 bits, and reads block 0 in the
+// place of an id that is out of range.
+bool slabs_fit(const pkv_cache_t* c) {
+    return c->num_blocks >= 1 && static_cast<int64_t>(c->num_blocks) * c->num_kv_heads <= INT32_MAX;
+}
+
 pkv_status check_cache(const pkv_cache_t* c) {
     if (c == nullptr || c->k_pool == nullptr || c->v_pool == nullptr) return PKV_ERR_NULL;
     if (c->block_size != 16) return PKV_ERR_BLOCKSIZE;
@@ -440,7 +446,7 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
                          const int32_t* query_start_loc, int32_t num_seqs, int32_t max_context_len, float scale,
                          float* out, void* workspace, size_t workspace_bytes, int32_t partition_blocks,
                          void* stream, const void* k_new = nullptr, const void* v_new = nullptr,
-                         const int32_t* slot_mapping = nullptr, int32_t shared_blocks = 0) {
+                         const int32_t* slot_mapping = nullptr, int32_t shared_blocks = 0, int32_t num_rows = -1) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
     if ((st = check_heads(num_q_heads, cache->num_kv_heads)) != PKV_OK) return st;
@@ -449,8 +455,7 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
     if (num_seqs == 0) return PKV_OK;
     if (q == nullptr || block_tables == nullptr || context_lens == nullptr || out == nullptr) return PKV_ERR_NULL;
     if (!aligned16(q) || !aligned16(out)) return PKV_ERR_ALIGN;
-    if (scaled(cache) && static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > INT32_MAX)
-        return PKV_ERR_SHAPE;  // slabs are counted in 32 bits
+    if (scaled(cache) && !slabs_fit(cache)) return PKV_ERR_SHAPE;
     DeviceState* dev = nullptr;
     if ((st = current_device(&dev)) != PKV_OK) return st;
     // out may be page-locked host memory: the kernel then writes the rows
@@ -486,6 +491,7 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
     a.num_q_heads = num_q_heads;
     a.head_dim = cache->head_dim;
     a.num_seqs = num_seqs;
+    a.num_rows = num_rows < 0 ? num_seqs : num_rows;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.max_context_len = max_context_len;
     a.plan = plan;
@@ -616,8 +622,7 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
         block_tables == nullptr || out == nullptr)
         return PKV_ERR_NULL;
     if (!aligned16(q) || !aligned16(out)) return PKV_ERR_ALIGN;
-    if (scaled(cache) && static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads > INT32_MAX)
-        return PKV_ERR_SHAPE;  // slabs are counted in 32 bits
+    if (scaled(cache) && !slabs_fit(cache)) return PKV_ERR_SHAPE;
     if (query_start_loc_host[0] != 0 || query_start_loc_host[num_seqs] != num_tokens) return PKV_ERR_SHAPE;
     int32_t tiles = 0, decode_rows = 0;
     for (int32_t s = 0; s < num_seqs; ++s) {
@@ -633,7 +638,8 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
     out = static_cast<float*>(const_cast<void*>(out_dev));
     if (decode_rows > 0) {
         st = decode_common(cache, q, num_q_heads, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
-                           num_seqs, max_context_len, scale, out, workspace, workspace_bytes, 0, stream);
+                           num_seqs, max_context_len, scale, out, workspace, workspace_bytes, 0, stream, nullptr,
+                           nullptr, nullptr, 0, num_tokens);
         if (st != PKV_OK) return st;
     }
     if (tiles > 0) {

@@ -163,6 +163,7 @@ struct DecodeParams {
     // Units a pair counts beyond its blocks in the cut of the work, for what
     // an item costs however short it is; they hold no keys.
     int32_t extra_units;
+    int32_t num_rows;  // of q and out
 };
 
 constexpr int align_up(int x, int a) { return (x + a - 1) / a * a; }
@@ -654,7 +655,11 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
             nparts = (b > P0 && b < P0 + u && min(down, up) > shift_max) ? 2 : 1;
         }
         const int rot = static_cast<int>(pos % C::W);
-        const int row = P.qsl ? __ldg(P.qsl + s) : s;
+        int row = P.qsl ? __ldg(P.qsl + s) : s;
+        if (row < 0 || row >= P.num_rows) {  // no row of the call: nothing is stored
+            record_error(P.err, kErrRange, static_cast<uint32_t>(s));
+            row = -1;
+        }
         const int32_t* trow = P.block_tables + static_cast<size_t>(s) * P.max_blocks;
         // First batch of table entries, requested before the descriptor work
         // (a lane's stage may hold two blocks: e and its odd one).
@@ -685,7 +690,7 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
             d.slot0 = 1;
             descs[slot] = d;
             mbar_arrive_expect_tx(&B.ifull[slot], C::QBYTES);
-            const uint8_t* qsrc = P.q + (static_cast<size_t>(row) * P.hq + static_cast<size_t>(g) * G) * D * 2;
+            const uint8_t* qsrc = P.q + (static_cast<size_t>(max(row, 0)) * P.hq + static_cast<size_t>(g) * G) * D * 2;
             bulk_g2s(smem + C::OFF_ITEMQ + slot * C::QBYTES, qsrc, C::QBYTES, &B.ifull[slot]);
         }
         __syncwarp();
@@ -704,10 +709,7 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
             // Two blocks a stage: stage i of the item holds blocks b0 + 2 i and
             // the next one, if the item has it, and goes to warp w = (i + rot)
             // % W, which issues the copies itself: lane k of a batch leaves
-            // the slabs and scales of one stage in w's ring of orders.  Issuing
-            // a stage's four tiled copies takes one thread about 740 cycles,
-            // two stages' share of HBM time, so one producer warp cannot
-            // (68 contexts of 40/40 x 128: 633 us; two of them 430).
+            // the slabs and scales of one stage in w's ring of orders.
             constexpr int kBatch = 32 < C::ORDERS / 2 * C::W ? 32 : C::ORDERS / 2 * C::W;
             Order* orders = reinterpret_cast<Order*>(smem + C::OFF_ORDERS);
             const int nst = (b1 - b0 + 1) / 2;
@@ -1411,7 +1413,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
 #pragma unroll
         for (int j = 0; j < (MCH + 31) / 32; ++j) {
             const int k = g0 * (D / 4) + lane + 32 * j;
-            if (lane + 32 * j < MCH) {
+            if (lane + 32 * j < MCH && (d.row >= 0 || d.nparts > 1)) {
                 const int g = k / (D / 4);
                 float4 v[W];
 #pragma unroll
@@ -1516,7 +1518,7 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
 #pragma unroll
                 for (int j = 0; j < NJ; ++j) {
                     const int c = lane + 32 * j;
-                    if (c < CH) {
+                    if (c < CH && d.row >= 0) {
                         out4[c] = finish_row<C>(acc[j], pick(L, c / (D / 4)), P.v_scale);
                     }
                 }
@@ -1805,6 +1807,7 @@ inline DecodeParams decode_params(const DecodeArgs& a, bool stall) {
     P.v_scale = 1.f;
     P.block_scales = reinterpret_cast<const float2*>(a.block_scales);
     P.extra_units = 0;
+    P.num_rows = a.num_rows;
     P.stall = stall ? 1 : 0;
     P.k_new = static_cast<const uint8_t*>(a.k_new);
     P.v_new = static_cast<const uint8_t*>(a.v_new);

@@ -9,19 +9,24 @@
 // scales only touch scores and weights, never the codes.
 //
 //  * A stage of the ring holds two blocks of one kv head (32 keys), K and V:
-//    four swizzled 16-row tiles and the two pairs of scales.  Twice the keys
-//    of a stage of the other pools: the maximum's shuffles, the wait and the
-//    hand-back are paid once for 32 keys, and the two blocks' chains of MMAs
-//    run side by side.
-//  * S = Q K^T (m16n8k16): rows 0-7 are the group's heads (the rest of the
-//    rows, and heads the group lacks, are zero), columns eight keys.  Lane
-//    (g, t) = (lane / 4, lane % 4) then holds head g's scores of keys 2t and
-//    2t + 1 of each tile: the layout of the A operand of P V, so P moves to no
-//    other lane, and a row's maximum takes two shuffles.
-//  * O += P V: an fp16 P would be off by 2^-11; the rows that the heads leave
-//    free carry the rest instead: rows 0-7 are P rounded to fp16, rows 8-15
-//    what the rounding lost, so P goes to 2^-22 in the same MMAs.  The two
-//    halves of O are added when the warp hands its state over.
+//    four swizzled 16-row tiles.  Twice the keys of a stage of the other pools:
+//    the maximum's shuffles, the wait and the hand-back are paid once for 32
+//    keys, and the two blocks' chains of MMAs run side by side (one block at a
+//    time, 68 contexts of 40/40 x 128: 467 us against 422).
+//  * The producer warp only leaves orders, slabs and scales of a stage; each
+//    consumer warp asks for its own stages as it frees them.  A stage is four
+//    tiled copies, which cost one issuing thread about 740 cycles, twice the
+//    stage's share of the HBM rate (one producer warp for all: 633 us).
+//  * S = K Q^T (m16n8k16): 16 keys by the group's heads (columns that the group
+//    lacks are zero).  Lane (g, t) = (lane / 4, lane % 4) gets keys g and g + 8
+//    for heads 2t and 2t + 1.  q is scaled per head by a power of two into
+//    fp16's upper range; the scores take the factor back.
+//  * O^T += V^T P^T, with P in two fp16 terms (rounded, and what the rounding
+//    lost: 2^-22, one term would be off by 2^-11), each an 8 x 8 transposition
+//    away from S's layout.  O^T's columns are S's heads, so a moved maximum
+//    rescales without a shuffle, and a lane holds D / 4 values of O (P V with
+//    the heads as rows holds twice that, which leaves room for 8 warps in place
+//    of 12: 412 us against 371).
 //  * Weights of a block carry its V scale, vs = f 2^e with f in [1, 2): the
 //    running maximum is that of s_j + e, u = 2^(s_j + e - m + 11), the weight
 //    u f and the term of the sum u 2^-e, so scales far apart lose nothing, and
@@ -30,6 +35,11 @@
 //    16-byte pieces of K rows and of V rows (8-byte pieces of V at head_dim
 //    64), and rows are dealt to lanes so that the lanes that read together hit
 //    different banks of the swizzled tiles (see key_row).
+//  * Bound: 68 contexts of 40/40 x 128 run at 0.89 of the measured copy rate.
+//    34 contexts of 640 tokens (16/8 x 128) stream their 45 MB in 6.2 us, 7.2
+//    TB/s; the other 9 are fixed: 3.3 us from the end of the launch before to
+//    the first order (lengths, cut, table, scales), 1.7 to the first stage, and
+//    about 3 for the merge.
 #pragma once
 
 #include "decode_kernel.cuh"
@@ -157,9 +167,8 @@ __device__ __forceinline__ uint32_t turned(uint32_t w) {
     return KIND == kKindInt8Blocks ? w ^ 0x80808080u : w;
 }
 
-// Unlike mma_f16 and lds128 free to be moved: the order of the products and of
-// the loads of a stage is the compiler's, so that chains run side by side (in
-// program order a stage takes three times as long).
+// Unlike mma_f16 and lds128 free to be moved: the order of a stage's products
+// and loads is the compiler's, so that chains run side by side.
 __device__ __forceinline__ void mma_free(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -356,59 +365,57 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
             const Order* order = orders + taken % C::ORDERS;
             const int blk = d.b0 + 2 * b;
             const int keys = min(2 * kBlockSize, (min(d.b1 * kBlockSize, d.n) - blk * kBlockSize));
-            {
-                constexpr int NB = C::BPS, i0 = 0;
-                const uint8_t* kst = ring + st * C::STAGE_BYTES + i0 * C::SLAB;
-                float u[NB][4];
-                BlockScales sc[NB];
-                int valid[NB];
-                float mb0 = -INFINITY, mb1 = -INFINITY;
+            constexpr int NB = C::BPS;
+            const uint8_t* kst = ring + st * C::STAGE_BYTES;
+            float u[NB][4];
+            BlockScales sc[NB];
+            int valid[NB];
+            float mb0 = -INFINITY, mb1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < NB; ++i) scores<D, KIND>(kst + i * C::SLAB, qb, u[i], at);
+            for (int i = 0; i < NB; ++i) scores<D, KIND>(kst + i * C::SLAB, qb, u[i], at);
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    valid[i] = min(max(keys - (i0 + i) * kBlockSize, 0), kBlockSize);
-                    sc[i] = order->scales[i0 + i];
-                    const float k0 = f0 * sc[i].k, k1 = f1 * sc[i].k;
-                    u[i][0] *= k0, u[i][1] *= k1, u[i][2] *= k0, u[i][3] *= k1;
-                    if (valid[i] < kBlockSize) {
-                        if (key_row<D>(g) >= valid[i]) u[i][0] = u[i][1] = -INFINITY;
-                        if (key_row<D>(g) + 8 >= valid[i]) u[i][2] = u[i][3] = -INFINITY;
-                    }
-                    mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]) + sc[i].e);
-                    mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]) + sc[i].e);
+            for (int i = 0; i < NB; ++i) {
+                valid[i] = min(max(keys - i * kBlockSize, 0), kBlockSize);
+                sc[i] = order->scales[i];
+                const float k0 = f0 * sc[i].k, k1 = f1 * sc[i].k;
+                u[i][0] *= k0, u[i][1] *= k1, u[i][2] *= k0, u[i][3] *= k1;
+                if (valid[i] < kBlockSize) {
+                    if (key_row<D>(g) >= valid[i]) u[i][0] = u[i][1] = -INFINITY;
+                    if (key_row<D>(g) + 8 >= valid[i]) u[i][2] = u[i][3] = -INFINITY;
                 }
+                mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]) + sc[i].e);
+                mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]) + sc[i].e);
+            }
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    mb0 = fmaxf(mb0, __shfl_xor_sync(FULL, mb0, off));
-                    mb1 = fmaxf(mb1, __shfl_xor_sync(FULL, mb1, off));
-                }
-                // A new reference only where the maximum grew by more than 2^3.
-                const bool moves0 = mb0 > m0 + kScaledThreshold, moves1 = mb1 > m1 + kScaledThreshold;
-                if (__any_sync(FULL, moves0 || moves1)) {
-                    const float a0 = moves0 ? fast_exp2(m0 - mb0) : 1.f, a1 = moves1 ? fast_exp2(m1 - mb1) : 1.f;
-                    m0 = moves0 ? mb0 : m0;
-                    m1 = moves1 ? mb1 : m1;
-                    l0 *= a0;
-                    l1 *= a1;
+            for (int off = 4; off < 32; off <<= 1) {
+                mb0 = fmaxf(mb0, __shfl_xor_sync(FULL, mb0, off));
+                mb1 = fmaxf(mb1, __shfl_xor_sync(FULL, mb1, off));
+            }
+            // A new reference only where the maximum grew by more than 2^3.
+            const bool moves0 = mb0 > m0 + kScaledThreshold, moves1 = mb1 > m1 + kScaledThreshold;
+            if (__any_sync(FULL, moves0 || moves1)) {
+                const float a0 = moves0 ? fast_exp2(m0 - mb0) : 1.f, a1 = moves1 ? fast_exp2(m1 - mb1) : 1.f;
+                m0 = moves0 ? mb0 : m0;
+                m1 = moves1 ? mb1 : m1;
+                l0 *= a0;
+                l1 *= a1;
 #pragma unroll
-                    for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
-                }
+                for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
+            }
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    if (NB > 1 && i > 0 && valid[i] == 0) break;
-                    const float add0 = sc[i].e + kScaledShift - m0, add1 = sc[i].e + kScaledShift - m1;
-                    u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
-                    u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
-                    l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);
-                    l1 = fmaf(u[i][1] + u[i][3], sc[i].inv_2e, l1);
-                    uint32_t p[4];
-                    split_pair_f16(u[i][0] * sc[i].f, u[i][1] * sc[i].f, p[0], p[1]);
-                    split_pair_f16(u[i][2] * sc[i].f, u[i][3] * sc[i].f, p[2], p[3]);
+            for (int i = 0; i < NB; ++i) {
+                if (i > 0 && valid[i] == 0) break;
+                const float add0 = sc[i].e + kScaledShift - m0, add1 = sc[i].e + kScaledShift - m1;
+                u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
+                u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
+                l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);
+                l1 = fmaf(u[i][1] + u[i][3], sc[i].inv_2e, l1);
+                uint32_t p[4];
+                split_pair_f16(u[i][0] * sc[i].f, u[i][1] * sc[i].f, p[0], p[1]);
+                split_pair_f16(u[i][2] * sc[i].f, u[i][3] * sc[i].f, p[2], p[3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) p[j] = transposed(p[j]);
-                    weigh<D, KIND>(kst + (2 + i) * C::SLAB, valid[i], p, o, at, t);
-                }
+                for (int j = 0; j < 4; ++j) p[j] = transposed(p[j]);
+                weigh<D, KIND>(kst + (2 + i) * C::SLAB, valid[i], p, o, at, t);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.oempty[warp * C::ORDERS + taken % C::ORDERS]);

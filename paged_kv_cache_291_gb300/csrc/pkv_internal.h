@@ -34,6 +34,7 @@ struct DecodeArgs {
     unsigned long long* err;       // device error word
     int32_t num_blocks, num_kv_heads, num_q_heads, head_dim;
     int32_t num_seqs, max_blocks_per_seq, max_context_len;
+    int32_t num_rows;              // of q and out
     DecodePlan plan;
     float scale;
     bool kv_e4m3;                  // pools hold e4m3 codes with one scale a pool

@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     if (warp == 0) {
         griddep_wait();
-        const PrefillTile tile = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.ctx_cap, P.units, P.split_last,
-                                                   blockIdx.x, blockIdx.y, P.err, lane);
+        const PrefillTile tile = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.num_tokens, P.ctx_cap,
+                                                   P.units, P.split_last, blockIdx.x, blockIdx.y, P.err, lane);
         if (lane == 0) {
             info[I_UNITS] = tile.units;
             info[I_H0] = tile.h0;

@@ -25,9 +25,9 @@
 //    the columns of the scores they replace; the row sum adds P / vs_b block by
 //    block.  m moves, and O is rescaled, when the maximum grows by more than 2^3:
 //    P stays below 2^15, and weights end 2^-36 below the largest.
-//  * A tile with a NaN code among its visible V (the append stores one for a
-//    NaN) is left out of the tensor cores' sums of earlier rows only by
-//    recomputing: such a CTA's rows are redone on CUDA cores.
+//  * A NaN code in V (the append stores one for a NaN) would reach, as 0 times
+//    NaN, the rows of its tile that do not see it: such a CTA's rows are done
+//    again on CUDA cores.
 //  * Every wait is bounded; tensor memory is freed on every exit path.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -96,7 +96,7 @@ struct Params {
     const int32_t* qsl;
     float* out;
     unsigned long long* err;
-    int32_t num_blocks, hkv, hq, num_seqs, max_blocks, ctx_cap, units, split_last;
+    int32_t num_blocks, hkv, hq, num_seqs, num_tokens, max_blocks, ctx_cap, units, split_last;
     float scale_log2;
 };
 
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     griddep_launch_dependents();
     if (warp == 0) {
         griddep_wait();
-        const PrefillTile t = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.ctx_cap, P.units, P.split_last,
-                                                blockIdx.x, blockIdx.y, P.err, lane);
+        const PrefillTile t = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.num_tokens, P.ctx_cap, P.units,
+                                                P.split_last, blockIdx.x, blockIdx.y, P.err, lane);
         if (lane == 0) {
             *info = t;
             *redo = 0;
@@ -818,6 +818,7 @@ cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
     P.hkv = a.num_kv_heads;
     P.hq = a.num_q_heads;
     P.num_seqs = a.num_seqs;
+    P.num_tokens = a.num_tokens;
     P.max_blocks = a.max_blocks_per_seq;
     P.ctx_cap = static_cast<int32_t>(
         std::min<int64_t>(a.max_context_len, static_cast<int64_t>(a.max_blocks_per_seq) * kBlockSize));

@@ -12,8 +12,8 @@ constexpr int kPrefillRows = 128;  // query rows of a CTA and q head
 
 // A CTA's share of a mixed batch: rows row0 .. row0 + rows - 1 of sequence s,
 // at positions pmin .. pmax, for `units` q heads from h0 on; nt key tiles of
-// 128, the last with klast visible keys.  bad: the sequence's arguments are
-// out of range (its rows are zero), or there is no such tile (s < 0).
+// 128, the last with klast visible keys.  bad: the sequence's context is out
+// of range (its rows are zero), or the call has no such tile or rows (s < 0).
 struct PrefillTile {
     int s, row0, rows, pmin, pmax, nt, klast, bad, units, h0;
 };
@@ -23,8 +23,8 @@ struct PrefillTile {
 // (ceil(qlen/128) tiles), and two for each of the last split_last tiles (one
 // per q head).
 __device__ __forceinline__ PrefillTile find_prefill_tile(const int32_t* qsl, const int32_t* context_lens,
-                                                         int num_seqs, int ctx_cap, int cta_units, int split_last,
-                                                         int tile, int pair, unsigned long long* err, int lane) {
+                                                         int num_seqs, int num_tokens, int ctx_cap,
+                                                         int cta_units, int split_last, int tile, int pair, unsigned long long* err, int lane) {
     const unsigned FULL = 0xffffffffu;
     const int split = cta_units == 2 ? split_last : 0;
     int base = 0, found = -1, e = 0, nt_s = 0;
@@ -72,6 +72,12 @@ __device__ __forceinline__ PrefillTile find_prefill_tile(const int32_t* qsl, con
     }
     const int q0 = __ldg(qsl + found);
     const int ql = __ldg(qsl + found + 1) - q0;
+    if (q0 < 0 || q0 > num_tokens - ql) {  // rows the call does not have
+        if (lane == 0) record_error(err, kErrRange, static_cast<uint32_t>(found));
+        r.s = -1;
+        r.bad = 1;
+        return r;
+    }
     const int ctx = __ldg(context_lens + found);
     if (ctx > ctx_cap || ql > ctx) {
         if (lane == 0) record_error(err, kErrRange, static_cast<uint32_t>(found));

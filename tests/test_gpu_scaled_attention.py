@@ -274,3 +274,118 @@ def test_a_serving_loop(pkv, kind, d):
         tol = attention_tolerance(exact, int(lens.max()), host[2][np.isfinite(host[2])])
         assert np.all(np.abs(got.double().cpu().numpy() - exact[0]) <= tol)
     assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("hkv,g,d", [(4, 1, 64), (2, 8, 128)])
+def test_decode_more_blocks_than_a_cut_of_equal_ranges_needs(pkv, kind, hkv, g, d):
+    """Enough work that short contexts count for more than their blocks (pairs then hold units without keys)."""
+    lens = [(i * 193) % 700 for i in range(150 * 4 // hkv)] + [9000, 1, 0, 16]
+    b = Batch(40, kind, [1] * len(lens), [n - 1 for n in lens], hkv, d)
+    q, qt = bf16_rows(b.rng, b.T, g * hkv, d)
+    got = decode(pkv, b, qt, d ** -0.5)
+    check(b, got, q, d ** -0.5)
+    assert torch.equal(got, decode(pkv, b, qt, d ** -0.5)) and pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_offsets_past_32_bits(pkv, kind):
+    """Pools of 4.3 GB, the contexts in blocks beyond 2^32 bytes."""
+    hkv, d = 40, 128
+    b = Batch(41, kind, [1, 20, 300], [100, 5, 40], hkv, d)
+    nb = 2 ** 32 // (hkv * 16 * d) + 64
+    k = torch.zeros((nb, hkv, 16, d), dtype=torch.int8 if kind == np.int8 else torch.uint8, device="cuda")
+    v, sc = torch.zeros_like(k), torch.ones((nb, hkv, 2), device="cuda")
+    ids = torch.arange(nb - b.nb, nb, device="cuda")
+    k[ids], v[ids], sc[ids] = (torch.from_numpy(x).cuda() for x in (b.k, b.v, b.scales))
+    q, qt = bf16_rows(b.rng, b.T, hkv, d)
+    _, _, _, start, lens, tables = b.dev()
+    got = pkv.chunked_prefill_attention(k, v, qt, start, lens, tables + (nb - b.nb), int(b.lens.max()), 0.1,
+                                        query_start_loc_host=b.start, block_scales=sc)
+    check(b, got, q, 0.1)
+    assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_calls_on_two_streams(pkv, kind):
+    """Two batches at once, each with a workspace of its own."""
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    todo = []
+    for i in range(2):
+        b = Batch(42 + i, kind, [1] * 9 + [150], [50 * n for n in range(9)] + [400], 2, 128)
+        q, qt = bf16_rows(b.rng, b.T, 4, 128)
+        todo.append((b, q, qt, b.dev(), torch.from_numpy(b.start)))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i, (b, _, qt, (k, v, sc, start, lens, tables), host) in enumerate(todo):
+            outs[i].append(pkv.chunked_prefill_attention(k, v, qt, start, lens, tables, int(b.lens.max()), 0.1,
+                                                         query_start_loc_host=host, block_scales=sc, stream=sides[i]))
+    torch.cuda.synchronize()
+    for (b, q, *_), got in zip(todo, outs):
+        check(b, got[0], q, 0.1)
+        assert all(torch.equal(got[0], x) for x in got[1:])
+    assert pkv.get_error()[0] == 0
+
+
+def test_rows_that_the_call_does_not_have(pkv):
+    """Device row starts that differ from the host's and leave the call's rows are reported; nothing is read or
+    written there, and the other sequences are right."""
+    for at, detail in (((3, 33), 2), ((1, 3), 1)):
+        b = Batch(44, np.int8, [1, 30, 1], [5, 9, 50], 1, 64)
+        q, qt = bf16_rows(b.rng, b.T, 2, 64)
+        k, v, sc, start, lens, tables = b.dev()
+        start[at[0]] = at[1]
+        if detail == 2:
+            start[2] = 32  # the last sequence's row is behind the rows
+        guard = torch.full((b.T + 8, 2, 64), 5.0, device="cuda")
+        got = pkv.chunked_prefill_attention(k, v, qt, start, lens, tables, int(b.lens.max()), 0.125, out=guard[:b.T],
+                                            query_start_loc_host=b.start, block_scales=sc)
+        if detail == 2:
+            assert pkv.get_error() == (9, 2)
+            exact = S.attention(b.k, b.v, b.scales, q, b.start, b.lens, b.tables, 0.125)[0]
+            assert np.abs(got[0].cpu().numpy() - exact[0]).max() < 1e-4
+        assert torch.all(guard[b.T:] == 5.0)
+        pkv.get_error()
+
+
+def test_an_expired_wait_is_reported_and_the_next_call_is_right(pkv):
+    b = Batch(45, np.uint8, [1] * 3, [39, 299, 1499], 2, 128)
+    q, qt = bf16_rows(b.rng, b.T, 4, 128)
+    ws = pkv.new_workspace(pkv.decode_workspace_size(3, 4, 2, 128, 1500))
+    out = torch.full((3, 4, 128), 7.0, device="cuda")
+    pkv.test_arm_decode_stall(1)
+    decode(pkv, b, qt, 0.1, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    status, detail = pkv.get_error()
+    assert status == 10 and detail in (2, 3)
+    assert torch.all(out == 7.0) and int(ws.count_nonzero()) == 0
+    check(b, decode(pkv, b, qt, 0.1, out=out, workspace=ws), q, 0.1)
+    assert pkv.get_error()[0] == 0
+
+
+def test_refusals_of_the_binding(pkv):
+    b = Batch(46, np.int8, [1, 3], [4, 5], 2, 64)
+    k, v, sc, start, lens, tables = b.dev()
+    _, q = bf16_rows(b.rng, 4, 4, 64)
+    args = dict(k_pool=k, v_pool=v, q=q[:2], block_tables=tables, context_lens=lens, max_context_len=8, scale=0.1,
+                block_scales=sc)
+    for bad in (dict(block_scales=sc[1:]), dict(block_scales=sc.double()), dict(q=q[:2].half()), dict(q=q[:2].float()),
+                dict(q=q[:2, :, :32]), dict(q=q[:2].transpose(0, 1)), dict(k_scale=1.0), dict(context_lens=lens[:1]),
+                dict(block_tables=tables[0]), dict(block_tables=tables.long()), dict(v_pool=v[1:]),
+                dict(v_pool=v.view(torch.uint8)), dict(out=torch.empty((2, 4, 64), dtype=torch.bfloat16, device="cuda")),
+                dict(out=torch.empty((3, 4, 64), device="cuda")), dict(out=torch.empty((2, 4, 64)))):
+        with pytest.raises((TypeError, ValueError)):
+            pkv.decode_attention(**(args | bad))
+    for bad in (dict(workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")), dict(max_context_len=-1)):
+        with pytest.raises(pkv.PKVError):
+            pkv.decode_attention(**(args | bad))
+    args = dict(k_pool=k, v_pool=v, q=q, query_start_loc=start, context_lens=lens, block_tables=tables,
+                max_context_len=8, scale=0.1, block_scales=sc)
+    for bad in (dict(query_start_loc=start[:2]), dict(query_start_loc_host=b.start[:2]), dict(q=q.half()),
+                dict(out=torch.empty((3, 4, 64), device="cuda")), dict(context_lens=lens.long())):
+        with pytest.raises((TypeError, ValueError)):
+            pkv.chunked_prefill_attention(**(args | bad))
+    with pytest.raises(pkv.PKVError):
+        pkv.chunked_prefill_attention(**(args | dict(query_start_loc_host=b.start + 1)))
+    assert pkv.get_error()[0] == 0

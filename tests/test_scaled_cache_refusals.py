@@ -113,6 +113,9 @@ def test_chunked_prefill_still_refuses_a_pool_with_one_scale(lib):
 def test_attention_heads_and_descriptor(lib):
     def decode(c, hq):
         return lib.pkv_decode_attention(ctypes.byref(c), MB, hq, 2 * MB, 3, 3 * MB, 0, 40, 1.0, 4 * MB, None, 0, 0, None)
+    def decode_some(c):
+        return lib.pkv_decode_attention(ctypes.byref(c), MB, 4, 2 * MB, 3, 3 * MB, 2, 40, 1.0, 4 * MB, None, 0, 0, None)
+    assert decode_some(cache(num_blocks=0)) == SHAPE and decode_some(cache(num_blocks=2 ** 31 - 1)) == SHAPE
     assert decode(cache(), 4) == 0 and decode(cache(), 6) == HEADS and decode(cache(block_scales=None), 4) == NULL
 
 
