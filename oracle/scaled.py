@@ -129,6 +129,6 @@ def attention(k_pool, v_pool, scales, q, start, context_lens, tables, scale):
                 w = np.exp(x - x.max())
                 w /= w.sum()
                 out[t, h], size[t, h] = w @ V[:m, g], w @ np.abs(V[:m, g])
-                terms[t, h] = scale * np.max(np.abs(K[:m, g]) @ np.abs(q[t, h]))
+                terms[t, h] = abs(scale) * np.max(np.abs(K[:m, g]) @ np.abs(q[t, h]))
                 peak[t, h] = np.max(w * sc[:m, g, 1]) * largest(v_pool)
     return out, size, terms, peak

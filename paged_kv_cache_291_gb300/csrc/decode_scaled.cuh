@@ -378,13 +378,14 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
                 valid[i] = min(max(keys - i * kBlockSize, 0), kBlockSize);
                 sc[i] = order->scales[i];
                 const float k0 = f0 * sc[i].k, k1 = f1 * sc[i].k;
-                u[i][0] *= k0, u[i][1] *= k1, u[i][2] *= k0, u[i][3] *= k1;
+                u[i][0] = fmaf(u[i][0], k0, sc[i].e), u[i][1] = fmaf(u[i][1], k1, sc[i].e);
+                u[i][2] = fmaf(u[i][2], k0, sc[i].e), u[i][3] = fmaf(u[i][3], k1, sc[i].e);
                 if (valid[i] < kBlockSize) {
                     if (key_row<D>(g) >= valid[i]) u[i][0] = u[i][1] = -INFINITY;
                     if (key_row<D>(g) + 8 >= valid[i]) u[i][2] = u[i][3] = -INFINITY;
                 }
-                mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]) + sc[i].e);
-                mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]) + sc[i].e);
+                mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]));
+                mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]));
             }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
@@ -392,7 +393,9 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
                 mb1 = fmaxf(mb1, __shfl_xor_sync(FULL, mb1, off));
             }
             // A new reference only where the maximum grew by more than 2^3.
-            const bool moves0 = mb0 > m0 + kScaledThreshold, moves1 = mb1 > m1 + kScaledThreshold;
+            // Rounded down, here and below, P stays below 2^16 however large the
+            // scores (past 2^20 or so these sums are no longer exact).
+            const bool moves0 = mb0 > __fadd_rd(m0, kScaledThreshold), moves1 = mb1 > __fadd_rd(m1, kScaledThreshold);
             if (__any_sync(FULL, moves0 || moves1)) {
                 const float a0 = moves0 ? fast_exp2(m0 - mb0) : 1.f, a1 = moves1 ? fast_exp2(m1 - mb1) : 1.f;
                 m0 = moves0 ? mb0 : m0;
@@ -402,10 +405,10 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
             }
+            const float add0 = __fsub_rd(kScaledShift, m0), add1 = __fsub_rd(kScaledShift, m1);
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 if (i > 0 && valid[i] == 0) break;
-                const float add0 = sc[i].e + kScaledShift - m0, add1 = sc[i].e + kScaledShift - m1;
                 u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
                 u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
                 l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);

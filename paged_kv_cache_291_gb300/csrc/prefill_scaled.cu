@@ -29,6 +29,7 @@
 //    NaN, the rows of its tile that do not see it: such a CTA's rows are done
 //    again on CUDA cores.
 //  * Every wait is bounded; tensor memory is freed on every exit path.
+#include <cfloat>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -58,8 +59,9 @@ constexpr int OFF_K = OFF_Q + kUnits * kTileBytes;   // 2 widened K tiles
 constexpr int OFF_V = OFF_K + 2 * kTileBytes;        // 2 widened V tiles
 constexpr int OFF_KC = OFF_V + 2 * kTileBytes;       // codes of one K tile
 constexpr int OFF_VC = OFF_KC + kCodeBytes;          // codes of one V tile
-constexpr int OFF_SCALES = OFF_VC + kCodeBytes;      // [4 tiles][8 blocks] (K scale, log2 of V's, 1 / V's, 0)
-constexpr int OFF_ROWF = OFF_SCALES + 4 * kBlocksPerTile * 16;  // [kUnits][128] factor of a row's scores
+constexpr int kScaleTiles = 3;                       // tiles whose scales are kept
+constexpr int OFF_SCALES = OFF_VC + kCodeBytes;      // [kScaleTiles][8 blocks] TileScales
+constexpr int OFF_ROWF = OFF_SCALES + kScaleTiles * kBlocksPerTile * 24;  // [kUnits][128] factor of a row's scores
 constexpr int OFF_BAR = OFF_ROWF + kUnits * kTileM * 4;
 constexpr int NBAR = 20;
 constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
@@ -98,6 +100,13 @@ struct Params {
     unsigned long long* err;
     int32_t num_blocks, hkv, hq, num_seqs, num_tokens, max_blocks, ctx_cap, units, split_last;
     float scale_log2;
+};
+
+// A block's scales as the softmax takes them, V's twice: operands of packed
+// arithmetic.
+struct __align__(8) TileScales {
+    float2 log2_v, inv_v;
+    float k, unused;
 };
 
 enum {
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     static_assert(sizeof(PrefillTile) + 4 <= 12 * 4, "info");
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     float* rowf = reinterpret_cast<float*>(smem + OFF_ROWF);
-    float4* scales = reinterpret_cast<float4*>(smem + OFF_SCALES);
+    TileScales* scales = reinterpret_cast<TileScales*>(smem + OFF_SCALES);
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
     const unsigned FULL = 0xffffffffu;
@@ -313,19 +322,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A tile's table entries and scales are looked up while the tile
         // before it is on its way.
         int slab = 0;
-        float4 sc = make_float4(1.f, 0.f, 1.f, 0.f);
+        float ks = 1.f, log2_v = 0.f, inv_v = 1.f;
         auto look_up = [&](int j) {
-            sc = make_float4(1.f, 0.f, 1.f, 0.f);
+            ks = 1.f, log2_v = 0.f, inv_v = 1.f;
             if (lane < min(kBlocksPerTile, nblk - j * kBlocksPerTile)) {
                 int e = __ldg(trow + j * kBlocksPerTile + lane);
                 bool bad = e < 0 || e >= P.num_blocks;
                 if (bad) e = 0;  // never dereference an invalid id
                 slab = e * P.hkv + g;
                 const float2 s = __ldg(P.scales + slab);
-                sc.x = checked_scale(s.x, bad);
+                ks = checked_scale(s.x, bad);
                 const float vs = checked_scale(s.y, bad);
-                sc.y = log2f(vs);
-                sc.z = 1.f / vs;
+                log2_v = log2f(vs);
+                inv_v = 1.f / vs;
                 if (bad) record_error(P.err, kErrRange, static_cast<uint32_t>(T.s));
             }
         };
@@ -335,9 +344,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bytes = static_cast<uint32_t>(nvb) * kBlockSize * D;
             const int now = slab;
             if (!mbar_wait_warp(&bar[B_KCEMPTY], (j & 1) ^ 1)) { ok = false; break; }
-            // The tile four before this one has been through its softmax:
+            // The tile three before this one has been through its softmax:
             // every warp widened the last K tile after that.
-            if (lane < kBlocksPerTile) scales[(j & 3) * kBlocksPerTile + lane] = sc;
+            if (lane < kBlocksPerTile)
+                scales[j % kScaleTiles * kBlocksPerTile + lane] = {
+                    make_float2(log2_v, log2_v), make_float2(inv_v, inv_v), ks, 0.f};
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&bar[B_KCFULL], bytes);
             __syncwarp();
@@ -469,7 +480,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
                 int e = 0;
                 if (mx < INFINITY) e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
-                const float down = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+                // The scale's sign goes with q, so that the scores' factor is
+                // not negative.
+                const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23), P.scale_log2);
                 if (mine) {
 #pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
@@ -483,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (pn == 0)
                     rowf[u * kTileM + row] =
-                        P.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+                        fabsf(P.scale_log2) * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
                 tc::fence_proxy_async_smem();
             }
         }
@@ -511,7 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = ok && mbar_wait_warp(&bar[B_QCONV], 0);
             const float fa = rowf[u * kTileM + ma], fb = rowf[u * kTileM + mb];
             // References of P, and of what was moved out of tensor memory.
-            float mua = 0.f, mub = 0.f, mfa = 0.f, mfb = 0.f, la = 0.f, lb = 0.f;
+            float mua = 0.f, mub = 0.f, mfa = 0.f, mfb = 0.f;
+            float2 la = make_float2(0.f, 0.f), lb = la;  // row sums, even and odd columns
             // Where rows start in out, worked out when wanted: held over the
             // tiles they would cost the scores their registers.
             const volatile PrefillTile* where = info;
@@ -578,49 +592,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after_sync();
                 const int kbase = j * kTileN;
                 const bool full = kbase + kTileN - 1 <= __shfl_sync(FULL, pos_a, 0);
-                const float4* sct = scales + (j & 3) * kBlocksPerTile;
+                const TileScales* sct = scales + j % kScaleTiles * kBlocksPerTile;
                 // The scores are taken from tensor memory twice, 32 keys at a
                 // time and the next 32 on their way: held over both passes, 64
                 // a thread, they would push other values out of registers.
-                // Exponents of P against a reference, of 32 keys.
-                auto exponents = [&](int c, uint32_t (&sr)[16], float ra, float rb) {
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float4 sc = sct[2 * c + b];
-                        const float2 pa = make_float2(fa * sc.x, fa * sc.x), pb = make_float2(fb * sc.x, fb * sc.x);
-                        const float2 ca = make_float2(sc.y + ra, sc.y + ra), cb = make_float2(sc.y + rb, sc.y + rb);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t* s = &sr[4 * (2 * b + h)];
-                            float2 ya = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), pa, ca);
-                            float2 yb = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), pb, cb);
-                            if (!full) {  // keys past the row's position (NaN in unused slots included)
-                                const int key = kbase + 32 * c + 16 * b + 8 * h + 2 * tq;
-                                if (key > pos_a) ya.x = -INFINITY;
-                                if (key + 1 > pos_a) ya.y = -INFINITY;
-                                if (key > pos_b) yb.x = -INFINITY;
-                                if (key + 1 > pos_b) yb.y = -INFINITY;
-                            }
-                            s[0] = __float_as_uint(ya.x), s[1] = __float_as_uint(ya.y);
-                            s[2] = __float_as_uint(yb.x), s[3] = __float_as_uint(yb.y);
-                        }
-                    }
-                };
                 const uint32_t ts = tmem + tlane + col_s(u);
                 uint32_t sr[2][16];
-                // Pass 1: each row's largest exponent against the reference so
-                // far.
+                // Keys past the row's position (NaN in unused slots included)
+                // out of 32 keys' scores.
+                auto mask = [&](int c, uint32_t (&s)[16]) {
+                    if (full) return;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (kbase + 32 * c + 8 * (i / 4) + 2 * tq + (i & 1) > (i & 2 ? pos_b : pos_a)) s[i] = 0xff800000u;
+                };
+                // A block's factor of a row's scores, never so small that it
+                // would turn what was masked into a NaN.
+                auto factor = [](float f, float ks) { return fmaxf(f * ks, FLT_MIN); };
+                // Pass 1: each row's largest y = s factor + log2 vs, block by
+                // block.
                 float xa = -INFINITY, xb = -INFINITY;
                 tc::tmem_ld16x256b_x4(ts, sr[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tc::tmem_wait_ld(sr[c & 1]);
                     tc::tmem_ld16x256b_x4(ts + 32 * ((c + 1) & 3), sr[(c + 1) & 1]);  // at last, the first again
-                    exponents(c, sr[c & 1], kShift - mua, kShift - mub);
+                    mask(c, sr[c & 1]);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        xa = fmax3(xa, __uint_as_float(sr[c & 1][i]), __uint_as_float(sr[c & 1][i + 1]));
-                        xb = fmax3(xb, __uint_as_float(sr[c & 1][i + 2]), __uint_as_float(sr[c & 1][i + 3]));
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t* s = &sr[c & 1][8 * b];
+                        const float ks = sct[2 * c + b].k, lv = sct[2 * c + b].log2_v.x;
+                        float va = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+                        float vb = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
+                        va = fmax3(va, __uint_as_float(s[4]), __uint_as_float(s[5]));
+                        vb = fmax3(vb, __uint_as_float(s[6]), __uint_as_float(s[7]));
+                        xa = fmaxf(xa, fmaf(va, factor(fa, ks), lv));
+                        xb = fmaxf(xb, fmaf(vb, factor(fb, ks), lv));
                     }
                 }
                 xa = fmaxf(xa, __shfl_xor_sync(FULL, xa, 1));
@@ -628,46 +635,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                 xa = fmaxf(xa, __shfl_xor_sync(FULL, xa, 2));
                 xb = fmaxf(xb, __shfl_xor_sync(FULL, xb, 2));
                 // The reference moves in the first tile, and where the largest
-                // passed it by more than 2^3.
+                // passed it by more than 2^3.  Rounded down, here and below, P
+                // stays below 2^16 however large the scores (past 2^20 or so
+                // the sums below are no longer exact).
                 float alpha_a = 1.f, alpha_b = 1.f;
-                const bool need_a = j == 0 || xa > kShift + kThreshold, need_b = j == 0 || xb > kShift + kThreshold;
+                const bool need_a = j == 0 || xa > __fadd_rd(mua, kThreshold);
+                const bool need_b = j == 0 || xb > __fadd_rd(mub, kThreshold);
                 const bool moves = __any_sync(FULL, need_a || need_b);
                 if (moves) {
-                    const float da = need_a ? xa - kShift : 0.f, db = need_b ? xb - kShift : 0.f;
-                    mua += da;
-                    mub += db;
-                    alpha_a = fast_exp2(-da);
-                    alpha_b = fast_exp2(-db);
+                    if (need_a) {
+                        alpha_a = fast_exp2(mua - xa);
+                        mua = xa;
+                    }
+                    if (need_b) {
+                        alpha_b = fast_exp2(mub - xb);
+                        mub = xb;
+                    }
                     if (j > 0) {
-                        la *= alpha_a;
-                        lb *= alpha_b;
+                        la = __fmul2_rn(la, make_float2(alpha_a, alpha_a));
+                        lb = __fmul2_rn(lb, make_float2(alpha_b, alpha_b));
+                    } else {
+                        mfa = mua;
+                        mfb = mub;
                     }
                 }
                 // Pass 2: P in two fp16 terms, its first 11 bits and the rest,
                 // over the 32 keys' scores; the row sums without the V scales.
+                const float sha = __fsub_rd(kShift, mua), shb = __fsub_rd(kShift, mub);
+                const float2 ra = make_float2(sha, sha), rb = make_float2(shb, shb);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tc::tmem_wait_ld(sr[c & 1]);
                     if (c < 3) tc::tmem_ld16x256b_x4(ts + 32 * (c + 1), sr[(c + 1) & 1]);
-                    exponents(c, sr[c & 1], kShift - mua, kShift - mub);
+                    mask(c, sr[c & 1]);
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        float2 ta = make_float2(0.f, 0.f), tb = make_float2(0.f, 0.f);
+                        const TileScales& sc = sct[2 * c + b];
+                        const float ka = factor(fa, sc.k), kb = factor(fb, sc.k);
+                        const float2 pa = make_float2(ka, ka), pb = make_float2(kb, kb);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t* s = &sr[c & 1][4 * (2 * b + h)];
                             const int at = 2 * (2 * b + h);
-                            const float2 pa = make_float2(fast_exp2(__uint_as_float(s[0])), fast_exp2(__uint_as_float(s[1])));
-                            const float2 pb = make_float2(fast_exp2(__uint_as_float(s[2])), fast_exp2(__uint_as_float(s[3])));
-                            ta = __fadd2_rn(ta, pa);
-                            tb = __fadd2_rn(tb, pb);
-                            split2(pa, hi[at], lo[at]);
-                            split2(pb, hi[at + 1], lo[at + 1]);
+                            float2 ya = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), pa, sc.log2_v);
+                            float2 yb = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), pb, sc.log2_v);
+                            ya = __fadd2_rn(ya, ra);
+                            yb = __fadd2_rn(yb, rb);
+                            ya = make_float2(fast_exp2(ya.x), fast_exp2(ya.y));
+                            yb = make_float2(fast_exp2(yb.x), fast_exp2(yb.y));
+                            la = __ffma2_rn(ya, sc.inv_v, la);
+                            lb = __ffma2_rn(yb, sc.inv_v, lb);
+                            split2(ya, hi[at], lo[at]);
+                            split2(yb, hi[at + 1], lo[at + 1]);
                         }
-                        const float inv = sct[2 * c + b].z;
-                        la = fmaf(ta.x + ta.y, inv, la);
-                        lb = fmaf(tb.x + tb.y, inv, lb);
                     }
                     tc::tmem_st16x128b_x4(ts + 32 * c, hi);
                     tc::tmem_st16x128b_x4(ts + 32 * c + 16, lo);
@@ -721,11 +742,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && !mbar_wait_warp(&bar[B_ODONE + u], (nt - 1) & 1)) ok = false;
             if (ok) {
                 tc::fence_after_sync();
-                la += __shfl_xor_sync(FULL, la, 1);
-                lb += __shfl_xor_sync(FULL, lb, 1);
-                la += __shfl_xor_sync(FULL, la, 2);
-                lb += __shfl_xor_sync(FULL, lb, 2);
-                const float inva = 1.f / la, invb = 1.f / lb;
+                float sa = la.x + la.y, sb = lb.x + lb.y;
+                sa += __shfl_xor_sync(FULL, sa, 1);
+                sb += __shfl_xor_sync(FULL, sb, 1);
+                sa += __shfl_xor_sync(FULL, sa, 2);
+                sb += __shfl_xor_sync(FULL, sb, 2);
+                const float inva = 1.f / sa, invb = 1.f / sb;
                 const float fac_a = fast_exp2(mfa - mua), fac_b = fast_exp2(mfb - mub);
                 auto kept_or_zero = [&](int c, float (&x)[32]) {
                     if (nt > kKeep) {

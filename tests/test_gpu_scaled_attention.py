@@ -132,6 +132,59 @@ def test_a_large_weight_far_back(pkv, kind):
     assert pkv.get_error()[0] == 0
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.1, 1.0), (0.1, 2.0 ** -120), (2.0 ** -100, 2.0 ** -100), (-0.0, 1.0)])
+def test_factors_of_any_sign_and_size(pkv, kind, d, scale, size):
+    """Weights that are all equal, a negative scale, q rows that vanish: what is masked stays out."""
+    b = Batch(8, kind, [70, 1, 1], [35, 0, 400], 2, d)
+    q, qt = bf16_rows(b.rng, b.T, 4, d, size=size)
+    check(b, prefill(pkv, b, qt, scale), q, scale)
+    one = Batch(9, kind, [1] * 5, [5, 0, 33, 700, 47], 2, d)
+    q, qt = bf16_rows(one.rng, one.T, 4, d, size=size)
+    check(one, decode(pkv, one, qt, scale), q, scale)
+    assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [8, 13, 14, 15, 16, 17, 18, 20, 24, 40, 100])
+def test_scores_of_any_size(pkv, kind, sign, power):
+    """One key far above the rest (scores of 40 and 96, or -96 and -40, times 2^power): its V row comes out.
+
+    The others' weights are at most e^(-56 * 2^8) = 0 of it; its own weight
+    cancels but for its two fp16 terms (2^-22), the products and sums with
+    others' zeros lose nothing, and the quotient's roundings (V's scale, its
+    reciprocal and log2, sum, inverse, product) are below 2^-20."""
+    high, low = (96, 40) if sign > 0 else (40, 96)
+    for place in (0, 150, 329):
+        b = Batch(place, kind, [40, 1], [290, 329], 1, 128, spread=0.5)
+        b.scales[..., 0] = 1
+        for s in range(2):
+            for j in range(330):
+                b.k[b.tables[s, j // 16], 0, j % 16] = 0
+                row = np.array([high if j == place else low], np.float32)
+                b.k[b.tables[s, j // 16], 0, j % 16, :1] = S.encode(row, b.k)
+        q = np.zeros((41, 2, 128), np.float32)
+        q[..., 0] = sign * 2.0 ** power
+        block = b.tables[:, place // 16]
+        rows = S.values(b.v[block, 0, place % 16]).astype(np.float64) * b.scales[block, 0, 1:].astype(np.float64)
+        sees = np.array([[j >= place] for j in range(290, 330)])
+        got = prefill(pkv, b, torch.from_numpy(q).bfloat16().cuda(), 1.0).double().cpu().numpy()
+        for s, part in enumerate((got[:40], got[40:])):
+            want = np.broadcast_to(rows[s], part.shape)
+            ok = np.abs(part - want) <= 2.0 ** -19 * np.abs(want)
+            if s == 0:
+                ok |= ~sees[..., None]
+            assert ok.all()
+        k, v, sc, _, lens, tables = b.dev()
+        one = torch.from_numpy(q[:2]).bfloat16().cuda()
+        got = pkv.decode_attention(k, v, one, tables, lens, 330, 1.0, block_scales=sc).double().cpu().numpy()
+        want = np.broadcast_to(rows[:, None], got.shape)
+        assert np.all(np.abs(got - want) <= 2.0 ** -19 * np.abs(want))
+    assert pkv.get_error()[0] == 0
+
+
 def test_e4m3_nan_codes_inside_a_context(pkv):
     """A NaN code in K or V of a visible row reaches the heads that read it, and no others."""
     for which in (0, 1):
