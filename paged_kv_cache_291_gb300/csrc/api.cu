@@ -826,7 +826,7 @@ PKV_API pkv_status pkv_cache_append(const pkv_cache_t* cache, const void* k_new,
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.err = dev->err;
-    cudaError_t e = pkv::launch_cache_append(a, static_cast<cudaStream_t>(stream));
+    cudaError_t e = pkv::launch_cache_append(a, dev->num_sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 

@@ -132,7 +132,7 @@ struct CacheRowsArgs {
     float k_scale, v_scale;           // pools with one scale
 };
 
-cudaError_t launch_cache_append(const CacheRowsArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_append(const CacheRowsArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRowsArgs& a, cudaStream_t stream);
 
 // Copy `chunks` 16-byte chunks from src to dst (device addresses) with a

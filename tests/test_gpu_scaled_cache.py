@@ -104,6 +104,29 @@ def test_append_values_that_are_not_finite(pkv, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_append_infinities_under_a_large_scale(pkv, kind):
+    """An infinity is the largest code even where the block's scale passes the largest bf16 by far."""
+    b = Batch(8, kind, [2, 1], [5, 0], 2, 64, empty=True)
+    b.scales[b.tables[0, 0]] = 2.0 ** 122
+    x, _ = bf16_rows(np.random.default_rng(14), 3, 2, 64)
+    x[0, 0, 3], x[1, 1, 60], x[2, 1, 7] = np.inf, -np.inf, np.inf
+    t = torch.from_numpy(x).bfloat16().cuda()
+    append_and_check(pkv, b, x, -x, t, -t)
+    assert pkv.get_error()[0] == 9
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_products_next_to_ties(pkv, kind):
+    """Codes of x (1 / scale) as fp32 rounds that product, over many scales."""
+    b = Batch(9, kind, [1600], [0], 4, 128, empty=True)
+    rng = np.random.default_rng(15)
+    kn, kt = bf16_rows(rng, 1600, 4, 128, size=1.0 + np.arange(1600)[:, None, None] / 16)
+    vn, vt = bf16_rows(rng, 1600, 4, 128)
+    append_and_check(pkv, b, kn, vn, kt, vt)
+    assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_append_bad_sequences(pkv, kind):
     """Sequences and blocks out of range store nothing and are reported; the others are stored."""
     for spoil, detail in ((lambda b: b.lens.__setitem__(1, 2), 1), (lambda b: b.lens.__setitem__(1, 16 * 9 + 1), 1),
