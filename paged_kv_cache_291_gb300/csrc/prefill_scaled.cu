@@ -28,6 +28,14 @@
 //  * A NaN code in V (the append stores one for a NaN) would reach, as 0 times
 //    NaN, the rows of its tile that do not see it: such a CTA's rows are done
 //    again on CUDA cores.
+//  * Measured: 2,048 of 16,384 tokens, 16/8 x 128, 454 us, 568 TFLOP/s (the two
+//    terms of P make it 850 of the tensor cores' work); 300 tokens, 32/8 x 64,
+//    12.6 us.  A tile of two heads takes some 7,000 cycles, 3,300 of MMAs; issue
+//    slots are 48 % busy, the ALU 39 %: what bounds it is each warp's chain
+//    through a tile, wait, scores, shuffles, exponentials, stores, with four
+//    warps on a scheduler.  Steps of 64 keys with two sets of scores, the MMAs
+//    of one beside the softmax of the other, pay that chain's fixed part twice:
+//    558 us (300 tokens: 11.2).
 //  * Every wait is bounded; tensor memory is freed on every exit path.
 #include <cfloat>
 #include <cuda.h>
