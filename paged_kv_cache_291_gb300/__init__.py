@@ -316,6 +316,8 @@ def cache_write(k_pool, v_pool, k_new, v_new, slot_mapping, stream=None, k_scale
 def _cache_rows(k_pool, v_pool, query_start_loc, context_lens, block_tables, k_scale, v_scale, block_scales, dev):
     """Descriptor and index arguments of cache_append and cache_read."""
     i32 = _torch().int32
+    if block_scales is None and k_pool.dtype == _torch().int8:
+        raise TypeError("an int8 pool needs block_scales")
     c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True, block_scales=block_scales)
     if k_pool.get_device() != dev or v_pool.get_device() != dev:
         raise ValueError(f"the pools are on {k_pool.device} and {v_pool.device}, the current device is cuda:{dev}")

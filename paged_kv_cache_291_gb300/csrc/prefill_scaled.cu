@@ -489,8 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int e = 0;
                 if (mx < INFINITY) e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
                 // The scale's sign goes with q, so that the scores' factor is
-                // not negative.
-                const float down = copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23), P.scale_log2);
+                // not negative, and so does a NaN, which that factor would lose.
+                const float down = isnan(P.scale_log2) ? P.scale_log2
+                                                       : copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23),
+                                                                   P.scale_log2);
                 if (mine) {
 #pragma unroll 2
                     for (int c = 0; c < 8; ++c) {

@@ -147,6 +147,28 @@ def test_factors_of_any_sign_and_size(pkv, kind, d, scale, size):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_a_scale_or_rows_of_nan(pkv, kind):
+    """NaN in every row that it reaches, and in no other."""
+    b = Batch(11, kind, [150, 1], [10, 400], 2, 64)
+    q, qt = bf16_rows(b.rng, b.T, 4, 64)
+    assert prefill(pkv, b, qt, float("nan")).isnan().all()
+    for spoil in (float("nan"), float("inf")):
+        qn = qt.clone()
+        qn[70, 1, 5] = qn[150, 3, 60] = spoil
+        got = prefill(pkv, b, qn, 0.1)
+        nan = torch.zeros_like(got, dtype=torch.bool)
+        nan[70, 1] = nan[150, 3] = True
+        assert torch.equal(got.isnan(), nan)
+    one = Batch(12, kind, [1] * 2, [30, 500], 2, 64)
+    q, qt = bf16_rows(one.rng, 2, 4, 64)
+    assert decode(pkv, one, qt, float("nan")).isnan().all()
+    qt[1, 2, 7] = float("nan")
+    got = decode(pkv, one, qt, 0.1).isnan()
+    assert got[1, 2].all() and int(got.sum()) == 64
+    assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("power", [8, 13, 14, 15, 16, 17, 18, 20, 24, 40, 100])
 def test_scores_of_any_size(pkv, kind, sign, power):
@@ -379,6 +401,26 @@ def test_calls_on_two_streams(pkv, kind):
         check(b, got[0], q, 0.1)
         assert all(torch.equal(got[0], x) for x in got[1:])
     assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_into_page_locked_host_memory(pkv, kind, d):
+    """A page-locked out gets the same bits as one on the device, tiles whose O is moved out between included."""
+    b = Batch(41, kind, [200, 1, 37], [400, 50, 900], 2, d)
+    q, qt = bf16_rows(b.rng, b.T, 4, d)
+    host = torch.full((b.T, 4, d), -1.0).pin_memory()
+    want = prefill(pkv, b, qt, 0.1)
+    prefill(pkv, b, qt, 0.1, out=host)
+    torch.cuda.synchronize()
+    assert torch.equal(host, want.cpu())
+    one = Batch(42, kind, [1] * 3, [700, 3, 90], 2, d)
+    q, qt = bf16_rows(one.rng, 3, 4, d)
+    host = torch.full((3, 4, d), -1.0).pin_memory()
+    want = decode(pkv, one, qt, 0.1)
+    decode(pkv, one, qt, 0.1, out=host)
+    torch.cuda.synchronize()
+    assert torch.equal(host, want.cpu()) and pkv.get_error()[0] == 0
 
 
 def test_rows_that_the_call_does_not_have(pkv):

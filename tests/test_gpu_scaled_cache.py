@@ -241,6 +241,9 @@ def test_refusals_of_the_binding(pkv):
         pkv.cache_read(k, v, start, lens, tables, 4, k_scale=1.0, v_scale=1.0, block_scales=sc)
     with pytest.raises(ValueError):
         pkv.cache_read(to_dev(b.k.view(np.uint8)), to_dev(b.v.view(np.uint8)), start, lens, tables, 4)
+    with pytest.raises(TypeError):
+        pkv.cache_read(to_dev(b.k.view(np.int8)), to_dev(b.v.view(np.int8)), start, lens, tables, 4, k_scale=1.0,
+                       v_scale=1.0)
     assert pkv.get_error()[0] == 0
 
 
