@@ -490,9 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (mx < INFINITY) e = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100);
                 // The scale's sign goes with q, so that the scores' factor is
                 // not negative, and so does a NaN, which that factor would lose.
-                const float down = isnan(P.scale_log2) ? P.scale_log2
-                                                       : copysignf(__uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23),
-                                                                   P.scale_log2);
+                float down = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+                down = isnan(P.scale_log2) ? P.scale_log2 : copysignf(down, P.scale_log2);
                 if (mine) {
 #pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
@@ -614,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (full) return;
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (kbase + 32 * c + 8 * (i / 4) + 2 * tq + (i & 1) > (i & 2 ? pos_b : pos_a)) s[i] = 0xff800000u;
+                        if (kbase + 32 * c + 8 * (i / 4) + 2 * tq + (i & 1) > (i & 2 ? pos_b : pos_a))
+                            s[i] = 0xff800000u;
                 };
                 // A block's factor of a row's scores, never so small that it
                 // would turn what was masked into a NaN.
@@ -688,8 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t* s = &sr[c & 1][4 * (2 * b + h)];
                             const int at = 2 * (2 * b + h);
-                            float2 ya = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), pa, sc.log2_v);
-                            float2 yb = __ffma2_rn(make_float2(__uint_as_float(s[2]), __uint_as_float(s[3])), pb, sc.log2_v);
+                            const float2 va = make_float2(__uint_as_float(s[0]), __uint_as_float(s[1]));
+                            const float2 vb = make_float2(__uint_as_float(s[2]), __uint_as_float(s[3]));
+                            float2 ya = __ffma2_rn(va, pa, sc.log2_v), yb = __ffma2_rn(vb, pb, sc.log2_v);
                             ya = __fadd2_rn(ya, ra);
                             yb = __fadd2_rn(yb, rb);
                             ya = make_float2(fast_exp2(ya.x), fast_exp2(ya.y));

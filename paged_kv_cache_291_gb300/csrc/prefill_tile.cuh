@@ -24,7 +24,8 @@ struct PrefillTile {
 // per q head).
 __device__ __forceinline__ PrefillTile find_prefill_tile(const int32_t* qsl, const int32_t* context_lens,
                                                          int num_seqs, int num_tokens, int ctx_cap,
-                                                         int cta_units, int split_last, int tile, int pair, unsigned long long* err, int lane) {
+                                                         int cta_units, int split_last, int tile, int pair,
+                                                         unsigned long long* err, int lane) {
     const unsigned FULL = 0xffffffffu;
     const int split = cta_units == 2 ? split_last : 0;
     int base = 0, found = -1, e = 0, nt_s = 0;
