@@ -279,6 +279,8 @@ def _cache(k_pool, v_pool, k_scale=None, v_scale=None, need_scales=False, block_
         return Cache(_dev(k_pool, "k_pool").value, _dev(v_pool, "v_pool").value, nb, hkv, d, bs,
                      PKV_KV_INT8_BLOCKS if k_pool.dtype == torch.int8 else PKV_KV_E4M3_BLOCKS, 1.0, 1.0,
                      _dev(block_scales, "block_scales", dtype=torch.float32).value)
+    if _torch().int8 in (k_pool.dtype, v_pool.dtype):
+        raise TypeError("an int8 pool needs block_scales")  # its codes are not e4m3's, and mean nothing without them
     if es == 1 and need_scales and (k_scale is None or v_scale is None):
         raise ValueError("an e4m3 pool needs k_scale and v_scale")
     return Cache(_dev(k_pool, "k_pool", es).value, _dev(v_pool, "v_pool", es).value, nb, hkv, d, bs,
@@ -316,8 +318,6 @@ def cache_write(k_pool, v_pool, k_new, v_new, slot_mapping, stream=None, k_scale
 def _cache_rows(k_pool, v_pool, query_start_loc, context_lens, block_tables, k_scale, v_scale, block_scales, dev):
     """Descriptor and index arguments of cache_append and cache_read."""
     i32 = _torch().int32
-    if block_scales is None and k_pool.dtype == _torch().int8:
-        raise TypeError("an int8 pool needs block_scales")
     c = _cache(k_pool, v_pool, k_scale, v_scale, need_scales=True, block_scales=block_scales)
     if k_pool.get_device() != dev or v_pool.get_device() != dev:
         raise ValueError(f"the pools are on {k_pool.device} and {v_pool.device}, the current device is cuda:{dev}")

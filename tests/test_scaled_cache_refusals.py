@@ -5,6 +5,7 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 import paged_kv_cache_291_gb300 as pkv
 
@@ -131,3 +132,36 @@ def test_descriptor_struct_matches_the_header(tmp_path):
     got = {ln.split()[0]: int(ln.split()[1]) for ln in out if ln}
     assert got.pop("size") == ctypes.sizeof(pkv.Cache) and got.pop("kinds") == E4M3 * 10 + INT8
     assert got == {f: getattr(pkv.Cache, f).offset for f, _ in pkv.Cache._fields_}
+
+
+def calls_without_block_scales(k, v):
+    """Every call that takes a pool, with valid arguments but for int8 pools that come without their scales."""
+    i32 = torch.zeros(2, dtype=torch.int32)
+    tables, rows = torch.zeros((1, 1), dtype=torch.int32), torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    attend = (rows, tables, i32[:1], 16, 0.125)
+    one = dict(k_scale=1.0, v_scale=1.0)
+    host = torch.zeros(2 * 2 * 16 * 64, dtype=torch.int8)
+    return {
+        "cache_write": lambda: pkv.cache_write(k, v, rows, rows, i32[:1], **one),
+        "cache_read": lambda: pkv.cache_read(k, v, i32, i32[:1], tables, 1, **one),
+        "copy_blocks": lambda: pkv.copy_blocks(k, v, i32[:1], i32[:1]),
+        "swap_out": lambda: pkv.swap_out(k, v, i32[:1], i32[:1], host),
+        "swap_in": lambda: pkv.swap_in(k, v, i32[:1], i32[:1], host),
+        "decode_attention": lambda: pkv.decode_attention(k, v, *attend, **one),
+        "decode_step": lambda: pkv.decode_step(k, v, rows, rows, i32[:1], *attend, **one),
+        "decode_attention_shared_prefix": lambda: pkv.decode_attention_shared_prefix(
+            k, v, rows, tables, i32[:1], 16, 0, 0.125, **one),
+        "chunked_prefill_attention": lambda: pkv.chunked_prefill_attention(k, v, rows, i32, i32[:1], tables, 16, 0.125),
+        "rotary_cache_write": lambda: pkv.rotary_cache_write(
+            k, v, rows, rows, rows, i32[:1], torch.zeros((1, 1), dtype=torch.int32), torch.zeros(32), 64, **one),
+    }
+
+
+@pytest.mark.parametrize("call", calls_without_block_scales(None, None))
+@pytest.mark.parametrize("which", ["both", "k", "v"])
+def test_int8_pools_without_their_scales(lib, monkeypatch, call, which):
+    """int8 codes are not e4m3 codes, and a copy that leaves the scales behind has lost the rows."""
+    monkeypatch.setattr(pkv, "_device", lambda: 0)
+    k, v = (torch.zeros((1, 2, 16, 64), dtype=torch.int8 if which in ("both", x) else torch.uint8) for x in "kv")
+    with pytest.raises(TypeError, match="int8 pool needs block_scales"):
+        calls_without_block_scales(k, v)[call]()
