@@ -244,6 +244,8 @@ struct Bars {
 
 // A stage a consumer warp is to load: the slabs of its blocks (the second if
 // `two`) and their scales, K's and V's, the latter as f 2^e with f in [1, 2).
+// Where the item's V scales up to here are more than 2^kWideSpread apart inv_2e
+// is zero, and the sum's terms are exponentials of their own.
 struct __align__(16) BlockScales {
     float k, f, e, inv_2e;
 };
@@ -251,6 +253,11 @@ struct __align__(16) Order {
     int32_t slab[2], two, unused;
     BlockScales scales[2];
 };
+
+// A key whose u = 2^(s + e - m + 11) is flushed to zero (below 2^-126; m is at
+// most the largest s plus the largest e) weighs less than 2^-(137 - spread) of
+// the largest 2^s: 2^-33 here, as little as what two fp16 terms drop.
+constexpr int kWideSpread = 104;
 
 __device__ __forceinline__ BlockScales block_scales_of(float2 s, bool& bad) {
     BlockScales r;
@@ -713,6 +720,7 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
             constexpr int kBatch = 32 < C::ORDERS / 2 * C::W ? 32 : C::ORDERS / 2 * C::W;
             Order* orders = reinterpret_cast<Order*>(smem + C::OFF_ORDERS);
             const int nst = (b1 - b0 + 1) / 2;
+            int high = -1000, low = 1000;  // exponents of the item's V scales so far
             for (int base = 0; base < nst; base += kBatch) {
                 const int cnt = min(kBatch, nst - base);
                 const int next = b0 + 2 * (base + kBatch + lane);
@@ -725,8 +733,8 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
                 const uint32_t jw = static_cast<uint32_t>(__shfl_sync(FULL, static_cast<int>(given), w)) +
                                     static_cast<uint32_t>((i - first_w) / C::W);
                 int bad = 0;
+                Order o;
                 if (lane < cnt) {
-                    Order o;
                     o.two = b0 + 2 * i + 1 < b1;
                     bool bad_scale = false;
 #pragma unroll
@@ -738,8 +746,15 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
                         }
                         o.slab[x] = id * P.hkv + g;
                         o.scales[x] = block_scales_of(__ldg(P.block_scales + o.slab[x]), bad_scale);
+                        high = max(high, static_cast<int>(o.scales[x].e));
+                        low = min(low, static_cast<int>(o.scales[x].e));
                     }
                     if (bad_scale) record_error(P.err, kErrRange, static_cast<uint32_t>(s));
+                }
+                high = __reduce_max_sync(FULL, high);
+                low = __reduce_min_sync(FULL, low);
+                if (lane < cnt) {
+                    if (high - low > kWideSpread) o.scales[0].inv_2e = o.scales[1].inv_2e = 0.f;
                     const uint32_t at = static_cast<uint32_t>(w * C::ORDERS) + jw % C::ORDERS;
                     if (!mbar_wait(&B.oempty[at], ((jw / C::ORDERS) & 1) ^ 1)) {
                         bad = 1;
@@ -1306,6 +1321,17 @@ __device__ void run_consumer(const DecodeParams& P, uint8_t* smem, const Bars& B
     }
 }
 
+// 2^x (x <= 0) as a square: pools with a scale per block move their sums to
+// another reference by its halves one after the other, since their references
+// hold the V scales' exponents and 2^x may be below what fp32 holds where the sum
+// times 2^x is not.
+struct Halves {
+    float half;
+    __device__ __forceinline__ explicit Halves(float x) : half(fast_exp2(0.5f * x)) {}
+    __device__ __forceinline__ float whole() const { return half * half; }
+    __device__ __forceinline__ float times(float l) const { return l * half * half; }
+};
+
 // The row of an item whose sum is L: o / L, or 0 for an empty context (L = 0).
 // Pools with a scale per block keep a NaN as it is; the others give 0 for it.
 template <class C>
@@ -1384,8 +1410,15 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
             float M = e.x;
 #pragma unroll
             for (int o = 1; o < WL; o <<= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
-            float wt = (e.x == -INFINITY) ? 0.f : fast_exp2(e.x - M);
-            float L = e.y * wt;
+            float wt, L;
+            if constexpr (C::SCALED) {
+                const Halves h(e.x == -INFINITY ? -INFINITY : e.x - M);
+                wt = h.whole();
+                L = h.times(e.y);
+            } else {
+                wt = (e.x == -INFINITY) ? 0.f : fast_exp2(e.x - M);
+                L = e.y * wt;
+            }
 #pragma unroll
             for (int o = 1; o < WL; o <<= 1) L += __shfl_xor_sync(FULL, L, o);
             float wp = 0.f;  // weight of the prefix state
@@ -1488,8 +1521,14 @@ __device__ void run_merger(const DecodeParams& P, uint8_t* smem, const Bars& B, 
                     for (int g = 0; g < G; ++g) {
                         const float2 e = (pp < d.nparts) ? __ldcg(P.part_ml + part_base(pp) + g)
                                                          : make_float2(-INFINITY, 0.f);
-                        wt[g] = (e.x == -INFINITY) ? 0.f : fast_exp2(e.x - M[g]);
-                        L[g] = fmaf(e.y, wt[g], L[g]);
+                        if constexpr (C::SCALED) {
+                            const Halves h(e.x == -INFINITY ? -INFINITY : e.x - M[g]);
+                            wt[g] = h.whole();
+                            L[g] += h.times(e.y);
+                        } else {
+                            wt[g] = (e.x == -INFINITY) ? 0.f : fast_exp2(e.x - M[g]);
+                            L[g] = fmaf(e.y, wt[g], L[g]);
+                        }
                     }
                     const int cnt = min(32, d.nparts - p0);
 #pragma unroll 2

@@ -29,8 +29,13 @@
 //    of 12: 412 us against 371).
 //  * Weights of a block carry its V scale, vs = f 2^e with f in [1, 2): the
 //    running maximum is that of s_j + e, u = 2^(s_j + e - m + 11), the weight
-//    u f and the term of the sum u 2^-e, so scales far apart lose nothing, and
-//    weights end 2^-36 below the largest (fp16 is exact to 2^-24).
+//    u f and the term of the sum u 2^-e, and weights end 2^-36 below the largest
+//    (fp16 is exact to 2^-24).  A key of a small V scale may count for nothing in
+//    O and for all in the sum (16 rows of zeros, whose scale is 2^-100, beside
+//    one of scale 2^40: v / 17).  So where an item's V scales are more than 2^104
+//    apart the sum's terms are 2^(s_j - m + 11), each the square of an
+//    exponential of half that, which fp32 holds for every scale, and sums move
+//    to other references in two such halves.
 //  * The order of dims in S and of keys in P V is free: a lane reads whole
 //    16-byte pieces of K rows and of V rows (8-byte pieces of V at head_dim
 //    64), and rows are dealt to lanes so that the lanes that read together hit
@@ -397,15 +402,26 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
             // scores (past 2^20 or so these sums are no longer exact).
             const bool moves0 = mb0 > __fadd_rd(m0, kScaledThreshold), moves1 = mb1 > __fadd_rd(m1, kScaledThreshold);
             if (__any_sync(FULL, moves0 || moves1)) {
-                const float a0 = moves0 ? fast_exp2(m0 - mb0) : 1.f, a1 = moves1 ? fast_exp2(m1 - mb1) : 1.f;
+                const Halves h0(moves0 ? m0 - mb0 : 0.f), h1(moves1 ? m1 - mb1 : 0.f);
+                const float a0 = h0.whole(), a1 = h1.whole();
                 m0 = moves0 ? mb0 : m0;
                 m1 = moves1 ? mb1 : m1;
-                l0 *= a0;
-                l1 *= a1;
+                l0 = h0.times(l0);
+                l1 = h1.times(l1);
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
             }
             const float add0 = __fsub_rd(kScaledShift, m0), add1 = __fsub_rd(kScaledShift, m1);
+            if (sc[0].inv_2e == 0.f) {  // V scales far apart
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const float s0 = add0 - sc[i].e, s1 = add1 - sc[i].e;
+                    const float t0 = fast_exp2(0.5f * (u[i][0] + s0)), t1 = fast_exp2(0.5f * (u[i][1] + s1));
+                    const float t2 = fast_exp2(0.5f * (u[i][2] + s0)), t3 = fast_exp2(0.5f * (u[i][3] + s1));
+                    l0 += fmaf(t0, t0, t2 * t2);
+                    l1 += fmaf(t1, t1, t3 * t3);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 if (i > 0 && valid[i] == 0) break;

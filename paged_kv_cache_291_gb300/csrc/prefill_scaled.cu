@@ -24,7 +24,12 @@
 //    the rounding lost: 2^-22, where one term would be 2^-11), which take exactly
 //    the columns of the scores they replace; the row sum adds P / vs_b block by
 //    block.  m moves, and O is rescaled, when the maximum grows by more than 2^3:
-//    P stays below 2^15, and weights end 2^-36 below the largest.
+//    P stays below 2^15, and weights end 2^-36 below the largest.  A key of a
+//    small V scale may count for nothing in O and for all in the sum (16 rows of
+//    zeros, whose scale is 2^-100, beside one of scale 2^40: v / 17), so from the
+//    tile on where the V scales are more than 2^104 apart a pass of its own sums
+//    2^(s_j - m + 12), each the square of an exponential of half that, which fp32
+//    holds for every scale; sums move to other references in two such halves.
 //  * A NaN code in V (the append stores one for a NaN) would reach, as 0 times
 //    NaN, the rows of its tile that do not see it: such a CTA's rows are done
 //    again on CUDA cores.
@@ -111,11 +116,17 @@ struct Params {
 };
 
 // A block's scales as the softmax takes them, V's twice: operands of packed
-// arithmetic.
+// arithmetic.  wide is not zero, and inv_v is, where the V scales of the tiles
+// up to this one are more than 2^kWideSpread apart: the row sums then come from
+// wide_sums.
 struct __align__(8) TileScales {
     float2 log2_v, inv_v;
-    float k, unused;
+    float k, wide;
 };
+// A key whose P = 2^(y - m + 12) is flushed to zero (below 2^-126; m is at most
+// the largest s plus the largest log2 vs) weighs less than 2^-(138 - spread) of
+// the largest 2^s: 2^-34 here, as little as what two fp16 terms drop.
+constexpr int kWideSpread = 104;
 
 enum {
     B_QFULL = 0,
@@ -205,6 +216,34 @@ __device__ __forceinline__ uint32_t widen_rows(uint32_t codes, uint32_t tile, in
         }
     }
     return nan & 0x80808080u;
+}
+
+// A block's factor of a row's scores, never so small that it would turn what
+// was masked into a NaN.
+__device__ __forceinline__ float block_factor(float f, float ks) { return fmaxf(f * ks, FLT_MIN); }
+
+// This thread's part of the sums of 2^(s + sh) over a tile's keys for its rows
+// a and b (see the softmax rows), whose scores are at ts.
+__device__ __noinline__ float2 wide_sums(uint32_t ts, const TileScales* sct, float fa, float fb, float sha, float shb,
+                                         int key0, int pos_a, int pos_b) {
+    float la = 0.f, lb = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t s[16];
+        tc::tmem_ld16x256b_x4(ts + 32 * c, s);
+        tc::tmem_wait_ld(s);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const bool row_b = i & 2;
+            const float ks = sct[2 * c + i / 8].k;
+            const float y = __uint_as_float(s[i]) * block_factor(row_b ? fb : fa, ks);
+            const float t = fast_exp2(0.5f * (y + (row_b ? shb : sha)));
+            const bool sees = key0 + 32 * c + 8 * (i / 4) + (i & 1) <= (row_b ? pos_b : pos_a);
+            if (row_b) lb = sees ? fmaf(t, t, lb) : lb;
+            else la = sees ? fmaf(t, t, la) : la;
+        }
+    }
+    return make_float2(la, lb);
 }
 
 // A CTA's rows on CUDA cores, for V with NaN codes: warp w takes the (row,
@@ -331,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // before it is on its way.
         int slab = 0;
         float ks = 1.f, log2_v = 0.f, inv_v = 1.f;
+        int high = -1000, low = 1000;  // exponents of the V scales up to here
         auto look_up = [&](int j) {
             ks = 1.f, log2_v = 0.f, inv_v = 1.f;
             if (lane < min(kBlocksPerTile, nblk - j * kBlocksPerTile)) {
@@ -343,6 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float vs = checked_scale(s.y, bad);
                 log2_v = log2f(vs);
                 inv_v = 1.f / vs;
+                const int e2 = static_cast<int>(__float_as_uint(vs) >> 23) - 127;
+                high = max(high, e2);
+                low = min(low, e2);
                 if (bad) record_error(P.err, kErrRange, static_cast<uint32_t>(T.s));
             }
         };
@@ -352,11 +395,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t bytes = static_cast<uint32_t>(nvb) * kBlockSize * D;
             const int now = slab;
             if (!mbar_wait_warp(&bar[B_KCEMPTY], (j & 1) ^ 1)) { ok = false; break; }
+            high = __reduce_max_sync(FULL, high);
+            low = __reduce_min_sync(FULL, low);
+            const bool wide = high - low > kWideSpread;
             // The tile three before this one has been through its softmax:
             // every warp widened the last K tile after that.
             if (lane < kBlocksPerTile)
                 scales[j % kScaleTiles * kBlocksPerTile + lane] = {
-                    make_float2(log2_v, log2_v), make_float2(inv_v, inv_v), ks, 0.f};
+                    make_float2(log2_v, log2_v), wide ? make_float2(0.f, 0.f) : make_float2(inv_v, inv_v), ks,
+                    wide ? 1.f : 0.f};
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&bar[B_KCFULL], bytes);
             __syncwarp();
@@ -602,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kbase = j * kTileN;
                 const bool full = kbase + kTileN - 1 <= __shfl_sync(FULL, pos_a, 0);
                 const TileScales* sct = scales + j % kScaleTiles * kBlocksPerTile;
+                const bool wide = __any_sync(FULL, sct[0].wide != 0.f);
                 // The scores are taken from tensor memory twice, 32 keys at a
                 // time and the next 32 on their way: held over both passes, 64
                 // a thread, they would push other values out of registers.
@@ -616,9 +664,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kbase + 32 * c + 8 * (i / 4) + 2 * tq + (i & 1) > (i & 2 ? pos_b : pos_a))
                             s[i] = 0xff800000u;
                 };
-                // A block's factor of a row's scores, never so small that it
-                // would turn what was masked into a NaN.
-                auto factor = [](float f, float ks) { return fmaxf(f * ks, FLT_MIN); };
                 // Pass 1: each row's largest y = s factor + log2 vs, block by
                 // block.
                 float xa = -INFINITY, xb = -INFINITY;
@@ -636,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float vb = fmaxf(__uint_as_float(s[2]), __uint_as_float(s[3]));
                         va = fmax3(va, __uint_as_float(s[4]), __uint_as_float(s[5]));
                         vb = fmax3(vb, __uint_as_float(s[6]), __uint_as_float(s[7]));
-                        xa = fmaxf(xa, fmaf(va, factor(fa, ks), lv));
-                        xb = fmaxf(xb, fmaf(vb, factor(fb, ks), lv));
+                        xa = fmaxf(xa, fmaf(va, block_factor(fa, ks), lv));
+                        xb = fmaxf(xb, fmaf(vb, block_factor(fb, ks), lv));
                     }
                 }
                 xa = fmaxf(xa, __shfl_xor_sync(FULL, xa, 1));
@@ -654,17 +699,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool moves = __any_sync(FULL, need_a || need_b);
                 if (moves) {
                     if (need_a) {
-                        alpha_a = fast_exp2(mua - xa);
+                        const float half = fast_exp2(0.5f * (mua - xa));
+                        alpha_a = half * half;
+                        if (j > 0) la = make_float2(la.x * half * half, la.y * half * half);
                         mua = xa;
                     }
                     if (need_b) {
-                        alpha_b = fast_exp2(mub - xb);
+                        const float half = fast_exp2(0.5f * (mub - xb));
+                        alpha_b = half * half;
+                        if (j > 0) lb = make_float2(lb.x * half * half, lb.y * half * half);
                         mub = xb;
                     }
-                    if (j > 0) {
-                        la = __fmul2_rn(la, make_float2(alpha_a, alpha_a));
-                        lb = __fmul2_rn(lb, make_float2(alpha_b, alpha_b));
-                    } else {
+                    if (j == 0) {
                         mfa = mua;
                         mfb = mub;
                     }
@@ -673,6 +719,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // over the 32 keys' scores; the row sums without the V scales.
                 const float sha = __fsub_rd(kShift, mua), shb = __fsub_rd(kShift, mub);
                 const float2 ra = make_float2(sha, sha), rb = make_float2(shb, shb);
+                if (wide) {
+                    tc::tmem_wait_ld(sr[0]);
+                    const float2 l = wide_sums(ts, sct, fa, fb, sha, shb, kbase + 2 * tq, full ? INT32_MAX : pos_a,
+                                               full ? INT32_MAX : pos_b);
+                    la.x += l.x;
+                    lb.x += l.y;
+                    tc::tmem_ld16x256b_x4(ts, sr[0]);
+                }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     tc::tmem_wait_ld(sr[c & 1]);
@@ -682,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const TileScales& sc = sct[2 * c + b];
-                        const float ka = factor(fa, sc.k), kb = factor(fb, sc.k);
+                        const float ka = block_factor(fa, sc.k), kb = block_factor(fb, sc.k);
                         const float2 pa = make_float2(ka, ka), pb = make_float2(kb, kb);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
