@@ -244,8 +244,9 @@ struct Bars {
 
 // A stage a consumer warp is to load: the slabs of its blocks (the second if
 // `two`) and their scales, K's and V's, the latter as f 2^e with f in [1, 2).
-// Where the item's V scales up to here are more than 2^kWideSpread apart inv_2e
-// is zero, and the sum's terms are exponentials of their own.
+// inv_2e: 2^-(e + kSumShift), or zero where the item's V scales up to here are
+// more than 2^kWideSpread apart or one is above 2^kWideTop: the sum's terms are
+// then exponentials of their own.
 struct __align__(16) BlockScales {
     float k, f, e, inv_2e;
 };
@@ -258,6 +259,11 @@ struct __align__(16) Order {
 // most the largest s plus the largest e) weighs less than 2^-(137 - spread) of
 // the largest 2^s: 2^-33 here, as little as what two fp16 terms drop.
 constexpr int kWideSpread = 104;
+// The sum's terms are 2^(s - m + 11 - kSumShift), and m is at least s + e - 3:
+// below 2^107 at the least scale, so that 2^21 keys of a warp fit fp32 (without
+// the shift 2^14 keys of zero rows would end beyond it).  The largest is at least
+// 2^(3 - 122).
+constexpr int kSumShift = 8, kWideTop = 100;
 
 __device__ __forceinline__ BlockScales block_scales_of(float2 s, bool& bad) {
     BlockScales r;
@@ -266,7 +272,7 @@ __device__ __forceinline__ BlockScales block_scales_of(float2 s, bool& bad) {
     const int e = static_cast<int>(bits >> 23) - 127;
     r.f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
     r.e = static_cast<float>(e);
-    r.inv_2e = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    r.inv_2e = __uint_as_float(static_cast<uint32_t>(max(127 - kSumShift - e, 0)) << 23);
     return r;
 }
 
@@ -754,7 +760,7 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
                 high = __reduce_max_sync(FULL, high);
                 low = __reduce_min_sync(FULL, low);
                 if (lane < cnt) {
-                    if (high - low > kWideSpread) o.scales[0].inv_2e = o.scales[1].inv_2e = 0.f;
+                    if (high - low > kWideSpread || high > kWideTop) o.scales[0].inv_2e = o.scales[1].inv_2e = 0.f;
                     const uint32_t at = static_cast<uint32_t>(w * C::ORDERS) + jw % C::ORDERS;
                     if (!mbar_wait(&B.oempty[at], ((jw / C::ORDERS) & 1) ^ 1)) {
                         bad = 1;
@@ -1337,6 +1343,10 @@ struct Halves {
 template <class C>
 __device__ __forceinline__ float4 finish_row(float4 a, float L, float v_scale) {
     const bool any = C::SCALED ? L != 0.f : L > 0.f;
+    if constexpr (C::SCALED) {  // the sum's shift
+        constexpr float f = 1.f / (1 << kSumShift);
+        a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    }
     return any ? normalise<C::SCALED ? 2 : C::ELEM>(a, L, v_scale) : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 

@@ -29,11 +29,11 @@
 //    of 12: 412 us against 371).
 //  * Weights of a block carry its V scale, vs = f 2^e with f in [1, 2): the
 //    running maximum is that of s_j + e, u = 2^(s_j + e - m + 11), the weight
-//    u f and the term of the sum u 2^-e, and weights end 2^-36 below the largest
+//    u f and the term of the sum u 2^-(e + 8), and weights end 2^-36 below the largest
 //    (fp16 is exact to 2^-24).  A key of a small V scale may count for nothing in
 //    O and for all in the sum (16 rows of zeros, whose scale is 2^-100, beside
 //    one of scale 2^40: v / 17).  So where an item's V scales are more than 2^104
-//    apart the sum's terms are 2^(s_j - m + 11), each the square of an
+//    apart the sum's terms are 2^(s_j - m + 3), each the square of an
 //    exponential of half that, which fp32 holds for every scale, and sums move
 //    to other references in two such halves.
 //  * The order of dims in S and of keys in P V is free: a lane reads whole
@@ -412,10 +412,10 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
                 for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
             }
             const float add0 = __fsub_rd(kScaledShift, m0), add1 = __fsub_rd(kScaledShift, m1);
-            if (sc[0].inv_2e == 0.f) {  // V scales far apart
+            if (sc[0].inv_2e == 0.f) {  // V scales far apart, or large
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
-                    const float s0 = add0 - sc[i].e, s1 = add1 - sc[i].e;
+                    const float s0 = add0 - (sc[i].e + kSumShift), s1 = add1 - (sc[i].e + kSumShift);
                     const float t0 = fast_exp2(0.5f * (u[i][0] + s0)), t1 = fast_exp2(0.5f * (u[i][1] + s1));
                     const float t2 = fast_exp2(0.5f * (u[i][2] + s0)), t3 = fast_exp2(0.5f * (u[i][3] + s1));
                     l0 += fmaf(t0, t0, t2 * t2);

@@ -22,13 +22,13 @@
 //  * The running maximum is that of y_j = s_j + log2 vs_b; P = 2^(y_j - m + 12) is
 //    the weight with its V scale, in two fp16 terms (the rounded value and what
 //    the rounding lost: 2^-22, where one term would be 2^-11), which take exactly
-//    the columns of the scores they replace; the row sum adds P / vs_b block by
-//    block.  m moves, and O is rescaled, when the maximum grows by more than 2^3:
+//    the columns of the scores they replace; the row sum adds 2^-9 P / vs_b block
+//    by block.  m moves, and O is rescaled, when the maximum grows by more than 2^3:
 //    P stays below 2^15, and weights end 2^-36 below the largest.  A key of a
 //    small V scale may count for nothing in O and for all in the sum (16 rows of
 //    zeros, whose scale is 2^-100, beside one of scale 2^40: v / 17), so from the
 //    tile on where the V scales are more than 2^104 apart a pass of its own sums
-//    2^(s_j - m + 12), each the square of an exponential of half that, which fp32
+//    2^(s_j - m + 3), each the square of an exponential of half that, which fp32
 //    holds for every scale; sums move to other references in two such halves.
 //  * A NaN code in V (the append stores one for a NaN) would reach, as 0 times
 //    NaN, the rows of its tile that do not see it: such a CTA's rows are done
@@ -116,9 +116,9 @@ struct Params {
 };
 
 // A block's scales as the softmax takes them, V's twice: operands of packed
-// arithmetic.  wide is not zero, and inv_v is, where the V scales of the tiles
-// up to this one are more than 2^kWideSpread apart: the row sums then come from
-// wide_sums.
+// arithmetic.  inv_v: 2^-kSumShift / vs, or zero, and wide not zero, where the V
+// scales of the tiles up to this one are more than 2^kWideSpread apart or one is
+// 2^(kWideTop + 1) or more: the row sums then come from wide_sums.
 struct __align__(8) TileScales {
     float2 log2_v, inv_v;
     float k, wide;
@@ -127,6 +127,11 @@ struct __align__(8) TileScales {
 // the largest s plus the largest log2 vs) weighs less than 2^-(138 - spread) of
 // the largest 2^s: 2^-34 here, as little as what two fp16 terms drop.
 constexpr int kWideSpread = 104;
+// The sums' terms are 2^(s - m + 12 - kSumShift), and m is at least s + log2 vs -
+// 3: below 2^107 at the least scale, so that rows of 2^21 keys fit fp32 (without
+// the shift 2^13 zero rows would end beyond it).  The largest is at least 2^(2 -
+// 122), and inv_v is a normal number.
+constexpr int kSumShift = 9, kWideTop = 100;
 
 enum {
     B_QFULL = 0,
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ks = checked_scale(s.x, bad);
                 const float vs = checked_scale(s.y, bad);
                 log2_v = log2f(vs);
-                inv_v = 1.f / vs;
+                inv_v = 1.f / (1 << kSumShift) / vs;
                 const int e2 = static_cast<int>(__float_as_uint(vs) >> 23) - 127;
                 high = max(high, e2);
                 low = min(low, e2);
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mbar_wait_warp(&bar[B_KCEMPTY], (j & 1) ^ 1)) { ok = false; break; }
             high = __reduce_max_sync(FULL, high);
             low = __reduce_min_sync(FULL, low);
-            const bool wide = high - low > kWideSpread;
+            const bool wide = high - low > kWideSpread || high > kWideTop;
             // The tile three before this one has been through its softmax:
             // every warp widened the last K tile after that.
             if (lane < kBlocksPerTile)
@@ -721,8 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 ra = make_float2(sha, sha), rb = make_float2(shb, shb);
                 if (wide) {
                     tc::tmem_wait_ld(sr[0]);
-                    const float2 l = wide_sums(ts, sct, fa, fb, sha, shb, kbase + 2 * tq, full ? INT32_MAX : pos_a,
-                                               full ? INT32_MAX : pos_b);
+                    const float2 l = wide_sums(ts, sct, fa, fb, sha - kSumShift, shb - kSumShift, kbase + 2 * tq,
+                                               full ? INT32_MAX : pos_a, full ? INT32_MAX : pos_b);
                     la.x += l.x;
                     lb.x += l.y;
                     tc::tmem_ld16x256b_x4(ts, sr[0]);
@@ -812,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sb += __shfl_xor_sync(FULL, sb, 1);
                 sa += __shfl_xor_sync(FULL, sa, 2);
                 sb += __shfl_xor_sync(FULL, sb, 2);
-                const float inva = 1.f / sa, invb = 1.f / sb;
+                const float inva = 1.f / (1 << kSumShift) / sa, invb = 1.f / (1 << kSumShift) / sb;
                 const float fac_a = fast_exp2(mfa - mua), fac_b = fast_exp2(mfb - mub);
                 auto kept_or_zero = [&](int c, float (&x)[32]) {
                     if (nt > kKeep) {

@@ -6,14 +6,16 @@ import numpy as np
 import pytest
 import torch
 
-from scaled_batch import Batch, bf16_rows
+from oracle import scaled as S
+from scaled_batch import Batch, bf16_rows, to_dev
 from test_gpu_scaled_attention import KINDS, check, decode, pkv, prefill  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 # Powers of the V scales of a context's blocks: the least beside larger ones (a
 # block of zeros has the least), steps up and down.
-POWERS = [[-100, 40], [40, -100], [-100, 116], [116, -100], [-100, 0, 116], [116, 0, -100], [-60, 90], [0, 116, -100, 50]]
+POWERS = [[-100, 40], [40, -100], [-100, 116], [116, -100], [-100, 0, 116], [116, 0, -100], [-60, 90], [0, 116, -100, 50],
+          [116, 110], [99, 103, 101]]
 
 
 def spread_v_scales(b, powers, stride):
@@ -54,4 +56,47 @@ def test_v_scales_far_apart_prefill(pkv, kind, powers, d, g):
         for size in (0.0, 1.0):
             q, qt = bf16_rows(b.rng, b.T, 2 * g, d, size=size)
             check(b, prefill(pkv, b, qt, d ** -0.5), q, d ** -0.5)
+    assert pkv.get_error()[0] == 0
+
+
+def long_run_of_zeros(kind, zeros, d, rows):
+    """A context of `zeros` keys with zero V at the least scale, then one block of scale 1, as a table over four
+    blocks.  The first 128 keys have score 0, the other zero rows 2, the last block's keys 0.  Returns the pools, the
+    table, q and the float64 out of the last `rows` rows."""
+    rng = np.random.default_rng(zeros)
+    k, v = np.zeros((4, 1, 16, d), kind), np.zeros((4, 1, 16, d), kind)
+    code = np.uint8(0x38) if kind == np.uint8 else np.int8(1)  # 1
+    k[1, 0, :, 0] = code
+    x = rng.standard_normal((16, d)).astype(np.float32) * 30
+    v[2, 0] = S.encode(x, v)
+    scales = np.ones((4, 1, 2), np.float32)
+    scales[:2, 0, 1] = 2.0 ** -100
+    table = np.full(zeros // 16 + 1, 1, np.int32)
+    table[:8], table[-1] = 0, 2
+    q = np.zeros((rows, 1, d), np.float32)
+    q[:, 0, 0] = 2.0
+    values = S.values(v[2, 0])
+    want = [values[:n].sum(0) / (128 + n + (zeros - 128) * np.exp(2.0)) for n in range(17 - rows, 17)]
+    dev = [to_dev(k), to_dev(v), torch.from_numpy(scales).cuda(), torch.from_numpy(table[None]).cuda(),
+           torch.tensor([zeros + 16], dtype=torch.int32, device="cuda"), torch.from_numpy(q).bfloat16().cuda()]
+    return dev, np.stack(want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_long_run_of_the_least_scale(pkv, kind, d):
+    """Sums of 2^(s - log2 vs) over long runs of zero rows stay in fp32.
+
+    A thread sums at most an eighth of the terms one by one, each addition off by 2^-24 of the sum; the other roundings
+    are the usual ones, below 2^-18."""
+    for zeros in (2 ** 12, 2 ** 17, 2 ** 18, 2 ** 20):
+        (k, v, sc, tables, lens, q), want = long_run_of_zeros(kind, zeros, d, 2)
+        tol = (zeros / 8 * 2.0 ** -24 + 2.0 ** -18) * np.abs(want)
+        start = torch.tensor([0, 2], dtype=torch.int32)
+        got = pkv.chunked_prefill_attention(k, v, q, start.cuda(), lens, tables, zeros + 16, 1.0,
+                                            query_start_loc_host=start, block_scales=sc)
+        assert np.all(np.abs(got[:, 0].double().cpu().numpy() - want) <= tol)
+        for part in (0, zeros // 16 + 1):
+            got = pkv.decode_attention(k, v, q[1:], tables, lens, zeros + 16, 1.0, block_scales=sc, partition_blocks=part)
+            assert np.all(np.abs(got[:, 0].double().cpu().numpy() - want[1:]) <= tol[1:])
     assert pkv.get_error()[0] == 0
