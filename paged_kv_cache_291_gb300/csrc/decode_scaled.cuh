@@ -112,6 +112,14 @@ struct ScaledCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
+// Stages after which a warp's O and sums join what it has of the item so far, in
+// its slot for the merger.  The tensor cores' sums lose half a unit in the last
+// place on average at each MMA, always to the same side: a row of 131,072 tokens
+// that one CTA reads came out 3e-5 (12 warps) to 8e-5 (8) short of its size, and
+// so 7e-7, in the same time (with 8 stages 3e-7; 31 contexts of 64/8 x 128: 37.0
+// us, 37.7 with 8).
+constexpr int kFoldStages = 16;
+
 // P's exponent against the running maximum: a weight is below 2^(3 + 11 + 1).
 constexpr float kScaledThreshold = 3.0f, kScaledShift = 11.0f;
 
@@ -347,125 +355,150 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.iempty[slot]);
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0, l1;
         float o[D / 16][4];
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         const int nst = (d.b1 - d.b0 + 1) / 2;
         const int first = (warp - d.rot + C::W) % C::W;
-        for (int b = first; b < nst; b += C::W) {
-            const uint32_t st = taken % C::SW;
-            issue();
-            if (issued == taken) {  // not even this one is ordered yet
-                if (!mbar_wait_warp(&ofull[taken % C::ORDERS], (taken / C::ORDERS) & 1)) {
+        const int buf = item_seq % C::MERGE_BUFS;
+        int b = first;
+        do {
+            const bool begun = b != first;
+            l0 = l1 = 0.f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+            for (const int stop = min(nst, b + kFoldStages * C::W); b < stop; b += C::W) {
+                const uint32_t st = taken % C::SW;
+                issue();
+                if (issued == taken) {  // not even this one is ordered yet
+                    if (!mbar_wait_warp(&ofull[taken % C::ORDERS], (taken / C::ORDERS) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    issue();
+                }
+                if (*abort_flag || !mbar_wait_warp(&full[st], (taken / C::SW) & 1)) {
                     ok = false;
                     break;
                 }
-                issue();
+                const Order* order = orders + taken % C::ORDERS;
+                const int blk = d.b0 + 2 * b;
+                const int keys = min(2 * kBlockSize, (min(d.b1 * kBlockSize, d.n) - blk * kBlockSize));
+                constexpr int NB = C::BPS;
+                const uint8_t* kst = ring + st * C::STAGE_BYTES;
+                float u[NB][4];
+                BlockScales sc[NB];
+                int valid[NB];
+                float mb0 = -INFINITY, mb1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NB; ++i) scores<D, KIND>(kst + i * C::SLAB, qb, u[i], at);
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    valid[i] = min(max(keys - i * kBlockSize, 0), kBlockSize);
+                    sc[i] = order->scales[i];
+                    const float k0 = f0 * sc[i].k, k1 = f1 * sc[i].k;
+                    u[i][0] = fmaf(u[i][0], k0, sc[i].e), u[i][1] = fmaf(u[i][1], k1, sc[i].e);
+                    u[i][2] = fmaf(u[i][2], k0, sc[i].e), u[i][3] = fmaf(u[i][3], k1, sc[i].e);
+                    if (valid[i] < kBlockSize) {
+                        if (key_row<D>(g) >= valid[i]) u[i][0] = u[i][1] = -INFINITY;
+                        if (key_row<D>(g) + 8 >= valid[i]) u[i][2] = u[i][3] = -INFINITY;
+                    }
+                    mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]));
+                    mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]));
+                }
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    mb0 = fmaxf(mb0, __shfl_xor_sync(FULL, mb0, off));
+                    mb1 = fmaxf(mb1, __shfl_xor_sync(FULL, mb1, off));
+                }
+                // A new reference only where the maximum grew by more than 2^3.
+                // Rounded down, here and below, P stays below 2^16 however large the
+                // scores (past 2^20 or so these sums are no longer exact).
+                const bool moves0 = mb0 > __fadd_rd(m0, kScaledThreshold);
+                const bool moves1 = mb1 > __fadd_rd(m1, kScaledThreshold);
+                if (__any_sync(FULL, moves0 || moves1)) {
+                    const Halves h0(moves0 ? m0 - mb0 : 0.f), h1(moves1 ? m1 - mb1 : 0.f);
+                    const float a0 = h0.whole(), a1 = h1.whole();
+                    m0 = moves0 ? mb0 : m0;
+                    m1 = moves1 ? mb1 : m1;
+                    l0 = h0.times(l0);
+                    l1 = h1.times(l1);
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
+                }
+                const float add0 = __fsub_rd(kScaledShift, m0), add1 = __fsub_rd(kScaledShift, m1);
+                if (sc[0].inv_2e == 0.f) {  // V scales far apart, or large
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        const float s0 = add0 - (sc[i].e + kSumShift), s1 = add1 - (sc[i].e + kSumShift);
+                        const float t0 = fast_exp2(0.5f * (u[i][0] + s0)), t1 = fast_exp2(0.5f * (u[i][1] + s1));
+                        const float t2 = fast_exp2(0.5f * (u[i][2] + s0)), t3 = fast_exp2(0.5f * (u[i][3] + s1));
+                        l0 += fmaf(t0, t0, t2 * t2);
+                        l1 += fmaf(t1, t1, t3 * t3);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (i > 0 && valid[i] == 0) break;
+                    u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
+                    u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
+                    l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);
+                    l1 = fmaf(u[i][1] + u[i][3], sc[i].inv_2e, l1);
+                    uint32_t p[4];
+                    split_pair_f16(u[i][0] * sc[i].f, u[i][1] * sc[i].f, p[0], p[1]);
+                    split_pair_f16(u[i][2] * sc[i].f, u[i][3] * sc[i].f, p[2], p[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[j] = transposed(p[j]);
+                    weigh<D, KIND>(kst + (2 + i) * C::SLAB, valid[i], p, o, at, t);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.oempty[warp * C::ORDERS + taken % C::ORDERS]);
+                ++taken;
             }
-            if (*abort_flag || !mbar_wait_warp(&full[st], (taken / C::SW) & 1)) {
+            if (!ok) break;
+            // This warp's state joins its slot for the merger: (m, l) and O of heads
+            // 2t and 2t + 1, each lane its D / 8 dims.  The first time the slot is
+            // waited for and set, then it is added to (m never falls).
+            if (!begun && !mbar_wait_warp(&B.mempty[buf], ((item_seq / C::MERGE_BUFS) & 1) ^ 1)) {
                 ok = false;
                 break;
             }
-            const Order* order = orders + taken % C::ORDERS;
-            const int blk = d.b0 + 2 * b;
-            const int keys = min(2 * kBlockSize, (min(d.b1 * kBlockSize, d.n) - blk * kBlockSize));
-            constexpr int NB = C::BPS;
-            const uint8_t* kst = ring + st * C::STAGE_BYTES;
-            float u[NB][4];
-            BlockScales sc[NB];
-            int valid[NB];
-            float mb0 = -INFINITY, mb1 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) scores<D, KIND>(kst + i * C::SLAB, qb, u[i], at);
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                valid[i] = min(max(keys - i * kBlockSize, 0), kBlockSize);
-                sc[i] = order->scales[i];
-                const float k0 = f0 * sc[i].k, k1 = f1 * sc[i].k;
-                u[i][0] = fmaf(u[i][0], k0, sc[i].e), u[i][1] = fmaf(u[i][1], k1, sc[i].e);
-                u[i][2] = fmaf(u[i][2], k0, sc[i].e), u[i][3] = fmaf(u[i][3], k1, sc[i].e);
-                if (valid[i] < kBlockSize) {
-                    if (key_row<D>(g) >= valid[i]) u[i][0] = u[i][1] = -INFINITY;
-                    if (key_row<D>(g) + 8 >= valid[i]) u[i][2] = u[i][3] = -INFINITY;
-                }
-                mb0 = fmaxf(mb0, fmaxf(u[i][0], u[i][2]));
-                mb1 = fmaxf(mb1, fmaxf(u[i][1], u[i][3]));
-            }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
-                mb0 = fmaxf(mb0, __shfl_xor_sync(FULL, mb0, off));
-                mb1 = fmaxf(mb1, __shfl_xor_sync(FULL, mb1, off));
+                l0 += __shfl_xor_sync(FULL, l0, off);
+                l1 += __shfl_xor_sync(FULL, l1, off);
             }
-            // A new reference only where the maximum grew by more than 2^3.
-            // Rounded down, here and below, P stays below 2^16 however large the
-            // scores (past 2^20 or so these sums are no longer exact).
-            const bool moves0 = mb0 > __fadd_rd(m0, kScaledThreshold), moves1 = mb1 > __fadd_rd(m1, kScaledThreshold);
-            if (__any_sync(FULL, moves0 || moves1)) {
-                const Halves h0(moves0 ? m0 - mb0 : 0.f), h1(moves1 ? m1 - mb1 : 0.f);
-                const float a0 = h0.whole(), a1 = h1.whole();
-                m0 = moves0 ? mb0 : m0;
-                m1 = moves1 ? mb1 : m1;
-                l0 = h0.times(l0);
-                l1 = h1.times(l1);
+            const size_t base = static_cast<size_t>((buf * C::W + warp) * G + 2 * t);
+            if (begun) {  // warp-uniform
 #pragma unroll
-                for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
+                for (int e = 0; e < 2; ++e) {
+                    if (2 * t + e >= G) continue;
+                    const float2 was = ml[base + e];
+                    const Halves f(was.x - (e ? m1 : m0));
+                    const float keep = f.whole();
+                    (e ? l1 : l0) += f.times(was.y);
+                    const float4* src = reinterpret_cast<const float4*>(mo + (base + e) * D + g * (D / 8));
+#pragma unroll
+                    for (int j = 0; j < D / 16; j += 2) {
+                        const float4 w = src[j / 2];
+                        o[j][e] = fmaf(w.x, keep, o[j][e]), o[j][2 + e] = fmaf(w.y, keep, o[j][2 + e]);
+                        o[j + 1][e] = fmaf(w.z, keep, o[j + 1][e]), o[j + 1][2 + e] = fmaf(w.w, keep, o[j + 1][2 + e]);
+                    }
+                }
+                __syncwarp();
             }
-            const float add0 = __fsub_rd(kScaledShift, m0), add1 = __fsub_rd(kScaledShift, m1);
-            if (sc[0].inv_2e == 0.f) {  // V scales far apart, or large
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const float s0 = add0 - (sc[i].e + kSumShift), s1 = add1 - (sc[i].e + kSumShift);
-                    const float t0 = fast_exp2(0.5f * (u[i][0] + s0)), t1 = fast_exp2(0.5f * (u[i][1] + s1));
-                    const float t2 = fast_exp2(0.5f * (u[i][2] + s0)), t3 = fast_exp2(0.5f * (u[i][3] + s1));
-                    l0 += fmaf(t0, t0, t2 * t2);
-                    l1 += fmaf(t1, t1, t3 * t3);
+            for (int e = 0; e < 2; ++e) {
+                if (2 * t + e < G) {
+                    if (g == 0) ml[base + e] = make_float2(e ? m1 : m0, e ? l1 : l0);
+                    float* dst = mo + (base + e) * D + g * (D / 8);
+#pragma unroll
+                    for (int j = 0; j < D / 16; j += 2)
+                        *reinterpret_cast<float4*>(dst + 2 * j) =
+                            make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
                 }
             }
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                if (i > 0 && valid[i] == 0) break;
-                u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
-                u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
-                l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);
-                l1 = fmaf(u[i][1] + u[i][3], sc[i].inv_2e, l1);
-                uint32_t p[4];
-                split_pair_f16(u[i][0] * sc[i].f, u[i][1] * sc[i].f, p[0], p[1]);
-                split_pair_f16(u[i][2] * sc[i].f, u[i][3] * sc[i].f, p[2], p[3]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] = transposed(p[j]);
-                weigh<D, KIND>(kst + (2 + i) * C::SLAB, valid[i], p, o, at, t);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B.oempty[warp * C::ORDERS + taken % C::ORDERS]);
-            ++taken;
-        }
+        } while (b < nst);
         if (!ok) break;
-        // This warp's state for the merger: (m, l) and O of heads 2t and
-        // 2t + 1, each lane its D / 8 dims.
-        const int buf = item_seq % C::MERGE_BUFS;
-        if (!mbar_wait_warp(&B.mempty[buf], ((item_seq / C::MERGE_BUFS) & 1) ^ 1)) {
-            ok = false;
-            break;
-        }
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            l0 += __shfl_xor_sync(FULL, l0, off);
-            l1 += __shfl_xor_sync(FULL, l1, off);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int h = 2 * t + e;
-            if (h < G) {
-                const size_t base = static_cast<size_t>((buf * C::W + warp) * G + h);
-                if (g == 0) ml[base] = make_float2(e ? m1 : m0, e ? l1 : l0);
-                float* dst = mo + base * D + g * (D / 8);
-#pragma unroll
-                for (int j = 0; j < D / 16; j += 2)
-                    *reinterpret_cast<float4*>(dst + 2 * j) =
-                        make_float4(o[j][e], o[j][2 + e], o[j + 1][e], o[j + 1][2 + e]);
-            }
-        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.mfull[buf]);
         ++item_seq;

@@ -100,3 +100,30 @@ def test_a_long_run_of_the_least_scale(pkv, kind, d):
             got = pkv.decode_attention(k, v, q[1:], tables, lens, zeros + 16, 1.0, block_scales=sc, partition_blocks=part)
             assert np.all(np.abs(got[:, 0].double().cpu().numpy() - want[1:]) <= tol[1:])
     assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,g", [(64, 1), (64, 8), (128, 1), (128, 2), (128, 4), (128, 8)])
+@pytest.mark.parametrize("n", [131072, 100003])
+def test_long_contexts_in_one_piece(pkv, kind, d, g, n):
+    """Rows of long contexts that one CTA reads do not come out short: V of one sign, all weights equal.
+
+    Of the sum of |w v|: a warp (8 or 12 of them) adds up 64 MMAs, each off by 2^-23, before it adds them to the rest,
+    n / 4,096 additions off by 2^-24; the weights' sum goes the same way with 36 additions at a time; P's two terms,
+    scales, merge and quotient together are below 2^-20."""
+    rng = np.random.default_rng(n + d + g)
+    k, v = (np.zeros((600, 1, 16, d), kind) for _ in range(2))
+    k[:] = S.encode(rng.standard_normal(k.shape).astype(np.float32) * 30, k)
+    v[:] = S.encode(np.abs(rng.standard_normal(v.shape)).astype(np.float32) * 30 + 20, v)
+    scales = (0.01 * np.exp(0.1 * rng.standard_normal((600, 1, 2)))).astype(np.float32)
+    table = rng.integers(0, 600, -(-n // 16)).astype(np.int32)
+    rows = S.values(v) * scales[..., 1, None, None].astype(np.float64)
+    want = rows[table, 0].reshape(-1, d)[:n].mean(0)
+    q = torch.zeros((1, g, d), dtype=torch.bfloat16, device="cuda")
+    tables, lens = torch.from_numpy(table[None]).cuda(), torch.tensor([n], dtype=torch.int32, device="cuda")
+    for part in (0, len(table)):
+        got = pkv.decode_attention(to_dev(k), to_dev(v), q, tables, lens, n, 0.1, partition_blocks=part,
+                                   block_scales=torch.from_numpy(scales).cuda())
+        off = np.abs(got[0].double().cpu().numpy() / want - 1).max()
+        assert off <= 64 * 2.0 ** -23 + 2 * n / 4096 * 2.0 ** -24 + 36 * 2.0 ** -24 + 2.0 ** -20, f"{off:.2e}"
+    assert pkv.get_error()[0] == 0
