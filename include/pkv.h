@@ -829,6 +829,15 @@ pkv_status pkv_prefix_keys(const int32_t* token_ids, const int32_t* token_start_
 pkv_status pkv_test_arm_decode_stall(int32_t launches);
 
 /*
+ * pkv_test_arm_prefill_stall -- the same for the prefill tiles of
+ * pkv_chunked_prefill_attention over PKV_KV_*_BLOCKS pools: the next `launches`
+ * launches run with a tensor-core warp that issues nothing, so that the others
+ * wait for scores that never come.  The copies that they started have landed
+ * when they leave; the output is not written.
+ */
+pkv_status pkv_test_arm_prefill_stall(int32_t launches);
+
+/*
  * pkv_get_error -- synchronise `stream`, then return (and clear) the first
  * error a kernel recorded on the current device since the last call:
  * PKV_OK, PKV_ERR_RANGE, PKV_ERR_ALIAS, PKV_ERR_NO_BLOCKS or PKV_ERR_TIMEOUT.

@@ -31,6 +31,7 @@ __all__ = [
     "rotary", "rotary_cache_write", "linear_decode_attention", "linear_prefill_attention",
     "linear_prefill_workspace_size",
     "get_error", "Cache", "Blocks", "prefix_keys", "swap_out", "swap_in", "test_arm_decode_stall",
+    "test_arm_prefill_stall",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -140,6 +141,7 @@ def load():
                                           f32, P, P, sz, P], ctypes.c_int),
         "pkv_get_error": ([P, ctypes.POINTER(i32)], ctypes.c_int),
         "pkv_test_arm_decode_stall": ([i32], ctypes.c_int),
+        "pkv_test_arm_prefill_stall": ([i32], ctypes.c_int),
         "pkv_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "pkv_last_cuda_error": ([], ctypes.c_char_p),
         "pkv_version": ([], ctypes.c_char_p),
@@ -1132,6 +1134,12 @@ def test_arm_decode_stall(launches: int) -> None:
     (their producer warp issues nothing; the bounded waits of the other warps
     expire after 2 s and record PKV_ERR_TIMEOUT).  0 disarms."""
     _check(load().pkv_test_arm_decode_stall(int(launches)), "pkv_test_arm_decode_stall")
+
+
+def test_arm_prefill_stall(launches: int) -> None:
+    """Test hook: the same for the next ``launches`` prefill launches over
+    pools with block_scales (their tensor-core warp issues nothing)."""
+    _check(load().pkv_test_arm_prefill_stall(int(launches)), "pkv_test_arm_prefill_stall")
 
 
 def get_error(stream=None) -> Tuple[int, int]:

@@ -41,12 +41,14 @@
 //    warps on a scheduler.  Steps of 64 keys with two sets of scores, the MMAs
 //    of one beside the softmax of the other, pay that chain's fixed part twice:
 //    558 us (300 tokens: 11.2).
-//  * Every wait is bounded; tensor memory is freed on every exit path.
+//  * Every wait is bounded; copies and MMAs have ended and tensor memory is freed
+//    on every exit path.
 #include <cfloat>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -76,7 +78,7 @@ constexpr int kScaleTiles = 3;                       // tiles whose scales are k
 constexpr int OFF_SCALES = OFF_VC + kCodeBytes;      // [kScaleTiles][8 blocks] TileScales
 constexpr int OFF_ROWF = OFF_SCALES + kScaleTiles * kBlocksPerTile * 24;  // [kUnits][128] factor of a row's scores
 constexpr int OFF_BAR = OFF_ROWF + kUnits * kTileM * 4;
-constexpr int NBAR = 20;
+constexpr int NBAR = 21;
 constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
 constexpr int OFF_TMEM = OFF_INFO + 12 * 4;
 constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;     // slack to align the base to 1024 B
@@ -112,6 +114,7 @@ struct Params {
     float* out;
     unsigned long long* err;
     int32_t num_blocks, hkv, hq, num_seqs, num_tokens, max_blocks, ctx_cap, units, split_last;
+    int32_t stall;          // test hook: the MMA warp issues nothing
     float scale_log2;
 };
 
@@ -147,6 +150,7 @@ enum {
     B_SFULL = 14,  // + unit
     B_PFULL = 16,  // + unit (8 warps)
     B_ODONE = 18,  // + unit
+    B_LAST = 20,   // every MMA issued
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -395,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         look_up(0);
+        int k_tiles = 0, v_tiles = 0;  // asked for
         for (int j = 0; j < nt && ok; ++j) {
             const int nvb = min(kBlocksPerTile, nblk - j * kBlocksPerTile);
             const uint32_t bytes = static_cast<uint32_t>(nvb) * kBlockSize * D;
@@ -414,15 +419,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane < nvb)
                 tc::tma_load_3d(smem + OFF_KC + lane * kBlockSize * D, &tm_k, 0, 0, now, &bar[B_KCFULL]);
+            ++k_tiles;
             if (j + 1 < nt) look_up(j + 1);
             if (!mbar_wait_warp(&bar[B_VCEMPTY], (j & 1) ^ 1)) { ok = false; break; }
             if (lane == 0) mbar_arrive_expect_tx(&bar[B_VCFULL], bytes);
             __syncwarp();
             if (lane < nvb)
                 tc::tma_load_3d(smem + OFF_VC + lane * kBlockSize * D, &tm_v, 0, 0, now, &bar[B_VCFULL]);
+            ++v_tiles;
             __syncwarp();
         }
-    } else if (warp == kMmaWarp && nt > 0) {
+        // Never leave with copies in flight, whatever became of the others.
+        ok = mbar_wait_warp(&bar[B_QFULL], 0) && ok;
+        if (k_tiles > 0) ok = mbar_wait_warp(&bar[B_KCFULL], (k_tiles - 1) & 1) && ok;
+        if (v_tiles > 0) ok = mbar_wait_warp(&bar[B_VCFULL], (v_tiles - 1) & 1) && ok;
+    } else if (warp == kMmaWarp && nt > 0 && !P.stall) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescQK = tc::idesc_f16_f32(kTileM, kTileN, 0, 0);
         constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kTileM, D, 0, 1);
@@ -486,6 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (next && tc::elect_one()) tc::mma_commit(&bar[B_KEMPTY + ((j + 1) & 1)]);
             __syncwarp();
         }
+        if (tc::elect_one()) tc::mma_commit(&bar[B_LAST]);
+        __syncwarp();
+        ok = mbar_wait_warp(&bar[B_LAST], 0) && ok;
     } else if (warp < kWidenWarps && nt > 0) {
         uint32_t nan = 0;
         // K and V tile j of the sequence to fp16, this warp's rows.
@@ -857,6 +871,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (KIND != kKindInt8Blocks && *redo && all_ok) redo_rows<D, KIND>(P, T, g, warp, lane);
 }
 
+// Launches still to be made with a stalled MMA warp (test hook).
+std::atomic<int> g_stall_launches{0};
+
+// Takes one armed stall, if any.
+bool take_stall() {
+    int n = g_stall_launches.load();
+    while (n > 0 && !g_stall_launches.compare_exchange_weak(n, n - 1)) {
+    }
+    return n > 0;
+}
+
 template <int D, int KIND>
 cudaError_t launch(const Params& P, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                    cudaStream_t stream) {
@@ -873,6 +898,8 @@ cudaError_t launch(const Params& P, const CUtensorMap& tq, const CUtensorMap& tk
 }
 
 }  // namespace
+
+void arm_prefill_stall(int32_t launches) { g_stall_launches.store(launches); }
 
 cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
     if (a.num_tiles == 0) return cudaSuccess;
@@ -917,6 +944,7 @@ cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
     // Two q heads per CTA when a GQA group holds an even number of them.
     P.units = ((a.num_q_heads / a.num_kv_heads) % 2 == 0) ? 2 : 1;
     P.split_last = P.units == 2 ? a.split_last : 0;
+    P.stall = take_stall() ? 1 : 0;
     P.scale_log2 = a.scale * kLog2e;
     const dim3 grid(static_cast<unsigned>(a.num_tiles + (P.units == 2 ? a.split_tiles : 0)),
                     static_cast<unsigned>(a.num_q_heads / P.units));
