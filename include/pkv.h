@@ -830,8 +830,7 @@ pkv_status pkv_test_arm_decode_stall(int32_t launches);
 
 /*
  * pkv_test_arm_prefill_stall -- the same for the prefill tiles of
- * pkv_chunked_prefill_attention over PKV_KV_*_BLOCKS pools: the next `launches`
- * launches run with a tensor-core warp that issues nothing, so that the others
+ * pkv_chunked_prefill_attention: the next `launches` launches run with a tensor-core warp that issues nothing, so that the others
  * wait for scores that never come.  The copies that they started have landed
  * when they leave; the output is not written.
  */

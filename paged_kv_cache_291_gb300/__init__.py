@@ -1137,8 +1137,8 @@ def test_arm_decode_stall(launches: int) -> None:
 
 
 def test_arm_prefill_stall(launches: int) -> None:
-    """Test hook: the same for the next ``launches`` prefill launches over
-    pools with block_scales (their tensor-core warp issues nothing)."""
+    """Test hook: the same for the next ``launches`` prefill launches (their
+    tensor-core warp issues nothing)."""
     _check(load().pkv_test_arm_prefill_stall(int(launches)), "pkv_test_arm_prefill_stall")
 
 

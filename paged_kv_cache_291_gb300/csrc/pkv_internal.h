@@ -165,9 +165,10 @@ struct PrefillArgs {
 };
 
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
-// Test hook: the next `launches` prefill launches over pools with a scale per
-// block run with an MMA warp that issues nothing (PKV_ERR_TIMEOUT).
+// Test hook: the next `launches` prefill launches run with an MMA warp that
+// issues nothing (PKV_ERR_TIMEOUT).  take_prefill_stall takes one, if any.
 void arm_prefill_stall(int32_t launches);
+bool take_prefill_stall();
 cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream);
 
 // Rotary positions (rotary.cu): q and k rows turned, or q turned and k, v

@@ -39,12 +39,14 @@
 //  * Keys past the last query position of the tile are masked; V rows past
 //    it are zeroed in shared memory during the conversion (a 0 weight
 //    times a NaN in an unused slot would otherwise poison the MMA).
-//  * Every wait is bounded; TMEM is freed on every exit path.
+//  * Every wait is bounded; copies and MMAs have ended and TMEM is freed on every
+//    exit path.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -72,7 +74,7 @@ constexpr int OFF_Q = 0;                             // kUnits Q tiles
 constexpr int OFF_K = OFF_Q + kUnits * kTileBytes;   // 2 stages
 constexpr int OFF_V = OFF_K + 2 * kTileBytes;        // kVStages stages
 constexpr int OFF_BAR = OFF_V + kVStages * kTileBytes;
-constexpr int NBAR = 20;
+constexpr int NBAR = 21;
 constexpr int OFF_INFO = OFF_BAR + NBAR * 8;         // tile info (ints)
 constexpr int OFF_TMEM = OFF_INFO + 16 * 4;
 constexpr int SMEM_USED = OFF_TMEM + 16;
@@ -111,6 +113,7 @@ struct PrefillParams {
     // they hold the most keys) run as two one-head CTAs instead of one
     // two-head CTA (units == 2 only), so that more SMs share them.
     int32_t split_last;
+    int32_t stall;  // test hook: the MMA warp issues nothing
     float scale_log2;
 };
 
@@ -125,6 +128,7 @@ enum {
     B_PFULL = 13,  // +unit (4 arrivals)
     B_ODONE = 15,  // +unit
     B_VCONV = 17,  // +V stage (8 arrivals): V tile converted to fp16
+    B_LAST = 20,   // every MMA issued
 };
 
 // Tile info slots (written by warp 0 before the CTA-wide sync).
@@ -310,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         const int32_t* trow = P.block_tables + static_cast<size_t>(s) * P.max_blocks;
+        int k_tiles = 0, v_tiles = 0;  // asked for
         for (int j = 0; j < nt && ok; ++j) {
             const int st = j & 1;
             const uint32_t ph = (j >> 1) & 1;
@@ -340,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            ++k_tiles;
             const int sv = j % kVStages;
             if (!warp_wait(&bar[B_VEMPTY + sv], ((j / kVStages) & 1) ^ 1)) { ok = false; break; }
             if (lane == 0) {
@@ -355,9 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            ++v_tiles;
             __syncwarp();
         }
-    } else if (warp == kMmaWarp && nt > 0) {
+        // Never leave with copies in flight, whatever became of the others.
+        ok = warp_wait(&bar[B_QFULL], 0) && ok;
+        for (int j = max(k_tiles - 2, 0); j < k_tiles; ++j) ok = warp_wait(&bar[B_KFULL + (j & 1)], (j >> 1) & 1) && ok;
+        for (int j = max(v_tiles - kVStages, 0); j < v_tiles; ++j)
+            ok = warp_wait(&bar[B_VFULL + j % kVStages], (j / kVStages) & 1) && ok;
+    } else if (warp == kMmaWarp && nt > 0 && !P.stall) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t kIdescQK = tc::idesc_bf16_f32(kTileM, kTileN, 0, 0);
         constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kTileM, D, 0, 1);
@@ -422,6 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && next) tc::mma_commit(&bar[B_KEMPTY + ((j + 1) & 1)]);
             __syncwarp();
         }
+        if (lane == 0) tc::mma_commit(&bar[B_LAST]);
+        __syncwarp();
+        ok = warp_wait(&bar[B_LAST], 0) && ok;
     } else if (warp < kConvWarps) {
         // ------------------------------------------------------ V to fp16
         // Warps 0-15 convert each V tile in place, a sixteenth (128 16-byte
@@ -695,6 +710,18 @@ bool make_bf16_map(CUtensorMap* map, const void* base, cuuint32_t rank, const cu
     return make_tile_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box);
 }
 
+// Launches still to be made with a stalled MMA warp (test hook).
+static std::atomic<int> g_stall_launches{0};
+
+void arm_prefill_stall(int32_t launches) { g_stall_launches.store(launches); }
+
+bool take_prefill_stall() {
+    int n = g_stall_launches.load();
+    while (n > 0 && !g_stall_launches.compare_exchange_weak(n, n - 1)) {
+    }
+    return n > 0;
+}
+
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     if (a.head_dim != 64 && a.head_dim != kMaxHeadDim) return cudaErrorNotSupported;
     if (a.num_tiles == 0) return cudaSuccess;
@@ -735,6 +762,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     // Two q heads per CTA when a GQA group holds an even number of them.
     P.units = ((a.num_q_heads / a.num_kv_heads) % 2 == 0) ? 2 : 1;
     P.split_last = P.units == 2 ? a.split_last : 0;
+    P.stall = take_prefill_stall() ? 1 : 0;
     P.scale_log2 = a.scale * kLog2e;
     auto kernel = a.head_dim == 64 ? prefill_kernel<64> : prefill_kernel<kMaxHeadDim>;
     static bool configured[2][64] = {};

@@ -48,7 +48,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -871,17 +870,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (KIND != kKindInt8Blocks && *redo && all_ok) redo_rows<D, KIND>(P, T, g, warp, lane);
 }
 
-// Launches still to be made with a stalled MMA warp (test hook).
-std::atomic<int> g_stall_launches{0};
-
-// Takes one armed stall, if any.
-bool take_stall() {
-    int n = g_stall_launches.load();
-    while (n > 0 && !g_stall_launches.compare_exchange_weak(n, n - 1)) {
-    }
-    return n > 0;
-}
-
 template <int D, int KIND>
 cudaError_t launch(const Params& P, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, dim3 grid,
                    cudaStream_t stream) {
@@ -898,8 +886,6 @@ cudaError_t launch(const Params& P, const CUtensorMap& tq, const CUtensorMap& tk
 }
 
 }  // namespace
-
-void arm_prefill_stall(int32_t launches) { g_stall_launches.store(launches); }
 
 cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
     if (a.num_tiles == 0) return cudaSuccess;
@@ -944,7 +930,7 @@ cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
     // Two q heads per CTA when a GQA group holds an even number of them.
     P.units = ((a.num_q_heads / a.num_kv_heads) % 2 == 0) ? 2 : 1;
     P.split_last = P.units == 2 ? a.split_last : 0;
-    P.stall = take_stall() ? 1 : 0;
+    P.stall = take_prefill_stall() ? 1 : 0;
     P.scale_log2 = a.scale * kLog2e;
     const dim3 grid(static_cast<unsigned>(a.num_tiles + (P.units == 2 ? a.split_tiles : 0)),
                     static_cast<unsigned>(a.num_q_heads / P.units));
