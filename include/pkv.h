@@ -426,7 +426,12 @@ size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t 
  *
  *   q                     bf16 [num_tokens][num_q_heads][head_dim]
  *   query_start_loc       int32 [num_seqs+1], device
- *   query_start_loc_host  the same values on the host (plans the launch)
+ *   query_start_loc_host  the same values on the host (plans the launch).
+ *                         The device's decide whose rows are whose.  Where they
+ *                         differ, a sequence with rows outside the call's or
+ *                         with rows that the plan has no launch for (those are
+ *                         not stored), and starts that decrease, raise
+ *                         PKV_ERR_RANGE (detail: the sequence)
  *   context_lens          int32 [num_seqs], device, including this step's rows
  *   out                   fp32 [num_tokens][num_q_heads][head_dim], device
  *                         memory or page-locked host memory mapped for the

@@ -446,7 +446,8 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
                          const int32_t* query_start_loc, int32_t num_seqs, int32_t max_context_len, float scale,
                          float* out, void* workspace, size_t workspace_bytes, int32_t partition_blocks,
                          void* stream, const void* k_new = nullptr, const void* v_new = nullptr,
-                         const int32_t* slot_mapping = nullptr, int32_t shared_blocks = 0, int32_t num_rows = -1) {
+                         const int32_t* slot_mapping = nullptr, int32_t shared_blocks = 0, int32_t num_rows = -1,
+                         bool prefill_launch = true) {
     pkv_status st = check_cache(cache);
     if (st != PKV_OK) return st;
     if ((st = check_heads(num_q_heads, cache->num_kv_heads)) != PKV_OK) return st;
@@ -492,6 +493,7 @@ pkv_status decode_common(const pkv_cache_t* cache, const void* q, int32_t num_q_
     a.head_dim = cache->head_dim;
     a.num_seqs = num_seqs;
     a.num_rows = num_rows < 0 ? num_seqs : num_rows;
+    a.prefill_launch = prefill_launch;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.max_context_len = max_context_len;
     a.plan = plan;
@@ -639,7 +641,7 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
     if (decode_rows > 0) {
         st = decode_common(cache, q, num_q_heads, block_tables, max_blocks_per_seq, context_lens, query_start_loc,
                            num_seqs, max_context_len, scale, out, workspace, workspace_bytes, 0, stream, nullptr,
-                           nullptr, nullptr, 0, num_tokens);
+                           nullptr, nullptr, 0, num_tokens, tiles > 0);
         if (st != PKV_OK) return st;
     }
     if (tiles > 0) {
@@ -679,6 +681,7 @@ PKV_API pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const
             a.split_last = k;
             a.split_tiles = static_cast<int32_t>(extra);
         }
+        a.decode_launch = decode_rows > 0;
         a.scale = scale;
         a.block_scales = scaled(cache) ? cache->block_scales : nullptr;
         a.int8_codes = cache->kv_dtype == PKV_KV_INT8_BLOCKS;

@@ -164,6 +164,7 @@ struct DecodeParams {
     // an item costs however short it is; they hold no keys.
     int32_t extra_units;
     int32_t num_rows;  // of q and out
+    int32_t prefill_launch;  // rows of longer sequences have a launch of their own
 };
 
 constexpr int align_up(int x, int a) { return (x + a - 1) / a * a; }
@@ -354,6 +355,8 @@ __device__ __forceinline__ int extra_units(const DecodeParams& P, long long T) {
 __device__ __forceinline__ int seq_units(const DecodeParams& P, int s, int& n_out, bool report) {
     const int qlen = P.qsl ? (__ldg(P.qsl + s + 1) - __ldg(P.qsl + s)) : 1;
     if (qlen != 1) {
+        if (report && (qlen < 0 || (qlen > 1 && !P.prefill_launch)))
+            record_error(P.err, kErrRange, static_cast<uint32_t>(s));
         n_out = 0;
         return 0;
     }
@@ -1857,6 +1860,7 @@ inline DecodeParams decode_params(const DecodeArgs& a, bool stall) {
     P.block_scales = reinterpret_cast<const float2*>(a.block_scales);
     P.extra_units = 0;
     P.num_rows = a.num_rows;
+    P.prefill_launch = a.prefill_launch ? 1 : 0;
     P.stall = stall ? 1 : 0;
     P.k_new = static_cast<const uint8_t*>(a.k_new);
     P.v_new = static_cast<const uint8_t*>(a.v_new);

@@ -35,6 +35,7 @@ struct DecodeArgs {
     int32_t num_blocks, num_kv_heads, num_q_heads, head_dim;
     int32_t num_seqs, max_blocks_per_seq, max_context_len;
     int32_t num_rows;              // of q and out
+    bool prefill_launch = true;    // longer sequences of the batch have a launch of their own
     DecodePlan plan;
     float scale;
     bool kv_e4m3;                  // pools hold e4m3 codes with one scale a pool
@@ -158,6 +159,7 @@ struct PrefillArgs {
     int32_t num_seqs, num_tokens, max_blocks_per_seq, max_context_len;
     int32_t num_tiles;                // query tiles of the prefill sequences
     int32_t split_last;               // last row tiles of each sequence split by head (two-head CTAs only)
+    bool decode_launch;               // single rows have a launch of their own
     int32_t split_tiles;              // tiles so split over all sequences (extra CTAs per head pair)
     float scale;
     const float* block_scales = nullptr;  // 8-bit pools with a scale per (block, kv head), else null

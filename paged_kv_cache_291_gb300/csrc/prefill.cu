@@ -113,6 +113,7 @@ struct PrefillParams {
     // they hold the most keys) run as two one-head CTAs instead of one
     // two-head CTA (units == 2 only), so that more SMs share them.
     int32_t split_last;
+    int32_t decode_launch;  // the call's decode rows have a launch of their own
     int32_t stall;  // test hook: the MMA warp issues nothing
     float scale_log2;
 };
@@ -660,6 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float wmax = warp_max(vmax);
         if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(&info[I_VMAX]), __float_as_uint(wmax));
     }
+    if (warp == kLoadWarp && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
+        report_unplanned_rows(P.qsl, P.num_seqs, P.units, P.split_last, gridDim.x, P.decode_launch != 0, P.err, lane);
     if (!ok) record_error(P.err, kErrTimeout, 0x100u + static_cast<uint32_t>(warp));
     // ---------------------------------------------------------- teardown
     tc::fence_before_sync();
@@ -762,6 +765,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
     // Two q heads per CTA when a GQA group holds an even number of them.
     P.units = ((a.num_q_heads / a.num_kv_heads) % 2 == 0) ? 2 : 1;
     P.split_last = P.units == 2 ? a.split_last : 0;
+    P.decode_launch = a.decode_launch ? 1 : 0;
     P.stall = take_prefill_stall() ? 1 : 0;
     P.scale_log2 = a.scale * kLog2e;
     auto kernel = a.head_dim == 64 ? prefill_kernel<64> : prefill_kernel<kMaxHeadDim>;

@@ -113,6 +113,7 @@ struct Params {
     float* out;
     unsigned long long* err;
     int32_t num_blocks, hkv, hq, num_seqs, num_tokens, max_blocks, ctx_cap, units, split_last;
+    int32_t decode_launch;  // the call's decode rows have a launch of their own
     int32_t stall;          // test hook: the MMA warp issues nothing
     float scale_log2;
 };
@@ -861,6 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
+    if (warp == kLoadWarp && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
+        report_unplanned_rows(P.qsl, P.num_seqs, P.units, P.split_last, gridDim.x, P.decode_launch != 0, P.err, lane);
     if (!ok) record_error(P.err, kErrTimeout, 0x100u + static_cast<uint32_t>(warp));
     // ---------------------------------------------------------- teardown
     tc::fence_before_sync();
@@ -930,6 +933,7 @@ cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
     // Two q heads per CTA when a GQA group holds an even number of them.
     P.units = ((a.num_q_heads / a.num_kv_heads) % 2 == 0) ? 2 : 1;
     P.split_last = P.units == 2 ? a.split_last : 0;
+    P.decode_launch = a.decode_launch ? 1 : 0;
     P.stall = take_prefill_stall() ? 1 : 0;
     P.scale_log2 = a.scale * kLog2e;
     const dim3 grid(static_cast<unsigned>(a.num_tiles + (P.units == 2 ? a.split_tiles : 0)),
