@@ -450,9 +450,8 @@ size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t 
  *   such tiles.  head_dim 64 or 128.  An e4m3 pool with one scale gives
  *   PKV_ERR_DTYPE.
  *   PKV_KV_*_BLOCKS pools: as for pkv_decode_attention; query rows are off
- *   by up to 1e-6 of their norm.  Where V holds a NaN code among a tile's keys,
- *   the tile's rows are computed again on CUDA cores.  The call uses out as
- *   scratch before it stores the rows there.
+ *   by up to 1e-6 of their norm.  A NaN code in V reaches the rows that see it,
+ *   in its dim.  The call uses out as scratch before it stores the rows there.
  */
 pkv_status pkv_chunked_prefill_attention(const pkv_cache_t* cache, const void* q, int32_t num_q_heads,
                                          int32_t num_tokens, const int32_t* query_start_loc,

@@ -31,11 +31,12 @@
 //    2^(s_j - m + 3), each the square of an exponential of half that, which fp32
 //    holds for every scale; sums move to other references in two such halves.
 //  * A NaN code in V (the append stores one for a NaN) would reach, as 0 times
-//    NaN, the rows of its tile that do not see it: such a CTA's rows are done
-//    again on CUDA cores.
-//  * Measured: 2,048 of 16,384 tokens, 16/8 x 128, 454 us, 568 TFLOP/s (the two
-//    terms of P make it 850 of the tensor cores' work); 300 tokens, 32/8 x 64,
-//    12.6 us.  A tile of two heads takes some 7,000 cycles, 3,300 of MMAs; issue
+//    NaN, the rows of its tile that do not see it.  So in tiles that not all rows
+//    see NaN codes are widened to zeros, each dim keeps the first of the CTA's rows
+//    that sees one, and from that row on its output is set to NaN after the store.
+//  * Measured: 2,048 of 16,384 tokens, 16/8 x 128, 462 us, 558 TFLOP/s (the two
+//    terms of P make it 835 of the tensor cores' work); 300 tokens, 32/8 x 64,
+//    12.7 us.  A tile of two heads takes some 7,000 cycles, 3,300 of MMAs; issue
 //    slots are 48 % busy, the ALU 39 %: what bounds it is each warp's chain
 //    through a tile, wait, scores, shuffles, exponentials, stores, with four
 //    warps on a scheduler.  Steps of 64 keys with two sets of scores, the MMAs
@@ -79,7 +80,8 @@ constexpr int OFF_ROWF = OFF_SCALES + kScaleTiles * kBlocksPerTile * 24;  // [kU
 constexpr int OFF_BAR = OFF_ROWF + kUnits * kTileM * 4;
 constexpr int NBAR = 21;
 constexpr int OFF_INFO = OFF_BAR + NBAR * 8;
-constexpr int OFF_TMEM = OFF_INFO + 12 * 4;
+constexpr int OFF_NANS = OFF_INFO + 12 * 4;          // [D] first row that sees a NaN of V, 255: none
+constexpr int OFF_TMEM = OFF_NANS + 128;
 constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;     // slack to align the base to 1024 B
 static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB)");
 static_assert(2 * SMEM_BYTES > 228 * 1024, "the 512-column TMEM allocation needs one CTA per SM");
@@ -103,9 +105,6 @@ constexpr float kThreshold = 3.0f, kShift = 12.0f;   // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
-    const uint8_t* q;       // bf16 [num_tokens][hq][D] (for the redo)
-    const uint8_t* k_pool;
-    const uint8_t* v_pool;
     const float2* scales;   // [num_blocks][hkv]
     const int32_t* block_tables;
     const int32_t* context_lens;
@@ -191,13 +190,45 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
     }
 }
 
+// Where 16 codes of V have NaNs: zeros in place of their fp16 values, at chunks at0
+// and at1 of a panel; first_row[dim], of four dims a word, becomes `row` for those
+// dims unless it is smaller.
+__device__ __noinline__ void take_nans(uint32_t codes, uint32_t at0, uint32_t at1, uint32_t* first_row, int row) {
+    uint32_t x[4], h[4];
+    tc::lds128(codes, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t nan = __vcmpeq4(x[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        if (i % 2 == 0) tc::lds128(i ? at1 : at0, h);
+        h[2 * (i % 2)] &= ~__byte_perm(nan, 0u, 0x1100);
+        h[2 * (i % 2) + 1] &= ~__byte_perm(nan, 0u, 0x3322);
+        if (i % 2) tc::sts128(i > 1 ? at1 : at0, h[0], h[1], h[2], h[3]);
+        if (nan == 0) continue;
+        const uint32_t from = (0x01010101u * static_cast<uint32_t>(row)) | ~nan;
+        for (uint32_t was = first_row[i], now; (now = __vminu4(was, from)) != was;) {
+            const uint32_t found = atomicCAS(first_row + i, was, now);
+            if (found == was) break;
+            was = found;
+        }
+    }
+}
+
+// NaN over the elements of a row, columns col + 8 i and one on, that see one.
+__device__ __noinline__ void store_nans(float* out, const uint8_t* first_row, int row, int col, int dims) {
+    for (; col < dims; col += 8)
+        for (int i = 0; i < 2; ++i)
+            if (row >= first_row[col + i]) out[col + i] = NAN;
+}
+
 // A warp's eighth rows of a tile, codes [128][D] to fp16 panels; rows >= nrows
 // become zero.  Lane l takes 16 codes of row 8 warp + 2 (l / 8) + (l / 4) % 2:
 // at head_dim 128 neighbouring rows take different halves of their chunks, so
 // that neither the eight lanes that load nor those that store together meet in
-// a bank.  Returns non-zero top bits where a visible code is NaN.
-template <int D, int KIND>
-__device__ __forceinline__ uint32_t widen_rows(uint32_t codes, uint32_t tile, int warp, int lane, int nrows) {
+// a bank.  NANS: NaN codes become zero (take_nans), rows of the CTA from r -
+// sees_all on see row r of the tile.
+template <int D, int KIND, bool NANS>
+__device__ __forceinline__ void widen_rows(uint32_t codes, uint32_t tile, int warp, int lane, int nrows,
+                                           uint32_t* first_row = nullptr, int sees_all = 0) {
     constexpr int PASSES = D / 64;
     const int rr = (lane >> 2) & 1, row = 8 * warp + 2 * (lane >> 3) + rr;
     uint32_t x[PASSES][4];
@@ -211,7 +242,7 @@ __device__ __forceinline__ uint32_t widen_rows(uint32_t codes, uint32_t tile, in
     for (int s = 0; s < PASSES; ++s) {
         const int c = PASSES == 2 ? (lane & 3) + 4 * (rr ^ s) : lane & 3;
         if (row >= nrows) x[s][0] = x[s][1] = x[s][2] = x[s][3] = 0u;
-        if constexpr (KIND != kKindInt8Blocks) {
+        if constexpr (NANS) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) nan |= (x[s][i] & 0x7f7f7f7fu) + 0x01010101u;
         }
@@ -224,7 +255,24 @@ __device__ __forceinline__ uint32_t widen_rows(uint32_t codes, uint32_t tile, in
             tc::sts128(at + (((2 * (c & 3) + i) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
         }
     }
-    return nan & 0x80808080u;
+    if (NANS && (nan & 0x80808080u)) {
+#pragma unroll
+        for (int s = 0; s < PASSES; ++s) {
+            const int c = PASSES == 2 ? (lane & 3) + 4 * (rr ^ s) : lane & 3;
+            const uint32_t at = tile + (c >> 2) * kPanelBytes + row * 128;
+            take_nans(codes + row * D + c * 16, at + (((2 * (c & 3)) ^ (row & 7)) << 4),
+                      at + (((2 * (c & 3) + 1) ^ (row & 7)) << 4), first_row + 4 * c,
+                      max(row - sees_all, 0));
+        }
+    }
+}
+
+// The same for a tile of V that may hold NaN codes and that not all rows see: the
+// last one or two of a CTA's, out of line.
+template <int D, int KIND>
+__device__ __noinline__ void widen_last_v(uint32_t codes, uint32_t tile, int warp, int lane, int nrows,
+                                          uint32_t* first_row, int sees_all) {
+    widen_rows<D, KIND, true>(codes, tile, warp, lane, nrows, first_row, sees_all);
 }
 
 // A block's factor of a row's scores, never so small that it would turn what
@@ -255,57 +303,6 @@ __device__ __noinline__ float2 wide_sums(uint32_t ts, const TileScales* sct, flo
     return make_float2(la, lb);
 }
 
-// A CTA's rows on CUDA cores, for V with NaN codes: warp w takes the (row,
-// unit) items w, w + 18, ...; lane l owns D / 32 consecutive dims; keys in order
-// with a running maximum and sum.
-template <int D, int KIND>
-__device__ __noinline__ void redo_rows(const Params& P, const PrefillTile& T, int g, int warp, int lane) {
-    constexpr int DPL = D / 32;
-    const int32_t* trow = P.block_tables + static_cast<size_t>(T.s) * P.max_blocks;
-    for (int item = warp; item < T.rows * T.units; item += kThreads / 32) {
-        const int m = item / T.units, h = T.h0 + item % T.units;
-        const size_t at = (static_cast<size_t>(T.row0 + m) * P.hq + h) * D + lane * DPL;
-        float q[DPL], o[DPL];
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) {
-            q[i] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(P.q)[at + i]) << 16) *
-                   P.scale_log2;
-            o[i] = 0.f;
-        }
-        float mx = -INFINITY, l = 0.f;
-        for (int j = 0; j <= T.pmin + m; ++j) {
-            int phys = __ldg(trow + j / kBlockSize);
-            if (phys < 0 || phys >= P.num_blocks) phys = 0;  // reported by the tensor-core pass already
-            const size_t slab = static_cast<size_t>(phys) * P.hkv + g;
-            const float2 s = __ldg(P.scales + slab);
-            bool bad = false;
-            const float ks = checked_scale(s.x, bad), vs = checked_scale(s.y, bad);
-            const size_t src = (slab * kBlockSize + j % kBlockSize) * D + lane * DPL;
-            uint32_t wk = 0, wv = 0;
-#pragma unroll
-            for (int i = 0; i < DPL; ++i) {
-                wk |= static_cast<uint32_t>(P.k_pool[src + i]) << (8 * i);
-                wv |= static_cast<uint32_t>(P.v_pool[src + i]) << (8 * i);
-            }
-            float k[4], v[4];
-            decode4<KIND>(wk, k);
-            decode4<KIND>(wv, v);
-            float part = 0.f;
-#pragma unroll
-            for (int i = 0; i < DPL; ++i) part = fmaf(q[i], k[i], part);
-            const float x = warp_sum(part) * ks;
-            const float mn = fmaxf(mx, x);
-            const float alpha = mx == mn ? 1.f : fast_exp2(mx - mn), p = fast_exp2(x - mn);
-            mx = mn;
-            l = fmaf(l, alpha, p);
-#pragma unroll
-            for (int i = 0; i < DPL; ++i) o[i] = fmaf(p, v[i] * vs, o[i] * alpha);
-        }
-#pragma unroll
-        for (int i = 0; i < DPL; ++i) P.out[at + i] = o[i] / l;
-    }
-}
-
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_scaled_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -315,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     PrefillTile* info = reinterpret_cast<PrefillTile*>(smem + OFF_INFO);
-    int* redo = reinterpret_cast<int*>(smem + OFF_INFO + sizeof(PrefillTile));
-    static_assert(sizeof(PrefillTile) + 4 <= 12 * 4, "info");
+    uint8_t* first_row = smem + OFF_NANS;
+    constexpr bool kNans = KIND != kKindInt8Blocks;
+    static_assert(sizeof(PrefillTile) <= 12 * 4, "info");
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     float* rowf = reinterpret_cast<float*>(smem + OFF_ROWF);
     TileScales* scales = reinterpret_cast<TileScales*>(smem + OFF_SCALES);
@@ -329,10 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         griddep_wait();
         const PrefillTile t = find_prefill_tile(P.qsl, P.context_lens, P.num_seqs, P.num_tokens, P.ctx_cap, P.units,
                                                 P.split_last, blockIdx.x, blockIdx.y, P.err, lane);
-        if (lane == 0) {
-            *info = t;
-            *redo = 0;
-        }
+        if (lane == 0) *info = t;
+        if (kNans) reinterpret_cast<uint32_t*>(first_row)[lane] = 0xffffffffu;
     }
     if (threadIdx.x == 32 * kMmaWarp) {
         for (int i = 0; i < NBAR; ++i) {
@@ -501,14 +497,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ok = mbar_wait_warp(&bar[B_LAST], 0) && ok;
     } else if (warp < kWidenWarps && nt > 0) {
-        uint32_t nan = 0;
         // K and V tile j of the sequence to fp16, this warp's rows.
         auto widen_k = [&](int j) -> bool {
             if (!mbar_wait_warp(&bar[B_KCFULL], j & 1) ||
                 !mbar_wait_warp(&bar[B_KEMPTY + (j & 1)], ((j >> 1) & 1) ^ 1))
                 return false;
-            widen_rows<D, KIND>(smem_addr(smem + OFF_KC), smem_addr(smem + OFF_K + (j & 1) * kTileBytes), warp, lane,
-                                kTileN);
+            widen_rows<D, KIND, false>(smem_addr(smem + OFF_KC), smem_addr(smem + OFF_K + (j & 1) * kTileBytes), warp,
+                                       lane, kTileN);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -521,8 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!mbar_wait_warp(&bar[B_VCFULL], j & 1) ||
                 !mbar_wait_warp(&bar[B_VEMPTY + (j & 1)], ((j >> 1) & 1) ^ 1))
                 return false;
-            nan |= widen_rows<D, KIND>(smem_addr(smem + OFF_VC), smem_addr(smem + OFF_V + (j & 1) * kTileBytes), warp,
-                                       lane, j == nt - 1 ? T.klast : kTileN);
+            const uint32_t codes = smem_addr(smem + OFF_VC), tile = smem_addr(smem + OFF_V + (j & 1) * kTileBytes);
+            const int nrows = j == nt - 1 ? T.klast : kTileN, sees_all = T.pmin - j * kTileN;
+            if (kNans && sees_all < kTileN - 1)
+                widen_last_v<D, KIND>(codes, tile, warp, lane, nrows, reinterpret_cast<uint32_t*>(first_row), sees_all);
+            else
+                widen_rows<D, KIND, false>(codes, tile, warp, lane, nrows);
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -794,7 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float4* dst = pieces() + static_cast<size_t>(8 * c) * pitch;
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                dst[static_cast<size_t>(i) * pitch] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                                dst[static_cast<size_t>(i) * pitch] =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                         } else {
                             store_rows(c, x);
                         }
@@ -851,9 +851,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     join(1, y, fac_a * inva, fac_b * invb, inva, invb);
                     store_rows(1, y);
                 }
+                if constexpr (kNans) {
+                    // Rows from a dim's first_row on see a NaN there.
+                    bool any = false;
+                    for (int i = lane; i < D / 4; i += 32)
+                        any |= reinterpret_cast<const volatile uint32_t*>(first_row)[i] != 0xffffffffu;
+                    if (__any_sync(FULL, any)) {
+                        if (ma < T.rows) store_nans(row_at(ma), first_row, ma, 2 * tq, D);
+                        if (mb < T.rows) store_nans(row_at(mb), first_row, mb, 2 * tq, D);
+                    }
+                }
             }
         }
-        if (__any_sync(FULL, nan != 0) && lane == 0) atomicOr(redo, 1);
     } else if (warp < kWidenWarps && T.bad && T.s >= 0) {
         // Zero rows for a sequence whose arguments are out of range.
         for (int i = threadIdx.x; i < T.rows * units * (D / 4); i += kWidenWarps * 32) {
@@ -867,10 +876,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) record_error(P.err, kErrTimeout, 0x100u + static_cast<uint32_t>(warp));
     // ---------------------------------------------------------- teardown
     tc::fence_before_sync();
-    const bool all_ok = __syncthreads_and(ok);
+    __syncthreads();
     tc::fence_after_sync();
     if (warp == kLoadWarp) tc::tmem_dealloc(tmem, kTmemCols);
-    if (KIND != kKindInt8Blocks && *redo && all_ok) redo_rows<D, KIND>(P, T, g, warp, lane);
 }
 
 template <int D, int KIND>
@@ -913,9 +921,6 @@ cudaError_t launch_prefill_scaled(const PrefillArgs& a, cudaStream_t stream) {
             return cudaErrorInvalidValue;
     }
     Params P;
-    P.q = static_cast<const uint8_t*>(a.q);
-    P.k_pool = static_cast<const uint8_t*>(a.k_pool);
-    P.v_pool = static_cast<const uint8_t*>(a.v_pool);
     P.scales = reinterpret_cast<const float2*>(a.block_scales);
     P.block_tables = a.block_tables;
     P.context_lens = a.context_lens;
