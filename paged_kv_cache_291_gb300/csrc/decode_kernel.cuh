@@ -343,7 +343,9 @@ __device__ __forceinline__ long long auto_range_units(long long T, unsigned grid
 }
 
 // What a pair counts beyond its blocks in the cut of T blocks of work: nothing
-// where the CTAs have few, whose pairs it would only split.
+// where the CTAs have few, whose pairs it would only split (16 contexts of 200 to
+// 1,679 tokens, 8 kv heads x 128: 16.7 us with the 4, 17.8 with 1 or 2; 24 with
+// groups of 8 23.9, 22.2 with 8 in its place, all else within 1 %).
 __device__ __forceinline__ int extra_units(const DecodeParams& P, long long T) {
     return P.extra_units > 0 && T >= 4ll * P.extra_units * gridDim.x ? P.extra_units : 0;
 }

@@ -67,9 +67,12 @@ struct ScaledCfg {
     static constexpr int MERGE_LANES = W <= 8 ? 8 : 16;
     // What a pair costs beyond its blocks, in blocks: its warps' states are
     // handed over and merged, and its last stages leave warps idle.  Without
-    // it the CTA that gets the short contexts ends last (31 contexts of 300
-    // to 4,096 tokens, 64/8 x 128: 44.2 us with 0, 41.6 with 4, 37 with 8 and
-    // 16; 68 contexts of 40/40 x 128: 359 with 0, 340 with 8 and 16).
+    // it the CTA that gets the short contexts ends last.  One number for all
+    // shapes: over 31 contexts of 300 to 4,011 tokens and 68 of 64 to 32,768,
+    // both head_dims, groups of 1, 2, 4 and 8, 0 takes 1.20 of the time with
+    // 12, 4 1.14, 8 1.05, 16 1.00 and 24 1.02, and 12 is at most 6 % above the
+    // best in any of them; 8 to 64 contexts of 200 to 1,679 tokens: 0 takes 1.05,
+    // 8 1.00, 16 1.01, 24 1.00.
     static constexpr int EXTRA_UNITS = 12;
     static constexpr int MERGE_BUFS = 1;
     static constexpr int MERGERS = G == 8 ? 2 : 1;
