@@ -245,9 +245,8 @@ struct Bars {
 
 // A stage a consumer warp is to load: the slabs of its blocks (the second if
 // `two`) and their scales, K's and V's, the latter as f 2^e with f in [1, 2).
-// inv_2e: 2^-(e + kSumShift), or zero where the item's V scales up to here are
-// more than 2^kWideSpread apart or one is above 2^kWideTop: the sum's terms are
-// then exponentials of their own.
+// inv_2e: 2^-(e + kSumShift).  Of a block far below the item's largest e so far, f
+// and inv_2e are 2^-kLift times that (see lifted).
 struct __align__(16) BlockScales {
     float k, f, e, inv_2e;
 };
@@ -256,15 +255,18 @@ struct __align__(16) Order {
     BlockScales scales[2];
 };
 
-// A key whose u = 2^(s + e - m + 11) is flushed to zero (below 2^-126; m is at
-// most the largest s plus the largest e) weighs less than 2^-(137 - spread) of
-// the largest 2^s: 2^-33 here, as little as what two fp16 terms drop.
-constexpr int kWideSpread = 104;
+// u = 2^(s + e - m + 11) is flushed to zero below 2^-126, and m is at most the
+// largest s plus the largest e: of blocks more than kWideSpread below that, keys
+// would be missing from the sum that weigh 2^-(137 - spread) of the largest 2^s.
+// Their u is 2^kLift times as large (below 2^127), f and inv_2e undo it; then what
+// is missing weighs below 2^-33 up to a spread of 216, 2^-29 at that of bf16's
+// whole range.
+constexpr int kWideSpread = 104, kLift = 112;
 // The sum's terms are 2^(s - m + 11 - kSumShift), and m is at least s + e - 3:
 // below 2^107 at the least scale, so that 2^21 keys of a warp fit fp32 (without
 // the shift 2^14 keys of zero rows would end beyond it).  The largest is at least
 // 2^(3 - 122).
-constexpr int kSumShift = 8, kWideTop = 100;
+constexpr int kSumShift = 8;
 
 __device__ __forceinline__ BlockScales block_scales_of(float2 s, bool& bad) {
     BlockScales r;
@@ -273,9 +275,17 @@ __device__ __forceinline__ BlockScales block_scales_of(float2 s, bool& bad) {
     const int e = static_cast<int>(bits >> 23) - 127;
     r.f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
     r.e = static_cast<float>(e);
-    r.inv_2e = __uint_as_float(static_cast<uint32_t>(max(127 - kSumShift - e, 0)) << 23);
+    r.inv_2e = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (1.f / (1 << kSumShift));
     return r;
 }
+
+__device__ __forceinline__ void lift(BlockScales& s) {
+    constexpr float down = 1.f / (1ull << (kLift / 2)) / (1ull << (kLift / 2));
+    s.f *= down;
+    s.inv_2e *= down;
+}
+// What u's exponent takes.
+__device__ __forceinline__ float lifted(const BlockScales& s) { return s.f < 1.f ? static_cast<float>(kLift) : 0.f; }
 
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
@@ -731,7 +741,7 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
             constexpr int kBatch = 32 < C::ORDERS / 2 * C::W ? 32 : C::ORDERS / 2 * C::W;
             Order* orders = reinterpret_cast<Order*>(smem + C::OFF_ORDERS);
             const int nst = (b1 - b0 + 1) / 2;
-            int high = -1000, low = 1000;  // exponents of the item's V scales so far
+            int high = -1000;  // largest exponent of the item's V scales so far
             for (int base = 0; base < nst; base += kBatch) {
                 const int cnt = min(kBatch, nst - base);
                 const int next = b0 + 2 * (base + kBatch + lane);
@@ -758,14 +768,14 @@ __device__ void run_producer(const DecodeParams& P, const CUtensorMap* tmk, cons
                         o.slab[x] = id * P.hkv + g;
                         o.scales[x] = block_scales_of(__ldg(P.block_scales + o.slab[x]), bad_scale);
                         high = max(high, static_cast<int>(o.scales[x].e));
-                        low = min(low, static_cast<int>(o.scales[x].e));
                     }
                     if (bad_scale) record_error(P.err, kErrRange, static_cast<uint32_t>(s));
                 }
                 high = __reduce_max_sync(FULL, high);
-                low = __reduce_min_sync(FULL, low);
                 if (lane < cnt) {
-                    if (high - low > kWideSpread || high > kWideTop) o.scales[0].inv_2e = o.scales[1].inv_2e = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (static_cast<int>(o.scales[x].e) < high - kWideSpread) lift(o.scales[x]);
                     const uint32_t at = static_cast<uint32_t>(w * C::ORDERS) + jw % C::ORDERS;
                     if (!mbar_wait(&B.oempty[at], ((jw / C::ORDERS) & 1) ^ 1)) {
                         bad = 1;

@@ -32,10 +32,10 @@
 //    u f and the term of the sum u 2^-(e + 8), and weights end 2^-36 below the largest
 //    (fp16 is exact to 2^-24).  A key of a small V scale may count for nothing in
 //    O and for all in the sum (16 rows of zeros, whose scale is 2^-100, beside
-//    one of scale 2^40: v / 17).  So where an item's V scales are more than 2^104
-//    apart the sum's terms are 2^(s_j - m + 3), each the square of an
-//    exponential of half that, which fp32 holds for every scale, and sums move
-//    to other references in two such halves.
+//    one of scale 2^40: v / 17), so u is 2^112 larger in blocks whose V scale is
+//    more than 2^104 below the item's largest, and sums move to other references
+//    by two factors of half the logarithm, since 2^x may be flushed where the sum
+//    times 2^x is not.
 //  * The order of dims in S and of keys in P V is free: a lane reads whole
 //    16-byte pieces of K rows and of V rows (8-byte pieces of V at head_dim
 //    64), and rows are dealt to lanes so that the lanes that read together hit
@@ -429,21 +429,12 @@ __device__ void run_consumer_scaled(const DecodeParams& P, const CUtensorMap* tm
                     for (int j = 0; j < D / 16; ++j) o[j][0] *= a0, o[j][1] *= a1, o[j][2] *= a0, o[j][3] *= a1;
                 }
                 const float add0 = __fsub_rd(kScaledShift, m0), add1 = __fsub_rd(kScaledShift, m1);
-                if (sc[0].inv_2e == 0.f) {  // V scales far apart, or large
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) {
-                        const float s0 = add0 - (sc[i].e + kSumShift), s1 = add1 - (sc[i].e + kSumShift);
-                        const float t0 = fast_exp2(0.5f * (u[i][0] + s0)), t1 = fast_exp2(0.5f * (u[i][1] + s1));
-                        const float t2 = fast_exp2(0.5f * (u[i][2] + s0)), t3 = fast_exp2(0.5f * (u[i][3] + s1));
-                        l0 += fmaf(t0, t0, t2 * t2);
-                        l1 += fmaf(t1, t1, t3 * t3);
-                    }
-                }
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     if (i > 0 && valid[i] == 0) break;
-                    u[i][0] = fast_exp2(u[i][0] + add0), u[i][1] = fast_exp2(u[i][1] + add1);
-                    u[i][2] = fast_exp2(u[i][2] + add0), u[i][3] = fast_exp2(u[i][3] + add1);
+                    const float up = lifted(sc[i]), up0 = add0 + up, up1 = add1 + up;
+                    u[i][0] = fast_exp2(u[i][0] + up0), u[i][1] = fast_exp2(u[i][1] + up1);
+                    u[i][2] = fast_exp2(u[i][2] + up0), u[i][3] = fast_exp2(u[i][3] + up1);
                     l0 = fmaf(u[i][0] + u[i][2], sc[i].inv_2e, l0);
                     l1 = fmaf(u[i][1] + u[i][3], sc[i].inv_2e, l1);
                     uint32_t p[4];
