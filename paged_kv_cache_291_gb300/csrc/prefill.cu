@@ -269,6 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             info[I_VMAX] = 0;  // largest |v| the converters see (fp32 bits; non-negative floats order as ints)
         }
     }
+    if (warp == 1 && blockIdx.x == 0 && blockIdx.y == 0) {
+        griddep_wait();
+        report_unplanned_rows(P.qsl, P.num_seqs, P.split_last, gridDim.x, P.decode_launch, P.err, lane);
+    }
     if (threadIdx.x == 32 * kMmaWarp) {
         for (int i = 0; i < NBAR; ++i)
             mbar_init(&bar[i], (i == B_PFULL || i == B_PFULL + 1) ? kSoftmaxWarps
@@ -661,8 +665,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float wmax = warp_max(vmax);
         if (lane == 0) atomicMax(reinterpret_cast<unsigned int*>(&info[I_VMAX]), __float_as_uint(wmax));
     }
-    if (warp == kLoadWarp && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
-        report_unplanned_rows(P.qsl, P.num_seqs, P.units, P.split_last, gridDim.x, P.decode_launch != 0, P.err, lane);
     if (!ok) record_error(P.err, kErrTimeout, 0x100u + static_cast<uint32_t>(warp));
     // ---------------------------------------------------------- teardown
     tc::fence_before_sync();

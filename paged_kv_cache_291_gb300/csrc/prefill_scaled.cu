@@ -330,6 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) *info = t;
         if (kNans) reinterpret_cast<uint32_t*>(first_row)[lane] = 0xffffffffu;
     }
+    if (warp == 1 && blockIdx.x == 0 && blockIdx.y == 0) {
+        griddep_wait();
+        report_unplanned_rows(P.qsl, P.num_seqs, P.split_last, gridDim.x, P.decode_launch, P.err, lane);
+    }
     if (threadIdx.x == 32 * kMmaWarp) {
         for (int i = 0; i < NBAR; ++i) {
             const bool widened = i == B_KCEMPTY || i == B_VCEMPTY || (i >= B_KCONV && i < B_KEMPTY) ||
@@ -871,8 +875,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
-    if (warp == kLoadWarp && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0)
-        report_unplanned_rows(P.qsl, P.num_seqs, P.units, P.split_last, gridDim.x, P.decode_launch != 0, P.err, lane);
     if (!ok) record_error(P.err, kErrTimeout, 0x100u + static_cast<uint32_t>(warp));
     // ---------------------------------------------------------- teardown
     tc::fence_before_sync();

@@ -93,37 +93,27 @@ __device__ __forceinline__ PrefillTile find_prefill_tile(const int32_t* qsl, con
     return r;
 }
 
-// Reports the first sequence that the device's starts give rows for which the
-// plan from the host's has nothing: a prefill sequence that needs more entries
-// than the grid's `entries`, a decode row in a call without a decode launch; or
-// a start below the one before.
-// For a whole warp of one CTA, off its critical path; out of line, which cost
-// the softmax warps' code less (2,048 of 16,384 tokens, 8-bit pools: 462 us, 465
-// inlined, 459 without the check).
-static __device__ __noinline__ void report_unplanned_rows(const int32_t* qsl, int num_seqs, int cta_units,
-                                                          int split_last, int entries, bool decode_launch,
-                                                          unsigned long long* err, int lane) {
+// Reports a sequence that the device's starts give rows for which the plan from
+// the host's has nothing: the last prefill sequence where they need more entries
+// than the grid's `entries`, a decode row in a call without a decode launch; or a
+// start below the one before.  For a whole warp of the CTA with the fewest keys,
+// beside the search for its tile (2,048 of 16,384 tokens, 8-bit pools: 458 us, 455
+// without; two prompts of 300 beside 4,096 decode rows: 274 and 269).
+static __device__ __noinline__ void report_unplanned_rows(const int32_t* qsl, int num_seqs, int split, int entries,
+                                                          int decode_launch, unsigned long long* err, int lane) {
     const unsigned FULL = 0xffffffffu;
-    const int split = cta_units == 2 ? split_last : 0;
-    int base = 0;
-    for (int s0 = 0; s0 < num_seqs; s0 += 32) {
-        const int s = s0 + lane;
-        const int ql = s < num_seqs ? __ldg(qsl + s + 1) - __ldg(qsl + s) : 0;
+    int count = 0, last = -1, wrong = INT32_MAX;
+#pragma unroll 4
+    for (int s = lane; s < num_seqs; s += 32) {
+        const int ql = __ldg(qsl + s + 1) - __ldg(qsl + s);
         const int nt = ql > 1 ? (ql + kPrefillRows - 1) / kPrefillRows : 0;
-        int incl = nt + min(split, nt);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(FULL, incl, o);
-            if (lane >= o) incl += t;
-        }
-        const bool beyond = nt > 0 && base + incl > entries;
-        const unsigned hit = __ballot_sync(FULL, ql < 0 || beyond || (ql == 1 && !decode_launch));
-        if (hit) {
-            if (lane == 0) record_error(err, kErrRange, static_cast<uint32_t>(s0 + __ffs(hit) - 1));
-            return;
-        }
-        base += __shfl_sync(FULL, incl, 31);
+        count += nt + min(split, nt);
+        if (nt > 0) last = s;
+        if (ql < 0 || (ql == 1 && !decode_launch)) wrong = min(wrong, s);
     }
+    wrong = __reduce_min_sync(FULL, wrong);
+    if (__reduce_add_sync(FULL, count) > entries) wrong = min(wrong, __reduce_max_sync(FULL, last));
+    if (wrong < INT32_MAX && lane == 0) record_error(err, kErrRange, static_cast<uint32_t>(wrong));
 }
 
 }  // namespace pkv
