@@ -34,9 +34,9 @@
 //    NaN, the rows of its tile that do not see it.  So in tiles that not all rows
 //    see NaN codes are widened to zeros, each dim keeps the first of the CTA's rows
 //    that sees one, and from that row on its output is set to NaN after the store.
-//  * Measured: 2,048 of 16,384 tokens, 16/8 x 128, 462 us, 558 TFLOP/s (the two
-//    terms of P make it 835 of the tensor cores' work); 300 tokens, 32/8 x 64,
-//    12.7 us.  A tile of two heads takes some 7,000 cycles, 3,300 of MMAs; issue
+//  * Measured: 2,048 of 16,384 tokens, 16/8 x 128, 458 us, 563 TFLOP/s (the two
+//    terms of P make it 844 of the tensor cores' work); 300 tokens, 32/8 x 64,
+//    12.6 us.  A tile of two heads takes some 7,000 cycles, 3,300 of MMAs; issue
 //    slots are 48 % busy, the ALU 39 %: what bounds it is each warp's chain
 //    through a tile, wait, scores, shuffles, exponentials, stores, with four
 //    warps on a scheduler.  Steps of 64 keys with two sets of scores, the MMAs
