@@ -53,30 +53,31 @@ L2_ROTATE_BYTES = 512 << 20
 # kernel's sources it was taken on; reported only while they still match.
 # Keys: (kernel entry, config).
 NCU_TRAFFIC = {
-    ("decode_step", 1): {"bytes": 1511680, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode_step", 2): {"bytes": 91181824, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode_step", 3): {"bytes": 4063371264, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode", 1): {"bytes": 1498880, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode", 2): {"bytes": 91179008, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode", 3): {"bytes": 4073321216, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode", 4): {"bytes": 18811392, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("decode", 5): {"bytes": 306025728, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("fp8_decode", 1): {"bytes": 814336, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("fp8_decode", 2): {"bytes": 44804608, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("fp8_decode", 3): {"bytes": 2038387456, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("fp8_decode", 4): {"bytes": 9532416, "sources": "decode", "sources_sha": "9924469a8935d603"},
-    ("fp8_decode", 5): {"bytes": 154604544, "sources": "decode", "sources_sha": "9924469a8935d603"},
+    ("decode_step", 1): {"bytes": 1512704, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode_step", 2): {"bytes": 91155968, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode_step", 3): {"bytes": 4063211776, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode", 1): {"bytes": 1501696, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode", 2): {"bytes": 91238656, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode", 3): {"bytes": 4073146880, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode", 4): {"bytes": 18812672, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("decode", 5): {"bytes": 306251264, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("fp8_decode", 1): {"bytes": 815616, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("fp8_decode", 2): {"bytes": 44808960, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("fp8_decode", 3): {"bytes": 2038086400, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("fp8_decode", 4): {"bytes": 9534208, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
+    ("fp8_decode", 5): {"bytes": 154563840, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
     # both kernels of the shared-prefix decode (shared_prefix_kernel, then decode_kernel)
-    ("shared_prefix", 4): {"bytes": 19253248, "sources": "decode", "sources_sha": "9924469a8935d603"},
+    ("shared_prefix", 4): {"bytes": 19255296, "sources": "decode", "sources_sha": "9a9490bf3310a027"},
     # prefill tiles of the mixed batch (the K and V tiles are read by every row-tile CTA of a kv head)
-    ("prefill", 5): {"bytes": 25325824, "sources": "prefill", "sources_sha": "334b56d190920b05"},
+    ("prefill", 5): {"bytes": 25330688, "sources": "prefill", "sources_sha": "6eb09d3363923808"},
 }
 KERNEL_SOURCES = {
     "decode": ["paged_kv_cache_291_gb300/csrc/decode_kernel.cuh", "paged_kv_cache_291_gb300/csrc/decode.cu",
                "paged_kv_cache_291_gb300/csrc/decode_fused.cu", "paged_kv_cache_291_gb300/csrc/pkv_device.cuh",
-               "paged_kv_cache_291_gb300/csrc/shared_prefix.cu"],
-    "prefill": ["paged_kv_cache_291_gb300/csrc/prefill.cu", "paged_kv_cache_291_gb300/csrc/tcgen05.cuh",
-                "paged_kv_cache_291_gb300/csrc/pkv_device.cuh"],
+               "paged_kv_cache_291_gb300/csrc/scaled_device.cuh", "paged_kv_cache_291_gb300/csrc/shared_prefix.cu",
+               "paged_kv_cache_291_gb300/csrc/tcgen05.cuh"],
+    "prefill": ["paged_kv_cache_291_gb300/csrc/prefill.cu", "paged_kv_cache_291_gb300/csrc/prefill_tile.cuh",
+                "paged_kv_cache_291_gb300/csrc/tcgen05.cuh", "paged_kv_cache_291_gb300/csrc/pkv_device.cuh"],
 }
 
 
