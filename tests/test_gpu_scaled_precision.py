@@ -127,3 +127,25 @@ def test_long_contexts_in_one_piece(pkv, kind, d, g, n):
         off = np.abs(got[0].double().cpu().numpy() / want - 1).max()
         assert off <= 64 * 2.0 ** -23 + 2 * n / 4096 * 2.0 ** -24 + 36 * 2.0 ** -24 + 2.0 ** -20, f"{off:.2e}"
     assert pkv.get_error()[0] == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,g", [(64, 2), (128, 1), (128, 8)])
+@pytest.mark.parametrize("powers", [[-6], [-100, 40], [40, -100, 0], [-6, 1, 8]])
+def test_long_items_in_turn(pkv, kind, d, g, powers):
+    """One CTA reads long and short contexts one after the other, each warp's state joining its slot several times,
+    with V scales and a running maximum that move meanwhile."""
+    lens = [20001, 300, 9000, 0, 16]
+    b = Batch(80 + g, kind, [1] * 5, [max(n - 1, 0) for n in lens], 2, d)
+    b.lens = np.array(lens, np.int32)
+    spread_v_scales(b, powers, 300)
+    for s, n in enumerate(lens):
+        for i in range(0, -(-n // 16), 97):  # K grows along the context
+            b.scales[b.tables[s, i], :, 0] *= 1 + i / 300
+    q, qt = bf16_rows(b.rng, b.T, 2 * g, d)
+    k, v, sc, _, lens_dev, tables = b.dev()
+    for part in (0, 4000):
+        got = pkv.decode_attention(k, v, qt, tables, lens_dev, max(lens), d ** -0.5, block_scales=sc,
+                                   partition_blocks=part)
+        check(b, got, q, d ** -0.5)
+    assert pkv.get_error()[0] == 0
