@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 # Powers of the V scales of a context's blocks: the least beside larger ones (a
 # block of zeros has the least), steps up and down.
 POWERS = [[-100, 40], [40, -100], [-100, 116], [116, -100], [-100, 0, 116], [116, 0, -100], [-60, 90], [0, 116, -100, 50],
-          [116, 110], [99, 103, 101]]
+          [116, 110], [99, 103, 101], [-100, 3], [-100, 4], [-100, 5], [5, -100], [-100, 4, 9]]
 
 
 def spread_v_scales(b, powers, stride):
@@ -39,7 +39,7 @@ def test_v_scales_far_apart_decode(pkv, kind, powers, d, g):
     for stride, part in ((1, 0), (2, 0), (12, 0), (40, 0), (1, 1), (3, 3), (20, 7)):
         b = Batch(stride + 100 * part, kind, [1] * 3, [16, 16 * 2 * stride + 4, 40 * 16], 2, d)
         spread_v_scales(b, powers, stride)
-        for size in (0.0, 1.0):
+        for size in (0.0, 8.0):
             q, qt = bf16_rows(b.rng, b.T, 2 * g, d, size=size)
             check(b, decode(pkv, b, qt, d ** -0.5, partition_blocks=part), q, d ** -0.5)
     assert pkv.get_error()[0] == 0
@@ -53,7 +53,7 @@ def test_v_scales_far_apart_prefill(pkv, kind, powers, d, g):
     for stride in (1, 3, 8, 17):
         b = Batch(stride, kind, [17, 150, 1], [0, 16 * 4 * stride, 40], 2, d)
         spread_v_scales(b, powers, stride)
-        for size in (0.0, 1.0):
+        for size in (0.0, 8.0):
             q, qt = bf16_rows(b.rng, b.T, 2 * g, d, size=size)
             check(b, prefill(pkv, b, qt, d ** -0.5), q, d ** -0.5)
     assert pkv.get_error()[0] == 0
