@@ -14,8 +14,8 @@ pytestmark = pytest.mark.gpu
 
 # Powers of the V scales of a context's blocks: the least beside larger ones (a
 # block of zeros has the least), steps up and down.
-POWERS = [[-100, 40], [40, -100], [-100, 116], [116, -100], [-100, 0, 116], [116, 0, -100], [-60, 90], [0, 116, -100, 50],
-          [116, 110], [99, 103, 101], [-100, 3], [-100, 4], [-100, 5], [5, -100], [-100, 4, 9]]
+POWERS = [[-100, 40], [40, -100], [-100, 116], [116, -100], [-100, 0, 116], [116, 0, -100], [-60, 90],
+          [0, 116, -100, 50], [116, 110], [99, 103, 101], [-100, 3], [-100, 4], [-100, 5], [5, -100], [-100, 4, 9]]
 
 
 def spread_v_scales(b, powers, stride):
